@@ -774,6 +774,99 @@ rx_status rx_kv_copy(const rx_pool_desc* src, const rx_pool_desc* dst,
                      const int32_t* d_src_slots, const int32_t* d_dst_slots,
                      int64_t n, rx_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit KV pool: keys and values held as e4m3 codes (sign, 4 exponent
+ * and 3 mantissa bits, largest value 448) with one fp32 scale for each KV
+ * head and block of `block` consecutive slots.  A key is its code times its
+ * block's K scale, a value its code times its block's V scale.  It takes
+ * half a bf16 pool's memory and half the bytes of a decode step.  Slots,
+ * slot tables, plans and tile schedules are those of the bf16 pool: the
+ * radix cache and rx_plan_decode / rx_extend_plan serve both.  A block
+ * belongs to one request or tree node, so `block` must divide the cache's
+ * page_size (at page_size 1: block 1, a scale for every token and head).
+ * ---------------------------------------------------------------------- */
+
+/* Owned by the caller.  Every call checks it first: pointers non-NULL, codes
+ * 16-byte and scales 8-byte aligned, head_dim 128 or 256, num_slots >= 2, L
+ * and Hkv > 0, L * Hkv * num_slots < 2^31, block a power of two up to 64
+ * that divides num_slots; RX_ERR_INVALID otherwise. */
+typedef struct rx_kv8_pool_desc {
+  void* k_codes;         /* device e4m3 [L][Hkv][num_slots][head_dim]      */
+  void* v_codes;         /* same layout                                    */
+  float* scales;         /* device fp32 [L][Hkv][num_slots / block][2]:
+                            {K scale, V scale}                             */
+  int64_t num_slots;
+  int32_t num_layers;
+  int32_t num_kv_heads;
+  int32_t head_dim;      /* 128 or 256                                     */
+  int32_t block;         /* slots per scale: 1, 2, 4, .. 64                */
+} rx_kv8_pool_desc;
+
+/* rx_kv_store into an 8-bit pool: the rows are quantised as they are
+ * written.  A block's scale is the least power of two 2^e, e >= -126, with
+ * amax <= 448 * 2^e over the magnitudes of its rows, and a code is the row's
+ * element over the scale rounded to nearest even.  A token stored in a
+ * block's first slot opens the block: whatever the block held before no
+ * longer counts.  A token stored in a later slot keeps the block's rows
+ * before it: the scale stays, or grows to hold the new row, and then those
+ * earlier rows are rounded again under it (the rows behind are left as they
+ * are).  Slots must be distinct, and the call's tokens of one block must
+ * stand next to one another in d_slots, in slot order, as the cache hands
+ * them out.  A NaN is stored as 0 and an infinity as the block's largest
+ * code, both reported by rx_device_check (bit 6); the scale is taken from
+ * the finite values.  A slot outside [1, num_slots) is skipped and reported
+ * (bit 0).  d_k, d_v: device bf16 [T][Hkv][head_dim], 16-byte aligned.
+ * Errors: RX_ERR_INVALID (the pool, T < 0, NULL or misaligned inputs); T = 0
+ * launches nothing. */
+rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
+                       const int32_t* d_slots, const void* d_k,
+                       const void* d_v, int64_t T, rx_stream_t stream);
+
+/* The rows of T slots read back: d_k[i][h][:] = bf16(code * scale) of slot
+ * d_slots[i], same for d_v (device bf16 [T][Hkv][head_dim], 16-byte
+ * aligned).  Rows that rx_kv8_store wrote are read back exactly (a code times
+ * a power of two is a bf16 value unless it is below 2^-126).  Slots may
+ * repeat.  A slot outside [1, num_slots) gives a row of zeros and is
+ * reported by rx_device_check (bit 0).  Errors as rx_kv8_store. */
+rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
+                      const int32_t* d_slots, void* d_k, void* d_v, int64_t T,
+                      rx_stream_t stream);
+
+/* Output types of the 8-bit pool's attention. */
+#define RX_OUT_F32 0
+#define RX_OUT_BF16 1
+
+/* rx_extend_attention over an 8-bit pool: the same queries, tables, tile
+ * schedule and causal rule.  d_out is fp32 or bf16 (out_type) [total_q][Hq]
+ * [head_dim], rounded once from fp32; d_lse fp32 [total_q][Hq].  Scores and
+ * softmax statistics are held in fp32; a query's softmax weights are rounded
+ * to f16 (11 significant bits) for the product with V.  scale must lie in
+ * [2^-40, 2^40].  A pool row that a table names must hold codes of
+ * rx_kv8_store or other finite ones (not 0x7f or 0xff) and finite scales
+ * of at least 2^-126; rows no table names are never read.  Errors: RX_ERR_INVALID as
+ * rx_extend_attention, for a scale out of range and an unknown out_type. */
+rx_status rx_kv8_extend_attention(
+    const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q,
+    int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,
+    const int32_t* d_req_rows, const int32_t* d_prefix_len,
+    const int32_t* d_qo_indptr, const int32_t* d_tile_indptr, int32_t R,
+    int64_t num_tiles, float scale, void* d_out, int32_t out_type,
+    float* d_lse, rx_stream_t stream);
+
+/* rx_decode_attention over an 8-bit pool, and with the drafts of a
+ * rx_verify_rows plan as its batch, rx_verify_attention: arguments as there,
+ * with out_type and numerics as rx_kv8_extend_attention.  step: the step of
+ * a plan of rx_plan_decode_steps (0 for rx_plan_decode); the step's tokens
+ * must be stored first (rx_kv8_store).  A request whose context is empty
+ * gets zeros and lse = -inf.  Errors: RX_ERR_INVALID as rx_decode_attention,
+ * for step < 0, a scale out of range and an unknown out_type. */
+rx_status rx_kv8_decode_attention(
+    const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q,
+    int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,
+    const int32_t* d_plan, const rx_decode_plan_info* info, int32_t B,
+    int32_t step, float scale, void* d_out, int32_t out_type, float* d_lse,
+    void* d_workspace, size_t workspace_bytes, rx_stream_t stream);
+
 /* Page-locked host memory of exactly `bytes` bytes, mapped into the device
  * address space and usable from every device (cudaHostAlloc, portable and
  * mapped): for a host pool that rx_kv_copy reads and writes directly, and
@@ -787,8 +880,8 @@ rx_status rx_host_alloc(size_t bytes, void** out);
 rx_status rx_host_free(void* p);
 
 /* Synchronise the current device and read the kernels' error words (then
- * clear them).  *out_flags (may be NULL): bit 0 = rx_kv_store met a slot
- * outside [1, num_slots) and skipped that write; bit 1 = an attention kernel
+ * clear them).  *out_flags (may be NULL): bit 0 = rx_kv_store, rx_kv8_store
+ * or rx_kv8_load met a slot outside [1, num_slots) and skipped it; bit 1 = an attention kernel
  * read a slot outside [0, num_slots) from req_to_token and used slot 0
  * instead; bit 2 = a tensor-core kernel gave up a barrier wait after its
  * time limit (about 2 s) and returned without results (every output of
@@ -797,7 +890,8 @@ rx_status rx_host_free(void* p);
  * tensor-core tile found its dynamic shared memory off a 1024-byte boundary
  * and returned without results; bit 4 = rx_req_to_token_write met a row or
  * position outside the table and skipped that entry; bit 5 = rx_kv_copy met
- * a slot outside its pool and skipped that entry.  Returns RX_ERR_CUDA
+ * a slot outside its pool and skipped that entry; bit 6 = rx_kv8_store met
+ * a value that is not finite.  Returns RX_ERR_CUDA
  * if a flag was set or the device reported an error. */
 rx_status rx_device_check(int32_t* out_flags);
 

@@ -1,0 +1,793 @@
+// Extend and decode attention over the 8-bit KV pool (e4m3 codes, one scale
+// for each KV head and block of slots), and the merge of decode partials.
+//
+// What is computed, for a query q and the keys j it sees, key j = ks_j kc_j
+// and value j = vs_j vc_j (codes kc, vc; scales ks, vs of the block of key
+// j's slot):
+//   x_j = scale * ks_j * (q . kc_j),  p_j = exp(x_j - m),  l = sum_j p_j,
+//   o = sum_j (p_j vs_j) vc_j / l,    lse = m + log l.
+// A code is exact in f16, so the scales never touch the codes: ks_j
+// multiplies a score, vs_j a softmax weight.  The products run on f16 tensor
+// instructions with fp32 accumulators: q (8 significant bits in bf16) is
+// exact in f16 once its row is scaled by a power of two, and p_j vs_j is
+// rounded to f16 (11 bits) relative to the largest vs so far.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv8.cuh"
+#include "ptx_util.cuh"
+#include "rx.h"
+#include "rx_internal.h"
+
+// Bit 0: a slot outside [0, num_slots) was read (slot 0 used instead).  Read
+// by rx_device_check().
+static __device__ int32_t g_kv8_att_error;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+// The softmax reference of a row moves when a score exceeds it by 2^8, and
+// weights are scaled by 2^7 and by 1 / vref with vref >= vs: at most 2^15,
+// within f16, and full f16 precision down to p vs / vref = 2^-21.
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kWeightBias = 128.f;
+
+struct Args8 {
+  const bf16* q;
+  const uint8_t* kc;  // layer base, [Hkv][num_slots][D]
+  const uint8_t* vc;
+  const float2* scales;  // layer base, [Hkv][num_slots >> block_log2]
+  int64_t head_stride;   // bytes between KV heads (num_slots * D)
+  int64_t scale_stride;  // scales between KV heads
+  int64_t num_slots;
+  int block_log2;
+  const int32_t* table;
+  int64_t row_stride;
+  int hq;
+  int group;
+  float scale_log2;
+  // extend
+  const int32_t* req_rows;
+  const int32_t* prefix_len;
+  const int32_t* qo_indptr;
+  const int32_t* tile_indptr;
+  int num_req;
+  int num_tiles;
+  void* out;
+  int out_bf16;
+  float* lse;
+  // decode
+  const int32_t* work;
+  const int32_t* members;
+  int n_small;       // items of up to decode_small_rows rows
+  int n_items;
+  int n_units;
+  int step;
+  float* ws_o;
+  float* ws_lse;
+  int32_t* counter;  // next unit, NULL: unit = warp index
+};
+
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (lo, hi) rounded to nearest f16 and packed.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Transpose of an 8x8 matrix of 16-bit elements held one row per four lanes.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, bool valid) {
+  int n = valid ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// One warp streams the keys of one KV head for up to 8 NR query rows, 32 keys
+// a step, through a ring of shared-memory stages filled with cp.async.  As in
+// the bf16 decode kernel the products are computed transposed, keys (then
+// output columns) in the M dimension and query rows in N:
+//   S^T (32 keys x 8 rows) = K (codes -> f16) . Q^T
+//   O^T (D x 8 rows)      += V^T (codes -> f16) . P^T
+// The contraction index of a product may be permuted freely, and the M index
+// of O^T too, so that codes go from ldmatrix to operand registers with one
+// conversion each: a lane of an untransposed ldmatrix holds four adjacent
+// codes of a key, taken as d = 4c .. 4c+3 of a k-step; a lane of a transposed
+// one holds the codes (d, d+1) of two adjacent keys, taken as operand rows g
+// and g + 8.
+constexpr int kWarps = 6;
+constexpr int kKeys = 32;  // keys per step
+template <int D>
+struct Pipe8 {
+  static constexpr int STAGES = D == 128 ? 4 : 2;
+  static constexpr int PITCH = D + 16;  // ldmatrix reads all 32 banks
+  static constexpr int SCALES = 2 * kKeys * PITCH;
+  static constexpr int STAGE_BYTES = SCALES + kKeys * 8;
+  static constexpr int WARP_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int BYTES = kWarps * WARP_BYTES + 128;
+};
+
+// What a warp works on: n_rows query rows (row r: query qi(r), head h(r)) over
+// keys [kb, ke) of one table row.
+struct Unit8 {
+  const int32_t* trow;
+  int kb, ke, kvh, n_rows;
+  // decode: row r is member (row0 + r) / G of members
+  const int32_t* members;
+  int part_base, row0;
+  // extend: row r is suffix row gr0 + r of a request; its keys end at
+  // prefix + (gr0 + r) / G + 1
+  int gr0, q_base, prefix;
+};
+
+template <int D, bool EXTEND>
+__device__ __forceinline__ const bf16* unit_query(const Args8& a, const Unit8& u, int r) {
+  const int G = a.group;
+  int64_t qi;
+  int head;
+  if constexpr (EXTEND) {
+    const int tok = (u.gr0 + r) / G;
+    qi = u.q_base + tok;
+    head = u.kvh * G + (u.gr0 + r - tok * G);
+  } else {
+    const int m = (u.row0 + r) / G;
+    qi = u.members[m];
+    head = u.kvh * G + (u.row0 + r - m * G);
+  }
+  return a.q + (qi * a.hq + head) * D;
+}
+
+template <int NR, int D, bool EXTEND>
+__device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint32_t ring,
+                                            const uint8_t* ring_g) {
+  using Cfg = Pipe8<D>;
+  constexpr int S = Cfg::STAGES;
+  constexpr int PITCH = Cfg::PITCH;
+  constexpr int NK = D / 16;
+  constexpr int LPR = D / 16;      // lanes (16 B chunks) per row
+  constexpr int RPI = 32 / LPR;    // rows per load instruction
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const uint8_t* kbase = a.kc + int64_t(u.kvh) * a.head_stride;
+  const uint8_t* vbase = a.vc + int64_t(u.kvh) * a.head_stride;
+  const float2* sbase = a.scales + int64_t(u.kvh) * a.scale_stride;
+  const int kb = u.kb, ke = u.ke;
+  const int n_steps = ke > kb ? (ke - kb + kKeys - 1) / kKeys : 0;
+
+  // the slot of key `lane` of a step (-1 past the range), read one step ahead
+  // of its use
+  auto read_slot = [&](int st) -> int32_t {
+    const int key = kb + st * kKeys + lane;
+    return key < ke ? __ldg(u.trow + key) : -1;
+  };
+  int32_t next_slot = n_steps > 0 ? read_slot(0) : -1;
+  auto issue = [&](int st) {
+    int32_t sl = next_slot;
+    if (st + 1 < n_steps) next_slot = read_slot(st + 1);
+    if (kb + st * kKeys + lane < ke && (sl < 0 || sl >= a.num_slots)) {
+      atomicOr(&g_kv8_att_error, 1);
+      sl = 0;
+    }
+    const uint32_t dst = ring + uint32_t(st % S) * Cfg::STAGE_BYTES;
+    cp_async_8(dst + Cfg::SCALES + lane * 8, sbase + ((sl < 0 ? 0 : sl) >> a.block_log2), sl >= 0);
+#pragma unroll
+    for (int i = 0; i < kKeys / RPI; ++i) {
+      const int row = i * RPI + lane / LPR;
+      const int32_t s = __shfl_sync(0xffffffffu, sl, row);
+      const int64_t at = int64_t(s < 0 ? 0 : s) * D + (lane % LPR) * 16;
+      const uint32_t to = dst + uint32_t(row * PITCH + (lane % LPR) * 16);
+      // keys past the range are zeros (their weights are 0, and 0 * V must be 0)
+      rxk::cp_async_16(to, kbase + at, s >= 0);
+      rxk::cp_async_16(to + kKeys * PITCH, vbase + at, s >= 0);
+    }
+  };
+  __syncwarp();  // the previous unit's last stage has been read
+#pragma unroll 1
+  for (int p = 0; p < S - 1; ++p) {
+    if (p < n_steps) issue(p);
+    rxk::cp_async_commit();
+  }
+
+  // Q^T operands: row nt * 8 + g, scaled by 2^sh (an exact product) so that
+  // its largest magnitude lies in [2^13, 2^14) of f16's range; below 2^-40 a
+  // row's scores are zero for every key in reach and sh stops there.
+  uint32_t qb[NR][NK][2];
+  float rs[NR][2];  // score to log2 units of rows 2c, 2c + 1 of each n-tile
+  int lim[NR][2];
+#pragma unroll
+  for (int nt = 0; nt < NR; ++nt) {
+    const int r = nt * 8 + g;
+    const bool ok = r < u.n_rows;
+    const uint2* src = reinterpret_cast<const uint2*>(
+        ok ? unit_query<D, EXTEND>(a, u, r) : a.q);
+    float amax = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      const uint2 x = ok ? __ldg(src + 4 * kk + c) : make_uint2(0, 0);
+      qb[nt][kk][0] = x.x;
+      qb[nt][kk][1] = x.y;
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(x.x << 16)),
+                                     fabsf(__uint_as_float(x.x & 0xffff0000u))),
+                               fmaxf(fabsf(__uint_as_float(x.y << 16)),
+                                     fabsf(__uint_as_float(x.y & 0xffff0000u)))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int sh = min(13 - (int(__float_as_uint(amax) >> 23) - 127), 53);
+    const float f = kv8::pow2(sh);
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qb[nt][kk][e] = pack_f16(__uint_as_float(qb[nt][kk][e] << 16) * f,
+                                 __uint_as_float(qb[nt][kk][e] & 0xffff0000u) * f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      rs[nt][e] = a.scale_log2 * kv8::pow2(-__shfl_sync(0xffffffffu, sh, 4 * (2 * c + e)));
+      lim[nt][e] = EXTEND ? u.prefix + (u.gr0 + nt * 8 + 2 * c + e) / a.group + 1 : ke;
+    }
+  }
+
+  float o[NR][NK][4];
+  float m_ref[NR][2], l_run[NR][2];
+#pragma unroll
+  for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+    for (int mt = 0; mt < NK; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
+    m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
+    l_run[nt][0] = l_run[nt][1] = 0.f;
+  }
+  float vref = 0.f, inv_vref = 0.f;
+
+  const uint32_t k_lane =
+      uint32_t(((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16);
+  const uint32_t v_lane = uint32_t(kKeys * PITCH) + k_lane;
+
+#pragma unroll 1
+  for (int st = 0; st < n_steps; ++st) {
+    rxk::cp_async_wait<S - 2>();
+    __syncwarp();
+    const uint32_t stage = ring + uint32_t(st % S) * Cfg::STAGE_BYTES;
+    const float2* sc = reinterpret_cast<const float2*>(
+        ring_g + (st % S) * Cfg::STAGE_BYTES + Cfg::SCALES);
+    float x[NR][2][4];  // m-tile h: keys 16 h + g (+ 8)
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][h][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < NK; kk += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r0, r1, r2, r3;
+        rxk::ldsm_x4(stage + k_lane + uint32_t(h * 16 * PITCH + kk * 16), r0, r1, r2, r3);
+        const uint32_t a0 = kv8::to_f16x2(r0), a1 = kv8::to_f16x2(r1),
+                       a2 = kv8::to_f16x2(r0 >> 16), a3 = kv8::to_f16x2(r1 >> 16);
+        const uint32_t b0 = kv8::to_f16x2(r2), b1 = kv8::to_f16x2(r3),
+                       b2 = kv8::to_f16x2(r2 >> 16), b3 = kv8::to_f16x2(r3 >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+          mma_f16(x[nt][h], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
+          mma_f16(x[nt][h], b0, b1, b2, b3, qb[nt][kk + 1][0], qb[nt][kk + 1][1]);
+        }
+      }
+    }
+    float2 s4[4];  // scales of keys g, g + 8, g + 16, g + 24
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s4[i] = sc[g + 8 * i];
+    const int key0 = kb + st * kKeys + g;
+    bool grow = fmaxf(fmaxf(s4[0].y, s4[1].y), fmaxf(s4[2].y, s4[3].y)) > vref;
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int end = EXTEND ? min(lim[nt][e], ke) : ke;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& y = x[nt][i >> 1][(i & 1) * 2 + e];
+          y = key0 + 8 * i < end ? y * (s4[i].x * rs[nt][e]) : -INFINITY;
+          grow |= y > m_ref[nt][e] + kRescaleThreshold;
+        }
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+      float vm = fmaxf(fmaxf(s4[0].y, s4[1].y), fmaxf(s4[2].y, s4[3].y));
+      float mx[NR][2];
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          mx[nt][e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]), fmaxf(x[nt][1][e], x[nt][1][2 + e]));
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+      }
+      float vf = 1.f;
+      if (vm > vref) {
+        vf = vref / vm;
+        vref = vm;
+        inv_vref = 1.f / vm;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float alpha = 1.f;
+          if (mx[nt][e] > m_ref[nt][e]) {
+            alpha = rxk::fast_exp2(m_ref[nt][e] - mx[nt][e]);  // 0 from -inf
+            m_ref[nt][e] = mx[nt][e];
+            l_run[nt][e] *= alpha;
+          }
+          alpha *= vf;
+#pragma unroll
+          for (int mt = 0; mt < NK; ++mt) {
+            o[nt][mt][e] *= alpha;
+            o[nt][mt][2 + e] *= alpha;
+          }
+        }
+    }
+    // P^T operands: b0 (keys 2c, 2c+1 of row g) is the transpose of the
+    // accumulators' (key g, rows 2c, 2c+1)
+    float wv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wv[i] = s4[i].y * inv_vref * kWeightBias;
+    uint32_t pb[NR][4];
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+      const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
+      const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2] - m0);
+        const float p1 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2 + 1] - m1);
+        l_run[nt][0] += p0;
+        l_run[nt][1] += p1;
+        pb[nt][i] = movmatrix_trans(pack_f16(p0 * wv[i], p1 * wv[i]));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int mt = 0; mt < NK; mt += 2) {
+        uint32_t r0, r1, r2, r3;
+        rxk::ldsm_x4_t(stage + v_lane + uint32_t(h * 16 * PITCH + mt * 16), r0, r1, r2, r3);
+        // bytes (d of key 2c, d of key 2c+1, d+1 of both)
+        r0 = __byte_perm(r0, 0, 0x3120);
+        r1 = __byte_perm(r1, 0, 0x3120);
+        r2 = __byte_perm(r2, 0, 0x3120);
+        r3 = __byte_perm(r3, 0, 0x3120);
+        const uint32_t a0 = kv8::to_f16x2(r0), a1 = kv8::to_f16x2(r0 >> 16),
+                       a2 = kv8::to_f16x2(r1), a3 = kv8::to_f16x2(r1 >> 16);
+        const uint32_t b0 = kv8::to_f16x2(r2), b1 = kv8::to_f16x2(r2 >> 16),
+                       b2 = kv8::to_f16x2(r3), b3 = kv8::to_f16x2(r3 >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+          mma_f16(o[nt][mt], a0, a1, a2, a3, pb[nt][2 * h], pb[nt][2 * h + 1]);
+          mma_f16(o[nt][mt + 1], b0, b1, b2, b3, pb[nt][2 * h], pb[nt][2 * h + 1]);
+        }
+      }
+    __syncwarp();  // every lane is done with this stage before it is refilled
+    if (st + S - 1 < n_steps) issue(st + S - 1);
+    rxk::cp_async_commit();
+  }
+  rxk::cp_async_wait<0>();
+
+  // rows nt * 8 + 2c + e: output columns 16 mt + 2g, + 1
+  const float unweight = vref * (1.f / kWeightBias);
+#pragma unroll
+  for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = l_run[nt][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int r = nt * 8 + 2 * c + e;
+      if (r >= u.n_rows) continue;
+      const float inv = l > 0.f ? unweight / l : 0.f;  // no key: zeros, lse -inf
+      const float lse = l > 0.f ? m_ref[nt][e] * kLn2 + logf(l) : -INFINITY;
+      if constexpr (EXTEND) {
+        const int tok = (u.gr0 + r) / a.group;
+        const int64_t row = int64_t(u.q_base + tok) * a.hq + u.kvh * a.group +
+                            (u.gr0 + r - tok * a.group);
+#pragma unroll
+        for (int mt = 0; mt < NK; ++mt) {
+          const float y0 = o[nt][mt][e] * inv, y1 = o[nt][mt][2 + e] * inv;
+          if (a.out_bf16)
+            reinterpret_cast<uint32_t*>(a.out)[row * (D / 2) + 8 * mt + g] = rxk::pack_bf16(y0, y1);
+          else
+            reinterpret_cast<float2*>(a.out)[row * (D / 2) + 8 * mt + g] = make_float2(y0, y1);
+        }
+        if (g == 0) a.lse[row] = lse;
+      } else {
+        const int mem = (u.row0 + r) / a.group;
+        const int head = u.kvh * a.group + (u.row0 + r - mem * a.group);
+        const int64_t at = int64_t(u.part_base + mem) * a.hq + head;
+        float2* dst = reinterpret_cast<float2*>(a.ws_o + at * D);
+#pragma unroll
+        for (int mt = 0; mt < NK; ++mt)
+          dst[8 * mt + g] = make_float2(o[nt][mt][e] * inv, o[nt][mt][2 + e] * inv);
+        if (g == 0) a.ws_lse[at] = lse;
+      }
+    }
+}
+
+// Decode: warps take units (item, KV head, block of query rows) until none is
+// left.
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 1) decode8_kernel(const __grid_constant__ Args8 a) {
+  constexpr int NR = D == 128 ? 2 : 1;
+  constexpr int SUB = 128 / (8 * NR);  // row blocks of a large item
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  rxk::griddep_launch_dependents();
+  rxk::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = rxk::smem_addr(smem_raw);
+  const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
+  const int hkv = a.hq / a.group;
+  int unit = int(blockIdx.x) * kWarps + warp;
+  while (true) {
+    if (a.counter) {
+      unit = lane == 0 ? atomicAdd(a.counter, 1) : 0;
+      unit = __shfl_sync(0xffffffffu, unit, 0);
+    }
+    if (unit >= a.n_units) break;
+    int item, sub = 0, kvh;
+    if (unit < a.n_small * hkv) {
+      item = unit / hkv;
+      kvh = unit - item * hkv;
+    } else {
+      const int v = unit - a.n_small * hkv;
+      sub = v % SUB;
+      item = a.n_small + (v / SUB) / hkv;
+      kvh = (v / SUB) % hkv;
+    }
+    const int32_t* w = a.work + int64_t(item) * RX_WORK_WORDS;
+    Unit8 u;
+    u.trow = a.table + int64_t(w[0]) * a.row_stride;
+    u.kb = w[1];
+    u.ke = w[7] > 0 ? min(w[2], w[7] + a.step) : w[2];
+    u.members = a.members + w[3];
+    u.part_base = w[5];
+    u.row0 = sub * 8 * NR;
+    u.n_rows = min(w[6] - u.row0, 8 * NR);
+    u.kvh = kvh;
+    if (u.n_rows > 0) stream_unit<NR, D, false>(a, u, raw + off, smem_raw + off);
+    if (!a.counter) break;
+  }
+}
+
+// Extend: warp w of CTA b takes row block b * kWarps + w, a block of 8 NR of
+// a tile's 128 query rows.
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 1) extend8_kernel(const __grid_constant__ Args8 a) {
+  constexpr int NR = D == 128 ? 2 : 1;
+  constexpr int SUB = 128 / (8 * NR);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5;
+  const uint32_t raw = rxk::smem_addr(smem_raw);
+  const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
+  const int hkv = a.hq / a.group;
+  const int64_t unit = int64_t(blockIdx.x) * kWarps + warp;
+  if (unit >= int64_t(a.num_tiles) * hkv * SUB) return;
+  const int sub = int(unit % SUB);
+  const int kvh = int((unit / SUB) % hkv);
+  const int tile = int(unit / SUB / hkv);
+  int lo = 0, hi = a.num_req;  // the last request with tile_indptr <= tile
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.tile_indptr + mid) <= tile) lo = mid; else hi = mid;
+  }
+  Unit8 u;
+  u.q_base = a.qo_indptr[lo];
+  u.prefix = a.prefix_len[lo];
+  u.trow = a.table + int64_t(a.req_rows[lo]) * a.row_stride;
+  u.gr0 = (tile - a.tile_indptr[lo]) * 128 + sub * 8 * NR;
+  const int rows = (a.qo_indptr[lo + 1] - u.q_base) * a.group;
+  u.n_rows = min(rows - u.gr0, 8 * NR);
+  if (u.n_rows <= 0) return;
+  u.kb = 0;
+  u.ke = u.prefix + (u.gr0 + u.n_rows - 1) / a.group + 1;
+  u.kvh = kvh;
+  stream_unit<NR, D, true>(a, u, raw + off, smem_raw + off);
+}
+
+// One warp per (request, query head): lse = log sum_s exp(lse_s), o = sum_s
+// exp(lse_s - lse) o_s over the request's parts, rounded once to the output
+// type.  A request without parts, or with empty ones only, gets zeros and
+// lse = -inf.
+template <int D>
+__global__ void __launch_bounds__(256) merge8_kernel(const int32_t* __restrict__ indptr,
+                                                     const int32_t* __restrict__ parts,
+                                                     const float* __restrict__ ws_o,
+                                                     const float* __restrict__ ws_lse, int hq,
+                                                     int B, void* out, int out_bf16,
+                                                     float* __restrict__ lse_out) {
+  constexpr int V = D / 128;
+  const int64_t gw = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const bool active = gw < int64_t(B) * hq;
+  const int b = active ? int(gw / hq) : 0;
+  const int h = active ? int(gw - int64_t(b) * hq) : 0;
+  rxk::griddep_wait();
+  if (!active) return;
+  const int p0 = indptr[b];
+  const int n = indptr[b + 1] - p0;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32)
+    m = fmaxf(m, __ldcg(ws_lse + int64_t(parts[p0 + i]) * hq + h));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const float4* o4 = reinterpret_cast<const float4*>(ws_o);
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    const int64_t e = i < n ? int64_t(parts[p0 + i]) * hq + h : 0;
+    const float li = i < n ? __ldcg(ws_lse + e) : -INFINITY;
+    const float w = li == -INFINITY ? 0.f : rxk::fast_exp2((li - m) * kLog2e);
+    sum += w;
+    const int cnt = min(32, n - base);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const int64_t ej = __shfl_sync(0xffffffffu, e, j);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float4 y = __ldcg(o4 + ej * (D / 4) + v * 32 + lane);
+        acc[v].x += wj * y.x;
+        acc[v].y += wj * y.y;
+        acc[v].z += wj * y.z;
+        acc[v].w += wj * y.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float4 y =
+        make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+    const int64_t at = gw * (D / 4) + v * 32 + lane;
+    if (out_bf16)
+      reinterpret_cast<uint2*>(out)[at] =
+          make_uint2(rxk::pack_bf16(y.x, y.y), rxk::pack_bf16(y.z, y.w));
+    else
+      reinterpret_cast<float4*>(out)[at] = y;
+  }
+  if (lane == 0) lse_out[gw] = sum > 0.f ? m + logf(sum) : -INFINITY;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// A kernel's dynamic shared-memory limit is raised once per device.
+constexpr int kMaxDevices = 64;
+template <typename K>
+rx_status ensure_smem(std::atomic<bool> (&done)[kMaxDevices], K* kernel, int bytes) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return rx_internal::set_error(RX_ERR_CUDA, "no usable current device");
+  if (done[dev].load(std::memory_order_acquire)) return RX_OK;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // not left for a later launch check to report
+    static thread_local char buf[160];
+    snprintf(buf, sizeof(buf), "raising a kernel's shared-memory limit: %s",
+             cudaGetErrorString(e));
+    return rx_internal::set_error(RX_ERR_CUDA, buf);
+  }
+  done[dev].store(true, std::memory_order_release);
+  return RX_OK;
+}
+
+// The arguments both calls share, checked before any CUDA call.
+rx_status common_args(const char* what, const rx_kv8_pool_desc* pool, int32_t layer,
+                      const void* d_q, int32_t num_q_heads, const int32_t* d_table,
+                      int64_t row_stride, float scale, int32_t out_type, Args8* a) {
+  static thread_local char buf[160];
+  rx_status st = rx_internal::check_kv8_pool(pool, layer);
+  if (st != RX_OK) return st;
+  const char* bad = nullptr;
+  if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
+    bad = "Hq % Hkv != 0";
+  else if (!(scale >= 0x1p-40f && scale <= 0x1p40f))
+    bad = "scale outside [2^-40, 2^40]";
+  else if (out_type != RX_OUT_F32 && out_type != RX_OUT_BF16)
+    bad = "unknown out_type";
+  else if (row_stride < 0)
+    bad = "row_stride < 0";
+  if (bad) {
+    snprintf(buf, sizeof(buf), "%s: %s", what, bad);
+    return rx_internal::set_error(RX_ERR_INVALID, buf);
+  }
+  const int D = pool->head_dim;
+  int lg = 0;
+  while ((1 << lg) < pool->block) ++lg;
+  const int64_t heads = int64_t(layer) * pool->num_kv_heads;
+  a->q = static_cast<const bf16*>(d_q);
+  a->kc = static_cast<const uint8_t*>(pool->k_codes) + heads * pool->num_slots * D;
+  a->vc = static_cast<const uint8_t*>(pool->v_codes) + heads * pool->num_slots * D;
+  a->scale_stride = pool->num_slots >> lg;
+  a->scales = reinterpret_cast<const float2*>(pool->scales) + heads * a->scale_stride;
+  a->head_stride = pool->num_slots * D;
+  a->num_slots = pool->num_slots;
+  a->block_log2 = lg;
+  a->table = d_table;
+  a->row_stride = row_stride;
+  a->hq = num_q_heads;
+  a->group = num_q_heads / pool->num_kv_heads;
+  a->scale_log2 = scale * kLog2e;
+  a->out_bf16 = out_type == RX_OUT_BF16;
+  return RX_OK;
+}
+
+}  // namespace
+
+namespace rx_internal {
+
+int32_t kv8_attention_error_flags(bool clear) {
+  int32_t v = 0;
+  cudaMemcpyFromSymbol(&v, g_kv8_att_error, sizeof(v));
+  if (clear && v) {
+    int32_t z = 0;
+    cudaMemcpyToSymbol(g_kv8_att_error, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace rx_internal
+
+extern "C" rx_status rx_kv8_extend_attention(
+    const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
+    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_req_rows,
+    const int32_t* d_prefix_len, const int32_t* d_qo_indptr, const int32_t* d_tile_indptr,
+    int32_t R, int64_t num_tiles, float scale, void* d_out, int32_t out_type, float* d_lse,
+    rx_stream_t stream) {
+  Args8 a{};
+  rx_status st = common_args("rx_kv8_extend_attention", pool, layer, d_q, num_q_heads,
+                             d_req_to_token, row_stride, scale, out_type, &a);
+  if (st != RX_OK) return st;
+  const int D = pool->head_dim;
+  const int sub = D == 128 ? 8 : 16;
+  if (R < 0 || num_tiles < 0 || num_tiles > INT32_MAX / sub / pool->num_kv_heads)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_extend_attention: bad R or num_tiles");
+  if (R == 0 || num_tiles == 0) return RX_OK;
+  if (!d_q || !d_req_to_token || !d_req_rows || !d_prefix_len || !d_qo_indptr ||
+      !d_tile_indptr || !d_out || !d_lse || !aligned16(d_q) || !aligned16(d_out))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_extend_attention: NULL or misaligned");
+  a.req_rows = d_req_rows;
+  a.prefix_len = d_prefix_len;
+  a.qo_indptr = d_qo_indptr;
+  a.tile_indptr = d_tile_indptr;
+  a.num_req = R;
+  a.num_tiles = int(num_tiles);
+  a.out = d_out;
+  a.lse = d_lse;
+  const int64_t units = num_tiles * pool->num_kv_heads * sub;
+  const unsigned ctas = unsigned((units + kWarps - 1) / kWarps);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
+  st = D == 128 ? ensure_smem(done128, extend8_kernel<128>, Pipe8<128>::BYTES)
+                : ensure_smem(done256, extend8_kernel<256>, Pipe8<256>::BYTES);
+  if (st != RX_OK) return st;
+  if (D == 128)
+    extend8_kernel<128><<<ctas, kWarps * 32, Pipe8<128>::BYTES, s>>>(a);
+  else
+    extend8_kernel<256><<<ctas, kWarps * 32, Pipe8<256>::BYTES, s>>>(a);
+  return rx_internal::launch_status("rx_kv8_extend_attention");
+}
+
+extern "C" rx_status rx_kv8_decode_attention(
+    const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
+    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
+    const rx_decode_plan_info* info, int32_t B, int32_t step, float scale, void* d_out,
+    int32_t out_type, float* d_lse, void* d_workspace, size_t workspace_bytes,
+    rx_stream_t stream) {
+  Args8 a{};
+  rx_status st = common_args("rx_kv8_decode_attention", pool, layer, d_q, num_q_heads,
+                             d_req_to_token, row_stride, scale, out_type, &a);
+  if (st != RX_OK) return st;
+  if (!info || B < 0 || step < 0)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: bad argument");
+  if (B == 0) return RX_OK;
+  if (int64_t(workspace_bytes) < info->workspace_bytes || !d_workspace ||
+      !aligned16(d_workspace))
+    return rx_internal::set_error(
+        RX_ERR_INVALID, "rx_kv8_decode_attention: workspace missing, small or misaligned");
+  if (!d_q || !d_req_to_token || !d_plan || !d_out || !d_lse || !aligned16(d_q) ||
+      !aligned16(d_out))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: NULL or misaligned");
+  const int D = pool->head_dim;
+  const int64_t hkv = pool->num_kv_heads;
+  const int64_t sub = D == 128 ? 8 : 16;
+  const int64_t n_small = info->n_work - info->n_work_tc;
+  if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
+      info->n_work > INT32_MAX / hkv / sub)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: bad plan info");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // the workspace layout of rx_plan_decode: partial rows, their lse, a counter
+  const int64_t o_bytes = (info->n_parts * num_q_heads * int64_t(D) * 4 + 255) / 256 * 256;
+  const int64_t l_bytes = (info->n_parts * num_q_heads * 4 + 255) / 256 * 256;
+  a.ws_o = static_cast<float*>(d_workspace);
+  a.ws_lse = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + o_bytes);
+  int32_t* counter =
+      reinterpret_cast<int32_t*>(static_cast<char*>(d_workspace) + o_bytes + l_bytes);
+  a.work = d_plan + info->off_work;
+  a.members = d_plan + info->off_members;
+  a.n_small = int(n_small);
+  a.n_items = int(info->n_work);
+  a.n_units = int(n_small * hkv + info->n_work_tc * hkv * sub);
+  a.step = step;
+  if (a.n_units > 0) {
+    const int64_t sms = rx_internal::sm_count();
+    int64_t ctas = (a.n_units + kWarps - 1) / kWarps;
+    if (ctas > sms) {
+      // more units than warps: taken from a counter, heaviest first
+      ctas = sms;
+      a.counter = counter;
+      if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
+        return rx_internal::launch_status("rx_kv8_decode_attention: counter reset");
+    }
+    static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
+    st = D == 128 ? ensure_smem(done128, decode8_kernel<128>, Pipe8<128>::BYTES)
+                  : ensure_smem(done256, decode8_kernel<256>, Pipe8<256>::BYTES);
+    if (st != RX_OK) return st;
+    if (D == 128)
+      decode8_kernel<128><<<unsigned(ctas), kWarps * 32, Pipe8<128>::BYTES, s>>>(a);
+    else
+      decode8_kernel<256><<<unsigned(ctas), kWarps * 32, Pipe8<256>::BYTES, s>>>(a);
+    st = rx_internal::launch_status("rx_kv8_decode_attention");
+    if (st != RX_OK) return st;
+  }
+  // launched while the decode kernel runs; it waits on the device for its end
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned((int64_t(B) * num_q_heads + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int32_t* indptr = d_plan + info->off_req_part_indptr;
+  const int32_t* parts = d_plan + info->off_req_parts;
+  const float* wo = a.ws_o;
+  const float* wl = a.ws_lse;
+  if (D == 128)
+    cudaLaunchKernelEx(&cfg, merge8_kernel<128>, indptr, parts, wo, wl, int(num_q_heads), int(B),
+                       d_out, int(a.out_bf16), d_lse);
+  else
+    cudaLaunchKernelEx(&cfg, merge8_kernel<256>, indptr, parts, wo, wl, int(num_q_heads), int(B),
+                       d_out, int(a.out_bf16), d_lse);
+  return rx_internal::launch_status("rx_kv8_decode_attention: merge");
+}

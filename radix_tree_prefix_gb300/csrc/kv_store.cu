@@ -287,8 +287,10 @@ extern "C" rx_status rx_device_check(int32_t* out_flags) {
     snprintf(buf, sizeof(buf), "rx_device_check: %s", cudaGetErrorString(e));
     return rx_internal::set_error(RX_ERR_CUDA, buf);
   }
-  const int32_t tcf = rx_internal::tc_error_flags(true);
-  int32_t f = rx_internal::kv_store_error_flags(true) | ((tcf & 7) << 1);
+  const int32_t tcf = rx_internal::tc_error_flags(true) |
+                      rx_internal::kv8_attention_error_flags(true);
+  int32_t f = rx_internal::kv_store_error_flags(true) |
+              rx_internal::kv8_store_error_flags(true) | ((tcf & 7) << 1);
   if (out_flags) *out_flags = f;
   if (f)
     return rx_internal::set_error(RX_ERR_CUDA,
@@ -300,6 +302,8 @@ extern "C" rx_status rx_device_check(int32_t* out_flags) {
                                                "or position outside the table"
                                   : (f & 32) ? "rx_device_check: a KV copy met a slot outside "
                                                "its pool"
+                                  : (f & 64) ? "rx_device_check: an 8-bit KV store met a value "
+                                               "that is not finite"
                                              : "rx_device_check: a kernel met a slot outside the pool");
   return RX_OK;
 }

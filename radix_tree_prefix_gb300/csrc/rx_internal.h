@@ -47,11 +47,14 @@ rx_status set_error(rx_status s, const char* msg);
 
 // Device-side helpers (kv_store.cu).
 rx_status check_pool(const rx_pool_desc* pool, int32_t layer);
+rx_status check_kv8_pool(const rx_kv8_pool_desc* pool, int32_t layer);
 rx_status launch_status(const char* what);
 int sm_count();
 // Error words of the kernels of each file: bit 0 = slot out of range.
 int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
+int32_t kv8_store_error_flags(bool clear);  // bits 0 and 6 of rx_device_check
+int32_t kv8_attention_error_flags(bool clear);  // as tc_error_flags
 // One decode step in a single launch: the tensor-core tiles of the plan's
 // large items and the warp-role units of its small items (attention_tc.cu).
 // *unit_counter must be 0 at launch.  k_new / v_new / slots_new non-NULL:

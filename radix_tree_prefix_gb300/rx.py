@@ -103,6 +103,14 @@ class rx_pool_desc(C.Structure):
                 ("head_dim", C.c_int32), ("reserved", C.c_int32)]
 
 
+class rx_kv8_pool_desc(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("scales", C.c_void_p),
+                ("num_slots", C.c_int64), ("num_layers", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("block", C.c_int32)]
+
+
+OUT_F32, OUT_BF16 = 0, 1      # RX_OUT_* of rx.h
+
 P = C.c_void_p
 I32, I64, F32, SZ = C.c_int32, C.c_int64, C.c_float, C.c_size_t
 _SIGS = {
@@ -154,6 +162,11 @@ _SIGS = {
     "rx_events_create": [I32, P],
     "rx_events_destroy": [I32, P],
     "rx_event_elapsed_ms": [P, P, P],
+    "rx_kv8_store": [P, I32, P, P, P, I64, P],
+    "rx_kv8_load": [P, I32, P, P, P, I64, P],
+    "rx_kv8_extend_attention": [P, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P, P],
+    "rx_kv8_decode_attention": [P, I32, P, I32, P, I64, P, P, I32, I32, F32, P, I32, P, P, SZ,
+                                P],
     "rx_device_check": [P],
 }
 for _name, _args in _SIGS.items():
@@ -661,6 +674,118 @@ def kv_copy(src_pool, dst_pool, d_src_slots, d_dst_slots, stream=None):
     """rx_kv_copy between (or within) pools given as rx_pool_desc."""
     _check(_lib.rx_kv_copy(C.byref(src_pool), C.byref(dst_pool), d_src_slots.data_ptr(),
                            d_dst_slots.data_ptr(), d_src_slots.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------- 8-bit KV pool
+class Kv8Pool(rx_kv8_pool_desc):
+    """Descriptor of an 8-bit pool that keeps its tensors alive (kv8_pool_desc)."""
+
+
+def kv8_pool_desc(k_codes, v_codes, scales):
+    """Descriptor of an 8-bit pool: codes [L, Hkv, N, d] (torch float8_e4m3fn
+    or uint8), scales fp32 [L, Hkv, N / block, 2]; the block follows from the
+    shapes."""
+    import torch
+    L, hkv, n, d = k_codes.shape
+    nb = scales.shape[2] if scales.dim() == 4 else 0
+    for t in (k_codes, v_codes):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.shape != k_codes.shape or \
+                not t.is_contiguous():
+            raise ValueError("kv8 codes: two contiguous float8_e4m3fn or uint8 tensors "
+                             "[L, Hkv, N, d]")
+    if scales.dtype != torch.float32 or not scales.is_contiguous() or nb <= 0 or n % nb or \
+            tuple(scales.shape) != (L, hkv, nb, 2):
+        raise ValueError("kv8 scales: a contiguous float32 tensor [L, Hkv, N / block, 2]")
+    if not k_codes.device == v_codes.device == scales.device:
+        raise ValueError("kv8 pool tensors are on different devices")
+    p = Kv8Pool(k_codes.data_ptr(), v_codes.data_ptr(), scales.data_ptr(), n, L, hkv, d, n // nb)
+    p.tensors = (k_codes, v_codes, scales)
+    p.device = k_codes.device
+    return p
+
+
+def _kv8_args(pool, stream, *tensors):
+    """Checks the (name, tensor, dtype, elements) of a call against the
+    kernels' layouts: contiguous, of the type, at least (d_slots: exactly)
+    the elements, on the pool's device, which must be the current one.
+    Returns the stream's handle."""
+    import torch
+    dev = pool.device
+    if dev.type != "cuda":
+        raise ValueError(f"kv8: the pool is on {dev}, not on a GPU")
+    for name, t, dtype, n in tensors:
+        if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n or t.device != dev:
+            raise ValueError(f"kv8: {name} must be a contiguous {dtype} tensor of at least {n} "
+                             f"elements on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"kv8: the stream is on {stream.device}, the pool on {dev}")
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError(f"kv8: the pool is on {dev}, which is not the current device")
+    return stream.cuda_stream
+
+
+def kv8_store(pool, layer, d_slots, d_k, d_v, stream=None):
+    """rx_kv8_store: bf16 rows [T, Hkv, d] quantised into their slots."""
+    import torch
+    T = d_slots.numel()
+    n = T * pool.num_kv_heads * pool.head_dim
+    s = _kv8_args(pool, stream, ("d_slots", d_slots, torch.int32, T),
+                  ("d_k", d_k, torch.bfloat16, n), ("d_v", d_v, torch.bfloat16, n))
+    _check(_lib.rx_kv8_store(C.byref(pool), layer, d_slots.data_ptr(), d_k.data_ptr(),
+                             d_v.data_ptr(), T, s))
+
+
+def kv8_load(pool, layer, d_slots, d_k, d_v, stream=None):
+    """rx_kv8_load: the rows of d_slots read back into d_k, d_v (bf16)."""
+    import torch
+    T = d_slots.numel()
+    n = T * pool.num_kv_heads * pool.head_dim
+    s = _kv8_args(pool, stream, ("d_slots", d_slots, torch.int32, T),
+                  ("d_k", d_k, torch.bfloat16, n), ("d_v", d_v, torch.bfloat16, n))
+    _check(_lib.rx_kv8_load(C.byref(pool), layer, d_slots.data_ptr(), d_k.data_ptr(),
+                            d_v.data_ptr(), T, s))
+
+
+def _out_type(d_out):
+    import torch
+    return OUT_BF16 if d_out.dtype is torch.bfloat16 else OUT_F32
+
+
+def kv8_extend_attention(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len, d_qo_indptr,
+                         d_tile_indptr, R, num_tiles, scale, d_out, d_lse, stream=None):
+    """rx_kv8_extend_attention; d_out is bf16 or fp32."""
+    import torch
+    i32, ot = torch.int32, _out_type(d_out)
+    n = d_q.numel()
+    s = _kv8_args(pool, stream, ("d_q", d_q, torch.bfloat16, 0), ("d_table", d_table, i32, 0),
+                  ("d_req_rows", d_req_rows, i32, R), ("d_prefix_len", d_prefix_len, i32, R),
+                  ("d_qo_indptr", d_qo_indptr, i32, R + 1),
+                  ("d_tile_indptr", d_tile_indptr, i32, R + 1),
+                  ("d_out", d_out, torch.bfloat16 if ot else torch.float32, n),
+                  ("d_lse", d_lse, torch.float32, n // pool.head_dim))
+    _check(_lib.rx_kv8_extend_attention(
+        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        d_req_rows.data_ptr(), d_prefix_len.data_ptr(), d_qo_indptr.data_ptr(),
+        d_tile_indptr.data_ptr(), R, num_tiles, scale, d_out.data_ptr(), ot, d_lse.data_ptr(), s))
+
+
+def kv8_decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_out, d_lse,
+                         d_workspace, step=0, stream=None):
+    """rx_kv8_decode_attention; d_out is bf16 or fp32."""
+    import torch
+    i32, ot = torch.int32, _out_type(d_out)
+    rows = B * hq
+    s = _kv8_args(pool, stream, ("d_q", d_q, torch.bfloat16, rows * pool.head_dim),
+                  ("d_table", d_table, i32, 0), ("d_plan", d_plan, i32, info.plan_words),
+                  ("d_out", d_out, torch.bfloat16 if ot else torch.float32, rows * pool.head_dim),
+                  ("d_lse", d_lse, torch.float32, rows),
+                  ("d_workspace", d_workspace, d_workspace.dtype, 0))
+    _check(_lib.rx_kv8_decode_attention(
+        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        d_plan.data_ptr(), C.byref(info), B, step, scale, d_out.data_ptr(), ot, d_lse.data_ptr(),
+        d_workspace.data_ptr(), d_workspace.numel() * d_workspace.element_size(), s))
 
 
 def decode_attention_static(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_out, d_lse,
