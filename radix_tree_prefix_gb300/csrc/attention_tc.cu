@@ -1275,20 +1275,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's tensor-map encoder, looked up once per process (a function-
-// local static is initialised exactly once, whichever thread gets there).
-EncodeTiled encode_fn() {
-  static const EncodeTiled fn = []() -> EncodeTiled {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<EncodeTiled>(p);
-    return nullptr;
-  }();
-  return fn;
-}
+EncodeTiled encode_fn() { return reinterpret_cast<EncodeTiled>(rx_internal::tensor_map_encoder()); }
 
 // Tensor map over a whole pool [L * Hkv * num_slots rows][D] of bf16, box of
 // 64 columns x BN rows, 128-byte swizzle (the shared-memory tile layout);
@@ -1390,6 +1377,21 @@ rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, int32_t layer, unsig
 }  // namespace
 
 namespace rx_internal {
+
+// Looked up once per process (a function-local static is initialised exactly
+// once, whichever thread gets there).
+void* tensor_map_encoder() {
+  static void* const fn = []() -> void* {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return p;
+    return nullptr;
+  }();
+  return fn;
+}
 
 int32_t tc_error_flags(bool clear) {
   int32_t v = 0;

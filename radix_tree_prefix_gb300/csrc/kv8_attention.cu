@@ -11,7 +11,12 @@
 // instructions with fp32 accumulators: q (8 significant bits in bf16) is
 // exact in f16 once its row is scaled by a power of two, and p_j vs_j is
 // rounded to f16 (11 bits) relative to the largest vs so far.
+//
+// Extend, and decode items of more query rows than one warp takes, run on the
+// tensor-core tile of kv8_tile.cuh; decode items of few rows (a request's own
+// tail) on warps that stream the keys (stream_unit below).
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -25,8 +30,8 @@
 #include "rx.h"
 #include "rx_internal.h"
 
-// Bit 0: a slot outside [0, num_slots) was read (slot 0 used instead).  Read
-// by rx_device_check().
+// Bit 0: a slot outside [0, num_slots) was read (slot 0 used instead); bit 1:
+// a barrier wait timed out.  Read by rx_device_check().
 static __device__ int32_t g_kv8_att_error;
 
 namespace {
@@ -48,6 +53,7 @@ struct Args8 {
   int64_t head_stride;   // bytes between KV heads (num_slots * D)
   int64_t scale_stride;  // scales between KV heads
   int64_t num_slots;
+  int64_t tma_row_base;  // row of (layer, KV head 0, slot 0) in the tensor map
   int block_log2;
   const int32_t* table;
   int64_t row_stride;
@@ -61,19 +67,18 @@ struct Args8 {
   const int32_t* tile_indptr;
   int num_req;
   int num_tiles;
+  int heads_interleaved;  // CTA order: 1 = tile-major over heads, 0 = head-major
   void* out;
   int out_bf16;
   float* lse;
   // decode
   const int32_t* work;
   const int32_t* members;
-  int n_small;       // items of up to decode_small_rows rows
-  int n_items;
-  int n_units;
+  int n_small;  // items of up to decode_small_rows rows, then the tile items
   int step;
   float* ws_o;
   float* ws_lse;
-  int32_t* counter;  // next unit, NULL: unit = warp index
+  int32_t* counter;  // next unit of the small items, NULL: unit = warp index
 };
 
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -102,6 +107,12 @@ __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, bool v
                : "memory");
 }
 
+}  // namespace
+
+#include "kv8_tile.cuh"
+
+namespace {
+
 // ---------------------------------------------------------------------------
 // One warp streams the keys of one KV head for up to 8 NR query rows, 32 keys
 // a step, through a ring of shared-memory stages filled with cp.async.  As in
@@ -127,37 +138,16 @@ struct Pipe8 {
   static constexpr int BYTES = kWarps * WARP_BYTES + 128;
 };
 
-// What a warp works on: n_rows query rows (row r: query qi(r), head h(r)) over
-// keys [kb, ke) of one table row.
+// What a warp works on: n_rows query rows over keys [kb, ke) of one table
+// row; row r is query head kvh G + r % G of member r / G.
 struct Unit8 {
   const int32_t* trow;
   int kb, ke, kvh, n_rows;
-  // decode: row r is member (row0 + r) / G of members
   const int32_t* members;
-  int part_base, row0;
-  // extend: row r is suffix row gr0 + r of a request; its keys end at
-  // prefix + (gr0 + r) / G + 1
-  int gr0, q_base, prefix;
+  int part_base;
 };
 
-template <int D, bool EXTEND>
-__device__ __forceinline__ const bf16* unit_query(const Args8& a, const Unit8& u, int r) {
-  const int G = a.group;
-  int64_t qi;
-  int head;
-  if constexpr (EXTEND) {
-    const int tok = (u.gr0 + r) / G;
-    qi = u.q_base + tok;
-    head = u.kvh * G + (u.gr0 + r - tok * G);
-  } else {
-    const int m = (u.row0 + r) / G;
-    qi = u.members[m];
-    head = u.kvh * G + (u.row0 + r - m * G);
-  }
-  return a.q + (qi * a.hq + head) * D;
-}
-
-template <int NR, int D, bool EXTEND>
+template <int NR, int D>
 __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint32_t ring,
                                             const uint8_t* ring_g) {
   using Cfg = Pipe8<D>;
@@ -213,13 +203,16 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
   // row's scores are zero for every key in reach and sh stops there.
   uint32_t qb[NR][NK][2];
   float rs[NR][2];  // score to log2 units of rows 2c, 2c + 1 of each n-tile
-  int lim[NR][2];
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
     const int r = nt * 8 + g;
     const bool ok = r < u.n_rows;
-    const uint2* src = reinterpret_cast<const uint2*>(
-        ok ? unit_query<D, EXTEND>(a, u, r) : a.q);
+    const uint2* src = reinterpret_cast<const uint2*>(a.q);
+    if (ok) {
+      const int m = r / a.group;
+      src = reinterpret_cast<const uint2*>(
+          a.q + (int64_t(u.members[m]) * a.hq + u.kvh * a.group + (r - m * a.group)) * D);
+    }
     float amax = 0.f;
 #pragma unroll
     for (int kk = 0; kk < NK; ++kk) {
@@ -242,10 +235,8 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
         qb[nt][kk][e] = pack_f16(__uint_as_float(qb[nt][kk][e] << 16) * f,
                                  __uint_as_float(qb[nt][kk][e] & 0xffff0000u) * f);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e)
       rs[nt][e] = a.scale_log2 * kv8::pow2(-__shfl_sync(0xffffffffu, sh, 4 * (2 * c + e)));
-      lim[nt][e] = EXTEND ? u.prefix + (u.gr0 + nt * 8 + 2 * c + e) / a.group + 1 : ke;
-    }
   }
 
   float o[NR][NK][4];
@@ -302,15 +293,13 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int end = EXTEND ? min(lim[nt][e], ke) : ke;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float& y = x[nt][i >> 1][(i & 1) * 2 + e];
-          y = key0 + 8 * i < end ? y * (s4[i].x * rs[nt][e]) : -INFINITY;
+          y = key0 + 8 * i < ke ? y * (s4[i].x * rs[nt][e]) : -INFINITY;
           grow |= y > m_ref[nt][e] + kRescaleThreshold;
         }
-      }
     if (__any_sync(0xffffffffu, grow)) {
       float vm = fmaxf(fmaxf(s4[0].y, s4[1].y), fmaxf(s4[2].y, s4[3].y));
       float mx[NR][2];
@@ -412,62 +401,39 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
       if (r >= u.n_rows) continue;
       const float inv = l > 0.f ? unweight / l : 0.f;  // no key: zeros, lse -inf
       const float lse = l > 0.f ? m_ref[nt][e] * kLn2 + logf(l) : -INFINITY;
-      if constexpr (EXTEND) {
-        const int tok = (u.gr0 + r) / a.group;
-        const int64_t row = int64_t(u.q_base + tok) * a.hq + u.kvh * a.group +
-                            (u.gr0 + r - tok * a.group);
+      const int mem = r / a.group;
+      const int64_t at =
+          int64_t(u.part_base + mem) * a.hq + u.kvh * a.group + (r - mem * a.group);
+      float2* dst = reinterpret_cast<float2*>(a.ws_o + at * D);
 #pragma unroll
-        for (int mt = 0; mt < NK; ++mt) {
-          const float y0 = o[nt][mt][e] * inv, y1 = o[nt][mt][2 + e] * inv;
-          if (a.out_bf16)
-            reinterpret_cast<uint32_t*>(a.out)[row * (D / 2) + 8 * mt + g] = rxk::pack_bf16(y0, y1);
-          else
-            reinterpret_cast<float2*>(a.out)[row * (D / 2) + 8 * mt + g] = make_float2(y0, y1);
-        }
-        if (g == 0) a.lse[row] = lse;
-      } else {
-        const int mem = (u.row0 + r) / a.group;
-        const int head = u.kvh * a.group + (u.row0 + r - mem * a.group);
-        const int64_t at = int64_t(u.part_base + mem) * a.hq + head;
-        float2* dst = reinterpret_cast<float2*>(a.ws_o + at * D);
-#pragma unroll
-        for (int mt = 0; mt < NK; ++mt)
-          dst[8 * mt + g] = make_float2(o[nt][mt][e] * inv, o[nt][mt][2 + e] * inv);
-        if (g == 0) a.ws_lse[at] = lse;
-      }
+      for (int mt = 0; mt < NK; ++mt)
+        dst[8 * mt + g] = make_float2(o[nt][mt][e] * inv, o[nt][mt][2 + e] * inv);
+      if (g == 0) a.ws_lse[at] = lse;
     }
 }
 
-// Decode: warps take units (item, KV head, block of query rows) until none is
-// left.
+// Decode, items of few rows: warps take units (item, KV head) until none is
+// left.  With tile items in the plan the kernel is launched after theirs and
+// starts beside it, on the SMs that the tiles leave free and as they finish;
+// it reads nothing that the tiles write, and ends only after they did, so
+// that the merge behind it sees both.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 1) decode8_kernel(const __grid_constant__ Args8 a) {
-  constexpr int NR = D == 128 ? 2 : 1;
-  constexpr int SUB = 128 / (8 * NR);  // row blocks of a large item
-  extern __shared__ __align__(128) uint8_t smem_raw[];
+__global__ void __launch_bounds__(kWarps * 32, 1) stream8_kernel(const __grid_constant__ Args8 a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  rxk::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = rxk::smem_addr(smem_raw);
   const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
   const int hkv = a.hq / a.group;
+  const int n_units = a.n_small * hkv;
   int unit = int(blockIdx.x) * kWarps + warp;
   while (true) {
     if (a.counter) {
       unit = lane == 0 ? atomicAdd(a.counter, 1) : 0;
       unit = __shfl_sync(0xffffffffu, unit, 0);
     }
-    if (unit >= a.n_units) break;
-    int item, sub = 0, kvh;
-    if (unit < a.n_small * hkv) {
-      item = unit / hkv;
-      kvh = unit - item * hkv;
-    } else {
-      const int v = unit - a.n_small * hkv;
-      sub = v % SUB;
-      item = a.n_small + (v / SUB) / hkv;
-      kvh = (v / SUB) % hkv;
-    }
+    if (unit >= n_units) break;
+    const int item = unit / hkv;
     const int32_t* w = a.work + int64_t(item) * RX_WORK_WORDS;
     Unit8 u;
     u.trow = a.table + int64_t(w[0]) * a.row_stride;
@@ -475,47 +441,41 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode8_kernel(const __grid_co
     u.ke = w[7] > 0 ? min(w[2], w[7] + a.step) : w[2];
     u.members = a.members + w[3];
     u.part_base = w[5];
-    u.row0 = sub * 8 * NR;
-    u.n_rows = min(w[6] - u.row0, 8 * NR);
-    u.kvh = kvh;
-    if (u.n_rows > 0) stream_unit<NR, D, false>(a, u, raw + off, smem_raw + off);
+    u.n_rows = w[6];
+    u.kvh = unit - item * hkv;
+    if (u.n_rows <= 8) {
+      stream_unit<1, D>(a, u, raw + off, smem_raw + off);
+    } else if constexpr (D == 128) {
+      stream_unit<2, D>(a, u, raw + off, smem_raw + off);
+    } else if (lane == 0) {
+      atomicOr(&g_kv8_att_error, 1);  // the plan gives head_dim 256 no such item
+    }
     if (!a.counter) break;
   }
+  rxk::griddep_wait();
 }
 
-// Extend: warp w of CTA b takes row block b * kWarps + w, a block of 8 NR of
-// a tile's 128 query rows.
+// Decode, items of more rows: one CTA per (item, KV head).
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 1) extend8_kernel(const __grid_constant__ Args8 a) {
-  constexpr int NR = D == 128 ? 2 : 1;
-  constexpr int SUB = 128 / (8 * NR);
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  const int warp = threadIdx.x >> 5;
-  const uint32_t raw = rxk::smem_addr(smem_raw);
-  const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
+__global__ void __launch_bounds__(kTileThreads, 1)
+    decode8_tile_kernel(const __grid_constant__ Args8 a, const __grid_constant__ CUtensorMap tmk) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  rxk::griddep_launch_dependents();
   const int hkv = a.hq / a.group;
-  const int64_t unit = int64_t(blockIdx.x) * kWarps + warp;
-  if (unit >= int64_t(a.num_tiles) * hkv * SUB) return;
-  const int sub = int(unit % SUB);
-  const int kvh = int((unit / SUB) % hkv);
-  const int tile = int(unit / SUB / hkv);
-  int lo = 0, hi = a.num_req;  // the last request with tile_indptr <= tile
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.tile_indptr + mid) <= tile) lo = mid; else hi = mid;
-  }
-  Unit8 u;
-  u.q_base = a.qo_indptr[lo];
-  u.prefix = a.prefix_len[lo];
-  u.trow = a.table + int64_t(a.req_rows[lo]) * a.row_stride;
-  u.gr0 = (tile - a.tile_indptr[lo]) * 128 + sub * 8 * NR;
-  const int rows = (a.qo_indptr[lo + 1] - u.q_base) * a.group;
-  u.n_rows = min(rows - u.gr0, 8 * NR);
-  if (u.n_rows <= 0) return;
-  u.kb = 0;
-  u.ke = u.prefix + (u.gr0 + u.n_rows - 1) / a.group + 1;
-  u.kvh = kvh;
-  stream_unit<NR, D, true>(a, u, raw + off, smem_raw + off);
+  tile8<D, true>(a, &tmk, smem_raw, int(blockIdx.x) / hkv, int(blockIdx.x) % hkv);
+}
+
+// Extend: one tile per CTA, heaviest row tile first; heads interleaved or
+// head-major, as in the bf16 kernel.
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    extend8_kernel(const __grid_constant__ Args8 a, const __grid_constant__ CUtensorMap tmk) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int c = int(blockIdx.x);
+  const int hkv = a.hq / a.group;
+  const int tile = a.heads_interleaved ? c / hkv : c % a.num_tiles;
+  const int kvh = a.heads_interleaved ? c % hkv : c / a.num_tiles;
+  tile8<D, false>(a, &tmk, smem_raw, a.num_tiles - 1 - tile, kvh);
 }
 
 // One warp per (request, query head): lse = log sum_s exp(lse_s), o = sum_s
@@ -610,6 +570,28 @@ rx_status ensure_smem(std::atomic<bool> (&done)[kMaxDevices], K* kernel, int byt
   return RX_OK;
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map over the pool's K codes [L * Hkv * num_slots rows][D] bytes, box
+// of 128 columns x BN rows, 128-byte swizzle.
+rx_status make_k_map(CUtensorMap* m, const rx_kv8_pool_desc* p, int BN) {
+  EncodeTiled fn = reinterpret_cast<EncodeTiled>(rx_internal::tensor_map_encoder());
+  const cuuint64_t dims[2] = {cuuint64_t(p->head_dim),
+                              cuuint64_t(p->num_layers) * p->num_kv_heads * p->num_slots};
+  const cuuint64_t strides[1] = {cuuint64_t(p->head_dim)};
+  const cuuint32_t box[2] = {128, cuuint32_t(BN)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (!fn ||
+      fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p->k_codes, dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the 8-bit pool's tensor map");
+  return RX_OK;
+}
+
 // The arguments both calls share, checked before any CUDA call.
 rx_status common_args(const char* what, const rx_kv8_pool_desc* pool, int32_t layer,
                       const void* d_q, int32_t num_q_heads, const int32_t* d_table,
@@ -641,6 +623,7 @@ rx_status common_args(const char* what, const rx_kv8_pool_desc* pool, int32_t la
   a->scales = reinterpret_cast<const float2*>(pool->scales) + heads * a->scale_stride;
   a->head_stride = pool->num_slots * D;
   a->num_slots = pool->num_slots;
+  a->tma_row_base = heads * pool->num_slots;
   a->block_log2 = lg;
   a->table = d_table;
   a->row_stride = row_stride;
@@ -678,8 +661,7 @@ extern "C" rx_status rx_kv8_extend_attention(
                              d_req_to_token, row_stride, scale, out_type, &a);
   if (st != RX_OK) return st;
   const int D = pool->head_dim;
-  const int sub = D == 128 ? 8 : 16;
-  if (R < 0 || num_tiles < 0 || num_tiles > INT32_MAX / sub / pool->num_kv_heads)
+  if (R < 0 || num_tiles < 0 || num_tiles > INT32_MAX / pool->num_kv_heads)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_extend_attention: bad R or num_tiles");
   if (R == 0 || num_tiles == 0) return RX_OK;
   if (!d_q || !d_req_to_token || !d_req_rows || !d_prefix_len || !d_qo_indptr ||
@@ -693,17 +675,25 @@ extern "C" rx_status rx_kv8_extend_attention(
   a.num_tiles = int(num_tiles);
   a.out = d_out;
   a.lse = d_lse;
-  const int64_t units = num_tiles * pool->num_kv_heads * sub;
-  const unsigned ctas = unsigned((units + kWarps - 1) / kWarps);
+  // heads interleaved (the heavy row tiles of every head first, a short
+  // tail) for up to 8 waves of CTAs or when a request's keys over all heads
+  // stay in L2 while its row tiles run; otherwise head-major, so the CTAs in
+  // flight read one head's long key ranges
+  a.heads_interleaved = num_tiles * pool->num_kv_heads <= int64_t(8) * rx_internal::sm_count() ||
+                        row_stride * pool->num_kv_heads * int64_t(D) * 2 <= (int64_t(32) << 20);
+  const unsigned ctas = unsigned(num_tiles * pool->num_kv_heads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
-  st = D == 128 ? ensure_smem(done128, extend8_kernel<128>, Pipe8<128>::BYTES)
-                : ensure_smem(done256, extend8_kernel<256>, Pipe8<256>::BYTES);
+  st = D == 128 ? ensure_smem(done128, extend8_kernel<128>, Tile8<128>::BYTES)
+                : ensure_smem(done256, extend8_kernel<256>, Tile8<256>::BYTES);
+  if (st != RX_OK) return st;
+  CUtensorMap tmk;
+  st = make_k_map(&tmk, pool, D == 128 ? Tile8<128>::BN : Tile8<256>::BN);
   if (st != RX_OK) return st;
   if (D == 128)
-    extend8_kernel<128><<<ctas, kWarps * 32, Pipe8<128>::BYTES, s>>>(a);
+    extend8_kernel<128><<<ctas, kTileThreads, Tile8<128>::BYTES, s>>>(a, tmk);
   else
-    extend8_kernel<256><<<ctas, kWarps * 32, Pipe8<256>::BYTES, s>>>(a);
+    extend8_kernel<256><<<ctas, kTileThreads, Tile8<256>::BYTES, s>>>(a, tmk);
   return rx_internal::launch_status("rx_kv8_extend_attention");
 }
 
@@ -729,10 +719,9 @@ extern "C" rx_status rx_kv8_decode_attention(
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: NULL or misaligned");
   const int D = pool->head_dim;
   const int64_t hkv = pool->num_kv_heads;
-  const int64_t sub = D == 128 ? 8 : 16;
   const int64_t n_small = info->n_work - info->n_work_tc;
   if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
-      info->n_work > INT32_MAX / hkv / sub)
+      info->n_work > INT32_MAX / hkv)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: bad plan info");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // the workspace layout of rx_plan_decode: partial rows, their lse, a counter
@@ -745,40 +734,61 @@ extern "C" rx_status rx_kv8_decode_attention(
   a.work = d_plan + info->off_work;
   a.members = d_plan + info->off_members;
   a.n_small = int(n_small);
-  a.n_items = int(info->n_work);
-  a.n_units = int(n_small * hkv + info->n_work_tc * hkv * sub);
   a.step = step;
-  if (a.n_units > 0) {
-    const int64_t sms = rx_internal::sm_count();
-    int64_t ctas = (a.n_units + kWarps - 1) / kWarps;
-    if (ctas > sms) {
-      // more units than warps: taken from a counter, heaviest first
-      ctas = sms;
-      a.counter = counter;
-      if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
-        return rx_internal::launch_status("rx_kv8_decode_attention: counter reset");
-    }
-    static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
-    st = D == 128 ? ensure_smem(done128, decode8_kernel<128>, Pipe8<128>::BYTES)
-                  : ensure_smem(done256, decode8_kernel<256>, Pipe8<256>::BYTES);
-    if (st != RX_OK) return st;
-    if (D == 128)
-      decode8_kernel<128><<<unsigned(ctas), kWarps * 32, Pipe8<128>::BYTES, s>>>(a);
-    else
-      decode8_kernel<256><<<unsigned(ctas), kWarps * 32, Pipe8<256>::BYTES, s>>>(a);
-    st = rx_internal::launch_status("rx_kv8_decode_attention");
-    if (st != RX_OK) return st;
+  const int64_t sms = rx_internal::sm_count();
+  const int64_t small_units = n_small * hkv;
+  int64_t ctas = (small_units + kWarps - 1) / kWarps;
+  if (ctas > sms || (ctas > 0 && info->n_work_tc > 0)) {
+    // more units than warps, or warps that start late (beside the tiles):
+    // units are taken from a counter, heaviest first
+    ctas = std::min(ctas, sms);
+    a.counter = counter;
+    if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
+      return rx_internal::launch_status("rx_kv8_decode_attention: counter reset");
   }
-  // launched while the decode kernel runs; it waits on the device for its end
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned((int64_t(B) * num_q_heads + 7) / 8));
-  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (info->n_work_tc > 0) {
+    static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
+    st = D == 128 ? ensure_smem(done128, decode8_tile_kernel<128>, Tile8<128>::BYTES)
+                  : ensure_smem(done256, decode8_tile_kernel<256>, Tile8<256>::BYTES);
+    CUtensorMap tmk;
+    if (st == RX_OK) st = make_k_map(&tmk, pool, D == 128 ? Tile8<128>::BN : Tile8<256>::BN);
+    if (st != RX_OK) return st;
+    const unsigned n = unsigned(info->n_work_tc * hkv);
+    if (D == 128)
+      decode8_tile_kernel<128><<<n, kTileThreads, Tile8<128>::BYTES, s>>>(a, tmk);
+    else
+      decode8_tile_kernel<256><<<n, kTileThreads, Tile8<256>::BYTES, s>>>(a, tmk);
+    st = rx_internal::launch_status("rx_kv8_decode_attention: tiles");
+    if (st != RX_OK) return st;
+  }
+  if (ctas > 0) {
+    static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
+    st = D == 128 ? ensure_smem(done128, stream8_kernel<128>, Pipe8<128>::BYTES)
+                  : ensure_smem(done256, stream8_kernel<256>, Pipe8<256>::BYTES);
+    if (st != RX_OK) return st;
+    cfg.gridDim = dim3(unsigned(ctas));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = D == 128 ? Pipe8<128>::BYTES : Pipe8<256>::BYTES;
+    cfg.numAttrs = info->n_work_tc > 0 ? 1 : 0;  // beside the tiles only
+    if (D == 128)
+      cudaLaunchKernelEx(&cfg, stream8_kernel<128>, a);
+    else
+      cudaLaunchKernelEx(&cfg, stream8_kernel<256>, a);
+    st = rx_internal::launch_status("rx_kv8_decode_attention: streams");
+    if (st != RX_OK) return st;
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+  }
+  // launched while the kernels before it run; it waits on the device for their end
+  cfg.gridDim = dim3(unsigned((int64_t(B) * num_q_heads + 7) / 8));
+  cfg.blockDim = dim3(256);
   const int32_t* indptr = d_plan + info->off_req_part_indptr;
   const int32_t* parts = d_plan + info->off_req_parts;
   const float* wo = a.ws_o;

@@ -50,6 +50,8 @@ rx_status check_pool(const rx_pool_desc* pool, int32_t layer);
 rx_status check_kv8_pool(const rx_kv8_pool_desc* pool, int32_t layer);
 rx_status launch_status(const char* what);
 int sm_count();
+// The driver's cuTensorMapEncodeTiled, NULL if it cannot be found.
+void* tensor_map_encoder();
 // Error words of the kernels of each file: bit 0 = slot out of range.
 int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
