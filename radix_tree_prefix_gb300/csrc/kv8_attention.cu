@@ -16,7 +16,6 @@
 // tensor-core tile of kv8_tile.cuh; decode items of few rows (a request's own
 // tail) on warps that stream the keys (stream_unit below).
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -39,11 +38,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-// The softmax reference of a row moves when a score exceeds it by 2^8, and
-// weights are scaled by 2^7 and by 1 / vref with vref >= vs: at most 2^15,
-// within f16, and full f16 precision down to p vs / vref = 2^-21.
-constexpr float kRescaleThreshold = 8.0f;
-constexpr float kWeightBias = 128.f;
+// The softmax reference of a row moves when a score exceeds it by 2^9, and
+// weights are scaled by 2^6: at most 2^15, within f16, and full f16 precision
+// down to 2^-20 of the reference.
+constexpr float kRescaleThreshold = 9.0f;
+constexpr float kWeightBias = 6.f;
 
 struct Args8 {
   const bf16* q;
@@ -53,7 +52,7 @@ struct Args8 {
   int64_t head_stride;   // bytes between KV heads (num_slots * D)
   int64_t scale_stride;  // scales between KV heads
   int64_t num_slots;
-  int64_t tma_row_base;  // row of (layer, KV head 0, slot 0) in the tensor map
+  int64_t tma_row_base;  // row of (layer, KV head 0, slot 0) in the tensor maps
   int block_log2;
   const int32_t* table;
   int64_t row_stride;
@@ -345,12 +344,12 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
     // accumulators' (key g, rows 2c, 2c+1)
     float wv[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wv[i] = s4[i].y * inv_vref * kWeightBias;
+    for (int i = 0; i < 4; ++i) wv[i] = s4[i].y * inv_vref;
     uint32_t pb[NR][4];
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
-      const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
-      const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+      const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0] - kWeightBias;
+      const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1] - kWeightBias;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p0 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2] - m0);
@@ -388,7 +387,6 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
   rxk::cp_async_wait<0>();
 
   // rows nt * 8 + 2c + e: output columns 16 mt + 2g, + 1
-  const float unweight = vref * (1.f / kWeightBias);
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -399,8 +397,10 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const int r = nt * 8 + 2 * c + e;
       if (r >= u.n_rows) continue;
-      const float inv = l > 0.f ? unweight / l : 0.f;  // no key: zeros, lse -inf
-      const float lse = l > 0.f ? m_ref[nt][e] * kLn2 + logf(l) : -INFINITY;
+      // (2^6 in both O and l; no key: zeros, lse -inf)
+      const float inv = l > 0.f ? vref / l : 0.f;
+      const float lse =
+          l > 0.f ? (m_ref[nt][e] - kWeightBias) * kLn2 + logf(l) : -INFINITY;
       const int mem = r / a.group;
       const int64_t at =
           int64_t(u.part_base + mem) * a.hq + u.kvh * a.group + (r - mem * a.group);
@@ -458,24 +458,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream8_kernel(const __grid_co
 // Decode, items of more rows: one CTA per (item, KV head).
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    decode8_tile_kernel(const __grid_constant__ Args8 a, const __grid_constant__ CUtensorMap tmk) {
+    decode8_tile_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
   const int hkv = a.hq / a.group;
-  tile8<D, true>(a, &tmk, smem_raw, int(blockIdx.x) / hkv, int(blockIdx.x) % hkv);
+  tile8<D, true>(a, maps, smem_raw, int(blockIdx.x) / hkv, int(blockIdx.x) % hkv);
 }
 
 // Extend: one tile per CTA, heaviest row tile first; heads interleaved or
 // head-major, as in the bf16 kernel.
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    extend8_kernel(const __grid_constant__ Args8 a, const __grid_constant__ CUtensorMap tmk) {
+    extend8_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int c = int(blockIdx.x);
   const int hkv = a.hq / a.group;
   const int tile = a.heads_interleaved ? c / hkv : c % a.num_tiles;
   const int kvh = a.heads_interleaved ? c % hkv : c / a.num_tiles;
-  tile8<D, false>(a, &tmk, smem_raw, a.num_tiles - 1 - tile, kvh);
+  tile8<D, false>(a, maps, smem_raw, a.num_tiles - 1 - tile, kvh);
 }
 
 // One warp per (request, query head): lse = log sum_s exp(lse_s), o = sum_s
@@ -575,20 +575,24 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Tensor map over the pool's K codes [L * Hkv * num_slots rows][D] bytes, box
-// of 128 columns x BN rows, 128-byte swizzle.
-rx_status make_k_map(CUtensorMap* m, const rx_kv8_pool_desc* p, int BN) {
+// Tensor maps over the pool's K codes [L * Hkv * num_slots rows][D] bytes, 128-
+// byte swizzle.
+rx_status make_maps(Maps8* m, const rx_kv8_pool_desc* p) {
   EncodeTiled fn = reinterpret_cast<EncodeTiled>(rx_internal::tensor_map_encoder());
   const cuuint64_t dims[2] = {cuuint64_t(p->head_dim),
                               cuuint64_t(p->num_layers) * p->num_kv_heads * p->num_slots};
   const cuuint64_t strides[1] = {cuuint64_t(p->head_dim)};
-  const cuuint32_t box[2] = {128, cuuint32_t(BN)};
   const cuuint32_t estr[2] = {1, 1};
-  if (!fn ||
-      fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p->k_codes, dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the 8-bit pool's tensor map");
+  auto encode = [&](CUtensorMap* map, cuuint32_t rows) {
+    const cuuint32_t box[2] = {128, rows};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p->k_codes, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const int rows = p->head_dim == 128 ? Tile8<128>::BN : Tile8<256>::BN;
+  if (!fn || !encode(&m->k, rows) || !encode(&m->k16, 16))
+    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the 8-bit pool's tensor maps");
   return RX_OK;
 }
 
@@ -686,14 +690,13 @@ extern "C" rx_status rx_kv8_extend_attention(
   static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
   st = D == 128 ? ensure_smem(done128, extend8_kernel<128>, Tile8<128>::BYTES)
                 : ensure_smem(done256, extend8_kernel<256>, Tile8<256>::BYTES);
-  if (st != RX_OK) return st;
-  CUtensorMap tmk;
-  st = make_k_map(&tmk, pool, D == 128 ? Tile8<128>::BN : Tile8<256>::BN);
+  Maps8 maps;
+  if (st == RX_OK) st = make_maps(&maps, pool);
   if (st != RX_OK) return st;
   if (D == 128)
-    extend8_kernel<128><<<ctas, kTileThreads, Tile8<128>::BYTES, s>>>(a, tmk);
+    extend8_kernel<128><<<ctas, kTileThreads, Tile8<128>::BYTES, s>>>(a, maps);
   else
-    extend8_kernel<256><<<ctas, kTileThreads, Tile8<256>::BYTES, s>>>(a, tmk);
+    extend8_kernel<256><<<ctas, kTileThreads, Tile8<256>::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_kv8_extend_attention");
 }
 
@@ -757,14 +760,14 @@ extern "C" rx_status rx_kv8_decode_attention(
     static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
     st = D == 128 ? ensure_smem(done128, decode8_tile_kernel<128>, Tile8<128>::BYTES)
                   : ensure_smem(done256, decode8_tile_kernel<256>, Tile8<256>::BYTES);
-    CUtensorMap tmk;
-    if (st == RX_OK) st = make_k_map(&tmk, pool, D == 128 ? Tile8<128>::BN : Tile8<256>::BN);
+    Maps8 maps;
+    if (st == RX_OK) st = make_maps(&maps, pool);
     if (st != RX_OK) return st;
     const unsigned n = unsigned(info->n_work_tc * hkv);
     if (D == 128)
-      decode8_tile_kernel<128><<<n, kTileThreads, Tile8<128>::BYTES, s>>>(a, tmk);
+      decode8_tile_kernel<128><<<n, kTileThreads, Tile8<128>::BYTES, s>>>(a, maps);
     else
-      decode8_tile_kernel<256><<<n, kTileThreads, Tile8<256>::BYTES, s>>>(a, tmk);
+      decode8_tile_kernel<256><<<n, kTileThreads, Tile8<256>::BYTES, s>>>(a, maps);
     st = rx_internal::launch_status("rx_kv8_decode_attention: tiles");
     if (st != RX_OK) return st;
   }

@@ -5,8 +5,8 @@
 // Per key tile of BN keys (128 at head_dim 128, 64 at 256):
 //   S = Q K^T      kind::f8f6f4, K's codes as they lie in the pool and Q as a
 //                  sum of two e4m3 operands;
-//   softmax        x = S ks rs, P = 2^(x - m) vs / vref in f16 into TMEM;
-//   O += P V       kind::f16, V's codes converted to f16 in shared memory.
+//   softmax        x = S ks rs, P = 2^(x - m + 6) in f16 into TMEM;
+//   O += P V       kind::f16, V's codes converted to f16 times vs / vref.
 // Q split: a bf16 query has 8 significant bits, an e4m3 number 4.  With the
 // row scaled by a power of two to at most 448, hi = e4m3(q) and lo =
 // e4m3(q - hi) add up to q exactly down to 2^-10 of the row's largest
@@ -16,16 +16,22 @@
 // not taken: a weight below 2^-18 of the row's largest would be lost, and
 // long contexts with one dominant key have most of their sum there.  P stays
 // f16, so V is converted.
+// vref is at least the largest V scale of the tile and the tiles before it (O
+// is rescaled when it grows, which a factor of 4 of headroom makes rare).  A
+// power-of-two scale, what rx_kv8_store writes, is exact in f16 over vref; any
+// other is rounded there, and again in its product with a code.
 //
 // 512 threads:
 //   warps 0-7    softmax in two warpgroups that split every key tile's keys;
 //                thread (w, i) owns query row i = TMEM lane i;
-//   warp 8       issues S; warp 10 issues P V;
-//   warp 9       loads K's codes (one TMA box per 128 columns where the tile's
-//                slots form a contiguous run, else a cp.async gather) and the
-//                tile's scales;
-//   warps 12-15  read V's codes into registers a tile ahead, convert them and
-//                write them to swizzled shared memory.
+//   warps 8-11   convert V: codes into registers a tile ahead, by slot, then to
+//                swizzled shared memory;
+//   warp 12      issues S; warp 13 issues P V;
+//   warp 14      loads K's codes, TMA boxes where the slots of the tile or of 16
+//                keys of it are consecutive (runs and pages), and a cp.async
+//                gather for other groups of 16; and the tile's scales.
+// The roles run side by side, so the code of their loops together is the
+// working set of the instruction cache (32 KB): what is rare is kept rolled.
 // Every mbarrier wait is bounded; on a timeout the CTA sets an error bit,
 // drains its tensor-core work and frees TMEM before returning.
 #pragma once
@@ -46,27 +52,32 @@ template <int HEAD_DIM>
 struct Tile8 {
   static constexpr int D = HEAD_DIM;
   static constexpr int BN = D == 128 ? 128 : 64;
-  static constexpr int NB = 3;     // S buffers and K stages
-  static constexpr int NV = 2;     // V stages
-  static constexpr int SR = 8;     // scale ring
-  static constexpr int Q_BYTES = BM * D;  // of each part
+  static constexpr int NS = 3;             // S buffers (TMEM)
+  static constexpr int NB = 3;             // K stages
+  static constexpr int NV = 2;             // V stages
+  static constexpr int SR = 8;             // ring of the tiles' scales
+  static constexpr int Q_BYTES = BM * D;   // of each part
   static constexpr int K_BYTES = BN * D;
   static constexpr int V_BYTES = BN * D * 2;
   static constexpr int Q = 0;
   static constexpr int K0 = Q + 2 * Q_BYTES;
   static constexpr int V0 = K0 + NB * K_BYTES;
-  static constexpr int XCH = V0 + NV * V_BYTES;    // [2][2 warpgroups][128] floats
-  static constexpr int KS = XCH + 2 * 2 * 128 * 4;  // [SR][BN] K scales
-  static constexpr int VS = KS + SR * BN * 4;       // [SR][BN] 2^7 vs / vref
-  static constexpr int VREF = VS + SR * BN * 4;     // [SR]
+  static constexpr int XCH = V0 + NV * V_BYTES;      // [2][2 warpgroups][128] floats
+  static constexpr int KS = XCH + 2 * 2 * 128 * 4;   // [SR][BN] K scales
+  static constexpr int VREF = KS + SR * BN * 4;      // [SR]
   static constexpr int BAR = VREF + SR * 4;
-  // q, kfull[NB], vfull[NV], s[NB], p[NB], o[2], pf[NB], xch[2], sum, final, scales[SR]
-  static constexpr int NBAR = 1 + NB + NV + NB + NB + 2 + NB + 2 + 1 + 1 + SR;
+  // q, kfull[NB], vfull[NV], s[NS], p[NS], o[2], pf[NS], xch[2], sum, final
+  static constexpr int NBAR = 1 + NB + NV + 3 * NS + 2 + 2 + 1 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16 + 1024;  // slack to align the swizzled tiles
-  static constexpr int O_COL = D == 128 ? NB * BN : 256;
-  static_assert(NB * BN <= O_COL && O_COL + D <= 512, "TMEM budget");
+  static constexpr int O_COL = D == 128 ? NS * BN : 256;
+  static_assert(NS * BN <= O_COL && O_COL + D <= 512, "TMEM budget");
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
+};
+
+// Tensor maps of the pool's K codes: boxes of 128 columns by a tile's keys or 16.
+struct Maps8 {
+  CUtensorMap k, k16;
 };
 
 struct TileDesc8 {
@@ -150,7 +161,8 @@ __device__ __forceinline__ void st_shared_16(uint32_t at, uint32_t a, uint32_t b
                : "memory");
 }
 
-// D(tmem) (+)= A B, descriptors as 32-bit halves with a common high half.
+// D(tmem) (+)= A B, shared-memory descriptors as 32-bit halves with a common
+// high half.
 __device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -179,6 +191,28 @@ __device__ __forceinline__ void tmem_st16x(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
+// Four e4m3 codes as two f16 pairs, exactly.
+__device__ __forceinline__ void to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Add `bytes` to the transaction count of the barrier's phase.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
@@ -206,37 +240,39 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 template <int D, bool DECODE>
-__device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, uint8_t* smem_raw,
+__device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t* smem_raw,
                                       int tile, int kvh) {
   using Lo = Tile8<D>;
-  constexpr int BN = Lo::BN, NB = Lo::NB, NV = Lo::NV, SR = Lo::SR;
+  constexpr int BN = Lo::BN, NB = Lo::NB, NV = Lo::NV, NS = Lo::NS, SR = Lo::SR;
   const uint32_t raw = rxk::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t sQ = base + Lo::Q;
   const uint32_t bar = base + Lo::BAR;
+  // Rings of n barriers: entry j % n completes its phase j / n for tile j.
+  constexpr uint32_t kKF = 1, kVF = kKF + NB, kS = kVF + NV, kP = kS + NS, kO = kP + NS,
+                     kPF = kO + 2, kX = kPF + NS, kXE = kX + 2, kFin = kXE + 1;
+  static_assert(kFin + 1 == Lo::NBAR, "barrier count");
   const uint32_t BAR_Q = bar;
-  auto BAR_KF = [&](int s) { return bar + 8u * (1 + s); };
-  auto BAR_VF = [&](int s) { return bar + 8u * (1 + NB + s); };
-  auto BAR_S = [&](int b) { return bar + 8u * (1 + NB + NV + b); };
-  auto BAR_P = [&](int b) { return bar + 8u * (1 + 2 * NB + NV + b); };
-  constexpr uint32_t kAfterP = 1 + 3 * NB + NV;
-  // PV_j completes phase j / 2 of BAR_O(j % 2) and phase j / NB of BAR_PF(j %
-  // NB).  S_j is issued after PV_{j-NB} completed, so once S_j is complete,
-  // PV_{j-3} is, and a wait for PV_{j-1} on BAR_O cannot see an older phase.
-  auto BAR_O = [&](int p) { return bar + 8u * (kAfterP + p); };
-  auto BAR_PF = [&](int b) { return bar + 8u * (kAfterP + 2 + b); };
-  auto XB = [&](int p) { return bar + 8u * (kAfterP + 2 + NB + p); };
-  const uint32_t XE = bar + 8u * (kAfterP + 4 + NB);
-  const uint32_t BAR_FIN = bar + 8u * (kAfterP + 5 + NB);
-  // the scales of tile j complete phase j / SR of BAR_SC(j % SR)
-  auto BAR_SC = [&](int s) { return bar + 8u * (kAfterP + 6 + NB + s); };
-  static_assert(kAfterP + 6 + NB + SR == Lo::NBAR, "barrier count");
+  auto BAR_KF = [&](int j) { return bar + 8u * (kKF + j % NB); };  // K converted
+  auto BAR_VF = [&](int j) { return bar + 8u * (kVF + j % NV); };  // V converted
+  auto BAR_S = [&](int j) { return bar + 8u * (kS + j % NS); };    // S_j complete
+  auto BAR_P = [&](int j) { return bar + 8u * (kP + j % NS); };    // P_j written
+  // P V_j complete, in a ring of two and one of NS.  S_j is issued after PV_{j-NS}
+  // completed, so once S_j is complete, PV_{j-3} is, and a wait for PV_{j-1} on
+  // BAR_O cannot see an older phase.
+  auto BAR_O = [&](int j) { return bar + 8u * (kO + (j & 1)); };
+  auto BAR_PF = [&](int j) { return bar + 8u * (kPF + j % NS); };
+  auto XB = [&](int j) { return bar + 8u * (kX + (j & 1)); };
+  const uint32_t XE = bar + 8u * kXE;
+  const uint32_t BAR_FIN = bar + 8u * kFin;
+  auto wait = [&](uint32_t b, int phase, volatile int* abort) {
+    return tc::mbar_wait(b, uint32_t(phase) & 1u, abort, kWaitLimit);
+  };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lo::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
   float* xch = reinterpret_cast<float*>(gbase + Lo::XCH);
   float* ks_ring = reinterpret_cast<float*>(gbase + Lo::KS);
-  float* vs_ring = reinterpret_cast<float*>(gbase + Lo::VS);
   float* vref_ring = reinterpret_cast<float*>(gbase + Lo::VREF);
 
   const int tid = threadIdx.x;
@@ -244,10 +280,6 @@ __device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, ui
   const int lane = tid & 31;
   const TileDesc8 t = describe8<DECODE>(a, tile);
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
-  // a tile of at most 64 rows runs M = 64 products; its row r then sits in
-  // TMEM lane 32 (r / 16) + r % 16
-  const bool m64 = t.n_rows <= 64;
-
   // ---- Q: thread (wg, i) reads half of query row i
   const int wg = warp >> 2;
   const int i = (warp & 3) * 32 + lane;
@@ -272,25 +304,24 @@ __device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, ui
     xch[wg * BM + i] = amax;
   }
   if (tid == 0) {
-    tc::mbar_init(BAR_Q, 8 * 32);
-    for (int s = 0; s < NV; ++s) tc::mbar_init(BAR_VF(s), 4);
-    for (int b = 0; b < NB; ++b) {
-      tc::mbar_init(BAR_KF(b), 1);
-      tc::mbar_init(BAR_S(b), 1);
-      tc::mbar_init(BAR_P(b), 8 * 32);
-      tc::mbar_init(BAR_PF(b), 1);
+    tc::mbar_init(BAR_Q, 8);
+    for (int j = 0; j < NB; ++j) tc::mbar_init(BAR_KF(j), 2);  // the codes, and the scales
+    for (int j = 0; j < NV; ++j) tc::mbar_init(BAR_VF(j), 4);
+    for (int j = 0; j < NS; ++j) {
+      tc::mbar_init(BAR_S(j), 2);  // the commit, and the issuer
+      tc::mbar_init(BAR_P(j), 8);
+      tc::mbar_init(BAR_PF(j), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(BAR_O(b), 1);
-      tc::mbar_init(XB(b), 8 * 32);
+    for (int j = 0; j < 2; ++j) {
+      tc::mbar_init(BAR_O(j), 1);
+      tc::mbar_init(XB(j), 8 * 32);
     }
     tc::mbar_init(XE, 8 * 32);
     tc::mbar_init(BAR_FIN, 2);  // one commit per issuing thread
-    for (int s = 0; s < SR; ++s) tc::mbar_init(BAR_SC(s), 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tc::tmem_alloc(rxk::smem_addr(tmem_slot), 512);
     tc::tmem_relinquish();
   }
@@ -299,467 +330,513 @@ __device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, ui
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Registers by warpgroup: 2 x 152 + 88 + 120 = 4 x 128, what the block was
+  // Registers by warpgroup: 2 x 152 + 120 + 88 = 4 x 128, what the block was
   // launched with.
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-  if (warp == 9) {
-    // ------------------------------------------------- K and scale loader
-    constexpr int SPL = BN / 32;  // keys lane + 32 i of a tile
-    constexpr int LPR = D / 16;   // 16-byte chunks per row
-    const uint8_t* kb = a.kc + int64_t(kvh) * a.head_stride;
-    const float2* sb = a.scales + int64_t(kvh) * a.scale_stride;
+  if (warp == 14) {
+    // ------------------------------------------------------------ K loader
+    constexpr int LPR = D / 16;   // 16-byte pieces per row
+    constexpr int RPI = 32 / LPR;  // rows a gather instruction copies
+    constexpr int rows = BN;
+    constexpr int SPL = BN / 32;
+    const uint8_t* src0 = a.kc + int64_t(kvh) * a.head_stride + (lane % LPR) * 16;
     const int64_t row0 = a.tma_row_base + int64_t(kvh) * a.num_slots;
-    // slots of tile j + 2 and scales of tile j + 1 are in flight while tile
-    // j is loaded
-    auto load_slots = [&](int j, int32_t (&dst)[SPL]) {
-      const int k0 = t.key_begin + j * BN;
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) {
-        const int key = k0 + lane + 32 * e;
-        dst[e] = (j < n_tiles && key < t.key_end) ? __ldg(t.trow + key) : -1;
-      }
-    };
-    auto check_slots = [&](int j, int32_t (&s)[SPL]) {
-      const int k0 = t.key_begin + j * BN;
+    // lane l holds the slots of keys l, l + 32, .. of a tile; the next tile's
+    // are on their way while one is loaded
+    int32_t cur[SPL], nxt[SPL];
+    auto load_slots = [&](int k0, int32_t (&dst)[SPL]) {
 #pragma unroll
       for (int e = 0; e < SPL; ++e)
-        if (j < n_tiles && k0 + lane + 32 * e < t.key_end && (s[e] < 0 || s[e] >= a.num_slots)) {
-          atomicOr(&g_kv8_att_error, 1);
-          s[e] = 0;
-        }
+        dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(t.trow + k0 + lane + 32 * e) : -1;
     };
-    auto load_scales = [&](const int32_t (&s)[SPL], float2 (&dst)[SPL]) {
-#pragma unroll
-      for (int e = 0; e < SPL; ++e)
-        dst[e] = s[e] >= 0 ? __ldg(sb + (s[e] >> a.block_log2)) : make_float2(0.f, 0.f);
-    };
-    int32_t cur[SPL], nxt[SPL], nx2[SPL];
+    load_slots(t.key_begin, nxt);
+    // It passes on the scales too: K's, and vref.  The next tile's are read a
+    // tile ahead.
+    const float2* sb = a.scales + int64_t(kvh) * a.scale_stride;
     float2 sc[SPL], sn[SPL];
-    load_slots(0, cur);
-    load_slots(1, nxt);
-    check_slots(0, cur);
-    load_scales(cur, sc);
-    float vref = 0.f;
-    int pend = -1;    // gathered tile whose arrival is still to be signalled
-    int issued = 0;
-    for (int j = 0; j < n_tiles; ++j) {
-      load_slots(j + 2, nx2);
-      check_slots(j + 1, nxt);
-      load_scales(nxt, sn);
-      // stage j % NB is free once S_{j-NB} completed, and the scales of tile
-      // j - SR have been read then (softmax j - 2 NB is done)
-      const int st = j % NB;
-      if (j >= NB && !__all_sync(0xffffffffu, tc::mbar_wait(BAR_S(st), uint32_t(j / NB - 1) & 1u,
-                                                             abort_flag, kWaitLimit)))
-        break;
-      float vm = 0.f;
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) vm = fmaxf(vm, sc[e].y);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-      vref = fmaxf(vref, vm);
-      const float inv = 1.f / vref;
+    auto load_scales = [&](int k0, const int32_t (&s)[SPL], float2 (&dst)[SPL]) {
 #pragma unroll
       for (int e = 0; e < SPL; ++e) {
-        ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x;
-        vs_ring[(j % SR) * BN + lane + 32 * e] = sc[e].y * inv * kWeightBias;
+        // (a bad slot is reported and read as slot 0 when its tile is loaded)
+        const uint32_t at = uint32_t(s[e]) < uint32_t(a.num_slots) ? uint32_t(s[e]) : 0u;
+        dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(sb + (at >> a.block_log2))
+                                                : make_float2(0.f, 0.f);
       }
-      if (lane == 0) vref_ring[j % SR] = vref;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(BAR_SC(j % SR));
-
-      const uint32_t dst = base + Lo::K0 + uint32_t(st * Lo::K_BYTES);
-      const int32_t first = __shfl_sync(0xffffffffu, cur[0], 0);
-      bool run = first >= 0 && int64_t(first) + BN <= a.num_slots;
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) run = run && cur[e] == first + lane + 32 * e;
-      run = __all_sync(0xffffffffu, run);
-      if (run) {
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(BAR_KF(st), uint32_t(Lo::K_BYTES));
-#pragma unroll
-          for (int cb = 0; cb < D / 128; ++cb)
-            tc::tma_load_2d(dst + uint32_t(cb * BN * 128), tmk, cb * 128, int(row0 + first),
-                            BAR_KF(st));
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < SPL; ++e)
-#pragma unroll 4
-          for (int k = 0; k < LPR; ++k) {
-            const int row = 32 * e + k * (32 / LPR) + lane / LPR;
-            const int32_t s = __shfl_sync(0xffffffffu, cur[e], row & 31);
-            const int ch = lane % LPR;
-            rxk::cp_async_16(swz(dst, BN, row, ch), kb + int64_t(s < 0 ? 0 : s) * D + ch * 16,
-                             s >= 0);
-          }
-        rxk::cp_async_commit();
-      }
-      issued = j + 1;
-      // a gathered tile is signalled once the next tile's loads are on their
-      // way, so two tiles' round trips overlap
-      if (pend >= 0) {
-        if (run)
-          rxk::cp_async_wait<0>();
-        else
-          rxk::cp_async_wait<1>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(BAR_KF(pend % NB));
-      }
-      pend = run ? -1 : j;
-      if (pend >= 0 && j + 1 == n_tiles) {
-        rxk::cp_async_wait<0>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(BAR_KF(pend % NB));
-        pend = -1;
-      }
+    };
+    float vref = 0.f;
+    load_scales(t.key_begin, nxt, sn);
+    uint32_t pend = 0;  // barrier of gathered rows whose arrival is still to be signalled
+    int j = 0;
+#pragma unroll 1
+    for (; j < n_tiles; ++j) {
+      const int k0 = t.key_begin + j * rows;
+      bool bad = false, whole = true;
 #pragma unroll
       for (int e = 0; e < SPL; ++e) {
         cur[e] = nxt[e];
-        nxt[e] = nx2[e];
-        sc[e] = sn[e];
+        if (k0 + lane + 32 * e < t.key_end && (cur[e] < 0 || cur[e] >= a.num_slots)) {
+          bad = true;
+          cur[e] = 0;
+        }
       }
+      load_slots(k0 + rows, nxt);
+      if (bad) atomicOr(&g_kv8_att_error, 1);
+      const int32_t first = __shfl_sync(0xffffffffu, cur[0], 0);
+#pragma unroll
+      for (int e = 0; e < SPL; ++e) whole = whole && cur[e] == first + lane + 32 * e;
+      whole = __all_sync(0xffffffffu, whole && first >= 0);
+      // stage j % NB is free once S_{j-NB} completed
+      static_assert(NB == NS, "a K stage is freed by the S of its index");
+      if (j >= NB && !__all_sync(0xffffffffu, wait(BAR_S(j), j / NB - 1, abort_flag))) break;
+      const uint32_t full = BAR_KF(j), dst = base + Lo::K0 + uint32_t((j % NB) * Lo::K_BYTES);
+      uint32_t done = 0;  // barrier of this stage, if it needs a signal later
+      if (whole) {
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(full, uint32_t(rows * D));
+#pragma unroll
+          for (int cb = 0; cb < D / 128; ++cb)
+            tc::tma_load_2d(dst + uint32_t(cb * rows * 128), &maps.k, cb * 128, int(row0 + first), full);
+        }
+      } else {
+        // groups of 16 keys: a box load where their slots are consecutive;
+        // the rest is gathered (past the key range a slot is -1, its row zeros)
+        uint32_t run = 0;
+        int32_t gfirst = 0;  // lane g: first slot of group g
+#pragma unroll
+        for (int e = 0; e < SPL; ++e) {
+          const int32_t f = __shfl_sync(0xffffffffu, cur[e], lane & 16);
+          const uint32_t m = __ballot_sync(0xffffffffu, f >= 0 && cur[e] == f + (lane & 15));
+          if ((m & 0xffffu) == 0xffffu) run |= 1u << (2 * e);
+          if (m >> 16 == 0xffffu) run |= 2u << (2 * e);
+          const int32_t g = __shfl_sync(0xffffffffu, cur[e], (lane & 1) << 4);
+          if ((lane >> 1) == e) gfirst = g;
+        }
+        const bool all = __popc(run) * 16 == rows;
+        if (lane == 0 && run) {
+          const uint32_t bytes = uint32_t(__popc(run)) * 16u * D;
+          if (all)
+            tc::mbar_arrive_expect_tx(full, bytes);
+          else
+            mbar_expect_tx(full, bytes);
+        }
+        __syncwarp();
+        if (lane < 8 && ((run >> lane) & 1u)) {
+#pragma unroll 1
+          for (int cb = 0; cb < D / 128; ++cb)
+            tc::tma_load_2d(dst + uint32_t(cb * rows * 128 + lane * 16 * 128), &maps.k16, cb * 128,
+                            int(row0 + gfirst), full);
+        }
+        if (!all) {
+#pragma unroll 1
+          for (int e = 0; e < rows / 32; ++e) {
+            int32_t ce = cur[0];
+#pragma unroll
+            for (int u = 1; u < SPL; ++u)
+              if (e == u) ce = cur[u];
+#pragma unroll 4
+            for (int k = 0; k < 32; k += RPI) {
+              const int row = k + lane / LPR;
+              const int32_t sl = __shfl_sync(0xffffffffu, ce, row);
+              if (!((run >> (2 * e + (row >> 4))) & 1u))
+                rxk::cp_async_16(swz(dst, rows, 32 * e + row, lane % LPR),
+                                 src0 + int64_t(sl < 0 ? 0 : sl) * D, sl >= 0);
+            }
+          }
+          rxk::cp_async_commit();
+          done = full;
+        }
+      }
+      // a gathered stage is signalled once the next one's loads are on their
+      // way, so two stages' round trips overlap
+      if (pend) {
+        if (done)
+          rxk::cp_async_wait<1>();
+        else
+          rxk::cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(pend);
+      }
+      pend = done;
+      // S_{j-NB} has completed, so the softmax of tile j - NB - NS is done, and
+      // with it every read of the ring's entry
+      static_assert(SR > NB + NS, "scale ring");
+#pragma unroll
+      for (int e = 0; e < SPL; ++e) sc[e] = sn[e];
+      load_scales(k0 + rows, nxt, sn);
+      float vm = 0.f;
+#pragma unroll
+      for (int e = 0; e < SPL; ++e) {
+        vm = fmaxf(vm, sc[e].y);
+        ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x;
+      }
+      // (positive floats compare as integers)
+      vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+      if (vm > vref) vref = 4.f * vm;
+      if (lane == 0) vref_ring[j % SR] = vref;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(BAR_KF(j));
     }
-    // no copy is in flight when the CTA gives up its shared memory (after an
-    // abort, a box load may still be)
     rxk::cp_async_wait<0>();
-    if (lane == 0) {
+    if (pend) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(pend);
+    }
+    // No copy is in flight when the CTA gives up its shared memory: every box
+    // load has been consumed, unless a wait gave up, and then the stages' last
+    // phases get one more bounded wait.
+    if (lane == 0 && *abort_flag) {
       int drain_abort = 0;
-      const int end = pend >= 0 ? pend : issued;  // a gather never signalled is not waited for
-      for (int j = end > NB ? end - NB : 0; j < end; ++j)
-        tc::mbar_wait(BAR_KF(j % NB), uint32_t(j / NB) & 1u, &drain_abort, kWaitLimit);
+      for (int e = j > NB ? j - NB : 0; e < j; ++e) wait(BAR_KF(e), e / NB, &drain_abort);
     }
     __syncwarp();
-  } else if (warp == 8 || warp == 10) {
+  } else if (warp < 14) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
-      const uint32_t MN = m64 ? 64 : BM;
       // shared-memory descriptors: 128-byte swizzle, 1024 bytes between
       // 8-row groups, version 1
       constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
-      static_assert(Lo::V0 + NV * Lo::V_BYTES < (1 << 18), "descriptor address field");
-      if (warp == 8) {
+      static_assert(Lo::XCH < (1 << 18), "descriptor address field");
+      if (warp == 12) {
         // e4m3 A and B (type 0), fp32 accumulator, both K-major
-        const uint32_t idesc = (1u << 4) | (uint32_t(BN >> 3) << 17) | ((MN >> 4) << 24);
+        constexpr uint32_t idesc =
+            (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
         const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
         const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
-        const bool ok = tc::mbar_wait(BAR_Q, 0, abort_flag, kWaitLimit);
-        int sb = 0;
-        uint32_t k_phase = 0, pf_phase = 0;
+        const bool ok = wait(BAR_Q, 0, abort_flag);
+#pragma unroll 1
         for (int j = 0; ok && j < n_tiles; ++j) {
-          if (j >= NB && !tc::mbar_wait(BAR_PF(sb), pf_phase, abort_flag, kWaitLimit)) break;
-          if (!tc::mbar_wait(BAR_KF(sb), k_phase, abort_flag, kWaitLimit)) break;
+          // buffer j % NS is free once P V_{j-NS} has read its P
+          if (j >= NS && !wait(BAR_PF(j), j / NS - 1, abort_flag)) break;
+          if (!wait(BAR_KF(j), j / NB, abort_flag)) break;
           tc::tc_fence_after();
-          const uint32_t k_lo = k_lo0 + uint32_t(sb) * (uint32_t(Lo::K_BYTES) >> 4);
-          const uint32_t d_s = tmem + uint32_t(sb * BN);
+          const uint32_t k_lo = k_lo0 + uint32_t(j % NB) * (uint32_t(Lo::K_BYTES) >> 4);
+          const uint32_t d_s = tmem + uint32_t((j % NS) * BN);
+          // Q's two parts by D / 128 blocks of 128 columns, 4 steps each
+#pragma unroll 1
+          for (int blk = 0; blk < 2 * (D / 128); ++blk) {
+            const uint32_t q_at = q_lo + uint32_t(blk) * uint32_t(BM * 128 / 16);
+            const uint32_t k_at = k_lo + uint32_t(blk % (D / 128)) * uint32_t(BN * 128 / 16);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) {
-              const uint32_t a_off =
-                  uint32_t((part * Lo::Q_BYTES + (ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4);
-              const uint32_t b_off = uint32_t(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4);
-              mma8_ss(d_s, q_lo + a_off, k_lo + b_off, DHI, idesc, (part | ks) ? 1u : 0u);
-            }
-          tc::mma_commit(BAR_S(sb));  // also frees K stage sb
-          if (++sb == NB) {
-            sb = 0;
-            k_phase ^= 1u;
-            if (j >= NB) pf_phase ^= 1u;
+            for (int ks = 0; ks < 4; ++ks)
+              mma8_ss(d_s, q_at + uint32_t(ks * 2), k_at + uint32_t(ks * 2), DHI, idesc,
+                      (blk | ks) ? 1u : 0u);
           }
+          tc::mma_commit(BAR_S(j));   // also frees the K stage
+          tc::mbar_arrive(BAR_S(j));  // (passes the scales on, seen through KF)
         }
       } else {
         // f16 A (TMEM) and B (shared, MN-major), fp32 accumulator
-        const uint32_t idesc =
-            (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | ((MN >> 4) << 24);
+        constexpr uint32_t idesc =
+            (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(BM >> 4) << 24);
         const uint32_t v_lo0 =
             (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BN * 128 / 16) << 16);
-        int sv = 0, pb = 0;
-        uint32_t v_phase = 0, p_phase = 0;
+#pragma unroll 1
         for (int j = 0; j < n_tiles; ++j) {
-          if (!tc::mbar_wait(BAR_P(pb), p_phase, abort_flag, kWaitLimit)) break;
-          if (!tc::mbar_wait(BAR_VF(sv), v_phase, abort_flag, kWaitLimit)) break;
+          if (!wait(BAR_VF(j), j / NV, abort_flag)) break;
+          if (!wait(BAR_P(j), j / NS, abort_flag)) break;
           tc::tc_fence_after();
-          const uint32_t v_lo = v_lo0 + uint32_t(sv) * (uint32_t(Lo::V_BYTES) >> 4);
-          const uint32_t p_t = tmem + uint32_t(pb * BN);
+          const uint32_t v_lo = v_lo0 + uint32_t(j % NV) * (uint32_t(Lo::V_BYTES) >> 4);
+          const uint32_t p_t = tmem + uint32_t((j % NS) * BN);
 #pragma unroll
           for (int ks = 0; ks < BN / 16; ++ks)
             mma16_ts(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
                      v_lo + uint32_t(ks * 2048 / 16), DHI, idesc, (j > 0 || ks > 0) ? 1u : 0u);
-          tc::mma_commit(BAR_O(j & 1));  // also frees V stage sv (== j & 1)
-          tc::mma_commit(BAR_PF(pb));    // S buffer pb may take S_{j+NB}
-          if (++sv == NV) {
-            sv = 0;
-            v_phase ^= 1u;
-          }
-          if (++pb == NB) {
-            pb = 0;
-            p_phase ^= 1u;
-          }
+          tc::mma_commit(BAR_O(j));   // also frees the V stage
+          tc::mma_commit(BAR_PF(j));  // S buffer j % NS may take S_{j+NS}
         }
       }
       // drained once both threads' products completed, whatever the abort flag
       tc::mma_commit(BAR_FIN);
       int drain_abort = 0;
-      tc::mbar_wait(BAR_FIN, 0, &drain_abort, kWaitLimit);
+      wait(BAR_FIN, 0, &drain_abort);
     }
     __syncwarp();
   }
-  } else if (warp >= 12) {
+  } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n");
     // ------------------------------------------------------ V converters
-    // A warp instruction reads 32 chunks of 16 codes, whole rows; a thread
-    // has one chunk of NP rows of a tile.  While tile j's codes are converted,
-    // tile j + 1's are in flight and tile j + 2's slots are read.
+    // A warp instruction reads 32 pieces of 16 codes, whole rows; a thread has
+    // a piece of NP rows of a tile, row p * RPP + row_in for p < NP.  A piece's
+    // registers are refilled with the next tile's as soon as it is converted.
     constexpr int LPR = D / 16;
-    constexpr int RPI = 32 / LPR;
-    constexpr int NP = BN / (4 * RPI);
-    const int row_in = (warp - 12) * RPI + lane / LPR;
-    const int c16 = lane % LPR;
-    const uint8_t* vb = a.vc + int64_t(kvh) * a.head_stride + c16 * 16;
-    auto load_slots = [&](int j, int32_t (&dst)[NP]) {
-      const int k0 = t.key_begin + j * BN + row_in;
+    constexpr int RPP = 4 * (32 / LPR);
+    constexpr int NP = BN / RPP;
+    constexpr int SPL = BN / 32;  // keys lane + 32 e of a tile
+    // Lane bits: piece within a column block (2), row (1), column block, row.
+    // A store's phase of 8 lanes is then two rows by four pieces of one column
+    // block, which hit all banks.
+    const int c16 = (lane & 3) | ((lane >> 3) % (LPR / 4)) << 2;
+    const int row_in = (warp & 3) * (32 / LPR) + ((lane >> 2) & 1) + 2 * ((lane >> 3) / (LPR / 4));
+    const uint8_t* src = a.vc + int64_t(kvh) * a.head_stride + c16 * 16;
+    const float2* sb = a.scales + int64_t(kvh) * a.scale_stride;
+    // pieces 2 c16 and 2 c16 + 1 of the f16 row (RPP is a multiple of 8: the
+    // swizzle of all its rows is the same)
+    uint8_t* at0 = gbase + swz(Lo::V0, BN, row_in, 2 * c16);
+    uint8_t* at1 = gbase + swz(Lo::V0, BN, row_in, 2 * c16 + 1);
+    // lane l holds the slots and scales of keys l, l + 32, .. of a tile
+    int32_t slot[SPL];
+    float sc[SPL];
+    uint4 v[NP];
+    auto load_slots = [&](int j) {
+      const int k0 = t.key_begin + j * BN + lane;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int key = k0 + p * 4 * RPI;
-        dst[p] = (j < n_tiles && key < t.key_end) ? __ldg(t.trow + key) : -1;
+      for (int e = 0; e < SPL; ++e)
+        slot[e] = __ldg(t.trow + min(k0 + 32 * e, t.key_end - 1));
+    };
+    // keys past the range take the last key's slot and scales of 0: their weights
+    // are 0, and 0 V is 0 for codes that count anyway
+    auto load_scales = [&](int j) {
+      const int k0 = t.key_begin + j * BN + lane;
+#pragma unroll
+      for (int e = 0; e < SPL; ++e) {
+        // (the K loader reports a bad slot)
+        if (slot[e] < 0 || slot[e] >= a.num_slots) slot[e] = 0;
+        sc[e] = k0 + 32 * e < t.key_end ? __ldg(&sb[slot[e] >> a.block_log2].y) : 0.f;
       }
     };
-    auto load_codes = [&](int32_t (&s)[NP], uint4 (&dst)[NP]) {
+    // piece p is of row p * RPP + row_in, i.e. of the key that lane row % 32 holds
+    // in its entry row / 32 (row_in < RPP <= 16)
+    int32_t s[NP];
+    auto spread_slots = [&]() {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        if (s[p] >= a.num_slots) s[p] = 0;  // (the K loader reports it)
-        // keys past the range are zeros (their weights are 0)
-        dst[p] = s[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(vb + int64_t(s[p]) * D))
-                           : make_uint4(0, 0, 0, 0);
-      }
+      for (int p = 0; p < NP; ++p)
+        s[p] = __shfl_sync(0xffffffffu, slot[(p * RPP) >> 5], ((p * RPP) & 31) + row_in);
     };
-    int32_t slot[NP];
-    uint4 va[NP], vc[NP];
-    load_slots(0, slot);
-    load_codes(slot, va);
-    load_slots(1, slot);
-    auto step = [&](int j, uint4 (&cur)[NP], uint4 (&nxt)[NP]) -> bool {
-      load_codes(slot, nxt);
-      load_slots(j + 2, slot);
-      const int sv = j & 1;
-      if (j >= NV && !__all_sync(0xffffffffu, tc::mbar_wait(BAR_O(sv), uint32_t(j / NV - 1) & 1u,
-                                                             abort_flag, kWaitLimit)))
-        return false;
-      const uint32_t dst = base + Lo::V0 + uint32_t(sv * Lo::V_BYTES);
+    auto load_pieces = [&]() {
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        v[p] = __ldg(reinterpret_cast<const uint4*>(src + uint64_t(uint32_t(s[p])) * D));
+    };
+    load_slots(0);
+    load_scales(0);
+    spread_slots();
+    load_pieces();
+    load_slots(1);
+    float vref = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < n_tiles; ++j) {
+      // vref as the K loader has it, and this tile's quotients
+      float vm = 0.f;
+#pragma unroll
+      for (int e = 0; e < SPL; ++e) vm = fmaxf(vm, sc[e]);
+      vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+      if (vm > vref) vref = 4.f * vm;
+      const float inv = 1.f / vref;
+      uint32_t f[NP];
+      {
+        uint32_t fl[SPL];
+#pragma unroll
+        for (int e = 0; e < SPL; ++e) {
+          fl[e] = pack_f16(sc[e] * inv, sc[e] * inv);
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          f[p] = __shfl_sync(0xffffffffu, fl[(p * RPP) >> 5], ((p * RPP) & 31) + row_in);
+      }
+      load_scales(j + 1);
+      // the stage is free once P V_{j-NV} completed
+      if (!__all_sync(0xffffffffu, j < NV || wait(BAR_O(j), j / 2 - 1, abort_flag))) break;
+      const uint32_t stage = uint32_t((j % NV) * Lo::V_BYTES);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const int row = p * 4 * RPI + row_in;
-        const uint32_t w[4] = {cur[p].x, cur[p].y, cur[p].z, cur[p].w};
+        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
         uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = kv8::to_f16x2((e & 1) ? w[e >> 1] >> 16 : w[e >> 1]);
-        // chunks 2 c16 and 2 c16 + 1 of the f16 row; lanes of the upper column
-        // blocks write theirs in the other order, so that the lanes of a row
-        // hit all banks
-        const bool sw = (c16 >> 2) & 1;
-        const uint32_t a0 = swz(dst, BN, row, 2 * c16 + (sw ? 1 : 0));
-        const uint32_t a1 = swz(dst, BN, row, 2 * c16 + (sw ? 0 : 1));
-        st_shared_16(a0, sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
-        st_shared_16(a1, sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+        for (int e = 0; e < 4; ++e) {
+          to_f16x4(w[e], h[2 * e], h[2 * e + 1]);
+          h[2 * e] = mul_f16x2(h[2 * e], f[p]);
+          h[2 * e + 1] = mul_f16x2(h[2 * e + 1], f[p]);
+        }
+        *reinterpret_cast<uint4*>(at0 + stage + p * RPP * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(at1 + stage + p * RPP * 128) = make_uint4(h[4], h[5], h[6], h[7]);
       }
+      // the next tile's codes, and the slots of the one after it
+      spread_slots();
+      load_pieces();
+      load_slots(j + 2);
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(BAR_VF(sv));
-      return true;
-    };
-    for (int j = 0; j < n_tiles; j += 2) {
-      if (!step(j, va, vc)) break;
-      if (j + 1 < n_tiles && !step(j + 1, vc, va)) break;
+      if (lane == 0) tc::mbar_arrive(BAR_VF(j));
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     // ------------------------------------------------------------ softmax
     constexpr int HALF = BN / 2;
+    const bool valid = i < t.n_rows;
+    int lim = t.key_end;
+    if (valid && !DECODE) lim = t.prefix + (t.gr0 + i) / a.group + 1;
     const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
-    // the row this thread's Q half belongs to, and its scale: 2^e with q 2^-e
-    // at most 448 (limited below, where the scores vanish anyway)
+    // The row's scale: 2^e with q 2^-e at most 448 (limited below, where the
+    // scores vanish anyway).  A query that is not finite has no defined
+    // scores: its row is NaN.
     const float qmax = fmaxf(xch[i], xch[BM + i]);
     const int qe = max(kv8::scale_exponent(qmax), -80);
-    const float qinv = kv8::pow2(-qe);
+    const float rs = qmax < INFINITY ? a.scale_log2 * kv8::pow2(qe) : NAN;
+    {
+      const float qinv = kv8::pow2(-qe);
 #pragma unroll
-    for (int c = 0; c < QC; c += 2) {
-      uint32_t hi[4], lo[4];
+      for (int c = 0; c < QC; c += 2) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t w[4] = {qv[c + u].x, qv[c + u].y, qv[c + u].z, qv[c + u].w};
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w[4] = {qv[c + u].x, qv[c + u].y, qv[c + u].z, qv[c + u].w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t h2[2], l2[2];
+          for (int e = 0; e < 2; ++e) {
+            uint32_t h2[2], l2[2];
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint32_t x = w[2 * e + f];
-            const float x0 = __uint_as_float(x << 16) * qinv;
-            const float x1 = __uint_as_float(x & 0xffff0000u) * qinv;
-            h2[f] = kv8::to_e4m3x2(x0, x1);
-            const float2 r = kv8::f16x2_to_float2(kv8::to_f16x2(h2[f]));
-            l2[f] = kv8::to_e4m3x2(x0 - r.x, x1 - r.y);
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t x = w[2 * e + f];
+              const float x0 = __uint_as_float(x << 16) * qinv;
+              const float x1 = __uint_as_float(x & 0xffff0000u) * qinv;
+              h2[f] = kv8::to_e4m3x2(x0, x1);
+              const float2 r = kv8::f16x2_to_float2(kv8::to_f16x2(h2[f]));
+              l2[f] = kv8::to_e4m3x2(x0 - r.x, x1 - r.y);
+            }
+            hi[2 * u + e] = h2[0] | (h2[1] << 16);
+            lo[2 * u + e] = l2[0] | (l2[1] << 16);
           }
-          hi[2 * u + e] = h2[0] | (h2[1] << 16);
-          lo[2 * u + e] = l2[0] | (l2[1] << 16);
         }
+        const int ch = wg * (QC / 2) + c / 2;
+        st_shared_16(swz(sQ, BM, i, ch), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_16(swz(sQ + Lo::Q_BYTES, BM, i, ch), lo[0], lo[1], lo[2], lo[3]);
       }
-      const int ch = wg * (QC / 2) + c / 2;
-      st_shared_16(swz(sQ, BM, i, ch), hi[0], hi[1], hi[2], hi[3]);
-      st_shared_16(swz(sQ + Lo::Q_BYTES, BM, i, ch), lo[0], lo[1], lo[2], lo[3]);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(BAR_Q);
     }
-    tc::fence_proxy_async_smem();
-    tc::mbar_arrive(BAR_Q);
-    // the tile row in this thread's TMEM lane
-    const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
-    const bool valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
-    int64_t q_row = 0, out_row = 0;
-    int lim = t.key_end;
-    if (valid) row_info8<DECODE>(a, t, kvh, row, q_row, out_row, lim);
-    const float rmax = m64 ? fmaxf(xch[row], xch[BM + row]) : qmax;
-    const int re = max(kv8::scale_exponent(rmax), -80);
-    // a query that is not finite has no defined scores: its row is NaN
-    const float rs = rmax < INFINITY ? a.scale_log2 * kv8::pow2(re) : NAN;
-    // every thread has read the Q maxima before the slots are used again
-    // below: the first tile's exchange slot is the other parity's
+    // a warp without query rows only keeps the barriers going
+    const bool busy = (warp & 3) * 32 < t.n_rows;
+    // the first tile's exchange slot is parity 1: the Q maxima lie in parity 0
     float m_ref = -INFINITY, vref = 0.f;
-    float l = 0.f;
+    float l = 0.f;  // times 2^6
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
-      const int s = j % NB;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(BAR_SC(j % SR), uint32_t(j / SR) & 1u, abort_flag,
-                                                  kWaitLimit) &&
-                                       tc::mbar_wait(BAR_S(s), uint32_t(j / NB) & 1u, abort_flag,
-                                                     kWaitLimit))) {
+      if (!__all_sync(0xffffffffu, wait(BAR_S(j), j / NS, abort_flag))) {
         ok = false;
         break;
       }
       tc::tc_fence_after();
+      const uint32_t s_col = tl + uint32_t((j % NS) * BN);
       const int k0 = t.key_begin + j * BN + wg * HALF;
-      const bool need_mask = k0 + HALF > t.nomask_end;
-      uint32_t sr[HALF];
-      tc::tmem_ld_row<HALF>(tl + uint32_t(s * BN + wg * HALF), sr);
-      tc::tmem_ld_wait();
       float x[HALF];
-      const float4* ks4 = reinterpret_cast<const float4*>(ks_ring + (j % SR) * BN + wg * HALF);
+      float mx_half = -INFINITY;
+      const float v_new = vref_ring[j % SR];
+      if (busy) {
+        uint32_t sr[HALF];
+        tc::tmem_ld_row<HALF>(s_col + uint32_t(wg * HALF), sr);
+        const float4* ks4 = reinterpret_cast<const float4*>(ks_ring + (j % SR) * BN + wg * HALF);
+        float4 kp[4];  // the first scales, read while S is on its way
 #pragma unroll
-      for (int e = 0; e < HALF; e += 4) {
-        const float4 k4 = ks4[e >> 2];
-        const float2 y0 = mul2(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])),
-                               make_float2(k4.x, k4.y));
-        const float2 y1 = mul2(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])),
-                               make_float2(k4.z, k4.w));
-        x[e] = y0.x;
-        x[e + 1] = y0.y;
-        x[e + 2] = y1.x;
-        x[e + 3] = y1.y;
+        for (int e = 0; e < 4; ++e) kp[e] = ks4[e];
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < HALF; e += 4) {
+          const float4 k4 = e < 16 ? kp[(e >> 2) & 3] : ks4[e >> 2];
+          const float2 y0 = mul2(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])),
+                                 make_float2(k4.x, k4.y));
+          const float2 y1 =
+              mul2(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])),
+                   make_float2(k4.z, k4.w));
+          x[e] = y0.x;
+          x[e + 1] = y0.y;
+          x[e + 2] = y1.x;
+          x[e + 3] = y1.y;
+        }
+        if (k0 + HALF > t.nomask_end) {
+          const int n = lim - k0;  // visible keys of this half
+#pragma unroll
+          for (int e = 0; e < HALF; ++e)
+            if (e >= n) x[e] = -INFINITY;
+        }
+        float mx4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx4[u] = max3(x[3 * u], x[3 * u + 1], x[3 * u + 2]);
+#pragma unroll
+        for (int e = 12; e < HALF; e += 2)
+          mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], x[e], x[e + 1]);
+        mx_half = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       }
-      if (need_mask) {
-#pragma unroll
-        for (int e = 0; e < HALF; ++e)
-          if (k0 + e >= lim) x[e] = -INFINITY;
-      }
-      float mx4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int e = 4; e < HALF; e += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          mx4[u] = e + 4 + u < HALF ? fmaxf(fmaxf(mx4[u], x[e + u]), x[e + 4 + u])
-                                    : fmaxf(mx4[u], x[e + u]);
-      const float mx_half = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       // the other half's max of this row (double-buffered by tile parity: a
       // thread writes tile j + 2's slot only after every thread has passed
-      // tile j + 1's exchange, hence has read tile j's; tile 0 uses parity 1,
-      // the Q maxima lie in parity 0)
+      // tile j + 1's exchange, hence has read tile j's)
       const int xp = (j + 1) & 1;
       xch[(xp * 2 + wg) * BM + i] = mx_half;
-      tc::mbar_arrive(XB(j & 1));
-      if (!__all_sync(0xffffffffu,
-                      tc::mbar_wait(XB(j & 1), (j >> 1) & 1, abort_flag, kWaitLimit))) {
+      tc::mbar_arrive(XB(j));
+      if (!__all_sync(0xffffffffu, wait(XB(j), j >> 1, abort_flag))) {
         ok = false;
         break;
       }
       const float mx = rs * fmaxf(mx_half, xch[(xp * 2 + (1 - wg)) * BM + i]);
-      const float m_new = fmaxf(m_ref, mx);
-      const float v_new = vref_ring[j % SR];
-      if (j == 0) {
-        m_ref = m_new;
-        vref = v_new;
-      } else {
-        const bool need = m_new > m_ref + kRescaleThreshold;
-        const bool vneed = v_new > vref;  // the same for every thread of the CTA
-        if (__any_sync(0xffffffffu, need || vneed)) {
-          // O is rescaled once PV_{j-1} has written it; each warpgroup takes
-          // half of its columns
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(BAR_O((j - 1) & 1), ((j - 1) >> 1) & 1,
-                                                      abort_flag, kWaitLimit))) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const float alpha = need ? rxk::fast_exp2(m_ref - m_new) : 1.f;
-          const float f = vneed ? alpha * (vref / v_new) : alpha;
-#pragma unroll
-          for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t r[32];
-            const uint32_t col = uint32_t(Lo::O_COL + wg * (D / 2) + cc * 32);
-            tc::tmem_ld32(tl + col, r);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-            tc::tmem_st32(tl + col, r);
-          }
-          l *= alpha;
-          if (need) m_ref = m_new;
-          vref = v_new;
+      // the reference moves when a score exceeds it by 2^9
+      const float m_new = j == 0 || mx > m_ref + kRescaleThreshold ? fmaxf(m_ref, mx) : m_ref;
+      if (j > 0 && __any_sync(0xffffffffu, m_new != m_ref || v_new != vref)) {
+        // O is rescaled once P V_{j-1} has written it; each warpgroup takes
+        // half of its columns
+        if (!__all_sync(0xffffffffu, wait(BAR_O(j - 1), (j - 1) >> 1, abort_flag))) {
+          ok = false;
+          break;
         }
+        tc::tc_fence_after();
+        const float alpha = m_new != m_ref ? rxk::fast_exp2(m_ref - m_new) : 1.f;  // 0 from -inf
+        const float f = alpha * (vref / v_new);
+#pragma unroll 1
+        for (int cc = 0; cc < D / 64; ++cc) {
+          uint32_t r[32];
+          const uint32_t col = tl + uint32_t(Lo::O_COL + wg * (D / 2) + cc * 32);
+          tc::tmem_ld32(col, r);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+          tc::tmem_st32(col, r);
+        }
+        l *= alpha;
       }
-      const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-      const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(neg_m, neg_m);
-      float2 l2[4];
+      m_ref = m_new;
+      vref = v_new;
+      if (busy) {
+        const float nm = m_ref == -INFINITY ? 0.f : kWeightBias - m_ref;
+        const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(nm, nm);
+        float2 l2[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) l2[u] = make_float2(0.f, 0.f);
-      const float4* vs4 = reinterpret_cast<const float4*>(vs_ring + (j % SR) * BN + wg * HALF);
+        for (int u = 0; u < 4; ++u) l2[u] = make_float2(u ? 0.f : l, 0.f);
 #pragma unroll
-      for (int cc = 0; cc < HALF / 32; ++cc) {
-        uint32_t pk[16];
+        for (int cc = 0; cc < HALF / 32; ++cc) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 v4 = vs4[cc * 8 + (e >> 2)];
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            const int n = cc * 32 + e + u;
+          for (int e = 0; e < 32; e += 2) {
+            const int n = cc * 32 + e;
             const float2 y = fma2(make_float2(x[n], x[n + 1]), rs2, nm2);
             const float2 p = make_float2(rxk::fast_exp2(y.x), rxk::fast_exp2(y.y));
-            l2[((e + u) >> 1) & 3] = add2(l2[((e + u) >> 1) & 3], p);
-            const float2 w = mul2(p, u ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
-            pk[(e + u) >> 1] = pack_f16(w.x, w.y);
+            l2[(e >> 1) & 3] = add2(l2[(e >> 1) & 3], p);
+            pk[e >> 1] = pack_f16(p.x, p.y);
           }
+          // two keys per column over the first BN / 2 columns of S_j's buffer
+          tmem_st16x(s_col + uint32_t(wg * (HALF / 2) + 16 * cc), pk);
         }
-        // two keys per column over the first BN / 2 columns of S_j's buffer
-        tmem_st16x(tl + uint32_t(s * BN + wg * (HALF / 2) + 16 * cc), pk);
+        const float2 ls = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
+        l = ls.x + ls.y;
       }
-      const float2 ls = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
-      l += ls.x + ls.y;
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(BAR_P(s));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(BAR_P(j));
     }
     // ----------------------------------------------------------- epilogue
-    const bool fin = ok && n_tiles > 0 &&
-                     __all_sync(0xffffffffu, tc::mbar_wait(BAR_FIN, 0, abort_flag, kWaitLimit));
+    const bool fin = ok && n_tiles > 0 && __all_sync(0xffffffffu, wait(BAR_FIN, 0, abort_flag));
     // the row sums go through the parity that the last tile did not use
     const int xp = n_tiles & 1 ? 0 : 1;
     if (fin) xch[(xp * 2 + wg) * BM + i] = l;
     tc::mbar_arrive(XE);
-    const bool xok = __all_sync(0xffffffffu, tc::mbar_wait(XE, 0, abort_flag, kWaitLimit));
+    const bool xok = __all_sync(0xffffffffu, wait(XE, 0, abort_flag));
     if (fin && xok) {
       tc::tc_fence_after();
       const float l_all = l + xch[(xp * 2 + (1 - wg)) * BM + i];
-      const float inv = vref * (1.f / kWeightBias) / l_all;
+      const float inv = vref / l_all;  // (2^6 in both O and l)
       // warpgroup w writes output columns [w D/2, (w+1) D/2): through shared
       // memory (Q and the K and V stages are idle), so that a warp writes
       // whole contiguous row segments
@@ -783,7 +860,9 @@ __device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, ui
       const int qrow = (warp & 3) * 32;
       const bool to_bf16 = !DECODE && a.out_bf16;
       uint8_t* obase = static_cast<uint8_t*>(DECODE ? static_cast<void*>(a.ws_o) : a.out);
-      const long long my_row = valid ? (long long)out_row : -1ll;
+      int64_t q_row, out_row = -1;
+      if (valid) row_info8<DECODE>(a, t, kvh, i, q_row, out_row, lim);
+      const long long my_row = out_row;
       if (to_bf16) {
         constexpr int CPR = HC / 8;  // 16-byte pieces (8 columns) per row
 #pragma unroll 4
@@ -812,13 +891,13 @@ __device__ __forceinline__ void tile8(const Args8& a, const CUtensorMap* tmk, ui
             *reinterpret_cast<float4*>(obase + (ro * D + wg * HC + c4 * 4) * 4) = v;
         }
       }
-      if (valid && wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = m_ref * kLn2 + logf(l_all);
+      if (valid && wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = (m_ref - kWeightBias) * kLn2 + logf(l_all);
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&g_kv8_att_error, 2);
-  if (warp == 8) {
+  if (warp == 12) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }

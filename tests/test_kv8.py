@@ -3,11 +3,15 @@ against softmax attention in 64 bits, and every refusal.
 
 Tolerances of the attention follow from its roundings.  A softmax weight is
 rounded to f16 (half a step: 2^-11 of it; below f16's normal range, where the
-weight is under 2^-21 of the largest, 2^-25 of 2^-7 of the largest V scale);
-a score carries fp32 rounding of its d products and, on tensor-core tiles, a
-query split into two e4m3 parts (off by at most 2^-18 of the row's largest
-magnitude per element); an fp32 output nothing else of size, a bf16 output
-half a step more (2^-8).
+weight is under 2^-20 of the largest, 2^-25 of 2^-6 of the largest V scale);
+a score carries fp32 rounding of its d products, and of a query elements under
+2^-27 of the row's largest or so, in all at most 2^-18 of the row's largest
+magnitude per element; an fp32 output nothing else of size, a bf16 output half
+a step more (2^-8).  The tiles apply a scale as the f16 product of a code and
+the quotient of the scale and a reference: exact for powers of two, for any
+other scale two more roundings of 2^-11 each.  Then a term p v is off by at
+most (1 + 2^-11)^3 - 1 < 3.01 2^-11 of itself, and a score by at most (1 +
+2^-11)^2 - 1 < 2.01 2^-11 of the sum of the magnitudes of its products.
 """
 
 import ctypes as C
@@ -393,7 +397,7 @@ class Case:
     requests over it, and attention in 64 bits with its error bound."""
 
     def __init__(self, torch, Hq, H, d, block, ctx, seed, shared=0, page=None, spread=0.5,
-                 unit_scale=False):
+                 unit_scale=False, pow2=False):
         self.torch, self.Hq, self.H, self.d, self.block = torch, Hq, H, d, block
         self.page = page = page or block
         rng = np.random.default_rng(seed)
@@ -429,6 +433,10 @@ class Case:
             c[1][:, torch.from_numpy(used).cuda()] = r
         e = torch.randn((H, self.N // block, 2), generator=g, device="cuda") * spread
         s = (torch.exp(e) * 0.01)
+        if pow2:
+            s = torch.exp2(torch.floor(torch.log2(s)))
+        self.term = 2.0 ** -11 if pow2 else 3.01 * 2.0 ** -11
+        self.score = 2.0 ** -20 if pow2 else 2.0 ** -20 + 2.01 * 2.0 ** -11
         ub = torch.from_numpy(np.unique(used // block)).cuda()
         self.sc[1][:, ub] = s[:, ub]
         self.scale = 1.0 / np.sqrt(d) if not unit_scale else 1.0
@@ -471,10 +479,10 @@ class Case:
             l = p.sum(axis=1, keepdims=True)
             o[:, h] = p @ v / l
             lse[:, h] = (m + np.log(l))[:, 0]
-            ds = (a * 2.0 ** -20 + split * 2.0 ** -18).max(axis=1) + 2.0 ** -20
+            ds = (a * self.score + split * 2.0 ** -18).max(axis=1) + 2.0 ** -20
             w = p @ np.abs(v) / l
             tiny = 448 * vs.max() * 2.0 ** -31 * p.astype(bool).sum(axis=1) / l[:, 0]
-            bo[:, h] = (2.0 ** -11 + ds)[:, None] * w + ds[:, None] * np.abs(o[:, h]) + \
+            bo[:, h] = (self.term + ds)[:, None] * w + ds[:, None] * np.abs(o[:, h]) + \
                 tiny[:, None]
             bl[:, h] = ds + np.abs(lse[:, h]) * 2.0 ** -22
         return o, lse, bo, bl
@@ -551,6 +559,20 @@ def test_decode_matches_64_bits(i, bf16):
         c.compare(o[b:b + 1], lse[b:b + 1], c.reference(qn[b:b + 1], b, [ctx[b]]), bf16)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("i", range(len(DECODE)))
+def test_decode_with_power_of_two_scales(i):
+    """Scales as rx_kv8_store writes them: one rounding of a weight is all."""
+    torch = pytest.importorskip("torch")
+    Hq, H, d, block, page, ctx, shared = DECODE[i]
+    c = Case(torch, Hq, H, d, block, ctx, 300 + i, shared=shared, page=page, spread=1.5, pow2=True)
+    q = c.queries(len(ctx))
+    o, lse = _decode(c, q, bf16=False)
+    qn = q.double().cpu().numpy()
+    for b in range(len(ctx)):
+        c.compare(o[b:b + 1], lse[b:b + 1], c.reference(qn[b:b + 1], b, [ctx[b]]), False)
+
+
 def _extend(c, prefix, q, bf16=True, R=None):
     torch = c.torch
     sfx = np.array(c.ctx) - np.array(prefix)
@@ -602,3 +624,21 @@ def test_extend_matches_64_bits(i, bf16):
         if e > a:
             lim = prefix[b] + 1 + np.arange(e - a)
             c.compare(o[a:e], lse[a:e], c.reference(qn[a:e], b, lim), bf16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i", range(len(EXTEND)))
+def test_extend_with_power_of_two_scales(i):
+    torch = pytest.importorskip("torch")
+    Hq, H, d, block, page, prefix, sfx = EXTEND[i]
+    ctx = [max(1, p + s) for p, s in zip(prefix, sfx)]
+    prefix = [x - s for x, s in zip(ctx, sfx)]
+    c = Case(torch, Hq, H, d, block, ctx, 400 + i, page=page, spread=1.5, pow2=True)
+    q = c.queries(int(sum(sfx)))
+    o, lse, qo = _extend(c, prefix, q, False)
+    qn = q.double().cpu().numpy()
+    for b in range(len(ctx)):
+        a, e = int(qo[b]), int(qo[b + 1])
+        if e > a:
+            lim = prefix[b] + 1 + np.arange(e - a)
+            c.compare(o[a:e], lse[a:e], c.reference(qn[a:e], b, lim), False)
