@@ -812,11 +812,14 @@ typedef struct rx_kv8_pool_desc {
  * earlier rows are rounded again under it (the rows behind are left as they
  * are).  Slots must be distinct, and the call's tokens of one block must
  * stand next to one another in d_slots, in slot order, as the cache hands
- * them out.  A NaN is stored as 0 and an infinity as the block's largest
+ * them out: a token whose neighbour before it lies in the same block but not
+ * in the slot before its own is skipped, with those that follow on from it,
+ * and reported (bit 7, blocks of 2 slots and more).  A NaN is stored as 0 and an infinity as the block's largest
  * code, both reported by rx_device_check (bit 6); the scale is taken from
  * the finite values.  A slot outside [1, num_slots) is skipped and reported
  * (bit 0).  d_k, d_v: device bf16 [T][Hkv][head_dim], 16-byte aligned.
- * Errors: RX_ERR_INVALID (the pool, T < 0, NULL or misaligned inputs); T = 0
+ * Errors: RX_ERR_INVALID (the pool, T < 0, T * num_kv_heads of 2^31 or more,
+ * NULL or misaligned inputs); T = 0
  * launches nothing. */
 rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
                        const int32_t* d_slots, const void* d_k,
@@ -891,8 +894,8 @@ rx_status rx_host_free(void* p);
  * and returned without results; bit 4 = rx_req_to_token_write met a row or
  * position outside the table and skipped that entry; bit 5 = rx_kv_copy met
  * a slot outside its pool and skipped that entry; bit 6 = rx_kv8_store met
- * a value that is not finite.  Returns RX_ERR_CUDA
- * if a flag was set or the device reported an error. */
+ * a value that is not finite; bit 7 = rx_kv8_store met the tokens of a
+ * block out of slot order and skipped some.  Returns RX_ERR_CUDA if a flag was set or the device reported an error. */
 rx_status rx_device_check(int32_t* out_flags);
 
 /* Test hook (host fault injection): the k-th page allocation from now, on

@@ -17,12 +17,15 @@
 #include <cuda_runtime.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "kv8.cuh"
 #include "rx.h"
 #include "rx_internal.h"
 
 // Bit 0: rx_kv8_store or rx_kv8_load met a slot outside [1, num_slots); bit
-// 6: rx_kv8_store met a value that is not finite.  Read by rx_device_check().
+// 6: rx_kv8_store met a value that is not finite; bit 7: it met a block's tokens
+// out of slot order.  Read by rx_device_check().
 static __device__ int32_t g_kv8_error;
 
 namespace {
@@ -98,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const StoreArgs a)
   for (int64_t base = int64_t(blockIdx.x) * (kThreads / L); base < rows; base += step) {
     const int64_t r = base + threadIdx.x / L;
     const bool in = r < rows;
-    const int64_t t = in ? r / a.hkv : 0;
+    // (fewer than 2^31 rows: checked on the host)
+    const int64_t t = in ? uint32_t(r) / uint32_t(a.hkv) : 0;
     const int64_t h = in ? r - t * a.hkv : 0;
     const int32_t slot = in ? __ldg(a.slots + t) : 0;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
@@ -132,36 +136,42 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const StoreArgs a)
 }
 
 // Blocks of 2 .. 64 slots.  The call's tokens of one block stand next to one
-// another in slot order (a run); the block of a CTA takes a window of tokens
-// and one of (head, K or V), lists the runs that start in the window, and a
-// group of D / 8 lanes takes one run at a time: a pass for its maximum, the
-// block's scale, the rows before the run rounded again if the scale grew,
-// then a pass that quantises the run's rows (read again, from L1 or L2).
+// another in slot order (a run); the CTA takes a window of tokens and one of
+// (head, K or V), lists the runs that start in the window, and a group of D / 8
+// lanes takes one run at a time: its maximum, the block's scale, the rows
+// before the run rounded again if the scale grew, then the run's codes.
+// Up to kHold rows stay in registers between the two passes, all of them on
+// their way at once; the rows of a longer run are read again, from L1 or L2.
+constexpr int kHold = 16;
+constexpr int kMaxBlock = 64;
+constexpr int kMaxWindow = 1024;
 template <int D>
 __global__ void __launch_bounds__(kThreads) store_runs_kernel(const StoreArgs a) {
   constexpr int L = D / 8;
   constexpr int GROUPS = kThreads / L;
-  __shared__ int32_t starts[kThreads];
+  __shared__ int32_t win[kMaxWindow + kMaxBlock + 1];  // slots of tokens w0 - 1 ..
+  __shared__ int32_t starts[kMaxWindow];
   __shared__ int count;
   const int tid = threadIdx.x;
   const int lane = tid % L;
   const int64_t w0 = int64_t(blockIdx.x) * a.window;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
+  const int blk = 1 << a.block_log2;
   if (tid == 0) count = 0;
+  for (int i = tid; i < a.window + blk + 1; i += kThreads) {
+    const int64_t t = w0 - 1 + i;
+    win[i] = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;  // -1 is in no run
+  }
   __syncthreads();
-  if (tid < a.window && w0 + tid < a.T) {
-    const int64_t t = w0 + tid;
-    const int32_t s = __ldg(a.slots + t);
-    bool start = true;
-    if (t > 0) {
-      const int32_t p = __ldg(a.slots + t - 1);
-      start = !(p >= 1 && s - 1 == p && (s >> a.block_log2) == (p >> a.block_log2));
-    }
+  for (int i = tid; i < a.window && w0 + i < a.T; i += kThreads) {
+    const int32_t s = win[i + 1], p = win[i];
     if (s < 1 || s >= a.num_slots) {
-      start = false;
       if (blockIdx.y == 0) atomicOr(&g_kv8_error, 1);
+    } else if (p < 1 || p >= a.num_slots || (s >> a.block_log2) != (p >> a.block_log2)) {
+      starts[atomicAdd(&count, 1)] = i;  // (the order of the runs changes no result)
+    } else if (s - 1 != p && blockIdx.y == 0) {
+      atomicOr(&g_kv8_error, 128);  // two runs of one block would race: the later one is skipped
     }
-    if (start) starts[atomicAdd(&count, 1)] = tid;
   }
   __syncthreads();
   const int n_runs = count;
@@ -171,32 +181,44 @@ __global__ void __launch_bounds__(kThreads) store_runs_kernel(const StoreArgs a)
   for (int i0 = 0; i0 < n_runs; i0 += GROUPS) {
     const int i = i0 + tid / L;
     const bool in = i < n_runs;
-    const int64_t t0 = w0 + (in ? starts[i] : 0);
-    const int32_t s0 = in ? __ldg(a.slots + t0) : 0;
-    const int first = s0 & ((1 << a.block_log2) - 1);
-    // the run ends with its block, its slots' order, the pool or the call
+    const int at = in ? starts[i] : 0;
+    const int64_t t0 = w0 + at;
+    const int32_t s0 = in ? win[at + 1] : 0;
+    const int first = s0 & (blk - 1);
+    // the run ends with its block (so within the pool), its slots' order or the
+    // call: the group's lanes look at L tokens together
     int n = 0;
-    if (in) {
-      const int64_t room = min(int64_t((1 << a.block_log2) - first), a.num_slots - s0);
-      const int most = int(min(room, a.T - t0));
-      for (n = 1; n < most && __ldg(a.slots + t0 + n) == s0 + n; ++n) {
-      }
+    for (int j0 = 0; j0 < blk; j0 += L) {
+      const int j = j0 + lane;
+      const bool ok = in && j < blk - first && win[at + 1 + j] == s0 + j;
+      uint32_t bits = __ballot_sync(0xffffffffu, ok);
+      if (L < 32) bits = (bits >> ((tid & 31) / L * L)) & ((1u << (L & 31)) - 1);
+      if (n == j0) n += bits == 0xffffffffu ? 32 : __ffs(~bits) - 1;
     }
+    float* sc = reinterpret_cast<float*>(
+        a.scales + int64_t(h) * (a.num_slots >> a.block_log2) + (s0 >> a.block_log2)) + which;
+    float old = in && first > 0 ? *sc : 0.f;
+    const uint4* row0 = src + t0 * tok;
+    uint4 x[kHold];
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      x[j] = j < n ? __ldg(row0 + j * tok) : make_uint4(0, 0, 0, 0);
     uint32_t m = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) m = max2_nan(m, row_max(__ldg(src + (t0 + j) * tok)));
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) m = max2_nan(m, row_max(x[j]));
+#pragma unroll 8
+    for (int j = kHold; j < n; ++j) m = max2_nan(m, row_max(__ldg(row0 + j * tok)));
     m = reduce_max<L>(m);
     const bool bad = m >= kInfBits;
     if (__any_sync(0xffffffffu, bad)) {
       if (bad && lane == 0) atomicOr(&g_kv8_error, 64);
       m = 0;
-      for (int j = 0; j < n; ++j) m = max2_nan(m, row_max(drop(__ldg(src + (t0 + j) * tok), true)));
+      for (int j = 0; j < n; ++j) m = max2_nan(m, row_max(drop(__ldg(row0 + j * tok), true)));
       m = reduce_max<L>(m);
+#pragma unroll
+      for (int j = 0; j < kHold; ++j) x[j] = drop(x[j], false);
     }
     float scale = kv8::pow2(kv8::scale_exponent(bf16_bits_to_float(m)));
-    float* sc = reinterpret_cast<float*>(
-        a.scales + int64_t(h) * (a.num_slots >> a.block_log2) + (s0 >> a.block_log2)) + which;
-    float old = in && first > 0 ? *sc : 0.f;
     __syncwarp();  // every lane has read the old scale before lane 0 writes
     if (!in) continue;
     // a scale that no store wrote (not positive and finite) counts as none
@@ -204,16 +226,23 @@ __global__ void __launch_bounds__(kThreads) store_runs_kernel(const StoreArgs a)
     if (first > 0 && scale > old) {
       const float f = old / scale;
       uint2* row = reinterpret_cast<uint2*>(codes + int64_t(s0 - first) * D) + lane;
-      for (int j = 0; j < first; ++j, row += L) {
-        const uint2 c = *row;
-        uint32_t q[4];
-        const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+      for (int j0 = 0; j0 < first; j0 += 8) {
+        uint2 c[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = kv8::f16x2_to_float2(kv8::to_f16x2(w[e]));
-          q[e] = kv8::to_e4m3x2(x.x * f, x.y * f);
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < first) c[j] = row[(j0 + j) * L];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j >= first) break;
+          uint32_t q[4];
+          const uint32_t w[4] = {c[j].x & 0xffffu, c[j].x >> 16, c[j].y & 0xffffu, c[j].y >> 16};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = kv8::f16x2_to_float2(kv8::to_f16x2(w[e]));
+            q[e] = kv8::to_e4m3x2(y.x * f, y.y * f);
+          }
+          row[(j0 + j) * L] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
         }
-        *row = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       }
     } else if (first > 0) {
       scale = old;
@@ -221,54 +250,76 @@ __global__ void __launch_bounds__(kThreads) store_runs_kernel(const StoreArgs a)
     if (lane == 0) *sc = scale;
     const float inv = 1.f / scale;
     uint2* row = reinterpret_cast<uint2*>(codes + int64_t(s0) * D) + lane;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if (j < n) row[j * L] = quant8(x[j], inv);
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      uint4 x = __ldg(src + (t0 + j) * tok);
-      if (bad) x = drop(x, false);
-      row[j * L] = quant8(x, inv);
+    for (int j = kHold; j < n; ++j) {
+      uint4 y = __ldg(row0 + j * tok);
+      if (bad) y = drop(y, false);
+      row[j * L] = quant8(y, inv);
     }
   }
 }
 
-// out[t][h] = bf16(code * scale), a lane for 16 codes of K and of V.
+// out[t][h] = bf16(code * scale), a lane for 8 codes of K and of V (a store
+// instruction of a warp then fills whole sectors), kRows rows of a thread on
+// their way together.
+constexpr int kRows = 4;
 template <int D>
 __global__ void __launch_bounds__(kThreads) load_kernel(const StoreArgs a, uint4* k_out,
                                                         uint4* v_out) {
-  constexpr int L = D / 16;
-  const int64_t total = a.T * a.hkv * L;
-  for (int64_t c = int64_t(blockIdx.x) * kThreads + threadIdx.x; c < total;
-       c += int64_t(gridDim.x) * kThreads) {
-    const int64_t r = c / L;
-    const int lane = int(c - r * L);
-    const int64_t t = r / a.hkv;
-    const int64_t h = r - t * a.hkv;
-    const int32_t slot = __ldg(a.slots + t);
-    uint4 kc = make_uint4(0, 0, 0, 0), vc = kc;
-    float2 s = make_float2(0.f, 0.f);
-    if (slot < 1 || slot >= a.num_slots) {  // never read outside the pool: a row of zeros
-      if (lane == 0) atomicOr(&g_kv8_error, 1);
-    } else {
-      const int64_t at = h * a.num_slots + slot;
-      kc = *(reinterpret_cast<const uint4*>(a.kc + at * D) + lane);
-      vc = *(reinterpret_cast<const uint4*>(a.vc + at * D) + lane);
-      s = a.scales[h * (a.num_slots >> a.block_log2) + (slot >> a.block_log2)];
+  constexpr int L = D / 8;
+  constexpr int GROUPS = kThreads / L;
+  const int lane = threadIdx.x % L;
+  const int64_t rows = a.T * a.hkv;
+  const int64_t step = int64_t(gridDim.x) * (GROUPS * kRows);
+  for (int64_t r0 = int64_t(blockIdx.x) * (GROUPS * kRows) + threadIdx.x / L; r0 < rows;
+       r0 += step) {
+    uint2 kc[kRows], vc[kRows];
+    float2 s[kRows];
+    int32_t slot[kRows];
+    int h[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t r = r0 + j * GROUPS;
+      // (fewer than 2^31 rows: checked on the host)
+      const uint32_t t = r < rows ? uint32_t(r) / uint32_t(a.hkv) : 0;
+      h[j] = r < rows ? int(uint32_t(r) - t * uint32_t(a.hkv)) : 0;
+      slot[j] = r < rows ? __ldg(a.slots + t) : 1;
     }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const uint4 x = which ? vc : kc;
-      const float f = which ? s.y : s.x;
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 y =
-            kv8::f16x2_to_float2(kv8::to_f16x2((e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y.x * f, y.y * f);
-        o[e] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int j = 0; j < kRows; ++j) {
+      kc[j] = vc[j] = make_uint2(0, 0);
+      s[j] = make_float2(0.f, 0.f);
+      if (slot[j] < 1 || slot[j] >= a.num_slots) {  // never read outside the pool: zeros
+        if (lane == 0) atomicOr(&g_kv8_error, 1);
+      } else if (r0 + j * GROUPS < rows) {
+        const int64_t at = int64_t(h[j]) * a.num_slots + slot[j];
+        kc[j] = *(reinterpret_cast<const uint2*>(a.kc + at * D) + lane);
+        vc[j] = *(reinterpret_cast<const uint2*>(a.vc + at * D) + lane);
+        s[j] = a.scales[int64_t(h[j]) * (a.num_slots >> a.block_log2) +
+                        (slot[j] >> a.block_log2)];
       }
-      uint4* dst = (which ? v_out : k_out) + r * (D / 8) + lane * 2;
-      __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-      __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t r = r0 + j * GROUPS;
+      if (r >= rows) break;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const uint2 x = which ? vc[j] : kc[j];
+        const float f = which ? s[j].y : s[j].x;
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = e & 2 ? x.y : x.x;
+          const float2 y = kv8::f16x2_to_float2(kv8::to_f16x2((e & 1) ? w >> 16 : w & 0xffffu));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(y.x * f, y.y * f);
+          o[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        __stcs((which ? v_out : k_out) + r * L + lane, make_uint4(o[0], o[1], o[2], o[3]));
+      }
     }
   }
 }
@@ -280,6 +331,9 @@ rx_status store_args(const rx_kv8_pool_desc* pool, int32_t layer, const int32_t*
   rx_status st = rx_internal::check_kv8_pool(pool, layer);
   if (st != RX_OK) return st;
   if (T < 0) return rx_internal::set_error(RX_ERR_INVALID, "8-bit KV store or load: T < 0");
+  if (T > INT32_MAX / pool->num_kv_heads)
+    return rx_internal::set_error(RX_ERR_INVALID,
+                                  "8-bit KV store or load: 2^31 rows (T x KV heads) or more");
   if (T > 0 && (!d_slots || !d_k || !d_v || !aligned(d_k, 16) || !aligned(d_v, 16)))
     return rx_internal::set_error(RX_ERR_INVALID,
                                   "8-bit KV store or load: NULL or misaligned rows or slots");
@@ -359,9 +413,12 @@ extern "C" rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
   } else {
     if (a.hkv > 32767)
       return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_store: too many KV heads");
-    // long windows keep every group of a CTA in whole blocks; short ones
-    // spread a decode step's tokens (one run each) over the SMs
-    a.window = T * a.hkv * 2 >= 2 * sms * kThreads ? kThreads : 16;
+    // a window of as many blocks as the CTA has groups keeps every group at
+    // whole blocks; a call too short to fill the SMs so has a token (a decode
+    // step: one run each) per group
+    const int groups = kThreads / (D / 8);
+    const int64_t whole = std::min<int64_t>(int64_t(groups) << a.block_log2, kMaxWindow);
+    a.window = int((T + whole - 1) / whole * a.hkv * 2 >= 2 * sms ? whole : groups);
     const int64_t gx = (T + a.window - 1) / a.window;
     if (gx > INT32_MAX) return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_store: T too large");
     const dim3 grid(unsigned(gx), unsigned(a.hkv * 2));
@@ -381,9 +438,9 @@ extern "C" rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
   if (st != RX_OK || T == 0) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int D = pool->head_dim;
-  int64_t ctas = (T * a.hkv * (D / 16) + kThreads - 1) / kThreads;
-  const int64_t cap = int64_t(rx_internal::sm_count()) * 8;
-  if (ctas > cap) ctas = cap;
+  const int64_t per_cta = kThreads / (D / 8) * kRows;
+  const int64_t ctas =
+      std::min((T * a.hkv + per_cta - 1) / per_cta, int64_t(rx_internal::sm_count()) * 8);
   if (D == 128)
     load_kernel<128><<<unsigned(ctas), kThreads, 0, s>>>(a, static_cast<uint4*>(d_k),
                                                          static_cast<uint4*>(d_v));

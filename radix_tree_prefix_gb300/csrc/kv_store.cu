@@ -304,6 +304,8 @@ extern "C" rx_status rx_device_check(int32_t* out_flags) {
                                                "its pool"
                                   : (f & 64) ? "rx_device_check: an 8-bit KV store met a value "
                                                "that is not finite"
+                                  : (f & 128) ? "rx_device_check: an 8-bit KV store met the "
+                                                "tokens of a block out of slot order"
                                              : "rx_device_check: a kernel met a slot outside the pool");
   return RX_OK;
 }

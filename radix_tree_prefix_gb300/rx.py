@@ -701,72 +701,72 @@ def kv8_pool_desc(k_codes, v_codes, scales):
     p = Kv8Pool(k_codes.data_ptr(), v_codes.data_ptr(), scales.data_ptr(), n, L, hkv, d, n // nb)
     p.tensors = (k_codes, v_codes, scales)
     p.device = k_codes.device
+    p.index = k_codes.get_device()  # -1 on the CPU
+    p.ref = C.byref(p)
+    p.dtypes = (torch.int32, torch.bfloat16, torch.float32)
+    p.cuda = torch.cuda
     return p
 
 
 def _kv8_args(pool, stream, *tensors):
     """Checks the (name, tensor, dtype, elements) of a call against the
-    kernels' layouts: contiguous, of the type, at least (d_slots: exactly)
-    the elements, on the pool's device, which must be the current one.
-    Returns the stream's handle."""
-    import torch
-    dev = pool.device
-    if dev.type != "cuda":
-        raise ValueError(f"kv8: the pool is on {dev}, not on a GPU")
+    kernels' layouts: contiguous, of the type, at least the elements, on the
+    pool's device, which must be the current one.  Returns the stream's
+    handle.  (A small call's time is this function's: attributes are read
+    once, and devices compared by their index.)"""
+    dev = pool.index
+    if dev < 0:
+        raise ValueError(f"kv8: the pool is on {pool.device}, not on a GPU")
     for name, t, dtype, n in tensors:
-        if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n or t.device != dev:
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or \
+                not t.is_contiguous():
             raise ValueError(f"kv8: {name} must be a contiguous {dtype} tensor of at least {n} "
-                             f"elements on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"kv8: the stream is on {stream.device}, the pool on {dev}")
-    if torch.cuda.current_device() != dev.index:
-        raise ValueError(f"kv8: the pool is on {dev}, which is not the current device")
-    return stream.cuda_stream
+                             f"elements on {pool.device}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
+    current = pool.cuda.current_stream() if stream is None else stream
+    if current.device_index != dev:
+        raise ValueError(f"kv8: the stream is on {current.device}, the pool on {pool.device}")
+    if stream is not None and pool.cuda.current_device() != dev:
+        raise ValueError(f"kv8: the pool is on {pool.device}, which is not the current device")
+    return current.cuda_stream
 
 
 def kv8_store(pool, layer, d_slots, d_k, d_v, stream=None):
     """rx_kv8_store: bf16 rows [T, Hkv, d] quantised into their slots."""
-    import torch
     T = d_slots.numel()
+    i32, bf16, _ = pool.dtypes
     n = T * pool.num_kv_heads * pool.head_dim
-    s = _kv8_args(pool, stream, ("d_slots", d_slots, torch.int32, T),
-                  ("d_k", d_k, torch.bfloat16, n), ("d_v", d_v, torch.bfloat16, n))
-    _check(_lib.rx_kv8_store(C.byref(pool), layer, d_slots.data_ptr(), d_k.data_ptr(),
+    s = _kv8_args(pool, stream, ("d_slots", d_slots, i32, T),
+                  ("d_k", d_k, bf16, n), ("d_v", d_v, bf16, n))
+    _check(_lib.rx_kv8_store(pool.ref, layer, d_slots.data_ptr(), d_k.data_ptr(),
                              d_v.data_ptr(), T, s))
 
 
 def kv8_load(pool, layer, d_slots, d_k, d_v, stream=None):
     """rx_kv8_load: the rows of d_slots read back into d_k, d_v (bf16)."""
-    import torch
     T = d_slots.numel()
+    i32, bf16, _ = pool.dtypes
     n = T * pool.num_kv_heads * pool.head_dim
-    s = _kv8_args(pool, stream, ("d_slots", d_slots, torch.int32, T),
-                  ("d_k", d_k, torch.bfloat16, n), ("d_v", d_v, torch.bfloat16, n))
-    _check(_lib.rx_kv8_load(C.byref(pool), layer, d_slots.data_ptr(), d_k.data_ptr(),
+    s = _kv8_args(pool, stream, ("d_slots", d_slots, i32, T),
+                  ("d_k", d_k, bf16, n), ("d_v", d_v, bf16, n))
+    _check(_lib.rx_kv8_load(pool.ref, layer, d_slots.data_ptr(), d_k.data_ptr(),
                             d_v.data_ptr(), T, s))
-
-
-def _out_type(d_out):
-    import torch
-    return OUT_BF16 if d_out.dtype is torch.bfloat16 else OUT_F32
 
 
 def kv8_extend_attention(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len, d_qo_indptr,
                          d_tile_indptr, R, num_tiles, scale, d_out, d_lse, stream=None):
     """rx_kv8_extend_attention; d_out is bf16 or fp32."""
-    import torch
-    i32, ot = torch.int32, _out_type(d_out)
+    i32, bf16, f32 = pool.dtypes
+    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
     n = d_q.numel()
-    s = _kv8_args(pool, stream, ("d_q", d_q, torch.bfloat16, 0), ("d_table", d_table, i32, 0),
+    s = _kv8_args(pool, stream, ("d_q", d_q, bf16, 0), ("d_table", d_table, i32, 0),
                   ("d_req_rows", d_req_rows, i32, R), ("d_prefix_len", d_prefix_len, i32, R),
                   ("d_qo_indptr", d_qo_indptr, i32, R + 1),
                   ("d_tile_indptr", d_tile_indptr, i32, R + 1),
-                  ("d_out", d_out, torch.bfloat16 if ot else torch.float32, n),
-                  ("d_lse", d_lse, torch.float32, n // pool.head_dim))
+                  ("d_out", d_out, bf16 if ot else f32, n),
+                  ("d_lse", d_lse, f32, n // pool.head_dim))
     _check(_lib.rx_kv8_extend_attention(
-        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        pool.ref, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
         d_req_rows.data_ptr(), d_prefix_len.data_ptr(), d_qo_indptr.data_ptr(),
         d_tile_indptr.data_ptr(), R, num_tiles, scale, d_out.data_ptr(), ot, d_lse.data_ptr(), s))
 
@@ -774,16 +774,16 @@ def kv8_extend_attention(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len
 def kv8_decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_out, d_lse,
                          d_workspace, step=0, stream=None):
     """rx_kv8_decode_attention; d_out is bf16 or fp32."""
-    import torch
-    i32, ot = torch.int32, _out_type(d_out)
+    i32, bf16, f32 = pool.dtypes
+    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
     rows = B * hq
-    s = _kv8_args(pool, stream, ("d_q", d_q, torch.bfloat16, rows * pool.head_dim),
+    s = _kv8_args(pool, stream, ("d_q", d_q, bf16, rows * pool.head_dim),
                   ("d_table", d_table, i32, 0), ("d_plan", d_plan, i32, info.plan_words),
-                  ("d_out", d_out, torch.bfloat16 if ot else torch.float32, rows * pool.head_dim),
-                  ("d_lse", d_lse, torch.float32, rows),
+                  ("d_out", d_out, bf16 if ot else f32, rows * pool.head_dim),
+                  ("d_lse", d_lse, f32, rows),
                   ("d_workspace", d_workspace, d_workspace.dtype, 0))
     _check(_lib.rx_kv8_decode_attention(
-        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        pool.ref, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
         d_plan.data_ptr(), C.byref(info), B, step, scale, d_out.data_ptr(), ot, d_lse.data_ptr(),
         d_workspace.data_ptr(), d_workspace.numel() * d_workspace.element_size(), s))
 

@@ -139,7 +139,7 @@ X8 = (1 << 24) + 8
 
 @pytest.mark.parametrize("call,bad", [
     (c, b) for c in ("store", "load") for b in (
-        dict(T=-1), dict(slots=None), dict(k=None), dict(v=None), dict(k=X8), dict(v=X8))] + [
+        dict(T=-1), dict(T=1 << 30), dict(slots=None), dict(k=None), dict(v=None), dict(k=X8), dict(v=X8))] + [
     ("extend", b) for b in (
         dict(hq=3), dict(hq=0), dict(hq=-2), dict(R=-1), dict(nt=-1), dict(nt=1 << 40),
         dict(q=None), dict(table=None), dict(rows=None), dict(prefix=None), dict(qo=None),
@@ -363,6 +363,33 @@ def test_bad_slots_are_skipped_and_reported(block):
             assert out[0][i].any()
     with pytest.raises(rx.RxError):
         rx.device_check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [0, 13, 250])
+def test_tokens_of_a_block_out_of_slot_order_are_skipped_and_reported(shift):
+    """A repeated slot, one before its neighbour's and one that leaves a gap:
+    the first run of the block is stored, the later one is not.  (shift: at
+    other places of the kernel's window of tokens.)"""
+    torch = pytest.importorskip("torch")
+    lead = list(range(512, 512 + shift))
+    slots = lead + [5, 4, 9, 9, 10, 16, 17, 19, 20, 24]
+    kept = [i for i in range(len(slots)) if i - shift not in (1, 3, 4, 7, 8)]
+    x = _rows(torch, len(slots), 2, 128, 9)
+    kc, vc, sc = _pool(torch, 1, 2, 1024, 128, 8, 4)
+    two = [t.clone() for t in (kc, vc, sc)]
+    rx.kv8_store(rx.kv8_pool_desc(kc, vc, sc), 0,
+                 torch.tensor(slots, dtype=torch.int32, device="cuda"), *x)
+    with pytest.raises(rx.RxError) as e:
+        rx.device_check()
+    assert "flags 128" in str(e.value) and "out of slot order" in str(e.value)
+    # what remains, without a repeat: 24's neighbour is 17, of another block
+    rx.kv8_store(rx.kv8_pool_desc(*two), 0,
+                 torch.tensor([slots[i] for i in kept], dtype=torch.int32, device="cuda"),
+                 *[t[kept].contiguous() for t in x])
+    assert rx.device_check() == 0
+    for u, v in zip((kc, vc, sc), two):
+        assert torch.equal(u, v)
 
 
 @pytest.mark.gpu
