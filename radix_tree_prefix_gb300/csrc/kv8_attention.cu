@@ -114,10 +114,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // One warp streams the keys of one KV head for up to 8 NR query rows, 32 keys
-// a step, through a ring of shared-memory stages filled with cp.async.  As in
+// a step (16 at d = 256), through a ring of shared-memory stages filled with cp.async.  As in
 // the bf16 decode kernel the products are computed transposed, keys (then
 // output columns) in the M dimension and query rows in N:
-//   S^T (32 keys x 8 rows) = K (codes -> f16) . Q^T
+//   S^T (keys x 8 rows)   = K (codes -> f16) . Q^T
 //   O^T (D x 8 rows)      += V^T (codes -> f16) . P^T
 // The contraction index of a product may be permuted freely, and the M index
 // of O^T too, so that codes go from ldmatrix to operand registers with one
@@ -125,14 +125,19 @@ namespace {
 // codes of a key, taken as d = 4c .. 4c+3 of a k-step; a lane of a transposed
 // one holds the codes (d, d+1) of two adjacent keys, taken as operand rows g
 // and g + 8.
-constexpr int kWarps = 6;
-constexpr int kKeys = 32;  // keys per step
+// Eight warps with three stages each beat six with four by 2 to 10 % over the
+// batches tried (contexts of 8,000 keys in private, d = 128: 155 us against 166
+// at 32 requests, 278 against 288 at 64): a warp's step is a chain of latencies.
+// Steps of 16 keys at d = 128 cost 16 % (180 us), at d = 256 they make room for
+// the third stage.
+constexpr int kWarps = 8;
 template <int D>
 struct Pipe8 {
-  static constexpr int STAGES = D == 128 ? 4 : 2;
+  static constexpr int KEYS = D == 128 ? 32 : 16;  // per step
+  static constexpr int STAGES = 3;
   static constexpr int PITCH = D + 16;  // ldmatrix reads all 32 banks
-  static constexpr int SCALES = 2 * kKeys * PITCH;
-  static constexpr int STAGE_BYTES = SCALES + kKeys * 8;
+  static constexpr int SCALES = 2 * KEYS * PITCH;
+  static constexpr int STAGE_BYTES = SCALES + KEYS * 8;
   static constexpr int WARP_BYTES = STAGES * STAGE_BYTES;
   static constexpr int BYTES = kWarps * WARP_BYTES + 128;
 };
@@ -151,6 +156,8 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
                                             const uint8_t* ring_g) {
   using Cfg = Pipe8<D>;
   constexpr int S = Cfg::STAGES;
+  constexpr int KEYS = Cfg::KEYS;
+  constexpr int MT = KEYS / 16;    // m-tiles of keys per step
   constexpr int PITCH = Cfg::PITCH;
   constexpr int NK = D / 16;
   constexpr int LPR = D / 16;      // lanes (16 B chunks) per row
@@ -161,33 +168,35 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
   const uint8_t* vbase = a.vc + int64_t(u.kvh) * a.head_stride;
   const float2* sbase = a.scales + int64_t(u.kvh) * a.scale_stride;
   const int kb = u.kb, ke = u.ke;
-  const int n_steps = ke > kb ? (ke - kb + kKeys - 1) / kKeys : 0;
+  const int n_steps = ke > kb ? (ke - kb + KEYS - 1) / KEYS : 0;
 
   // the slot of key `lane` of a step (-1 past the range), read one step ahead
   // of its use
   auto read_slot = [&](int st) -> int32_t {
-    const int key = kb + st * kKeys + lane;
-    return key < ke ? __ldg(u.trow + key) : -1;
+    const int key = kb + st * KEYS + lane;
+    return (KEYS == 32 || lane < KEYS) && key < ke ? __ldg(u.trow + key) : -1;
   };
   int32_t next_slot = n_steps > 0 ? read_slot(0) : -1;
   auto issue = [&](int st) {
     int32_t sl = next_slot;
     if (st + 1 < n_steps) next_slot = read_slot(st + 1);
-    if (kb + st * kKeys + lane < ke && (sl < 0 || sl >= a.num_slots)) {
+    if ((KEYS == 32 || lane < KEYS) && kb + st * KEYS + lane < ke &&
+        (sl < 0 || sl >= a.num_slots)) {
       atomicOr(&g_kv8_att_error, 1);
       sl = 0;
     }
     const uint32_t dst = ring + uint32_t(st % S) * Cfg::STAGE_BYTES;
-    cp_async_8(dst + Cfg::SCALES + lane * 8, sbase + ((sl < 0 ? 0 : sl) >> a.block_log2), sl >= 0);
+    if (KEYS == 32 || lane < KEYS)
+      cp_async_8(dst + Cfg::SCALES + lane * 8, sbase + ((sl < 0 ? 0 : sl) >> a.block_log2), sl >= 0);
 #pragma unroll
-    for (int i = 0; i < kKeys / RPI; ++i) {
+    for (int i = 0; i < KEYS / RPI; ++i) {
       const int row = i * RPI + lane / LPR;
       const int32_t s = __shfl_sync(0xffffffffu, sl, row);
       const int64_t at = int64_t(s < 0 ? 0 : s) * D + (lane % LPR) * 16;
       const uint32_t to = dst + uint32_t(row * PITCH + (lane % LPR) * 16);
       // keys past the range are zeros (their weights are 0, and 0 * V must be 0)
       rxk::cp_async_16(to, kbase + at, s >= 0);
-      rxk::cp_async_16(to + kKeys * PITCH, vbase + at, s >= 0);
+      rxk::cp_async_16(to + KEYS * PITCH, vbase + at, s >= 0);
     }
   };
   __syncwarp();  // the previous unit's last stage has been read
@@ -251,26 +260,31 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
 
   const uint32_t k_lane =
       uint32_t(((lane & 7) + ((lane >> 3) & 1) * 8) * PITCH + (lane >> 4) * 16);
-  const uint32_t v_lane = uint32_t(kKeys * PITCH) + k_lane;
+  const uint32_t v_lane = uint32_t(KEYS * PITCH) + k_lane;
 
 #pragma unroll 1
   for (int st = 0; st < n_steps; ++st) {
     rxk::cp_async_wait<S - 2>();
-    __syncwarp();
+    __syncwarp();  // every lane has its part of this stage, and is done with the last one
+    if (st + S - 1 < n_steps) issue(st + S - 1);
+    rxk::cp_async_commit();
     const uint32_t stage = ring + uint32_t(st % S) * Cfg::STAGE_BYTES;
     const float2* sc = reinterpret_cast<const float2*>(
         ring_g + (st % S) * Cfg::STAGE_BYTES + Cfg::SCALES);
-    float x[NR][2][4];  // m-tile h: keys 16 h + g (+ 8)
+    // (K is converted too: mma.sync on e4m3 operands, with Q in two parts, is
+    // slower than f16 with the conversions, 161 us against 155 at 32 private
+    // contexts of 8,000 keys)
+    float x[NR][MT][4];  // m-tile h: keys 16 h + g (+ 8)
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < MT; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[nt][h][e] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < NK; kk += 2) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < MT; ++h) {
         uint32_t r0, r1, r2, r3;
         rxk::ldsm_x4(stage + k_lane + uint32_t(h * 16 * PITCH + kk * 16), r0, r1, r2, r3);
         const uint32_t a0 = kv8::to_f16x2(r0), a1 = kv8::to_f16x2(r1),
@@ -284,29 +298,36 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
         }
       }
     }
-    float2 s4[4];  // scales of keys g, g + 8, g + 16, g + 24
+    float2 s4[2 * MT];  // scales of keys g, g + 8, ..
+    float vmax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s4[i] = sc[g + 8 * i];
-    const int key0 = kb + st * kKeys + g;
-    bool grow = fmaxf(fmaxf(s4[0].y, s4[1].y), fmaxf(s4[2].y, s4[3].y)) > vref;
+    for (int i = 0; i < 2 * MT; ++i) {
+      s4[i] = sc[g + 8 * i];
+      vmax = fmaxf(vmax, s4[i].y);
+    }
+    const int key0 = kb + st * KEYS + g;
+    bool grow = vmax > vref;
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * MT; ++i) {
           float& y = x[nt][i >> 1][(i & 1) * 2 + e];
           y = key0 + 8 * i < ke ? y * (s4[i].x * rs[nt][e]) : -INFINITY;
           grow |= y > m_ref[nt][e] + kRescaleThreshold;
         }
     if (__any_sync(0xffffffffu, grow)) {
-      float vm = fmaxf(fmaxf(s4[0].y, s4[1].y), fmaxf(s4[2].y, s4[3].y));
+      float vm = vmax;
       float mx[NR][2];
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          mx[nt][e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]), fmaxf(x[nt][1][e], x[nt][1][2 + e]));
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(x[nt][0][e], x[nt][0][2 + e]);
+          if (MT == 2)
+            mx[nt][e] = fmaxf(mx[nt][e], fmaxf(x[nt][MT - 1][e], x[nt][MT - 1][2 + e]));
+        }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
@@ -342,16 +363,16 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
     }
     // P^T operands: b0 (keys 2c, 2c+1 of row g) is the transpose of the
     // accumulators' (key g, rows 2c, 2c+1)
-    float wv[4];
+    float wv[2 * MT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wv[i] = s4[i].y * inv_vref;
-    uint32_t pb[NR][4];
+    for (int i = 0; i < 2 * MT; ++i) wv[i] = s4[i].y * inv_vref;
+    uint32_t pb[NR][2 * MT];
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
       const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0] - kWeightBias;
       const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1] - kWeightBias;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2 * MT; ++i) {
         const float p0 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2] - m0);
         const float p1 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2 + 1] - m1);
         l_run[nt][0] += p0;
@@ -360,7 +381,7 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < MT; ++h)
 #pragma unroll
       for (int mt = 0; mt < NK; mt += 2) {
         uint32_t r0, r1, r2, r3;
@@ -380,9 +401,6 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
           mma_f16(o[nt][mt + 1], b0, b1, b2, b3, pb[nt][2 * h], pb[nt][2 * h + 1]);
         }
       }
-    __syncwarp();  // every lane is done with this stage before it is refilled
-    if (st + S - 1 < n_steps) issue(st + S - 1);
-    rxk::cp_async_commit();
   }
   rxk::cp_async_wait<0>();
 
