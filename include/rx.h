@@ -870,6 +870,28 @@ rx_status rx_kv8_decode_attention(
     int32_t step, float scale, void* d_out, int32_t out_type, float* d_lse,
     void* d_workspace, size_t workspace_bytes, rx_stream_t stream);
 
+/* rx_extend_batches over an 8-bit pool: per batch rx_kv8_store of its new
+ * tokens, then rx_kv8_extend_attention into its fp32 outputs.  The new slots
+ * of a batch stand in the order rx_kv8_store asks for, as the cache's calls
+ * return them when the page size is a multiple of the pool's block. */
+rx_status rx_kv8_extend_batches(const rx_kv8_pool_desc* pool, int32_t layer,
+                                int32_t num_q_heads,
+                                const rx_extend_batch* batches, int32_t n,
+                                float scale, const rx_event_t* events,
+                                rx_stream_t stream);
+
+/* rx_decode_steps over an 8-bit pool: per step rx_kv8_store of its B tokens
+ * (always a launch of its own), then rx_kv8_decode_attention into its fp32
+ * outputs.  At B = 0 nothing is launched.  Stops at the first error; errors
+ * as rx_decode_steps. */
+rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t layer,
+                              int32_t num_q_heads,
+                              const int32_t* d_req_to_token,
+                              int64_t row_stride, const rx_decode_step* steps,
+                              int32_t n_steps, int32_t B, float scale,
+                              void* d_workspace, size_t workspace_bytes,
+                              rx_stream_t stream);
+
 /* Page-locked host memory of exactly `bytes` bytes, mapped into the device
  * address space and usable from every device (cudaHostAlloc, portable and
  * mapped): for a host pool that rx_kv_copy reads and writes directly, and

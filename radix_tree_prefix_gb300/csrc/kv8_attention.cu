@@ -242,9 +242,10 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
       for (int e = 0; e < 2; ++e)
         qb[nt][kk][e] = pack_f16(__uint_as_float(qb[nt][kk][e] << 16) * f,
                                  __uint_as_float(qb[nt][kk][e] & 0xffff0000u) * f);
+    // a query that is not finite has no defined scores: its row is NaN
+    const float mine = amax < INFINITY ? a.scale_log2 * kv8::pow2(-sh) : NAN;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      rs[nt][e] = a.scale_log2 * kv8::pow2(-__shfl_sync(0xffffffffu, sh, 4 * (2 * c + e)));
+    for (int e = 0; e < 2; ++e) rs[nt][e] = __shfl_sync(0xffffffffu, mine, 4 * (2 * c + e));
   }
 
   float o[NR][NK][4];
@@ -878,4 +879,60 @@ extern "C" rx_status rx_kv8_decode_attention(
   cudaLaunchKernelEx(&cfg, merge, indptr, parts, wo, wl, int(num_q_heads), int(B), d_out,
                      int(a.out_bf16), d_lse);
   return rx_internal::launch_status("rx_kv8_decode_attention: merge");
+}
+
+extern "C" rx_status rx_kv8_extend_batches(const rx_kv8_pool_desc* pool, int32_t layer,
+                                           int32_t num_q_heads, const rx_extend_batch* batches,
+                                           int32_t n, float scale, const rx_event_t* events,
+                                           rx_stream_t stream) {
+  if (n < 0 || (n && !batches))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_extend_batches: bad batch list");
+  rx_status r = rx_internal::check_kv8_pool(pool, layer);
+  if (r != RX_OK) return r;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto mark = [&](int32_t i, int k) -> rx_status {
+    if (!events) return RX_OK;
+    if (cudaEventRecord(reinterpret_cast<cudaEvent_t>(events[4 * int64_t(i) + k]), s) !=
+        cudaSuccess)
+      return rx_internal::launch_status("rx_kv8_extend_batches: event record");
+    return RX_OK;
+  };
+  // in batch order on one stream: a batch reads what the ones before it stored
+  for (int32_t i = 0; i < n; ++i) {
+    const rx_extend_batch& b = batches[i];
+    if ((r = mark(i, 0)) != RX_OK) return r;
+    r = rx_kv8_store(pool, layer, b.d_new_slots, b.d_k, b.d_v, b.n_new, stream);
+    if (r != RX_OK) return r;
+    if ((r = mark(i, 1)) != RX_OK || (r = mark(i, 2)) != RX_OK) return r;
+    r = rx_kv8_extend_attention(pool, layer, b.d_q, num_q_heads, b.d_req_to_token, b.row_stride,
+                                b.d_req_rows, b.d_prefix_len, b.d_qo_indptr, b.d_tile_indptr, b.R,
+                                b.num_tiles, scale, b.d_out, RX_OUT_F32, b.d_lse, stream);
+    if (r != RX_OK) return r;
+    if ((r = mark(i, 3)) != RX_OK) return r;
+  }
+  return RX_OK;
+}
+
+extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t layer,
+                                         int32_t num_q_heads, const int32_t* d_req_to_token,
+                                         int64_t row_stride, const rx_decode_step* steps,
+                                         int32_t n_steps, int32_t B, float scale,
+                                         void* d_workspace, size_t workspace_bytes,
+                                         rx_stream_t stream) {
+  if (n_steps < 0 || (n_steps && !steps))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_steps: bad step list");
+  rx_status r = rx_internal::check_kv8_pool(pool, layer);
+  if (r != RX_OK) return r;
+  if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_steps: Hq % Hkv != 0");
+  for (int32_t i = 0; i < n_steps; ++i) {
+    const rx_decode_step& t = steps[i];
+    r = rx_kv8_store(pool, layer, t.d_slots, t.d_k, t.d_v, B, stream);
+    if (r != RX_OK) return r;
+    r = rx_kv8_decode_attention(pool, layer, t.d_q, num_q_heads, d_req_to_token, row_stride,
+                                t.d_plan, t.info, B, t.step, scale, t.d_out, RX_OUT_F32, t.d_lse,
+                                d_workspace, workspace_bytes, stream);
+    if (r != RX_OK) return r;
+  }
+  return RX_OK;
 }

@@ -535,6 +535,11 @@ class Engine:
     prefilled, and after each wave's finish every finished sequence is
     written through to the host pool (``rx_write_through_batch`` +
     ``rx_kv_copy``).
+    ``kv8_block`` > 0 keeps the KV in an 8-bit pool (e4m3 codes, a scale per
+    KV head and block of that many slots; a power of two up to 64 that divides
+    the page size, so that a page's blocks fill in order) instead of bf16:
+    half the memory and half the bytes a decode step reads.  It has no host
+    tier.
     With ``out_ring`` (an ``OutputRing``) every launch writes into the ring's
     next device buffer and the ring copies each buffer back to the host once
     the next launch takes a buffer (and at the end of a run); the tensors the
@@ -544,7 +549,14 @@ class Engine:
     def __init__(self, wl, device=None, inputs=None, layers=None, on_extend=None,
                  on_decode=None, stream=None, timing=False, on_decode_wave=None,
                  reuse_outputs=False, out_ring=None, policy="fcfs", chunk_tokens=None,
-                 host_slots=0):
+                 host_slots=0, kv8_block=0):
+        if kv8_block:
+            if kv8_block not in (1, 2, 4, 8, 16, 32, 64) or wl.page_size % kv8_block:
+                raise ValueError(f"kv8_block {kv8_block}: a power of two up to 64 that divides "
+                                 f"the page size {wl.page_size}")
+            if host_slots:
+                raise ValueError("the 8-bit KV pool has no host tier (host_slots)")
+        self.kv8_block = int(kv8_block)
         self.wl = wl
         self.device = device
         self.inputs = inputs
@@ -576,10 +588,16 @@ class Engine:
             if self.stream is None:
                 self.stream = torch.cuda.current_stream(device)
             L, hkv, d = wl.num_layers, wl.num_kv_heads, wl.head_dim
-            self.k_pool = torch.empty((L, hkv, wl.num_slots, d), dtype=torch.bfloat16,
-                                      device=device)
+            self.k_pool = torch.empty((L, hkv, wl.num_slots, d), device=device,
+                                      dtype=torch.float8_e4m3fn if self.kv8_block else
+                                      torch.bfloat16)
             self.v_pool = torch.empty_like(self.k_pool)
-            self.pool = rx.pool_desc(self.k_pool, self.v_pool)
+            if self.kv8_block:
+                self.kv_scales = torch.empty((L, hkv, wl.num_slots // self.kv8_block, 2),
+                                             dtype=torch.float32, device=device)
+                self.pool = rx.kv8_pool_desc(self.k_pool, self.v_pool, self.kv_scales)
+            else:
+                self.pool = rx.pool_desc(self.k_pool, self.v_pool)
             if self.host_slots:
                 self.hk_pool = torch.empty((L, hkv, self.host_slots, d), dtype=torch.bfloat16,
                                            pin_memory=True)
@@ -922,8 +940,7 @@ class Engine:
                 for g in range(lo, hi):
                     e = [rx.NativeEvent(x) for x in ev[4 * (g - lo):4 * (g - lo) + 4]]
                     self.kernel_events.append(
-                        ("kv_store", e[0], e[1],
-                         float(4 * total_new_bytes(n_new[g], wl) + 4 * n_new[g])))
+                        ("kv_store", e[0], e[1], self._store_bytes(n_new[g])))
                     self.kernel_events.append(("extend", e[2], e[3], flops[g]))
 
         if self.out_ring is not None or getattr(self.inputs, "host", False):
@@ -973,9 +990,17 @@ class Engine:
         self.max_extend_rows = max(self.max_extend_rows, total_q)
         flops = self._extend_flops(prefix, qo) if self.timing else 0.0
         outs = {}
-        store_bytes = float(4 * total_new_bytes(len(new_slots), wl) + 4 * len(new_slots))
+        store_bytes = self._store_bytes(len(new_slots))
         for layer in self.layers:
             q, k, v = inputs[layer]
+            if self.kv8_block:
+                out, lse = self._outputs(("ext", self.batch_no, layer),
+                                         (total_q, wl.num_q_heads, wl.head_dim))
+                self._extend_kv8(layer, chunks, (d_tab, d_rows, d_prefix, d_qo, d_tiles, d_slots),
+                                 d_extra, (R, n_tiles, width, len(new_slots)), q, k, v, out, lse,
+                                 store_bytes, flops)
+                outs[layer] = (out, lse)
+                continue
             ev = self._event_start()
             rx.kv_store(self.pool, layer, d_slots, k, v, self.stream)
             self._event_end(ev, "kv_store", store_bytes)
@@ -1002,6 +1027,35 @@ class Engine:
             outs[layer] = (out, lse)
         if self.on_extend is not None:
             self.on_extend(self.batch_no, [r.rid for r in reqs], prefix.copy(), qo, outs)
+
+    def _extend_kv8(self, layer, chunks, spans, d_extra, sizes, q, k, v, out, lse, store_bytes,
+                    flops):
+        """One layer of an extend batch over the 8-bit pool: a record that
+        stores the new tokens, then one per chunk of queries (a single chunk:
+        both in one record)."""
+        d_tab, d_rows, d_prefix, d_qo, d_tiles, d_slots = spans
+        R, n_tiles, width, n_new = sizes
+        parts = [(d_rows, d_prefix, d_qo, d_tiles, R, n_tiles, 0)] if len(chunks) == 1 else [
+            (*d_extra[4 * i:4 * i + 4], len(ch["rows"]), ch["n_tiles"], ch["q0"])
+            for i, ch in enumerate(chunks)]
+        rec = np.zeros(len(parts), dtype=rx.EXTEND_BATCH_DTYPE)
+        rec["d_k"], rec["d_v"] = k.data_ptr(), v.data_ptr()
+        rec["d_new_slots"], rec["d_req_to_token"] = d_slots.ptr, d_tab.ptr
+        rec["row_stride"] = width
+        rec["n_new"][0] = n_new
+        for i, (rows, prefix, qo, tiles, n, nt, q0) in enumerate(parts):
+            rec["d_req_rows"][i], rec["d_prefix_len"][i] = rows.ptr, prefix.ptr
+            rec["d_qo_indptr"][i], rec["d_tile_indptr"][i] = qo.ptr, tiles.ptr
+            rec["R"][i], rec["num_tiles"][i] = n, nt
+            rec["d_q"][i], rec["d_out"][i], rec["d_lse"][i] = (
+                q[q0:].data_ptr(), out[q0:].data_ptr(), lse[q0:].data_ptr())
+        ev = self._events.take(4 * len(rec)) if self.timing else None
+        rx.extend_batches(self.pool, layer, self.wl.num_q_heads, rec, self.scale, ev, self.stream)
+        self.gpu_launches += 1 + len(rec)
+        if ev is not None:
+            e = [rx.NativeEvent(x) for x in ev]
+            self.kernel_events.append(("kv_store", e[0], e[1], store_bytes))
+            self.kernel_events.append(("extend", e[2], e[-1], flops))
 
     def _decode_phase(self, wave, ctx0, prompt_nodes):
         """All decode steps of a wave.  Slot allocation and the decode plan
@@ -1095,6 +1149,8 @@ class Engine:
         stores the new tokens itself), the decode kernel (one fused launch
         for tensor-core and warp-role items), merge."""
         i = infos[0]
+        if self.kv8_block:   # store, tiles, streams, merge
+            return 2 + int(int(i.n_work_tc) > 0) + int(int(i.n_work) > int(i.n_work_tc))
         store = 0 if int(i.tails_private) == 1 else 1
         return store + int(int(i.n_work) > 0) + 1
 
@@ -1113,6 +1169,19 @@ class Engine:
         e.record(self.stream)
         self.kernel_events.append((kind, start, e, work))
 
+    def _kv_bytes(self):
+        """Bytes of a stored token's K and V, of one layer (8-bit pool: with
+        its share of the scales)."""
+        wl = self.wl
+        if self.kv8_block:
+            return wl.num_kv_heads * (2 * wl.head_dim + 8 / self.kv8_block)
+        return 2 * wl.num_kv_heads * wl.head_dim * 2
+
+    def _store_bytes(self, n):
+        """Algorithmic bytes of a store of n tokens: bf16 K and V read, the
+        pool's written, the slots."""
+        return float(2 * total_new_bytes(n, self.wl) + n * self._kv_bytes() + 4 * n)
+
     def _extend_flops(self, prefix, qo):
         """Algorithmic FLOPs of one extend launch: 4 * d * Hq per visible
         (query, key) pair; query i of a suffix of s over a prefix p sees
@@ -1124,11 +1193,11 @@ class Engine:
 
     def decode_bytes(self, info, B, extra_tokens=0):
         """Algorithmic bytes of one decode launch: the distinct KV of the
-        batch read once (K and V, bf16), its slot indices, Q (bf16) and the
+        batch read once (K and V, as stored), its slot indices, Q (bf16) and the
         fp32 output and lse.  ``extra_tokens`` adds tokens beyond the plan's
         step-0 count (later steps of a multi-step plan)."""
         wl = self.wl
-        kv = (info.distinct_kv_tokens + extra_tokens) * (2 * wl.num_kv_heads * wl.head_dim * 2 + 4)
+        kv = (info.distinct_kv_tokens + extra_tokens) * (self._kv_bytes() + 4)
         q = B * wl.num_q_heads * wl.head_dim * 2
         o = B * wl.num_q_heads * (wl.head_dim + 1) * 4
         return float(kv + q + o)

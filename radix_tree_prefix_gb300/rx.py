@@ -167,6 +167,8 @@ _SIGS = {
     "rx_kv8_extend_attention": [P, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P, P],
     "rx_kv8_decode_attention": [P, I32, P, I32, P, I64, P, P, I32, I32, F32, P, I32, P, P, SZ,
                                 P],
+    "rx_kv8_extend_batches": [P, I32, I32, P, I32, F32, P, P],
+    "rx_kv8_decode_steps": [P, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
     "rx_device_check": [P],
 }
 for _name, _args in _SIGS.items():
@@ -582,15 +584,18 @@ def decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_ou
 
 
 def extend_batches(pool, layer, hq, batches, scale, events=None, stream=None):
-    """rx_extend_batches over a numpy array of EXTEND_BATCH_DTYPE records;
+    """rx_extend_batches (for an 8-bit pool rx_kv8_extend_batches) over a numpy
+    array of EXTEND_BATCH_DTYPE records;
     ``events`` is None or a uint64 array of 4 event handles per batch."""
     assert batches.dtype == EXTEND_BATCH_DTYPE and batches.flags.c_contiguous
     ev = None
     if events is not None:
         assert events.dtype == np.uint64 and len(events) >= 4 * len(batches)
         ev = events.ctypes.data
-    _check(_lib.rx_extend_batches(C.byref(pool), layer, hq, batches.ctypes.data, len(batches),
-                                  scale, ev, _stream(stream)))
+    fn = _lib.rx_kv8_extend_batches if isinstance(pool, rx_kv8_pool_desc) else \
+        _lib.rx_extend_batches
+    _check(fn(C.byref(pool), layer, hq, batches.ctypes.data, len(batches), scale, ev,
+              _stream(stream)))
 
 
 class EventPool:
@@ -636,16 +641,17 @@ class NativeEvent:
 
 
 def decode_steps(pool, layer, hq, d_table, steps, B, scale, d_workspace, stream=None):
-    """rx_decode_steps over a ctypes array of rx_decode_step or a numpy array
-    of DECODE_STEP_DTYPE records."""
+    """rx_decode_steps (for an 8-bit pool rx_kv8_decode_steps) over a ctypes
+    array of rx_decode_step or a numpy array of DECODE_STEP_DTYPE records."""
     if isinstance(steps, np.ndarray):
         assert steps.dtype == DECODE_STEP_DTYPE and steps.flags.c_contiguous
         ptr = steps.ctypes.data
     else:
         ptr = C.cast(steps, C.c_void_p)
-    _check(_lib.rx_decode_steps(C.byref(pool), layer, hq, d_table.data_ptr(), d_table.shape[1],
-                                ptr, len(steps), B, scale, d_workspace.data_ptr(),
-                                d_workspace.numel() * d_workspace.element_size(), _stream(stream)))
+    fn = _lib.rx_kv8_decode_steps if isinstance(pool, rx_kv8_pool_desc) else _lib.rx_decode_steps
+    _check(fn(C.byref(pool), layer, hq, d_table.data_ptr(), d_table.shape[1], ptr, len(steps), B,
+              scale, d_workspace.data_ptr(), d_workspace.numel() * d_workspace.element_size(),
+              _stream(stream)))
 
 
 def verify_rows(prefix_len, prefix_rows, draft_indptr, parents, draft_slots, out_stride):
