@@ -710,7 +710,10 @@ def kv8_pool_desc(k_codes, v_codes, scales):
     p.index = k_codes.get_device()  # -1 on the CPU
     p.ref = C.byref(p)
     p.dtypes = (torch.int32, torch.bfloat16, torch.float32)
-    p.cuda = torch.cuda
+    p.current_device = torch.cuda.current_device
+    # the handle of a device's current stream (torch.cuda.current_stream makes
+    # a Stream object, 2.9 us of a store's 8)
+    p.current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return p
 
 
@@ -729,12 +732,13 @@ def _kv8_args(pool, stream, *tensors):
             raise ValueError(f"kv8: {name} must be a contiguous {dtype} tensor of at least {n} "
                              f"elements on {pool.device}, got {t.dtype} {tuple(t.shape)} on "
                              f"{t.device}")
-    current = pool.cuda.current_stream() if stream is None else stream
-    if current.device_index != dev:
-        raise ValueError(f"kv8: the stream is on {current.device}, the pool on {pool.device}")
-    if stream is not None and pool.cuda.current_device() != dev:
+    if pool.current_device() != dev:
         raise ValueError(f"kv8: the pool is on {pool.device}, which is not the current device")
-    return current.cuda_stream
+    if stream is None:
+        return pool.current_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"kv8: the stream is on {stream.device}, the pool on {pool.device}")
+    return stream.cuda_stream
 
 
 def kv8_store(pool, layer, d_slots, d_k, d_v, stream=None):
