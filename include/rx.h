@@ -843,7 +843,9 @@ rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
  * schedule and causal rule.  d_out is fp32 or bf16 (out_type) [total_q][Hq]
  * [head_dim], rounded once from fp32; d_lse fp32 [total_q][Hq].  Scores and
  * softmax statistics are held in fp32; a query's softmax weights are rounded
- * to f16 (11 significant bits) for the product with V.  scale must lie in
+ * to f16 (11 significant bits) for the product with V, and V times a scale
+ * that is not a power of two (rx_kv8_store writes no such) too.  A query that
+ * is not finite gives NaN, in its own row alone.  scale must lie in
  * [2^-40, 2^40].  A pool row that a table names must hold codes of
  * rx_kv8_store or other finite ones (not 0x7f or 0xff) and finite scales
  * of at least 2^-126; rows no table names are never read.  Errors: RX_ERR_INVALID as

@@ -6,15 +6,20 @@
 // j's slot):
 //   x_j = scale * ks_j * (q . kc_j),  p_j = exp(x_j - m),  l = sum_j p_j,
 //   o = sum_j (p_j vs_j) vc_j / l,    lse = m + log l.
-// A code is exact in f16, so the scales never touch the codes: ks_j
-// multiplies a score, vs_j a softmax weight.  The products run on f16 tensor
-// instructions with fp32 accumulators: q (8 significant bits in bf16) is
-// exact in f16 once its row is scaled by a power of two, and p_j vs_j is
-// rounded to f16 (11 bits) relative to the largest vs so far.
+// ks_j multiplies a score.  vs_j joins the weight or the value, as a quotient
+// by a reference vref that is at least the largest vs so far; the result is
+// scaled back at the end.
 //
 // Extend, and decode items of more query rows than one warp takes, run on the
 // tensor-core tile of kv8_tile.cuh; decode items of few rows (a request's own
-// tail) on warps that stream the keys (stream_unit below).
+// tail) on warps that stream the keys (stream_unit below).  Statistics, scores
+// and accumulators are fp32.  What is rounded further:
+//   q        not at all but for elements under 2^-18 (tile, two e4m3 parts) or
+//            2^-27 (streams, f16) of its row's largest: 8 bits in bf16;
+//   weights  to f16, 11 bits: p_j in the tile, p_j vs_j / vref in the streams;
+//   values   in the tile vs_j / vref and its product with a code are f16: exact
+//            for the power-of-two scales that rx_kv8_store writes;
+//   output   once, if bf16.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -7,11 +7,11 @@ weight is under 2^-20 of the largest, 2^-25 of 2^-6 of the largest V scale);
 a score carries fp32 rounding of its d products, and of a query elements under
 2^-27 of the row's largest or so, in all at most 2^-18 of the row's largest
 magnitude per element; an fp32 output nothing else of size, a bf16 output half
-a step more (2^-8).  The tiles apply a scale as the f16 product of a code and
+a step more (2^-8).  The tiles apply a V scale as the f16 product of a code and
 the quotient of the scale and a reference: exact for powers of two, for any
 other scale two more roundings of 2^-11 each.  Then a term p v is off by at
-most (1 + 2^-11)^3 - 1 < 3.01 2^-11 of itself, and a score by at most (1 +
-2^-11)^2 - 1 < 2.01 2^-11 of the sum of the magnitudes of its products.
+most (1 + 2^-11)^3 - 1 < 3.01 2^-11 of itself.  K scales multiply scores in
+fp32.
 """
 
 import ctypes as C
@@ -463,7 +463,7 @@ class Case:
         if pow2:
             s = torch.exp2(torch.floor(torch.log2(s)))
         self.term = 2.0 ** -11 if pow2 else 3.01 * 2.0 ** -11
-        self.score = 2.0 ** -20 if pow2 else 2.0 ** -20 + 2.01 * 2.0 ** -11
+        self.score = 2.0 ** -20
         ub = torch.from_numpy(np.unique(used // block)).cuda()
         self.sc[1][:, ub] = s[:, ub]
         self.scale = 1.0 / np.sqrt(d) if not unit_scale else 1.0
