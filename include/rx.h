@@ -847,8 +847,8 @@ rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
  * that is not a power of two (rx_kv8_store writes no such) too.  A query that
  * is not finite gives NaN, in its own row alone.  scale must lie in
  * [2^-40, 2^40].  A pool row that a table names must hold codes of
- * rx_kv8_store or other finite ones (not 0x7f or 0xff) and finite scales
- * of at least 2^-126; rows no table names are never read.  Errors: RX_ERR_INVALID as
+ * rx_kv8_store or other finite ones (not 0x7f or 0xff) and scales in
+ * [2^-126, 2^120]; rows no table names are never read.  Errors: RX_ERR_INVALID as
  * rx_extend_attention, for a scale out of range and an unknown out_type. */
 rx_status rx_kv8_extend_attention(
     const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q,

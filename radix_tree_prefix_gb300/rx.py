@@ -113,6 +113,8 @@ OUT_F32, OUT_BF16 = 0, 1      # RX_OUT_* of rx.h
 
 P = C.c_void_p
 I32, I64, F32, SZ = C.c_int32, C.c_int64, C.c_float, C.c_size_t
+# a call takes the descriptor of its own kind of pool (ctypes refuses the other)
+POOL, POOL8 = C.POINTER(rx_pool_desc), C.POINTER(rx_kv8_pool_desc)
 _SIGS = {
     "rx_cache_create": [P, P],
     "rx_cache_destroy": [P],
@@ -149,26 +151,26 @@ _SIGS = {
     "rx_alloc_decode_steps": [P, I32, I32, P, P, P],
     "rx_schedule": [P, I32, I32, P, P, P],
     "rx_verify_rows": [I32, P, P, I64, P, P, P, P, I64, P, P],
-    "rx_verify_attention": [P, I32, P, I32, P, I64, P, P, I32, F32, P, P, P, SZ, P],
-    "rx_kv_copy": [P, P, P, P, I64, P],
-    "rx_kv_store": [P, I32, P, P, P, I64, P],
+    "rx_verify_attention": [POOL, I32, P, I32, P, I64, P, P, I32, F32, P, P, P, SZ, P],
+    "rx_kv_copy": [POOL, POOL, P, P, I64, P],
+    "rx_kv_store": [POOL, I32, P, P, P, I64, P],
     "rx_req_to_token_write": [P, I64, I64, P, P, P, I64, P],
     "rx_extend_plan": [P, I32, I32, I32, I32, P, P],
-    "rx_extend_attention": [P, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, P, P],
-    "rx_decode_attention": [P, I32, P, I32, P, I64, P, P, I32, F32, P, P, P, SZ, P],
-    "rx_decode_attention_static": [P, I32, P, I32, P, I64, P, P, I32, F32, P, P, P],
-    "rx_decode_steps": [P, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
-    "rx_extend_batches": [P, I32, I32, P, I32, F32, P, P],
+    "rx_extend_attention": [POOL, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, P, P],
+    "rx_decode_attention": [POOL, I32, P, I32, P, I64, P, P, I32, F32, P, P, P, SZ, P],
+    "rx_decode_attention_static": [POOL, I32, P, I32, P, I64, P, P, I32, F32, P, P, P],
+    "rx_decode_steps": [POOL, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
+    "rx_extend_batches": [POOL, I32, I32, P, I32, F32, P, P],
     "rx_events_create": [I32, P],
     "rx_events_destroy": [I32, P],
     "rx_event_elapsed_ms": [P, P, P],
-    "rx_kv8_store": [P, I32, P, P, P, I64, P],
-    "rx_kv8_load": [P, I32, P, P, P, I64, P],
-    "rx_kv8_extend_attention": [P, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P, P],
-    "rx_kv8_decode_attention": [P, I32, P, I32, P, I64, P, P, I32, I32, F32, P, I32, P, P, SZ,
+    "rx_kv8_store": [POOL8, I32, P, P, P, I64, P],
+    "rx_kv8_load": [POOL8, I32, P, P, P, I64, P],
+    "rx_kv8_extend_attention": [POOL8, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P, P],
+    "rx_kv8_decode_attention": [POOL8, I32, P, I32, P, I64, P, P, I32, I32, F32, P, I32, P, P, SZ,
                                 P],
-    "rx_kv8_extend_batches": [P, I32, I32, P, I32, F32, P, P],
-    "rx_kv8_decode_steps": [P, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
+    "rx_kv8_extend_batches": [POOL8, I32, I32, P, I32, F32, P, P],
+    "rx_kv8_decode_steps": [POOL8, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
     "rx_device_check": [P],
 }
 for _name, _args in _SIGS.items():

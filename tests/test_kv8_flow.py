@@ -66,6 +66,28 @@ def test_waves_refuse_bad_lists_before_any_cuda_call():
     assert _calls()["store"](ok, T=-1) == rx.RX_ERR_INVALID
 
 
+def test_calls_refuse_the_other_kind_of_pool():
+    """A bf16 call never reads an 8-bit pool's descriptor, nor the reverse."""
+    torch = pytest.importorskip("torch")
+    kc = torch.zeros((1, 2, 64, 128), dtype=torch.uint8)
+    p8 = rx.kv8_pool_desc(kc, kc.clone(), torch.ones((1, 2, 16, 2)))
+    kp = torch.zeros((1, 2, 64, 128), dtype=torch.bfloat16)
+    p16 = rx.pool_desc(kp, kp)
+    lib = rx._lib
+    for name, types in rx._SIGS.items():
+        if types and types[0] in (rx.POOL, rx.POOL8):
+            other = p16 if types[0] is rx.POOL8 else p8
+            args = [C.byref(other) if t in (rx.POOL, rx.POOL8) else
+                    0 if t in (C.c_int32, C.c_int64, C.c_size_t) else
+                    0.0 if t is C.c_float else None for t in types]
+            with pytest.raises(C.ArgumentError):
+                getattr(lib, name)(*args)
+    s = torch.zeros(3, dtype=torch.int32)
+    x = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(AttributeError):
+        rx.kv8_store(p16, 0, s, x, x)
+
+
 # --------------------------------------------------------------------- flows
 def _to_e4m3_values(vals):
     import torch
