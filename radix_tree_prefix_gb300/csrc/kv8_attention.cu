@@ -436,6 +436,16 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
     }
 }
 
+// Extend calls of few tiles: a cluster of CTAs per tile, which share its keys.
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    extend8_split_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int c = int(blockIdx.x) / cluster_size();
+  const int hkv = a.hq / a.group;
+  tile8<D, false, true>(a, maps, smem_raw, a.num_tiles - 1 - c / hkv, c % hkv);
+}
+
 // Decode, items of few rows: warps take units (item, KV head) until none is
 // left.  With tile items in the plan the kernel is launched after theirs and
 // starts beside it, on the SMs that the tiles leave free and as they finish;
@@ -733,6 +743,67 @@ int32_t kv8_attention_error_flags(bool clear) {
 
 }  // namespace rx_internal
 
+namespace {
+
+void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned tiles, int split,
+                    int bytes) {
+  cfg->gridDim = dim3(tiles * unsigned(split));
+  cfg->blockDim = dim3(kTileThreads);
+  cfg->dynamicSmemBytes = size_t(bytes);
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// CTAs that share a tile's keys: the most, a power of two up to 16, of which the
+// device runs all clusters at once and a table row (the host knows its width,
+// not the contexts) gives each a part.  20 queries over 8,000 keys, 8 heads: 91
+// us with one CTA a tile, 29 so; 200 queries of one head over 21,800 keys: 375
+// and 49.  Parts below three key tiles lose (20 queries over 400 keys, 8 heads:
+// 19 us unsplit, 21 in two), and so do clusters in more than one wave (168
+// tiles of 3,200 keys: 75 us unsplit, 87).
+constexpr int kMaxSplitLog2 = 4;
+template <int D>
+rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
+  static std::atomic<bool> done[kMaxDevices];
+  static std::atomic<int> fit[kMaxDevices][kMaxSplitLog2 + 1];  // clusters at once, + 1
+  *split = 1;
+  if (tiles * 2 > rx_internal::sm_count() || key_tiles < 2 * kMinPart) return RX_OK;
+  rx_status st = ensure_smem(done, extend8_split_kernel<D>, Tile8<D>::BYTES);
+  if (st != RX_OK) return st;
+  int dev = -1;
+  cudaGetDevice(&dev);
+  for (int lg = kMaxSplitLog2; lg >= 1; --lg) {
+    if (key_tiles >> lg < kMinPart) continue;
+    int n = fit[dev][lg].load(std::memory_order_relaxed);
+    if (n == 0) {
+      if (lg > 3 && cudaFuncSetAttribute(extend8_split_kernel<D>,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                         1) != cudaSuccess)
+        cudaGetLastError();
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute attr[1];
+      cluster_config(&cfg, attr, 1, 1 << lg, Tile8<D>::BYTES);
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, extend8_split_kernel<D>, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // no cluster of this size
+        c = 0;
+      }
+      n = c + 1;
+      fit[dev][lg].store(n, std::memory_order_relaxed);
+    }
+    if (tiles <= n - 1) {
+      *split = 1 << lg;
+      break;
+    }
+  }
+  return RX_OK;
+}
+
+}  // namespace
+
 extern "C" rx_status rx_kv8_extend_attention(
     const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
     const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_req_rows,
@@ -766,6 +837,26 @@ extern "C" rx_status rx_kv8_extend_attention(
                         row_stride * pool->num_kv_heads * int64_t(D) * 2 <= (int64_t(32) << 20);
   const unsigned ctas = unsigned(num_tiles * pool->num_kv_heads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int split = 1;
+  const int bn = D == 128 ? Tile8<128>::BN : Tile8<256>::BN;
+  const int64_t key_tiles = (row_stride + bn - 1) / bn;
+  st = D == 128 ? cluster_split<128>(ctas, key_tiles, &split)
+                : cluster_split<256>(ctas, key_tiles, &split);
+  if (st != RX_OK) return st;
+  if (split > 1) {
+    Maps8 maps;
+    st = make_maps(&maps, pool);
+    if (st != RX_OK) return st;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cluster_config(&cfg, attr, ctas, split, D == 128 ? Tile8<128>::BYTES : Tile8<256>::BYTES);
+    cfg.stream = s;
+    if (D == 128)
+      cudaLaunchKernelEx(&cfg, extend8_split_kernel<128>, a, maps);
+    else
+      cudaLaunchKernelEx(&cfg, extend8_split_kernel<256>, a, maps);
+    return rx_internal::launch_status("rx_kv8_extend_attention");
+  }
   static std::atomic<bool> done128[kMaxDevices], done256[kMaxDevices];
   st = D == 128 ? ensure_smem(done128, extend8_kernel<128>, Tile8<128>::BYTES)
                 : ensure_smem(done256, extend8_kernel<256>, Tile8<256>::BYTES);

@@ -239,7 +239,48 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return r;
 }
 
-template <int D, bool DECODE>
+// The CTA's place in its cluster, and an address in another CTA's shared memory.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return int(r);
+}
+__device__ __forceinline__ int cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+  return int(r);
+}
+// Every thread of the cluster meets; what was written to shared memory before
+// is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;\n" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// SPLIT: the CTAs of a cluster share the tile's keys (a part has kMinPart key
+// tiles at least, so short ranges use fewer CTAs) and join their normalised
+// partial rows through each other's shared memory: no workspace, one launch.
+constexpr int kMinPart = 3;
+template <int D, bool DECODE, bool SPLIT = false>
 __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t* smem_raw,
                                       int tile, int kvh) {
   using Lo = Tile8<D>;
@@ -278,7 +319,18 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const TileDesc8 t = describe8<DECODE>(a, tile);
+  TileDesc8 t = describe8<DECODE>(a, tile);
+  int parts = 1, rank = 0;
+  if constexpr (SPLIT) {
+    const int all = (t.key_end + BN - 1) / BN;
+    rank = cluster_rank();
+    parts = max(1, min(cluster_size(), all / kMinPart));
+    // (every CTA of the cluster decides alike)
+    if (parts == 1 && rank > 0) return;
+    const int first = int(int64_t(all) * rank / parts), last = int(int64_t(all) * (rank + 1) / parts);
+    if (rank < parts) t.key_end = min(t.key_end, last * BN);
+    t.key_begin = rank < parts ? first * BN : t.key_end;  // (CTAs without a part: no keys)
+  }
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
   // ---- Q: thread (wg, i) reads half of query row i
   const int wg = warp >> 2;
@@ -836,7 +888,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     if (fin && xok) {
       tc::tc_fence_after();
       const float l_all = l + xch[(xp * 2 + (1 - wg)) * BM + i];
-      const float inv = vref / l_all;  // (2^6 in both O and l)
+      // (2^6 in both O and l; a part whose keys a row does not see leaves zeros)
+      const float inv = SPLIT && l_all == 0.f ? 0.f : vref / l_all;
       // warpgroup w writes output columns [w D/2, (w+1) D/2): through shared
       // memory (Q and the K and V stages are idle), so that a warp writes
       // whole contiguous row segments
@@ -861,8 +914,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
       const bool to_bf16 = !DECODE && a.out_bf16;
       uint8_t* obase = static_cast<uint8_t*>(DECODE ? static_cast<void*>(a.ws_o) : a.out);
       int64_t q_row, out_row = -1;
-      if (valid) row_info8<DECODE>(a, t, kvh, i, q_row, out_row, lim);
-      const long long my_row = out_row;
+      if (valid && parts == 1) row_info8<DECODE>(a, t, kvh, i, q_row, out_row, lim);
+      const long long my_row = out_row;  // (-1: stays in shared memory)
       if (to_bf16) {
         constexpr int CPR = HC / 8;  // 16-byte pieces (8 columns) per row
 #pragma unroll 4
@@ -891,12 +944,60 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
             *reinterpret_cast<float4*>(obase + (ro * D + wg * HC + c4 * 4) * 4) = v;
         }
       }
-      if (valid && wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = (m_ref - kWeightBias) * kLn2 + logf(l_all);
+      const float lse = SPLIT && l_all == 0.f ? -INFINITY
+                                              : (m_ref - kWeightBias) * kLn2 + logf(l_all);
+      if (SPLIT && parts > 1) {
+        if (wg == 0) ks_ring[i] = lse;  // (the scales are done with)
+      } else if (valid && wg == 0) {
+        (DECODE ? a.ws_lse : a.lse)[out_row] = lse;
+      }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&g_kv8_att_error, 2);
+  if constexpr (SPLIT) {
+    if (parts > 1) {
+      // each CTA of the cluster joins 128 / C rows of all parts
+      cluster_sync();
+      constexpr int HC = D / 2, PITCH = HC * 4 + 16;
+      const int per = BM / cluster_size();
+      for (int idx = tid; idx < per * (D / 4); idx += kTileThreads) {
+        const int row = rank * per + idx / (D / 4), col = idx % (D / 4) * 4;
+        if (row >= t.n_rows) break;
+        const uint32_t at = base + uint32_t(col / HC * (BM * PITCH) + row * PITCH + col % HC * 4);
+        const uint32_t lse_at = base + uint32_t(Lo::KS + row * 4);
+        float m = -INFINITY;
+        for (int p = 0; p < parts; ++p) m = fmaxf(m, ld_peer(peer_addr(lse_at, p)));
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+          const float li = ld_peer(peer_addr(lse_at, p));
+          const float4 v = ld_peer4(peer_addr(at, p));
+          const float w = li == -INFINITY ? 0.f : rxk::fast_exp2((li - m) * kLog2e);
+          sum += w;
+          y.x += w * v.x;
+          y.y += w * v.y;
+          y.z += w * v.z;
+          y.w += w * v.w;
+        }
+        const float inv = 1.f / sum;
+        y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        int64_t q_row, out_row;
+        int lim;
+        row_info8<DECODE>(a, t, kvh, row, q_row, out_row, lim);
+        if (a.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + out_row * D + col) =
+              make_uint2(rxk::pack_bf16(y.x, y.y), rxk::pack_bf16(y.z, y.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * D + col) = y;
+        if (col == 0) a.lse[out_row] = m + logf(sum);
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another reads its rows
+    }
+  }
   if (warp == 12) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);

@@ -631,6 +631,13 @@ EXTEND = [
     (64, 1, 128, 8, 8, [15], [5]),
     (16, 2, 256, 1, 16, [1500], [20]),
     (8, 8, 128, 32, 32, [0], [700]),
+    # few tiles over many keys: clusters share a tile's keys, rows see some parts only
+    (1, 1, 128, 1, 1, [0], [2000]),
+    (8, 2, 128, 16, 16, [4992], [3]),
+    (2, 1, 256, 16, 16, [1488, 0, 4000], [100, 900, 1]),
+    (4, 4, 256, 1, 1, [700, 0], [30, 5]),
+    (32, 8, 128, 8, 8, [600], [400]),                # 104 CTAs: none
+    (16, 4, 256, 64, 64, [576], [390]),
 ]
 
 
