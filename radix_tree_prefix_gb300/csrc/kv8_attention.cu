@@ -501,6 +501,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tile8<D, true>(a, maps, smem_raw, int(blockIdx.x) / hkv, int(blockIdx.x) % hkv);
 }
 
+// Few of those: a cluster of CTAs per (item, KV head), which share its keys.
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    decode8_split_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  rxk::griddep_launch_dependents();
+  const int c = int(blockIdx.x) / cluster_size();
+  const int hkv = a.hq / a.group;
+  tile8<D, true, true>(a, maps, smem_raw, c / hkv, c % hkv);
+}
+
 // Extend: one tile per CTA, heaviest row tile first; heads interleaved or
 // head-major, as in the bf16 kernel.
 template <int D>
@@ -765,13 +776,14 @@ void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned
 // 19 us unsplit, 21 in two), and so do clusters in more than one wave (168
 // tiles of 3,200 keys: 75 us unsplit, 87).
 constexpr int kMaxSplitLog2 = 4;
-template <int D>
+template <int D, bool DECODE>
 rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
+  constexpr auto* kernel = DECODE ? decode8_split_kernel<D> : extend8_split_kernel<D>;
   static std::atomic<bool> done[kMaxDevices];
   static std::atomic<int> fit[kMaxDevices][kMaxSplitLog2 + 1];  // clusters at once, + 1
   *split = 1;
   if (tiles * 2 > rx_internal::sm_count() || key_tiles < 2 * kMinPart) return RX_OK;
-  rx_status st = ensure_smem(done, extend8_split_kernel<D>, Tile8<D>::BYTES);
+  rx_status st = ensure_smem(done, kernel, Tile8<D>::BYTES);
   if (st != RX_OK) return st;
   int dev = -1;
   cudaGetDevice(&dev);
@@ -779,7 +791,7 @@ rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
     if (key_tiles >> lg < kMinPart) continue;
     int n = fit[dev][lg].load(std::memory_order_relaxed);
     if (n == 0) {
-      if (lg > 3 && cudaFuncSetAttribute(extend8_split_kernel<D>,
+      if (lg > 3 && cudaFuncSetAttribute(kernel,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed,
                                          1) != cudaSuccess)
         cudaGetLastError();
@@ -787,7 +799,7 @@ rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
       cudaLaunchAttribute attr[1];
       cluster_config(&cfg, attr, 1, 1 << lg, Tile8<D>::BYTES);
       int c = 0;
-      if (cudaOccupancyMaxActiveClusters(&c, extend8_split_kernel<D>, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&c, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();  // no cluster of this size
         c = 0;
       }
@@ -840,8 +852,8 @@ extern "C" rx_status rx_kv8_extend_attention(
   int split = 1;
   const int bn = D == 128 ? Tile8<128>::BN : Tile8<256>::BN;
   const int64_t key_tiles = (row_stride + bn - 1) / bn;
-  st = D == 128 ? cluster_split<128>(ctas, key_tiles, &split)
-                : cluster_split<256>(ctas, key_tiles, &split);
+  st = D == 128 ? cluster_split<128, false>(ctas, key_tiles, &split)
+                : cluster_split<256, false>(ctas, key_tiles, &split);
   if (st != RX_OK) return st;
   if (split > 1) {
     Maps8 maps;
@@ -934,10 +946,35 @@ extern "C" rx_status rx_kv8_decode_attention(
     if (st == RX_OK) st = make_maps(&maps, pool);
     if (st != RX_OK) return st;
     const unsigned n = unsigned(info->n_work_tc * hkv);
-    if (D == 128)
+    const int bn = D == 128 ? Tile8<128>::BN : Tile8<256>::BN;
+    const int64_t key_tiles = (row_stride + bn - 1) / bn;
+    // Sharing the tiles' keys pays when they outlast the streams beside them by
+    // far (193 requests over 8,098 common keys: 92 us unsplit, 50), not when
+    // the streams fill the time (a chat step of 256: 126 us, 136 split; 32
+    // requests over 4,000 common keys and 1,088 of their own: 52 and 56).
+    // A key tile is about 1.3 us, the plan's keys read once 5.8 TB/s.
+    int split = 1;
+    const float read_us = float(info->distinct_kv_tokens) * float(hkv) *
+                          (2.f * float(D) + 8.f / float(pool->block)) / 5.8e6f;
+    if (1.3f * float(key_tiles) >= 6.f * read_us) {
+      st = D == 128 ? cluster_split<128, true>(n, key_tiles, &split)
+                    : cluster_split<256, true>(n, key_tiles, &split);
+      if (st != RX_OK) return st;
+    }
+    if (split > 1) {
+      cudaLaunchConfig_t tc{};
+      cudaLaunchAttribute ta[1];
+      cluster_config(&tc, ta, n, split, D == 128 ? Tile8<128>::BYTES : Tile8<256>::BYTES);
+      tc.stream = s;
+      if (D == 128)
+        cudaLaunchKernelEx(&tc, decode8_split_kernel<128>, a, maps);
+      else
+        cudaLaunchKernelEx(&tc, decode8_split_kernel<256>, a, maps);
+    } else if (D == 128) {
       decode8_tile_kernel<128><<<n, kTileThreads, Tile8<128>::BYTES, s>>>(a, maps);
-    else
+    } else {
       decode8_tile_kernel<256><<<n, kTileThreads, Tile8<256>::BYTES, s>>>(a, maps);
+    }
     st = rx_internal::launch_status("rx_kv8_decode_attention: tiles");
     if (st != RX_OK) return st;
   }

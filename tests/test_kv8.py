@@ -569,6 +569,11 @@ DECODE = [
     (8, 1, 128, 1, 1, [800 + i for i in range(3)], 800),
     (16, 2, 256, 1, 1, [600 + (i % 3) for i in range(70)], 599),
     (64, 8, 128, 8, 16, [2600 + 3 * i for i in range(24)], 2592),
+    # few tiles over many common keys: clusters share a tile's keys
+    (16, 2, 128, 1, 1, [3000 + i for i in range(30)], 2999),
+    (8, 1, 256, 16, 16, [4100 + (i % 5) for i in range(20)], 4096),
+    (64, 1, 256, 1, 1, [1500], 0),
+    (128, 1, 128, 64, 64, [2500, 1], 0),
 ]
 
 
