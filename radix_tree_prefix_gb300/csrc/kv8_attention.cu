@@ -131,7 +131,7 @@ namespace {
 // one holds the codes (d, d+1) of two adjacent keys, taken as operand rows g
 // and g + 8.
 // Eight warps with three stages each beat six with four by 2 to 10 % over the
-// batches tried (contexts of 8,000 keys in private, d = 128: 155 us against 166
+// batches tried (private contexts of 7,001 to 16,001 keys, d = 128: 155 us against 166
 // at 32 requests, 278 against 288 at 64): a warp's step is a chain of latencies.
 // Steps of 16 keys at d = 128 cost 16 % (180 us), at d = 256 they make room for
 // the third stage.
@@ -279,7 +279,7 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
         ring_g + (st % S) * Cfg::STAGE_BYTES + Cfg::SCALES);
     // (K is converted too: mma.sync on e4m3 operands, with Q in two parts, is
     // slower than f16 with the conversions, 161 us against 155 at 32 private
-    // contexts of 8,000 keys)
+    // contexts of 7,001 to 16,001 keys)
     float x[NR][MT][4];  // m-tile h: keys 16 h + g (+ 8)
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
