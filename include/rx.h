@@ -814,10 +814,11 @@ typedef struct rx_kv8_pool_desc {
  * stand next to one another in d_slots, in slot order, as the cache hands
  * them out: a token whose neighbour before it lies in the same block but not
  * in the slot before its own is skipped, with those that follow on from it,
- * and reported (bit 7, blocks of 2 slots and more).  A NaN is stored as 0 and an infinity as the block's largest
- * code, both reported by rx_device_check (bit 6); the scale is taken from
- * the finite values.  A slot outside [1, num_slots) is skipped and reported
- * (bit 0).  d_k, d_v: device bf16 [T][Hkv][head_dim], 16-byte aligned.
+ * and reported (bit 7, blocks of 2 slots and more).  A NaN is stored as 0 and
+ * an infinity as the block's largest code, both reported by rx_device_check
+ * (bit 6); the scale is taken from the finite values.  A slot outside
+ * [1, num_slots) is skipped and reported (bit 0).  d_k, d_v: device bf16
+ * [T][Hkv][head_dim], 16-byte aligned.
  * Errors: RX_ERR_INVALID (the pool, T < 0, T * num_kv_heads of 2^31 or more,
  * NULL or misaligned inputs); T = 0
  * launches nothing. */
@@ -919,7 +920,8 @@ rx_status rx_host_free(void* p);
  * position outside the table and skipped that entry; bit 5 = rx_kv_copy met
  * a slot outside its pool and skipped that entry; bit 6 = rx_kv8_store met
  * a value that is not finite; bit 7 = rx_kv8_store met the tokens of a
- * block out of slot order and skipped some.  Returns RX_ERR_CUDA if a flag was set or the device reported an error. */
+ * block out of slot order and skipped some.  Returns RX_ERR_CUDA if a flag
+ * was set or the device reported an error. */
 rx_status rx_device_check(int32_t* out_flags);
 
 /* Test hook (host fault injection): the k-th page allocation from now, on

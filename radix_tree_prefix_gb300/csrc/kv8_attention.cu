@@ -192,7 +192,8 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
     }
     const uint32_t dst = ring + uint32_t(st % S) * Cfg::STAGE_BYTES;
     if (KEYS == 32 || lane < KEYS)
-      cp_async_8(dst + Cfg::SCALES + lane * 8, sbase + ((sl < 0 ? 0 : sl) >> a.block_log2), sl >= 0);
+      cp_async_8(dst + Cfg::SCALES + lane * 8, sbase + ((sl < 0 ? 0 : sl) >> a.block_log2),
+                 sl >= 0);
 #pragma unroll
     for (int i = 0; i < KEYS / RPI; ++i) {
       const int row = i * RPI + lane / LPR;

@@ -382,7 +382,8 @@ rx_status check_kv8_pool(const rx_kv8_pool_desc* pool, int32_t layer) {
   // the attention kernels address pool rows with 32-bit TMA coordinates
   if (pool->num_slots > INT32_MAX ||
       int64_t(pool->num_layers) * pool->num_kv_heads > INT32_MAX / pool->num_slots)
-    return set_error(RX_ERR_INVALID, "8-bit pool has 2^31 rows (layers x KV heads x slots) or more");
+    return set_error(RX_ERR_INVALID,
+                     "8-bit pool has 2^31 rows (layers x KV heads x slots) or more");
   if (layer < 0 || layer >= pool->num_layers)
     return set_error(RX_ERR_INVALID, "layer out of range");
   if (!aligned(pool->k_codes, 16) || !aligned(pool->v_codes, 16) || !aligned(pool->scales, 8))

@@ -331,11 +331,24 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     parts = max(1, min(cluster_size(), all / kMinPart));
     // (every CTA of the cluster decides alike)
     if (parts == 1 && rank > 0) return;
-    const int first = int(int64_t(all) * rank / parts), last = int(int64_t(all) * (rank + 1) / parts);
+    const int first = int(int64_t(all) * rank / parts);
+    const int last = int(int64_t(all) * (rank + 1) / parts);
     if (rank < parts) t.key_end = min(t.key_end, t.key_begin + last * BN);
     t.key_begin = rank < parts ? t.key_begin + first * BN : t.key_end;  // (no part: no keys)
   }
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
+  if (DECODE && parts == 1 && n_tiles <= 0) {
+    // keys that a later step of the plan brings: empty partial rows
+    for (int idx = tid; idx < t.n_rows * (D / 4); idx += kTileThreads) {
+      const int col = idx % (D / 4) * 4;
+      int64_t q_row, out_row;
+      int lim;
+      row_info8<DECODE>(a, t, kvh, idx / (D / 4), q_row, out_row, lim);
+      *reinterpret_cast<float4*>(a.ws_o + out_row * D + col) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (col == 0) a.ws_lse[out_row] = -INFINITY;
+    }
+    return;
+  }
   // ---- Q: thread (wg, i) reads half of query row i
   const int wg = warp >> 2;
   const int i = (warp & 3) * 32 + lane;
@@ -390,227 +403,228 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
   // launched with.
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-  if (warp == 14) {
-    // ------------------------------------------------------------ K loader
-    constexpr int LPR = D / 16;   // 16-byte pieces per row
-    constexpr int RPI = 32 / LPR;  // rows a gather instruction copies
-    constexpr int rows = BN;
-    constexpr int SPL = BN / 32;
-    const uint8_t* src0 = a.kc + int64_t(kvh) * a.head_stride + (lane % LPR) * 16;
-    const int64_t row0 = a.tma_row_base + int64_t(kvh) * a.num_slots;
-    // lane l holds the slots of keys l, l + 32, .. of a tile; the next tile's
-    // are on their way while one is loaded
-    int32_t cur[SPL], nxt[SPL];
-    auto load_slots = [&](int k0, int32_t (&dst)[SPL]) {
-#pragma unroll
-      for (int e = 0; e < SPL; ++e)
-        dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(t.trow + k0 + lane + 32 * e) : -1;
-    };
-    load_slots(t.key_begin, nxt);
-    // It passes on the scales too: K's, and vref.  The next tile's are read a
-    // tile ahead.
-    const float2* sb = a.scales + int64_t(kvh) * a.scale_stride;
-    float2 sc[SPL], sn[SPL];
-    auto load_scales = [&](int k0, const int32_t (&s)[SPL], float2 (&dst)[SPL]) {
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) {
-        // (a bad slot is reported and read as slot 0 when its tile is loaded)
-        const uint32_t at = uint32_t(s[e]) < uint32_t(a.num_slots) ? uint32_t(s[e]) : 0u;
-        dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(sb + (at >> a.block_log2))
-                                                : make_float2(0.f, 0.f);
-      }
-    };
-    float vref = 0.f;
-    load_scales(t.key_begin, nxt, sn);
-    uint32_t pend = 0;  // barrier of gathered rows whose arrival is still to be signalled
-    int j = 0;
-#pragma unroll 1
-    for (; j < n_tiles; ++j) {
-      const int k0 = t.key_begin + j * rows;
-      bool bad = false, whole = true;
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) {
-        cur[e] = nxt[e];
-        if (k0 + lane + 32 * e < t.key_end && (cur[e] < 0 || cur[e] >= a.num_slots)) {
-          bad = true;
-          cur[e] = 0;
-        }
-      }
-      load_slots(k0 + rows, nxt);
-      if (bad) atomicOr(&g_kv8_att_error, 1);
-      const int32_t first = __shfl_sync(0xffffffffu, cur[0], 0);
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) whole = whole && cur[e] == first + lane + 32 * e;
-      whole = __all_sync(0xffffffffu, whole && first >= 0);
-      // stage j % NB is free once S_{j-NB} completed
-      static_assert(NB == NS, "a K stage is freed by the S of its index");
-      if (j >= NB && !__all_sync(0xffffffffu, wait(BAR_S(j), j / NB - 1, abort_flag))) break;
-      const uint32_t full = BAR_KF(j), dst = base + Lo::K0 + uint32_t((j % NB) * Lo::K_BYTES);
-      uint32_t done = 0;  // barrier of this stage, if it needs a signal later
-      if (whole) {
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(full, uint32_t(rows * D));
-#pragma unroll
-          for (int cb = 0; cb < D / 128; ++cb)
-            tc::tma_load_2d(dst + uint32_t(cb * rows * 128), &maps.k, cb * 128, int(row0 + first), full);
-        }
-      } else {
-        // groups of 16 keys: a box load where their slots are consecutive;
-        // the rest is gathered (past the key range a slot is -1, its row zeros)
-        uint32_t run = 0;
-        int32_t gfirst = 0;  // lane g: first slot of group g
-#pragma unroll
+    if (warp == 14) {
+      // ------------------------------------------------------------ K loader
+      constexpr int LPR = D / 16;   // 16-byte pieces per row
+      constexpr int RPI = 32 / LPR;  // rows a gather instruction copies
+      constexpr int rows = BN;
+      constexpr int SPL = BN / 32;
+      const uint8_t* src0 = a.kc + int64_t(kvh) * a.head_stride + (lane % LPR) * 16;
+      const int64_t row0 = a.tma_row_base + int64_t(kvh) * a.num_slots;
+      // lane l holds the slots of keys l, l + 32, .. of a tile; the next tile's
+      // are on their way while one is loaded
+      int32_t cur[SPL], nxt[SPL];
+      auto load_slots = [&](int k0, int32_t (&dst)[SPL]) {
+  #pragma unroll
+        for (int e = 0; e < SPL; ++e)
+          dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(t.trow + k0 + lane + 32 * e) : -1;
+      };
+      load_slots(t.key_begin, nxt);
+      // It passes on the scales too: K's, and vref.  The next tile's are read a
+      // tile ahead.
+      const float2* sb = a.scales + int64_t(kvh) * a.scale_stride;
+      float2 sc[SPL], sn[SPL];
+      auto load_scales = [&](int k0, const int32_t (&s)[SPL], float2 (&dst)[SPL]) {
+  #pragma unroll
         for (int e = 0; e < SPL; ++e) {
-          const int32_t f = __shfl_sync(0xffffffffu, cur[e], lane & 16);
-          const uint32_t m = __ballot_sync(0xffffffffu, f >= 0 && cur[e] == f + (lane & 15));
-          if ((m & 0xffffu) == 0xffffu) run |= 1u << (2 * e);
-          if (m >> 16 == 0xffffu) run |= 2u << (2 * e);
-          const int32_t g = __shfl_sync(0xffffffffu, cur[e], (lane & 1) << 4);
-          if ((lane >> 1) == e) gfirst = g;
+          // (a bad slot is reported and read as slot 0 when its tile is loaded)
+          const uint32_t at = uint32_t(s[e]) < uint32_t(a.num_slots) ? uint32_t(s[e]) : 0u;
+          dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(sb + (at >> a.block_log2))
+                                                  : make_float2(0.f, 0.f);
         }
-        const bool all = __popc(run) * 16 == rows;
-        if (lane == 0 && run) {
-          const uint32_t bytes = uint32_t(__popc(run)) * 16u * D;
-          if (all)
-            tc::mbar_arrive_expect_tx(full, bytes);
-          else
-            mbar_expect_tx(full, bytes);
-        }
-        __syncwarp();
-        if (lane < 8 && ((run >> lane) & 1u)) {
-#pragma unroll 1
-          for (int cb = 0; cb < D / 128; ++cb)
-            tc::tma_load_2d(dst + uint32_t(cb * rows * 128 + lane * 16 * 128), &maps.k16, cb * 128,
-                            int(row0 + gfirst), full);
-        }
-        if (!all) {
-#pragma unroll 1
-          for (int e = 0; e < rows / 32; ++e) {
-            int32_t ce = cur[0];
-#pragma unroll
-            for (int u = 1; u < SPL; ++u)
-              if (e == u) ce = cur[u];
-#pragma unroll 4
-            for (int k = 0; k < 32; k += RPI) {
-              const int row = k + lane / LPR;
-              const int32_t sl = __shfl_sync(0xffffffffu, ce, row);
-              if (!((run >> (2 * e + (row >> 4))) & 1u))
-                rxk::cp_async_16(swz(dst, rows, 32 * e + row, lane % LPR),
-                                 src0 + int64_t(sl < 0 ? 0 : sl) * D, sl >= 0);
-            }
+      };
+      float vref = 0.f;
+      load_scales(t.key_begin, nxt, sn);
+      uint32_t pend = 0;  // barrier of gathered rows whose arrival is still to be signalled
+      int j = 0;
+  #pragma unroll 1
+      for (; j < n_tiles; ++j) {
+        const int k0 = t.key_begin + j * rows;
+        bool bad = false, whole = true;
+  #pragma unroll
+        for (int e = 0; e < SPL; ++e) {
+          cur[e] = nxt[e];
+          if (k0 + lane + 32 * e < t.key_end && (cur[e] < 0 || cur[e] >= a.num_slots)) {
+            bad = true;
+            cur[e] = 0;
           }
-          rxk::cp_async_commit();
-          done = full;
         }
+        load_slots(k0 + rows, nxt);
+        if (bad) atomicOr(&g_kv8_att_error, 1);
+        const int32_t first = __shfl_sync(0xffffffffu, cur[0], 0);
+  #pragma unroll
+        for (int e = 0; e < SPL; ++e) whole = whole && cur[e] == first + lane + 32 * e;
+        whole = __all_sync(0xffffffffu, whole && first >= 0);
+        // stage j % NB is free once S_{j-NB} completed
+        static_assert(NB == NS, "a K stage is freed by the S of its index");
+        if (j >= NB && !__all_sync(0xffffffffu, wait(BAR_S(j), j / NB - 1, abort_flag))) break;
+        const uint32_t full = BAR_KF(j), dst = base + Lo::K0 + uint32_t((j % NB) * Lo::K_BYTES);
+        uint32_t done = 0;  // barrier of this stage, if it needs a signal later
+        if (whole) {
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(full, uint32_t(rows * D));
+  #pragma unroll
+            for (int cb = 0; cb < D / 128; ++cb)
+              tc::tma_load_2d(dst + uint32_t(cb * rows * 128), &maps.k, cb * 128,
+                              int(row0 + first), full);
+          }
+        } else {
+          // groups of 16 keys: a box load where their slots are consecutive;
+          // the rest is gathered (past the key range a slot is -1, its row zeros)
+          uint32_t run = 0;
+          int32_t gfirst = 0;  // lane g: first slot of group g
+  #pragma unroll
+          for (int e = 0; e < SPL; ++e) {
+            const int32_t f = __shfl_sync(0xffffffffu, cur[e], lane & 16);
+            const uint32_t m = __ballot_sync(0xffffffffu, f >= 0 && cur[e] == f + (lane & 15));
+            if ((m & 0xffffu) == 0xffffu) run |= 1u << (2 * e);
+            if (m >> 16 == 0xffffu) run |= 2u << (2 * e);
+            const int32_t g = __shfl_sync(0xffffffffu, cur[e], (lane & 1) << 4);
+            if ((lane >> 1) == e) gfirst = g;
+          }
+          const bool all = __popc(run) * 16 == rows;
+          if (lane == 0 && run) {
+            const uint32_t bytes = uint32_t(__popc(run)) * 16u * D;
+            if (all)
+              tc::mbar_arrive_expect_tx(full, bytes);
+            else
+              mbar_expect_tx(full, bytes);
+          }
+          __syncwarp();
+          if (lane < 8 && ((run >> lane) & 1u)) {
+  #pragma unroll 1
+            for (int cb = 0; cb < D / 128; ++cb)
+              tc::tma_load_2d(dst + uint32_t(cb * rows * 128 + lane * 16 * 128), &maps.k16,
+                              cb * 128, int(row0 + gfirst), full);
+          }
+          if (!all) {
+  #pragma unroll 1
+            for (int e = 0; e < rows / 32; ++e) {
+              int32_t ce = cur[0];
+  #pragma unroll
+              for (int u = 1; u < SPL; ++u)
+                if (e == u) ce = cur[u];
+  #pragma unroll 4
+              for (int k = 0; k < 32; k += RPI) {
+                const int row = k + lane / LPR;
+                const int32_t sl = __shfl_sync(0xffffffffu, ce, row);
+                if (!((run >> (2 * e + (row >> 4))) & 1u))
+                  rxk::cp_async_16(swz(dst, rows, 32 * e + row, lane % LPR),
+                                   src0 + int64_t(sl < 0 ? 0 : sl) * D, sl >= 0);
+              }
+            }
+            rxk::cp_async_commit();
+            done = full;
+          }
+        }
+        // a gathered stage is signalled once the next one's loads are on their
+        // way, so two stages' round trips overlap
+        if (pend) {
+          if (done)
+            rxk::cp_async_wait<1>();
+          else
+            rxk::cp_async_wait<0>();
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(pend);
+        }
+        pend = done;
+        // S_{j-NB} has completed, so the softmax of tile j - NB - NS is done, and
+        // with it every read of the ring's entry
+        static_assert(SR > NB + NS, "scale ring");
+  #pragma unroll
+        for (int e = 0; e < SPL; ++e) sc[e] = sn[e];
+        load_scales(k0 + rows, nxt, sn);
+        float vm = 0.f;
+  #pragma unroll
+        for (int e = 0; e < SPL; ++e) {
+          vm = fmaxf(vm, sc[e].y);
+          ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x;
+        }
+        // (positive floats compare as integers)
+        vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+        if (vm > vref) vref = 4.f * vm;
+        if (lane == 0) vref_ring[j % SR] = vref;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(BAR_KF(j));
       }
-      // a gathered stage is signalled once the next one's loads are on their
-      // way, so two stages' round trips overlap
+      rxk::cp_async_wait<0>();
       if (pend) {
-        if (done)
-          rxk::cp_async_wait<1>();
-        else
-          rxk::cp_async_wait<0>();
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(pend);
       }
-      pend = done;
-      // S_{j-NB} has completed, so the softmax of tile j - NB - NS is done, and
-      // with it every read of the ring's entry
-      static_assert(SR > NB + NS, "scale ring");
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) sc[e] = sn[e];
-      load_scales(k0 + rows, nxt, sn);
-      float vm = 0.f;
-#pragma unroll
-      for (int e = 0; e < SPL; ++e) {
-        vm = fmaxf(vm, sc[e].y);
-        ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x;
+      // No copy is in flight when the CTA gives up its shared memory: every box
+      // load has been consumed, unless a wait gave up, and then the stages' last
+      // phases get one more bounded wait.
+      if (lane == 0 && *abort_flag) {
+        int drain_abort = 0;
+        for (int e = j > NB ? j - NB : 0; e < j; ++e) wait(BAR_KF(e), e / NB, &drain_abort);
       }
-      // (positive floats compare as integers)
-      vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
-      if (vm > vref) vref = 4.f * vm;
-      if (lane == 0) vref_ring[j % SR] = vref;
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(BAR_KF(j));
-    }
-    rxk::cp_async_wait<0>();
-    if (pend) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(pend);
-    }
-    // No copy is in flight when the CTA gives up its shared memory: every box
-    // load has been consumed, unless a wait gave up, and then the stages' last
-    // phases get one more bounded wait.
-    if (lane == 0 && *abort_flag) {
-      int drain_abort = 0;
-      for (int e = j > NB ? j - NB : 0; e < j; ++e) wait(BAR_KF(e), e / NB, &drain_abort);
-    }
-    __syncwarp();
-  } else if (warp < 14) {
-    // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      // shared-memory descriptors: 128-byte swizzle, 1024 bytes between
-      // 8-row groups, version 1
-      constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
-      static_assert(Lo::XCH < (1 << 18), "descriptor address field");
-      if (warp == 12) {
-        // e4m3 A and B (type 0), fp32 accumulator, both K-major
-        constexpr uint32_t idesc =
-            (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
-        const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
-        const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
-        const bool ok = wait(BAR_Q, 0, abort_flag);
-#pragma unroll 1
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          // buffer j % NS is free once P V_{j-NS} has read its P
-          if (j >= NS && !wait(BAR_PF(j), j / NS - 1, abort_flag)) break;
-          if (!wait(BAR_KF(j), j / NB, abort_flag)) break;
-          tc::tc_fence_after();
-          const uint32_t k_lo = k_lo0 + uint32_t(j % NB) * (uint32_t(Lo::K_BYTES) >> 4);
-          const uint32_t d_s = tmem + uint32_t((j % NS) * BN);
-          // Q's two parts by D / 128 blocks of 128 columns, 4 steps each
-#pragma unroll 1
-          for (int blk = 0; blk < 2 * (D / 128); ++blk) {
-            const uint32_t q_at = q_lo + uint32_t(blk) * uint32_t(BM * 128 / 16);
-            const uint32_t k_at = k_lo + uint32_t(blk % (D / 128)) * uint32_t(BN * 128 / 16);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma8_ss(d_s, q_at + uint32_t(ks * 2), k_at + uint32_t(ks * 2), DHI, idesc,
-                      (blk | ks) ? 1u : 0u);
+    } else if (warp < 14) {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        // shared-memory descriptors: 128-byte swizzle, 1024 bytes between
+        // 8-row groups, version 1
+        constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
+        static_assert(Lo::XCH < (1 << 18), "descriptor address field");
+        if (warp == 12) {
+          // e4m3 A and B (type 0), fp32 accumulator, both K-major
+          constexpr uint32_t idesc =
+              (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+          const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
+          const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
+          const bool ok = wait(BAR_Q, 0, abort_flag);
+  #pragma unroll 1
+          for (int j = 0; ok && j < n_tiles; ++j) {
+            // buffer j % NS is free once P V_{j-NS} has read its P
+            if (j >= NS && !wait(BAR_PF(j), j / NS - 1, abort_flag)) break;
+            if (!wait(BAR_KF(j), j / NB, abort_flag)) break;
+            tc::tc_fence_after();
+            const uint32_t k_lo = k_lo0 + uint32_t(j % NB) * (uint32_t(Lo::K_BYTES) >> 4);
+            const uint32_t d_s = tmem + uint32_t((j % NS) * BN);
+            // Q's two parts by D / 128 blocks of 128 columns, 4 steps each
+  #pragma unroll 1
+            for (int blk = 0; blk < 2 * (D / 128); ++blk) {
+              const uint32_t q_at = q_lo + uint32_t(blk) * uint32_t(BM * 128 / 16);
+              const uint32_t k_at = k_lo + uint32_t(blk % (D / 128)) * uint32_t(BN * 128 / 16);
+  #pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma8_ss(d_s, q_at + uint32_t(ks * 2), k_at + uint32_t(ks * 2), DHI, idesc,
+                        (blk | ks) ? 1u : 0u);
+            }
+            tc::mma_commit(BAR_S(j));   // also frees the K stage
+            tc::mbar_arrive(BAR_S(j));  // (passes the scales on, seen through KF)
           }
-          tc::mma_commit(BAR_S(j));   // also frees the K stage
-          tc::mbar_arrive(BAR_S(j));  // (passes the scales on, seen through KF)
+        } else {
+          // f16 A (TMEM) and B (shared, MN-major), fp32 accumulator
+          constexpr uint32_t idesc =
+              (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+          const uint32_t v_lo0 =
+              (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BN * 128 / 16) << 16);
+  #pragma unroll 1
+          for (int j = 0; j < n_tiles; ++j) {
+            if (!wait(BAR_VF(j), j / NV, abort_flag)) break;
+            if (!wait(BAR_P(j), j / NS, abort_flag)) break;
+            tc::tc_fence_after();
+            const uint32_t v_lo = v_lo0 + uint32_t(j % NV) * (uint32_t(Lo::V_BYTES) >> 4);
+            const uint32_t p_t = tmem + uint32_t((j % NS) * BN);
+  #pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+              mma16_ts(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
+                       v_lo + uint32_t(ks * 2048 / 16), DHI, idesc, (j > 0 || ks > 0) ? 1u : 0u);
+            tc::mma_commit(BAR_O(j));   // also frees the V stage
+            tc::mma_commit(BAR_PF(j));  // S buffer j % NS may take S_{j+NS}
+          }
         }
-      } else {
-        // f16 A (TMEM) and B (shared, MN-major), fp32 accumulator
-        constexpr uint32_t idesc =
-            (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(BM >> 4) << 24);
-        const uint32_t v_lo0 =
-            (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BN * 128 / 16) << 16);
-#pragma unroll 1
-        for (int j = 0; j < n_tiles; ++j) {
-          if (!wait(BAR_VF(j), j / NV, abort_flag)) break;
-          if (!wait(BAR_P(j), j / NS, abort_flag)) break;
-          tc::tc_fence_after();
-          const uint32_t v_lo = v_lo0 + uint32_t(j % NV) * (uint32_t(Lo::V_BYTES) >> 4);
-          const uint32_t p_t = tmem + uint32_t((j % NS) * BN);
-#pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks)
-            mma16_ts(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
-                     v_lo + uint32_t(ks * 2048 / 16), DHI, idesc, (j > 0 || ks > 0) ? 1u : 0u);
-          tc::mma_commit(BAR_O(j));   // also frees the V stage
-          tc::mma_commit(BAR_PF(j));  // S buffer j % NS may take S_{j+NS}
-        }
+        // drained once both threads' products completed, whatever the abort flag
+        tc::mma_commit(BAR_FIN);
+        int drain_abort = 0;
+        wait(BAR_FIN, 0, &drain_abort);
       }
-      // drained once both threads' products completed, whatever the abort flag
-      tc::mma_commit(BAR_FIN);
-      int drain_abort = 0;
-      wait(BAR_FIN, 0, &drain_abort);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n");
     // ------------------------------------------------------ V converters

@@ -166,7 +166,8 @@ _SIGS = {
     "rx_event_elapsed_ms": [P, P, P],
     "rx_kv8_store": [POOL8, I32, P, P, P, I64, P],
     "rx_kv8_load": [POOL8, I32, P, P, P, I64, P],
-    "rx_kv8_extend_attention": [POOL8, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P, P],
+    "rx_kv8_extend_attention": [POOL8, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, I32, P,
+                                P],
     "rx_kv8_decode_attention": [POOL8, I32, P, I32, P, I64, P, P, I32, I32, F32, P, I32, P, P, SZ,
                                 P],
     "rx_kv8_extend_batches": [POOL8, I32, I32, P, I32, F32, P, P],

@@ -139,7 +139,8 @@ X8 = (1 << 24) + 8
 
 @pytest.mark.parametrize("call,bad", [
     (c, b) for c in ("store", "load") for b in (
-        dict(T=-1), dict(T=1 << 30), dict(slots=None), dict(k=None), dict(v=None), dict(k=X8), dict(v=X8))] + [
+        dict(T=-1), dict(T=1 << 30), dict(slots=None), dict(k=None), dict(v=None), dict(k=X8),
+        dict(v=X8))] + [
     ("extend", b) for b in (
         dict(hq=3), dict(hq=0), dict(hq=-2), dict(R=-1), dict(nt=-1), dict(nt=1 << 40),
         dict(q=None), dict(table=None), dict(rows=None), dict(prefix=None), dict(qo=None),

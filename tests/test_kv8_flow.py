@@ -318,6 +318,26 @@ def test_steps_of_one_plan_match_64_bits(Hq, H, d, block, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d,G", [(64, 1, 128, 64), (16, 1, 256, 16), (32, 2, 256, 16),
+                                      (8, 2, 128, 4), (4, 1, 256, 4)])
+def test_items_whose_keys_come_at_later_steps(Hq, H, d, G):
+    """A plan of 700 steps from a short context: chunks of the growing tail
+    that no step has reached yet leave empty partial rows (tiles where the
+    group is large, streams where it is not)."""
+    torch = pytest.importorskip("torch")
+    assert Hq == H * G
+    steps, base = 700, [1, 100]
+    c = Case(torch, Hq, H, d, 1, [x + steps - 1 for x in base], 78)
+    q = c.queries(len(base))
+    qn = q.double().cpu().numpy()
+    for t in (0, 1, 300, steps - 1):
+        o, lse = _decode(c, q, depth=[x - 1 for x in base], bf16=False, n_steps=steps, step=t,
+                         ctx=base)
+        for b, x in enumerate(base):
+            c.compare(o[b:b + 1], lse[b:b + 1], c.reference(qn[b:b + 1], b, [x + t]), False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Hq,H,d,block", [(32, 8, 128, 1), (16, 4, 256, 1)])
 def test_drafts_of_a_tree_match_64_bits(Hq, H, d, block):
     """The rows of rx_verify_rows as a decode batch: each draft sees the
