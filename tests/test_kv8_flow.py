@@ -251,13 +251,14 @@ def test_decode_on_streams_and_in_graphs(i):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("d,block", [(128, 1), (256, 16), (128, 64)])
-def test_store_extend_and_load_in_a_graph(d, block):
+@pytest.mark.parametrize("d,block,Hq,T", [(128, 1, 16, 200), (256, 16, 16, 200),
+                                          (128, 64, 16, 200), (128, 1, 4, 1000),
+                                          (256, 8, 4, 700)])
+def test_store_extend_and_load_in_a_graph(d, block, Hq, T):
     """A captured prefill (store, extend over it, load) replayed with other
-    rows equals the eager calls."""
+    rows equals the eager calls (the last two: over clusters)."""
     torch = pytest.importorskip("torch")
-    H, Hq, T = 4, 16, 200
-    N = 512
+    H, N = 4, 1088
     slots = torch.arange(64, 64 + T, dtype=torch.int32, device="cuda")
     g = torch.Generator(device="cuda").manual_seed(1)
 
