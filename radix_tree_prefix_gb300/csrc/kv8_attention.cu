@@ -82,6 +82,7 @@ struct Args8 {
   int step;
   float* ws_o;
   float* ws_lse;
+  bool beside_tiles;  // the streams run beside tiles
   int32_t* counter;  // next unit of the small items, NULL: unit = warp index
 };
 
@@ -451,13 +452,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // left.  With tile items in the plan the kernel is launched after theirs and
 // starts beside it, on the SMs that the tiles leave free and as they finish;
 // it reads nothing that the tiles write, and ends only after they did, so
-// that the merge behind it sees both.  (The other order, streams first on half
+// that the merge behind it sees both.  Without tiles it may be chained to a
+// step's store, and waits for that first.  (The other order, streams first on half
 // of the SMs or on those that the tiles leave, is slower: a chat step of 256
 // 139 us against 129, 64 requests over a document of 32,768 keys 161 against 122.)
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 1) stream8_kernel(const __grid_constant__ Args8 a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
+  if (!a.beside_tiles) rxk::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = rxk::smem_addr(smem_raw);
   const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
@@ -554,6 +557,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge8_kernel(
   const int p0 = active ? __ldg(indptr + b) : 0;
   const int n = active ? __ldg(indptr + b + 1) - p0 : 0;
   int64_t e = lane < n ? int64_t(__ldg(parts + p0 + lane)) * hq + h : 0;  // of part `lane`
+  rxk::griddep_launch_dependents();
   rxk::griddep_wait();
   const float4* o4 = reinterpret_cast<const float4*>(ws_o);
   float m = lane < n ? __ldcg(ws_lse + e) : -INFINITY;
@@ -883,12 +887,18 @@ extern "C" rx_status rx_kv8_extend_attention(
   return rx_internal::launch_status("rx_kv8_extend_attention");
 }
 
-extern "C" rx_status rx_kv8_decode_attention(
+namespace {
+
+// rx_kv8_decode_attention.  step_counter: a counter of the call's own that is
+// zero already (NULL: the one behind the workspace's partials, reset here);
+// chained: the launch before is the step's store, of which the streams need not
+// wait for the end to be launched.
+rx_status decode8(
     const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
     const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
     const rx_decode_plan_info* info, int32_t B, int32_t step, float scale, void* d_out,
     int32_t out_type, float* d_lse, void* d_workspace, size_t workspace_bytes,
-    rx_stream_t stream) {
+    rx_stream_t stream, int32_t* step_counter, bool chained) {
   Args8 a{};
   rx_status st = common_args("rx_kv8_decode_attention", pool, layer, d_q, num_q_heads,
                              d_req_to_token, row_stride, scale, out_type, &a);
@@ -928,8 +938,8 @@ extern "C" rx_status rx_kv8_decode_attention(
     // more units than warps, or warps that start late (beside the tiles):
     // units are taken from a counter, heaviest first
     ctas = std::min(ctas, sms);
-    a.counter = counter;
-    if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
+    a.counter = step_counter ? step_counter : counter;
+    if (!step_counter && cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
       return rx_internal::launch_status("rx_kv8_decode_attention: counter reset");
   }
   cudaLaunchConfig_t cfg{};
@@ -987,7 +997,8 @@ extern "C" rx_status rx_kv8_decode_attention(
     cfg.gridDim = dim3(unsigned(ctas));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = D == 128 ? Pipe8<128>::BYTES : Pipe8<256>::BYTES;
-    cfg.numAttrs = info->n_work_tc > 0 ? 1 : 0;  // beside the tiles only
+    a.beside_tiles = info->n_work_tc > 0;
+    cfg.numAttrs = a.beside_tiles || chained ? 1 : 0;
     if (D == 128)
       cudaLaunchKernelEx(&cfg, stream8_kernel<128>, a);
     else
@@ -1013,6 +1024,19 @@ extern "C" rx_status rx_kv8_decode_attention(
   cudaLaunchKernelEx(&cfg, merge, indptr, parts, wo, wl, int(num_q_heads), int(B), d_out,
                      int(a.out_bf16), d_lse);
   return rx_internal::launch_status("rx_kv8_decode_attention: merge");
+}
+
+}  // namespace
+
+extern "C" rx_status rx_kv8_decode_attention(
+    const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
+    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
+    const rx_decode_plan_info* info, int32_t B, int32_t step, float scale, void* d_out,
+    int32_t out_type, float* d_lse, void* d_workspace, size_t workspace_bytes,
+    rx_stream_t stream) {
+  return decode8(pool, layer, d_q, num_q_heads, d_req_to_token, row_stride, d_plan, info, B, step,
+                 scale, d_out, out_type, d_lse, d_workspace, workspace_bytes, stream, nullptr,
+                 false);
 }
 
 extern "C" rx_status rx_kv8_extend_batches(const rx_kv8_pool_desc* pool, int32_t layer,
@@ -1059,13 +1083,36 @@ extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t l
   if (r != RX_OK) return r;
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_steps: Hq % Hkv != 0");
+  // Every step has its own unit counter, reset together behind the largest
+  // step's partials if the workspace has room, and its launches are chained:
+  // from the second step on the store is launched while the merge before it
+  // runs, and the streams, where no tiles come first, while the store does.  Each
+  // waits on the device for the end of the kernel before it, which did so too.
+  int64_t region = 0;
+  bool own_counters = n_steps > 0 && B > 0;
+  for (int32_t i = 0; own_counters && i < n_steps; ++i) {
+    const rx_decode_plan_info* inf = steps[i].info;
+    own_counters = inf && inf->n_parts >= 0;
+    if (!own_counters) break;
+    const int64_t o = inf->n_parts * num_q_heads * int64_t(pool->head_dim) * 4;
+    const int64_t l = inf->n_parts * num_q_heads * 4;
+    region = std::max(region, (o + 255) / 256 * 256 + (l + 255) / 256 * 256);
+  }
+  own_counters = own_counters && d_workspace && aligned16(d_workspace) &&
+                 int64_t(workspace_bytes) >= region + 4 * int64_t(n_steps);
+  int32_t* counters =
+      own_counters ? reinterpret_cast<int32_t*>(static_cast<char*>(d_workspace) + region) : nullptr;
+  if (own_counters && cudaMemsetAsync(counters, 0, 4 * size_t(n_steps),
+                                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return rx_internal::launch_status("rx_kv8_decode_steps: counters reset");
   for (int32_t i = 0; i < n_steps; ++i) {
     const rx_decode_step& t = steps[i];
-    r = rx_kv8_store(pool, layer, t.d_slots, t.d_k, t.d_v, B, stream);
+    r = rx_internal::kv8_store(pool, layer, t.d_slots, t.d_k, t.d_v, B, stream,
+                               i > 0 && own_counters);
     if (r != RX_OK) return r;
-    r = rx_kv8_decode_attention(pool, layer, t.d_q, num_q_heads, d_req_to_token, row_stride,
-                                t.d_plan, t.info, B, t.step, scale, t.d_out, RX_OUT_F32, t.d_lse,
-                                d_workspace, workspace_bytes, stream);
+    r = decode8(pool, layer, t.d_q, num_q_heads, d_req_to_token, row_stride, t.d_plan, t.info, B,
+                t.step, scale, t.d_out, RX_OUT_F32, t.d_lse, d_workspace, workspace_bytes, stream,
+                own_counters ? counters + i : nullptr, i > 0 && own_counters);
     if (r != RX_OK) return r;
   }
   return RX_OK;

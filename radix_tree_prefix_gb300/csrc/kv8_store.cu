@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "kv8.cuh"
+#include "ptx_util.cuh"
 #include "rx.h"
 #include "rx_internal.h"
 
@@ -101,6 +102,8 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const StoreArgs a)
   const int lane = threadIdx.x % L;
   const int64_t rows = a.T * a.hkv;
   const int64_t base = int64_t(blockIdx.x) * (GROUPS * kRows) + threadIdx.x / L;
+  rxk::griddep_launch_dependents();
+  rxk::griddep_wait();  // (a chained launch: the kernels before read the pool)
   uint4 k[kRows], v[kRows];
   int32_t slot[kRows];
   int h[kRows];
@@ -170,6 +173,8 @@ __global__ void __launch_bounds__(kThreads) store_runs_kernel(const StoreArgs a)
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int blk = 1 << a.block_log2;
   if (tid == 0) count = 0;
+  rxk::griddep_launch_dependents();
+  rxk::griddep_wait();  // (a chained launch: the kernels before read the pool)
   for (int i = tid; i < a.window + blk + 1; i += kThreads) {
     const int64_t t = w0 - 1 + i;
     win[i] = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;  // -1 is in no run
@@ -404,22 +409,27 @@ int32_t kv8_store_error_flags(bool clear) {
 
 }  // namespace rx_internal
 
-extern "C" rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
-                                  const int32_t* d_slots, const void* d_k, const void* d_v,
-                                  int64_t T, rx_stream_t stream) {
+rx_status rx_internal::kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
+                                 const int32_t* d_slots, const void* d_k, const void* d_v,
+                                 int64_t T, rx_stream_t stream, bool chained) {
   StoreArgs a;
   rx_status st = store_args(pool, layer, d_slots, d_k, d_v, T, &a);
   if (st != RX_OK || T == 0) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
   const int D = pool->head_dim;
   const int64_t sms = rx_internal::sm_count();
   if (pool->block == 1) {
     const int64_t per_cta = kThreads / (D / 8) * kRows;
     const int64_t ctas = (T * a.hkv + per_cta - 1) / per_cta;
-    if (D == 128)
-      store_rows_kernel<128><<<unsigned(ctas), kThreads, 0, s>>>(a);
-    else
-      store_rows_kernel<256><<<unsigned(ctas), kThreads, 0, s>>>(a);
+    cfg.gridDim = dim3(unsigned(ctas));
+    cudaLaunchKernelEx(&cfg, D == 128 ? store_rows_kernel<128> : store_rows_kernel<256>, a);
   } else {
     if (a.hkv > 32767)
       return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_store: too many KV heads");
@@ -431,13 +441,16 @@ extern "C" rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
     a.window = int((T + whole - 1) / whole * a.hkv * 2 >= 2 * sms ? whole : groups);
     const int64_t gx = (T + a.window - 1) / a.window;
     if (gx > INT32_MAX) return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_store: T too large");
-    const dim3 grid(unsigned(gx), unsigned(a.hkv * 2));
-    if (D == 128)
-      store_runs_kernel<128><<<grid, kThreads, 0, s>>>(a);
-    else
-      store_runs_kernel<256><<<grid, kThreads, 0, s>>>(a);
+    cfg.gridDim = dim3(unsigned(gx), unsigned(a.hkv * 2));
+    cudaLaunchKernelEx(&cfg, D == 128 ? store_runs_kernel<128> : store_runs_kernel<256>, a);
   }
   return rx_internal::launch_status("rx_kv8_store");
+}
+
+extern "C" rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
+                                  const int32_t* d_slots, const void* d_k, const void* d_v,
+                                  int64_t T, rx_stream_t stream) {
+  return rx_internal::kv8_store(pool, layer, d_slots, d_k, d_v, T, stream, false);
 }
 
 extern "C" rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,

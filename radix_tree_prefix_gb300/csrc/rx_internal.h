@@ -48,6 +48,10 @@ rx_status set_error(rx_status s, const char* msg);
 // Device-side helpers (kv_store.cu).
 rx_status check_pool(const rx_pool_desc* pool, int32_t layer);
 rx_status check_kv8_pool(const rx_kv8_pool_desc* pool, int32_t layer);
+// rx_kv8_store; chained: launched while the kernel before it still runs (it
+// waits on the device before it writes).
+rx_status kv8_store(const rx_kv8_pool_desc* pool, int32_t layer, const int32_t* d_slots,
+                    const void* d_k, const void* d_v, int64_t T, rx_stream_t stream, bool chained);
 rx_status launch_status(const char* what);
 int sm_count();
 // The driver's cuTensorMapEncodeTiled, NULL if it cannot be found.
