@@ -885,8 +885,10 @@ rx_status rx_kv8_extend_batches(const rx_kv8_pool_desc* pool, int32_t layer,
 
 /* rx_decode_steps over an 8-bit pool: per step rx_kv8_store of its B tokens
  * (always a launch of its own), then rx_kv8_decode_attention into its fp32
- * outputs.  At B = 0 nothing is launched.  Stops at the first error; errors
- * as rx_decode_steps. */
+ * outputs.  A block must hold no rows of a shared segment of the plan and of a
+ * request's own tail, as is so when the page size is a multiple of the block.
+ * At B = 0 nothing is launched.  Stops at the first error; errors as
+ * rx_decode_steps. */
 rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t layer,
                               int32_t num_q_heads,
                               const int32_t* d_req_to_token,

@@ -83,6 +83,7 @@ struct Args8 {
   float* ws_o;
   float* ws_lse;
   bool beside_tiles;  // the streams run beside tiles
+  bool chained;       // the launch before is this step's store
   int32_t* counter;  // next unit of the small items, NULL: unit = warp index
 };
 
@@ -460,7 +461,10 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 1) stream8_kernel(const __grid_constant__ Args8 a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  if (!a.beside_tiles) rxk::griddep_wait();
+  if (!a.beside_tiles)
+    rxk::griddep_wait();
+  else if (a.chained)
+    __threadfence();  // the store completed before the tiles let this kernel start
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = rxk::smem_addr(smem_raw);
   const uint32_t off = ((raw + 127u) & ~127u) - raw + uint32_t(warp * Pipe8<D>::WARP_BYTES);
@@ -500,7 +504,7 @@ template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     decode8_tile_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  rxk::griddep_launch_dependents();
+  if (!a.chained) rxk::griddep_launch_dependents();
   const int hkv = a.hq / a.group;
   tile8<D, true>(a, maps, smem_raw, int(blockIdx.x) / hkv, int(blockIdx.x) % hkv);
 }
@@ -510,7 +514,7 @@ template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     decode8_split_kernel(const __grid_constant__ Args8 a, const __grid_constant__ Maps8 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  rxk::griddep_launch_dependents();
+  if (!a.chained) rxk::griddep_launch_dependents();
   const int c = int(blockIdx.x) / cluster_size();
   const int hkv = a.hq / a.group;
   tile8<D, true, true>(a, maps, smem_raw, c / hkv, c % hkv);
@@ -891,8 +895,8 @@ namespace {
 
 // rx_kv8_decode_attention.  step_counter: a counter of the call's own that is
 // zero already (NULL: the one behind the workspace's partials, reset here);
-// chained: the launch before is the step's store, of which the streams need not
-// wait for the end to be launched.
+// chained: the launch before is the step's store, whose end the kernels wait for
+// on the device, where they need it.
 rx_status decode8(
     const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
     const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
@@ -942,6 +946,7 @@ rx_status decode8(
     if (!step_counter && cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
       return rx_internal::launch_status("rx_kv8_decode_attention: counter reset");
   }
+  a.chained = chained;
   cudaLaunchConfig_t cfg{};
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -967,25 +972,23 @@ rx_status decode8(
     int split = 1;
     const float read_us = float(info->distinct_kv_tokens) * float(hkv) *
                           (2.f * float(D) + 8.f / float(pool->block)) / 5.8e6f;
-    if (1.3f * float(key_tiles) >= 6.f * read_us) {
+    if (1.3f * float(key_tiles) >= 10.f * read_us) {
       st = D == 128 ? cluster_split<128, true>(n, key_tiles, &split)
                     : cluster_split<256, true>(n, key_tiles, &split);
       if (st != RX_OK) return st;
     }
-    if (split > 1) {
-      cudaLaunchConfig_t tc{};
-      cudaLaunchAttribute ta[1];
-      cluster_config(&tc, ta, n, split, D == 128 ? Tile8<128>::BYTES : Tile8<256>::BYTES);
-      tc.stream = s;
-      if (D == 128)
-        cudaLaunchKernelEx(&tc, decode8_split_kernel<128>, a, maps);
-      else
-        cudaLaunchKernelEx(&tc, decode8_split_kernel<256>, a, maps);
-    } else if (D == 128) {
-      decode8_tile_kernel<128><<<n, kTileThreads, Tile8<128>::BYTES, s>>>(a, maps);
-    } else {
-      decode8_tile_kernel<256><<<n, kTileThreads, Tile8<256>::BYTES, s>>>(a, maps);
-    }
+    cudaLaunchConfig_t tc{};
+    cudaLaunchAttribute ta[2];
+    cluster_config(&tc, ta, n, split, D == 128 ? Tile8<128>::BYTES : Tile8<256>::BYTES);
+    tc.stream = s;
+    if (split == 1) tc.numAttrs = 0;
+    if (chained) ta[tc.numAttrs++] = attr[0];
+    if (split > 1)
+      cudaLaunchKernelEx(&tc, D == 128 ? decode8_split_kernel<128> : decode8_split_kernel<256>, a,
+                         maps);
+    else
+      cudaLaunchKernelEx(&tc, D == 128 ? decode8_tile_kernel<128> : decode8_tile_kernel<256>, a,
+                         maps);
     st = rx_internal::launch_status("rx_kv8_decode_attention: tiles");
     if (st != RX_OK) return st;
   }
@@ -1086,8 +1089,10 @@ extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t l
   // Every step has its own unit counter, reset together behind the largest
   // step's partials if the workspace has room, and its launches are chained:
   // from the second step on the store is launched while the merge before it
-  // runs, and the streams, where no tiles come first, while the store does.  Each
-  // waits on the device for the end of the kernel before it, which did so too.
+  // runs, and the tiles or streams while the store does.  Each waits on the device
+  // for the end of the kernel before it (which did so too) before it reads what
+  // that writes or writes what that reads; tiles of shared segments so run beside
+  // the end of the step before.
   int64_t region = 0;
   bool own_counters = n_steps > 0 && B > 0;
   for (int32_t i = 0; own_counters && i < n_steps; ++i) {

@@ -89,6 +89,7 @@ struct TileDesc8 {
   int key_begin, key_end, nomask_end, n_rows;
   int gr0, q_base, prefix;
   int member_off, part_base;
+  bool grows;  // its end moves with the step
 };
 
 template <bool DECODE>
@@ -98,7 +99,8 @@ __device__ __forceinline__ TileDesc8 describe8(const Args8& a, int tile) {
     const int32_t* w = a.work + int64_t(a.n_small + tile) * RX_WORK_WORDS;
     t.trow = a.table + int64_t(w[0]) * a.row_stride;
     t.key_begin = w[1];
-    t.key_end = w[7] > 0 ? min(w[2], w[7] + a.step) : w[2];
+    t.grows = w[7] > 0;
+    t.key_end = t.grows ? min(w[2], w[7] + a.step) : w[2];
     t.member_off = w[3];
     t.part_base = w[5];
     t.n_rows = w[6];
@@ -129,6 +131,7 @@ __device__ __forceinline__ TileDesc8 describe8(const Args8& a, int tile) {
     t.key_end = t.prefix + (t.gr0 + t.n_rows - 1) / G + 1;
     t.nomask_end = t.prefix + t.gr0 / G + 1;
     t.member_off = t.part_base = 0;
+    t.grows = false;
   }
   return t;
 }
@@ -337,8 +340,13 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     t.key_begin = rank < parts ? t.key_begin + first * BN : t.key_end;  // (no part: no keys)
   }
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
+  // Chained to a step's store: a segment that grows waits for it, any other
+  // reads what no kernel of the run writes (a block of slots holds no rows of a
+  // shared segment and of a tail), and waits before it writes partial rows.
+  if (DECODE && a.chained && t.grows) rxk::griddep_wait();
   if (DECODE && parts == 1 && n_tiles <= 0) {
     // keys that a later step of the plan brings: empty partial rows
+    if (a.chained) rxk::griddep_wait();
     for (int idx = tid; idx < t.n_rows * (D / 4); idx += kTileThreads) {
       const int col = idx % (D / 4) * 4;
       int64_t q_row, out_row;
@@ -624,6 +632,11 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
         wait(BAR_FIN, 0, &drain_abort);
       }
       __syncwarp();
+    } else if (DECODE && a.chained) {
+      // (warp 15, idle otherwise) the streams beside the tiles start once the
+      // store has completed
+      rxk::griddep_wait();
+      rxk::griddep_launch_dependents();
     }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n");
@@ -897,6 +910,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
       if (lane == 0) tc::mbar_arrive(BAR_P(j));
     }
     // ----------------------------------------------------------- epilogue
+    if (DECODE && a.chained) rxk::griddep_wait();
     const bool fin = ok && n_tiles > 0 && __all_sync(0xffffffffu, wait(BAR_FIN, 0, abort_flag));
     // the row sums go through the parity that the last tile did not use
     const int xp = n_tiles & 1 ? 0 : 1;
@@ -977,6 +991,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
   if constexpr (SPLIT) {
     if (parts > 1) {
       // each CTA of the cluster joins 128 / C rows of all parts
+      if (DECODE && a.chained) rxk::griddep_wait();
       cluster_sync();
       constexpr int HC = D / 2, PITCH = HC * 4 + 16;
       const int per = BM / cluster_size();

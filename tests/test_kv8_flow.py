@@ -503,3 +503,49 @@ def test_binding_refuses_other_types_devices_and_layouts():
     with pytest.raises(ValueError):
         rx.kv8_extend_attention(pool, 0, q, 4, t.float(), i, i, i, i, 1, 1, 0.1, o, l)
     assert not kc.any() and rx.device_check() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,page,block", [("agent", 1, 1), ("agent", 16, 16), ("chat", 16, 8),
+                                             ("wide", 1, 1), ("wide", 16, 4), ("alone", 32, 32)])
+def test_chained_steps_equal_steps_one_by_one(name, page, block, monkeypatch):
+    """rx_kv8_decode_steps overlaps the kernels of consecutive steps: every
+    output of a run of steps has the bits of the steps called one at a time
+    with a wait between them (shared segments in tiles beside private tails,
+    tails in tiles where the group is large, no tiles at all)."""
+    torch = pytest.importorskip("torch")
+    from radix_tree_prefix_gb300.engine import GatherInputs
+    wl = {
+        "agent": lambda: workloads.agent_loop(calls=40, preamble=1500, lo=150, hi=250,
+                                              decode_steps=48),
+        "chat": lambda: workloads.multi_turn_chat(sessions=48, turns=2, system=600, user=60,
+                                                  decode_steps=32, layers=1),
+        "wide": lambda: workloads.agent_loop(calls=6, preamble=300, lo=20, hi=900,
+                                             decode_steps=40, q_heads=64, kv_heads=2),
+        "alone": lambda: workloads.agent_loop(calls=2, preamble=0, lo=30, hi=90,
+                                              decode_steps=40, head_dim=256),
+    }[name]()
+    wl = workloads.with_pages(wl, page) if page > 1 else wl
+    dev = torch.device("cuda:0")
+    vals = workloads.make_values(wl, dev, [0])
+    runs = []
+    steps = rx.decode_steps
+
+    def one_by_one(pool, layer, hq, d_table, recs, B, scale, ws, stream=None):
+        for i in range(len(recs)):
+            steps(pool, layer, hq, d_table, recs[i:i + 1], B, scale, ws, stream)
+            torch.cuda.synchronize()
+    for fn in (one_by_one, steps, steps, steps):
+        monkeypatch.setattr(rx, "decode_steps", fn)
+        got = {}
+        Engine(wl, device=dev, inputs=GatherInputs(wl, vals, [0]), layers=[0], kv8_block=block,
+               on_decode_wave=lambda s, rids, ctx, outs, info: got.__setitem__(
+                   s, tuple(x.clone() for x in outs[0]))).run()
+        torch.cuda.synchronize()
+        assert rx.device_check() == 0
+        runs.append(got)
+    assert runs[0]
+    for got in runs[1:]:
+        assert got.keys() == runs[0].keys()
+        for k in got:
+            assert torch.equal(got[k][0], runs[0][k][0]) and torch.equal(got[k][1], runs[0][k][1])
