@@ -786,7 +786,7 @@ void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned
 // tiles of 3,200 keys: 75 us unsplit, 87).
 constexpr int kMaxSplitLog2 = 4;
 template <int D, bool DECODE>
-rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
+rx_status cluster_split(int64_t tiles, int64_t key_tiles, int64_t max_ctas, int* split) {
   constexpr auto* kernel = DECODE ? decode8_split_kernel<D> : extend8_split_kernel<D>;
   static std::atomic<bool> done[kMaxDevices];
   static std::atomic<int> fit[kMaxDevices][kMaxSplitLog2 + 1];  // clusters at once, + 1
@@ -797,7 +797,7 @@ rx_status cluster_split(int64_t tiles, int64_t key_tiles, int* split) {
   int dev = -1;
   cudaGetDevice(&dev);
   for (int lg = kMaxSplitLog2; lg >= 1; --lg) {
-    if (key_tiles >> lg < kMinPart) continue;
+    if (key_tiles >> lg < kMinPart || tiles << lg > max_ctas) continue;
     int n = fit[dev][lg].load(std::memory_order_relaxed);
     if (n == 0) {
       if (lg > 3 && cudaFuncSetAttribute(kernel,
@@ -861,8 +861,8 @@ extern "C" rx_status rx_kv8_extend_attention(
   int split = 1;
   const int bn = D == 128 ? Tile8<128>::BN : Tile8<256>::BN;
   const int64_t key_tiles = (row_stride + bn - 1) / bn;
-  st = D == 128 ? cluster_split<128, false>(ctas, key_tiles, &split)
-                : cluster_split<256, false>(ctas, key_tiles, &split);
+  st = D == 128 ? cluster_split<128, false>(ctas, key_tiles, INT64_MAX, &split)
+                : cluster_split<256, false>(ctas, key_tiles, INT64_MAX, &split);
   if (st != RX_OK) return st;
   if (split > 1) {
     Maps8 maps;
@@ -963,18 +963,26 @@ rx_status decode8(
     if (st != RX_OK) return st;
     const unsigned n = unsigned(info->n_work_tc * hkv);
     const int bn = D == 128 ? Tile8<128>::BN : Tile8<256>::BN;
-    const int64_t key_tiles = (row_stride + bn - 1) / bn;
-    // Sharing the tiles' keys pays when they outlast the streams beside them by
-    // far (193 requests over 8,098 common keys: 92 us unsplit, 50), not when
-    // the streams fill the time (a chat step of 256: 126 us, 136 split; 32
-    // requests over 4,000 common keys and 1,088 of their own: 52 and 56).
-    // A key tile is about 1.3 us, the plan's keys read once 5.8 TB/s.
+    // Sharing the tiles' keys pays when they outlast the streams beside them: by
+    // far, on all SMs (193 requests over 8,098 common keys: 92 us unsplit, 49),
+    // by less on three eighths, beside the streams (64 over 2,000 and some 460 of
+    // their own, d = 256: 65 and 45, and a step of such a run 49 and 41), and not
+    // when the streams fill the time (a chat step of 256: 126 us, 136 split).
+    // A key tile is about 1.3 us, the plan's keys are read at 5.8 TB/s, and a
+    // tile item has kDecodeKeysPerRow keys per query row at most.
+    const int64_t chunk =
+        std::min(row_stride, std::max<int64_t>(rx_internal::kDecodeMinChunk,
+                                               int64_t(rx_internal::kDecodeKeysPerRow) * B *
+                                                   a.group));
+    const int64_t key_tiles = (chunk + bn - 1) / bn;
     int split = 1;
     const float read_us = float(info->distinct_kv_tokens) * float(hkv) *
                           (2.f * float(D) + 8.f / float(pool->block)) / 5.8e6f;
-    if (1.3f * float(key_tiles) >= 10.f * read_us) {
-      st = D == 128 ? cluster_split<128, true>(n, key_tiles, &split)
-                    : cluster_split<256, true>(n, key_tiles, &split);
+    const float ratio = 1.3f * float(key_tiles) / read_us;
+    if (ratio >= 2.f) {
+      const int64_t max_ctas = ratio >= 6.f ? INT64_MAX : sms * 3 / 8;
+      st = D == 128 ? cluster_split<128, true>(n, key_tiles, max_ctas, &split)
+                    : cluster_split<256, true>(n, key_tiles, max_ctas, &split);
       if (st != RX_OK) return st;
     }
     cudaLaunchConfig_t tc{};
