@@ -549,3 +549,48 @@ def test_chained_steps_equal_steps_one_by_one(name, page, block, monkeypatch):
         assert got.keys() == runs[0].keys()
         for k in got:
             assert torch.equal(got[k][0], runs[0][k][0]) and torch.equal(got[k][1], runs[0][k][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["agent", "wide", "alone"])
+def test_chained_steps_in_a_graph(name, monkeypatch):
+    """A captured run of steps, replayed, gives the eager run's bits (blocks of
+    one slot: storing a token again changes nothing)."""
+    torch = pytest.importorskip("torch")
+    from radix_tree_prefix_gb300.engine import GatherInputs
+    wl = {
+        "agent": lambda: workloads.agent_loop(calls=24, preamble=900, lo=50, hi=150,
+                                              decode_steps=12),
+        "wide": lambda: workloads.agent_loop(calls=4, preamble=300, lo=20, hi=600,
+                                             decode_steps=12, q_heads=64, kv_heads=2),
+        "alone": lambda: workloads.agent_loop(calls=2, preamble=0, lo=30, hi=90,
+                                              decode_steps=12, head_dim=256),
+    }[name]()
+    dev = torch.device("cuda:0")
+    vals = workloads.make_values(wl, dev, [0])
+    steps = rx.decode_steps
+
+    def replayed(*args):
+        steps(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps(*args[:-1], torch.cuda.current_stream())
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        kept.append(graph)
+    runs, kept = [], []
+    for fn in (steps, replayed):
+        monkeypatch.setattr(rx, "decode_steps", fn)
+        got = {}
+        Engine(wl, device=dev, inputs=GatherInputs(wl, vals, [0]), layers=[0], kv8_block=1,
+               on_decode_wave=lambda s, rids, ctx, outs, info: got.__setitem__(
+                   s, tuple(x.clone() for x in outs[0]))).run()
+        torch.cuda.synchronize()
+        assert rx.device_check() == 0
+        runs.append(got)
+    assert runs[0] and kept and runs[0].keys() == runs[1].keys()
+    for k in runs[0]:
+        assert torch.equal(runs[0][k][0], runs[1][k][0])
+        assert torch.equal(runs[0][k][1], runs[1][k][1])
