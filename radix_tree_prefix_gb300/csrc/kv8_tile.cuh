@@ -247,6 +247,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return r;
 }
 
+// A load from the pool.  A decode tile may be chained to a step's store, which
+// then writes the pool while the kernel is alive: the non-coherent path is for
+// memory that nothing writes so long (a scale's 32-byte sector holds its
+// neighbours' too, which an item before on this SM may have fetched), so those
+// loads go to L2.
+template <bool DECODE, typename T>
+__device__ __forceinline__ T ld_pool(const T* p) {
+  if constexpr (DECODE)
+    return __ldcg(p);
+  else
+    return __ldg(p);
+}
+
 // The CTA's place in its cluster, and an address in another CTA's shared memory.
 __device__ __forceinline__ int cluster_rank() {
   uint32_t r;
@@ -438,7 +451,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
         for (int e = 0; e < SPL; ++e) {
           // (a bad slot is reported and read as slot 0 when its tile is loaded)
           const uint32_t at = uint32_t(s[e]) < uint32_t(a.num_slots) ? uint32_t(s[e]) : 0u;
-          dst[e] = k0 + lane + 32 * e < t.key_end ? __ldg(sb + (at >> a.block_log2))
+          dst[e] = k0 + lane + 32 * e < t.key_end ? ld_pool<DECODE>(sb + (at >> a.block_log2))
                                                   : make_float2(0.f, 0.f);
         }
       };
@@ -678,7 +691,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
       for (int e = 0; e < SPL; ++e) {
         // (the K loader reports a bad slot)
         if (slot[e] < 0 || slot[e] >= a.num_slots) slot[e] = 0;
-        sc[e] = k0 + 32 * e < t.key_end ? __ldg(&sb[slot[e] >> a.block_log2].y) : 0.f;
+        sc[e] = k0 + 32 * e < t.key_end ? ld_pool<DECODE>(&sb[slot[e] >> a.block_log2].y) : 0.f;
       }
     };
     // piece p is of row p * RPP + row_in, i.e. of the key that lane row % 32 holds
@@ -692,7 +705,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     auto load_pieces = [&]() {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        v[p] = __ldg(reinterpret_cast<const uint4*>(src + uint64_t(uint32_t(s[p])) * D));
+        v[p] = ld_pool<DECODE>(
+            reinterpret_cast<const uint4*>(src + uint64_t(uint32_t(s[p])) * D));
     };
     load_slots(0);
     load_scales(0);

@@ -1,0 +1,130 @@
+"""Runs of decode steps over the 8-bit KV pool (rx_kv8_decode_steps), whose
+kernels overlap: a run gives the bits of its steps called one at a time, also
+where a step reads what the store just before it wrote.
+"""
+
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from radix_tree_prefix_gb300 import rx
+
+
+class Steps:
+    """A pool filled by rx_kv8_store, table rows of given lengths that may share
+    their first part with another row, and lists of decode steps over them."""
+
+    def __init__(self, torch, Hq, H, d, block, lens, parent, seed):
+        """Row b has lens[b] positions; parent[b] is None or (row, n): its
+        first n positions are that row's."""
+        self.torch, self.Hq, self.H, self.d, self.block = torch, Hq, H, d, block
+        rng = np.random.default_rng(seed)
+        self.gen = torch.Generator(device="cuda")
+        self.gen.manual_seed(seed)
+        own = [n - (p[1] if p else 0) for n, p in zip(lens, parent)]
+        pages = [-(-n // block) for n in own]
+        order = 1 + rng.permutation(sum(pages))
+        self.N = (1 + sum(pages)) * block
+        self.table = np.zeros((len(lens), max(lens)), dtype=np.int32)
+        at = 0
+        for b, (n, p) in enumerate(zip(own, parent)):
+            if p:
+                self.table[b, :p[1]] = self.table[p[0], :p[1]]
+            ids = order[at:at + pages[b]]
+            at += pages[b]
+            s = (ids[:, None] * block + np.arange(block)).reshape(-1)[:n]
+            self.table[b, lens[b] - n:lens[b]] = s
+        kc, vc = (torch.zeros((1, H, self.N, d), dtype=torch.uint8, device="cuda")
+                  for _ in range(2))
+        sc = torch.zeros((1, H, self.N // block, 2), device="cuda")
+        pool = rx.kv8_pool_desc(kc, vc, sc)
+        for b in range(len(lens)):
+            s = self.table[b, lens[b] - own[b]:lens[b]]
+            if len(s):
+                rx.kv8_store(pool, 0, self.up(s), *self.rows(len(s), H, 0.5))
+        self.start = (kc, vc, sc)
+        self.d_table = self.up(self.table)
+        self.keep = []
+
+    def up(self, a):
+        return self.torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+    def rows(self, n, heads, mag):
+        t = self.torch
+        return [(t.randn((n, heads, self.d), generator=self.gen, device="cuda") * mag)
+                .to(t.bfloat16) for _ in range(2)]
+
+    def plan(self, rows, ctx, depth, n_steps=1):
+        """A plan of the given table rows; the first depth[b] positions of a
+        row are its cached path (equal slots are equal tokens)."""
+        cache = rx.RadixCache(self.N, self.block)
+        nodes = [cache.insert(self.table[r, :n], self.table[r, :n])[1]
+                 for r, n in zip(rows, depth)]
+        plan, info = cache.plan_decode(nodes, ctx, rows, self.Hq, self.H, self.d, n_steps=n_steps)
+        d_plan = self.up(plan[:int(info.plan_words)])
+        self.keep.append((d_plan, info))
+        return d_plan, info, list(rows), list(ctx)
+
+    def entries(self, entries, mag=2.0):
+        """Decode steps [(plan, step)], each with new K and V for its tokens."""
+        torch, B = self.torch, len(entries[0][0][2])
+        rec = np.zeros(len(entries), dtype=rx.DECODE_STEP_DTYPE)
+        ins = []
+        for i, ((d_plan, info, rows, ctx), t) in enumerate(entries):
+            slots = np.array([self.table[r, c + t - 1] for r, c in zip(rows, ctx)])
+            assert len(set(slots.tolist())) == B
+            q, _ = self.rows(B, self.Hq, 1.0)
+            k, v = self.rows(B, self.H, mag)
+            ins.append((q, k, v, self.up(slots)))
+            rec["d_q"][i], rec["d_k"][i], rec["d_v"][i], rec["d_slots"][i] = (
+                x.data_ptr() for x in ins[-1])
+            rec["d_plan"][i], rec["info"][i] = d_plan.data_ptr(), C.addressof(info)
+            rec["step"][i] = t
+        need = max(int(e[0][1].workspace_bytes) for e in entries) + 4 * len(entries)
+        self.keep.append(ins)
+
+        def run(one_by_one):
+            pool = rx.kv8_pool_desc(*(x.clone() for x in self.start))
+            out = torch.full((len(entries), B, self.Hq, self.d), 9.0, device="cuda")
+            lse = torch.full((len(entries), B, self.Hq), 9.0, device="cuda")
+            ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+            r = rec.copy()
+            for i in range(len(entries)):
+                r["d_out"][i], r["d_lse"][i] = out[i].data_ptr(), lse[i].data_ptr()
+            torch.cuda.synchronize()
+            for part in ([r[i:i + 1] for i in range(len(r))] if one_by_one else [r]):
+                rx.decode_steps(pool, 0, self.Hq, self.d_table, part, B, self.d ** -0.5, ws)
+                if one_by_one:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            assert rx.device_check() == 0
+            return (out, lse, *pool.tensors)
+        return run
+
+
+def _equal(torch, run, times=8):
+    want = run(True)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    for _ in range(times):
+        got = run(False)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d", [(64, 2, 128), (32, 2, 256)])
+@pytest.mark.parametrize("block", [1, 4])
+def test_more_tiles_than_sms_read_the_new_tokens(Hq, H, d, block):
+    """Large groups: the tails are tile items too, more of them than the device
+    has SMs, so that one follows another on an SM that has read the pool before
+    the step's store (slots of the shared path and of the tails mixed, so that
+    their scales share sectors)."""
+    torch = pytest.importorskip("torch")
+    B, depth, steps = 84, 2048, 12
+    lens = [depth + steps + 1 + 5 * (b % 7) // block * block for b in range(B)]
+    c = Steps(torch, Hq, H, d, block, lens, [None] + [(0, depth)] * (B - 1), 12)
+    p = c.plan(range(B), [n - steps + 1 for n in lens], [depth] * B, n_steps=steps)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert p[1].n_work == p[1].n_work_tc and p[1].n_work_tc * H > sms
+    _equal(torch, c.entries([(p, t) for t in range(steps)]))
