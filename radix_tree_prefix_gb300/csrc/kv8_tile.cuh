@@ -361,6 +361,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
   if (DECODE && parts == 1 && n_tiles <= 0) {
     // keys that a later step of the plan brings: empty partial rows
     if (a.chained) rxk::griddep_wait();
+    if (a.chained && a.counter && tid == 0) release_counter(a.counter);
     for (int idx = tid; idx < t.n_rows * (D / 4); idx += kTileThreads) {
       const int col = idx % (D / 4) * 4;
       int64_t q_row, out_row;
@@ -650,6 +651,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
       // (warp 15, idle otherwise) the streams beside the tiles start once the
       // store has completed
       rxk::griddep_wait();
+      if (a.counter && lane == 0) release_counter(a.counter);
+      __syncwarp();
       rxk::griddep_launch_dependents();
     }
   } else if (warp >= 8) {

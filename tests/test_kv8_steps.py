@@ -128,3 +128,19 @@ def test_more_tiles_than_sms_read_the_new_tokens(Hq, H, d, block):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     assert p[1].n_work == p[1].n_work_tc and p[1].n_work_tc * H > sms
     _equal(torch, c.entries([(p, t) for t in range(steps)]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d,block", [(32, 8, 128, 1), (32, 8, 128, 4), (16, 4, 256, 1),
+                                          (16, 4, 256, 16)])
+@pytest.mark.parametrize("B,depth", [(48, 2048), (12, 4096)])
+def test_streams_beside_tiles_read_the_new_tokens(Hq, H, d, block, B, depth):
+    """The shared path in tiles, the tails in streams that start beside them:
+    every tail holds the token that the store just before wrote."""
+    torch = pytest.importorskip("torch")
+    steps = 24
+    lens = [depth + steps + 1 + 37 * (b % 11) // block * block for b in range(B)]
+    c = Steps(torch, Hq, H, d, block, lens, [None] + [(0, depth)] * (B - 1), 13)
+    p = c.plan(range(B), [n - steps + 1 for n in lens], [depth] * B, n_steps=steps)
+    assert 0 < p[1].n_work_tc < p[1].n_work
+    _equal(torch, c.entries([(p, t) for t in range(steps)]))
