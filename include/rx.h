@@ -448,10 +448,12 @@ rx_status rx_extend_wave(rx_cache* cache, int32_t R, const int32_t* tokens,
  *   req_part_indptr[B+1], req_parts[n_parts]: partial results of request b
  *       are entries req_parts[req_part_indptr[b] .. req_part_indptr[b+1]).
  * Partial entry p of work item w's member i is part_base(w) + i.  Word 7 of a
- * work item is 0, or for a request's private tail the end of that tail at
- * step 0 of a multi-step plan: at step t the item's keys end at
- * min(kv_end, word7 + t) (an item left empty writes a zero partial with
- * lse = -inf, which the merge weighs 0). */
+ * work item is 0 if no step of the plan stores a token in the item's segment.
+ * Otherwise it is the segment's end at step 0, and at step t the item's keys
+ * end at min(kv_end, word7 + t) (an item left empty writes a zero partial with
+ * lse = -inf, which the merge weighs 0): a request's private tail, or a shared
+ * segment at whose end a request's context ends at step 0, which is whole at
+ * every step. */
 #define RX_WORK_WORDS 8
 typedef struct rx_decode_plan_info {
   int64_t plan_words;     /* int32 words used                             */

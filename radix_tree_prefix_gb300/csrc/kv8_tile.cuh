@@ -90,7 +90,7 @@ struct TileDesc8 {
   int key_begin, key_end, nomask_end, n_rows;
   int gr0, q_base, prefix;
   int member_off, part_base;
-  bool grows;  // its end moves with the step
+  bool grows;  // steps of the plan store into its segment
 };
 
 template <bool DECODE>
@@ -354,9 +354,10 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     t.key_begin = rank < parts ? t.key_begin + first * BN : t.key_end;  // (no part: no keys)
   }
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
-  // Chained to a step's store: a segment that grows waits for it, any other
-  // reads what no kernel of the run writes (a block of slots holds no rows of a
-  // shared segment and of a tail), and waits before it writes partial rows.
+  // Chained to a step's store: a segment that steps of the plan store into
+  // waits for it, any other reads what no kernel of the run writes (a block of
+  // slots holds no rows of a shared segment and of a tail), and waits before it
+  // writes partial rows.
   if (DECODE && a.chained && t.grows) rxk::griddep_wait();
   if (DECODE && parts == 1 && n_tiles <= 0) {
     // keys that a later step of the plan brings: empty partial rows

@@ -870,7 +870,10 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
     int32_t row;
     int64_t kb, ke;
     std::vector<int32_t> members;
-    int64_t grow = 0;  // private tail: its end at step t is min(ke, grow + t)
+    // 0: no step of the plan stores into the segment.  Otherwise one does, and
+    // its end at step t is min(ke, grow + t): a private tail, or a shared segment
+    // with a request's newest token at its end (grow = ke: always whole)
+    int64_t grow = 0;
   };
   std::vector<Seg> segs;
   std::unordered_map<const Node*, size_t> seg_of;
@@ -882,7 +885,7 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
   for (int32_t b = 0; b < B; ++b) {
     const auto& path = paths[b];
     int64_t pos = 0;
-    size_t i = 0;
+    size_t i = 0, last_shared = 0;
     while (i < path.size() && visits[path[i]] >= 2) {
       int32_t cnt = visits[path[i]];
       const Node* first = path[i];
@@ -893,17 +896,22 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
       }
       auto it = seg_of.find(first);
       if (it == seg_of.end()) {
-        seg_of.emplace(first, segs.size());
+        last_shared = segs.size();
+        seg_of.emplace(first, last_shared);
         segs.push_back(Seg{req_rows[b], start, pos, {b}});
         ++n_shared;
       } else {
-        segs[it->second].members.push_back(b);
+        last_shared = it->second;
+        segs[last_shared].members.push_back(b);
       }
     }
     // private tail: covers the context of the last step; at step t it ends at
     // ctx_len[b] + t
     const int64_t last = int64_t(ctx_len[b]) + n_steps - 1;
-    if (int64_t(ctx_len[b]) <= pos) tails_private = false;
+    if (int64_t(ctx_len[b]) <= pos) {
+      tails_private = false;
+      segs[last_shared].grow = pos;  // (ctx_len >= 1, so there is a shared segment)
+    }
     if (last > pos) segs.push_back(Seg{req_rows[b], pos, last, {b}, int64_t(ctx_len[b])});
   }
   // work items: (key chunk, member block) of each segment.  Segments with <=

@@ -11,6 +11,49 @@ import pytest
 from radix_tree_prefix_gb300 import rx
 
 
+def _plan_words(plan, info):
+    n = int(info.n_work)
+    return np.asarray(plan[int(info.off_work):int(info.off_work) + 8 * n]).reshape(n, 8)
+
+
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("Hq,H,d", [(32, 8, 128), (16, 4, 256), (64, 2, 128)])
+def test_plans_mark_shared_segments_that_a_step_stores_into(page, Hq, H, d):
+    """Word 7 of a work item is 0 only if no step of the plan stores a token in
+    the item's segment: a request whose context ends with the shared path has
+    its first step's token at that path's end."""
+    cache = rx.RadixCache(8192, page)
+    slots = np.arange(1, 1 + 2048, dtype=np.int32) + page - 1
+    path = np.arange(960, dtype=np.int32)
+    mid = cache.insert(path[:640], slots[:640])[1]
+    end = cache.insert(path, slots[:960])[1]
+    B = 40
+    for n_steps in (1, 5):
+        # every context ends past the shared path: nothing is stored into it
+        plan, info = cache.plan_decode([end] * B, [961 + b for b in range(B)], np.arange(B), Hq, H,
+                                       d, n_steps=n_steps)
+        w = _plan_words(plan, info)
+        assert (w[w[:, 4] > 1, 7] == 0).all() and (w[w[:, 2] > 960, 7] > 960).all()
+        # request 3 ends at the path's end, or at the end of its first part
+        for node, depth in ((end, 960), (mid, 640)):
+            nodes, ctx = [end] * B, [961 + b for b in range(B)]
+            nodes[3], ctx[3] = node, depth
+            plan, info = cache.plan_decode(nodes, ctx, np.arange(B), Hq, H, d, n_steps=n_steps)
+            w = _plan_words(plan, info)
+            into = (w[:, 1] < depth) & (depth <= w[:, 2]) & (w[:, 4] > 1)
+            assert into.any() and (w[into, 7] == depth).all()
+            shared = w[w[:, 4] > 1]
+            first = depth if node == mid else 0     # the segment that ends at `depth`
+            rest = shared[shared[:, 1] >= first] if node == mid else shared[:0]
+            assert (rest[:, 7] == 0).all()
+            # the keys of every step are those of before: the whole segment
+            for t in range(n_steps):
+                ends = np.where(w[into, 7] > 0, np.minimum(w[into, 2], w[into, 7] + t), w[into, 2])
+                assert (ends == w[into, 2]).all()
+            assert info.tails_private == 0
+            assert info.distinct_kv_tokens == 960 + sum(max(0, c - 960) for c in ctx)
+
+
 class Steps:
     """A pool filled by rx_kv8_store, table rows of given lengths that may share
     their first part with another row, and lists of decode steps over them."""
@@ -144,3 +187,18 @@ def test_streams_beside_tiles_read_the_new_tokens(Hq, H, d, block, B, depth):
     p = c.plan(range(B), [n - steps + 1 for n in lens], [depth] * B, n_steps=steps)
     assert 0 < p[1].n_work_tc < p[1].n_work
     _equal(torch, c.entries([(p, t) for t in range(steps)]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d", [(32, 8, 128), (16, 4, 256), (64, 2, 128)])
+@pytest.mark.parametrize("block", [1, 16])
+def test_new_tokens_at_the_end_of_a_shared_segment(Hq, H, d, block):
+    """One request of 40 ends with the path that all share, so each step stores
+    into a segment that tiles read (its token anew at every step)."""
+    torch = pytest.importorskip("torch")
+    B, depth = 40, 1024
+    lens = [depth] + [depth + 1 + 3 * b for b in range(1, B)]
+    c = Steps(torch, Hq, H, d, block, lens, [None] + [(0, depth)] * (B - 1), 11)
+    p = c.plan(range(B), lens, [depth] * B)
+    assert p[1].n_work_tc > 0
+    _equal(torch, c.entries([(p, 0)] * 6))
