@@ -1121,12 +1121,14 @@ extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t l
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_steps: Hq % Hkv != 0");
   // Every step has its own unit counter, reset together behind the largest
-  // step's partials if the workspace has room, and its launches are chained:
-  // from the second step on the store is launched while the merge before it
-  // runs, and the tiles or streams while the store does.  Each waits on the device
-  // for the end of the kernel before it (which did so too) before it reads what
-  // that writes or writes what that reads; tiles of shared segments so run beside
-  // the end of the step before.
+  // step's partials if the workspace has room, and the launches of steps that
+  // follow on under one plan are chained: the store is launched while the merge
+  // before it runs, and the tiles or streams while the store does.  Each waits on
+  // the device for the end of the kernel before it (which did so too) before it
+  // reads what that writes or writes what that reads; tiles of shared segments so
+  // run beside the end of the step before.  The plan says which segments its steps
+  // store into.  Another plan's segments may hold what the steps before stored, so
+  // its first step starts when those have ended.
   int64_t region = 0;
   bool own_counters = n_steps > 0 && B > 0;
   for (int32_t i = 0; own_counters && i < n_steps; ++i) {
@@ -1146,12 +1148,12 @@ extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t l
     return rx_internal::launch_status("rx_kv8_decode_steps: counters reset");
   for (int32_t i = 0; i < n_steps; ++i) {
     const rx_decode_step& t = steps[i];
-    r = rx_internal::kv8_store(pool, layer, t.d_slots, t.d_k, t.d_v, B, stream,
-                               i > 0 && own_counters);
+    const bool chained = own_counters && i > 0 && t.d_plan == steps[i - 1].d_plan;
+    r = rx_internal::kv8_store(pool, layer, t.d_slots, t.d_k, t.d_v, B, stream, chained);
     if (r != RX_OK) return r;
     r = decode8(pool, layer, t.d_q, num_q_heads, d_req_to_token, row_stride, t.d_plan, t.info, B,
                 t.step, scale, t.d_out, RX_OUT_F32, t.d_lse, d_workspace, workspace_bytes, stream,
-                own_counters ? counters + i : nullptr, i > 0 && own_counters);
+                own_counters ? counters + i : nullptr, chained);
     if (r != RX_OK) return r;
   }
   return RX_OK;

@@ -202,3 +202,22 @@ def test_new_tokens_at_the_end_of_a_shared_segment(Hq, H, d, block):
     p = c.plan(range(B), lens, [depth] * B)
     assert p[1].n_work_tc > 0
     _equal(torch, c.entries([(p, 0)] * 6))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d", [(32, 8, 128), (16, 4, 256), (64, 2, 128)])
+@pytest.mark.parametrize("block", [1, 16])
+def test_a_plan_over_what_the_plan_before_stored(Hq, H, d, block):
+    """A list of two plans: the first one's steps append to a context that the
+    second one's requests share, so its tiles read the rows that the entries
+    just before stored."""
+    torch = pytest.importorskip("torch")
+    B, end = 40, 1024
+    lens = [end] + [60 + b for b in range(1, B)] + [end + 9 + b for b in range(B)]
+    c = Steps(torch, Hq, H, d, block, lens, [None] * B + [(0, end)] * B, 14)
+    steps = 4
+    first = c.plan(range(B), [n - steps + 1 for n in lens[:B]], [0] * B, n_steps=steps)
+    then = c.plan(range(B, 2 * B), [n - 3 for n in lens[B:]], [end] * B, n_steps=3)
+    assert then[1].n_work_tc > 0
+    _equal(torch, c.entries([(first, t) for t in range(steps)] + [(then, t) for t in range(3)] +
+                            [(first, steps - 1), (then, 0)]))
