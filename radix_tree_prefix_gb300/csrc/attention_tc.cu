@@ -128,7 +128,7 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
     const int32_t* w = a.work + int64_t(bx) * RX_WORK_WORDS;
     t.trow = a.table + int64_t(w[0]) * a.row_stride;
     t.key_begin = w[1];
-    t.key_end = w[2];
+    t.key_end = w[7] > 0 ? min(w[2], w[7] + a.step) : w[2];
     t.member_off = w[3];
     t.part_base = w[5];
     t.n_rows = w[6];
@@ -338,6 +338,20 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   const int lane = tid & 31;
   const TileDesc t = describe<DECODE>(a, bx);
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
+  if (DECODE && n_tiles <= 0) {
+    // keys that a later step of the plan brings: empty partial rows
+    rxk::griddep_wait();
+    for (int idx = tid; idx < t.n_rows * (D / 4); idx += int(blockDim.x)) {
+      int64_t qi = 0, part = 0;
+      int head = 0, lim = 0;
+      row_info<DECODE>(a, t, kvh, idx / (D / 4), qi, head, part, lim);
+      const int64_t row = part * a.hq + head;
+      *reinterpret_cast<float4*>(a.ws_o + row * D + idx % (D / 4) * 4) =
+          make_float4(0.f, 0.f, 0.f, 0.f);
+      if (idx % (D / 4) == 0) a.ws_lse[row] = -INFINITY;
+    }
+    return;
+  }
 
   // Softmax threads: the query row of their TMEM lane, and the gather of
   // half of Q row i, issued before the barriers and TMEM are set up so the

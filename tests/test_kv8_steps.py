@@ -78,17 +78,25 @@ class Steps:
             at += pages[b]
             s = (ids[:, None] * block + np.arange(block)).reshape(-1)[:n]
             self.table[b, lens[b] - n:lens[b]] = s
-        kc, vc = (torch.zeros((1, H, self.N, d), dtype=torch.uint8, device="cuda")
-                  for _ in range(2))
-        sc = torch.zeros((1, H, self.N // block, 2), device="cuda")
-        pool = rx.kv8_pool_desc(kc, vc, sc)
+        self.start = self.empty_pool()
+        pool = self.desc(self.start)
         for b in range(len(lens)):
             s = self.table[b, lens[b] - own[b]:lens[b]]
             if len(s):
-                rx.kv8_store(pool, 0, self.up(s), *self.rows(len(s), H, 0.5))
-        self.start = (kc, vc, sc)
+                self.store(pool, 0, self.up(s), *self.rows(len(s), H, 0.5))
         self.d_table = self.up(self.table)
         self.keep = []
+
+    store = staticmethod(rx.kv8_store)
+
+    def empty_pool(self):
+        torch = self.torch
+        return (*(torch.zeros((1, self.H, self.N, self.d), dtype=torch.uint8, device="cuda")
+                  for _ in range(2)),
+                torch.zeros((1, self.H, self.N // self.block, 2), device="cuda"))
+
+    def desc(self, tensors):
+        return rx.kv8_pool_desc(*tensors)
 
     def up(self, a):
         return self.torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
@@ -128,7 +136,8 @@ class Steps:
         self.keep.append(ins)
 
         def run(one_by_one):
-            pool = rx.kv8_pool_desc(*(x.clone() for x in self.start))
+            tensors = [x.clone() for x in self.start]
+            pool = self.desc(tensors)
             out = torch.full((len(entries), B, self.Hq, self.d), 9.0, device="cuda")
             lse = torch.full((len(entries), B, self.Hq), 9.0, device="cuda")
             ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
@@ -142,7 +151,8 @@ class Steps:
                     torch.cuda.synchronize()
             torch.cuda.synchronize()
             assert rx.device_check() == 0
-            return (out, lse, *pool.tensors)
+            return (out, lse, *tensors)
+        run.inputs = ins
         return run
 
 
