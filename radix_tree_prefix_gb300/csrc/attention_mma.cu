@@ -271,7 +271,8 @@ extern "C" rx_status rx_decode_steps(const rx_pool_desc* pool, int32_t layer, in
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_decode_steps: Hq % Hkv != 0");
   const int G = num_q_heads / pool->num_kv_heads;
-  // A run of steps whose new tokens all lie in private tails: every step has
+  // A run of steps of one plan whose new tokens all lie in private tails (another
+  // plan's shared segments may hold what the steps before stored): every step has
   // its own work counter (zeroed here at once, after the largest step's
   // partial results), step 0's merge lets the next kernel launch only after
   // step 0 has completed, and later steps' tiles then read their queries and
@@ -281,7 +282,7 @@ extern "C" rx_status rx_decode_steps(const rx_pool_desc* pool, int32_t layer, in
   int64_t region = 0;
   for (int32_t i = 0; early && i < n_steps; ++i) {
     const rx_decode_plan_info* inf = steps[i].info;
-    if (!inf || inf->tails_private != 1) {
+    if (!inf || inf->tails_private != 1 || steps[i].d_plan != steps[0].d_plan) {
       early = false;
       break;
     }
@@ -309,10 +310,12 @@ extern "C" rx_status rx_decode_steps(const rx_pool_desc* pool, int32_t layer, in
                (reinterpret_cast<uintptr_t>(st.d_v) & 15)) {
       return rx_internal::set_error(RX_ERR_INVALID, "rx_decode_steps: NULL or misaligned K/V");
     }
+    // (the merge leaves a plan's counter at 0 for that plan's next step)
+    const bool first = i == 0 || st.d_plan != steps[i - 1].d_plan;
     r = decode_attention_impl(pool, layer, st.d_q, num_q_heads, d_req_to_token, row_stride,
                               st.d_plan, st.info, B, scale, st.d_out, st.d_lse, d_workspace,
                               workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
-                              i == 0 && !early, st.step, fused ? st.d_k : nullptr,
+                              first && !early, st.step, fused ? st.d_k : nullptr,
                               fused ? st.d_v : nullptr, fused ? st.d_slots : nullptr,
                               early ? counters + i : nullptr, early && i > 0, early && i == 0);
     if (r != RX_OK) return r;

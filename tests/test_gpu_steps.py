@@ -1,5 +1,5 @@
 """Runs of decode steps over the bf16 pool (rx_decode_steps): steps of one plan
-against softmax attention in 64 bits.
+against softmax attention in 64 bits, and lists of several plans.
 """
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 
 from radix_tree_prefix_gb300 import rx
 
-from test_kv8_steps import Steps
+from test_kv8_steps import Steps, _equal
 
 
 class Bf16Steps(Steps):
@@ -60,3 +60,21 @@ def test_a_step_sees_no_token_of_a_later_step(Hq, H, d, depth, own, steps):
             bound = (2.0 ** -7 + ds)[:, None] * torch.einsum("hn,hnd->hd", w, vv.abs())
             assert ((out[t, b].double() - want).abs() <= bound).all(), (t, b)
             assert ((lse[t, b].double() - s.logsumexp(-1)).abs() <= 2.0 ** -8 + ds).all(), (t, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H,d", [(32, 8, 128), (16, 4, 256), (64, 2, 128)])
+@pytest.mark.parametrize("first_end", [1024, 300])
+def test_a_list_of_two_plans(Hq, H, d, first_end):
+    """Plans of other sizes in one list, the second one's shared path appended
+    to by the first one's steps: the entries called one at a time give the same
+    bits."""
+    torch = pytest.importorskip("torch")
+    B, end, steps = 40, first_end, 4
+    lens = [end] + [60 + b for b in range(1, B)] + [end + 9 + b for b in range(B)]
+    c = Bf16Steps(torch, Hq, H, d, 1, lens, [None] * B + [(0, end)] * B, 22)
+    first = c.plan(range(B), [n - steps + 1 for n in lens[:B]], [0] * B, n_steps=steps)
+    then = c.plan(range(B, 2 * B), [n - 3 for n in lens[B:]], [end] * B, n_steps=3)
+    assert then[1].n_work_tc > 0 and first[1].n_parts != then[1].n_parts
+    _equal(torch, c.entries([(first, t) for t in range(steps)] + [(then, t) for t in range(3)] +
+                            [(first, steps - 1), (then, 0)]))
