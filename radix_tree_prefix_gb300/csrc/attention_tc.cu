@@ -338,21 +338,6 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   const int lane = tid & 31;
   const TileDesc t = describe<DECODE>(a, bx);
   const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
-  if (DECODE && n_tiles <= 0) {
-    // keys that a later step of the plan brings: empty partial rows
-    rxk::griddep_wait();
-    for (int idx = tid; idx < t.n_rows * (D / 4); idx += int(blockDim.x)) {
-      int64_t qi = 0, part = 0;
-      int head = 0, lim = 0;
-      row_info<DECODE>(a, t, kvh, idx / (D / 4), qi, head, part, lim);
-      const int64_t row = part * a.hq + head;
-      *reinterpret_cast<float4*>(a.ws_o + row * D + idx % (D / 4) * 4) =
-          make_float4(0.f, 0.f, 0.f, 0.f);
-      if (idx % (D / 4) == 0) a.ws_lse[row] = -INFINITY;
-    }
-    return;
-  }
-
   // Softmax threads: the query row of their TMEM lane, and the gather of
   // half of Q row i, issued before the barriers and TMEM are set up so the
   // copies overlap that start-up (nothing else uses the Q buffer yet; the
@@ -824,6 +809,12 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
         if (rd) reinterpret_cast<float4*>(rd)[c4] = v;
       }
       if (valid && wg == 0) *lse_dst = m_ref * kLn2 + logf(l_all);
+    } else if (DECODE && n_tiles <= 0 && valid) {
+      // keys that a later step of the plan brings: an empty partial row
+      float4* dst = reinterpret_cast<float4*>(a.ws_o + (part * a.hq + head) * D + wg * (D / 2));
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) dst[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wg == 0) a.ws_lse[part * a.hq + head] = -INFINITY;
     }
   }
   tc::tc_fence_before();
