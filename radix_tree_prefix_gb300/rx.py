@@ -711,7 +711,6 @@ def kv8_pool_desc(k_codes, v_codes, scales):
     p.tensors = (k_codes, v_codes, scales)
     p.device = k_codes.device
     p.index = k_codes.get_device()  # -1 on the CPU
-    p.ref = C.byref(p)
     p.dtypes = (torch.int32, torch.bfloat16, torch.float32)
     p.current_device = torch.cuda.current_device
     # the handle of a device's current stream (torch.cuda.current_stream makes
@@ -751,7 +750,7 @@ def kv8_store(pool, layer, d_slots, d_k, d_v, stream=None):
     n = T * pool.num_kv_heads * pool.head_dim
     s = _kv8_args(pool, stream, ("d_slots", d_slots, i32, T),
                   ("d_k", d_k, bf16, n), ("d_v", d_v, bf16, n))
-    _check(_lib.rx_kv8_store(pool.ref, layer, d_slots.data_ptr(), d_k.data_ptr(),
+    _check(_lib.rx_kv8_store(pool, layer, d_slots.data_ptr(), d_k.data_ptr(),
                              d_v.data_ptr(), T, s))
 
 
@@ -762,7 +761,7 @@ def kv8_load(pool, layer, d_slots, d_k, d_v, stream=None):
     n = T * pool.num_kv_heads * pool.head_dim
     s = _kv8_args(pool, stream, ("d_slots", d_slots, i32, T),
                   ("d_k", d_k, bf16, n), ("d_v", d_v, bf16, n))
-    _check(_lib.rx_kv8_load(pool.ref, layer, d_slots.data_ptr(), d_k.data_ptr(),
+    _check(_lib.rx_kv8_load(pool, layer, d_slots.data_ptr(), d_k.data_ptr(),
                             d_v.data_ptr(), T, s))
 
 
@@ -779,7 +778,7 @@ def kv8_extend_attention(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len
                   ("d_out", d_out, bf16 if ot else f32, n),
                   ("d_lse", d_lse, f32, n // pool.head_dim))
     _check(_lib.rx_kv8_extend_attention(
-        pool.ref, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        pool, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
         d_req_rows.data_ptr(), d_prefix_len.data_ptr(), d_qo_indptr.data_ptr(),
         d_tile_indptr.data_ptr(), R, num_tiles, scale, d_out.data_ptr(), ot, d_lse.data_ptr(), s))
 
@@ -796,7 +795,7 @@ def kv8_decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, 
                   ("d_lse", d_lse, f32, rows),
                   ("d_workspace", d_workspace, d_workspace.dtype, 0))
     _check(_lib.rx_kv8_decode_attention(
-        pool.ref, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        pool, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
         d_plan.data_ptr(), C.byref(info), B, step, scale, d_out.data_ptr(), ot, d_lse.data_ptr(),
         d_workspace.data_ptr(), d_workspace.numel() * d_workspace.element_size(), s))
 
