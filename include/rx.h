@@ -851,8 +851,12 @@ rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
  * is not finite gives NaN, in its own row alone.  scale must lie in
  * [2^-40, 2^40].  A pool row that a table names must hold codes of
  * rx_kv8_store or other finite ones (not 0x7f or 0xff) and scales in
- * [2^-126, 2^120]; rows no table names are never read.  Errors: RX_ERR_INVALID as
- * rx_extend_attention, for a scale out of range and an unknown out_type. */
+ * [2^-126, 2^120]; rows no table names are never read.  With a the largest
+ * magnitude of a query row, its scores hold for scale * a up to 2^80 and
+ * scale * a * (a K scale) up to 2^106 (beyond, the row may come out NaN), and
+ * for a = 0 or a >= 2^-60 (below, its elements lose bits).
+ * Errors: RX_ERR_INVALID as rx_extend_attention, for a scale out of range and
+ * an unknown out_type. */
 rx_status rx_kv8_extend_attention(
     const rx_kv8_pool_desc* pool, int32_t layer, const void* d_q,
     int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,

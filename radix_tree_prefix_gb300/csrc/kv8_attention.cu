@@ -43,11 +43,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-// The softmax reference of a row moves when a score exceeds it by 2^9, and
-// weights are scaled by 2^6: at most 2^15, within f16, and full f16 precision
-// down to 2^-20 of the reference.
-constexpr float kRescaleThreshold = 9.0f;
+// A row's weights are 2^(x - m + 6), m its reference, which moves to the largest
+// score when a weight would exceed 2^15: within f16, and full f16 precision down
+// to 2^-20 of the reference's.
 constexpr float kWeightBias = 6.f;
+constexpr float kMaxWeight = 15.f;
 
 struct Args8 {
   const bf16* q;
@@ -63,7 +63,9 @@ struct Args8 {
   int64_t row_stride;
   int hq;
   int group;
-  float scale_log2;
+  float scale_log2;  // scale * log2(e)
+  float key_mul;     // its mantissa, times 2^-kKeyShift (tiles)
+  int scale_exp;     // its exponent
   // extend
   const int32_t* req_rows;
   const int32_t* prefix_len;
@@ -274,12 +276,12 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
   }
 
   float o[NR][NK][4];
-  float m_ref[NR][2], l_run[NR][2];
+  float m_off[NR][2], l_run[NR][2];  // the reference less 6; the weights' sum
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
     for (int mt = 0; mt < NK; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
-    m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
+    m_off[nt][0] = m_off[nt][1] = -INFINITY;
     l_run[nt][0] = l_run[nt][1] = 0.f;
   }
   float vref = 0.f, inv_vref = 0.f;
@@ -336,13 +338,16 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        // (rounded down: scores of 2^24 and more are whole steps apart)
+        const float limit = __fadd_rd(m_off[nt][e], kMaxWeight);
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
           float& y = x[nt][i >> 1][(i & 1) * 2 + e];
           y = key0 + 8 * i < ke ? y * (s4[i].x * rs[nt][e]) : -INFINITY;
-          grow |= y > m_ref[nt][e] + kRescaleThreshold;
+          grow |= y > limit;
         }
+      }
     if (__any_sync(0xffffffffu, grow)) {
       float vm = vmax;
       float mx[NR][2];
@@ -374,9 +379,9 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float alpha = 1.f;
-          if (mx[nt][e] > m_ref[nt][e]) {
-            alpha = rxk::fast_exp2(m_ref[nt][e] - mx[nt][e]);  // 0 from -inf
-            m_ref[nt][e] = mx[nt][e];
+          if (mx[nt][e] - kWeightBias > m_off[nt][e]) {
+            alpha = rxk::fast_exp2(m_off[nt][e] - (mx[nt][e] - kWeightBias));  // 0 from -inf
+            m_off[nt][e] = mx[nt][e] - kWeightBias;
             l_run[nt][e] *= alpha;
           }
           alpha *= vf;
@@ -395,8 +400,8 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
     uint32_t pb[NR][2 * MT];
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
-      const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0] - kWeightBias;
-      const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1] - kWeightBias;
+      const float m0 = m_off[nt][0] == -INFINITY ? 0.f : m_off[nt][0];
+      const float m1 = m_off[nt][1] == -INFINITY ? 0.f : m_off[nt][1];
 #pragma unroll
       for (int i = 0; i < 2 * MT; ++i) {
         const float p0 = rxk::fast_exp2(x[nt][i >> 1][(i & 1) * 2] - m0);
@@ -443,8 +448,7 @@ __device__ __forceinline__ void stream_unit(const Args8& a, const Unit8& u, uint
       if (r >= u.n_rows) continue;
       // (2^6 in both O and l; no key: zeros, lse -inf)
       const float inv = l == 0.f ? 0.f : vref / l;
-      const float lse =
-          l == 0.f ? -INFINITY : (m_ref[nt][e] - kWeightBias) * kLn2 + logf(l);
+      const float lse = l == 0.f ? -INFINITY : m_off[nt][e] * kLn2 + logf(l);
       const int mem = r / a.group;
       const int64_t at =
           int64_t(u.part_base + mem) * a.hq + u.kvh * a.group + (r - mem * a.group);
@@ -769,6 +773,8 @@ rx_status common_args(const char* what, const rx_kv8_pool_desc* pool, int32_t la
   a->hq = num_q_heads;
   a->group = num_q_heads / pool->num_kv_heads;
   a->scale_log2 = scale * kLog2e;
+  a->key_mul = ldexpf(frexpf(a->scale_log2, &a->scale_exp), 1 - kKeyShift);
+  --a->scale_exp;
   a->out_bf16 = out_type == RX_OUT_BF16;
   return RX_OK;
 }

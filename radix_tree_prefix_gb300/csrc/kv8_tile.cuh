@@ -52,6 +52,12 @@ namespace {
 constexpr int kTileThreads = 512;
 constexpr int BM = 128;
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
+// A score is S (at most 448^2 D < 2^26) times its K scale (up to 2^120) times the
+// row's scale.  The K scale comes times 2^-20 and the mantissa of scale log2(e)
+// (Args8::key_mul), so that the first product does not overflow, and the row's
+// scale is a power of two, so that the second is exact: the largest score and the
+// reference taken from it then differ by nothing, however large they are.
+constexpr int kKeyShift = 20;
 
 template <int HEAD_DIM>
 struct Tile8 {
@@ -563,7 +569,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
   #pragma unroll
         for (int e = 0; e < SPL; ++e) {
           vm = fmaxf(vm, sc[e].y);
-          ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x;
+          ks_ring[(j % SR) * BN + lane + 32 * e] = sc[e].x * a.key_mul;
         }
         // (positive floats compare as integers)
         vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
@@ -777,7 +783,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     // scores: its row is NaN.
     const float qmax = fmaxf(xch[i], xch[BM + i]);
     const int qe = max(kv8::scale_exponent(qmax), -80);
-    const float rs = qmax < INFINITY ? a.scale_log2 * kv8::pow2(qe) : NAN;
+    const float rs =
+        qmax < INFINITY ? kv8::pow2(min(qe + a.scale_exp + kKeyShift, 127)) : NAN;
     {
       const float qinv = kv8::pow2(-qe);
 #pragma unroll
@@ -813,8 +820,8 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
     // a warp without query rows only keeps the barriers going
     const bool busy = (warp & 3) * 32 < t.n_rows;
     // the first tile's exchange slot is parity 1: the Q maxima lie in parity 0
-    float m_ref = -INFINITY, vref = 0.f;
-    float l = 0.f;  // times 2^6
+    float nm = INFINITY, vref = 0.f;  // 6 - the row's reference
+    float l = 0.f;                    // times 2^6
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < n_tiles; ++j) {
@@ -874,9 +881,9 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
         break;
       }
       const float mx = rs * fmaxf(mx_half, xch[(xp * 2 + (1 - wg)) * BM + i]);
-      // the reference moves when a score exceeds it by 2^9
-      const float m_new = j == 0 || mx > m_ref + kRescaleThreshold ? fmaxf(m_ref, mx) : m_ref;
-      if (j > 0 && __any_sync(0xffffffffu, m_new != m_ref || v_new != vref)) {
+      // the reference moves when a weight would exceed 2^15
+      const float nm_new = mx + nm > kMaxWeight ? kWeightBias - mx : nm;
+      if (j > 0 && __any_sync(0xffffffffu, nm_new != nm || v_new != vref)) {
         // O is rescaled once P V_{j-1} has written it; each warpgroup takes
         // half of its columns
         if (!__all_sync(0xffffffffu, wait(BAR_O(j - 1), (j - 1) >> 1, abort_flag))) {
@@ -884,7 +891,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
           break;
         }
         tc::tc_fence_after();
-        const float alpha = m_new != m_ref ? rxk::fast_exp2(m_ref - m_new) : 1.f;  // 0 from -inf
+        const float alpha = nm_new != nm ? rxk::fast_exp2(nm_new - nm) : 1.f;  // 0 from inf
         const float f = alpha * (vref / v_new);
 #pragma unroll 1
         for (int cc = 0; cc < D / 64; ++cc) {
@@ -898,11 +905,11 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
         }
         l *= alpha;
       }
-      m_ref = m_new;
+      nm = nm_new;
       vref = v_new;
       if (busy) {
-        const float nm = m_ref == -INFINITY ? 0.f : kWeightBias - m_ref;
-        const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(nm, nm);
+        const float add = nm == INFINITY ? 0.f : nm;
+        const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(add, add);
         float2 l2[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) l2[u] = make_float2(u ? 0.f : l, 0.f);
@@ -995,8 +1002,7 @@ __device__ __forceinline__ void tile8(const Args8& a, const Maps8& maps, uint8_t
             *reinterpret_cast<float4*>(obase + (ro * D + wg * HC + c4 * 4) * 4) = v;
         }
       }
-      const float lse = SPLIT && l_all == 0.f ? -INFINITY
-                                              : (m_ref - kWeightBias) * kLn2 + logf(l_all);
+      const float lse = SPLIT && l_all == 0.f ? -INFINITY : logf(l_all) - nm * kLn2;
       if (SPLIT && parts > 1) {
         if (wg == 0) ks_ring[i] = lse;  // (the scales are done with)
       } else if (valid && wg == 0) {
