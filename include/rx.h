@@ -845,9 +845,13 @@ rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
 /* rx_extend_attention over an 8-bit pool: the same queries, tables, tile
  * schedule and causal rule.  d_out is fp32 or bf16 (out_type) [total_q][Hq]
  * [head_dim], rounded once from fp32; d_lse fp32 [total_q][Hq].  Scores and
- * softmax statistics are held in fp32; a query's softmax weights are rounded
- * to f16 (11 significant bits) for the product with V, and V times a scale
- * that is not a power of two (rx_kv8_store writes no such) too.  A query that
+ * softmax statistics are held in fp32.  Rounded are: a query's elements below
+ * 2^-9.8 of its row's largest magnitude, to 2^-17.8 of that; its softmax weights
+ * for the product with V, to f16 (11 significant bits, from 2^-20 of the row's
+ * largest; below, to 2^-31 of that); and values, exact under the power-of-two
+ * scales of rx_kv8_store from 2^-13 of the largest V scale among the request's
+ * keys, off by at most 2^-23 of that scale from 2^-22 of it, and counted as 0 at
+ * worst below (under other scales two roundings to f16 besides).  A query that
  * is not finite gives NaN, in its own row alone.  scale must lie in
  * [2^-40, 2^40].  A pool row that a table names must hold codes of
  * rx_kv8_store or other finite ones (not 0x7f or 0xff) and scales in

@@ -14,11 +14,16 @@
 // tensor-core tile of kv8_tile.cuh; decode items of few rows (a request's own
 // tail) on warps that stream the keys (stream_unit below).  Statistics, scores
 // and accumulators are fp32.  What is rounded further:
-//   q        not at all but for elements under 2^-18 (tile, two e4m3 parts) or
-//            2^-27 (streams, f16) of its row's largest: 8 bits in bf16;
-//   weights  to f16, 11 bits: p_j in the tile, p_j vs_j / vref in the streams;
-//   values   in the tile vs_j / vref and its product with a code are f16: exact
-//            for the power-of-two scales that rx_kv8_store writes;
+//   q        tile, two e4m3 parts: exact from 2^-9.8 of its row's largest
+//            magnitude, to 2^-17.8 of that below; streams, f16: exact from
+//            2^-30 of it, to 2^-38 below;
+//   weights  to f16, 11 bits, and to 2^-31 of the reference's below 2^-20 of it:
+//            p_j in the tile, p_j vs_j / vref in the streams;
+//   values   in the tile vs_j / vref and its product with a code are f16.  For
+//            the power-of-two scales that rx_kv8_store writes that is exact
+//            from 2^-13 of the largest scale so far, and off by at most 2^-23 of
+//            that scale from 2^-22 of it; below, a value may count as 0.  Any
+//            other scale costs two roundings of 2^-11;
 //   output   once, if bf16.
 
 #include <cuda_bf16.h>

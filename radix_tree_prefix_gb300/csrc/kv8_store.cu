@@ -5,7 +5,8 @@
 // and is a power of two: the least 2^e with amax <= 448 * 2^e over the
 // block's rows.  e4m3 is a floating format, so a power-of-two scale costs no
 // precision against amax / 448 (an element's rounding is relative, at most
-// 2^-4 of it, down to amax * 2^-15), every division by it is exact, and
+// 2^-4 of it, down to 2^-6 of the scale, which is amax * 2^-14.8 to amax * 2^-13.8
+// as amax is above 224 scales), every division by it is exact, and
 // rounding a block's rows again under a larger scale (a token appended to the
 // block raised its amax) changes only the rows' smallest elements.
 //

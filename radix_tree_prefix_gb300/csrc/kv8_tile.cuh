@@ -9,8 +9,9 @@
 //   O += P V       kind::f16, V's codes converted to f16 times vs / vref.
 // Q split: a bf16 query has 8 significant bits, an e4m3 number 4.  With the
 // row scaled by a power of two to at most 448, hi = e4m3(q) and lo =
-// e4m3(q - hi) add up to q exactly down to 2^-10 of the row's largest
-// magnitude, and are off by at most 2^-19 of that below.  The two products
+// e4m3(q - hi) add up to q exactly down to 2^-9.8 of the row's largest
+// magnitude, and are off by at most 2^-17.8 of that below (lo's steps end at
+// 2^-9, and the largest is above 224).  The two products
 // cost what one f16 product does (the e4m3 rate is twice f16's), and K needs
 // no conversion and half the shared memory.  Splitting P the same way was
 // not taken: a weight below 2^-18 of the row's largest would be lost, and
@@ -18,8 +19,10 @@
 // f16, so V is converted.
 // vref is at least the largest V scale of the tile and the tiles before it (O
 // is rescaled when it grows, which a factor of 4 of headroom makes rare).  A
-// power-of-two scale, what rx_kv8_store writes, is exact in f16 over vref; any
-// other is rounded there, and again in its product with a code.
+// power-of-two scale, what rx_kv8_store writes, is exact in f16 over vref from
+// 2^-24 of it, and its product with every code from 2^-15 of it (between them a
+// product is off by 2^-25 vref at most); any other is rounded there, and again in
+// its product with a code.
 //
 // 512 threads:
 //   warps 0-7    softmax in two warpgroups that split every key tile's keys;

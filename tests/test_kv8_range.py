@@ -9,20 +9,22 @@ from test_kv8 import Case, _decode, _extend
 
 
 def _scaled(c, ks=None, vs=None):
-    """Sets the K scales (one value) or multiplies V scales (powers of two by
-    slot, equal within a block)."""
+    """Sets the K scales (one value) or the V scales (one value a block) of a
+    case's pool."""
     torch = c.torch
-    used = c.index >= 0
-    if ks is not None:
-        old = c.sc[1][..., 0].double().cpu().numpy()[:, np.nonzero(used)[0] // c.block]
-        c.k = c.k / old[..., None] * ks
-        c.sc[1][..., 0] = torch.where(torch.isnan(c.sc[1][..., 0]), c.sc[1][..., 0],
-                                      torch.tensor(ks, dtype=torch.float32, device="cuda"))
-    if vs is not None:
-        by_block = vs.reshape(-1, c.block)[:, 0]
-        c.sc[1][..., 1] *= torch.from_numpy(by_block).float().cuda()
-        c.v = c.v * vs[used][None, :, None]
-        c.vs = c.vs * vs[used][None]
+    blocks = np.nonzero(c.index >= 0)[0] // c.block
+    for which, new in ((0, ks), (1, vs)):
+        if new is None:
+            continue
+        new = np.full(c.N // c.block, new, dtype=np.float64)
+        sc = c.sc[1][..., which]
+        old = sc.double().cpu().numpy()[:, blocks]
+        sc.copy_(torch.where(torch.isnan(sc), sc, torch.from_numpy(new).float().cuda()))
+        if which == 0:
+            c.k = c.k / old[..., None] * new[blocks][None, :, None]
+        else:
+            c.v = c.v / old[..., None] * new[blocks][None, :, None]
+            c.vs = np.broadcast_to(new[blocks], old.shape)
 
 
 def _aimed(c, b, js, mag):
@@ -53,11 +55,11 @@ RANGES = [(2.0 ** 120, 2.0 ** -14), (2.0 ** 103, 2.0 ** 4), (2.0 ** 22, 2.0 ** 8
           (1.0, 2.0 ** 16), (2.0 ** 20, 1.0)]
 
 
-def _check(got_o, got_l, want, score, c):
+def _check(got_o, got_l, want, score, c, value=2.0 ** -23):
     go, gl = got_o.double().cpu().numpy(), got_l.double().cpu().numpy()
-    # one weight of 1, exact; V to 2^-23 of the largest V scale (times it and
+    # one weight of 1, exact; V to `value` of the largest V scale (times it and
     # its inverse in fp32)
-    assert (np.abs(go - want) <= np.abs(want) * 2.0 ** -20 + c.vs.max() * 2.0 ** -23).all()
+    assert (np.abs(go - want) <= np.abs(want) * 2.0 ** -20 + c.vs.max() * value).all()
     # fp32 sums of d products, the row's scale, the logarithm's base
     assert (np.abs(gl - score) <= np.abs(score) * 2.0 ** -17 + 2.0 ** -20).all()
 
@@ -131,3 +133,24 @@ def test_scores_whose_neighbours_are_whole_steps_apart(i, exp):
             lo, hi = (np.repeat(f(v, axis=1), Hq // H, axis=0) for f in (np.min, np.max))
             room = 2.0 ** -10 * np.abs(v).max()
             assert (go[b] >= lo - room).all() and (go[b] <= hi + room).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [10, 13, 20, 22])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_the_key_that_counts_has_a_small_v_scale(i, apart):
+    """V scales 2^-10 to 2^-22 of the largest: exact to 2^-13, then off by at
+    most 2^-23 of the largest scale."""
+    torch = pytest.importorskip("torch")
+    Hq, H, d, block, ctx, shared = SHAPES[i]
+    c = Case(torch, Hq, H, d, block, ctx, 800 + i, shared=shared, pow2=True)
+    rng = np.random.default_rng(i)
+    js = [int(rng.integers(x)) for x in ctx]
+    vs = np.full(c.N // block, 2.0 ** -5)
+    vs[[c.table[b, j] // block for b, j in enumerate(js)]] *= 2.0 ** -apart
+    _scaled(c, ks=2.0 ** -7, vs=vs)
+    parts = [_aimed(c, b, [(js[b], x)], 32.0) for b, x in enumerate(ctx)]
+    q, want, score = (np.concatenate([p[k] for p in parts]) for k in range(3))
+    q = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    for o, lse in (_decode(c, q, bf16=False), _extend(c, [x - 1 for x in ctx], q, False)[:2]):
+        _check(o, lse, want, score, c, 0.0 if apart <= 13 else 2.0 ** -23)
