@@ -77,4 +77,4 @@ def test_a_list_of_two_plans(Hq, H, d, first_end):
     then = c.plan(range(B, 2 * B), [n - 3 for n in lens[B:]], [end] * B, n_steps=3)
     assert then[1].n_work_tc > 0 and first[1].n_parts != then[1].n_parts
     _equal(torch, c.entries([(first, t) for t in range(steps)] + [(then, t) for t in range(3)] +
-                            [(first, steps - 1), (then, 0)]))
+                            [(first, steps - 1), (then, 0)]), graph=True)
