@@ -94,8 +94,8 @@ struct StoreArgs {
 
 // One slot a block: every row has its own scale.  A group of D / 8 lanes
 // takes kRows (token, head) rows, their K and V on their way together.  Two rows
-// and a grid of one pass: 8,017 tokens x 8 heads x 128 in 8.2 us, call after call
-// (one row and CTAs that loop, 9.1).
+// and a grid of one pass: 8,017 tokens x 8 heads x 128 in 7.8 us in a graph, 10.4
+// call after call (one row and CTAs that loop, 9.1 in a graph).
 template <int D>
 __global__ void __launch_bounds__(kThreads) store_rows_kernel(const StoreArgs a) {
   constexpr int L = D / 8;
@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const StoreArgs a)
 // before the run rounded again if the scale grew, then the run's codes.
 // Up to kHold rows stay in registers between the two passes, all of them on
 // their way at once; the rows of a longer run are read again, from L1 or L2.
-// 51,200 tokens x 4 heads x 256 in blocks of 16, L2 flushed: 62 us, 5.1 TB/s
-// (every row read twice and a run's slots one after the other, 82.6).
+// 51,200 tokens x 4 heads x 256 in blocks of 16: 62 us with L2 flushed, 5.1 TB/s
+// (every row read twice and a run's slots one after the other, 82.6), 57.4 call
+// after call.
 constexpr int kHold = 16;
 constexpr int kMaxBlock = 64;
 constexpr int kMaxWindow = 1024;

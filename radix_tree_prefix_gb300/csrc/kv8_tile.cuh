@@ -36,10 +36,12 @@
 // The roles run side by side, so the code of their loops together is the
 // working set of the instruction cache (32 KB): what is rare is kept rolled.
 // A tile takes about 1.3 us per key tile at both head dimensions (8,191 queries
-// over themselves, 32 / 8 heads, d = 128: 668 us, 43 % of the bf16 peak on the
+// over themselves, 32 / 8 heads, d = 128: 674 us, 42 % of the bf16 peak on the
 // causal products).  Issue and latency of the 15 warps' instructions set the
 // pace (a softmax warp works 2,050 clocks a key tile, 670 if it is alone), not
-// the tensor pipe (35 % busy) or shared memory (30 %).
+// the tensor pipe (35 % busy) or shared memory (30 %).  At 128 registers a thread
+// the d = 128 kernels spill a little (extend 12 bytes, with clusters 28; decode
+// 28, with clusters 32).
 // Every mbarrier wait is bounded; on a timeout the CTA sets an error bit,
 // drains its tensor-core work and frees TMEM before returning.
 #pragma once

@@ -59,7 +59,7 @@ void* tensor_map_encoder();
 // Error words of the kernels of each file: bit 0 = slot out of range.
 int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
-int32_t kv8_store_error_flags(bool clear);  // bits 0 and 6 of rx_device_check
+int32_t kv8_store_error_flags(bool clear);  // bits 0, 6 and 7 of rx_device_check
 int32_t kv8_attention_error_flags(bool clear);  // as tc_error_flags
 // One decode step in a single launch: the tensor-core tiles of the plan's
 // large items and the warp-role units of its small items (attention_tc.cu).
