@@ -812,7 +812,9 @@ typedef struct rx_kv8_pool_desc {
  * longer counts.  A token stored in a later slot keeps the block's rows
  * before it: the scale stays, or grows to hold the new row, and then those
  * earlier rows are rounded again under it (the rows behind are left as they
- * are).  Slots must be distinct, and the call's tokens of one block must
+ * are).  Slot 0 takes no token, so nothing opens the first block of 2 slots and
+ * more: a caller of its own slots there sets its scales to 0 first (the cache
+ * hands out none of them).  Slots must be distinct, and the call's tokens of one block must
  * stand next to one another in d_slots, in slot order, as the cache hands
  * them out: a token whose neighbour before it lies in the same block but not
  * in the slot before its own is skipped, with those that follow on from it,

@@ -78,3 +78,17 @@ def test_a_list_of_two_plans(Hq, H, d, first_end):
     assert then[1].n_work_tc > 0 and first[1].n_parts != then[1].n_parts
     _equal(torch, c.entries([(first, t) for t in range(steps)] + [(then, t) for t in range(3)] +
                             [(first, steps - 1), (then, 0)]), graph=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [dict(q_heads=64, kv_heads=2),
+                                   dict(q_heads=32, kv_heads=2, head_dim=256)])
+def test_flow_with_large_groups_matches_the_oracle(heads):
+    """The request flow where every tail is a tile: tolerances of the other
+    flows' comparisons with the oracle."""
+    pytest.importorskip("torch")
+    from parity_util import DeviceRun
+
+    from radix_tree_prefix_gb300 import workloads
+    wl = workloads.agent_loop(calls=6, preamble=300, lo=20, hi=400, decode_steps=7, **heads)
+    DeviceRun(wl, layers=[0], extend_tokens=5).assert_close()
