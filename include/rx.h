@@ -777,6 +777,184 @@ rx_status rx_kv_copy(const rx_pool_desc* src, const rx_pool_desc* dst,
                      int64_t n, rx_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Before the pool: the norm and position rotation of queries and keys
+ * ---------------------------------------------------------------------- */
+
+/* How the pairs of a head lie: pair i is elements (i, i + rot_dim / 2), or
+ * interleaved (2i, 2i + 1). */
+#define RX_ROPE_HALF 0
+#define RX_ROPE_INTERLEAVED 1
+#define RX_ROPE_MAX_PAIRS 128
+
+/* How frequencies f_i = base^(-2i / rot_dim), in radians a position, are
+ * scaled by `factor` >= 1 for contexts longer than the trained one:
+ *   NONE        as they are (factor is not read);
+ *   LINEAR      f / factor (positions interpolated);
+ *   BASE        base * factor^(rot_dim / (rot_dim - 2)) in base's place;
+ *   PARTS       f / factor for slow pairs, f for fast ones, and between them
+ *               f / factor * w + f * (1 - w) with w rising linearly with the
+ *               pair's index, from the pair that turns `high` times over
+ *               original_len to the one that turns `low` times (c(n) =
+ *               rot_dim ln(original_len / (2 pi n)) / (2 ln base), rounded
+ *               down for `high` and up for `low`, within [0, rot_dim - 1]);
+ *   WAVELENGTH  the same with w = 1 - (n_i - low) / (high - low) clamped to
+ *               [0, 1], n_i = original_len f_i / (2 pi) the pair's turns. */
+#define RX_ROPE_SCALE_NONE 0
+#define RX_ROPE_SCALE_LINEAR 1
+#define RX_ROPE_SCALE_BASE 2
+#define RX_ROPE_SCALE_PARTS 3
+#define RX_ROPE_SCALE_WAVELENGTH 4
+
+typedef struct rx_rope_config {
+  double base;         /* > 1                                              */
+  double factor;       /* >= 1                                             */
+  double original_len; /* PARTS, WAVELENGTH: trained context, > 0          */
+  double low, high;    /* PARTS, WAVELENGTH: 0 < low < high turns          */
+  double magnitude;    /* factor on cosine and sine; 0: the scaling's own
+                          (PARTS 0.1 ln(factor) + 1, else 1)               */
+  int32_t rot_dim;     /* leading elements of a head that are rotated: even,
+                          0 to 256                                         */
+  int32_t layout;      /* RX_ROPE_HALF or RX_ROPE_INTERLEAVED              */
+  int32_t scaling;     /* RX_ROPE_SCALE_*                                  */
+  int32_t reserved;    /* must be 0                                        */
+} rx_rope_config;
+
+/* A rotation as the kernels take it (host memory, passed by value to them).
+ * turns[i] is f_i / (2 pi) as a 64-bit fraction of a turn: any position's
+ * angle follows exactly, modulo a turn. */
+typedef struct rx_rope {
+  uint64_t turns[RX_ROPE_MAX_PAIRS];
+  float magnitude;
+  int32_t rot_dim;
+  int32_t layout;
+  int32_t reserved;
+} rx_rope;
+
+/* Host: fills *out from *cfg.  Errors: RX_ERR_INVALID (a NULL argument, a
+ * value outside the ranges above). */
+rx_status rx_rope_init(const rx_rope_config* cfg, rx_rope* out);
+
+/* RMS norm of each head's row: x / sqrt(mean(x^2) + eps) * w, or times 1 + w.
+ * Weights: device bf16 [head_dim], 16-byte aligned; a NULL weight leaves
+ * queries or keys as they are. */
+typedef struct rx_head_norm {
+  const void* d_q_weight;
+  const void* d_k_weight;
+  float eps;           /* >= 0                                             */
+  int32_t plus_one;    /* 1: the factor is 1 + w                           */
+} rx_head_norm;
+
+/* Queries and keys of T tokens normalised (norm; NULL: not) and rotated to
+ * their positions (rope; NULL: not), in fp32, rounded once to bf16.
+ * d_positions: device int32 [T], of any value (not read without a rotation).
+ * d_q: device bf16, token t's heads at d_q + t * q_stride elements,
+ * [num_q_heads][head_dim] side by side; d_k alike.  Strides are in elements,
+ * multiples of 8 and at least a token's heads, so the parts of one fused
+ * projection can be passed as they lie.  The outputs may be the inputs (same
+ * pointer and stride); they must not overlap them otherwise.  num_q_heads or
+ * num_kv_heads may be 0: that side's pointers and strides are not read.
+ * Bytes between the tokens' heads are left as they are.  Errors:
+ * RX_ERR_INVALID (head_dim not 128 or 256, T < 0 or of 2^31 and more, a
+ * rotation wider than the head, eps < 0, strides, NULL or not 16-byte aligned
+ * pointers); T = 0 launches nothing. */
+rx_status rx_qk_rope(const rx_rope* rope, const rx_head_norm* norm,
+                     int32_t head_dim, const int32_t* d_positions, int64_t T,
+                     const void* d_q, int64_t q_stride, int32_t num_q_heads,
+                     const void* d_k, int64_t k_stride, int32_t num_kv_heads,
+                     void* d_q_out, int64_t q_out_stride, void* d_k_out,
+                     int64_t k_out_stride, rx_stream_t stream);
+
+/* rx_qk_rope and rx_kv_store in one pass: the queries go to d_q_out, the
+ * normalised and rotated keys and the values as they are to their slots of
+ * the pool.  d_slots as rx_kv_store (distinct; a slot outside [1, num_slots)
+ * stores nothing and is reported by rx_device_check, bit 0; its token's
+ * queries are written all the same).  num_q_heads = 0: keys and values only.
+ * Errors: those of both. */
+rx_status rx_qkv_store(const rx_pool_desc* pool, int32_t layer,
+                       const rx_rope* rope, const rx_head_norm* norm,
+                       const int32_t* d_positions, const int32_t* d_slots,
+                       int64_t T, const void* d_q, int64_t q_stride,
+                       int32_t num_q_heads, const void* d_k, int64_t k_stride,
+                       const void* d_v, int64_t v_stride, void* d_q_out,
+                       int64_t q_out_stride, rx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention with modified scores over the bf16 pool
+ * ---------------------------------------------------------------------- */
+
+/* Query i (its position in the request) scores key j by
+ *   s = softcap * tanh(scale * q.k / softcap) - slope_h * |i - j|
+ * and sees it if  (j <= i or j < bidir_end)  and  i - j < window  and
+ * j >= key_begin.  Each part is left out when its field is 0 or NULL.  A query
+ * that sees no key gets zeros and lse = -inf. */
+typedef struct rx_score_mod {
+  float softcap;              /* > 0; 0: scores are not capped              */
+  int32_t window;             /* keys back that a query sees, itself
+                                 counted; 0: all                           */
+  const float* d_slopes;      /* device fp32 [Hq]                          */
+  const int32_t* d_key_begin; /* device int32 [queries]: the first key each
+                                 query sees (its document's first)         */
+  const int32_t* d_bidir_end; /* extend: device int32 [R]: request r's keys
+                                 before it are seen by all its queries, also
+                                 by those before them (cut to its tokens)  */
+  const int32_t* d_ctx_len;   /* decode: device int32 [B], each request's
+                                 context length at the plan's first step    */
+} rx_score_mod;
+
+/* Output types of attention that has a choice. */
+#define RX_OUT_F32 0
+#define RX_OUT_BF16 1
+
+/* rx_extend_attention with modified scores (mod NULL: none), into fp32 or
+ * bf16 (out_type).  Scores, statistics and sums are held in fp32; softmax
+ * weights are rounded to bf16 for the product with V.  Scores must lie within
+ * +-1e29.  Keys that no query of a tile of 128 query rows sees are not read;
+ * the K and V rows that a tile reads must be finite (a masked key weighs 0, and
+ * 0 times an infinity would reach its tile's other queries).  d_ctx_len is
+ * not read.  Errors: RX_ERR_INVALID as rx_extend_attention, for an unknown
+ * out_type, softcap < 0 or not finite, window < 0. */
+rx_status rx_extend_attention_mod(
+    const rx_pool_desc* pool, int32_t layer, const void* d_q,
+    int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,
+    const int32_t* d_req_rows, const int32_t* d_prefix_len,
+    const int32_t* d_qo_indptr, const int32_t* d_tile_indptr, int32_t R,
+    int64_t num_tiles, float scale, const rx_score_mod* mod, void* d_out,
+    int32_t out_type, float* d_lse, rx_stream_t stream);
+
+/* rx_plan_decode_steps for attention with a window (0: none): keys that no
+ * step's window of any request reaches are left out of the plan, and a
+ * request whose window ends before a shared segment is not among the
+ * segment's members.  distinct_kv_tokens counts the keys that step 0 reads.
+ * Such a plan serves rx_decode_attention_mod with this window or a
+ * smaller one only.  Errors: as rx_plan_decode_steps, and window < 0. */
+rx_status rx_plan_decode_window(const rx_cache* cache, int32_t B,
+                                int32_t n_steps, int32_t window,
+                                const rx_node* prompt_node,
+                                const int32_t* ctx_len,
+                                const int32_t* req_rows, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim,
+                                int32_t* plan, int64_t plan_cap,
+                                rx_decode_plan_info* out_info);
+
+/* rx_decode_attention with modified scores (mod NULL: none), into fp32 or
+ * bf16, and with the drafts of a rx_verify_rows plan as its batch,
+ * rx_verify_attention.  Request b's query is at position d_ctx_len[b] + step
+ * - 1 (drafts: out_ctx_len of rx_verify_rows).  step: the step of a plan of
+ * several (else 0); its tokens must be stored first.  d_key_begin is [B];
+ * d_bidir_end is not read (every key of a context lies before its query).
+ * d_ctx_len is needed with a window or slopes.  The K and V rows of the plan's
+ * keys must be finite.  Numerics as rx_extend_attention_mod.  Errors:
+ * RX_ERR_INVALID as rx_decode_attention and rx_extend_attention_mod, for
+ * step < 0 and a missing d_ctx_len. */
+rx_status rx_decode_attention_mod(
+    const rx_pool_desc* pool, int32_t layer, const void* d_q,
+    int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,
+    const int32_t* d_plan, const rx_decode_plan_info* info, int32_t B,
+    int32_t step, float scale, const rx_score_mod* mod, void* d_out,
+    int32_t out_type, float* d_lse, void* d_workspace, size_t workspace_bytes,
+    rx_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * The 8-bit KV pool: keys and values held as e4m3 codes (sign, 4 exponent
  * and 3 mantissa bits, largest value 448) with one fp32 scale for each KV
  * head and block of `block` consecutive slots.  A key is its code times its
@@ -839,10 +1017,6 @@ rx_status rx_kv8_store(const rx_kv8_pool_desc* pool, int32_t layer,
 rx_status rx_kv8_load(const rx_kv8_pool_desc* pool, int32_t layer,
                       const int32_t* d_slots, void* d_k, void* d_v, int64_t T,
                       rx_stream_t stream);
-
-/* Output types of the 8-bit pool's attention. */
-#define RX_OUT_F32 0
-#define RX_OUT_BF16 1
 
 /* rx_extend_attention over an 8-bit pool: the same queries, tables, tile
  * schedule and causal rule.  d_out is fp32 or bf16 (out_type) [total_q][Hq]
@@ -922,8 +1096,8 @@ rx_status rx_host_alloc(size_t bytes, void** out);
 rx_status rx_host_free(void* p);
 
 /* Synchronise the current device and read the kernels' error words (then
- * clear them).  *out_flags (may be NULL): bit 0 = rx_kv_store, rx_kv8_store
- * or rx_kv8_load met a slot outside [1, num_slots) and skipped it; bit 1 = an attention kernel
+ * clear them).  *out_flags (may be NULL): bit 0 = rx_kv_store, rx_qkv_store,
+ * rx_kv8_store or rx_kv8_load met a slot outside [1, num_slots) and skipped it; bit 1 = an attention kernel
  * read a slot outside [0, num_slots) from req_to_token and used slot 0
  * instead; bit 2 = a tensor-core kernel gave up a barrier wait after its
  * time limit (about 2 s) and returned without results (every output of

@@ -112,6 +112,15 @@ struct TcArgs {
   const bf16* k_new;       // bf16 [B][Hkv][D] of the step's tokens, or NULL
   const bf16* v_new;
   const int32_t* slots_new;
+  // modified scores (the MOD kernels only; rx_score_mod)
+  float cap_in;            // scale / softcap, 0: no cap
+  float cap_out;           // softcap * log2(e)
+  int window;              // 0: none
+  const float* slopes;
+  const int32_t* key_begin;
+  const int32_t* bidir_end;
+  const int32_t* ctx_len;
+  int out_bf16;
 };
 
 struct TileDesc {
@@ -119,9 +128,10 @@ struct TileDesc {
   int key_begin, key_end, nomask_end, n_rows;
   int gr0, q_base, prefix;
   int member_off, part_base;
+  int bidir;  // MOD: keys before it are seen by every row
 };
 
-template <bool DECODE>
+template <bool DECODE, bool MOD>
 __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
   TileDesc t;
   if constexpr (DECODE) {
@@ -133,7 +143,7 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
     t.part_base = w[5];
     t.n_rows = w[6];
     t.nomask_end = t.key_end;
-    t.gr0 = t.q_base = t.prefix = 0;
+    t.gr0 = t.q_base = t.prefix = t.bidir = 0;
   } else {
     const int tile = a.num_tiles - 1 - bx;  // heaviest first
     // the request of this tile: the last r with tile_indptr[r] <= tile, found
@@ -166,6 +176,19 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
     t.key_end = t.prefix + (t.gr0 + t.n_rows - 1) / G + 1;
     t.nomask_end = t.prefix + t.gr0 / G + 1;
     t.member_off = t.part_base = 0;
+    if constexpr (MOD) {
+      // the keys that some row of the tile sees lie in [key_begin, key_end)
+      const int tok0 = t.gr0 / G, tok1 = (t.gr0 + t.n_rows - 1) / G;
+      t.bidir = a.bidir_end ? min(__ldg(a.bidir_end + lo), t.prefix + s_r) : 0;
+      t.key_end = max(t.key_end, t.bidir);
+      if (a.window > 0) t.key_begin = max(0, t.prefix + tok0 - a.window + 1);
+      if (a.key_begin) {
+        int least = INT32_MAX;
+        for (int tok = tok0 + ln; tok <= tok1; tok += 32)
+          least = min(least, __ldg(a.key_begin + t.q_base + tok));
+        t.key_begin = max(t.key_begin, __reduce_min_sync(0xffffffffu, least));
+      }
+    }
   }
   return t;
 }
@@ -291,7 +314,49 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-template <int D, bool DECODE>
+// Modified scores (rx_score_mod), in log2 units: what a row adds to a raw
+// score, and the keys [lo, lim) that it sees.
+constexpr float kMaskedRow = -1.0e29f;  // a row whose maximum is not above it saw no key
+struct RowMod {
+  int lo = 0;
+  float slope = 0.f;  // slope of the row's head times log2(e)
+  float pos = 0.f;    // the query's position
+};
+
+// position `pos`, first key `begin` of its own (if any)
+__device__ __forceinline__ RowMod row_mod(const TcArgs& a, int64_t qi, int head, int pos) {
+  RowMod r;
+  if (a.window > 0) r.lo = max(0, pos - a.window + 1);
+  if (a.key_begin) r.lo = max(r.lo, __ldg(a.key_begin + qi));
+  if (a.slopes) r.slope = __ldg(a.slopes + head) * kLog2e;
+  r.pos = float(pos);
+  return r;
+}
+
+// tanh(u) for |u| <= 1: u times the polynomial in u^2 of degree 6 that is nearest
+// to tanh(u) / u there by relative error (Remez exchange): 5e-8 in exact
+// arithmetic, 1.6e-7 in fp32.
+__device__ __forceinline__ float tanh_small(float u) {
+  const float v = u * u;
+  float p = fmaf(0.0010410226f, v, -0.006203379f);
+  p = fmaf(p, v, 0.02028998f);
+  p = fmaf(p, v, -0.05345703f);
+  p = fmaf(p, v, 0.13325204f);
+  p = fmaf(p, v, -0.3333284f);
+  p = fmaf(p, v, 0.99999994f);
+  return u * p;
+}
+// tanh(u) = 1 - 2 / (1 + e^2u), off by some 2^-22 at most: for |u| > 1
+__device__ __forceinline__ float tanh_large(float u) {
+  return fmaf(-2.f, __fdividef(1.f, 1.f + rxk::fast_exp2(u * (2.f * kLog2e))), 1.f);
+}
+// softcap * tanh(scale * s / softcap) * log2(e)
+__device__ __forceinline__ float capped(const TcArgs& a, float s) {
+  const float u = s * a.cap_in;
+  return a.cap_out * (fabsf(u) <= 1.f ? tanh_small(u) : tanh_large(u));
+}
+
+template <int D, bool DECODE, bool MOD>
 __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk,
                                          const CUtensorMap* tmv, uint8_t* smem_raw, int bx,
                                          int kvh) {
@@ -336,8 +401,9 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const TileDesc t = describe<DECODE>(a, bx);
-  const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
+  const TileDesc t = describe<DECODE, MOD>(a, bx);
+  const int n_tiles =
+      MOD && t.key_begin >= t.key_end ? 0 : (t.key_end - t.key_begin + BN - 1) / BN;
   // Softmax threads: the query row of their TMEM lane, and the gather of
   // half of Q row i, issued before the barriers and TMEM are set up so the
   // copies overlap that start-up (nothing else uses the Q buffer yet; the
@@ -351,6 +417,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   int64_t qi = 0, part = 0;
   int head = 0, lim = t.key_end;
   bool valid = false;
+  RowMod rm;
   if (warp < 8) {
     valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
     if (valid) row_info<DECODE>(a, t, kvh, row, qi, head, part, lim);
@@ -372,6 +439,13 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
     // stream are done; with early inputs the queries are complete already
     // and only the partial writes wait
     if (!DECODE || !a.early_inputs) rxk::griddep_wait();
+    if constexpr (MOD) {
+      if (valid) {
+        const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
+        if (!DECODE) lim = max(lim, t.bidir);
+        rm = row_mod(a, qi, head, pos);
+      }
+    }
     // chunks [8 w, 8 w + 8) of Q row i (zeros past the tile's rows) while
     // the loader warps already stream the first K/V tiles
     const bf16* src = a.q + (gqi * a.hq + ghead) * D;
@@ -641,6 +715,12 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
     tc::mbar_arrive(BAR_Q);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
+    // MOD: keys [lo_max, lim_min) are seen by every row of the warp
+    int lo_max = 0, lim_min = 0;
+    if constexpr (MOD) {
+      lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
+      lim_min = __reduce_min_sync(0xffffffffu, lim);
+    }
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % NB;  // S buffer
       // waits are made warp-uniform before any warp-collective tcgen05 op
@@ -651,7 +731,8 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       }
       tc::tc_fence_after();
       const int k0 = t.key_begin + j * BN + wg * HALF;  // first key of this half
-      const bool need_mask = k0 + HALF > t.nomask_end;
+      const bool need_mask =
+          MOD ? k0 < lo_max || k0 + HALF > lim_min : k0 + HALF > t.nomask_end;
       uint32_t sr[HALF];
       tc::tmem_ld_row<HALF>(tl + uint32_t(s * BN + wg * HALF), sr);
       tc::tmem_ld_wait();
@@ -662,7 +743,44 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       float mx8[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) mx8[u] = kMasked;
-      if (need_mask) {
+      if constexpr (MOD) {
+        // the raw scores become modified ones in log2 units, in place
+        if (a.cap_in != 0.f) {
+          float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < HALF; ++e)
+            am[e & 3] = fmaxf(am[e & 3], fabsf(__uint_as_float(sr[e])));
+          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+          if (__all_sync(0xffffffffu, most * fabsf(a.cap_in) <= 1.f)) {
+#pragma unroll
+            for (int e = 0; e < HALF; ++e)
+              sr[e] = __float_as_uint(a.cap_out *
+                                      tanh_small(__uint_as_float(sr[e]) * a.cap_in));
+          } else {
+#pragma unroll
+            for (int e = 0; e < HALF; ++e)
+              sr[e] = __float_as_uint(capped(a, __uint_as_float(sr[e])));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < HALF; ++e)
+            sr[e] = __float_as_uint(__uint_as_float(sr[e]) * a.scale_log2);
+        }
+        if (a.slopes) {
+          const float away = float(k0) - rm.pos;
+#pragma unroll
+          for (int e = 0; e < HALF; ++e)
+            sr[e] = __float_as_uint(
+                fmaf(-rm.slope, fabsf(away + float(e)), __uint_as_float(sr[e])));
+        }
+      }
+      if (MOD && need_mask) {
+#pragma unroll
+        for (int e = 0; e < HALF; ++e) {
+          if (k0 + e >= lim || k0 + e < rm.lo) sr[e] = __float_as_uint(kMasked);
+          mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sr[e]));
+        }
+      } else if (need_mask) {
 #pragma unroll
         for (int e = 0; e < HALF; ++e) {
           if (k0 + e >= lim) sr[e] = __float_as_uint(kMasked);
@@ -684,7 +802,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
         break;
       }
       const float mx_other = xch[((j & 1) * 2 + (1 - wg)) * BM + i];
-      const float mx = a.scale_log2 * fmaxf(mx_half, mx_other);
+      const float mx = (MOD ? 1.f : a.scale_log2) * fmaxf(mx_half, mx_other);
       const float m_new = fmaxf(m_ref, mx);
       if (j == 0) {
         m_ref = m_new;
@@ -717,7 +835,9 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
           }
         }
       }
-      const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+      // MOD: a row that saw no key yet weighs its masked ones 0
+      const float m_use = MOD ? (m_ref <= kMaskedRow ? 0.f : m_ref)
+                              : (m_ref == -INFINITY) ? 0.f : m_ref;
       float l8[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) l8[u] = 0.f;
@@ -733,6 +853,15 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
           // would cost up to 1% per weight on peaked rows.  The row sum adds
           // exactly the rounded values in fp32, in eight independent partial
           // sums.
+          if constexpr (MOD) {
+            // the row sum adds the weights before their rounding: lse is then
+            // good to fp32, and o to the roundings of its weights
+            const float p0 = rxk::fast_exp2(__uint_as_float(sr[cc * 32 + e]) - m_use);
+            const float p1 = rxk::fast_exp2(__uint_as_float(sr[cc * 32 + e + 1]) - m_use);
+            l8[(e >> 1) & 7] += p0 + p1;
+            pk[e >> 1] = rxk::pack_bf16(p0, p1);
+            continue;
+          }
           const float x0 = fmaf(__uint_as_float(sr[cc * 32 + e]), a.scale_log2, -m_use);
           const float x1 = fmaf(__uint_as_float(sr[cc * 32 + e + 1]), a.scale_log2, -m_use);
           const uint32_t h = rxk::pack_bf16(rxk::fast_exp2(x0), rxk::fast_exp2(x1));
@@ -771,7 +900,9 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
         dst = a.ws_o + (part * a.hq + head) * D;
         lse_dst = a.ws_lse + part * a.hq + head;
       } else {
-        dst = a.out + (qi * a.hq + head) * D;
+        dst = a.out + (qi * a.hq + head) * D;  // MOD: of bf16 with out_bf16
+        if (MOD && a.out_bf16)
+          dst = reinterpret_cast<float*>(reinterpret_cast<bf16*>(a.out) + (qi * a.hq + head) * D);
         lse_dst = a.lse + qi * a.hq + head;
       }
       // Warpgroup w owns output columns [w D/2, (w+1) D/2).  Its rows go
@@ -799,16 +930,35 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       __syncwarp();
       const int qrow = (warp & 3) * 32;  // first row of this warp's quadrant
       const unsigned long long my_dst =
-          valid ? reinterpret_cast<unsigned long long>(dst + wg * HC) : 0ull;
+          valid ? (MOD && !DECODE && a.out_bf16
+                       ? reinterpret_cast<unsigned long long>(reinterpret_cast<bf16*>(dst) + wg * HC)
+                       : reinterpret_cast<unsigned long long>(dst + wg * HC))
+                : 0ull;
 #pragma unroll 4
       for (int k = 0; k < LPR; ++k) {
         const int idx = k * 32 + lane;
         const int rr = idx / LPR, c4 = idx - rr * LPR;  // row within the quadrant, float4
         const unsigned long long rd = __shfl_sync(0xffffffffu, my_dst, rr);
         const float4 v = *reinterpret_cast<const float4*>(stage + (qrow + rr) * PITCH + c4 * 16);
+        if (MOD && !DECODE && a.out_bf16) {
+          if (rd)
+            reinterpret_cast<uint2*>(rd)[c4] =
+                make_uint2(rxk::pack_bf16(v.x, v.y), rxk::pack_bf16(v.z, v.w));
+          continue;
+        }
         if (rd) reinterpret_cast<float4*>(rd)[c4] = v;
       }
-      if (valid && wg == 0) *lse_dst = m_ref * kLn2 + logf(l_all);
+      if (valid && wg == 0)
+        *lse_dst = MOD && l_all == 0.f ? -INFINITY : m_ref * kLn2 + logf(l_all);
+    } else if (MOD && !DECODE && n_tiles <= 0 && valid) {
+      // no row of the tile sees a key
+      const int64_t at = (qi * a.hq + head) * D + wg * (D / 2);
+      uint4* dst = a.out_bf16 ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
+                              : reinterpret_cast<uint4*>(a.out + at);
+      const int n = a.out_bf16 ? D / 16 : D / 8;
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (wg == 0) a.lse[qi * a.hq + head] = -INFINITY;
     } else if (DECODE && n_tiles <= 0 && valid) {
       // keys that a later step of the plan brings: an empty partial row
       float4* dst = reinterpret_cast<float4*>(a.ws_o + (part * a.hq + head) * D + wg * (D / 2));
@@ -832,7 +982,8 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
 // ones and the last wave is short; otherwise CTA c takes head c / tiles, so
 // the CTAs resident at one time read the keys of one head and those stay in
 // L2.
-template <int D>
+// MOD: with modified scores (rx_score_mod).
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads3, 1)
     attn_tc3_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
@@ -840,9 +991,9 @@ __global__ void __launch_bounds__(kThreads3, 1)
   const int c = int(blockIdx.x);
   if (a.heads_interleaved) {
     const int hkv = a.hq / a.group;
-    tc_tile3<D, false>(a, &tmk, &tmv, smem_raw, c / hkv, c - (c / hkv) * hkv);
+    tc_tile3<D, false, MOD>(a, &tmk, &tmv, smem_raw, c / hkv, c - (c / hkv) * hkv);
   } else {
-    tc_tile3<D, false>(a, &tmk, &tmv, smem_raw, c % a.num_tiles, c / a.num_tiles);
+    tc_tile3<D, false, MOD>(a, &tmk, &tmv, smem_raw, c % a.num_tiles, c / a.num_tiles);
   }
 }
 
@@ -913,7 +1064,7 @@ __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
   if (n.stage < 3) ++n.stage;
 }
 
-template <int NR, int D>
+template <int NR, int D, bool MOD>
 __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_t* slot_buf,
                                           uint32_t& gstep, const NextUnit& cur, NextUnit& nxt) {
   using Cfg = PipeCfg<D>;
@@ -1060,6 +1211,23 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     }
   }
 
+  // MOD: what the scores of rows nt*8 + 2c + e add, and the first key they see
+  RowMod rm[NR][2];
+  if constexpr (MOD) {
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * c + e;
+        if (r < n_rows) {
+          const int u = r / G;
+          const int64_t b = a.members[member_off + u];
+          const int pos = a.ctx_len ? __ldg(a.ctx_len + b) + a.step - 1 : 0;
+          rm[nt][e] = row_mod(a, b, kvh * G + (r - u * G), pos);
+        }
+      }
+  }
+
   // ldmatrix lane addresses: K (A of S^T, keys x d) and V^T (A of O^T, d x keys)
   const uint32_t k_lane = uint32_t(((lane & 7) + ((lane >> 3) & 1) * 8) * kRowPitch + (lane >> 4) * 16);
   const uint32_t v_lane =
@@ -1101,10 +1269,21 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
+      if constexpr (MOD) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + 8 * (e >> 1);
+          const RowMod& r = rm[nt][e & 1];
+          float y = a.cap_in != 0.f ? capped(a, sacc[nt][e]) : sacc[nt][e] * a.scale_log2;
+          y = fmaf(-r.slope, fabsf(float(key) - r.pos), y);
+          x[nt][e] = key < ke && key >= r.lo ? y : -INFINITY;
+        }
+      } else {
       x[nt][0] = in0 ? sacc[nt][0] * a.scale_log2 : -INFINITY;
       x[nt][1] = in0 ? sacc[nt][1] * a.scale_log2 : -INFINITY;
       x[nt][2] = in1 ? sacc[nt][2] * a.scale_log2 : -INFINITY;
       x[nt][3] = in1 ? sacc[nt][3] * a.scale_log2 : -INFINITY;
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         grow |= fmaxf(x[nt][e], x[nt][2 + e]) > m_ref[nt][e] + kRescaleThreshold;
@@ -1144,6 +1323,13 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float m_use = m_ref[nt][e] == -INFINITY ? 0.f : m_ref[nt][e];
+        if constexpr (MOD) {
+          const float p0 = rxk::fast_exp2(x[nt][e] - m_use);
+          const float p1 = rxk::fast_exp2(x[nt][2 + e] - m_use);
+          pk[nt][e] = rxk::pack_bf16(p0, p1);
+          l_run[nt][e] += p0 + p1;
+          continue;
+        }
         uint32_t h;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
             : "=r"(h)
@@ -1230,7 +1416,7 @@ struct Fused {
   static_assert(SMEM <= 227 * 1024, "fused decode CTA fits in shared memory");
 };
 
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
     decode_fused_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
@@ -1240,7 +1426,7 @@ __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
   const int cta = int(blockIdx.x) - a.n_warp_first;
   if (cta >= 0 && cta < a.n_tc_ctas) {
     const int hkv = a.hq / a.group;
-    tc_tile3<D, true>(a, &tmk, &tmv, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
+    tc_tile3<D, true, MOD>(a, &tmk, &tmv, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
   }
   if (threadIdx.x >= kPipeWarps * 32) return;  // the warp role uses the first six warps
   // tiles_leave: in a run of steps a tile CTA leaves its SM to the next
@@ -1264,9 +1450,9 @@ __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
     nxt.stage = 0;
     const int rows = cur.word(6);
     if (rows <= 8) {
-      pipe_unit<1, D>(a, ring, slot_buf, gstep, cur, nxt);
+      pipe_unit<1, D, MOD>(a, ring, slot_buf, gstep, cur, nxt);
     } else if constexpr (D == 128) {
-      pipe_unit<2, D>(a, ring, slot_buf, gstep, cur, nxt);
+      pipe_unit<2, D, MOD>(a, ring, slot_buf, gstep, cur, nxt);
     } else if (lane == 0) {
       atomicOr(&g_tc_error, 1);  // the plan gives head_dim 256 no such item
     }
@@ -1363,19 +1549,29 @@ rx_status ensure_smem(std::atomic<bool> (&done)[kMaxDevices], K* kernel, int byt
   return RX_OK;
 }
 
-template <int D>
+void set_mod(TcArgs* a, const rx_score_mod& m, float scale) {
+  a->cap_in = m.softcap > 0.f ? scale / m.softcap : 0.f;
+  a->cap_out = m.softcap * kLog2e;
+  a->window = m.window;
+  a->slopes = m.d_slopes;
+  a->key_begin = m.d_key_begin;
+  a->bidir_end = m.d_bidir_end;
+  a->ctx_len = m.d_ctx_len;
+}
+
+template <int D, bool MOD>
 rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, int32_t layer, unsigned gx,
                         unsigned gy, cudaStream_t s) {
   using Lo = Layout3<D>;
   static std::atomic<bool> configured[kMaxDevices];
-  const rx_status cs = ensure_smem(configured, attn_tc3_kernel<D>, Lo::BYTES);
+  const rx_status cs = ensure_smem(configured, attn_tc3_kernel<D, MOD>, Lo::BYTES);
   if (cs != RX_OK) return cs;
   const CUtensorMap *tmk, *tmv;
   if (!pool_maps(pool, Lo::BN, &tmk, &tmv))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   a.tma_row_base = int64_t(layer) * pool->num_kv_heads * pool->num_slots;
   a.tma_head_rows = pool->num_slots;
-  attn_tc3_kernel<D><<<dim3(gx * gy), kThreads3, Lo::BYTES, s>>>(a, *tmk, *tmv);
+  attn_tc3_kernel<D, MOD><<<dim3(gx * gy), kThreads3, Lo::BYTES, s>>>(a, *tmk, *tmv);
   return rx_internal::launch_status("extend attention (tcgen05)");
 }
 
@@ -1414,7 +1610,7 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                        int64_t n_tc, const int32_t* d_members, float scale, float* ws_o,
                        float* ws_lse, int32_t* unit_counter, int step, const void* k_new,
                        const void* v_new, const int32_t* slots_new, cudaStream_t stream,
-                       bool early_inputs) {
+                       bool early_inputs, const rx_score_mod* mod) {
   const int D = pool->head_dim;
   if (D != 128 && D != 256) return set_error(RX_ERR_INVALID, "decode needs head_dim 128 or 256");
   const int64_t hkv = pool->num_kv_heads;
@@ -1464,12 +1660,14 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
   a.k_new = static_cast<const bf16*>(k_new);
   a.v_new = static_cast<const bf16*>(v_new);
   a.slots_new = slots_new;
+  if (mod) set_mod(&a, *mod, scale);
   a.tma_row_base = int64_t(layer) * hkv * pool->num_slots;
   a.tma_head_rows = pool->num_slots;
-  static std::atomic<bool> configured128[kMaxDevices], configured256[kMaxDevices];
-  const rx_status cs =
-      D == 128 ? ensure_smem(configured128, decode_fused_kernel<128>, Fused<128>::SMEM)
-               : ensure_smem(configured256, decode_fused_kernel<256>, Fused<256>::SMEM);
+  static std::atomic<bool> configured[2][2][kMaxDevices];  // [head_dim 256][mod]
+  auto* kernel = D == 128 ? (mod ? decode_fused_kernel<128, true> : decode_fused_kernel<128, false>)
+                          : (mod ? decode_fused_kernel<256, true> : decode_fused_kernel<256, false>);
+  const rx_status cs = ensure_smem(configured[D == 256][mod != nullptr], kernel,
+                                   D == 128 ? Fused<128>::SMEM : Fused<256>::SMEM);
   if (cs != RX_OK) return cs;
   const CUtensorMap *tmk, *tmv;
   if (!pool_maps(pool, D == 128 ? 128 : 64, &tmk, &tmv))
@@ -1484,10 +1682,7 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (D == 128)
-    cudaLaunchKernelEx(&cfg, decode_fused_kernel<128>, a, *tmk, *tmv);
-  else
-    cudaLaunchKernelEx(&cfg, decode_fused_kernel<256>, a, *tmk, *tmv);
+  cudaLaunchKernelEx(&cfg, kernel, a, *tmk, *tmv);
   return launch_status("decode attention (fused)");
 }
 
@@ -1496,7 +1691,8 @@ rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const voi
                               int64_t row_stride, const int32_t* d_req_rows,
                               const int32_t* d_prefix_len, const int32_t* d_qo_indptr,
                               const int32_t* d_tile_indptr, int32_t R, int64_t num_tiles,
-                              float scale, float* d_out, float* d_lse, cudaStream_t stream) {
+                              float scale, float* d_out, float* d_lse, cudaStream_t stream,
+                              const rx_score_mod* mod, bool out_bf16) {
   const int D = pool->head_dim;
   TcArgs a{};
   a.q = static_cast<const bf16*>(d_q);
@@ -1527,9 +1723,15 @@ rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const voi
       kv_row_bytes <= kExtendInterleaveKvBytes;
   a.out = d_out;
   a.lse = d_lse;
-  if (D == 128)
-    return launch_extend<128>(a, pool, layer, unsigned(num_tiles), pool->num_kv_heads, stream);
-  return launch_extend<256>(a, pool, layer, unsigned(num_tiles), pool->num_kv_heads, stream);
+  const unsigned gx = unsigned(num_tiles), gy = unsigned(pool->num_kv_heads);
+  if (mod) {
+    set_mod(&a, *mod, scale);
+    a.out_bf16 = out_bf16;
+    return D == 128 ? launch_extend<128, true>(a, pool, layer, gx, gy, stream)
+                    : launch_extend<256, true>(a, pool, layer, gx, gy, stream);
+  }
+  return D == 128 ? launch_extend<128, false>(a, pool, layer, gx, gy, stream)
+                  : launch_extend<256, false>(a, pool, layer, gx, gy, stream);
 }
 
 }  // namespace rx_internal

@@ -798,6 +798,29 @@ int32_t kv8_attention_error_flags(bool clear) {
   return v;
 }
 
+rx_status merge_parts(int head_dim, const int32_t* indptr, const int32_t* parts, const float* ws_o,
+                      const float* ws_lse, int hq, int B, void* d_out, bool out_bf16, float* d_lse,
+                      bool chained, cudaStream_t stream, const char* what) {
+  const int64_t rows = int64_t(B) * hq;
+  const bool wide = rows < int64_t(sm_count()) * 16;  // eight warps a row
+  const int64_t ctas = wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
+  if (ctas > INT32_MAX) return set_error(RX_ERR_INVALID, "decode merge: too many rows");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  auto* merge = head_dim == 128 ? (wide ? merge8_kernel<128, 8> : merge8_kernel<128, 1>)
+                                : (wide ? merge8_kernel<256, 8> : merge8_kernel<256, 1>);
+  cudaLaunchKernelEx(&cfg, merge, indptr, parts, ws_o, ws_lse, hq, B, d_out, out_bf16 ? 1 : 0,
+                     d_lse);
+  return launch_status(what);
+}
+
 }  // namespace rx_internal
 
 namespace {
@@ -1054,24 +1077,13 @@ rx_status decode8(
     st = rx_internal::launch_status("rx_kv8_decode_attention: streams");
     if (st != RX_OK) return st;
   }
-  cfg.dynamicSmemBytes = 0;
   // launched while the kernels before it run; it waits on the device for their
   // end (a plan without items has none, and its lists may be behind the
   // caller's last kernel)
-  cfg.numAttrs = info->n_work > 0 ? 1 : 0;
-  const int64_t rows = int64_t(B) * num_q_heads;
-  const bool wide = rows < sms * 16;  // eight warps a row
-  cfg.gridDim = dim3(unsigned(wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  const int32_t* indptr = d_plan + info->off_req_part_indptr;
-  const int32_t* parts = d_plan + info->off_req_parts;
-  const float* wo = a.ws_o;
-  const float* wl = a.ws_lse;
-  auto* merge = D == 128 ? (wide ? merge8_kernel<128, 8> : merge8_kernel<128, 1>)
-                         : (wide ? merge8_kernel<256, 8> : merge8_kernel<256, 1>);
-  cudaLaunchKernelEx(&cfg, merge, indptr, parts, wo, wl, int(num_q_heads), int(B), d_out,
-                     int(a.out_bf16), d_lse);
-  return rx_internal::launch_status("rx_kv8_decode_attention: merge");
+  return rx_internal::merge_parts(D, d_plan + info->off_req_part_indptr,
+                                  d_plan + info->off_req_parts, a.ws_o, a.ws_lse, num_q_heads, B,
+                                  d_out, a.out_bf16, d_lse, info->n_work > 0, s,
+                                  "rx_kv8_decode_attention: merge");
 }
 
 }  // namespace

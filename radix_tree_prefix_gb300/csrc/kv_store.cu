@@ -290,7 +290,8 @@ extern "C" rx_status rx_device_check(int32_t* out_flags) {
   const int32_t tcf = rx_internal::tc_error_flags(true) |
                       rx_internal::kv8_attention_error_flags(true);
   int32_t f = rx_internal::kv_store_error_flags(true) |
-              rx_internal::kv8_store_error_flags(true) | ((tcf & 7) << 1);
+              rx_internal::kv8_store_error_flags(true) | rx_internal::rope_error_flags(true) |
+              ((tcf & 7) << 1);
   if (out_flags) *out_flags = f;
   if (f)
     return rx_internal::set_error(RX_ERR_CUDA,

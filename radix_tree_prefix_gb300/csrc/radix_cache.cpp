@@ -840,7 +840,9 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
                                   const rx_node* prompt_node, const int32_t* ctx_len,
                                   const int32_t* req_rows, int32_t num_q_heads,
                                   int32_t num_kv_heads, int32_t head_dim, int32_t* plan,
-                                  int64_t plan_cap, rx_decode_plan_info* info) {
+                                  int64_t plan_cap, rx_decode_plan_info* info,
+                                  int32_t window = 0) {
+  if (window < 0) return fail(RX_ERR_INVALID, "rx_plan_decode_window: window < 0");
   if (n_steps < 1) return fail(RX_ERR_INVALID, "rx_plan_decode: n_steps < 1");
   if (!c || B < 0 || !info || (B && (!prompt_node || !ctx_len || !req_rows)))
     return fail(RX_ERR_INVALID, "rx_plan_decode: bad argument");
@@ -913,6 +915,32 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
       segs[last_shared].grow = pos;  // (ctx_len >= 1, so there is a shared segment)
     }
     if (last > pos) segs.push_back(Seg{req_rows[b], pos, last, {b}, int64_t(ctx_len[b])});
+  }
+  // A window's first key at step 0, the earliest of its steps: a segment keeps
+  // the members whose window reaches into it, and its keys from their earliest
+  // one on.  (A request's newest token is always within its window.)
+  if (window > 0) {
+    size_t kept = 0;
+    n_shared = 0;
+    for (size_t i = 0; i < segs.size(); ++i) {
+      Seg& s = segs[i];
+      size_t n = 0;
+      int64_t first = s.ke;
+      for (int32_t b : s.members) {
+        const int64_t lo = std::max<int64_t>(0, int64_t(ctx_len[b]) - window);
+        if (lo >= s.ke) continue;
+        first = std::min(first, lo);
+        s.members[n++] = b;
+      }
+      if (n == 0) continue;
+      s.members.resize(n);
+      s.row = req_rows[s.members[0]];
+      s.kb = std::max(s.kb, first);
+      n_shared += n >= 2;
+      if (kept != i) segs[kept] = std::move(s);
+      ++kept;
+    }
+    segs.resize(kept);
   }
   // work items: (key chunk, member block) of each segment.  Segments with <=
   // small_rows rows go to the warp role of the decode kernel (listed
@@ -1079,6 +1107,16 @@ extern "C" rx_status rx_plan_decode_steps(const rx_cache* c, int32_t B, int32_t 
                                           int64_t plan_cap, rx_decode_plan_info* info) {
   return plan_decode_impl(c, B, n_steps, prompt_node, ctx_len, req_rows, num_q_heads,
                           num_kv_heads, head_dim, plan, plan_cap, info);
+}
+
+extern "C" rx_status rx_plan_decode_window(const rx_cache* c, int32_t B, int32_t n_steps,
+                                           int32_t window, const rx_node* prompt_node,
+                                           const int32_t* ctx_len, const int32_t* req_rows,
+                                           int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t* plan, int64_t plan_cap,
+                                           rx_decode_plan_info* info) {
+  return plan_decode_impl(c, B, n_steps, prompt_node, ctx_len, req_rows, num_q_heads,
+                          num_kv_heads, head_dim, plan, plan_cap, info, window);
 }
 
 extern "C" rx_status rx_alloc_steps(rx_cache* c, int64_t k, int32_t n_steps, int32_t* out_slots) {

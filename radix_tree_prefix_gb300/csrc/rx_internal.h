@@ -61,6 +61,7 @@ int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
 int32_t kv8_store_error_flags(bool clear);  // bits 0, 6 and 7 of rx_device_check
 int32_t kv8_attention_error_flags(bool clear);  // as tc_error_flags
+int32_t rope_error_flags(bool clear);  // bit 0 of rx_device_check
 // One decode step in a single launch: the tensor-core tiles of the plan's
 // large items and the warp-role units of its small items (attention_tc.cu).
 // *unit_counter must be 0 at launch.  k_new / v_new / slots_new non-NULL:
@@ -76,12 +77,19 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                        int64_t n_tc, const int32_t* d_members, float scale, float* ws_o,
                        float* ws_lse, int32_t* unit_counter, int step, const void* k_new,
                        const void* v_new, const int32_t* slots_new, cudaStream_t stream,
-                       bool early_inputs);
+                       bool early_inputs, const rx_score_mod* mod = nullptr);
 rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                               int32_t num_q_heads, const int32_t* d_req_to_token,
                               int64_t row_stride, const int32_t* d_req_rows,
                               const int32_t* d_prefix_len, const int32_t* d_qo_indptr,
                               const int32_t* d_tile_indptr, int32_t R, int64_t num_tiles,
-                              float scale, float* d_out, float* d_lse, cudaStream_t stream);
+                              float scale, float* d_out, float* d_lse, cudaStream_t stream,
+                              const rx_score_mod* mod = nullptr, bool out_bf16 = false);
+// Partial results merged into fp32 or bf16 rows (kv8_attention.cu); a request
+// without parts, or with empty ones only, gets zeros and lse = -inf.  chained:
+// launched while the kernel that writes the parts runs.
+rx_status merge_parts(int head_dim, const int32_t* indptr, const int32_t* parts, const float* ws_o,
+                      const float* ws_lse, int hq, int B, void* d_out, bool out_bf16, float* d_lse,
+                      bool chained, cudaStream_t stream, const char* what);
 
 }  // namespace rx_internal

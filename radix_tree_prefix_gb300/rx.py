@@ -110,6 +110,32 @@ class rx_kv8_pool_desc(C.Structure):
 
 
 OUT_F32, OUT_BF16 = 0, 1      # RX_OUT_* of rx.h
+ROPE_MAX_PAIRS = 128
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}      # RX_ROPE_* of rx.h
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3, "wavelength": 4}
+
+
+class rx_rope_config(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("base", "factor", "original_len", "low", "high",
+                                          "magnitude")] + \
+               [(n, C.c_int32) for n in ("rot_dim", "layout", "scaling", "reserved")]
+
+
+class rx_rope(C.Structure):
+    _fields_ = [("turns", C.c_uint64 * ROPE_MAX_PAIRS), ("magnitude", C.c_float),
+                ("rot_dim", C.c_int32), ("layout", C.c_int32), ("reserved", C.c_int32)]
+
+
+class rx_head_norm(C.Structure):
+    _fields_ = [("d_q_weight", C.c_void_p), ("d_k_weight", C.c_void_p), ("eps", C.c_float),
+                ("plus_one", C.c_int32)]
+
+
+class rx_score_mod(C.Structure):
+    _fields_ = [("softcap", C.c_float), ("window", C.c_int32), ("d_slopes", C.c_void_p),
+                ("d_key_begin", C.c_void_p), ("d_bidir_end", C.c_void_p),
+                ("d_ctx_len", C.c_void_p)]
+
 
 P = C.c_void_p
 I32, I64, F32, SZ = C.c_int32, C.c_int64, C.c_float, C.c_size_t
@@ -172,6 +198,14 @@ _SIGS = {
                                 P],
     "rx_kv8_extend_batches": [POOL8, I32, I32, P, I32, F32, P, P],
     "rx_kv8_decode_steps": [POOL8, I32, I32, P, I64, P, I32, I32, F32, P, SZ, P],
+    "rx_rope_init": [P, P],
+    "rx_qk_rope": [P, P, I32, P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, P],
+    "rx_qkv_store": [POOL, I32, P, P, P, P, I64, P, I64, I32, P, I64, P, I64, P, I64, P],
+    "rx_extend_attention_mod": [POOL, I32, P, I32, P, I64, P, P, P, P, I32, I64, F32, P, P, I32, P,
+                                P],
+    "rx_plan_decode_window": [P, I32, I32, I32, P, P, P, I32, I32, I32, P, I64, P],
+    "rx_decode_attention_mod": [POOL, I32, P, I32, P, I64, P, P, I32, I32, F32, P, P, I32, P, P,
+                                SZ, P],
     "rx_device_check": [P],
 }
 for _name, _args in _SIGS.items():
@@ -492,8 +526,10 @@ class RadixCache:
         _check(_lib.rx_host_eviction_log(self._h, 0, recs, n, C.byref(total)))
         return [(recs[i].node_id, recs[i].num_tokens) for i in range(n)]
 
-    def plan_decode(self, prompt_nodes, ctx_len, req_rows, hq, hkv, d, plan=None, n_steps=None):
-        """rx_plan_decode, or rx_plan_decode_steps when n_steps is given."""
+    def plan_decode(self, prompt_nodes, ctx_len, req_rows, hq, hkv, d, plan=None, n_steps=None,
+                    window=0):
+        """rx_plan_decode, or rx_plan_decode_steps when n_steps is given; with
+        a window, rx_plan_decode_window."""
         B = len(prompt_nodes)
         info = rx_decode_plan_info()
         pn, cl, rr = _i64(prompt_nodes), _i32(ctx_len), _i32(req_rows)
@@ -501,6 +537,10 @@ class RadixCache:
         def call(buf):
             cap = 0 if buf is None else len(buf)
             ptr = _p(buf) if buf is not None else None
+            if window:
+                return _lib.rx_plan_decode_window(self._h, B, int(n_steps or 1), int(window),
+                                                  _p(pn), _p(cl), _p(rr), hq, hkv, d, ptr, cap,
+                                                  C.byref(info))
             if n_steps is None:
                 return _lib.rx_plan_decode(self._h, B, _p(pn), _p(cl), _p(rr), hq, hkv, d, ptr,
                                            cap, C.byref(info))
@@ -798,6 +838,201 @@ def kv8_decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, 
         pool, layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
         d_plan.data_ptr(), C.byref(info), B, step, scale, d_out.data_ptr(), ot, d_lse.data_ptr(),
         d_workspace.data_ptr(), d_workspace.numel() * d_workspace.element_size(), s))
+
+
+# ---------------------------------- norm, rotation and modified scores
+def _cuda_args(what, dev, stream, *tensors):
+    """Checks the (name, tensor, dtype, elements) of a call: contiguous, of the
+    type, at least the elements, all on `dev` (a CUDA device index), which
+    must be the current device.  Returns the stream's handle."""
+    import torch
+    if dev < 0:
+        raise ValueError(f"{what}: the tensors are not on a GPU")
+    for name, t, dtype, n in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or \
+                not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be a contiguous {dtype} tensor of at least {n} "
+                             f"elements on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"{what}: cuda:{dev} is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def rope(rot_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=0.0,
+         low=0.0, high=0.0, magnitude=0.0):
+    """rx_rope_init: the rotation of the first rot_dim elements of a head."""
+    cfg = rx_rope_config(base, factor, original_len, low, high, magnitude, rot_dim,
+                         ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], 0)
+    out = rx_rope()
+    _check(_lib.rx_rope_init(C.byref(cfg), C.byref(out)))
+    return out
+
+
+class HeadNorm(rx_head_norm):
+    """Norm of queries and keys that keeps its weights alive (head_norm)."""
+
+
+def head_norm(q_weight, k_weight, eps, plus_one=False):
+    """RMS norm of each head: bf16 weights [d] (None: that side is left as it
+    is), the factor 1 + w with plus_one."""
+    import torch
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.bfloat16 or w.dim() != 1 or not w.is_contiguous()):
+            raise ValueError("head_norm: weights are contiguous bfloat16 tensors [d]")
+    n = HeadNorm(None if q_weight is None else q_weight.data_ptr(),
+                 None if k_weight is None else k_weight.data_ptr(), float(eps),
+                 1 if plus_one else 0)
+    n.tensors = tuple(w for w in (q_weight, k_weight) if w is not None)
+    return n
+
+
+def _heads(what, name, t, T, d, dev):
+    """Checks bf16 [T, H, d] with its heads side by side; (pointer, token
+    stride, H)."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or \
+            t.get_device() != dev or (t.numel() and (t.stride(2) != 1 or (
+                t.shape[1] > 1 and t.stride(1) != d))):
+        raise ValueError(f"{what}: {name} must be a bfloat16 tensor [{T}, H, {d}] on cuda:{dev} "
+                         f"whose heads lie side by side, got {t.dtype} {tuple(t.shape)} of strides "
+                         f"{t.stride()} on {t.device}")
+    # (one token's stride is free)
+    return t.data_ptr(), t.stride(0) if T > 1 else t.shape[1] * d, t.shape[1]
+
+
+def _norm_args(what, norm, d, dev):
+    if norm is not None:
+        for w in norm.tensors:
+            if w.numel() != d or w.get_device() != dev:
+                raise ValueError(f"{what}: the norm's weights must have {d} elements on cuda:{dev}")
+    return None if norm is None else C.byref(norm)
+
+
+def qk_rope(rope, d_positions, d_q, d_k, d_q_out, d_k_out, norm=None, stream=None):
+    """rx_qk_rope: bf16 queries [T, Hq, d] and keys [T, Hkv, d] (views of one
+    projection, if need be) normalised and rotated into the outputs, which may
+    be the inputs."""
+    import torch
+    T, _, d = d_q.shape
+    dev = d_q.get_device()
+    s = _cuda_args("qk_rope", dev, stream, ("d_positions", d_positions, torch.int32, T))
+    q, qs, hq = _heads("qk_rope", "d_q", d_q, T, d, dev)
+    k, ks, hkv = _heads("qk_rope", "d_k", d_k, T, d, dev)
+    qo, qos, hqo = _heads("qk_rope", "d_q_out", d_q_out, T, d, dev)
+    ko, kos, hko = _heads("qk_rope", "d_k_out", d_k_out, T, d, dev)
+    if (hq, hkv) != (hqo, hko):
+        raise ValueError("qk_rope: the outputs have other head counts than the inputs")
+    _check(_lib.rx_qk_rope(None if rope is None else C.byref(rope),
+                           _norm_args("qk_rope", norm, d, dev), d, d_positions.data_ptr(), T, q,
+                           qs, hq, k, ks, hkv, qo, qos, ko, kos, s))
+
+
+def qkv_store(pool, layer, rope, d_positions, d_slots, d_q, d_k, d_v, d_q_out, norm=None,
+              stream=None):
+    """rx_qkv_store: queries normalised and rotated into d_q_out, keys
+    alike and values as they are into their slots of the pool.  d_q and
+    d_q_out None: keys and values only."""
+    import torch
+    T, d, hkv = d_slots.numel(), pool.head_dim, pool.num_kv_heads
+    dev = d_k.get_device()
+    s = _cuda_args("qkv_store", dev, stream, ("d_positions", d_positions, torch.int32, T),
+                   ("d_slots", d_slots, torch.int32, T))
+    k, ks, hk = _heads("qkv_store", "d_k", d_k, T, d, dev)
+    v, vs, hv = _heads("qkv_store", "d_v", d_v, T, d, dev)
+    q, qs, hq, qo, qos = None, 0, 0, None, 0
+    if d_q is not None:
+        q, qs, hq = _heads("qkv_store", "d_q", d_q, T, d, dev)
+        qo, qos, hqo = _heads("qkv_store", "d_q_out", d_q_out, T, d, dev)
+        if hqo != hq:
+            raise ValueError("qkv_store: d_q_out has another head count than d_q")
+    if hk != hkv or hv != hkv:
+        raise ValueError(f"qkv_store: the pool has {hkv} KV heads, d_k {hk} and d_v {hv}")
+    _check(_lib.rx_qkv_store(C.byref(pool), layer, None if rope is None else C.byref(rope),
+                             _norm_args("qkv_store", norm, d, dev), d_positions.data_ptr(),
+                             d_slots.data_ptr(), T, q, qs, hq, k, ks, v, vs, qo, qos, s))
+
+
+class ScoreMod(rx_score_mod):
+    """Modified scores that keep their tensors alive (score_mod)."""
+
+
+def score_mod(softcap=0.0, window=0, slopes=None, key_begin=None, bidir_end=None, ctx_len=None):
+    """What modifies attention's scores (rx_score_mod): a tanh cap, a window,
+    fp32 slopes [Hq], int32 first keys [queries], int32 ends of the part seen
+    both ways [R] (extend), int32 context lengths [B] (decode)."""
+    import torch
+    m = ScoreMod(float(softcap), int(window))
+    m.tensors = {}
+    for field, t, dtype in (("d_slopes", slopes, torch.float32),
+                            ("d_key_begin", key_begin, torch.int32),
+                            ("d_bidir_end", bidir_end, torch.int32),
+                            ("d_ctx_len", ctx_len, torch.int32)):
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"score_mod: {field[2:]} must be a contiguous {dtype} tensor of one "
+                             "dimension")
+        setattr(m, field, t.data_ptr())
+        m.tensors[field] = t
+    return m
+
+
+def _mod_args(what, mod, dev, **need):
+    if mod is None:
+        return None
+    for field, t in mod.tensors.items():
+        n = need.get(field)
+        if n is not None and (t.numel() < n or t.get_device() != dev):
+            raise ValueError(f"{what}: {field[2:]} of the score mod must have at least {n} "
+                             f"elements on cuda:{dev}, has {t.numel()} on {t.device}")
+    return C.byref(mod)
+
+
+def extend_attention_mod(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len, d_qo_indptr,
+                         d_tile_indptr, R, num_tiles, scale, mod, d_out, d_lse, stream=None):
+    """rx_extend_attention_mod; d_out is bf16 or fp32.  A key_begin of the score
+    mod has an entry for every token of d_q."""
+    import torch
+    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
+    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
+    dev, n = d_q.get_device(), d_q.numel()
+    nq = n // (hq * pool.head_dim)
+    s = _cuda_args("extend_attention_mod", dev, stream, ("d_q", d_q, bf16, 0),
+                   ("d_table", d_table, i32, 0), ("d_req_rows", d_req_rows, i32, R),
+                   ("d_prefix_len", d_prefix_len, i32, R),
+                   ("d_qo_indptr", d_qo_indptr, i32, R + 1),
+                   ("d_tile_indptr", d_tile_indptr, i32, R + 1),
+                   ("d_out", d_out, bf16 if ot else f32, n), ("d_lse", d_lse, f32, nq * hq))
+    m = _mod_args("extend_attention_mod", mod, dev, d_slopes=hq, d_key_begin=nq, d_bidir_end=R)
+    _check(_lib.rx_extend_attention_mod(
+        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        d_req_rows.data_ptr(), d_prefix_len.data_ptr(), d_qo_indptr.data_ptr(),
+        d_tile_indptr.data_ptr(), R, num_tiles, scale, m, d_out.data_ptr(), ot, d_lse.data_ptr(),
+        s))
+
+
+def decode_attention_mod(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, mod, d_out, d_lse,
+                         d_workspace, step=0, stream=None):
+    """rx_decode_attention_mod (drafts: B of them); d_out is bf16 or fp32."""
+    import torch
+    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
+    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
+    dev, rows = d_q.get_device(), B * hq
+    s = _cuda_args("decode_attention_mod", dev, stream, ("d_q", d_q, bf16, rows * pool.head_dim),
+                   ("d_table", d_table, i32, 0), ("d_plan", d_plan, i32, info.plan_words),
+                   ("d_out", d_out, bf16 if ot else f32, rows * pool.head_dim),
+                   ("d_lse", d_lse, f32, rows),
+                   ("d_workspace", d_workspace, d_workspace.dtype, 0))
+    m = _mod_args("decode_attention_mod", mod, dev, d_slopes=hq, d_key_begin=B, d_ctx_len=B)
+    _check(_lib.rx_decode_attention_mod(
+        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
+        d_plan.data_ptr(), C.byref(info), B, step, scale, m, d_out.data_ptr(), ot,
+        d_lse.data_ptr(), d_workspace.data_ptr(),
+        d_workspace.numel() * d_workspace.element_size(), s))
 
 
 def decode_attention_static(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_out, d_lse,
