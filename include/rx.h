@@ -907,12 +907,13 @@ typedef struct rx_score_mod {
 
 /* rx_extend_attention with modified scores (mod NULL: none), into fp32 or
  * bf16 (out_type).  Scores, statistics and sums are held in fp32; softmax
- * weights are rounded to bf16 for the product with V.  Scores must lie within
- * +-1e29.  Keys that no query of a tile of 128 query rows sees are not read;
- * the K and V rows that a tile reads must be finite (a masked key weighs 0, and
- * 0 times an infinity would reach its tile's other queries).  d_ctx_len is
- * not read.  Errors: RX_ERR_INVALID as rx_extend_attention, for an unknown
- * out_type, softcap < 0 or not finite, window < 0. */
+ * weights are rounded to bf16 for the product with V.  A tile of 128 query
+ * rows (rx_extend_plan) reads the keys from the first to the last that one of
+ * its rows sees; their V rows must be finite (a masked key weighs 0, and 0 times
+ * an infinity would reach the tile's other queries), their K rows need not
+ * be where they are masked.  d_ctx_len is not read.  Errors: RX_ERR_INVALID
+ * as rx_extend_attention, for an unknown out_type, softcap < 0 or not finite,
+ * window < 0, scale <= 0 or not finite. */
 rx_status rx_extend_attention_mod(
     const rx_pool_desc* pool, int32_t layer, const void* d_q,
     int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,
@@ -942,8 +943,8 @@ rx_status rx_plan_decode_window(const rx_cache* cache, int32_t B,
  * - 1 (drafts: out_ctx_len of rx_verify_rows).  step: the step of a plan of
  * several (else 0); its tokens must be stored first.  d_key_begin is [B];
  * d_bidir_end is not read (every key of a context lies before its query).
- * d_ctx_len is needed with a window or slopes.  The K and V rows of the plan's
- * keys must be finite.  Numerics as rx_extend_attention_mod.  Errors:
+ * d_ctx_len is needed with a window or slopes.  The V rows of the plan's keys
+ * must be finite.  Numerics as rx_extend_attention_mod.  Errors:
  * RX_ERR_INVALID as rx_decode_attention and rx_extend_attention_mod, for
  * step < 0 and a missing d_ctx_len. */
 rx_status rx_decode_attention_mod(

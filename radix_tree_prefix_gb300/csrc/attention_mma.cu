@@ -159,90 +159,6 @@ extern "C" rx_status rx_extend_attention(const rx_pool_desc* pool, int32_t layer
                                          reinterpret_cast<cudaStream_t>(stream));
 }
 
-// What both attention calls with modified scores check of them.
-static rx_status check_mod(const rx_score_mod* mod, int32_t out_type) {
-  if (out_type != RX_OUT_F32 && out_type != RX_OUT_BF16)
-    return rx_internal::set_error(RX_ERR_INVALID, "attention: unknown out_type");
-  if (mod && (!(mod->softcap >= 0.f) || !isfinite(mod->softcap)))
-    return rx_internal::set_error(RX_ERR_INVALID, "score mod: softcap < 0 or not finite");
-  if (mod && mod->window < 0)
-    return rx_internal::set_error(RX_ERR_INVALID, "score mod: window < 0");
-  return RX_OK;
-}
-
-extern "C" rx_status rx_extend_attention_mod(
-    const rx_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
-    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_req_rows,
-    const int32_t* d_prefix_len, const int32_t* d_qo_indptr, const int32_t* d_tile_indptr,
-    int32_t R, int64_t num_tiles, float scale, const rx_score_mod* mod, void* d_out,
-    int32_t out_type, float* d_lse, rx_stream_t stream) {
-  rx_status st = rx_internal::check_pool(pool, layer);
-  if (st == RX_OK) st = check_mod(mod, out_type);
-  if (st != RX_OK) return st;
-  if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
-    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: Hq % Hkv != 0");
-  if (R < 0 || num_tiles < 0 || num_tiles * pool->num_kv_heads > INT32_MAX)
-    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: bad R or num_tiles");
-  if (R == 0 || num_tiles == 0) return RX_OK;
-  if (!d_q || !d_req_to_token || !d_req_rows || !d_prefix_len || !d_qo_indptr ||
-      !d_tile_indptr || !d_out || !d_lse || !aligned16(d_q) || !aligned16(d_out))
-    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: NULL or misaligned");
-  const rx_score_mod none{};
-  return rx_internal::extend_attention_tc(
-      pool, layer, d_q, num_q_heads, d_req_to_token, row_stride, d_req_rows, d_prefix_len,
-      d_qo_indptr, d_tile_indptr, R, num_tiles, scale, static_cast<float*>(d_out), d_lse,
-      reinterpret_cast<cudaStream_t>(stream), mod ? mod : &none, out_type == RX_OUT_BF16);
-}
-
-extern "C" rx_status rx_decode_attention_mod(
-    const rx_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
-    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
-    const rx_decode_plan_info* info, int32_t B, int32_t step, float scale,
-    const rx_score_mod* mod, void* d_out, int32_t out_type, float* d_lse, void* d_workspace,
-    size_t workspace_bytes, rx_stream_t stream) {
-  rx_status st = rx_internal::check_pool(pool, layer);
-  if (st == RX_OK) st = check_mod(mod, out_type);
-  if (st != RX_OK) return st;
-  auto bad = [](const char* why) { return rx_internal::set_error(RX_ERR_INVALID, why); };
-  if (!info || num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0 || B < 0 || step < 0)
-    return bad("rx_decode_attention_mod: bad argument");
-  if (B == 0) return RX_OK;
-  if (int64_t(workspace_bytes) < info->workspace_bytes || !d_workspace || !aligned16(d_workspace))
-    return bad("rx_decode_attention_mod: workspace missing, small or misaligned");
-  if (!d_q || !d_req_to_token || !d_plan || !d_out || !d_lse || !aligned16(d_q) ||
-      !aligned16(d_out))
-    return bad("rx_decode_attention_mod: NULL or misaligned");
-  if (mod && (mod->window > 0 || mod->d_slopes) && !mod->d_ctx_len)
-    return bad("rx_decode_attention_mod: a window or slopes need d_ctx_len");
-  const int64_t n_small = info->n_work - info->n_work_tc;
-  if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
-      info->n_work > INT32_MAX / pool->num_kv_heads)
-    return bad("rx_decode_attention_mod: bad plan info");
-  const int D = pool->head_dim;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t o_bytes = (info->n_parts * num_q_heads * int64_t(D) * 4 + 255) / 256 * 256;
-  const int64_t l_bytes = (info->n_parts * num_q_heads * 4 + 255) / 256 * 256;
-  char* ws = static_cast<char*>(d_workspace);
-  float* ws_o = reinterpret_cast<float*>(ws);
-  float* ws_lse = reinterpret_cast<float*>(ws + o_bytes);
-  int32_t* counter = reinterpret_cast<int32_t*>(ws + o_bytes + l_bytes);
-  const rx_score_mod none{};
-  if (info->n_work > 0) {
-    if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
-      return rx_internal::launch_status("rx_decode_attention_mod: counter reset");
-    const int32_t* work = d_plan + info->off_work;
-    st = rx_internal::decode_fused(pool, layer, d_q, num_q_heads, d_req_to_token, row_stride, work,
-                                   n_small, work + n_small * RX_WORK_WORDS, info->n_work_tc,
-                                   d_plan + info->off_members, scale, ws_o, ws_lse, counter, step,
-                                   nullptr, nullptr, nullptr, s, false, mod ? mod : &none);
-    if (st != RX_OK) return st;
-  }
-  return rx_internal::merge_parts(D, d_plan + info->off_req_part_indptr,
-                                  d_plan + info->off_req_parts, ws_o, ws_lse, num_q_heads, B,
-                                  d_out, out_type == RX_OUT_BF16, d_lse, info->n_work > 0, s,
-                                  "rx_decode_attention_mod: merge");
-}
-
 namespace {
 
 rx_status decode_attention_impl(const rx_pool_desc* pool, int32_t layer, const void* d_q,

@@ -1,0 +1,1017 @@
+// Extend and decode attention with modified scores (rx_score_mod): a tanh cap,
+// distance slopes, a window, documents, a part that is seen both ways.
+//
+// Query i scores key j by s = softcap tanh(scale q.k / softcap) - slope |i - j|
+// and sees the keys [lo_i, lim_i): lo_i from its window and its document, lim_i =
+// i + 1 or the end of the part seen both ways.  What is computed from s is the
+// one-pass softmax of attention_tc.cu.
+//
+// One tile = 128 query rows that read one KV head over one key range, as in
+// attention_tc.cu (extend: suffix tokens x heads of a group; decode: members x
+// heads of a shared segment).  Modified scores cost the softmax warps several
+// times what the plain ones do (a cap alone some ten operations a score), and
+// two warpgroups that share a key tile wait for one another at its maximum. So
+// here the two warpgroups take whole key tiles in turn, thread = row:
+//   warps 0-7   warpgroup j % 2 takes key tile j: scores from TMEM, modified, masked,
+//               the row's maximum; then the row's reference m of tile j - 1
+//               comes from the other warpgroup through shared memory (barrier
+//               H), is raised if a score exceeds it by more than 2^32 (O is then
+//               rescaled in TMEM), and goes on to tile j + 1; only then the
+//               exponentials, P (bf16) into TMEM over S.  So one warpgroup's
+//               exponentials run beside the other's scores, and the chain between
+//               them is a compare and a barrier.  Each warpgroup keeps the row
+//               sums of its own tiles; they meet in the epilogue;
+//   warp 8      S_j = Q K_j^T into a ring of TMEM buffers; warp 11 O += P_j V_j;
+//   warps 9-10  K and V into shared memory: a tile of one run of slots is one TMA
+//               box per 64 columns, else every group of 16 keys that is a run
+//               (pages of 16 slots and more, aligned runs) one smaller box,
+//               and the groups left are gathered by 16-byte cp.async, whose
+//               completion is waited for only when the next tile's loads are out.
+// Rows of a tile see different keys: the key range is what some row sees, and
+// masks are applied only in key tiles that some row of the warp sees in part.
+// A masked score is -inf; a row that has seen no key yet has m = -inf and weighs
+// its masked keys 0, and one that never sees any gets o = 0, lse = -inf.
+
+#include "attention_tile.cuh"
+
+namespace {
+
+constexpr int kGroup = 16;  // keys of a small TMA box
+// Softmax warpgroups.
+constexpr int kExtendGroups = 3, kExtendThreads = 128 * (kExtendGroups + 1);
+constexpr int kDecodeGroups = 2, kDecodeThreads = 128 * (kDecodeGroups + 1);
+// A row's reference is raised when a score exceeds it by more than this (log2
+// units).  Raising stops the chain between the warpgroups until the product
+// before it has completed, so it is made rare; 2^32 times the weights' usual size
+// leaves fp32 (and bf16, of the same range) room for the sums of 2^60 keys.
+constexpr float kRaise = 32.f;
+
+// Keys are loaded, and S computed, BS at a time (the wider product at head_dim
+// 128: one of 64 keys reads Q's 16 columns from shared memory for half the
+// work); the softmax and O += P V go by tiles of BN = 64 keys, SUBS to a load.
+// Rings of NK and NV stages of K and V, NS of S (TMEM).
+constexpr int BN = 64;
+template <int D>
+struct Layout4 {
+  static constexpr int BS = D == 128 ? 128 : 64;
+  static constexpr int SUBS = BS / BN;
+  static constexpr int KV_BYTES = BS * D * 2;
+  static constexpr int NK = 3, NV = D == 128 ? 3 : 2;
+  static constexpr int NS = D == 128 ? 3 : 4;
+  static constexpr int NB = NS * SUBS;  // tiles of P
+  static constexpr int Q = 0;
+  static constexpr int K0 = BM * D * 2;
+  static constexpr int V0 = K0 + NK * KV_BYTES;
+  static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
+  static constexpr int BAR = REF + 2 * BM * 4;
+  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + NS + 2 * NB + 8 + 2;
+  static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
+  static constexpr int BYTES = MISC + 16;
+  static constexpr int O_COL = NB * BN;
+  static constexpr int TMEM_COLS = 512;
+  // the epilogue's rows in the K and V stages, then the warpgroups' (m, l)
+  static constexpr int PITCH = D / 2 * 4 + 16;
+  static constexpr int XCH = K0 + 2 * BM * PITCH;
+  static_assert(O_COL + D <= TMEM_COLS, "TMEM budget");
+  static_assert(XCH + 3 * BM * 8 <= REF, "the exchange fits in the stages");
+  static_assert(BYTES <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+
+struct Maps4 {
+  CUtensorMap k, v;      // boxes of a tile's keys x 64 columns
+  CUtensorMap k16, v16;  // boxes of 16 keys
+};
+
+// One lane of the warp, known to the compiler as such.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Barriers between warps: a warp waits as one and arrives once.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, kWaitLimit));
+}
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// One warp loads the K or V tiles into a ring of `stages` stages; barriers full
+// and empty of stage s at full0 + 8 s and empty0 + 8 s (empty: the products that
+// read the stage's last tile completed).  One piece of code for both warps, its
+// loops rolled: with the roles' loops unrolled the kernel was 195 KB of code, and
+// its warps, each somewhere else in it, waited for instructions most of the
+// time.
+template <int D, int BS>
+__device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, int n_loads,
+                                           const CUtensorMap* tm, const CUtensorMap* tm16,
+                                           const bf16* src_base, int row0, uint32_t smem0,
+                                           uint32_t full0, uint32_t empty0, int stages,
+                                           volatile int* abort_flag) {
+  constexpr int CPR = D / 8, CB = D / 64;
+  constexpr int SPL = BS / 32;   // slots per lane: keys lane + 32 i
+  constexpr int AHEAD = 3;       // tiles whose slots are on their way
+  const int lane = threadIdx.x & 31;
+  int32_t slot[SPL], next[AHEAD][SPL];
+  auto load_slots = [&](int j, int32_t (&dst)[SPL]) {
+    const int k0 = t.key_begin + j * BS;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+      const int key = k0 + lane + 32 * i;
+      dst[i] = j < n_loads && key >= t.key_lo && key < t.key_end ? __ldg(t.trow + key) : -1;
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) load_slots(u, next[u]);
+  int stage = 0, ahead_stage = 0;  // of tile j, and of the tile whose rows are gathered
+  uint32_t phase = 1;              // of the wait for an empty stage (the first round's: none)
+  bool pending = false;            // a tile's gathered rows are still on their way
+  int j = 0;
+#pragma unroll 1
+  for (; j < n_loads; ++j) {
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+      slot[i] = next[0][i];
+#pragma unroll
+      for (int u = 0; u + 1 < AHEAD; ++u) next[u][i] = next[u + 1][i];
+      if (slot[i] >= a.num_slots || slot[i] < -1) {
+        atomicOr(&g_tc_error, 1);
+        slot[i] = 0;
+      }
+    }
+    load_slots(j + AHEAD, next[AHEAD - 1]);
+    const uint32_t full = full0 + 8u * uint32_t(stage);
+    const uint32_t dst = smem0 + uint32_t(stage * BS * D * 2);
+    if (j >= stages && !warp_wait(empty0 + 8u * uint32_t(stage), phase, abort_flag)) break;
+    // which groups of 16 keys are runs of slots (bit g), and whether they all are one
+    const int32_t first = __shfl_sync(0xffffffffu, slot[0], 0);
+    bool one = first >= 0 && int64_t(first) + BS <= a.num_slots;
+    uint32_t runs = 0;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+      one = one && slot[i] == first + lane + 32 * i;
+      const int32_t b = __shfl_sync(0xffffffffu, slot[i], lane & 16);
+      const uint32_t ok = __ballot_sync(
+          0xffffffffu, b >= 0 && int64_t(b) + kGroup <= a.num_slots && slot[i] == b + (lane & 15));
+      runs |= ((ok & 0xffffu) == 0xffffu ? 1u : 0u) << (2 * i) |
+              (ok >> 16 == 0xffffu ? 2u : 0u) << (2 * i);
+    }
+    one = __all_sync(0xffffffffu, one);
+    bool gathered = false;
+    if (one) {
+      if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(BS * D * 2));
+      __syncwarp();
+      if (lane < CB)
+        tc::tma_load_2d(dst + uint32_t(lane * BS * 128), tm, lane * 64, row0 + first, full);
+    } else {
+      constexpr uint32_t ALL = (1u << (BS / kGroup)) - 1u;
+      gathered = runs != ALL;
+      if (lane == 0) mbar_expect_tx(full, uint32_t(__popc(runs) * kGroup * D * 2));
+      __syncwarp();
+      {
+        // a lane a box: columns 64 (lane % CB) of group lane / CB
+        const int g = lane / CB;
+        int32_t b = 0;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) {
+          const int32_t x = __shfl_sync(0xffffffffu, slot[i], 16 * (g & 1));
+          if (g >> 1 == i) b = x;
+        }
+        if (g < BS / kGroup && (runs >> g & 1u))
+          tc::tma_load_2d(dst + uint32_t((lane % CB) * BS * 128 + g * kGroup * 128), tm16,
+                          (lane % CB) * 64, row0 + b, full);
+      }
+#pragma unroll 1
+      for (uint32_t left = ALL & ~runs; left; left &= left - 1u) {
+        const int g = __ffs(left) - 1;
+        int32_t mine = slot[0];
+#pragma unroll
+        for (int i = 1; i < SPL; ++i) mine = (g >> 1) == i ? slot[i] : mine;
+        // lanes 0-15 and 16-31 copy chunks (lane % 16) + 16 h of rows 2k, 2k + 1
+#pragma unroll 4
+        for (int k = 0; k < 8; ++k) {
+          const int in = 2 * k + (lane >> 4);
+          const int32_t sl = __shfl_sync(0xffffffffu, mine, 16 * (g & 1) + in);
+          const bool ok = sl >= 0;
+          const bf16* src = src_base + int64_t(ok ? sl : 0) * D;
+#pragma unroll
+          for (int h = 0; h < CPR / 16; ++h) {
+            const int ch = (lane & 15) + 16 * h;
+            rxk::cp_async_16(sw128(dst, BS, g * kGroup + in, ch), src + ch * 8, ok);
+          }
+        }
+      }
+      if (gathered)
+        rxk::cp_async_commit();
+      else if (lane == 0)
+        tc::mbar_arrive(full);
+    }
+    // the gather of the tile before has had this tile's issue to land in
+    if (pending) {
+      if (gathered)
+        rxk::cp_async_wait<1>();
+      else
+        rxk::cp_async_wait<0>();
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(ahead_stage));
+    }
+    pending = gathered;
+    ahead_stage = stage;
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (pending) {
+    rxk::cp_async_wait<0>();
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(ahead_stage));
+  }
+  // Before the CTA gives up its shared memory the last load of every stage has
+  // landed: at once on the normal path; after a wait of another warp gave up, one
+  // more bounded wait that does not look at the abort flag.
+  if (lane == 0) {
+    int drain_abort = 0;
+#pragma unroll 1
+    for (int i = j > stages ? j - stages : 0; i < j; ++i)
+      tc::mbar_wait(full0 + 8u * uint32_t(i % stages), uint32_t(i / stages) & 1u, &drain_abort,
+                    kWaitLimit);
+  }
+  __syncwarp();
+}
+
+// CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
+// kernel of its own: jumps over the code of what a call does not use cost its
+// warps more in instruction fetches than the work.
+template <int D, int NW, bool DECODE, bool CAP, bool SLOPES>
+__device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_t* gbase, int bx,
+                                      int kvh) {
+  using Lo = Layout4<D>;
+  constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
+  constexpr int SUBS = Lo::SUBS;
+  constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
+  const uint32_t base = rxk::smem_addr(gbase);
+  if (base & 1023u) {  // uniform over the CTA: nothing initialised yet
+    if (threadIdx.x == 0) atomicOr(&g_tc_error, 4);
+    return;
+  }
+  const uint32_t sQ = base + Lo::Q;
+  const uint32_t BAR_Q = base + Lo::BAR;
+  const uint32_t KF = BAR_Q + 8u, KE = KF + 8u * NK, VF = KE + 8u * NK, VE = VF + 8u * NV;
+  const uint32_t BAR_S = VE + 8u * NV, BAR_P = BAR_S + 8u * NS;
+  // PV_j completes phase j / NB of its buffer's barrier: S may overwrite P_j
+  const uint32_t BAR_PF = BAR_P + 8u * NB;
+  // the references of a quadrant's rows at even (0-3) and odd (4-7) tiles are set
+  const uint32_t BAR_H = BAR_PF + 8u * NB;
+  const uint32_t BAR_FIN = BAR_H + 64u, BAR_X = BAR_FIN + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lo::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if constexpr (DECODE) rxk::griddep_wait();
+  const TileDesc t = describe<DECODE, true>(a, bx);
+  const int n_keys = t.key_lo >= t.key_end ? 0 : t.key_end - t.key_begin;
+  const int n_tiles = (n_keys + BN - 1) / BN, n_loads = (n_keys + BS - 1) / BS;
+  const int wg = warp >> 2;
+  const int i = (warp & 3) * 32 + lane;  // TMEM lane
+  // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
+  // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
+  const bool m64 = t.n_rows <= 64;
+  const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
+  int64_t qi = 0, part = 0;
+  int head = 0, lim = t.key_end;
+  bool valid = false;
+  RowMod rm;
+  if (warp < SW) {
+    valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
+    if (valid) {
+      row_info<DECODE>(a, t, kvh, row, qi, head, part, lim);
+      const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
+      if (!DECODE) lim = max(lim, t.bidir);
+      rm = row_mod(a, qi, head, pos);
+      rm.lo = max(rm.lo, t.key_lo);
+    } else {
+      // a lane without a row: nothing it holds is masked or counts
+      rm.lo = t.key_lo;
+      rm.pos = INT32_MAX;
+    }
+    // the Q row this thread gathers: tile row i into shared-memory row i,
+    // whatever the TMEM layout of the products
+    int64_t gqi = qi;
+    int ghead = head;
+    bool gvalid = valid;
+    if (m64) {
+      int64_t gpart = 0;
+      int glim = 0;
+      gqi = 0;
+      ghead = 0;
+      gvalid = i < t.n_rows;
+      if (gvalid) row_info<DECODE>(a, t, kvh, i, gqi, ghead, gpart, glim);
+    }
+    if (wg < 2) {  // each half of a row
+      const bf16* src = a.q + (gqi * a.hq + ghead) * D;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int ch = wg * (D / 16) + c;
+        rxk::cp_async_16(sw128(sQ, BM, i, ch), src + ch * 8, gvalid);
+      }
+      rxk::cp_async_commit();
+    }
+  }
+  if (tid == 0) {
+    tc::mbar_init(BAR_Q, 8);
+    for (int s = 0; s < NK; ++s) tc::mbar_init(KF + 8u * s, 1);
+    for (int s = 0; s < NK; ++s) tc::mbar_init(KE + 8u * s, 1);
+    for (int s = 0; s < NV; ++s) tc::mbar_init(VF + 8u * s, 1);
+    for (int s = 0; s < NV; ++s) tc::mbar_init(VE + 8u * s, 1);
+    for (int b = 0; b < NS; ++b) tc::mbar_init(BAR_S + 8u * b, 1);
+    for (int b = 0; b < NB; ++b) {
+      tc::mbar_init(BAR_P + 8u * b, 4);
+      tc::mbar_init(BAR_PF + 8u * b, 1);
+    }
+    for (int b = 0; b < 8; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
+    tc::mbar_init(BAR_FIN, 2);  // one commit per issuing thread
+    tc::mbar_init(BAR_X, SW);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == SW) {
+    tc::tmem_alloc(rxk::smem_addr(tmem_slot), Lo::TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= SW) {
+    if (warp == SW + 1 || warp == SW + 2) {
+      const bool v = warp == SW + 2;
+      load_tiles<D, BS>(a, t, n_loads, v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
+                        (v ? a.vpool : a.kpool) + int64_t(kvh) * a.head_stride,
+                        int(a.tma_row_base + int64_t(kvh) * a.tma_head_rows),
+                        base + (v ? Lo::V0 : Lo::K0), v ? VF : KF, v ? VE : KE, v ? NV : NK,
+                        abort_flag);
+    } else {
+      if (elect_one()) {
+        const uint32_t idesc_s = m64 ? tc::idesc_bf16(64, BS, 0) : tc::idesc_bf16(BM, BS, 0);
+        const uint32_t idesc_pv = m64 ? tc::idesc_bf16(64, D, 1) : tc::idesc_bf16(BM, D, 1);
+        // descriptors as in attention_tc.cu: 128-byte swizzle, 1024 bytes
+        // between 8-row groups in the high half
+        constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
+        constexpr uint32_t KV_STEP = uint32_t(Lo::KV_BYTES) >> 4;
+        static_assert(Lo::REF < (1 << 18), "descriptor address field");
+        if (warp == SW) {
+          const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
+          const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
+          const bool ok = tc::mbar_wait(BAR_Q, 0, abort_flag, kWaitLimit, kSleepNs);
+          int sk = 0, sb = 0;
+          uint32_t k_phase = 0, b_phase = 1;
+#pragma unroll 1
+          for (int j = 0; ok && j < n_loads; ++j) {
+            // (products complete in order: the last tile of the buffer's P is enough)
+            if (j >= NS && !tc::mbar_wait(BAR_PF + 8u * (sb * SUBS + SUBS - 1), b_phase, abort_flag,
+                                          kWaitLimit, kSleepNs))
+              break;
+            if (!tc::mbar_wait(KF + 8u * sk, k_phase, abort_flag, kWaitLimit, kSleepNs)) break;
+            tc::tc_fence_after();
+            const uint32_t k_lo = k_lo0 + uint32_t(sk) * KV_STEP;
+            const uint32_t d_s = tmem + uint32_t(sb * BS);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t a_off = uint32_t(((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4);
+              const uint32_t b_off = uint32_t(((ks >> 2) * (BS * 128) + (ks & 3) * 32) >> 4);
+              mma_ss_split(d_s, q_lo + a_off, k_lo + b_off, DHI, idesc_s, ks > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(BAR_S + 8u * sb);
+            tc::mma_commit(KE + 8u * sk);
+            if (++sk == NK) sk = 0, k_phase ^= 1u;
+            if (++sb == NS) sb = 0, b_phase ^= 1u;
+          }
+        } else {
+          const uint32_t v_lo0 =
+              (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BS * 128 / 16) << 16);
+          int sv = 0, pb = 0;
+          uint32_t v_phase = 0, p_phase = 0;
+#pragma unroll 1
+          for (int j = 0; j < n_tiles; ++j) {
+            if (!tc::mbar_wait(BAR_P + 8u * pb, p_phase, abort_flag, kWaitLimit, kSleepNs)) break;
+            const int sub = j % SUBS;
+            if (sub == 0 &&
+                !tc::mbar_wait(VF + 8u * sv, v_phase, abort_flag, kWaitLimit, kSleepNs))
+              break;
+            tc::tc_fence_after();
+            const uint32_t v_lo = v_lo0 + uint32_t(sv) * KV_STEP + uint32_t(sub * (BN * 128 / 16));
+            const uint32_t p_t = tmem + uint32_t(pb * BN);
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+              mma_ts_split(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
+                           v_lo + uint32_t(ks * 2048 / 16), DHI, idesc_pv,
+                           (j > 0 || ks > 0) ? 1u : 0u);
+            tc::mma_commit(BAR_PF + 8u * pb);
+            if (sub == SUBS - 1) {
+              tc::mma_commit(VE + 8u * sv);
+              if (++sv == NV) sv = 0, v_phase ^= 1u;
+            }
+            if (++pb == NB) pb = 0, p_phase ^= 1u;
+          }
+        }
+        // every MMA this thread issued has completed once the final barrier (one
+        // arrival per issuing thread) completes; the wait ignores the abort flag
+        tc::mma_commit(BAR_FIN);
+        int drain_abort = 0;
+        tc::mbar_wait(BAR_FIN, 0, &drain_abort, kWaitLimit);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    // (fences of the async and tcgen05 proxies are each lane's, before its warp arrives)
+    const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
+    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);  // [2][BM]
+    if (wg < 2) {
+      rxk::cp_async_wait<0>();
+      tc::fence_proxy_async_smem();
+      warp_arrive(BAR_Q);
+    }
+    // what the rows of this warp have in common: keys [lo_max, lim_min) are seen
+    // by all of them, and keys up to pos_min lie behind all of them
+    const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
+    const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+    const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
+    float m_ref = -INFINITY;  // reference of the row's weights, log2 units
+    float l = 0.f;            // sum of this warpgroup's weights under it
+    bool ok = true;
+#pragma unroll 1
+    for (int j = wg; j < n_tiles; j += NW) {
+      const int s = j % NB;
+      // waits are made warp-uniform before any warp-collective tcgen05 op
+      const int load = j / SUBS;
+      if (!warp_wait(BAR_S + 8u * uint32_t(load % NS), uint32_t(load / NS) & 1u, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const int k0 = t.key_begin + j * BN;
+      uint32_t sr[BN];
+      tc::tmem_ld_row<BN>(tl + uint32_t(s * BN), sr);
+      tc::tmem_ld_wait();
+      auto get = [&](int e) { return __uint_as_float(sr[e]); };
+      auto get2 = [&](int e) { return make_float2(get(e), get(e + 1)); };
+      auto put2 = [&](int e, float2 v) {
+        sr[e] = __float_as_uint(v.x);
+        sr[e + 1] = __float_as_uint(v.y);
+      };
+      // ---- the modified scores, in log2 units once multiplied by a.mul
+      if constexpr (CAP) {
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) {
+          // the shortest polynomial that holds for all of these 32 x 32 scores
+          float am = 0.f, an = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            am = fmaxf(am, fmaxf(fabsf(get(c + e)), fabsf(get(c + e + 1))));
+            an = fmaxf(an, fmaxf(fabsf(get(c + e + 2)), fabsf(get(c + e + 3))));
+          }
+          const float most = valid ? fmaxf(am, an) * a.cap_in : 0.f;
+          if (__all_sync(0xffffffffu, most <= 0.5f)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 u = __fmul2_rn(get2(c + e), a.cap_in2);
+              const float2 v = __fmul2_rn(u, u);
+              float2 p = __ffma2_rn(a.cap_near2[3], v, a.cap_near2[2]);
+              p = __ffma2_rn(p, v, a.cap_near2[1]);
+              p = __ffma2_rn(p, v, a.cap_near2[0]);
+              put2(c + e, __fmul2_rn(u, p));
+            }
+          } else if (__all_sync(0xffffffffu, most <= 1.f)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 u = __fmul2_rn(get2(c + e), a.cap_in2);
+              const float2 v = __fmul2_rn(u, u);
+              float2 p = a.cap_poly2[kTanhTerms - 1];
+#pragma unroll
+              for (int k = kTanhTerms - 2; k >= 0; --k) p = __ffma2_rn(p, v, a.cap_poly2[k]);
+              put2(c + e, __fmul2_rn(u, p));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              sr[c + e] = __float_as_uint(a.cap_out * tanh_exp(get(c + e) * a.cap_in));
+          }
+        }
+      }
+      if constexpr (SLOPES) {
+        const float scale = CAP ? 1.f : a.scale_log2;  // (a cap has taken it in)
+        const float2 scale2 = make_float2(scale, scale);
+        const float away = float(k0 - rm.pos);
+        if (k0 + BN - 1 <= pos_min) {
+          // every key lies behind every row: -slope (pos - key) is linear in it
+          float2 in8[4];  // within a group of eight keys
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            in8[u] = make_float2(rm.slope * float(2 * u), rm.slope * float(2 * u + 1));
+#pragma unroll
+          for (int e = 0; e < BN; e += 8) {
+            const float b = rm.slope * (away + float(e));
+            const float2 b2 = make_float2(b, b);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              put2(e + 2 * u, __ffma2_rn(get2(e + 2 * u), scale2, __fadd2_rn(b2, in8[u])));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            sr[e] = __float_as_uint(
+                fmaf(-rm.slope, fabsf(away + float(e)), get(e) * scale));
+        }
+      }
+      if (k0 < lo_max || k0 + BN > lim_min) {
+        const int from = rm.lo - k0;
+        const uint32_t span = uint32_t(max(0, lim - rm.lo));
+#pragma unroll
+        for (int e = 0; e < BN; ++e)
+          if (uint32_t(e - from) >= span) sr[e] = 0xff800000u;  // -inf
+      }
+      // ---- the row's reference: that of tile j - 1, raised if need be
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < BN; e += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          mx4[u] = fmaxf(mx4[u], fmaxf(get(e + 2 * u), get(e + 2 * u + 1)));
+      float mx = a.mul * fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      if (!valid) mx = 0.f;
+      if (j == 0) {
+        m_ref = mx;
+      } else {
+        const int p = (j - 1) & 1;
+        if (!warp_wait(BAR_H + 8u * (4 * p + (warp & 3)), uint32_t((j - 1) >> 1) & 1u,
+                       abort_flag)) {
+          ok = false;
+          break;
+        }
+        const float m_prev = ref[p * BM + i];
+        if (m_prev > m_ref) {
+          l *= rxk::fast_exp2(m_ref - m_prev);  // 0 from -inf
+          m_ref = m_prev;
+        }
+        const bool empty = m_ref == -INFINITY;  // no weight yet: O is 0
+        const bool grow = !empty && mx > m_ref + kRaise;
+        if (__any_sync(0xffffffffu, grow)) {
+          // O is rescaled once PV_{j-1} has written it.  (Its barrier cannot be a
+          // phase behind: tile j - 1's scores were issued after PV_{j-1-NB} completed,
+          // and are done.)
+          if (!warp_wait(BAR_PF + 8u * uint32_t((j - 1) % NB), uint32_t((j - 1) / NB) & 1u,
+                         abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const float alpha = grow ? rxk::fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tc::tmem_ld32(tl + uint32_t(Lo::O_COL + c), r);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tc::tmem_st32(tl + uint32_t(Lo::O_COL + c), r);
+          }
+          tc::tmem_st_wait();
+          tc::tc_fence_before();
+          if (grow) {
+            l *= alpha;
+            m_ref = mx;
+          }
+        }
+        if (empty) m_ref = mx;
+      }
+      // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
+      ref[(j & 1) * BM + i] = m_ref;
+      warp_arrive(BAR_H + 8u * uint32_t(4 * (j & 1) + (warp & 3)));
+      // ---- weights: bf16 into TMEM over S, their sum in fp32 before the rounding
+      // (lse is then good to fp32, and o to the roundings of its weights)
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      const float2 neg2 = make_float2(-m_use, -m_use);
+      float2 l4[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = __ffma2_rn(get2(c + e), a.mul2, neg2);
+          const float2 p = make_float2(rxk::fast_exp2(x.x), rxk::fast_exp2(x.y));
+          l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
+          pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
+        }
+        tmem_st16(tl + uint32_t(s * BN + c / 2), pk);
+      }
+      const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+      l += lt.x + lt.y;
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      warp_arrive(BAR_P + 8u * s);
+    }
+    // The final barrier completes after every MMA of the CTA; then the stages are
+    // idle and the warpgroups exchange their rows' (m, l).  Every softmax thread
+    // arrives, so no waiter is left behind when a wait gave up.
+    const bool fin = ok && n_tiles > 0 && warp_wait(BAR_FIN, 0, abort_flag);
+    float2* xch = reinterpret_cast<float2*>(gbase + Lo::XCH);  // [NW][BM]
+    if (fin) xch[wg * BM + i] = make_float2(m_ref, l);
+    warp_arrive(BAR_X);
+    const bool xok = warp_wait(BAR_X, 0, abort_flag);
+    if (fin && xok && wg < 2) {
+      tc::tc_fence_after();
+      float m_fin = m_ref;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m_fin = fmaxf(m_fin, xch[w * BM + i].x);
+      float l_all = 0.f;
+      if (m_fin > -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 x = xch[w * BM + i];
+          l_all += x.y * rxk::fast_exp2(x.x - m_fin);
+        }
+      }
+      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      // Warpgroup w writes columns [w D/2, (w+1) D/2), through shared memory so
+      // that each warp stores whole row segments.
+      constexpr int HC = D / 2, PITCH = Lo::PITCH, LPR = HC / 4;
+      const bool narrow = !DECODE && a.out_bf16;
+      uint8_t* stage = gbase + Lo::K0 + wg * (BM * PITCH);
+#pragma unroll 1
+      for (int c = 0; c < HC; c += 32) {
+        uint32_t r[32];
+        tc::tmem_ld32(tl + uint32_t(Lo::O_COL + wg * HC + c), r);
+        tc::tmem_ld_wait();
+        float4* s4 = reinterpret_cast<float4*>(stage + i * PITCH + c * 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          s4[e] = make_float4(__uint_as_float(r[4 * e]) * inv, __uint_as_float(r[4 * e + 1]) * inv,
+                              __uint_as_float(r[4 * e + 2]) * inv,
+                              __uint_as_float(r[4 * e + 3]) * inv);
+      }
+      __syncwarp();
+      const int qrow = (warp & 3) * 32;  // first row of this warp's quadrant
+      unsigned long long my_dst = 0ull;
+      if (valid) {
+        const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * HC;
+        my_dst = narrow ? reinterpret_cast<unsigned long long>(reinterpret_cast<bf16*>(a.out) + at)
+                        : reinterpret_cast<unsigned long long>((DECODE ? a.ws_o : a.out) + at);
+      }
+#pragma unroll 4
+      for (int k = 0; k < LPR; ++k) {
+        const int idx = k * 32 + lane;
+        const int rr = idx / LPR, c4 = idx - rr * LPR;  // row within the quadrant, float4
+        const unsigned long long rd = __shfl_sync(0xffffffffu, my_dst, rr);
+        const float4 v = *reinterpret_cast<const float4*>(stage + (qrow + rr) * PITCH + c4 * 16);
+        if (!rd) continue;
+        if (narrow)
+          reinterpret_cast<uint2*>(rd)[c4] =
+              make_uint2(rxk::pack_bf16(v.x, v.y), rxk::pack_bf16(v.z, v.w));
+        else
+          reinterpret_cast<float4*>(rd)[c4] = v;
+      }
+      if (valid && wg == 0)
+        (DECODE ? a.ws_lse : a.lse)[(DECODE ? part : qi) * a.hq + head] =
+            l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_all);
+    } else if (n_tiles <= 0 && valid && wg < 2) {
+      // no row of the tile sees a key (decode: at this step of the plan)
+      const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * (D / 2);
+      const bool narrow = !DECODE && a.out_bf16;
+      uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
+                          : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
+      const int n = narrow ? D / 16 : D / 8;
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (wg == 0) (DECODE ? a.ws_lse : a.lse)[(DECODE ? part : qi) * a.hq + head] = -INFINITY;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) atomicOr(&g_tc_error, 2);
+  if (warp == SW) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, Lo::TMEM_COLS);
+  }
+}
+
+// Extend: one tile per CTA, the heaviest row tiles first; heads as in
+// attention_tc.cu.
+template <int D, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(kExtendThreads, 1)
+    extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int c = int(blockIdx.x);
+  const int hkv = a.hq / a.group;
+  const int tile = a.heads_interleaved ? c / hkv : c % a.num_tiles;
+  const int kvh = a.heads_interleaved ? c - tile * hkv : c / a.num_tiles;
+  tile4<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, tile, kvh);
+}
+
+// Decode: tiles of the plan's large items, then warp-role units of its small ones
+// from a shared counter, as in attention_tc.cu's decode kernel (nothing is read
+// before the kernels ahead of it are done).
+template <int D>
+struct FusedMod {
+  static constexpr int PIPE_BYTES = kPipeWarps * PipeCfg<D>::WARP_BYTES + 1024;
+  static constexpr int TILE_BYTES = Layout4<D>::BYTES;
+  static constexpr int SMEM = TILE_BYTES > PIPE_BYTES ? TILE_BYTES : PIPE_BYTES;
+  static_assert(SMEM <= 227 * 1024, "a decode CTA fits in shared memory");
+};
+
+template <int D, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(kDecodeThreads, 1)
+    decode_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
+  using Cfg = PipeCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  rxk::griddep_launch_dependents();
+  const int cta = int(blockIdx.x) - a.n_warp_first;
+  if (cta >= 0 && cta < a.n_tc_ctas) {
+    const int hkv = a.hq / a.group;
+    tile4<D, kDecodeGroups, true, CAP, SLOPES>(a, maps, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
+  }
+  if (threadIdx.x >= kPipeWarps * 32) return;  // the warp role uses the first six warps
+  rxk::griddep_wait();
+  const uint32_t raw = rxk::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const int warp = int(threadIdx.x >> 5);
+  const int lane = int(threadIdx.x & 31);
+  const uint32_t ring = base + uint32_t(warp * Cfg::WARP_BYTES);
+  int32_t* slot_buf = reinterpret_cast<int32_t*>(smem_raw + (base - raw) + warp * Cfg::WARP_BYTES +
+                                                 Cfg::STAGES * Cfg::STAGE_BYTES);
+  uint32_t gstep = 0;
+  NextUnit cur, nxt;
+  cur.stage = 0;
+  while (cur.stage < 3) next_unit_step(a, cur);
+  while (cur.idx < a.n_small_units) {
+    nxt.stage = 0;
+    const int rows = cur.word(6);
+    if (rows <= 8) {
+      pipe_unit<1, D, true, CAP, SLOPES>(a, ring, slot_buf, gstep, cur, nxt);
+    } else if constexpr (D == 128) {
+      pipe_unit<2, D, true, CAP, SLOPES>(a, ring, slot_buf, gstep, cur, nxt);
+    } else if (lane == 0) {
+      atomicOr(&g_tc_error, 1);  // the plan gives head_dim 256 no such item
+    }
+    while (nxt.stage < 3) next_unit_step(a, nxt);
+    cur = nxt;
+  }
+}
+
+bool make_maps(Maps4* m, const rx_pool_desc* pool, int BN) {
+  const CUtensorMap *k, *v, *k16, *v16;
+  if (!pool_maps(pool, BN, &k, &v)) return false;
+  m->k = *k;
+  m->v = *v;
+  if (!pool_maps(pool, kGroup, &k16, &v16)) return false;
+  m->k16 = *k16;
+  m->v16 = *v16;
+  return true;
+}
+
+void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* d_q,
+                int32_t num_q_heads, const int32_t* table, int64_t row_stride, float scale,
+                const rx_score_mod& m) {
+  const int D = pool->head_dim;
+  const int64_t rows = int64_t(layer) * pool->num_kv_heads * pool->num_slots;
+  a->q = static_cast<const bf16*>(d_q);
+  a->kpool = static_cast<const bf16*>(pool->k_pool) + rows * D;
+  a->vpool = static_cast<const bf16*>(pool->v_pool) + rows * D;
+  a->head_stride = pool->num_slots * D;
+  a->num_slots = pool->num_slots;
+  a->table = table;
+  a->row_stride = row_stride;
+  a->hq = num_q_heads;
+  a->group = num_q_heads / pool->num_kv_heads;
+  a->scale_log2 = scale * kLog2e;
+  a->tma_row_base = rows;
+  a->tma_head_rows = pool->num_slots;
+  a->cap_in = m.softcap > 0.f ? scale / m.softcap : 0.f;
+  a->cap_out = m.softcap * kLog2e;
+  a->cap_in2 = make_float2(a->cap_in, a->cap_in);
+  for (int i = 0; i < kTanhTerms; ++i) {
+    a->cap_poly[i] = kTanh[i] * a->cap_out;
+    a->cap_poly2[i] = make_float2(a->cap_poly[i], a->cap_poly[i]);
+  }
+  for (int i = 0; i < kTanhNearTerms; ++i)
+    a->cap_near2[i] = make_float2(kTanhNear[i] * a->cap_out, kTanhNear[i] * a->cap_out);
+  a->window = m.window;
+  a->slopes = m.d_slopes;
+  a->key_begin = m.d_key_begin;
+  a->bidir_end = m.d_bidir_end;
+  a->ctx_len = m.d_ctx_len;
+  a->mul = a->cap_in != 0.f || m.d_slopes ? 1.f : a->scale_log2;
+  a->mul2 = make_float2(a->mul, a->mul);
+}
+
+template <int D, bool CAP, bool SLOPES>
+rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
+                            cudaStream_t s) {
+  using Lo = Layout4<D>;
+  static std::atomic<bool> configured[kMaxDevices];
+  const rx_status cs = ensure_smem(configured, extend_mod_kernel<D, CAP, SLOPES>, Lo::BYTES);
+  if (cs != RX_OK) return cs;
+  Maps4 maps;
+  if (!make_maps(&maps, pool, Lo::BS))
+    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+  extend_mod_kernel<D, CAP, SLOPES><<<ctas, kExtendThreads, Lo::BYTES, s>>>(a, maps);
+  return rx_internal::launch_status("rx_extend_attention_mod");
+}
+
+template <int D, bool CAP, bool SLOPES>
+rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
+                            cudaStream_t s) {
+  static std::atomic<bool> configured[kMaxDevices];
+  const rx_status cs =
+      ensure_smem(configured, decode_mod_kernel<D, CAP, SLOPES>, FusedMod<D>::SMEM);
+  if (cs != RX_OK) return cs;
+  Maps4 maps;
+  if (!make_maps(&maps, pool, Layout4<D>::BS))
+    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+  decode_mod_kernel<D, CAP, SLOPES><<<ctas, kDecodeThreads, FusedMod<D>::SMEM, s>>>(a, maps);
+  return rx_internal::launch_status("rx_decode_attention_mod");
+}
+
+// By modification: none (masks), cap, slopes, both.
+using Launch = rx_status (*)(const TcArgs&, const rx_pool_desc*, unsigned, cudaStream_t);
+constexpr Launch kExtend128[4] = {
+    launch_extend_mod<128, false, false>, launch_extend_mod<128, true, false>,
+    launch_extend_mod<128, false, true>, launch_extend_mod<128, true, true>};
+constexpr Launch kExtend256[4] = {
+    launch_extend_mod<256, false, false>, launch_extend_mod<256, true, false>,
+    launch_extend_mod<256, false, true>, launch_extend_mod<256, true, true>};
+constexpr Launch kDecode128[4] = {
+    launch_decode_mod<128, false, false>, launch_decode_mod<128, true, false>,
+    launch_decode_mod<128, false, true>, launch_decode_mod<128, true, true>};
+constexpr Launch kDecode256[4] = {
+    launch_decode_mod<256, false, false>, launch_decode_mod<256, true, false>,
+    launch_decode_mod<256, false, true>, launch_decode_mod<256, true, true>};
+
+rx_status pick(int D, const rx_score_mod& m, const Launch (&f128)[4], const Launch (&f256)[4],
+               const TcArgs& a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
+  const int which = (m.softcap > 0.f ? 1 : 0) | (m.d_slopes ? 2 : 0);
+  return (D == 128 ? f128[which] : f256[which])(a, pool, ctas, s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+namespace rx_internal {
+
+int32_t mod_error_flags(bool clear) {
+  int32_t v = 0;
+  cudaMemcpyFromSymbol(&v, g_tc_error, sizeof(v));
+  if (clear && v) {
+    int32_t z = 0;
+    cudaMemcpyToSymbol(g_tc_error, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace rx_internal
+
+// What both attention calls with modified scores check of them.
+static rx_status check_mod(const rx_score_mod* mod, int32_t out_type) {
+  if (out_type != RX_OUT_F32 && out_type != RX_OUT_BF16)
+    return rx_internal::set_error(RX_ERR_INVALID, "attention: unknown out_type");
+  if (mod && (!(mod->softcap >= 0.f) || !isfinite(mod->softcap)))
+    return rx_internal::set_error(RX_ERR_INVALID, "score mod: softcap < 0 or not finite");
+  if (mod && mod->window < 0)
+    return rx_internal::set_error(RX_ERR_INVALID, "score mod: window < 0");
+  return RX_OK;
+}
+
+extern "C" rx_status rx_extend_attention_mod(
+    const rx_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
+    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_req_rows,
+    const int32_t* d_prefix_len, const int32_t* d_qo_indptr, const int32_t* d_tile_indptr,
+    int32_t R, int64_t num_tiles, float scale, const rx_score_mod* mod, void* d_out,
+    int32_t out_type, float* d_lse, rx_stream_t stream) {
+  rx_status st = rx_internal::check_pool(pool, layer);
+  if (st == RX_OK) st = check_mod(mod, out_type);
+  if (st != RX_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: Hq % Hkv != 0");
+  if (R < 0 || num_tiles < 0 || num_tiles * pool->num_kv_heads > INT32_MAX)
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: bad R or num_tiles");
+  if (R == 0 || num_tiles == 0) return RX_OK;
+  if (!d_q || !d_req_to_token || !d_req_rows || !d_prefix_len || !d_qo_indptr ||
+      !d_tile_indptr || !d_out || !d_lse || !aligned16(d_q) || !aligned16(d_out))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: NULL or misaligned");
+  if (!(scale > 0.f) || !isfinite(scale))
+    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: scale must be above 0");
+  const int D = pool->head_dim;
+  const rx_score_mod none{};
+  TcArgs a{};
+  set_common(&a, pool, layer, d_q, num_q_heads, d_req_to_token, row_stride, scale,
+             mod ? *mod : none);
+  a.req_rows = d_req_rows;
+  a.prefix_len = d_prefix_len;
+  a.qo_indptr = d_qo_indptr;
+  a.tile_indptr = d_tile_indptr;
+  a.num_req = R;
+  a.num_tiles = int(num_tiles);
+  // heads interleaved as in rx_extend_attention; a window bounds a tile's keys
+  const int64_t keys = a.window > 0 ? std::min<int64_t>(row_stride, a.window) : row_stride;
+  const int64_t ctas = num_tiles * pool->num_kv_heads;
+  a.heads_interleaved =
+      ctas <= int64_t(kExtendInterleaveWaves) * rx_internal::sm_count() ||
+      keys * pool->num_kv_heads * int64_t(D) * 4 <= kExtendInterleaveKvBytes;
+  a.out = static_cast<float*>(d_out);
+  a.lse = d_lse;
+  a.out_bf16 = out_type == RX_OUT_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return pick(D, mod ? *mod : none, kExtend128, kExtend256, a, pool, unsigned(ctas), s);
+}
+
+extern "C" rx_status rx_decode_attention_mod(
+    const rx_pool_desc* pool, int32_t layer, const void* d_q, int32_t num_q_heads,
+    const int32_t* d_req_to_token, int64_t row_stride, const int32_t* d_plan,
+    const rx_decode_plan_info* info, int32_t B, int32_t step, float scale,
+    const rx_score_mod* mod, void* d_out, int32_t out_type, float* d_lse, void* d_workspace,
+    size_t workspace_bytes, rx_stream_t stream) {
+  rx_status st = rx_internal::check_pool(pool, layer);
+  if (st == RX_OK) st = check_mod(mod, out_type);
+  if (st != RX_OK) return st;
+  auto bad = [](const char* why) { return rx_internal::set_error(RX_ERR_INVALID, why); };
+  if (!info || num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0 || B < 0 || step < 0)
+    return bad("rx_decode_attention_mod: bad argument");
+  if (B == 0) return RX_OK;
+  if (int64_t(workspace_bytes) < info->workspace_bytes || !d_workspace || !aligned16(d_workspace))
+    return bad("rx_decode_attention_mod: workspace missing, small or misaligned");
+  if (!d_q || !d_req_to_token || !d_plan || !d_out || !d_lse || !aligned16(d_q) ||
+      !aligned16(d_out))
+    return bad("rx_decode_attention_mod: NULL or misaligned");
+  if (!(scale > 0.f) || !isfinite(scale))
+    return bad("rx_decode_attention_mod: scale must be above 0");
+  if (mod && (mod->window > 0 || mod->d_slopes) && !mod->d_ctx_len)
+    return bad("rx_decode_attention_mod: a window or slopes need d_ctx_len");
+  const int64_t n_small = info->n_work - info->n_work_tc;
+  if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
+      info->n_work > INT32_MAX / pool->num_kv_heads)
+    return bad("rx_decode_attention_mod: bad plan info");
+  const int D = pool->head_dim;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t o_bytes = (info->n_parts * num_q_heads * int64_t(D) * 4 + 255) / 256 * 256;
+  const int64_t l_bytes = (info->n_parts * num_q_heads * 4 + 255) / 256 * 256;
+  char* ws = static_cast<char*>(d_workspace);
+  float* ws_o = reinterpret_cast<float*>(ws);
+  float* ws_lse = reinterpret_cast<float*>(ws + o_bytes);
+  int32_t* counter = reinterpret_cast<int32_t*>(ws + o_bytes + l_bytes);
+  const rx_score_mod none{};
+  if (info->n_work > 0) {
+    TcArgs a{};
+    set_common(&a, pool, layer, d_q, num_q_heads, d_req_to_token, row_stride, scale,
+               mod ? *mod : none);
+    const int64_t hkv = pool->num_kv_heads;
+    const int64_t small_units = n_small * hkv, tc_ctas = info->n_work_tc * hkv;
+    // CTAs as in rx_decode_attention: the tiles, and CTAs for the warp-role units
+    // behind them when all fit in one wave, else some before them
+    const int64_t sms = rx_internal::sm_count();
+    const int64_t unit_ctas = (small_units + kPipeWarps - 1) / kPipeWarps;
+    int64_t warp_first = 0, ctas = tc_ctas;
+    if (tc_ctas + unit_ctas <= sms)
+      ctas = tc_ctas + unit_ctas;
+    else if (tc_ctas >= sms)
+      warp_first = std::min<int64_t>(unit_ctas, (sms + 3) / 4);
+    else
+      ctas = sms;
+    ctas += warp_first;
+    a.work_small = d_plan + info->off_work;
+    a.work = a.work_small + n_small * RX_WORK_WORDS;
+    a.members = d_plan + info->off_members;
+    a.ws_o = ws_o;
+    a.ws_lse = ws_lse;
+    a.n_small_units = int(small_units);
+    a.n_tc_ctas = int(tc_ctas);
+    a.n_warp_first = int(warp_first);
+    a.unit_counter = counter;
+    a.step = step;
+    if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
+      return rx_internal::launch_status("rx_decode_attention_mod: counter reset");
+    st = pick(D, mod ? *mod : none, kDecode128, kDecode256, a, pool, unsigned(ctas), s);
+    if (st != RX_OK) return st;
+  }
+  return rx_internal::merge_parts(D, d_plan + info->off_req_part_indptr,
+                                  d_plan + info->off_req_parts, ws_o, ws_lse, num_q_heads, B,
+                                  d_out, out_type == RX_OUT_BF16, d_lse, info->n_work > 0, s,
+                                  "rx_decode_attention_mod: merge");
+}
+

@@ -35,190 +35,9 @@
 // Every mbarrier wait is bounded (about 2 s); on a timeout the CTA sets an
 // error bit, drains its tensor-core work and frees TMEM before returning.
 
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-#include <stdio.h>
-
-#include <algorithm>
-#include <atomic>
-
-#include "ptx_util.cuh"
-#include "rx.h"
-#include "rx_internal.h"
-#include "tc_util.cuh"
-
-// Bit 0: a slot outside [0, num_slots) was read (slot 0 used instead);
-// bit 1: a barrier wait timed out; bit 2: a tile found its dynamic shared
-// memory off a 1024-byte boundary and did nothing.  Read by rx_device_check().
-static __device__ int32_t g_tc_error;
-
+#include "attention_tile.cuh"
 
 namespace {
-
-using bf16 = __nv_bfloat16;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (~2 s)
-constexpr float kRescaleThreshold = 8.0f;       // log2 units
-constexpr uint32_t kSleepNs = 0;                // MMA / loader waits: plain try_wait polling
-constexpr float kMasked = -1.0e30f;             // raw score of a masked key
-constexpr int kExtendInterleaveWaves = 8;
-// Extend CTA order: heads interleaved also when one request's keys over all
-// KV heads (K and V, bf16) take at most this much: the row tiles in flight
-// then read a few requests' keys, which stay in L2 for every head at once.
-constexpr int64_t kExtendInterleaveKvBytes = 32ll << 20;
-constexpr int BM = 128;
-
-struct TcArgs {
-  const bf16* q;
-  const bf16* kpool;  // layer base, [Hkv][num_slots][D]
-  const bf16* vpool;
-  int64_t head_stride;
-  int64_t num_slots;
-  const int32_t* table;
-  int64_t row_stride;
-  int hq;
-  int group;
-  float scale_log2;
-  // extend
-  const int32_t* req_rows;
-  const int32_t* prefix_len;
-  const int32_t* qo_indptr;
-  const int32_t* tile_indptr;
-  int num_req;
-  int num_tiles;
-  int heads_interleaved;   // extend CTA order: 1 = tile-major over heads, 0 = head-major
-  float* out;
-  float* lse;
-  int64_t tma_row_base;  // row of (layer, KV head 0, slot 0) in the tensor maps
-  int64_t tma_head_rows; // rows per KV head (num_slots)
-  // decode
-  const int32_t* work;     // tensor-core items
-  const int32_t* members;
-  float* ws_o;
-  float* ws_lse;
-  // fused decode: warp-role items (<= 16 rows) and the step's new tokens
-  const int32_t* work_small;
-  int n_small_units;       // warp-role (item, KV head) units
-  int n_tc_ctas;           // tensor-core CTAs
-  int n_warp_first;        // warp-role-only CTAs placed before them
-  int* unit_counter;       // next warp-role unit to take (0 at launch)
-  int tiles_leave;         // decode: tile CTAs exit after their tile
-  int early_inputs;        // decode: the tiles may read Q and shared-segment keys
-                           // before griddepcontrol.wait (see decode_fused)
-  int step;                // step index within a multi-step plan
-  const bf16* k_new;       // bf16 [B][Hkv][D] of the step's tokens, or NULL
-  const bf16* v_new;
-  const int32_t* slots_new;
-  // modified scores (the MOD kernels only; rx_score_mod)
-  float cap_in;            // scale / softcap, 0: no cap
-  float cap_out;           // softcap * log2(e)
-  int window;              // 0: none
-  const float* slopes;
-  const int32_t* key_begin;
-  const int32_t* bidir_end;
-  const int32_t* ctx_len;
-  int out_bf16;
-};
-
-struct TileDesc {
-  const int32_t* trow;
-  int key_begin, key_end, nomask_end, n_rows;
-  int gr0, q_base, prefix;
-  int member_off, part_base;
-  int bidir;  // MOD: keys before it are seen by every row
-};
-
-template <bool DECODE, bool MOD>
-__device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
-  TileDesc t;
-  if constexpr (DECODE) {
-    const int32_t* w = a.work + int64_t(bx) * RX_WORK_WORDS;
-    t.trow = a.table + int64_t(w[0]) * a.row_stride;
-    t.key_begin = w[1];
-    t.key_end = w[7] > 0 ? min(w[2], w[7] + a.step) : w[2];
-    t.member_off = w[3];
-    t.part_base = w[5];
-    t.n_rows = w[6];
-    t.nomask_end = t.key_end;
-    t.gr0 = t.q_base = t.prefix = t.bidir = 0;
-  } else {
-    const int tile = a.num_tiles - 1 - bx;  // heaviest first
-    // the request of this tile: the last r with tile_indptr[r] <= tile, found
-    // by the warp in rounds of 32 samples (each round one load per lane and
-    // a ballot) instead of a binary search's chain of dependent loads, which
-    // held every CTA's start-up for several microseconds
-    const int ln = int(threadIdx.x & 31);
-    int lo = 0, hi = a.num_req;
-    while (hi - lo > 32) {
-      const int step = (hi - lo + 31) >> 5;
-      const int p = lo + ln * step;
-      const bool le = p < hi && __ldg(a.tile_indptr + p) <= tile;
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // lane 0's sample is <= tile
-      lo = lo + k * step;
-      hi = min(hi, lo + step);
-    }
-    {
-      const int p = lo + ln;
-      const bool le = p < hi && __ldg(a.tile_indptr + p) <= tile;
-      lo += 31 - __clz(__ballot_sync(0xffffffffu, le));
-    }
-    const int G = a.group;
-    t.q_base = a.qo_indptr[lo];
-    const int s_r = a.qo_indptr[lo + 1] - t.q_base;
-    t.prefix = a.prefix_len[lo];
-    t.trow = a.table + int64_t(a.req_rows[lo]) * a.row_stride;
-    t.gr0 = (tile - a.tile_indptr[lo]) * BM;
-    t.n_rows = min(BM, s_r * G - t.gr0);
-    t.key_begin = 0;
-    t.key_end = t.prefix + (t.gr0 + t.n_rows - 1) / G + 1;
-    t.nomask_end = t.prefix + t.gr0 / G + 1;
-    t.member_off = t.part_base = 0;
-    if constexpr (MOD) {
-      // the keys that some row of the tile sees lie in [key_begin, key_end)
-      const int tok0 = t.gr0 / G, tok1 = (t.gr0 + t.n_rows - 1) / G;
-      t.bidir = a.bidir_end ? min(__ldg(a.bidir_end + lo), t.prefix + s_r) : 0;
-      t.key_end = max(t.key_end, t.bidir);
-      if (a.window > 0) t.key_begin = max(0, t.prefix + tok0 - a.window + 1);
-      if (a.key_begin) {
-        int least = INT32_MAX;
-        for (int tok = tok0 + ln; tok <= tok1; tok += 32)
-          least = min(least, __ldg(a.key_begin + t.q_base + tok));
-        t.key_begin = max(t.key_begin, __reduce_min_sync(0xffffffffu, least));
-      }
-    }
-  }
-  return t;
-}
-
-// row i -> (query index, head, part index for decode, causal limit)
-template <bool DECODE>
-__device__ __forceinline__ void row_info(const TcArgs& a, const TileDesc& t, int kvh, int i,
-                                         int64_t& qi, int& head, int64_t& part, int& lim) {
-  const int G = a.group;
-  if constexpr (DECODE) {
-    const int unit = i / G;
-    qi = a.members[t.member_off + unit];
-    head = kvh * G + (i - unit * G);
-    part = int64_t(t.part_base) + unit;
-    lim = t.key_end;
-  } else {
-    const int gr = t.gr0 + i;
-    const int tok = gr / G;
-    qi = int64_t(t.q_base) + tok;
-    head = kvh * G + (gr - tok * G);
-    part = 0;
-    lim = t.prefix + tok + 1;
-  }
-}
-
-// 128-byte-swizzled tile of `rows` rows, stored as column blocks of 64 bf16:
-// byte address of 16-byte chunk `ch` (of the full row) of row r.
-__device__ __forceinline__ uint32_t sw128(uint32_t base, int rows, int r, int ch) {
-  return base + uint32_t((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-}
 
 // Tensor-core tile: 128 query rows, key tiles of BN = 128 keys at head_dim
 // 128 and 64 at head_dim 256 (a K or V tile is 32 KB either way), 384
@@ -278,85 +97,7 @@ struct Layout3 {
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
-// D(tmem) (+)= A * B(smem), A from shared memory (ss) or TMEM (ts), issued
-// by a single thread, with the shared-memory descriptors passed as 32-bit
-// halves: the high half (stride between 8-row groups, version, swizzle) is
-// common to every operand of the tile, and the low half (start address >> 4
-// and leading-byte offset) moves by compile-time steps, so the issuing thread
-// spends one add per operand instead of rebuilding 64-bit descriptors.
-__device__ __forceinline__ void mma_ss_split(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 ad, bd;\n setp.ne.b32 p, %5, 0;\n"
-      " mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_split(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 bd;\n setp.ne.b32 p, %5, 0;\n"
-      " mov.b64 bd, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 32 lanes x 16 columns of 32-bit values from registers (thread t: lane t).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-
-// Modified scores (rx_score_mod), in log2 units: what a row adds to a raw
-// score, and the keys [lo, lim) that it sees.
-constexpr float kMaskedRow = -1.0e29f;  // a row whose maximum is not above it saw no key
-struct RowMod {
-  int lo = 0;
-  float slope = 0.f;  // slope of the row's head times log2(e)
-  float pos = 0.f;    // the query's position
-};
-
-// position `pos`, first key `begin` of its own (if any)
-__device__ __forceinline__ RowMod row_mod(const TcArgs& a, int64_t qi, int head, int pos) {
-  RowMod r;
-  if (a.window > 0) r.lo = max(0, pos - a.window + 1);
-  if (a.key_begin) r.lo = max(r.lo, __ldg(a.key_begin + qi));
-  if (a.slopes) r.slope = __ldg(a.slopes + head) * kLog2e;
-  r.pos = float(pos);
-  return r;
-}
-
-// tanh(u) for |u| <= 1: u times the polynomial in u^2 of degree 6 that is nearest
-// to tanh(u) / u there by relative error (Remez exchange): 5e-8 in exact
-// arithmetic, 1.6e-7 in fp32.
-__device__ __forceinline__ float tanh_small(float u) {
-  const float v = u * u;
-  float p = fmaf(0.0010410226f, v, -0.006203379f);
-  p = fmaf(p, v, 0.02028998f);
-  p = fmaf(p, v, -0.05345703f);
-  p = fmaf(p, v, 0.13325204f);
-  p = fmaf(p, v, -0.3333284f);
-  p = fmaf(p, v, 0.99999994f);
-  return u * p;
-}
-// tanh(u) = 1 - 2 / (1 + e^2u), off by some 2^-22 at most: for |u| > 1
-__device__ __forceinline__ float tanh_large(float u) {
-  return fmaf(-2.f, __fdividef(1.f, 1.f + rxk::fast_exp2(u * (2.f * kLog2e))), 1.f);
-}
-// softcap * tanh(scale * s / softcap) * log2(e)
-__device__ __forceinline__ float capped(const TcArgs& a, float s) {
-  const float u = s * a.cap_in;
-  return a.cap_out * (fabsf(u) <= 1.f ? tanh_small(u) : tanh_large(u));
-}
-
-template <int D, bool DECODE, bool MOD>
+template <int D, bool DECODE>
 __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk,
                                          const CUtensorMap* tmv, uint8_t* smem_raw, int bx,
                                          int kvh) {
@@ -401,9 +142,8 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const TileDesc t = describe<DECODE, MOD>(a, bx);
-  const int n_tiles =
-      MOD && t.key_begin >= t.key_end ? 0 : (t.key_end - t.key_begin + BN - 1) / BN;
+  const TileDesc t = describe<DECODE, false>(a, bx);
+  const int n_tiles = (t.key_end - t.key_begin + BN - 1) / BN;
   // Softmax threads: the query row of their TMEM lane, and the gather of
   // half of Q row i, issued before the barriers and TMEM are set up so the
   // copies overlap that start-up (nothing else uses the Q buffer yet; the
@@ -417,7 +157,6 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
   int64_t qi = 0, part = 0;
   int head = 0, lim = t.key_end;
   bool valid = false;
-  RowMod rm;
   if (warp < 8) {
     valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
     if (valid) row_info<DECODE>(a, t, kvh, row, qi, head, part, lim);
@@ -439,13 +178,6 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
     // stream are done; with early inputs the queries are complete already
     // and only the partial writes wait
     if (!DECODE || !a.early_inputs) rxk::griddep_wait();
-    if constexpr (MOD) {
-      if (valid) {
-        const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
-        if (!DECODE) lim = max(lim, t.bidir);
-        rm = row_mod(a, qi, head, pos);
-      }
-    }
     // chunks [8 w, 8 w + 8) of Q row i (zeros past the tile's rows) while
     // the loader warps already stream the first K/V tiles
     const bf16* src = a.q + (gqi * a.hq + ghead) * D;
@@ -715,12 +447,6 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
     tc::mbar_arrive(BAR_Q);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
-    // MOD: keys [lo_max, lim_min) are seen by every row of the warp
-    int lo_max = 0, lim_min = 0;
-    if constexpr (MOD) {
-      lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
-      lim_min = __reduce_min_sync(0xffffffffu, lim);
-    }
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % NB;  // S buffer
       // waits are made warp-uniform before any warp-collective tcgen05 op
@@ -731,8 +457,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       }
       tc::tc_fence_after();
       const int k0 = t.key_begin + j * BN + wg * HALF;  // first key of this half
-      const bool need_mask =
-          MOD ? k0 < lo_max || k0 + HALF > lim_min : k0 + HALF > t.nomask_end;
+      const bool need_mask = k0 + HALF > t.nomask_end;
       uint32_t sr[HALF];
       tc::tmem_ld_row<HALF>(tl + uint32_t(s * BN + wg * HALF), sr);
       tc::tmem_ld_wait();
@@ -743,44 +468,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       float mx8[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) mx8[u] = kMasked;
-      if constexpr (MOD) {
-        // the raw scores become modified ones in log2 units, in place
-        if (a.cap_in != 0.f) {
-          float am[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < HALF; ++e)
-            am[e & 3] = fmaxf(am[e & 3], fabsf(__uint_as_float(sr[e])));
-          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-          if (__all_sync(0xffffffffu, most * fabsf(a.cap_in) <= 1.f)) {
-#pragma unroll
-            for (int e = 0; e < HALF; ++e)
-              sr[e] = __float_as_uint(a.cap_out *
-                                      tanh_small(__uint_as_float(sr[e]) * a.cap_in));
-          } else {
-#pragma unroll
-            for (int e = 0; e < HALF; ++e)
-              sr[e] = __float_as_uint(capped(a, __uint_as_float(sr[e])));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < HALF; ++e)
-            sr[e] = __float_as_uint(__uint_as_float(sr[e]) * a.scale_log2);
-        }
-        if (a.slopes) {
-          const float away = float(k0) - rm.pos;
-#pragma unroll
-          for (int e = 0; e < HALF; ++e)
-            sr[e] = __float_as_uint(
-                fmaf(-rm.slope, fabsf(away + float(e)), __uint_as_float(sr[e])));
-        }
-      }
-      if (MOD && need_mask) {
-#pragma unroll
-        for (int e = 0; e < HALF; ++e) {
-          if (k0 + e >= lim || k0 + e < rm.lo) sr[e] = __float_as_uint(kMasked);
-          mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sr[e]));
-        }
-      } else if (need_mask) {
+      if (need_mask) {
 #pragma unroll
         for (int e = 0; e < HALF; ++e) {
           if (k0 + e >= lim) sr[e] = __float_as_uint(kMasked);
@@ -802,7 +490,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
         break;
       }
       const float mx_other = xch[((j & 1) * 2 + (1 - wg)) * BM + i];
-      const float mx = (MOD ? 1.f : a.scale_log2) * fmaxf(mx_half, mx_other);
+      const float mx = a.scale_log2 * fmaxf(mx_half, mx_other);
       const float m_new = fmaxf(m_ref, mx);
       if (j == 0) {
         m_ref = m_new;
@@ -835,9 +523,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
           }
         }
       }
-      // MOD: a row that saw no key yet weighs its masked ones 0
-      const float m_use = MOD ? (m_ref <= kMaskedRow ? 0.f : m_ref)
-                              : (m_ref == -INFINITY) ? 0.f : m_ref;
+      const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       float l8[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) l8[u] = 0.f;
@@ -853,15 +539,6 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
           // would cost up to 1% per weight on peaked rows.  The row sum adds
           // exactly the rounded values in fp32, in eight independent partial
           // sums.
-          if constexpr (MOD) {
-            // the row sum adds the weights before their rounding: lse is then
-            // good to fp32, and o to the roundings of its weights
-            const float p0 = rxk::fast_exp2(__uint_as_float(sr[cc * 32 + e]) - m_use);
-            const float p1 = rxk::fast_exp2(__uint_as_float(sr[cc * 32 + e + 1]) - m_use);
-            l8[(e >> 1) & 7] += p0 + p1;
-            pk[e >> 1] = rxk::pack_bf16(p0, p1);
-            continue;
-          }
           const float x0 = fmaf(__uint_as_float(sr[cc * 32 + e]), a.scale_log2, -m_use);
           const float x1 = fmaf(__uint_as_float(sr[cc * 32 + e + 1]), a.scale_log2, -m_use);
           const uint32_t h = rxk::pack_bf16(rxk::fast_exp2(x0), rxk::fast_exp2(x1));
@@ -900,9 +577,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
         dst = a.ws_o + (part * a.hq + head) * D;
         lse_dst = a.ws_lse + part * a.hq + head;
       } else {
-        dst = a.out + (qi * a.hq + head) * D;  // MOD: of bf16 with out_bf16
-        if (MOD && a.out_bf16)
-          dst = reinterpret_cast<float*>(reinterpret_cast<bf16*>(a.out) + (qi * a.hq + head) * D);
+        dst = a.out + (qi * a.hq + head) * D;
         lse_dst = a.lse + qi * a.hq + head;
       }
       // Warpgroup w owns output columns [w D/2, (w+1) D/2).  Its rows go
@@ -930,35 +605,16 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
       __syncwarp();
       const int qrow = (warp & 3) * 32;  // first row of this warp's quadrant
       const unsigned long long my_dst =
-          valid ? (MOD && !DECODE && a.out_bf16
-                       ? reinterpret_cast<unsigned long long>(reinterpret_cast<bf16*>(dst) + wg * HC)
-                       : reinterpret_cast<unsigned long long>(dst + wg * HC))
-                : 0ull;
+          valid ? reinterpret_cast<unsigned long long>(dst + wg * HC) : 0ull;
 #pragma unroll 4
       for (int k = 0; k < LPR; ++k) {
         const int idx = k * 32 + lane;
         const int rr = idx / LPR, c4 = idx - rr * LPR;  // row within the quadrant, float4
         const unsigned long long rd = __shfl_sync(0xffffffffu, my_dst, rr);
         const float4 v = *reinterpret_cast<const float4*>(stage + (qrow + rr) * PITCH + c4 * 16);
-        if (MOD && !DECODE && a.out_bf16) {
-          if (rd)
-            reinterpret_cast<uint2*>(rd)[c4] =
-                make_uint2(rxk::pack_bf16(v.x, v.y), rxk::pack_bf16(v.z, v.w));
-          continue;
-        }
         if (rd) reinterpret_cast<float4*>(rd)[c4] = v;
       }
-      if (valid && wg == 0)
-        *lse_dst = MOD && l_all == 0.f ? -INFINITY : m_ref * kLn2 + logf(l_all);
-    } else if (MOD && !DECODE && n_tiles <= 0 && valid) {
-      // no row of the tile sees a key
-      const int64_t at = (qi * a.hq + head) * D + wg * (D / 2);
-      uint4* dst = a.out_bf16 ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
-                              : reinterpret_cast<uint4*>(a.out + at);
-      const int n = a.out_bf16 ? D / 16 : D / 8;
-#pragma unroll 1
-      for (int c = 0; c < n; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (wg == 0) a.lse[qi * a.hq + head] = -INFINITY;
+      if (valid && wg == 0) *lse_dst = m_ref * kLn2 + logf(l_all);
     } else if (DECODE && n_tiles <= 0 && valid) {
       // keys that a later step of the plan brings: an empty partial row
       float4* dst = reinterpret_cast<float4*>(a.ws_o + (part * a.hq + head) * D + wg * (D / 2));
@@ -982,8 +638,7 @@ __device__ __forceinline__ void tc_tile3(const TcArgs& a, const CUtensorMap* tmk
 // ones and the last wave is short; otherwise CTA c takes head c / tiles, so
 // the CTAs resident at one time read the keys of one head and those stay in
 // L2.
-// MOD: with modified scores (rx_score_mod).
-template <int D, bool MOD>
+template <int D>
 __global__ void __launch_bounds__(kThreads3, 1)
     attn_tc3_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
@@ -991,406 +646,10 @@ __global__ void __launch_bounds__(kThreads3, 1)
   const int c = int(blockIdx.x);
   if (a.heads_interleaved) {
     const int hkv = a.hq / a.group;
-    tc_tile3<D, false, MOD>(a, &tmk, &tmv, smem_raw, c / hkv, c - (c / hkv) * hkv);
+    tc_tile3<D, false>(a, &tmk, &tmv, smem_raw, c / hkv, c - (c / hkv) * hkv);
   } else {
-    tc_tile3<D, false, MOD>(a, &tmk, &tmv, smem_raw, c % a.num_tiles, c / a.num_tiles);
+    tc_tile3<D, false>(a, &tmk, &tmv, smem_raw, c % a.num_tiles, c / a.num_tiles);
   }
-}
-
-// ---------------------------------------------------------------------------
-// Warp role of the fused decode kernel: work items of <= 16 query rows at
-// head_dim 128, <= 8 at 256 (a request's private tail, or a shared segment
-// chunk with few rows).  One warp owns one (item, KV head) unit and streams its keys
-// in steps of 16.  With few query rows per item the products are computed transposed,
-// keys in the M dimension of mma.sync m16n8k16 and query rows in N (8 or 16
-// rows, NR n-tiles), so no MMA row is wasted on keys:
-//   S^T (16 keys x 8 rows)  = K (16 x D, ldmatrix)        . Q^T (registers)
-//   O^T (D x 8 rows)       += V^T (16 d x 16 keys per m-tile, ldmatrix.trans)
-//                             . P^T (the S^T accumulators, bf16, moved into
-//                               operand layout with four shuffles)
-// A thread of the S^T accumulators holds keys g, g+8 of rows 2c, 2c+1 (g =
-// lane/4, c = lane%4): the running max and sum of a row live in the 8 lanes
-// that share c.  K and V rows of a step are gathered by slot with 16-byte
-// cp.async into a ring of PipeCfg<D>::STAGES stages (one fewer steps in
-// flight) whose rows are padded by 16 B, so ldmatrix reads all 32 banks.
-// The max is rescaled lazily: O and the sum are rescaled only when a row's
-// max grows by more than 2^8.
-constexpr int kPipeWarps = 6;                    // warps of a CTA in the warp role
-constexpr int kSlotBuf = 128;                    // key slots per slot block (x 16 B aligned)
-constexpr int kSlotRegs = kSlotBuf / 32;         // slots of a block per lane
-template <int D>
-struct PipeCfg {
-  static constexpr int STAGES = D == 128 ? 4 : 2;     // ring stages per warp
-  static constexpr int PITCH = 2 * D + 16;            // shared bytes per K/V row
-  static constexpr int STAGE_BYTES = 32 * PITCH;      // 16 K rows, then 16 V rows
-  // the ring, then two slot blocks (the one in use and the next)
-  static constexpr int WARP_BYTES = STAGES * STAGE_BYTES + 2 * kSlotBuf * 4;
-};
-
-// A warp's next warp-role unit, fetched in stages while the current one
-// streams, so that the counter, work-item and slot-table round trips are off
-// the path: stage 1 takes an index from the counter (lane 0), stage 2 loads
-// the item's work words (lane k < 8 holds word k), stage 3 its first block
-// of key slots (lane l holds keys l + 32 i).  idx >= n_small_units: none left.
-struct NextUnit {
-  int idx;  // lane 0 only until stage 2
-  int32_t wk;
-  int32_t s[kSlotRegs];
-  int stage;
-  __device__ __forceinline__ int32_t word(int k) const { return __shfl_sync(0xffffffffu, wk, k); }
-};
-
-__device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
-  const int lane = threadIdx.x & 31;
-  if (n.stage == 0) {
-    n.idx = lane == 0 ? atomicAdd(a.unit_counter, 1) : 0;
-  } else if (n.stage == 1) {
-    n.idx = __shfl_sync(0xffffffffu, n.idx, 0);
-    n.wk = 0;
-    if (n.idx < a.n_small_units && lane < RX_WORK_WORDS)
-      n.wk = __ldg(a.work_small + int64_t(n.idx / (a.hq / a.group)) * RX_WORK_WORDS + lane);
-  } else if (n.stage == 2) {
-    const int32_t row = n.word(0), kb = n.word(1), kend = n.word(2), grow = n.word(7);
-    if (n.idx < a.n_small_units) {
-      const int32_t* trow = a.table + int64_t(row) * a.row_stride;
-      const int ke = grow > 0 ? min(kend, grow + a.step) : kend;
-#pragma unroll
-      for (int i = 0; i < kSlotRegs; ++i) {
-        const int key = kb + lane + 32 * i;
-        n.s[i] = key < ke ? __ldg(trow + key) : -1;
-      }
-    }
-  }
-  if (n.stage < 3) ++n.stage;
-}
-
-template <int NR, int D, bool MOD>
-__device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_t* slot_buf,
-                                          uint32_t& gstep, const NextUnit& cur, NextUnit& nxt) {
-  using Cfg = PipeCfg<D>;
-  constexpr int S = Cfg::STAGES;
-  constexpr int kRowPitch = Cfg::PITCH;
-  constexpr int kStageBytes = Cfg::STAGE_BYTES;
-  constexpr int NK = D / 16;  // k-steps of S^T, m-tiles of O^T
-  const int lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int n_heads_kv = a.hq / a.group;
-  const int unit = cur.idx;
-  const int kvh = unit - (unit / n_heads_kv) * n_heads_kv;
-  const int G = a.group;
-  const int32_t w_row = cur.word(0), w_kend = cur.word(2), w_grow = cur.word(7);
-  const int32_t* trow = a.table + int64_t(w_row) * a.row_stride;
-  const int kb = cur.word(1), member_off = cur.word(3), part_base = cur.word(5),
-            n_rows = cur.word(6);
-  // a private tail of a multi-step plan ends at its step-0 end + step
-  const int ke = w_grow > 0 ? min(w_kend, w_grow + a.step) : w_kend;
-  const bf16* kbase = a.kpool + int64_t(kvh) * a.head_stride;
-  const bf16* vbase = a.vpool + int64_t(kvh) * a.head_stride;
-
-  // The unit whose chunk holds this step's newest token (the end of a growing
-  // private tail) stores that token's K/V row for its KV head first, so no
-  // separate store launch is needed; the bulk copies below then see the row.
-  if (a.k_new && w_grow > 0 && ke == w_grow + a.step && kb < ke) {
-    const int64_t b = a.members[member_off];
-    const int64_t sl = a.slots_new[b];
-    if (sl >= 1 && sl < a.num_slots) {
-      const int half = lane >> 4, ch = lane & 15;  // lanes 0-15: K, 16-31: V
-      const bf16* src = (half ? a.v_new : a.k_new) + (b * n_heads_kv + kvh) * D;
-      bf16* dst = const_cast<bf16*>(half ? vbase : kbase) + sl * D;
-#pragma unroll
-      for (int h = 0; h < D / 128; ++h)
-        reinterpret_cast<uint4*>(dst)[ch + 16 * h] =
-            __ldg(reinterpret_cast<const uint4*>(src) + ch + 16 * h);
-    } else {
-      atomicOr(&g_tc_error, 1);
-    }
-    // only this warp reads the row back (cp.async below): order the lanes'
-    // stores before those reads within the CTA
-    __threadfence_block();
-    __syncwarp();
-  }
-
-  const int n_steps = ke > kb ? (ke - kb + 15) >> 4 : 0;
-  // Key slots go through two shared blocks of kSlotBuf: block b (keys
-  // [kb + 128 b, ..)) sits in half b % 2.  Block 0 comes prefetched with the
-  // unit; block b + 1 is loaded into registers when block b is stored, and
-  // stored when the first step of block b + 1 is issued, so no table read
-  // waits.  -1 past the key range; a slot outside the pool is flagged and
-  // read as slot 0.
-  int32_t blk[kSlotRegs];
-  auto store_block = [&](const int32_t (&r)[kSlotRegs], int half) {
-#pragma unroll
-    for (int i = 0; i < kSlotRegs; ++i) {
-      int32_t sl = r[i];
-      if (sl < -1 || sl >= a.num_slots) {
-        atomicOr(&g_tc_error, 1);
-        sl = 0;
-      }
-      slot_buf[half * kSlotBuf + lane + 32 * i] = sl;
-    }
-    __syncwarp();
-  };
-  auto load_block = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kSlotRegs; ++i) {
-      const int key = kb + base + lane + 32 * i;
-      blk[i] = key < ke ? __ldg(trow + key) : -1;
-    }
-  };
-  if (n_steps > 0) {
-    store_block(cur.s, 0);
-    load_block(kSlotBuf);
-  }
-  // step st of this unit: 16 K rows and 16 V rows of 2D bytes, gathered by
-  // slot with 16-byte cp.async (lane: chunks lane % 16 (+ 16 h) of rows
-  // 8 (lane / 16) + i); rows past the key range are zero-filled (P is 0
-  // there, and 0 * V must be 0)
-  const int r0 = (lane >> 4) * 8;
-  const char* ksrc = reinterpret_cast<const char*>(kbase) + (lane & 15) * 16;
-  const int64_t v_minus_k = reinterpret_cast<const char*>(vbase) - reinterpret_cast<const char*>(kbase);
-  auto issue = [&](int st) {
-    const int block = (st * 16) / kSlotBuf;
-    if (block > 0 && st * 16 == block * kSlotBuf) {
-      store_block(blk, block & 1);
-      load_block((block + 1) * kSlotBuf);
-    }
-    const uint32_t dst = ring + ((gstep + uint32_t(st)) % S) * kStageBytes +
-                         uint32_t(r0 * kRowPitch + (lane & 15) * 16);
-    const int4* sp = reinterpret_cast<const int4*>(
-        slot_buf + ((block & 1) * kSlotBuf + st * 16 - block * kSlotBuf + r0));
-    const int4 s0 = sp[0], s1 = sp[1];
-    const int32_t sl[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool ok = sl[i] >= 0;
-      const char* src = ksrc + int64_t(ok ? sl[i] : 0) * (D * 2);
-#pragma unroll
-      for (int h = 0; h < D / 128; ++h) {
-        rxk::cp_async_16(dst + uint32_t(i * kRowPitch + 256 * h), src + 256 * h, ok);
-        rxk::cp_async_16(dst + uint32_t((16 + i) * kRowPitch + 256 * h), src + 256 * h + v_minus_k,
-                         ok);
-      }
-    }
-  };
-
-  float o[NR][NK][4];
-#pragma unroll
-  for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-    for (int mt = 0; mt < NK; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
-  float m_ref[NR][2], l_run[NR][2];
-#pragma unroll
-  for (int nt = 0; nt < NR; ++nt) {
-    m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
-    l_run[nt][0] = l_run[nt][1] = 0.f;
-  }
-
-#pragma unroll 1
-  for (int p = 0; p < S - 1; ++p) {
-    if (p < n_steps) issue(p);
-    rxk::cp_async_commit();
-  }
-
-  // Q^T operand, loaded while the first steps' keys are in flight: n-tile nt,
-  // k-step kk: (d 16kk + 2c, +1 | 16kk + 2c + 8, +9) of row nt*8 + g
-  uint32_t qb[NR][NK][2];
-#pragma unroll
-  for (int nt = 0; nt < NR; ++nt) {
-    const int r = nt * 8 + g;
-    const bool ok = r < n_rows;
-    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q);
-    if (ok) {
-      const int u = r / G;
-      const int64_t b = a.members[member_off + u];
-      qrow = reinterpret_cast<const uint32_t*>(a.q + (b * a.hq + kvh * G + (r - u * G)) * D);
-    }
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-      qb[nt][kk][0] = ok ? __ldg(qrow + 8 * kk + c) : 0u;
-      qb[nt][kk][1] = ok ? __ldg(qrow + 8 * kk + c + 4) : 0u;
-    }
-  }
-
-  // MOD: what the scores of rows nt*8 + 2c + e add, and the first key they see
-  RowMod rm[NR][2];
-  if constexpr (MOD) {
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * c + e;
-        if (r < n_rows) {
-          const int u = r / G;
-          const int64_t b = a.members[member_off + u];
-          const int pos = a.ctx_len ? __ldg(a.ctx_len + b) + a.step - 1 : 0;
-          rm[nt][e] = row_mod(a, b, kvh * G + (r - u * G), pos);
-        }
-      }
-  }
-
-  // ldmatrix lane addresses: K (A of S^T, keys x d) and V^T (A of O^T, d x keys)
-  const uint32_t k_lane = uint32_t(((lane & 7) + ((lane >> 3) & 1) * 8) * kRowPitch + (lane >> 4) * 16);
-  const uint32_t v_lane =
-      uint32_t((16 + (lane & 7) + (lane >> 4) * 8) * kRowPitch + ((lane >> 3) & 1) * 16);
-
-#pragma unroll 1
-  for (int st = 0; st < n_steps; ++st) {
-    // the next unit: index at step 0, work words at step 2, slots at step 4
-    if (st == 0 || st == 2 || st == 4) next_unit_step(a, nxt);
-    rxk::cp_async_wait<S - 2>();
-    __syncwarp();
-    const uint32_t stage = ring + ((gstep + uint32_t(st)) % S) * kStageBytes;
-    // S^T = K . Q^T, even and odd k-steps in two accumulator chains
-    float sacc[NR][4], sodd[NR][4];
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sacc[nt][e] = sodd[nt][e] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-      uint32_t a0, a1, a2, a3;
-      rxk::ldsm_x4(stage + k_lane + uint32_t(kk * 32), a0, a1, a2, a3);
-#pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
-        rxk::mma_bf16((kk & 1) ? sodd[nt] : sacc[nt], a0, a1, a2, a3, qb[nt][kk][0], qb[nt][kk][1]);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sacc[nt][e] += sodd[nt][e];
-    // online softmax over the keys of this step (rows 2c, 2c+1 of each n-tile).
-    // The row reference m_ref changes only when some key of the row exceeds it
-    // by more than 2^8: each lane tests its own keys, one vote per step, and
-    // only then are the row maxima reduced over the 8 lanes of a row and O and
-    // the sums rescaled (rare after the first step of a unit).
-    const int key0 = kb + st * 16 + g;
-    const bool in0 = key0 < ke, in1 = key0 + 8 < ke;
-    float x[NR][4];
-    bool grow = false;
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      if constexpr (MOD) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 8 * (e >> 1);
-          const RowMod& r = rm[nt][e & 1];
-          float y = a.cap_in != 0.f ? capped(a, sacc[nt][e]) : sacc[nt][e] * a.scale_log2;
-          y = fmaf(-r.slope, fabsf(float(key) - r.pos), y);
-          x[nt][e] = key < ke && key >= r.lo ? y : -INFINITY;
-        }
-      } else {
-      x[nt][0] = in0 ? sacc[nt][0] * a.scale_log2 : -INFINITY;
-      x[nt][1] = in0 ? sacc[nt][1] * a.scale_log2 : -INFINITY;
-      x[nt][2] = in1 ? sacc[nt][2] * a.scale_log2 : -INFINITY;
-      x[nt][3] = in1 ? sacc[nt][3] * a.scale_log2 : -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        grow |= fmaxf(x[nt][e], x[nt][2 + e]) > m_ref[nt][e] + kRescaleThreshold;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
-      float mx[NR][2];
-#pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(x[nt][e], x[nt][2 + e]);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
-#pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (mx[nt][e] > m_ref[nt][e]) {
-            const float alpha = rxk::fast_exp2(m_ref[nt][e] - mx[nt][e]);  // 0 from -inf
-            m_ref[nt][e] = mx[nt][e];
-            l_run[nt][e] *= alpha;
-#pragma unroll
-            for (int mt = 0; mt < NK; ++mt) {
-              o[nt][mt][e] *= alpha;
-              o[nt][mt][2 + e] *= alpha;
-            }
-          }
-        }
-    }
-    uint32_t pk[NR][2];  // (key g | key g+8) of rows 2c, 2c+1 as bf16x2
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float m_use = m_ref[nt][e] == -INFINITY ? 0.f : m_ref[nt][e];
-        if constexpr (MOD) {
-          const float p0 = rxk::fast_exp2(x[nt][e] - m_use);
-          const float p1 = rxk::fast_exp2(x[nt][2 + e] - m_use);
-          pk[nt][e] = rxk::pack_bf16(p0, p1);
-          l_run[nt][e] += p0 + p1;
-          continue;
-        }
-        uint32_t h;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
-            : "=r"(h)
-            : "f"(rxk::fast_exp2(x[nt][2 + e] - m_use)), "f"(rxk::fast_exp2(x[nt][e] - m_use)));
-        pk[nt][e] = h;  // low half: key g, high half: key g+8
-        l_run[nt][e] += __uint_as_float(h << 16) + __uint_as_float(h & 0xffff0000u);
-      }
-    // P^T operand for n-tile nt: b0 = (P[key 2c][row g], P[key 2c+1][row g]),
-    // b1 = keys 2c+8, 2c+9; key k of row r sits in lane 4k + r/2, half r%2
-    uint32_t pb[NR][2];
-    const int src1 = 8 * c + (g >> 1), src2 = src1 + 4;
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      const uint32_t v0 = __shfl_sync(0xffffffffu, pk[nt][0], src1);
-      const uint32_t v1 = __shfl_sync(0xffffffffu, pk[nt][1], src1);
-      const uint32_t w0 = __shfl_sync(0xffffffffu, pk[nt][0], src2);
-      const uint32_t w1 = __shfl_sync(0xffffffffu, pk[nt][1], src2);
-      const uint32_t s1 = (g & 1) ? v1 : v0;
-      const uint32_t s2 = (g & 1) ? w1 : w0;
-      pb[nt][0] = __byte_perm(s1, s2, 0x5410);
-      pb[nt][1] = __byte_perm(s1, s2, 0x7632);
-    }
-    // O^T += V^T . P^T
-#pragma unroll
-    for (int mt = 0; mt < NK; ++mt) {
-      uint32_t a0, a1, a2, a3;
-      rxk::ldsm_x4_t(stage + v_lane + uint32_t(mt * 32), a0, a1, a2, a3);
-#pragma unroll
-      for (int nt = 0; nt < NR; ++nt) rxk::mma_bf16(o[nt][mt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-    }
-    __syncwarp();  // every lane is done with this stage before it is refilled
-    if (st + S - 1 < n_steps) issue(st + S - 1);
-    rxk::cp_async_commit();
-  }
-  rxk::cp_async_wait<0>();
-  __syncwarp();
-  gstep += uint32_t(n_steps);
-
-  // write the partial (o, lse) of rows nt*8 + 2c + e
-#pragma unroll
-  for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = l_run[nt][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int r = nt * 8 + 2 * c + e;
-      if (r >= n_rows) continue;
-      const int uu = r / G;
-      const int head = kvh * G + (r - uu * G);
-      const int64_t part = int64_t(part_base) + uu;
-      float* dst = a.ws_o + (part * a.hq + head) * D;
-      const float inv = l > 0.f ? 1.f / l : 0.f;  // an empty chunk: zero partial, lse -inf
-#pragma unroll
-      for (int mt = 0; mt < NK; ++mt) {
-        dst[16 * mt + g] = o[nt][mt][e] * inv;
-        dst[16 * mt + g + 8] = o[nt][mt][2 + e] * inv;
-      }
-      if (g == 0) a.ws_lse[part * a.hq + head] = l > 0.f ? m_ref[nt][e] * kLn2 + logf(l) : -INFINITY;
-    }
 }
 
 // One launch per decode step, at most one CTA per SM.  CTAs [w, w + n_tc_ctas)
@@ -1416,7 +675,7 @@ struct Fused {
   static_assert(SMEM <= 227 * 1024, "fused decode CTA fits in shared memory");
 };
 
-template <int D, bool MOD>
+template <int D>
 __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
     decode_fused_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
@@ -1426,7 +685,7 @@ __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
   const int cta = int(blockIdx.x) - a.n_warp_first;
   if (cta >= 0 && cta < a.n_tc_ctas) {
     const int hkv = a.hq / a.group;
-    tc_tile3<D, true, MOD>(a, &tmk, &tmv, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
+    tc_tile3<D, true>(a, &tmk, &tmv, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
   }
   if (threadIdx.x >= kPipeWarps * 32) return;  // the warp role uses the first six warps
   // tiles_leave: in a run of steps a tile CTA leaves its SM to the next
@@ -1450,9 +709,9 @@ __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
     nxt.stage = 0;
     const int rows = cur.word(6);
     if (rows <= 8) {
-      pipe_unit<1, D, MOD>(a, ring, slot_buf, gstep, cur, nxt);
+      pipe_unit<1, D>(a, ring, slot_buf, gstep, cur, nxt);
     } else if constexpr (D == 128) {
-      pipe_unit<2, D, MOD>(a, ring, slot_buf, gstep, cur, nxt);
+      pipe_unit<2, D>(a, ring, slot_buf, gstep, cur, nxt);
     } else if (lane == 0) {
       atomicOr(&g_tc_error, 1);  // the plan gives head_dim 256 no such item
     }
@@ -1461,117 +720,19 @@ __global__ void __launch_bounds__(Fused<D>::THREADS, 1)
   }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() { return reinterpret_cast<EncodeTiled>(rx_internal::tensor_map_encoder()); }
-
-// Tensor map over a whole pool [L * Hkv * num_slots rows][D] of bf16, box of
-// 64 columns x BN rows, 128-byte swizzle (the shared-memory tile layout);
-// false if it cannot be encoded or the pool has 2^31 rows or more.
-bool make_pool_map(CUtensorMap* m, const void* pool, const rx_pool_desc* d, int BN) {
-  EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  // TMA row coordinates are 32-bit signed
-  if (int64_t(d->num_layers) * d->num_kv_heads * d->num_slots > INT32_MAX) return false;
-  const cuuint64_t dims[2] = {cuuint64_t(d->head_dim),
-                              cuuint64_t(d->num_layers) * d->num_kv_heads * d->num_slots};
-  const cuuint64_t strides[1] = {cuuint64_t(d->head_dim) * 2};
-  const cuuint32_t box[2] = {64, cuuint32_t(BN)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tensor maps of the pools last used on this thread (K and V of one pool
-// descriptor): encoding them is host work repeated on every launch otherwise.
-struct PoolMaps {
-  const void* k = nullptr;
-  const void* v = nullptr;
-  int64_t num_slots = 0;
-  int32_t layers = 0, heads = 0, dim = 0, box_rows = 0;
-  CUtensorMap mk, mv;
-};
-
-bool pool_maps(const rx_pool_desc* d, int BN, const CUtensorMap** mk, const CUtensorMap** mv) {
-  thread_local PoolMaps cache[4];
-  thread_local int next = 0;
-  for (PoolMaps& c : cache) {
-    if (c.k == d->k_pool && c.v == d->v_pool && c.num_slots == d->num_slots &&
-        c.layers == d->num_layers && c.heads == d->num_kv_heads && c.dim == d->head_dim &&
-        c.box_rows == BN) {
-      *mk = &c.mk;
-      *mv = &c.mv;
-      return true;
-    }
-  }
-  PoolMaps& c = cache[next];
-  next = (next + 1) & 3;
-  c.k = nullptr;
-  if (!make_pool_map(&c.mk, d->k_pool, d, BN) || !make_pool_map(&c.mv, d->v_pool, d, BN))
-    return false;
-  c.k = d->k_pool;
-  c.v = d->v_pool;
-  c.num_slots = d->num_slots;
-  c.layers = d->num_layers;
-  c.heads = d->num_kv_heads;
-  c.dim = d->head_dim;
-  c.box_rows = BN;
-  *mk = &c.mk;
-  *mv = &c.mv;
-  return true;
-}
-
-// A kernel's dynamic shared-memory limit is an attribute of the kernel in
-// the current device's context: it is raised once per device (any thread
-// may do it first; setting it twice is harmless).
-constexpr int kMaxDevices = 64;
-
-template <typename K>
-rx_status ensure_smem(std::atomic<bool> (&done)[kMaxDevices], K* kernel, int bytes) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
-    return rx_internal::set_error(RX_ERR_CUDA, "no usable current device");
-  if (done[dev].load(std::memory_order_acquire)) return RX_OK;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) {
-    cudaGetLastError();  // not left for a later launch check to report
-    static thread_local char buf[160];
-    snprintf(buf, sizeof(buf), "raising a kernel's shared-memory limit: %s",
-             cudaGetErrorString(e));
-    return rx_internal::set_error(RX_ERR_CUDA, buf);
-  }
-  done[dev].store(true, std::memory_order_release);
-  return RX_OK;
-}
-
-void set_mod(TcArgs* a, const rx_score_mod& m, float scale) {
-  a->cap_in = m.softcap > 0.f ? scale / m.softcap : 0.f;
-  a->cap_out = m.softcap * kLog2e;
-  a->window = m.window;
-  a->slopes = m.d_slopes;
-  a->key_begin = m.d_key_begin;
-  a->bidir_end = m.d_bidir_end;
-  a->ctx_len = m.d_ctx_len;
-}
-
-template <int D, bool MOD>
+template <int D>
 rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, int32_t layer, unsigned gx,
                         unsigned gy, cudaStream_t s) {
   using Lo = Layout3<D>;
   static std::atomic<bool> configured[kMaxDevices];
-  const rx_status cs = ensure_smem(configured, attn_tc3_kernel<D, MOD>, Lo::BYTES);
+  const rx_status cs = ensure_smem(configured, attn_tc3_kernel<D>, Lo::BYTES);
   if (cs != RX_OK) return cs;
   const CUtensorMap *tmk, *tmv;
   if (!pool_maps(pool, Lo::BN, &tmk, &tmv))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   a.tma_row_base = int64_t(layer) * pool->num_kv_heads * pool->num_slots;
   a.tma_head_rows = pool->num_slots;
-  attn_tc3_kernel<D, MOD><<<dim3(gx * gy), kThreads3, Lo::BYTES, s>>>(a, *tmk, *tmv);
+  attn_tc3_kernel<D><<<dim3(gx * gy), kThreads3, Lo::BYTES, s>>>(a, *tmk, *tmv);
   return rx_internal::launch_status("extend attention (tcgen05)");
 }
 
@@ -1610,7 +771,7 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                        int64_t n_tc, const int32_t* d_members, float scale, float* ws_o,
                        float* ws_lse, int32_t* unit_counter, int step, const void* k_new,
                        const void* v_new, const int32_t* slots_new, cudaStream_t stream,
-                       bool early_inputs, const rx_score_mod* mod) {
+                       bool early_inputs) {
   const int D = pool->head_dim;
   if (D != 128 && D != 256) return set_error(RX_ERR_INVALID, "decode needs head_dim 128 or 256");
   const int64_t hkv = pool->num_kv_heads;
@@ -1660,14 +821,12 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
   a.k_new = static_cast<const bf16*>(k_new);
   a.v_new = static_cast<const bf16*>(v_new);
   a.slots_new = slots_new;
-  if (mod) set_mod(&a, *mod, scale);
   a.tma_row_base = int64_t(layer) * hkv * pool->num_slots;
   a.tma_head_rows = pool->num_slots;
-  static std::atomic<bool> configured[2][2][kMaxDevices];  // [head_dim 256][mod]
-  auto* kernel = D == 128 ? (mod ? decode_fused_kernel<128, true> : decode_fused_kernel<128, false>)
-                          : (mod ? decode_fused_kernel<256, true> : decode_fused_kernel<256, false>);
-  const rx_status cs = ensure_smem(configured[D == 256][mod != nullptr], kernel,
-                                   D == 128 ? Fused<128>::SMEM : Fused<256>::SMEM);
+  static std::atomic<bool> configured128[kMaxDevices], configured256[kMaxDevices];
+  const rx_status cs =
+      D == 128 ? ensure_smem(configured128, decode_fused_kernel<128>, Fused<128>::SMEM)
+               : ensure_smem(configured256, decode_fused_kernel<256>, Fused<256>::SMEM);
   if (cs != RX_OK) return cs;
   const CUtensorMap *tmk, *tmv;
   if (!pool_maps(pool, D == 128 ? 128 : 64, &tmk, &tmv))
@@ -1682,7 +841,10 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, a, *tmk, *tmv);
+  if (D == 128)
+    cudaLaunchKernelEx(&cfg, decode_fused_kernel<128>, a, *tmk, *tmv);
+  else
+    cudaLaunchKernelEx(&cfg, decode_fused_kernel<256>, a, *tmk, *tmv);
   return launch_status("decode attention (fused)");
 }
 
@@ -1691,8 +853,7 @@ rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const voi
                               int64_t row_stride, const int32_t* d_req_rows,
                               const int32_t* d_prefix_len, const int32_t* d_qo_indptr,
                               const int32_t* d_tile_indptr, int32_t R, int64_t num_tiles,
-                              float scale, float* d_out, float* d_lse, cudaStream_t stream,
-                              const rx_score_mod* mod, bool out_bf16) {
+                              float scale, float* d_out, float* d_lse, cudaStream_t stream) {
   const int D = pool->head_dim;
   TcArgs a{};
   a.q = static_cast<const bf16*>(d_q);
@@ -1723,15 +884,9 @@ rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const voi
       kv_row_bytes <= kExtendInterleaveKvBytes;
   a.out = d_out;
   a.lse = d_lse;
-  const unsigned gx = unsigned(num_tiles), gy = unsigned(pool->num_kv_heads);
-  if (mod) {
-    set_mod(&a, *mod, scale);
-    a.out_bf16 = out_bf16;
-    return D == 128 ? launch_extend<128, true>(a, pool, layer, gx, gy, stream)
-                    : launch_extend<256, true>(a, pool, layer, gx, gy, stream);
-  }
-  return D == 128 ? launch_extend<128, false>(a, pool, layer, gx, gy, stream)
-                  : launch_extend<256, false>(a, pool, layer, gx, gy, stream);
+  if (D == 128)
+    return launch_extend<128>(a, pool, layer, unsigned(num_tiles), pool->num_kv_heads, stream);
+  return launch_extend<256>(a, pool, layer, unsigned(num_tiles), pool->num_kv_heads, stream);
 }
 
 }  // namespace rx_internal

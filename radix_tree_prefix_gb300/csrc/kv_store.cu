@@ -287,7 +287,7 @@ extern "C" rx_status rx_device_check(int32_t* out_flags) {
     snprintf(buf, sizeof(buf), "rx_device_check: %s", cudaGetErrorString(e));
     return rx_internal::set_error(RX_ERR_CUDA, buf);
   }
-  const int32_t tcf = rx_internal::tc_error_flags(true) |
+  const int32_t tcf = rx_internal::tc_error_flags(true) | rx_internal::mod_error_flags(true) |
                       rx_internal::kv8_attention_error_flags(true);
   int32_t f = rx_internal::kv_store_error_flags(true) |
               rx_internal::kv8_store_error_flags(true) | rx_internal::rope_error_flags(true) |

@@ -59,6 +59,7 @@ void* tensor_map_encoder();
 // Error words of the kernels of each file: bit 0 = slot out of range.
 int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
+int32_t mod_error_flags(bool clear);  // as tc_error_flags
 int32_t kv8_store_error_flags(bool clear);  // bits 0, 6 and 7 of rx_device_check
 int32_t kv8_attention_error_flags(bool clear);  // as tc_error_flags
 int32_t rope_error_flags(bool clear);  // bit 0 of rx_device_check
@@ -77,14 +78,13 @@ rx_status decode_fused(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                        int64_t n_tc, const int32_t* d_members, float scale, float* ws_o,
                        float* ws_lse, int32_t* unit_counter, int step, const void* k_new,
                        const void* v_new, const int32_t* slots_new, cudaStream_t stream,
-                       bool early_inputs, const rx_score_mod* mod = nullptr);
+                       bool early_inputs);
 rx_status extend_attention_tc(const rx_pool_desc* pool, int32_t layer, const void* d_q,
                               int32_t num_q_heads, const int32_t* d_req_to_token,
                               int64_t row_stride, const int32_t* d_req_rows,
                               const int32_t* d_prefix_len, const int32_t* d_qo_indptr,
                               const int32_t* d_tile_indptr, int32_t R, int64_t num_tiles,
-                              float scale, float* d_out, float* d_lse, cudaStream_t stream,
-                              const rx_score_mod* mod = nullptr, bool out_bf16 = false);
+                              float scale, float* d_out, float* d_lse, cudaStream_t stream);
 // Partial results merged into fp32 or bf16 rows (kv8_attention.cu); a request
 // without parts, or with empty ones only, gets zeros and lse = -inf.  chained:
 // launched while the kernel that writes the parts runs.

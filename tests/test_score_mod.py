@@ -38,23 +38,24 @@ def test_calls_refuse_before_any_cuda_call():
         return m
 
     def ext(pool=pool, layer=0, q=X, hq=4, table=X, rows=X, pre=X, qo=X, tiles=X, R=1, nt=1,
-            m=mod(), out=X, ot=0, lse=X):
+            m=mod(), out=X, ot=0, lse=X, scale=0.1):
         return rx._lib.rx_extend_attention_mod(C.byref(pool), layer, q, hq, table, 64, rows, pre,
-                                               qo, tiles, R, nt, 0.1, C.byref(m), out, ot, lse,
+                                               qo, tiles, R, nt, scale, C.byref(m), out, ot, lse,
                                                None)
 
     def dec(pool=pool, layer=0, q=X, hq=4, table=X, plan=X, info=info, B=1, step=0, m=mod(), out=X,
-            ot=0, lse=X, ws=X, nb=4096):
+            ot=0, lse=X, ws=X, nb=4096, scale=0.1):
         return rx._lib.rx_decode_attention_mod(
             C.byref(pool), layer, q, hq, table, 64, plan, None if info is None else C.byref(info),
-            B, step, 0.1, C.byref(m), out, ot, lse, ws, nb, None)
+            B, step, scale, C.byref(m), out, ot, lse, ws, nb, None)
     assert ext(R=0) == rx.RX_OK and ext(nt=0) == rx.RX_OK and dec(B=0) == rx.RX_OK
     for fn in (ext, dec):
         for kw in (dict(layer=2), dict(layer=-1), dict(q=None), dict(q=X + 8), dict(hq=3),
                    dict(hq=0), dict(table=None), dict(out=None), dict(out=X + 8), dict(ot=2),
                    dict(ot=-1), dict(lse=None), dict(m=mod(softcap=-1.0)),
                    dict(m=mod(softcap=math.nan)), dict(m=mod(softcap=INF)),
-                   dict(m=mod(window=-1)), dict(pool=rx.rx_pool_desc(X, X, 64, 2, 2, 96, 0))):
+                   dict(m=mod(window=-1)), dict(scale=0.0), dict(scale=-1.0),
+                   dict(scale=math.nan), dict(scale=INF), dict(pool=rx.rx_pool_desc(X, X, 64, 2, 2, 96, 0))):
             assert fn(**kw) == rx.RX_ERR_INVALID, (fn, kw)
     for kw in (dict(rows=None), dict(pre=None), dict(qo=None), dict(tiles=None), dict(R=-1),
                dict(nt=-1), dict(nt=1 << 31)):
