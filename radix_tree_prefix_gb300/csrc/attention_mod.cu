@@ -112,7 +112,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 // loops rolled: with the roles' loops unrolled the kernel was 195 KB of code, and
 // its warps, each somewhere else in it, waited for instructions most of the
 // time.
-template <int D, int BS>
+template <int D, int BS, bool BACK>
 __device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, int n_loads,
                                            const CUtensorMap* tm, const CUtensorMap* tm16,
                                            const bf16* src_base, int row0, uint32_t smem0,
@@ -124,7 +124,7 @@ __device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, i
   const int lane = threadIdx.x & 31;
   int32_t slot[SPL], next[AHEAD][SPL];
   auto load_slots = [&](int j, int32_t (&dst)[SPL]) {
-    const int k0 = t.key_begin + j * BS;
+    const int k0 = t.key_begin + (BACK ? n_loads - 1 - j : j) * BS;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
       const int key = k0 + lane + 32 * i;
@@ -283,7 +283,12 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
   if constexpr (DECODE) rxk::griddep_wait();
   const TileDesc t = describe<DECODE, true>(a, bx);
   const int n_keys = t.key_lo >= t.key_end ? 0 : t.key_end - t.key_begin;
-  const int n_tiles = (n_keys + BN - 1) / BN, n_loads = (n_keys + BS - 1) / BS;
+  // With slopes the loads go from the newest keys back: scores fall with distance,
+  // so a row's first maximum is about its last, where it would rise with
+  // almost every tile the other way round (an agent loop's calls under slopes
+  // of 2^(-8 h / 32): 639 us forwards).
+  const int n_loads = (n_keys + BS - 1) / BS;
+  const int n_tiles = SLOPES ? n_loads * SUBS : (n_keys + BN - 1) / BN;
   const int wg = warp >> 2;
   const int i = (warp & 3) * 32 + lane;  // TMEM lane
   // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
@@ -359,7 +364,7 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
   if (warp >= SW) {
     if (warp == SW + 1 || warp == SW + 2) {
       const bool v = warp == SW + 2;
-      load_tiles<D, BS>(a, t, n_loads, v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
+      load_tiles<D, BS, SLOPES>(a, t, n_loads, v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
                         (v ? a.vpool : a.kpool) + int64_t(kvh) * a.head_stride,
                         int(a.tma_row_base + int64_t(kvh) * a.tma_head_rows),
                         base + (v ? Lo::V0 : Lo::K0), v ? VF : KF, v ? VE : KE, v ? NV : NK,
@@ -464,7 +469,8 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
         break;
       }
       tc::tc_fence_after();
-      const int k0 = t.key_begin + j * BN;
+      const int k0 =
+          t.key_begin + (SLOPES ? (n_loads - 1 - load) * BS + (j % SUBS) * BN : j * BN);
       uint32_t sr[BN];
       tc::tmem_ld_row<BN>(tl + uint32_t(s * BN), sr);
       tc::tmem_ld_wait();
@@ -488,13 +494,21 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
           const float most = valid ? fmaxf(am, an) * a.cap_in : 0.f;
           if (__all_sync(0xffffffffu, most <= 0.5f)) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 u = __fmul2_rn(get2(c + e), a.cap_in2);
-              const float2 v = __fmul2_rn(u, u);
-              float2 p = __ffma2_rn(a.cap_near2[3], v, a.cap_near2[2]);
-              p = __ffma2_rn(p, v, a.cap_near2[1]);
-              p = __ffma2_rn(p, v, a.cap_near2[0]);
-              put2(c + e, __fmul2_rn(u, p));
+            for (int e = 0; e < 32; e += 16) {
+              float2 u[8], v[8], p[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) u[k] = __fmul2_rn(get2(c + e + 2 * k), a.cap_in2);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __fmul2_rn(u[k], u[k]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                p[k] = __ffma2_rn(a.cap_near2[3], v[k], a.cap_near2[2]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_near2[1]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_near2[0]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) put2(c + e + 2 * k, __fmul2_rn(u[k], p[k]));
             }
           } else if (__all_sync(0xffffffffu, most <= 1.f)) {
 #pragma unroll
@@ -758,7 +772,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   uint32_t gstep = 0;
   NextUnit cur, nxt;
   cur.stage = 0;
-  while (cur.stage < 3) next_unit_step(a, cur);
+  while (cur.stage < 3) next_unit_step<SLOPES>(a, cur);
   while (cur.idx < a.n_small_units) {
     nxt.stage = 0;
     const int rows = cur.word(6);
@@ -769,7 +783,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     } else if (lane == 0) {
       atomicOr(&g_tc_error, 1);  // the plan gives head_dim 256 no such item
     }
-    while (nxt.stage < 3) next_unit_step(a, nxt);
+    while (nxt.stage < 3) next_unit_step<SLOPES>(a, nxt);
     cur = nxt;
   }
 }

@@ -322,6 +322,7 @@ struct NextUnit {
   __device__ __forceinline__ int32_t word(int k) const { return __shfl_sync(0xffffffffu, wk, k); }
 };
 
+template <bool BACK = false>
 __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
   const int lane = threadIdx.x & 31;
   if (n.stage == 0) {
@@ -338,8 +339,8 @@ __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
       const int ke = grow > 0 ? min(kend, grow + a.step) : kend;
 #pragma unroll
       for (int i = 0; i < kSlotRegs; ++i) {
-        const int key = kb + lane + 32 * i;
-        n.s[i] = key < ke ? __ldg(trow + key) : -1;
+        const int at = lane + 32 * i;
+        n.s[i] = at < ke - kb ? __ldg(trow + (BACK ? ke - 1 - at : kb + at)) : -1;
       }
     }
   }
@@ -416,8 +417,8 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
   auto load_block = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kSlotRegs; ++i) {
-      const int key = kb + base + lane + 32 * i;
-      blk[i] = key < ke ? __ldg(trow + key) : -1;
+      const int at = base + lane + 32 * i;
+      blk[i] = at < ke - kb ? __ldg(trow + (SLOPES ? ke - 1 - at : kb + at)) : -1;
     }
   };
   if (n_steps > 0) {
@@ -519,7 +520,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
 #pragma unroll 1
   for (int st = 0; st < n_steps; ++st) {
     // the next unit: index at step 0, work words at step 2, slots at step 4
-    if (st == 0 || st == 2 || st == 4) next_unit_step(a, nxt);
+    if (st == 0 || st == 2 || st == 4) next_unit_step<SLOPES>(a, nxt);
     rxk::cp_async_wait<S - 2>();
     __syncwarp();
     const uint32_t stage = ring + ((gstep + uint32_t(st)) % S) * kStageBytes;
@@ -546,8 +547,9 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     // by more than 2^8: each lane tests its own keys, one vote per step, and
     // only then are the row maxima reduced over the 8 lanes of a row and O and
     // the sums rescaled (rare after the first step of a unit).
-    const int key0 = kb + st * 16 + g;
-    const bool in0 = key0 < ke, in1 = key0 + 8 < ke;
+    // (with slopes from the newest key back, so that a row's maximum settles at once)
+    const int key0 = SLOPES ? ke - 1 - (st * 16 + g) : kb + st * 16 + g;
+    const bool in0 = SLOPES ? key0 >= kb : key0 < ke, in1 = SLOPES ? key0 - 8 >= kb : key0 + 8 < ke;
     float x[NR][4];
     bool grow = false;
 #pragma unroll
@@ -555,11 +557,11 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
       if constexpr (MOD) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 8 * (e >> 1);
+          const int key = SLOPES ? key0 - 8 * (e >> 1) : key0 + 8 * (e >> 1);
           const RowMod& r = rm[nt][e & 1];
           float y = CAP ? capped(a, sacc[nt][e]) : sacc[nt][e] * a.scale_log2;
           if constexpr (SLOPES) y = fmaf(-r.slope, fabsf(float(key - r.pos)), y);
-          x[nt][e] = key < ke && key >= r.lo ? y : -INFINITY;
+          x[nt][e] = (e >> 1 ? in1 : in0) && key >= r.lo ? y : -INFINITY;
         }
       } else {
       x[nt][0] = in0 ? sacc[nt][0] * a.scale_log2 : -INFINITY;
