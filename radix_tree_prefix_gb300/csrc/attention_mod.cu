@@ -69,11 +69,8 @@ struct Layout4 {
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
   static constexpr int TMEM_COLS = 512;
-  // the epilogue's rows in the K and V stages, then the warpgroups' (m, l)
-  static constexpr int PITCH = D / 2 * 4 + 16;
-  static constexpr int XCH = K0 + 2 * BM * PITCH;
+  static constexpr int XCH = K0;  // the epilogue's (m, l) of each warpgroup
   static_assert(O_COL + D <= TMEM_COLS, "TMEM budget");
-  static_assert(XCH + 3 * BM * 8 <= REF, "the exchange fits in the stages");
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -86,6 +83,18 @@ struct Maps4 {
   CUtensorMap k, v;      // boxes of a tile's keys x 64 columns
   CUtensorMap k16, v16;  // boxes of 16 keys
 };
+
+// 32 bytes at a 16-byte boundary, in one store at a 32-byte one.
+__device__ __forceinline__ void store_32(void* dst, const uint32_t* r, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
 
 // One lane of the warp, known to the compiler as such.
 __device__ __forceinline__ bool elect_one() {
@@ -280,6 +289,27 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == SW && lane == 0) {
+    tc::mbar_init(BAR_Q, 8);
+    for (int s = 0; s < NK; ++s) tc::mbar_init(KF + 8u * s, 1);
+    for (int s = 0; s < NK; ++s) tc::mbar_init(KE + 8u * s, 1);
+    for (int s = 0; s < NV; ++s) tc::mbar_init(VF + 8u * s, 1);
+    for (int s = 0; s < NV; ++s) tc::mbar_init(VE + 8u * s, 1);
+    for (int b = 0; b < NS; ++b) tc::mbar_init(BAR_S + 8u * b, 1);
+    for (int b = 0; b < NB; ++b) {
+      tc::mbar_init(BAR_P + 8u * b, 4);
+      tc::mbar_init(BAR_PF + 8u * b, 1);
+    }
+    for (int b = 0; b < 8; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
+    tc::mbar_init(BAR_FIN, 2);  // one commit per issuing thread
+    tc::mbar_init(BAR_X, SW);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == SW) {
+    tc::tmem_alloc(rxk::smem_addr(tmem_slot), Lo::TMEM_COLS);
+    tc::tmem_relinquish();
+  }
   if constexpr (DECODE) rxk::griddep_wait();
   const TileDesc t = describe<DECODE, true>(a, bx);
   const int n_keys = t.key_lo >= t.key_end ? 0 : t.key_end - t.key_begin;
@@ -312,49 +342,28 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
       rm.lo = t.key_lo;
       rm.pos = INT32_MAX;
     }
-    // the Q row this thread gathers: tile row i into shared-memory row i,
-    // whatever the TMEM layout of the products
-    int64_t gqi = qi;
-    int ghead = head;
-    bool gvalid = valid;
-    if (m64) {
-      int64_t gpart = 0;
-      int glim = 0;
-      gqi = 0;
-      ghead = 0;
-      gvalid = i < t.n_rows;
-      if (gvalid) row_info<DECODE>(a, t, kvh, i, gqi, ghead, gpart, glim);
+  }
+  if (warp < 8) {
+    // Q rows 16 warp .. + 15 into shared memory (zeros past the tile's rows): a
+    // lane finds a row, and the warp copies whole rows, whose pieces lie together
+    const int mine = 16 * warp + (lane & 15);
+    const bf16* src = nullptr;
+    if (mine < t.n_rows) {
+      int64_t gqi = 0, gpart = 0;
+      int ghead = 0, glim = 0;
+      row_info<DECODE>(a, t, kvh, mine, gqi, ghead, gpart, glim);
+      src = a.q + (gqi * a.hq + ghead) * D;
     }
-    if (wg < 2) {  // each half of a row
-      const bf16* src = a.q + (gqi * a.hq + ghead) * D;
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows an instruction
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const int ch = wg * (D / 16) + c;
-        rxk::cp_async_16(sw128(sQ, BM, i, ch), src + ch * 8, gvalid);
-      }
-      rxk::cp_async_commit();
+    for (int k = 0; k < 16 / RPI; ++k) {
+      const int r = k * RPI + lane / CPR, ch = lane % CPR;
+      const bf16* from = reinterpret_cast<const bf16*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+      rxk::cp_async_16(sw128(sQ, BM, 16 * warp + r, ch), (from ? from : a.q) + ch * 8,
+                       from != nullptr);
     }
-  }
-  if (tid == 0) {
-    tc::mbar_init(BAR_Q, 8);
-    for (int s = 0; s < NK; ++s) tc::mbar_init(KF + 8u * s, 1);
-    for (int s = 0; s < NK; ++s) tc::mbar_init(KE + 8u * s, 1);
-    for (int s = 0; s < NV; ++s) tc::mbar_init(VF + 8u * s, 1);
-    for (int s = 0; s < NV; ++s) tc::mbar_init(VE + 8u * s, 1);
-    for (int b = 0; b < NS; ++b) tc::mbar_init(BAR_S + 8u * b, 1);
-    for (int b = 0; b < NB; ++b) {
-      tc::mbar_init(BAR_P + 8u * b, 4);
-      tc::mbar_init(BAR_PF + 8u * b, 1);
-    }
-    for (int b = 0; b < 8; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
-    tc::mbar_init(BAR_FIN, 2);  // one commit per issuing thread
-    tc::mbar_init(BAR_X, SW);
-    *abort_flag = 0;
-    tc::fence_barrier_init();
-  }
-  if (warp == SW) {
-    tc::tmem_alloc(rxk::smem_addr(tmem_slot), Lo::TMEM_COLS);
-    tc::tmem_relinquish();
+    rxk::cp_async_commit();
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -446,7 +455,7 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
     // (fences of the async and tcgen05 proxies are each lane's, before its warp arrives)
     const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
     float* ref = reinterpret_cast<float*>(gbase + Lo::REF);  // [2][BM]
-    if (wg < 2) {
+    if (warp < 8) {
       rxk::cp_async_wait<0>();
       tc::fence_proxy_async_smem();
       warp_arrive(BAR_Q);
@@ -663,43 +672,33 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
         }
       }
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-      // Warpgroup w writes columns [w D/2, (w+1) D/2), through shared memory so
-      // that each warp stores whole row segments.
-      constexpr int HC = D / 2, PITCH = Lo::PITCH, LPR = HC / 4;
+      // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
+      // sector) a thread and store: the rows need no trip through shared memory.
+      constexpr int HC = D / 2;
       const bool narrow = !DECODE && a.out_bf16;
-      uint8_t* stage = gbase + Lo::K0 + wg * (BM * PITCH);
+      const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * HC;
+      const bool whole = (reinterpret_cast<uintptr_t>(DECODE ? a.ws_o : a.out) & 31) == 0;
 #pragma unroll 1
       for (int c = 0; c < HC; c += 32) {
         uint32_t r[32];
         tc::tmem_ld32(tl + uint32_t(Lo::O_COL + wg * HC + c), r);
         tc::tmem_ld_wait();
-        float4* s4 = reinterpret_cast<float4*>(stage + i * PITCH + c * 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          s4[e] = make_float4(__uint_as_float(r[4 * e]) * inv, __uint_as_float(r[4 * e + 1]) * inv,
-                              __uint_as_float(r[4 * e + 2]) * inv,
-                              __uint_as_float(r[4 * e + 3]) * inv);
-      }
-      __syncwarp();
-      const int qrow = (warp & 3) * 32;  // first row of this warp's quadrant
-      unsigned long long my_dst = 0ull;
-      if (valid) {
-        const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * HC;
-        my_dst = narrow ? reinterpret_cast<unsigned long long>(reinterpret_cast<bf16*>(a.out) + at)
-                        : reinterpret_cast<unsigned long long>((DECODE ? a.ws_o : a.out) + at);
-      }
-#pragma unroll 4
-      for (int k = 0; k < LPR; ++k) {
-        const int idx = k * 32 + lane;
-        const int rr = idx / LPR, c4 = idx - rr * LPR;  // row within the quadrant, float4
-        const unsigned long long rd = __shfl_sync(0xffffffffu, my_dst, rr);
-        const float4 v = *reinterpret_cast<const float4*>(stage + (qrow + rr) * PITCH + c4 * 16);
-        if (!rd) continue;
-        if (narrow)
-          reinterpret_cast<uint2*>(rd)[c4] =
-              make_uint2(rxk::pack_bf16(v.x, v.y), rxk::pack_bf16(v.z, v.w));
-        else
-          reinterpret_cast<float4*>(rd)[c4] = v;
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+        if (!valid) continue;
+        if (narrow) {
+          uint32_t h[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            h[e] = rxk::pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          bf16* dst = reinterpret_cast<bf16*>(a.out) + at + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) store_32(dst + 2 * e, &h[e], whole);
+        } else {
+          float* dst = (DECODE ? a.ws_o : a.out) + at + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store_32(dst + e, &r[e], whole);
+        }
       }
       if (valid && wg == 0)
         (DECODE ? a.ws_lse : a.lse)[(DECODE ? part : qi) * a.hq + head] =

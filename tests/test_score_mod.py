@@ -382,6 +382,30 @@ def test_extend_without_modification_is_extend_attention():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_outputs_that_start_on_16_bytes(dtype):
+    """Outputs and workspaces need 16-byte alignment, not more."""
+    import torch
+    dt = getattr(torch, dtype)
+    e = Extend([(90, 70), (0, 9)], 8, 2, 128, seed=12)
+    want, _ = e.run(dt, softcap=20.0)
+    room = torch.full((want.numel() + 64,), 7.0, dtype=dt, device="cuda")
+    off = (16 - room.data_ptr() % 32) % 32 // room.element_size()
+    out = room[off:off + want.numel()].view_as(want)
+    assert out.data_ptr() % 32 == 16
+    rx.extend_attention_mod(*e.args[:13], out, e.args[14])
+    assert torch.equal(out, want)
+    c = Decode([40 + 3 * i for i in range(37)], 300, 8, 2, 128, seed=1)
+    want, _ = c.run(dt, softcap=20.0)
+    ws = torch.zeros(c.args[12].numel() + 64, dtype=torch.uint8, device="cuda")
+    ws = ws[(16 - ws.data_ptr() % 32) % 32:]
+    out = room.new_full((want.numel() + 64,), 7.0)
+    out = out[off:off + want.numel()].view_as(want)
+    rx.decode_attention_mod(*c.args[:10], out, c.args[11], ws)
+    assert torch.equal(out, want) and rx.device_check() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [128, 256])
 def test_extend_reads_no_key_before_its_windows(d):
     e = Extend([(700, 90), (0, 400), (64, 1)], 8, 2, d, seed=9)
