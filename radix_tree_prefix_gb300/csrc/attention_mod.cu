@@ -63,14 +63,16 @@ struct Layout4 {
   static constexpr int K0 = BM * D * 2;
   static constexpr int V0 = K0 + NK * KV_BYTES;
   static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
-  static constexpr int BAR = REF + 2 * BM * 4;
-  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + NS + 2 * NB + 8 + 2;
+  static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
+  static constexpr int DESC = SUM + 3 * BM * 4;   // the row tile in hand and the next
+  static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
+  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 8 + 9;
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int XCH = K0;  // the epilogue's (m, l) of each warpgroup
   static_assert(O_COL + D <= TMEM_COLS, "TMEM budget");
+  static_assert(BAR % 8 == 0 && DESC % 8 == 0, "alignment");
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -115,18 +117,24 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
-// One warp loads the K or V tiles into a ring of `stages` stages; barriers full
+// Where a loader stands in its ring of `stages` stages, row tile after row tile.
+struct Ring {
+  int stage = 0, count = 0;  // the next load's stage, and its number
+  uint32_t phase = 1;        // of its wait for an empty stage (none in the first round)
+};
+
+// One warp loads the K or V tiles of a row tile into its ring; barriers full
 // and empty of stage s at full0 + 8 s and empty0 + 8 s (empty: the products that
-// read the stage's last tile completed).  One piece of code for both warps, its
+// read the stage's last keys completed).  Returns false if a wait gave up.  One piece of code for both warps, its
 // loops rolled: with the roles' loops unrolled the kernel was 195 KB of code, and
 // its warps, each somewhere else in it, waited for instructions most of the
 // time.
 template <int D, int BS, bool BACK>
-__device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, int n_loads,
+__device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, int n_loads,
                                            const CUtensorMap* tm, const CUtensorMap* tm16,
                                            const bf16* src_base, int row0, uint32_t smem0,
                                            uint32_t full0, uint32_t empty0, int stages,
-                                           volatile int* abort_flag) {
+                                           Ring& ring, volatile int* abort_flag) {
   constexpr int CPR = D / 8, CB = D / 64;
   constexpr int SPL = BS / 32;   // slots per lane: keys lane + 32 i
   constexpr int AHEAD = 3;       // tiles whose slots are on their way
@@ -142,12 +150,11 @@ __device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, i
   };
 #pragma unroll
   for (int u = 0; u < AHEAD; ++u) load_slots(u, next[u]);
-  int stage = 0, ahead_stage = 0;  // of tile j, and of the tile whose rows are gathered
-  uint32_t phase = 1;              // of the wait for an empty stage (the first round's: none)
-  bool pending = false;            // a tile's gathered rows are still on their way
-  int j = 0;
+  int before = 0;        // stage of the load before
+  bool pending = false;  // whose gathered rows are still on their way
+  bool ok = true;
 #pragma unroll 1
-  for (; j < n_loads; ++j) {
+  for (int j = 0; j < n_loads; ++j) {
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
       slot[i] = next[0][i];
@@ -159,9 +166,13 @@ __device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, i
       }
     }
     load_slots(j + AHEAD, next[AHEAD - 1]);
-    const uint32_t full = full0 + 8u * uint32_t(stage);
-    const uint32_t dst = smem0 + uint32_t(stage * BS * D * 2);
-    if (j >= stages && !warp_wait(empty0 + 8u * uint32_t(stage), phase, abort_flag)) break;
+    const uint32_t full = full0 + 8u * uint32_t(ring.stage);
+    const uint32_t dst = smem0 + uint32_t(ring.stage * BS * D * 2);
+    if (ring.count >= stages &&
+        !warp_wait(empty0 + 8u * uint32_t(ring.stage), ring.phase, abort_flag)) {
+      ok = false;
+      break;
+    }
     // which groups of 16 keys are runs of slots (bit g), and whether they all are one
     const int32_t first = __shfl_sync(0xffffffffu, slot[0], 0);
     bool one = first >= 0 && int64_t(first) + BS <= a.num_slots;
@@ -233,40 +244,35 @@ __device__ __forceinline__ void load_tiles(const TcArgs& a, const TileDesc& t, i
         rxk::cp_async_wait<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(ahead_stage));
+      if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(before));
     }
     pending = gathered;
-    ahead_stage = stage;
-    if (++stage == stages) {
-      stage = 0;
-      phase ^= 1u;
+    before = ring.stage;
+    ++ring.count;
+    if (++ring.stage == stages) {
+      ring.stage = 0;
+      ring.phase ^= 1u;
     }
   }
   if (pending) {
     rxk::cp_async_wait<0>();
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(ahead_stage));
+    if (lane == 0) tc::mbar_arrive(full0 + 8u * uint32_t(before));
   }
-  // Before the CTA gives up its shared memory the last load of every stage has
-  // landed: at once on the normal path; after a wait of another warp gave up, one
-  // more bounded wait that does not look at the abort flag.
-  if (lane == 0) {
-    int drain_abort = 0;
-#pragma unroll 1
-    for (int i = j > stages ? j - stages : 0; i < j; ++i)
-      tc::mbar_wait(full0 + 8u * uint32_t(i % stages), uint32_t(i / stages) & 1u, &drain_abort,
-                    kWaitLimit);
-  }
-  __syncwarp();
+  return ok;
 }
 
+// A CTA's row tiles first, first + step, .. below total, one after another: the
+// loaders and the issuing warps run ahead into the next row tile while the softmax
+// warps finish one and write it.  (One CTA a row tile left its SM idle for some 9
+// us of start and end: a prompt of 8,191 in a window of 1,024 took 253 us.)
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
 template <int D, int NW, bool DECODE, bool CAP, bool SLOPES>
-__device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_t* gbase, int bx,
-                                      int kvh) {
+__device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
+                                          int first, int step, int total) {
   using Lo = Layout4<D>;
   constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS;
@@ -277,32 +283,40 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
     return;
   }
   const uint32_t sQ = base + Lo::Q;
-  const uint32_t BAR_Q = base + Lo::BAR;
-  const uint32_t KF = BAR_Q + 8u, KE = KF + 8u * NK, VF = KE + 8u * NK, VE = VF + 8u * NV;
+  const uint32_t KF = base + Lo::BAR, KE = KF + 8u * NK, VF = KE + 8u * NK, VE = VF + 8u * NV;
   const uint32_t BAR_S = VE + 8u * NV, BAR_P = BAR_S + 8u * NS;
-  // PV_j completes phase j / NB of its buffer's barrier: S may overwrite P_j
+  // PV of tile g completes phase g / NB of its buffer's barrier: S may overwrite P
   const uint32_t BAR_PF = BAR_P + 8u * NB;
   // the references of a quadrant's rows at even (0-3) and odd (4-7) tiles are set
   const uint32_t BAR_H = BAR_PF + 8u * NB;
-  const uint32_t BAR_FIN = BAR_H + 64u, BAR_X = BAR_FIN + 8u;
+  const uint32_t BAR_FIN = BAR_H + 64u;   // a row tile's products are done
+  const uint32_t BAR_X = BAR_FIN + 8u;    // its warpgroups' sums are written
+  const uint32_t BAR_OE = BAR_X + 8u;     // its O has been read
+  const uint32_t BAR_QE = BAR_OE + 8u;    // its Q has
+  const uint32_t BAR_DF = BAR_QE + 8u;    // descriptors of even and odd row tiles: written,
+  const uint32_t BAR_DE = BAR_DF + 16u;   // read
+  const uint32_t BAR_END = BAR_DE + 16u;  // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lo::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
+  TileDesc* descs = reinterpret_cast<TileDesc*>(gbase + Lo::DESC);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == SW && lane == 0) {
-    tc::mbar_init(BAR_Q, 8);
-    for (int s = 0; s < NK; ++s) tc::mbar_init(KF + 8u * s, 1);
-    for (int s = 0; s < NK; ++s) tc::mbar_init(KE + 8u * s, 1);
-    for (int s = 0; s < NV; ++s) tc::mbar_init(VF + 8u * s, 1);
-    for (int s = 0; s < NV; ++s) tc::mbar_init(VE + 8u * s, 1);
-    for (int b = 0; b < NS; ++b) tc::mbar_init(BAR_S + 8u * b, 1);
+    for (int s = 0; s < 2 * NK + 2 * NV + NS; ++s) tc::mbar_init(KF + 8u * s, 1);
     for (int b = 0; b < NB; ++b) {
       tc::mbar_init(BAR_P + 8u * b, 4);
       tc::mbar_init(BAR_PF + 8u * b, 1);
     }
     for (int b = 0; b < 8; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
-    tc::mbar_init(BAR_FIN, 2);  // one commit per issuing thread
+    tc::mbar_init(BAR_FIN, 1);
     tc::mbar_init(BAR_X, SW);
+    tc::mbar_init(BAR_OE, 8);
+    tc::mbar_init(BAR_QE, 1);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(BAR_DF + 8u * b, 1);
+      tc::mbar_init(BAR_DE + 8u * b, SW + 3);
+    }
+    tc::mbar_init(BAR_END, 2);  // one commit per issuing thread
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -310,155 +324,263 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
     tc::tmem_alloc(rxk::smem_addr(tmem_slot), Lo::TMEM_COLS);
     tc::tmem_relinquish();
   }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   if constexpr (DECODE) rxk::griddep_wait();
-  const TileDesc t = describe<DECODE, true>(a, bx);
-  const int n_keys = t.key_lo >= t.key_end ? 0 : t.key_end - t.key_begin;
-  // With slopes the loads go from the newest keys back: scores fall with distance,
-  // so a row's first maximum is about its last, where it would rise with
-  // almost every tile the other way round (an agent loop's calls under slopes
-  // of 2^(-8 h / 32): 639 us forwards).
-  const int n_loads = (n_keys + BS - 1) / BS;
-  const int n_tiles = SLOPES ? n_loads * SUBS : (n_keys + BN - 1) / BN;
-  const int wg = warp >> 2;
-  const int i = (warp & 3) * 32 + lane;  // TMEM lane
-  // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
-  // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
-  const bool m64 = t.n_rows <= 64;
-  const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
-  int64_t qi = 0, part = 0;
-  int head = 0, lim = t.key_end;
-  bool valid = false;
-  RowMod rm;
-  if (warp < SW) {
-    valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
+
+  // the k-th row tile's descriptor, as the K loader wrote it
+  auto read_desc = [&](int k, TileDesc& t) -> bool {
+    if (!warp_wait(BAR_DF + 8u * uint32_t(k & 1), uint32_t(k >> 1) & 1u, abort_flag)) return false;
+    t = descs[k & 1];
+    warp_arrive(BAR_DE + 8u * uint32_t(k & 1));
+    return true;
+  };
+  // Loads of BS keys, and tiles of BN among them that hold keys.  With slopes the
+  // loads go from the newest keys back: scores fall with distance, so a row's first
+  // maximum is about its last, where it would rise with almost every tile the
+  // other way round (an agent loop's calls under slopes of 2^(-8 h / 32): 639 us
+  // forwards, 418).
+  auto loads_of = [](const TileDesc& t) {
+    return t.key_lo >= t.key_end ? 0 : (t.key_end - t.key_begin + BS - 1) / BS;
+  };
+  auto tiles_of = [](const TileDesc& t, int n_loads) {
+    return SLOPES || n_loads == 0 ? n_loads * SUBS : (t.key_end - t.key_begin + BN - 1) / BN;
+  };
+
+  if (warp == SW + 1 || warp == SW + 2) {
+    // ------------------------------------------------------------- loaders
+    const bool v = warp == SW + 2;
+    Ring ring;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+      TileDesc t;
+      if (!v) {
+        const int hkv = a.hq / a.group;
+        int bx = c / hkv, kvh = c - bx * hkv;
+        if (!DECODE && !a.heads_interleaved) {
+          kvh = c / a.num_tiles;
+          bx = c - kvh * a.num_tiles;
+        }
+        t = describe<DECODE, true>(a, bx);
+        t.kvh = kvh;
+        if (k >= 2 && !warp_wait(BAR_DE + 8u * uint32_t(k & 1), uint32_t((k >> 1) - 1) & 1u,
+                                 abort_flag))
+          break;
+        if (lane == 0) descs[k & 1] = t;
+        warp_arrive(BAR_DF + 8u * uint32_t(k & 1));
+      } else if (!read_desc(k, t)) {
+        break;
+      }
+      ok = load_tiles<D, BS, SLOPES>(
+          a, t, loads_of(t), v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
+          (v ? a.vpool : a.kpool) + int64_t(t.kvh) * a.head_stride,
+          int(a.tma_row_base + int64_t(t.kvh) * a.tma_head_rows), base + (v ? Lo::V0 : Lo::K0),
+          v ? VF : KF, v ? VE : KE, v ? NV : NK, ring, abort_flag);
+    }
+    // Before the CTA gives up its shared memory the last load of every stage has
+    // landed: at once on the normal path; after a wait of another warp gave up, one
+    // more bounded wait that does not look at the abort flag.
+    if (lane == 0) {
+      const int stages = v ? NV : NK;
+      int drain_abort = 0;
+#pragma unroll 1
+      for (int n = max(0, ring.count - stages); n < ring.count; ++n)
+        tc::mbar_wait((v ? VF : KF) + 8u * uint32_t(n % stages), uint32_t(n / stages) & 1u,
+                      &drain_abort, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == SW) {
+    // --------------------------------------------------- Q, and S = Q K^T
+    // descriptors as in attention_tc.cu: 128-byte swizzle, 1024 bytes between
+    // 8-row groups in the high half
+    constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
+    constexpr uint32_t KV_STEP = uint32_t(Lo::KV_BYTES) >> 4;
+    static_assert(Lo::REF < (1 << 18), "descriptor address field");
+    const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
+    const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
+    int sk = 0, sb = 0, count = 0, used = 0;  // used: row tiles with keys so far
+    uint32_t k_phase = 0, b_phase = 1;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+      TileDesc t;
+      if (!read_desc(k, t)) break;
+      const int n_loads = loads_of(t);
+      if (n_loads == 0) continue;
+      // Q rows into shared memory once the last row tile's products have read
+      // theirs (zeros past the tile's rows): a lane finds four rows, and the warp
+      // copies whole rows, whose pieces lie together
+      if (used > 0 && !warp_wait(BAR_QE, uint32_t(used - 1) & 1u, abort_flag)) break;
+      ++used;
+      constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows an instruction
+#pragma unroll 1
+      for (int r0 = 0; r0 < BM; r0 += 32) {
+        const bf16* src = nullptr;
+        if (r0 + lane < t.n_rows) {
+          int64_t qi = 0, part = 0;
+          int head = 0, lim = 0;
+          row_info<DECODE>(a, t, t.kvh, r0 + lane, qi, head, part, lim);
+          src = a.q + (qi * a.hq + head) * D;
+        }
+#pragma unroll 8
+        for (int r = 0; r < 32; r += RPI) {
+          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(
+              0xffffffffu, reinterpret_cast<unsigned long long>(src), r + lane / CPR));
+          rxk::cp_async_16(sw128(sQ, BM, r0 + r + lane / CPR, lane % CPR),
+                           (from ? from : a.q) + lane % CPR * 8, from != nullptr);
+        }
+      }
+      rxk::cp_async_commit();
+      rxk::cp_async_wait<0>();
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (elect_one()) {
+        const uint32_t idesc = t.n_rows <= 64 ? tc::idesc_bf16(64, BS, 0)
+                                              : tc::idesc_bf16(BM, BS, 0);
+#pragma unroll 1
+        for (int j = 0; j < n_loads; ++j) {
+          // (products complete in order: the last tile of the buffer's P is enough)
+          if (count >= NS && !tc::mbar_wait(BAR_PF + 8u * (sb * SUBS + SUBS - 1), b_phase,
+                                            abort_flag, kWaitLimit, kSleepNs)) {
+            ok = false;
+            break;
+          }
+          if (!tc::mbar_wait(KF + 8u * sk, k_phase, abort_flag, kWaitLimit, kSleepNs)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t k_lo = k_lo0 + uint32_t(sk) * KV_STEP;
+          const uint32_t d_s = tmem + uint32_t(sb * BS);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t a_off = uint32_t(((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4);
+            const uint32_t b_off = uint32_t(((ks >> 2) * (BS * 128) + (ks & 3) * 32) >> 4);
+            mma_ss_split(d_s, q_lo + a_off, k_lo + b_off, DHI, idesc, ks > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(BAR_S + 8u * sb);
+          tc::mma_commit(KE + 8u * sk);
+          ++count;
+          if (++sk == NK) sk = 0, k_phase ^= 1u;
+          if (++sb == NS) sb = 0, b_phase ^= 1u;
+        }
+        tc::mma_commit(BAR_QE);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (elect_one()) {
+      tc::mma_commit(BAR_END);
+      int drain_abort = 0;
+      tc::mbar_wait(BAR_END, 0, &drain_abort, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == SW + 3) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
+    constexpr uint32_t KV_STEP = uint32_t(Lo::KV_BYTES) >> 4;
+    const uint32_t v_lo0 = (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BS * 128 / 16) << 16);
+    int sv = 0, pb = 0, used = 0;
+    uint32_t v_phase = 0, p_phase = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+      TileDesc t;
+      if (!read_desc(k, t)) break;
+      const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
+      if (n_loads == 0) continue;
+      if (elect_one()) {
+        const uint32_t idesc = t.n_rows <= 64 ? tc::idesc_bf16(64, D, 1) : tc::idesc_bf16(BM, D, 1);
+#pragma unroll 1
+        for (int j = 0; ok && j < n_loads * SUBS; ++j) {
+          const int sub = j % SUBS;
+          ok = tc::mbar_wait(BAR_P + 8u * pb, p_phase, abort_flag, kWaitLimit, kSleepNs) &&
+               (sub != 0 ||
+                tc::mbar_wait(VF + 8u * sv, v_phase, abort_flag, kWaitLimit, kSleepNs)) &&
+               (j > 0 || used == 0 || tc::mbar_wait(BAR_OE, uint32_t(used - 1) & 1u, abort_flag,
+                                                    kWaitLimit, kSleepNs));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (j < n_tiles) {
+            const uint32_t v_lo =
+                v_lo0 + uint32_t(sv) * KV_STEP + uint32_t(sub * (BN * 128 / 16));
+            const uint32_t p_t = tmem + uint32_t(pb * BN);
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+              mma_ts_split(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
+                           v_lo + uint32_t(ks * 2048 / 16), DHI, idesc,
+                           (j > 0 || ks > 0) ? 1u : 0u);
+          }
+          tc::mma_commit(BAR_PF + 8u * pb);
+          if (sub == SUBS - 1) {
+            tc::mma_commit(VE + 8u * sv);
+            if (++sv == NV) sv = 0, v_phase ^= 1u;
+          }
+          if (++pb == NB) pb = 0, p_phase ^= 1u;
+        }
+        tc::mma_commit(BAR_FIN);
+      }
+      ++used;
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (elect_one()) {
+      tc::mma_commit(BAR_END);
+      int drain_abort = 0;
+      tc::mbar_wait(BAR_END, 0, &drain_abort, kWaitLimit);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    // (fences of the tcgen05 proxy are each lane's, before its warp arrives)
+    const int wg = warp >> 2;
+    const int i = (warp & 3) * 32 + lane;  // TMEM lane
+    const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
+    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);   // [2][BM]
+    float* sums = reinterpret_cast<float*>(gbase + Lo::SUM);  // [NW][BM]
+    int g0 = 0;    // the row tile's first tile among all of the CTA's
+    int used = 0;  // row tiles with keys before it
+#pragma unroll 1
+    for (int k = 0, c = first; c < total; ++k, c += step) {
+    TileDesc t;
+    if (!read_desc(k, t)) break;
+    const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
+    // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
+    // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
+    const bool m64 = t.n_rows <= 64;
+    const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
+    const bool valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
+    int64_t out_row = 0;  // of the outputs, or of the partial ones
+    int lim = t.key_end;
+    RowMod rm;
     if (valid) {
-      row_info<DECODE>(a, t, kvh, row, qi, head, part, lim);
+      int64_t qi = 0, part = 0;
+      int head = 0;
+      row_info<DECODE>(a, t, t.kvh, row, qi, head, part, lim);
       const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
       if (!DECODE) lim = max(lim, t.bidir);
       rm = row_mod(a, qi, head, pos);
       rm.lo = max(rm.lo, t.key_lo);
+      out_row = (DECODE ? part : qi) * a.hq + head;
     } else {
       // a lane without a row: nothing it holds is masked or counts
       rm.lo = t.key_lo;
       rm.pos = INT32_MAX;
     }
-  }
-  if (warp < 8) {
-    // Q rows 16 warp .. + 15 into shared memory (zeros past the tile's rows): a
-    // lane finds a row, and the warp copies whole rows, whose pieces lie together
-    const int mine = 16 * warp + (lane & 15);
-    const bf16* src = nullptr;
-    if (mine < t.n_rows) {
-      int64_t gqi = 0, gpart = 0;
-      int ghead = 0, glim = 0;
-      row_info<DECODE>(a, t, kvh, mine, gqi, ghead, gpart, glim);
-      src = a.q + (gqi * a.hq + ghead) * D;
-    }
-    constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows an instruction
-#pragma unroll
-    for (int k = 0; k < 16 / RPI; ++k) {
-      const int r = k * RPI + lane / CPR, ch = lane % CPR;
-      const bf16* from = reinterpret_cast<const bf16*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-      rxk::cp_async_16(sw128(sQ, BM, 16 * warp + r, ch), (from ? from : a.q) + ch * 8,
-                       from != nullptr);
-    }
-    rxk::cp_async_commit();
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp >= SW) {
-    if (warp == SW + 1 || warp == SW + 2) {
-      const bool v = warp == SW + 2;
-      load_tiles<D, BS, SLOPES>(a, t, n_loads, v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
-                        (v ? a.vpool : a.kpool) + int64_t(kvh) * a.head_stride,
-                        int(a.tma_row_base + int64_t(kvh) * a.tma_head_rows),
-                        base + (v ? Lo::V0 : Lo::K0), v ? VF : KF, v ? VE : KE, v ? NV : NK,
-                        abort_flag);
-    } else {
-      if (elect_one()) {
-        const uint32_t idesc_s = m64 ? tc::idesc_bf16(64, BS, 0) : tc::idesc_bf16(BM, BS, 0);
-        const uint32_t idesc_pv = m64 ? tc::idesc_bf16(64, D, 1) : tc::idesc_bf16(BM, D, 1);
-        // descriptors as in attention_tc.cu: 128-byte swizzle, 1024 bytes
-        // between 8-row groups in the high half
-        constexpr uint32_t DHI = (1024u >> 4) | (1u << 14) | (2u << 29);
-        constexpr uint32_t KV_STEP = uint32_t(Lo::KV_BYTES) >> 4;
-        static_assert(Lo::REF < (1 << 18), "descriptor address field");
-        if (warp == SW) {
-          const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
-          const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
-          const bool ok = tc::mbar_wait(BAR_Q, 0, abort_flag, kWaitLimit, kSleepNs);
-          int sk = 0, sb = 0;
-          uint32_t k_phase = 0, b_phase = 1;
+    const bool narrow = !DECODE && a.out_bf16;
+    if (n_loads == 0) {
+      // no row of the tile sees a key (decode: at this step of the plan)
+      if (valid && wg < 2) {
+        const int64_t at = out_row * D + wg * (D / 2);
+        uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
+                            : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
+        const int n = narrow ? D / 16 : D / 8;
 #pragma unroll 1
-          for (int j = 0; ok && j < n_loads; ++j) {
-            // (products complete in order: the last tile of the buffer's P is enough)
-            if (j >= NS && !tc::mbar_wait(BAR_PF + 8u * (sb * SUBS + SUBS - 1), b_phase, abort_flag,
-                                          kWaitLimit, kSleepNs))
-              break;
-            if (!tc::mbar_wait(KF + 8u * sk, k_phase, abort_flag, kWaitLimit, kSleepNs)) break;
-            tc::tc_fence_after();
-            const uint32_t k_lo = k_lo0 + uint32_t(sk) * KV_STEP;
-            const uint32_t d_s = tmem + uint32_t(sb * BS);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t a_off = uint32_t(((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4);
-              const uint32_t b_off = uint32_t(((ks >> 2) * (BS * 128) + (ks & 3) * 32) >> 4);
-              mma_ss_split(d_s, q_lo + a_off, k_lo + b_off, DHI, idesc_s, ks > 0 ? 1u : 0u);
-            }
-            tc::mma_commit(BAR_S + 8u * sb);
-            tc::mma_commit(KE + 8u * sk);
-            if (++sk == NK) sk = 0, k_phase ^= 1u;
-            if (++sb == NS) sb = 0, b_phase ^= 1u;
-          }
-        } else {
-          const uint32_t v_lo0 =
-              (((base + Lo::V0) & 0x3FFFFu) >> 4) | (uint32_t(BS * 128 / 16) << 16);
-          int sv = 0, pb = 0;
-          uint32_t v_phase = 0, p_phase = 0;
-#pragma unroll 1
-          for (int j = 0; j < n_tiles; ++j) {
-            if (!tc::mbar_wait(BAR_P + 8u * pb, p_phase, abort_flag, kWaitLimit, kSleepNs)) break;
-            const int sub = j % SUBS;
-            if (sub == 0 &&
-                !tc::mbar_wait(VF + 8u * sv, v_phase, abort_flag, kWaitLimit, kSleepNs))
-              break;
-            tc::tc_fence_after();
-            const uint32_t v_lo = v_lo0 + uint32_t(sv) * KV_STEP + uint32_t(sub * (BN * 128 / 16));
-            const uint32_t p_t = tmem + uint32_t(pb * BN);
-#pragma unroll
-            for (int ks = 0; ks < BN / 16; ++ks)
-              mma_ts_split(tmem + uint32_t(Lo::O_COL), p_t + uint32_t(ks * 8),
-                           v_lo + uint32_t(ks * 2048 / 16), DHI, idesc_pv,
-                           (j > 0 || ks > 0) ? 1u : 0u);
-            tc::mma_commit(BAR_PF + 8u * pb);
-            if (sub == SUBS - 1) {
-              tc::mma_commit(VE + 8u * sv);
-              if (++sv == NV) sv = 0, v_phase ^= 1u;
-            }
-            if (++pb == NB) pb = 0, p_phase ^= 1u;
-          }
-        }
-        // every MMA this thread issued has completed once the final barrier (one
-        // arrival per issuing thread) completes; the wait ignores the abort flag
-        tc::mma_commit(BAR_FIN);
-        int drain_abort = 0;
-        tc::mbar_wait(BAR_FIN, 0, &drain_abort, kWaitLimit);
+        for (int u = 0; u < n; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = -INFINITY;
       }
-      __syncwarp();
-    }
-  } else {
-    // ------------------------------------------------------------ softmax
-    // (fences of the async and tcgen05 proxies are each lane's, before its warp arrives)
-    const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
-    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);  // [2][BM]
-    if (warp < 8) {
-      rxk::cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      warp_arrive(BAR_Q);
+      continue;
     }
     // what the rows of this warp have in common: keys [lo_max, lim_min) are seen
     // by all of them, and keys up to pos_min lie behind all of them
@@ -469,17 +591,30 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
     float l = 0.f;            // sum of this warpgroup's weights under it
     bool ok = true;
 #pragma unroll 1
-    for (int j = wg; j < n_tiles; j += NW) {
-      const int s = j % NB;
-      // waits are made warp-uniform before any warp-collective tcgen05 op
-      const int load = j / SUBS;
+    for (int j = (wg + NW - g0 % NW) % NW; j < n_loads * SUBS; j += NW) {
+      const int g = g0 + j;
+      const int s = g % NB;
+      const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g & 1) + (warp & 3));
+      if (j >= n_tiles) {
+        // the half of the last load without keys; it takes its turn all the same, so
+        // that no barrier runs ahead of the tile before
+        if (!warp_wait(BAR_H + 8u * uint32_t(4 * ((g - 1) & 1) + (warp & 3)),
+                       uint32_t((g - 1) >> 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        warp_arrive(h_bar);
+        warp_arrive(BAR_P + 8u * s);
+        continue;
+      }
+      const int load = g / SUBS;
       if (!warp_wait(BAR_S + 8u * uint32_t(load % NS), uint32_t(load / NS) & 1u, abort_flag)) {
         ok = false;
         break;
       }
       tc::tc_fence_after();
-      const int k0 =
-          t.key_begin + (SLOPES ? (n_loads - 1 - load) * BS + (j % SUBS) * BN : j * BN);
+      const int k0 = t.key_begin +
+                     (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
       uint32_t sr[BN];
       tc::tmem_ld_row<BN>(tl + uint32_t(s * BN), sr);
       tc::tmem_ld_wait();
@@ -580,8 +715,8 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
       if (j == 0) {
         m_ref = mx;
       } else {
-        const int p = (j - 1) & 1;
-        if (!warp_wait(BAR_H + 8u * (4 * p + (warp & 3)), uint32_t((j - 1) >> 1) & 1u,
+        const int p = (g - 1) & 1;
+        if (!warp_wait(BAR_H + 8u * uint32_t(4 * p + (warp & 3)), uint32_t((g - 1) >> 1) & 1u,
                        abort_flag)) {
           ok = false;
           break;
@@ -594,10 +729,10 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
         const bool empty = m_ref == -INFINITY;  // no weight yet: O is 0
         const bool grow = !empty && mx > m_ref + kRaise;
         if (__any_sync(0xffffffffu, grow)) {
-          // O is rescaled once PV_{j-1} has written it.  (Its barrier cannot be a
-          // phase behind: tile j - 1's scores were issued after PV_{j-1-NB} completed,
-          // and are done.)
-          if (!warp_wait(BAR_PF + 8u * uint32_t((j - 1) % NB), uint32_t((j - 1) / NB) & 1u,
+          // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
+          // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
+          // completed, and are done.)
+          if (!warp_wait(BAR_PF + 8u * uint32_t((g - 1) % NB), uint32_t((g - 1) / NB) & 1u,
                          abort_flag)) {
             ok = false;
             break;
@@ -605,13 +740,13 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
           tc::tc_fence_after();
           const float alpha = grow ? rxk::fast_exp2(m_ref - mx) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int oc = 0; oc < D; oc += 32) {
             uint32_t r[32];
-            tc::tmem_ld32(tl + uint32_t(Lo::O_COL + c), r);
+            tc::tmem_ld32(tl + uint32_t(Lo::O_COL + oc), r);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tc::tmem_st32(tl + uint32_t(Lo::O_COL + c), r);
+            tc::tmem_st32(tl + uint32_t(Lo::O_COL + oc), r);
           }
           tc::tmem_st_wait();
           tc::tc_fence_before();
@@ -623,8 +758,8 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
         if (empty) m_ref = mx;
       }
       // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
-      ref[(j & 1) * BM + i] = m_ref;
-      warp_arrive(BAR_H + 8u * uint32_t(4 * (j & 1) + (warp & 3)));
+      ref[(g & 1) * BM + i] = m_ref;
+      warp_arrive(h_bar);
       // ---- weights: bf16 into TMEM over S, their sum in fp32 before the rounding
       // (lse is then good to fp32, and o to the roundings of its weights)
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
@@ -650,39 +785,35 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
       tc::tc_fence_before();
       warp_arrive(BAR_P + 8u * s);
     }
-    // The final barrier completes after every MMA of the CTA; then the stages are
-    // idle and the warpgroups exchange their rows' (m, l).  Every softmax thread
-    // arrives, so no waiter is left behind when a wait gave up.
-    const bool fin = ok && n_tiles > 0 && warp_wait(BAR_FIN, 0, abort_flag);
-    float2* xch = reinterpret_cast<float2*>(gbase + Lo::XCH);  // [NW][BM]
-    if (fin) xch[wg * BM + i] = make_float2(m_ref, l);
+    // Once the row tile's products are done, O stands under the last reference; the
+    // warpgroups bring their sums there and exchange them.
+    if (!ok || !warp_wait(BAR_FIN, uint32_t(used) & 1u, abort_flag)) break;
+    tc::tc_fence_after();
+    const float m_fin = ref[((g0 + n_tiles - 1) & 1) * BM + i];
+    sums[wg * BM + i] = m_ref == -INFINITY ? 0.f : l * rxk::fast_exp2(m_ref - m_fin);
     warp_arrive(BAR_X);
-    const bool xok = warp_wait(BAR_X, 0, abort_flag);
-    if (fin && xok && wg < 2) {
-      tc::tc_fence_after();
-      float m_fin = m_ref;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) m_fin = fmaxf(m_fin, xch[w * BM + i].x);
+    if (!warp_wait(BAR_X, uint32_t(used) & 1u, abort_flag)) break;
+    g0 += n_loads * SUBS;
+    ++used;
+    if (wg < 2) {
       float l_all = 0.f;
-      if (m_fin > -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 x = xch[w * BM + i];
-          l_all += x.y * rxk::fast_exp2(x.x - m_fin);
-        }
-      }
+      for (int w = 0; w < NW; ++w) l_all += sums[w * BM + i];
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
       // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
       // sector) a thread and store: the rows need no trip through shared memory.
       constexpr int HC = D / 2;
-      const bool narrow = !DECODE && a.out_bf16;
-      const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * HC;
+      const int64_t at = out_row * D + wg * HC;
       const bool whole = (reinterpret_cast<uintptr_t>(DECODE ? a.ws_o : a.out) & 31) == 0;
 #pragma unroll 1
-      for (int c = 0; c < HC; c += 32) {
+      for (int oc = 0; oc < HC; oc += 32) {
         uint32_t r[32];
-        tc::tmem_ld32(tl + uint32_t(Lo::O_COL + wg * HC + c), r);
+        tc::tmem_ld32(tl + uint32_t(Lo::O_COL + wg * HC + oc), r);
         tc::tmem_ld_wait();
+        if (oc + 32 >= HC) {  // the next row tile's products may overwrite O
+          tc::tc_fence_before();
+          warp_arrive(BAR_OE);
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
         if (!valid) continue;
@@ -691,28 +822,19 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             h[e] = rxk::pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          bf16* dst = reinterpret_cast<bf16*>(a.out) + at + c;
+          bf16* dst = reinterpret_cast<bf16*>(a.out) + at + oc;
 #pragma unroll
           for (int e = 0; e < 16; e += 8) store_32(dst + 2 * e, &h[e], whole);
         } else {
-          float* dst = (DECODE ? a.ws_o : a.out) + at + c;
+          float* dst = (DECODE ? a.ws_o : a.out) + at + oc;
 #pragma unroll
           for (int e = 0; e < 32; e += 8) store_32(dst + e, &r[e], whole);
         }
       }
       if (valid && wg == 0)
-        (DECODE ? a.ws_lse : a.lse)[(DECODE ? part : qi) * a.hq + head] =
+        (DECODE ? a.ws_lse : a.lse)[out_row] =
             l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_all);
-    } else if (n_tiles <= 0 && valid && wg < 2) {
-      // no row of the tile sees a key (decode: at this step of the plan)
-      const int64_t at = ((DECODE ? part : qi) * a.hq + head) * D + wg * (D / 2);
-      const bool narrow = !DECODE && a.out_bf16;
-      uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
-                          : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
-      const int n = narrow ? D / 16 : D / 8;
-#pragma unroll 1
-      for (int c = 0; c < n; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (wg == 0) (DECODE ? a.ws_lse : a.lse)[(DECODE ? part : qi) * a.hq + head] = -INFINITY;
+    }
     }
   }
   tc::tc_fence_before();
@@ -724,17 +846,15 @@ __device__ __forceinline__ void tile4(const TcArgs& a, const Maps4& maps, uint8_
   }
 }
 
-// Extend: one tile per CTA, the heaviest row tiles first; heads as in
+// Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
 // attention_tc.cu.
 template <int D, bool CAP, bool SLOPES>
 __global__ void __launch_bounds__(kExtendThreads, 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const int c = int(blockIdx.x);
-  const int hkv = a.hq / a.group;
-  const int tile = a.heads_interleaved ? c / hkv : c % a.num_tiles;
-  const int kvh = a.heads_interleaved ? c - tile * hkv : c / a.num_tiles;
-  tile4<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, tile, kvh);
+  row_tiles<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
+                                                  int(gridDim.x),
+                                                  a.num_tiles * (a.hq / a.group));
 }
 
 // Decode: tiles of the plan's large items, then warp-role units of its small ones
@@ -755,10 +875,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
   const int cta = int(blockIdx.x) - a.n_warp_first;
-  if (cta >= 0 && cta < a.n_tc_ctas) {
-    const int hkv = a.hq / a.group;
-    tile4<D, kDecodeGroups, true, CAP, SLOPES>(a, maps, smem_raw, cta / hkv, cta - (cta / hkv) * hkv);
-  }
+  if (cta >= 0 && cta < a.n_tc_ctas)
+    row_tiles<D, kDecodeGroups, true, CAP, SLOPES>(a, maps, smem_raw, cta, a.n_tc_ctas,
+                                                   a.n_tc_ctas);
   if (threadIdx.x >= kPipeWarps * 32) return;  // the warp role uses the first six warps
   rxk::griddep_wait();
   const uint32_t raw = rxk::smem_addr(smem_raw);
@@ -843,7 +962,8 @@ rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   Maps4 maps;
   if (!make_maps(&maps, pool, Lo::BS))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
-  extend_mod_kernel<D, CAP, SLOPES><<<ctas, kExtendThreads, Lo::BYTES, s>>>(a, maps);
+  const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()));
+  extend_mod_kernel<D, CAP, SLOPES><<<grid, kExtendThreads, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 

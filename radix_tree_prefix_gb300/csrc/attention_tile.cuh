@@ -106,11 +106,13 @@ struct TileDesc {
   // before it, where the 16-key groups of the loads start), and every key
   // before bidir
   int key_lo, bidir;
+  int kvh;
 };
 
 template <bool DECODE, bool MOD>
 __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
   TileDesc t;
+  t.kvh = t.key_lo = t.bidir = 0;
   if constexpr (DECODE) {
     const int32_t* w = a.work + int64_t(bx) * RX_WORK_WORDS;
     t.trow = a.table + int64_t(w[0]) * a.row_stride;
@@ -120,7 +122,7 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
     t.part_base = w[5];
     t.n_rows = w[6];
     t.nomask_end = t.key_end;
-    t.gr0 = t.q_base = t.prefix = t.bidir = 0;
+    t.gr0 = t.q_base = t.prefix = 0;
   } else {
     const int tile = a.num_tiles - 1 - bx;  // heaviest first
     // the request of this tile: the last r with tile_indptr[r] <= tile, found
