@@ -38,7 +38,10 @@ namespace {
 
 constexpr int kGroup = 16;  // keys of a small TMA box
 // Softmax warpgroups.
-constexpr int kExtendGroups = 3, kExtendThreads = 128 * (kExtendGroups + 1);
+template <int D>
+struct ExtendGroups {
+  static constexpr int N = D == 128 ? 4 : 3, THREADS = 128 * (N + 1);
+};
 constexpr int kDecodeGroups = 2, kDecodeThreads = 128 * (kDecodeGroups + 1);
 // A row's reference is raised when a score exceeds it by more than this (log2
 // units).  Raising stops the chain between the warpgroups until the product
@@ -56,17 +59,20 @@ struct Layout4 {
   static constexpr int BS = D == 128 ? 128 : 64;
   static constexpr int SUBS = BS / BN;
   static constexpr int KV_BYTES = BS * D * 2;
-  static constexpr int NK = 3, NV = D == 128 ? 3 : 2;
+  static constexpr int NK = 3, NV = 2;
   static constexpr int NS = D == 128 ? 3 : 4;
   static constexpr int NB = NS * SUBS;  // tiles of P
+  // Barriers of the reference's way from tile to tile.  A warpgroup that waits for
+  // tile g - 1 knows tile g - NW - 1 done; NW = 4 of them need a ring of four.
+  static constexpr int NH = D == 128 ? 4 : 2;
   static constexpr int Q = 0;
   static constexpr int K0 = BM * D * 2;
   static constexpr int V0 = K0 + NK * KV_BYTES;
   static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
   static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
-  static constexpr int DESC = SUM + 3 * BM * 4;   // the row tile in hand and the next
+  static constexpr int DESC = SUM + (D == 128 ? 4 : 3) * BM * 4;   // the row tile in hand and the next
   static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
-  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 8 + 9;
+  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 9;
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
@@ -263,6 +269,88 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
   return ok;
 }
 
+// What the cap multiplies a raw score near 0 by, a polynomial in its square; the
+// same of the scores sr[at .. at + 15].
+__device__ __forceinline__ float cap_factor(const TcArgs& a, float s) {
+  const float v = s * s;
+  float p = a.cap_fold2[kTanhNearTerms - 1].x;
+#pragma unroll
+  for (int d = kTanhNearTerms - 2; d >= 0; --d) p = fmaf(p, v, a.cap_fold2[d].x);
+  return p;
+}
+__device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr)[32], int at,
+                                            float2 (&p)[8]) {
+  float2 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 x = make_float2(__uint_as_float(sr[at + 2 * k]),
+                                 __uint_as_float(sr[at + 2 * k + 1]));
+    v[k] = __fmul2_rn(x, x);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    p[k] = __ffma2_rn(a.cap_fold2[kTanhNearTerms - 1], v[k], a.cap_fold2[kTanhNearTerms - 2]);
+#pragma unroll
+  for (int d = kTanhNearTerms - 3; d >= 0; --d)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_fold2[d]);
+}
+// Raw scores capped in place, in log2 units.
+__device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near) {
+  if (near) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 16) {
+      float2 p[8];
+      cap_factors(a, sr, e, p);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sr[e + 2 * k] = __float_as_uint(__uint_as_float(sr[e + 2 * k]) * p[k].x);
+        sr[e + 2 * k + 1] = __float_as_uint(__uint_as_float(sr[e + 2 * k + 1]) * p[k].y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      sr[e] = __float_as_uint(a.cap_out * tanh_exp(__uint_as_float(sr[e]) * a.cap_in));
+  }
+}
+// sr * scale - slope |away + e|; behind: no key lies after the row's query, and the
+// bias is linear in the key.
+__device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, float slope,
+                                           float away, bool behind) {
+  if (behind) {
+    const float2 scale2 = make_float2(scale, scale);
+    float2 in8[4];  // within a group of eight keys
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      in8[u] = make_float2(slope * float(2 * u), slope * float(2 * u + 1));
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      const float b = slope * (away + float(e));
+      const float2 b2 = make_float2(b, b);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 x = make_float2(__uint_as_float(sr[e + 2 * u]),
+                                     __uint_as_float(sr[e + 2 * u + 1]));
+        const float2 y = __ffma2_rn(x, scale2, __fadd2_rn(b2, in8[u]));
+        sr[e + 2 * u] = __float_as_uint(y.x);
+        sr[e + 2 * u + 1] = __float_as_uint(y.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      sr[e] = __float_as_uint(
+          fmaf(-slope, fabsf(away + float(e)), __uint_as_float(sr[e]) * scale));
+  }
+}
+// -inf but in [from, from + span)
+__device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int span) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (uint32_t(e - from) >= uint32_t(span)) sr[e] = 0xff800000u;
+}
+
 // A CTA's row tiles first, first + step, .. below total, one after another: the
 // loaders and the issuing warps run ahead into the next row tile while the softmax
 // warps finish one and write it.  (One CTA a row tile left its SM idle for some 9
@@ -275,7 +363,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
                                           int first, int step, int total) {
   using Lo = Layout4<D>;
   constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
-  constexpr int SUBS = Lo::SUBS;
+  constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
+  static_assert(NW <= 3 || NH >= 4, "reference barriers");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
   const uint32_t base = rxk::smem_addr(gbase);
   if (base & 1023u) {  // uniform over the CTA: nothing initialised yet
@@ -287,9 +376,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   const uint32_t BAR_S = VE + 8u * NV, BAR_P = BAR_S + 8u * NS;
   // PV of tile g completes phase g / NB of its buffer's barrier: S may overwrite P
   const uint32_t BAR_PF = BAR_P + 8u * NB;
-  // the references of a quadrant's rows at even (0-3) and odd (4-7) tiles are set
+  // the reference of tile g is set for a quadrant's rows: 4 (g % NH) + quadrant
   const uint32_t BAR_H = BAR_PF + 8u * NB;
-  const uint32_t BAR_FIN = BAR_H + 64u;   // a row tile's products are done
+  const uint32_t BAR_FIN = BAR_H + 32u * NH;   // a row tile's products are done
   const uint32_t BAR_X = BAR_FIN + 8u;    // its warpgroups' sums are written
   const uint32_t BAR_OE = BAR_X + 8u;     // its O has been read
   const uint32_t BAR_QE = BAR_OE + 8u;    // its Q has
@@ -307,7 +396,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       tc::mbar_init(BAR_P + 8u * b, 4);
       tc::mbar_init(BAR_PF + 8u * b, 1);
     }
-    for (int b = 0; b < 8; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
+    for (int b = 0; b < 4 * NH; ++b) tc::mbar_init(BAR_H + 8u * b, 1);
     tc::mbar_init(BAR_FIN, 1);
     tc::mbar_init(BAR_X, SW);
     tc::mbar_init(BAR_OE, 8);
@@ -594,12 +683,15 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     for (int j = (wg + NW - g0 % NW) % NW; j < n_loads * SUBS; j += NW) {
       const int g = g0 + j;
       const int s = g % NB;
-      const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g & 1) + (warp & 3));
+      const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g % NH) + (warp & 3));
+      const uint32_t h_before = BAR_H + 8u * uint32_t(4 * ((g + NH - 1) % NH) + (warp & 3));
+      const uint32_t h_parity = uint32_t((g + NH - 1) / NH - 1) & 1u;
       if (j >= n_tiles) {
         // the half of the last load without keys; it takes its turn all the same, so
-        // that no barrier runs ahead of the tile before
-        if (!warp_wait(BAR_H + 8u * uint32_t(4 * ((g - 1) & 1) + (warp & 3)),
-                       uint32_t((g - 1) >> 1) & 1u, abort_flag)) {
+        // that no barrier is arrived at before its last phase is done
+        if (!warp_wait(h_before, h_parity, abort_flag) ||
+            (g >= NB && !warp_wait(BAR_PF + 8u * uint32_t(s), uint32_t(g / NB - 1) & 1u,
+                                   abort_flag))) {
           ok = false;
           break;
         }
@@ -615,109 +707,56 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       tc::tc_fence_after();
       const int k0 = t.key_begin +
                      (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
-      uint32_t sr[BN];
-      tc::tmem_ld_row<BN>(tl + uint32_t(s * BN), sr);
-      tc::tmem_ld_wait();
-      auto get = [&](int e) { return __uint_as_float(sr[e]); };
-      auto get2 = [&](int e) { return make_float2(get(e), get(e + 1)); };
-      auto put2 = [&](int e, float2 v) {
-        sr[e] = __float_as_uint(v.x);
-        sr[e + 1] = __float_as_uint(v.y);
-      };
-      // ---- the modified scores, in log2 units once multiplied by a.mul
-      if constexpr (CAP) {
+      const bool masked = k0 < lo_max || k0 + BN > lim_min;
+      const bool behind = k0 + BN - 1 <= pos_min;
+      // ---- first pass over the scores, 32 at a time: the row's maximum (raw where
+      // nothing but a cap modifies them, since that keeps their order).  near: the
+      // raw scores of 32 x 32 are within the cap's polynomial (bit c / 32).
+      float mx = -INFINITY;
+      uint32_t near = 0;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t sr[32];
+        tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
+        tc::tmem_ld_wait();
+        if constexpr (CAP) {
+          float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) {
-          // the shortest polynomial that holds for all of these 32 x 32 scores
-          float am = 0.f, an = 0.f;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            am = fmaxf(am, fmaxf(fabsf(get(c + e)), fabsf(get(c + e + 1))));
-            an = fmaxf(an, fmaxf(fabsf(get(c + e + 2)), fabsf(get(c + e + 3))));
-          }
-          const float most = valid ? fmaxf(am, an) * a.cap_in : 0.f;
-          if (__all_sync(0xffffffffu, most <= 0.5f)) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              float2 u[8], v[8], p[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) u[k] = __fmul2_rn(get2(c + e + 2 * k), a.cap_in2);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = __fmul2_rn(u[k], u[k]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                p[k] = __ffma2_rn(a.cap_near2[3], v[k], a.cap_near2[2]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_near2[1]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_near2[0]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) put2(c + e + 2 * k, __fmul2_rn(u[k], p[k]));
-            }
-          } else if (__all_sync(0xffffffffu, most <= 1.f)) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 u = __fmul2_rn(get2(c + e), a.cap_in2);
-              const float2 v = __fmul2_rn(u, u);
-              float2 p = a.cap_poly2[kTanhTerms - 1];
-#pragma unroll
-              for (int k = kTanhTerms - 2; k >= 0; --k) p = __ffma2_rn(p, v, a.cap_poly2[k]);
-              put2(c + e, __fmul2_rn(u, p));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              sr[c + e] = __float_as_uint(a.cap_out * tanh_exp(get(c + e) * a.cap_in));
-          }
-        }
-      }
-      if constexpr (SLOPES) {
-        const float scale = CAP ? 1.f : a.scale_log2;  // (a cap has taken it in)
-        const float2 scale2 = make_float2(scale, scale);
-        const float away = float(k0 - rm.pos);
-        if (k0 + BN - 1 <= pos_min) {
-          // every key lies behind every row: -slope (pos - key) is linear in it
-          float2 in8[4];  // within a group of eight keys
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            in8[u] = make_float2(rm.slope * float(2 * u), rm.slope * float(2 * u + 1));
-#pragma unroll
-          for (int e = 0; e < BN; e += 8) {
-            const float b = rm.slope * (away + float(e));
-            const float2 b2 = make_float2(b, b);
+          for (int e = 0; e < 32; e += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              put2(e + 2 * u, __ffma2_rn(get2(e + 2 * u), scale2, __fadd2_rn(b2, in8[u])));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            sr[e] = __float_as_uint(
-                fmaf(-rm.slope, fabsf(away + float(e)), get(e) * scale));
+              am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
+                                         fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
+          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+          if (__all_sync(0xffffffffu, !valid || most <= a.cap_near)) near |= 1u << (c >> 5);
         }
+        if constexpr (SLOPES) {
+          if constexpr (CAP) cap_scores(a, sr, (near >> (c >> 5) & 1u) != 0);
+          add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
+        }
+        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        float mx4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
+                                         __uint_as_float(sr[e + 2 * u + 1])));
+        mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       }
-      if (k0 < lo_max || k0 + BN > lim_min) {
-        const int from = rm.lo - k0;
-        const uint32_t span = uint32_t(max(0, lim - rm.lo));
-#pragma unroll
-        for (int e = 0; e < BN; ++e)
-          if (uint32_t(e - from) >= span) sr[e] = 0xff800000u;  // -inf
+      if constexpr (CAP && !SLOPES) {
+        const float u = mx * a.cap_in;
+        mx = fabsf(mx) <= a.cap_near ? mx * cap_factor(a, mx) : a.cap_out * tanh_exp(u);
+      } else {
+        mx *= a.mul;
       }
-      // ---- the row's reference: that of tile j - 1, raised if need be
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < BN; e += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          mx4[u] = fmaxf(mx4[u], fmaxf(get(e + 2 * u), get(e + 2 * u + 1)));
-      float mx = a.mul * fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      // ---- the row's reference: that of tile g - 1, raised if need be
       if (!valid) mx = 0.f;
       if (j == 0) {
         m_ref = mx;
       } else {
         const int p = (g - 1) & 1;
-        if (!warp_wait(BAR_H + 8u * uint32_t(4 * p + (warp & 3)), uint32_t((g - 1) >> 1) & 1u,
-                       abort_flag)) {
+        if (!warp_wait(h_before, h_parity, abort_flag)) {
           ok = false;
           break;
         }
@@ -767,16 +806,52 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       float2 l4[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
-        uint32_t pk[16];
+        uint32_t sr[32], pk[16];
+        tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
+        tc::tmem_ld_wait();
+        auto get2 = [&](int e) {
+          return make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+        };
+        auto put2 = [&](int e, float2 v) {
+          sr[e] = __float_as_uint(v.x);
+          sr[e + 1] = __float_as_uint(v.y);
+        };
+        // the exponents, in place
+        if constexpr (CAP && !SLOPES) {
+          if (near >> (c >> 5) & 1u) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              float2 f[8];
+              cap_factors(a, sr, e, f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                put2(e + 2 * k, __ffma2_rn(get2(e + 2 * k), f[k], neg2));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              sr[e] = __float_as_uint(
+                  fmaf(a.cap_out, tanh_exp(__uint_as_float(sr[e]) * a.cap_in), neg2.x));
+          }
+        } else {
+          if constexpr (SLOPES) {
+            if constexpr (CAP) cap_scores(a, sr, (near >> (c >> 5) & 1u) != 0);
+            add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) put2(e, __ffma2_rn(get2(e), a.mul2, neg2));
+        }
+        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 x = __ffma2_rn(get2(c + e), a.mul2, neg2);
-          const float2 p = make_float2(rxk::fast_exp2(x.x), rxk::fast_exp2(x.y));
+          const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
+                                       rxk::fast_exp2(__uint_as_float(sr[e + 1])));
           l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
           pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
         }
+        // (over scores read already)
         tmem_st16(tl + uint32_t(s * BN + c / 2), pk);
       }
       const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
@@ -849,10 +924,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 // Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
 // attention_tc.cu.
 template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kExtendThreads, 1)
+__global__ void __launch_bounds__(ExtendGroups<D>::THREADS, 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  row_tiles<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
+  row_tiles<D, ExtendGroups<D>::N, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
                                                   int(gridDim.x),
                                                   a.num_tiles * (a.hq / a.group));
 }
@@ -936,13 +1011,24 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
   a->tma_head_rows = pool->num_slots;
   a->cap_in = m.softcap > 0.f ? scale / m.softcap : 0.f;
   a->cap_out = m.softcap * kLog2e;
-  a->cap_in2 = make_float2(a->cap_in, a->cap_in);
-  for (int i = 0; i < kTanhTerms; ++i) {
-    a->cap_poly[i] = kTanh[i] * a->cap_out;
-    a->cap_poly2[i] = make_float2(a->cap_poly[i], a->cap_poly[i]);
+  for (int i = 0; i < kTanhTerms; ++i) a->cap_poly[i] = kTanh[i] * a->cap_out;
+  if (m.softcap > 0.f) {
+    // kTanhNear with cap_in, a power of it and cap_out folded in.  A coefficient too
+    // small for fp32 is left out, and with it the scores for which its term would
+    // count (2^-27 of the sum).
+    double u = 0.6;  // largest |scale s / softcap|
+    for (int i = 0; i < kTanhNearTerms; ++i) {
+      const double k = double(a->cap_in);
+      const double c = double(kTanhNear[i]) * double(a->cap_out) * pow(k, 2 * i + 1);
+      float f = float(c);
+      if (fabs(c) < 1e-37) {
+        f = 0.f;
+        if (i > 0) u = std::min(u, pow(7e-9 / fabs(double(kTanhNear[i])), 0.5 / i));
+      }
+      a->cap_fold2[i] = make_float2(f, f);
+    }
+    a->cap_near = float(u / double(a->cap_in));
   }
-  for (int i = 0; i < kTanhNearTerms; ++i)
-    a->cap_near2[i] = make_float2(kTanhNear[i] * a->cap_out, kTanhNear[i] * a->cap_out);
   a->window = m.window;
   a->slopes = m.d_slopes;
   a->key_begin = m.d_key_begin;
@@ -963,7 +1049,7 @@ rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   if (!make_maps(&maps, pool, Lo::BS))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()));
-  extend_mod_kernel<D, CAP, SLOPES><<<grid, kExtendThreads, Lo::BYTES, s>>>(a, maps);
+  extend_mod_kernel<D, CAP, SLOPES><<<grid, ExtendGroups<D>::THREADS, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 

@@ -87,8 +87,10 @@ struct TcArgs {
   float cap_poly[7];       // of tanh (kTanh), times cap_out
   float mul;               // what a modified score is still to be multiplied by: 1, or
                            // scale_log2 when nothing but masks modifies it
-  float2 cap_in2, mul2, cap_poly2[7];  // the same twice, for two scores at a time
-  float2 cap_near2[4];     // of kTanhNear
+  float2 mul2;             // twice, for two scores at a time
+  float2 cap_fold2[5];     // of kTanhNear with cap_in and cap_out in it, twice: a raw
+  float cap_near;          // score of at most this magnitude times a polynomial in its
+                           // square
   int window;              // 0: none
   const float* slopes;
   const int32_t* key_begin;
@@ -263,9 +265,10 @@ __device__ __forceinline__ RowMod row_mod(const TcArgs& a, int64_t qi, int head,
 constexpr int kTanhTerms = 7;
 constexpr float kTanh[kTanhTerms] = {0.99999994f, -0.3333284f,   0.13325204f,  -0.05345703f,
                                      0.02028998f, -0.006203379f, 0.0010410226f};
-// The same for |u| <= 1/2, of degree 3: 5.4e-7, 6.2e-7 in fp32.
-constexpr int kTanhNearTerms = 4;
-constexpr float kTanhNear[kTanhNearTerms] = {0.99999946f, -0.3332632f, 0.13190296f, -0.044402227f};
+// The same for |u| <= 0.6, of degree 4: 7e-8, 1.8e-7 in fp32.
+constexpr int kTanhNearTerms = 5;
+constexpr float kTanhNear[kTanhNearTerms] = {0.99999994f, -0.3333231f, 0.13310173f, -0.05210148f,
+                                             0.015475428f};
 // tanh(u) = 1 - 2 / (1 + e^2u), off by some 2^-22 at most
 __device__ __forceinline__ float tanh_exp(float u) {
   return fmaf(-2.f, __fdividef(1.f, 1.f + rxk::fast_exp2(u * (2.f * kLog2e))), 1.f);
