@@ -40,7 +40,7 @@ constexpr int kGroup = 16;  // keys of a small TMA box
 // Softmax warpgroups.
 template <int D>
 struct ExtendGroups {
-  static constexpr int N = D == 128 ? 4 : 3, THREADS = 128 * (N + 1);
+  static constexpr int N = D == 128 ? 3 : 3, THREADS = 128 * (N + 1);
 };
 constexpr int kDecodeGroups = 2, kDecodeThreads = 128 * (kDecodeGroups + 1);
 // A row's reference is raised when a score exceeds it by more than this (log2
@@ -113,10 +113,19 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Waits out of line: what a wait does when its barrier is not ready stands
+// elsewhere, so that the roles' loops are short stretches of code.  (They share
+// an instruction cache with the softmax, and fetch from it most of the time.)
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return tc::mbar_wait(bar, parity, abort_flag, kWaitLimit);
+}
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag);
+}
 // Barriers between warps: a warp waits as one and arrives once.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, kWaitLimit));
+  if (__builtin_expect(__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)), 1)) return true;
+  return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag));
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -269,15 +278,8 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
   return ok;
 }
 
-// What the cap multiplies a raw score near 0 by, a polynomial in its square; the
-// same of the scores sr[at .. at + 15].
-__device__ __forceinline__ float cap_factor(const TcArgs& a, float s) {
-  const float v = s * s;
-  float p = a.cap_fold2[kTanhNearTerms - 1].x;
-#pragma unroll
-  for (int d = kTanhNearTerms - 2; d >= 0; --d) p = fmaf(p, v, a.cap_fold2[d].x);
-  return p;
-}
+// What the cap multiplies the raw scores sr[at .. at + 15] by, a polynomial in their
+// squares.
 __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr)[32], int at,
                                             float2 (&p)[8]) {
   float2 v[8];
@@ -297,15 +299,17 @@ __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr
 }
 // Raw scores capped in place, in log2 units.
 __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near) {
-  if (near) {
+  if (__builtin_expect(near, 1)) {
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
       float2 p[8];
       cap_factors(a, sr, e, p);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        sr[e + 2 * k] = __float_as_uint(__uint_as_float(sr[e + 2 * k]) * p[k].x);
-        sr[e + 2 * k + 1] = __float_as_uint(__uint_as_float(sr[e + 2 * k + 1]) * p[k].y);
+        const float2 y = __fmul2_rn(make_float2(__uint_as_float(sr[e + 2 * k]),
+                                                __uint_as_float(sr[e + 2 * k + 1])), p[k]);
+        sr[e + 2 * k] = __float_as_uint(y.x);
+        sr[e + 2 * k + 1] = __float_as_uint(y.y);
       }
     }
   } else {
@@ -318,7 +322,7 @@ __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], 
 // bias is linear in the key.
 __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, float slope,
                                            float away, bool behind) {
-  if (behind) {
+  if (__builtin_expect(behind, 1)) {
     const float2 scale2 = make_float2(scale, scale);
     float2 in8[4];  // within a group of eight keys
 #pragma unroll
@@ -532,12 +536,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 #pragma unroll 1
         for (int j = 0; j < n_loads; ++j) {
           // (products complete in order: the last tile of the buffer's P is enough)
-          if (count >= NS && !tc::mbar_wait(BAR_PF + 8u * (sb * SUBS + SUBS - 1), b_phase,
-                                            abort_flag, kWaitLimit, kSleepNs)) {
-            ok = false;
-            break;
-          }
-          if (!tc::mbar_wait(KF + 8u * sk, k_phase, abort_flag, kWaitLimit, kSleepNs)) {
+          if ((count >= NS &&
+               !lane_wait(BAR_PF + 8u * (sb * SUBS + SUBS - 1), b_phase, abort_flag)) ||
+              !lane_wait(KF + 8u * sk, k_phase, abort_flag)) {
             ok = false;
             break;
           }
@@ -585,11 +586,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 #pragma unroll 1
         for (int j = 0; ok && j < n_loads * SUBS; ++j) {
           const int sub = j % SUBS;
-          ok = tc::mbar_wait(BAR_P + 8u * pb, p_phase, abort_flag, kWaitLimit, kSleepNs) &&
-               (sub != 0 ||
-                tc::mbar_wait(VF + 8u * sv, v_phase, abort_flag, kWaitLimit, kSleepNs)) &&
-               (j > 0 || used == 0 || tc::mbar_wait(BAR_OE, uint32_t(used - 1) & 1u, abort_flag,
-                                                    kWaitLimit, kSleepNs));
+          ok = lane_wait(BAR_P + 8u * pb, p_phase, abort_flag) &&
+               (sub != 0 || lane_wait(VF + 8u * sv, v_phase, abort_flag)) &&
+               (j > 0 || used == 0 || lane_wait(BAR_OE, uint32_t(used - 1) & 1u, abort_flag));
           if (!ok) break;
           tc::tc_fence_after();
           if (j < n_tiles) {
@@ -686,7 +685,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g % NH) + (warp & 3));
       const uint32_t h_before = BAR_H + 8u * uint32_t(4 * ((g + NH - 1) % NH) + (warp & 3));
       const uint32_t h_parity = uint32_t((g + NH - 1) / NH - 1) & 1u;
-      if (j >= n_tiles) {
+      if (__builtin_expect(j >= n_tiles, 0)) {
         // the half of the last load without keys; it takes its turn all the same, so
         // that no barrier is arrived at before its last phase is done
         if (!warp_wait(h_before, h_parity, abort_flag) ||
@@ -709,11 +708,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
                      (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
       const bool masked = k0 < lo_max || k0 + BN > lim_min;
       const bool behind = k0 + BN - 1 <= pos_min;
-      // ---- first pass over the scores, 32 at a time: the row's maximum (raw where
-      // nothing but a cap modifies them, since that keeps their order).  near: the
-      // raw scores of 32 x 32 are within the cap's polynomial (bit c / 32).
+      // ---- first pass over the scores, 32 at a time: modified, back into TMEM, and
+      // the row's maximum
       float mx = -INFINITY;
-      uint32_t near = 0;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t sr[32];
@@ -728,13 +725,12 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
               am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
                                          fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
           const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-          if (__all_sync(0xffffffffu, !valid || most <= a.cap_near)) near |= 1u << (c >> 5);
+          cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near));
         }
-        if constexpr (SLOPES) {
-          if constexpr (CAP) cap_scores(a, sr, (near >> (c >> 5) & 1u) != 0);
+        if constexpr (SLOPES)
           add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
-        }
-        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        if (__builtin_expect(masked, 0)) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        if constexpr (CAP || SLOPES) tc::tmem_st32(tl + uint32_t(s * BN + c), sr);
         float mx4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
@@ -744,12 +740,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
                                          __uint_as_float(sr[e + 2 * u + 1])));
         mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       }
-      if constexpr (CAP && !SLOPES) {
-        const float u = mx * a.cap_in;
-        mx = fabsf(mx) <= a.cap_near ? mx * cap_factor(a, mx) : a.cap_out * tanh_exp(u);
-      } else {
-        mx *= a.mul;
-      }
+      if constexpr (CAP || SLOPES) tc::tmem_st_wait();
+      mx *= a.mul;
       // ---- the row's reference: that of tile g - 1, raised if need be
       if (!valid) mx = 0.f;
       if (j == 0) {
@@ -767,7 +759,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
         const bool empty = m_ref == -INFINITY;  // no weight yet: O is 0
         const bool grow = !empty && mx > m_ref + kRaise;
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
           // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
           // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
           // completed, and are done.)
@@ -819,31 +811,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           sr[e + 1] = __float_as_uint(v.y);
         };
         // the exponents, in place
-        if constexpr (CAP && !SLOPES) {
-          if (near >> (c >> 5) & 1u) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              float2 f[8];
-              cap_factors(a, sr, e, f);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                put2(e + 2 * k, __ffma2_rn(get2(e + 2 * k), f[k], neg2));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              sr[e] = __float_as_uint(
-                  fmaf(a.cap_out, tanh_exp(__uint_as_float(sr[e]) * a.cap_in), neg2.x));
-          }
-        } else {
-          if constexpr (SLOPES) {
-            if constexpr (CAP) cap_scores(a, sr, (near >> (c >> 5) & 1u) != 0);
-            add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) put2(e, __ffma2_rn(get2(e), a.mul2, neg2));
-        }
-        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        for (int e = 0; e < 32; e += 2) put2(e, __ffma2_rn(get2(e), a.mul2, neg2));
+        if (!CAP && !SLOPES && __builtin_expect(masked, 0))
+          mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
