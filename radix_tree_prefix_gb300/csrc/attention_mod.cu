@@ -37,11 +37,9 @@
 namespace {
 
 constexpr int kGroup = 16;  // keys of a small TMA box
-// Softmax warpgroups.
-template <int D>
-struct ExtendGroups {
-  static constexpr int N = D == 128 ? 3 : 3, THREADS = 128 * (N + 1);
-};
+// Softmax warpgroups: three where 128 registers a thread are enough, two beside
+// decode's warp role.
+constexpr int kExtendGroups = 3, kExtendThreads = 128 * (kExtendGroups + 1);
 constexpr int kDecodeGroups = 2, kDecodeThreads = 128 * (kDecodeGroups + 1);
 // A row's reference is raised when a score exceeds it by more than this (log2
 // units).  Raising stops the chain between the warpgroups until the product
@@ -62,15 +60,15 @@ struct Layout4 {
   static constexpr int NK = 3, NV = 2;
   static constexpr int NS = D == 128 ? 3 : 4;
   static constexpr int NB = NS * SUBS;  // tiles of P
-  // Barriers of the reference's way from tile to tile.  A warpgroup that waits for
-  // tile g - 1 knows tile g - NW - 1 done; NW = 4 of them need a ring of four.
-  static constexpr int NH = D == 128 ? 4 : 2;
+  // Barriers of the reference's way from tile to tile: a warpgroup of three that
+  // waits for tile g - 1 did tile g - 3 itself, so a ring of two is enough.
+  static constexpr int NH = 2;
   static constexpr int Q = 0;
   static constexpr int K0 = BM * D * 2;
   static constexpr int V0 = K0 + NK * KV_BYTES;
   static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
   static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
-  static constexpr int DESC = SUM + (D == 128 ? 4 : 3) * BM * 4;   // the row tile in hand and the next
+  static constexpr int DESC = SUM + 3 * BM * 4;   // the row tile in hand and the next
   static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
   static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 9;
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
@@ -124,7 +122,7 @@ __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatil
 }
 // Barriers between warps: a warp waits as one and arrives once.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (__builtin_expect(__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)), 1)) return true;
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag));
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -299,7 +297,7 @@ __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr
 }
 // Raw scores capped in place, in log2 units.
 __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near) {
-  if (__builtin_expect(near, 1)) {
+  if (near) {
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
       float2 p[8];
@@ -322,7 +320,7 @@ __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], 
 // bias is linear in the key.
 __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, float slope,
                                            float away, bool behind) {
-  if (__builtin_expect(behind, 1)) {
+  if (behind) {
     const float2 scale2 = make_float2(scale, scale);
     float2 in8[4];  // within a group of eight keys
 #pragma unroll
@@ -368,7 +366,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   using Lo = Layout4<D>;
   constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
-  static_assert(NW <= 3 || NH >= 4, "reference barriers");
+  static_assert(NW <= 3, "reference barriers");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
   const uint32_t base = rxk::smem_addr(gbase);
   if (base & 1023u) {  // uniform over the CTA: nothing initialised yet
@@ -685,7 +683,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g % NH) + (warp & 3));
       const uint32_t h_before = BAR_H + 8u * uint32_t(4 * ((g + NH - 1) % NH) + (warp & 3));
       const uint32_t h_parity = uint32_t((g + NH - 1) / NH - 1) & 1u;
-      if (__builtin_expect(j >= n_tiles, 0)) {
+      if (j >= n_tiles) {
         // the half of the last load without keys; it takes its turn all the same, so
         // that no barrier is arrived at before its last phase is done
         if (!warp_wait(h_before, h_parity, abort_flag) ||
@@ -729,7 +727,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
         if constexpr (SLOPES)
           add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
-        if (__builtin_expect(masked, 0)) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
         if constexpr (CAP || SLOPES) tc::tmem_st32(tl + uint32_t(s * BN + c), sr);
         float mx4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -759,7 +757,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
         const bool empty = m_ref == -INFINITY;  // no weight yet: O is 0
         const bool grow = !empty && mx > m_ref + kRaise;
-        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+        if (__any_sync(0xffffffffu, grow)) {
           // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
           // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
           // completed, and are done.)
@@ -813,8 +811,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         // the exponents, in place
 #pragma unroll
         for (int e = 0; e < 32; e += 2) put2(e, __ffma2_rn(get2(e), a.mul2, neg2));
-        if (!CAP && !SLOPES && __builtin_expect(masked, 0))
-          mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
+        if (!CAP && !SLOPES && masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
@@ -895,10 +892,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 // Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
 // attention_tc.cu.
 template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(ExtendGroups<D>::THREADS, 1)
+__global__ void __launch_bounds__(kExtendThreads, 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  row_tiles<D, ExtendGroups<D>::N, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
+  row_tiles<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
                                                   int(gridDim.x),
                                                   a.num_tiles * (a.hq / a.group));
 }
@@ -1020,7 +1017,7 @@ rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   if (!make_maps(&maps, pool, Lo::BS))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()));
-  extend_mod_kernel<D, CAP, SLOPES><<<grid, ExtendGroups<D>::THREADS, Lo::BYTES, s>>>(a, maps);
+  extend_mod_kernel<D, CAP, SLOPES><<<grid, kExtendThreads, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 
