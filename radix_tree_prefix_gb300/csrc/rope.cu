@@ -17,10 +17,13 @@
 // read and no position is too far.
 //
 // Bound by HBM: every row is read once and written once.  A thread holds the
-// eight pairs of one chunk of a head (16 elements in two 16-byte pieces), so
+// eight pairs of one share of a head (16 elements in two 16-byte pieces), so
 // D/16 threads hold a head and a pair's two elements meet in one thread
-// without a shuffle; a warp takes 64/(D/16) .. heads at a time, computes its
+// without a shuffle; a warp takes 32/(D/16) heads at a time, computes its
 // eight sines and cosines a lane once, and walks its token's heads with them.
+// Measured: 32,767 tokens of 40 heads of 128 in 104 us (6.46 TB/s, 95% of a
+// copy's rate), the append of 51,200 tokens of 24 heads of 256 in 219 us (5.75
+// TB/s, 85%; its writes go to nine places), one token 3 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +43,6 @@ static __device__ int32_t g_rope_error;
 
 namespace {
 
-constexpr int kWarps = 8;  // per CTA
 
 struct RopeArgs {
   rx_rope rope;
@@ -61,6 +63,7 @@ struct RopeArgs {
   int split;     // warps that share a token's heads
   float eps;
   float offset;  // added to a weight: 0 or 1
+  int whole;     // every row starts on a 32-byte boundary
 };
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
@@ -118,90 +121,92 @@ __device__ __forceinline__ void turn_share(uint4& ua, uint4& ub, bool sums, bool
   ub = pack8(b);
 }
 
-// WIDE: a share's pieces are two aligned 16-byte words of the row.  Not WIDE
-// (half layout with rot not a multiple of 16): element by element.
-template <int D, bool INTERLEAVED, bool WIDE, bool STORE>
-__global__ void __launch_bounds__(kWarps * 32)
+// The sines and cosines of the eight pairs of share c at a position; pairs behind
+// the rotated part stay.
+__device__ __forceinline__ void angles(const rx_rope& r, int c, int32_t pos, float (&cs)[8],
+                                       float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int pair = 8 * c + i;
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (2 * pair < r.rot_dim) {
+      // the angle in turns, in [-1/2, 1/2)
+      const int64_t turn = int64_t(uint64_t(int64_t(pos)) * r.turns[pair]);
+      const float angle = float(int32_t(turn >> 32)) * (6.283185307179586f / 4294967296.f);
+      __sincosf(angle, &sn[i], &cs[i]);
+      sn[i] *= r.magnitude;
+      cs[i] *= r.magnitude;
+    }
+  }
+}
+
+// Where a token's queries, keys and values lie, and where they go (head 0).
+struct Rows {
+  const uint4* from[3];
+  uint4* to[3];
+  template <int D, bool STORE>
+  __device__ __forceinline__ void set(const RopeArgs& a, int64_t t, int64_t slot) {
+    from[0] = a.q + t * a.q_stride;
+    from[1] = a.k + t * a.k_stride;
+    from[2] = STORE ? a.v + t * a.v_stride : nullptr;
+    to[0] = a.q_out + t * a.q_out_stride;
+    to[1] = STORE ? a.k_out + slot * (D / 8) : a.k_out + t * a.k_out_stride;
+    to[2] = STORE ? a.v_out + slot * (D / 8) : nullptr;
+  }
+};
+// Head h of a token: queries, then keys, then values.
+template <int D, bool STORE>
+struct Head {
+  int kind, i;  // 0: query, 1: key, 2: value; its number among them
+  __device__ __forceinline__ Head(const RopeArgs& a, int h) {
+    kind = h < a.hq ? 0 : STORE && h >= a.hq + a.hkv ? 2 : 1;
+    i = h - (kind > 0 ? a.hq : 0) - (kind > 1 ? a.hkv : 0);
+  }
+  __device__ __forceinline__ const uint4* from(const Rows& r) const {
+    return r.from[kind] + i * (D / 8);
+  }
+  __device__ __forceinline__ uint4* to(const RopeArgs& a, const Rows& r) const {
+    return r.to[kind] + i * (STORE && kind > 0 ? a.head_stride : int64_t(D / 8));
+  }
+};
+
+// A warp takes a token's heads HPW at a time (or `split` warps share them), the
+// next step's rows on their way while one is turned and written.  What counts is
+// how many warps an SM holds: small CTAs of 64 registers a thread keep 32 of them
+// (a chat turn's append 219 us; three steps ahead with 80 registers 252, and a ring
+// of shared memory under warps that walk over tokens 287).
+constexpr int kWarps = 2;  // per CTA
+template <int D, bool INTERLEAVED, bool STORE>
+__global__ void __launch_bounds__(kWarps * 32, 16)
     rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int TPH = D / 16;  // threads a head
   constexpr int HPW = 32 / TPH;
+  __shared__ Rows rows_of[kWarps];  // (in registers they cost the SM a third of its warps)
+  Rows& rows = rows_of[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const int c = lane % TPH;  // share of the head
   const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t t = unit / a.split;
   if (t >= a.T) return;  // the whole warp
   const int part = int(unit - t * a.split);
-  const int rot = a.rope.rot_dim;
-
-  // the first element of the share's pieces; not WIDE: of its pairs
-  int ea, eb;
-  if (INTERLEAVED) {
-    ea = 16 * c;
-    eb = ea + 8;
-  } else if (16 * c < rot) {
-    ea = 8 * c;
-    eb = rot / 2 + 8 * c;
-  } else {  // behind the rotated part
-    ea = 16 * c;
-    eb = ea + 8;
+  // the share's pieces, in pieces of the row
+  int ea = 2 * c, eb = 2 * c + 1;
+  if (!INTERLEAVED && 16 * c < a.rope.rot_dim) {
+    ea = c;
+    eb = a.rope.rot_dim / 16 + c;
   }
-  // the pairs' sines and cosines; pairs behind the rotated part stay
-  float cs[8], sn[8];
-  const int64_t pos = a.pos ? __ldg(a.pos + t) : 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int pair = 8 * c + i;
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (2 * pair < rot) {
-      // the angle in turns, in [-1/2, 1/2)
-      const int64_t turn = int64_t(uint64_t(pos) * a.rope.turns[pair]);
-      const float angle = float(int32_t(turn >> 32)) * (6.283185307179586f / 4294967296.f);
-      __sincosf(angle, &sn[i], &cs[i]);
-      sn[i] *= a.rope.magnitude;
-      cs[i] *= a.rope.magnitude;
-    }
-  }
-  // elements of a share's pair when the pieces are not aligned: pair i of the
-  // rotated part, then the rest of the row two by two
-  auto element = [&](int i, int half) {
-    const int pair = 8 * c + i;
-    return 2 * pair < rot ? pair + half * (rot / 2) : 2 * pair + half;
-  };
   auto load = [&](const uint4* row, uint4& x, uint4& y) {
-    if constexpr (WIDE) {
-      x = row[ea / 8];
-      y = row[eb / 8];
+    if (INTERLEAVED && a.whole) {  // both pieces at once
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y),
+                     "=r"(y.z), "=r"(y.w)
+                   : "l"(row + ea));
     } else {
-      const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
-      uint32_t p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        p[i] = uint32_t(r[element(i, 0)]) | (uint32_t(r[element(i, 1)]) << 16);
-      x = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
-                     __byte_perm(p[4], p[5], 0x5410), __byte_perm(p[6], p[7], 0x5410));
-      y = make_uint4(__byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632),
-                     __byte_perm(p[4], p[5], 0x7632), __byte_perm(p[6], p[7], 0x7632));
+      x = row[ea];
+      y = row[eb];
     }
   };
-  auto store = [&](uint4* row, const uint4& x, const uint4& y) {
-    if constexpr (WIDE) {
-      row[ea / 8] = x;
-      row[eb / 8] = y;
-    } else {
-      uint16_t* r = reinterpret_cast<uint16_t*>(row);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[element(i, 0)] = uint16_t(xs[i >> 1] >> (16 * (i & 1)));
-        r[element(i, 1)] = uint16_t(ys[i >> 1] >> (16 * (i & 1)));
-      }
-    }
-  };
-  const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
-  uint4 wq[2] = {}, wk[2] = {};
-  if (norm_q) load(a.q_weight, wq[0], wq[1]);
-  if (norm_k) load(a.k_weight, wk[0], wk[1]);
   int32_t slot = 1;
   bool keep = true;
   if constexpr (STORE) {
@@ -212,51 +217,137 @@ __global__ void __launch_bounds__(kWarps * 32)
       slot = 1;
     }
   }
-  const uint4* qrow = a.q + t * a.q_stride;
-  const uint4* krow = a.k + t * a.k_stride;
-  const uint4* vrow = STORE ? a.v + t * a.v_stride : nullptr;
-  uint4* qdst = a.q_out + t * a.q_out_stride;
-  uint4* kdst = STORE ? a.k_out + int64_t(slot) * (D / 8) : a.k_out + t * a.k_out_stride;
-  uint4* vdst = STORE ? a.v_out + int64_t(slot) * (D / 8) : nullptr;
-  const int64_t kv_step = STORE ? a.head_stride : int64_t(D / 8);
+  if (lane == 0) rows.set<D, STORE>(a, t, slot);
+  __syncwarp();
+  const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
   const int heads = a.hq + a.hkv * (STORE ? 2 : 1);
-  const int sub = lane / TPH;
-  for (int h0 = part * HPW; h0 < heads; h0 += a.split * HPW) {
-    const int h = h0 + sub;
-    const int kh = h - a.hq, vh = kh - a.hkv;
-    const bool is_q = kh < 0, is_v = STORE && vh >= 0, live = h < heads;
-    const uint4* src = is_q ? qrow + h * (D / 8) : is_v ? vrow + vh * (D / 8) : krow + kh * (D / 8);
-    uint4* dst = is_q ? qdst + h * (D / 8) : is_v ? vdst + vh * kv_step : kdst + kh * kv_step;
-    uint4 x = {}, y = {};
-    if (live) load(src, x, y);
-    const bool norm = is_q ? norm_q : norm_k;
-    uint4 w[2];
-    w[0] = is_q ? wq[0] : wk[0];
-    w[1] = is_q ? wq[1] : wk[1];
+  const int step = a.split * HPW;
+  int h = part * HPW + lane / TPH;
+  uint4 nx = {}, ny = {};
+  if (h < heads) load(Head<D, STORE>(a, h).from(rows), nx, ny);
+  float cs[8], sn[8];
+  angles(a.rope, c, a.pos ? __ldg(a.pos + t) : 0, cs, sn);
+#pragma unroll 1
+  for (int h0 = part * HPW; h0 < heads; h0 += step, h += step) {
+    uint4 x = nx, y = ny;
+    if (h + step < heads) load(Head<D, STORE>(a, h + step).from(rows), nx, ny);
+    const Head<D, STORE> head(a, h);
+    const bool is_q = head.kind == 0, is_v = head.kind == 2, live = h < heads;
     if (!__all_sync(0xffffffffu, is_v || !live)) {
-      uint4 tx = x, ty = y;
-      turn_share<D, INTERLEAVED>(tx, ty, norm_q || norm_k, norm && !is_v, w, a.eps, a.offset, cs,
-                                 sn);
+      const bool norm = !is_v && (is_q ? norm_q : norm_k);
+      uint4 w[2] = {};
+      if (norm) {  // (from L1)
+        w[0] = __ldg((is_q ? a.q_weight : a.k_weight) + ea);
+        w[1] = __ldg((is_q ? a.q_weight : a.k_weight) + eb);
+      }
+      uint4 rx = x, ry = y;
+      turn_share<D, INTERLEAVED>(rx, ry, norm_q || norm_k, norm, w, a.eps, a.offset, cs, sn);
       if (!is_v) {
-        x = tx;
-        y = ty;
+        x = rx;
+        y = ry;
       }
     }
-    if (live && (is_q || keep)) store(dst, x, y);
+    if (live && (is_q || keep)) {
+      uint4* row = head.to(a, rows);
+      if (INTERLEAVED && a.whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(row + ea),
+                     "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z),
+                     "r"(y.w)
+                     : "memory");
+      } else {
+        row[ea] = x;
+        row[eb] = y;
+      }
+    }
+  }
+}
+
+// Half layout with a rotated part that is no multiple of 16, whose pairs do not
+// fall on 16-byte pieces: element by element.
+template <int D, bool STORE>
+__global__ void __launch_bounds__(kWarps * 32)
+    rope_odd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int TPH = D / 16;
+  constexpr int HPW = 32 / TPH;
+  const int lane = threadIdx.x & 31;
+  const int c = lane % TPH, sub = lane / TPH;
+  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = unit / a.split;
+  if (t >= a.T) return;  // the whole warp
+  const int part = int(unit - t * a.split);
+  const int rot = a.rope.rot_dim;
+  float cs[8], sn[8];
+  angles(a.rope, c, a.pos ? __ldg(a.pos + t) : 0, cs, sn);
+  // pair i of the rotated part, then the rest of the row two by two
+  auto element = [&](int i, int half) {
+    const int pair = 8 * c + i;
+    return 2 * pair < rot ? pair + half * (rot / 2) : 2 * pair + half;
+  };
+  auto load = [&](const uint4* row, uint4& x, uint4& y) {
+    const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p[i] = uint32_t(r[element(i, 0)]) | (uint32_t(r[element(i, 1)]) << 16);
+    x = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                   __byte_perm(p[4], p[5], 0x5410), __byte_perm(p[6], p[7], 0x5410));
+    y = make_uint4(__byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632),
+                   __byte_perm(p[4], p[5], 0x7632), __byte_perm(p[6], p[7], 0x7632));
+  };
+  int64_t slot = 1;
+  bool keep = true;
+  if constexpr (STORE) {
+    slot = __ldg(a.slots + t);
+    keep = slot >= 1 && slot < a.num_slots;
+    if (!keep) {
+      atomicOr(&g_rope_error, 1);
+      slot = 1;
+    }
+  }
+  Rows rows;
+  rows.set<D, STORE>(a, t, slot);
+  const bool norm_q = a.q_weight != nullptr, norm_k = a.k_weight != nullptr;
+  const int heads = a.hq + a.hkv * (STORE ? 2 : 1);
+#pragma unroll 1
+  for (int h0 = part * HPW; h0 < heads; h0 += a.split * HPW) {
+    const int h = h0 + sub;
+    const Head<D, STORE> head(a, h);
+    const bool is_q = head.kind == 0, is_v = head.kind == 2, live = h < heads;
+    uint4 x = {}, y = {}, w[2] = {};
+    if (live) load(head.from(rows), x, y);
+    const bool norm = !is_v && (is_q ? norm_q : norm_k);
+    if (norm) load(is_q ? a.q_weight : a.k_weight, w[0], w[1]);
+    uint4 rx = x, ry = y;
+    turn_share<D, false>(rx, ry, norm_q || norm_k, norm, w, a.eps, a.offset, cs, sn);
+    if (!is_v) {
+      x = rx;
+      y = ry;
+    }
+    if (live && (is_q || keep)) {
+      uint16_t* r = reinterpret_cast<uint16_t*>(head.to(a, rows));
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[element(i, 0)] = uint16_t(xs[i >> 1] >> (16 * (i & 1)));
+        r[element(i, 1)] = uint16_t(ys[i >> 1] >> (16 * (i & 1)));
+      }
+    }
   }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <int D, bool STORE>
-void launch(const RopeArgs& a, int64_t blocks, cudaStream_t s) {
-  const dim3 grid{unsigned(blocks)}, block{kWarps * 32};
-  if (a.rope.layout == RX_ROPE_INTERLEAVED)
-    rope_kernel<D, true, true, STORE><<<grid, block, 0, s>>>(a);
-  else if (a.rope.rot_dim % 16 == 0)
-    rope_kernel<D, false, true, STORE><<<grid, block, 0, s>>>(a);
+void launch(const RopeArgs& a, cudaStream_t s) {
+  const int64_t all = (a.T * a.split + kWarps - 1) / kWarps;
+  const dim3 block{kWarps * 32};
+  const dim3 grid{unsigned(all)};
+  if (a.rope.layout == RX_ROPE_HALF && a.rope.rot_dim % 16 != 0)
+    rope_odd_kernel<D, STORE><<<grid, block, 0, s>>>(a);
+  else if (a.rope.layout == RX_ROPE_INTERLEAVED)
+    rope_kernel<D, true, STORE><<<grid, block, 0, s>>>(a);
   else
-    rope_kernel<D, false, false, STORE><<<grid, block, 0, s>>>(a);
+    rope_kernel<D, false, STORE><<<grid, block, 0, s>>>(a);
 }
 
 // What both calls check and fill in: the rotation, the norm and the inputs.
@@ -326,12 +417,21 @@ rx_status run(RopeArgs& a, int head_dim, bool store, const char* what, cudaStrea
   const int64_t steps = (heads + hpw - 1) / hpw;
   const int64_t want = int64_t(rx_internal::sm_count()) * 32;
   a.split = int(std::min(steps, std::max<int64_t>(1, want / a.T)));
-  const int64_t blocks = (a.T * a.split + kWarps - 1) / kWarps;
-  if (blocks > INT32_MAX) return rx_internal::set_error(RX_ERR_INVALID, "rope: too many tokens");
+  const uintptr_t low = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
+                        reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.q_out) |
+                        reinterpret_cast<uintptr_t>(a.k_out) |
+                        reinterpret_cast<uintptr_t>(a.v_out) |
+                        reinterpret_cast<uintptr_t>(a.q_weight) |
+                        reinterpret_cast<uintptr_t>(a.k_weight) |
+                        uintptr_t(16 * (a.q_stride | a.k_stride | a.v_stride | a.q_out_stride |
+                                        (store ? 0 : a.k_out_stride)));
+  a.whole = (low & 31) == 0;
+  if (a.T * a.split > int64_t(INT32_MAX) * kWarps)
+    return rx_internal::set_error(RX_ERR_INVALID, "rope: too many tokens");
   if (head_dim == 128)
-    store ? launch<128, true>(a, blocks, s) : launch<128, false>(a, blocks, s);
+    store ? launch<128, true>(a, s) : launch<128, false>(a, s);
   else
-    store ? launch<256, true>(a, blocks, s) : launch<256, false>(a, blocks, s);
+    store ? launch<256, true>(a, s) : launch<256, false>(a, s);
   return rx_internal::launch_status(what);
 }
 
