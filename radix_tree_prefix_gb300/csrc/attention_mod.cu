@@ -37,10 +37,8 @@
 namespace {
 
 constexpr int kGroup = 16;  // keys of a small TMA box
-// Softmax warpgroups: three where 128 registers a thread are enough, two beside
-// decode's warp role.
-constexpr int kExtendGroups = 3, kExtendThreads = 128 * (kExtendGroups + 1);
-constexpr int kDecodeGroups = 2, kDecodeThreads = 128 * (kDecodeGroups + 1);
+// Softmax warpgroups of a tile.
+constexpr int NW = 3, kTileThreads = 128 * (NW + 1);
 // A row's reference is raised when a score exceeds it by more than this (log2
 // units).  Raising stops the chain between the warpgroups until the product
 // before it has completed, so it is made rare; 2^32 times the weights' usual size
@@ -360,13 +358,13 @@ __device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int sp
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
-template <int D, int NW, bool DECODE, bool CAP, bool SLOPES>
+template <int D, bool DECODE, bool CAP, bool SLOPES>
 __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
                                           int first, int step, int total) {
   using Lo = Layout4<D>;
   constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
-  static_assert(NW <= 3, "reference barriers");
+  static_assert(NW <= 3, "reference barriers and sums");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
   const uint32_t base = rxk::smem_addr(gbase);
   if (base & 1023u) {  // uniform over the CTA: nothing initialised yet
@@ -419,7 +417,6 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if constexpr (DECODE) rxk::griddep_wait();
 
   // the k-th row tile's descriptor, as the K loader wrote it
   auto read_desc = [&](int k, TileDesc& t) -> bool {
@@ -892,52 +889,54 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 // Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
 // attention_tc.cu.
 template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kExtendThreads, 1)
+__global__ void __launch_bounds__(kTileThreads, 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  row_tiles<D, kExtendGroups, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x),
-                                                  int(gridDim.x),
-                                                  a.num_tiles * (a.hq / a.group));
+  row_tiles<D, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), int(gridDim.x),
+                                   a.num_tiles * (a.hq / a.group));
 }
 
-// Decode: tiles of the plan's large items, then warp-role units of its small ones
-// from a shared counter, as in attention_tc.cu's decode kernel (nothing is read
-// before the kernels ahead of it are done).
-template <int D>
-struct FusedMod {
-  static constexpr int PIPE_BYTES = kPipeWarps * PipeCfg<D>::WARP_BYTES + 1024;
-  static constexpr int TILE_BYTES = Layout4<D>::BYTES;
-  static constexpr int SMEM = TILE_BYTES > PIPE_BYTES ? TILE_BYTES : PIPE_BYTES;
-  static_assert(SMEM <= 227 * 1024, "a decode CTA fits in shared memory");
-};
-
+// Decode: the plan's large items as tiles, a CTA each, and beside them the units
+// of its small ones on whatever SMs are free (two kernels: the softmax of the
+// tiles has three warpgroups, and a unit more registers than those leave).
 template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kDecodeThreads, 1)
-    decode_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    decode_mod_tile_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  rxk::griddep_launch_dependents();
+  row_tiles<D, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas, a.n_tc_ctas);
+}
+
+// A warp a unit (an item and a KV head): unit blockIdx.x + gridDim.x * warp when
+// every unit has a warp, else from a counter, heaviest first.  n_tc_ctas > 0: the
+// tiles' kernel runs beside this one, which ends only after it, so that the merge
+// behind this one finds both done.
+template <int D, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(kPipeWarps * 32, 1)
+    decode_mod_stream_kernel(const __grid_constant__ TcArgs a) {
   using Cfg = PipeCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  const int cta = int(blockIdx.x) - a.n_warp_first;
-  if (cta >= 0 && cta < a.n_tc_ctas)
-    row_tiles<D, kDecodeGroups, true, CAP, SLOPES>(a, maps, smem_raw, cta, a.n_tc_ctas,
-                                                   a.n_tc_ctas);
-  if (threadIdx.x >= kPipeWarps * 32) return;  // the warp role uses the first six warps
-  rxk::griddep_wait();
-  const uint32_t raw = rxk::smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
   const int warp = int(threadIdx.x >> 5);
   const int lane = int(threadIdx.x & 31);
-  const uint32_t ring = base + uint32_t(warp * Cfg::WARP_BYTES);
-  int32_t* slot_buf = reinterpret_cast<int32_t*>(smem_raw + (base - raw) + warp * Cfg::WARP_BYTES +
+  const uint32_t ring = rxk::smem_addr(smem_raw) + uint32_t(warp * Cfg::WARP_BYTES);
+  int32_t* slot_buf = reinterpret_cast<int32_t*>(smem_raw + warp * Cfg::WARP_BYTES +
                                                  Cfg::STAGES * Cfg::STAGE_BYTES);
   uint32_t gstep = 0;
   NextUnit cur, nxt;
   cur.stage = 0;
+  if (!a.unit_counter) {
+    cur.idx = int(blockIdx.x) + int(gridDim.x) * warp;
+    cur.stage = 1;  // (it has its index)
+  }
   while (cur.stage < 3) next_unit_step<SLOPES>(a, cur);
   while (cur.idx < a.n_small_units) {
     nxt.stage = 0;
-    const int rows = cur.word(6);
-    if (rows <= 8) {
+    if (!a.unit_counter) {
+      nxt.idx = a.n_small_units;
+      nxt.stage = 3;
+    }
+    if (cur.word(6) <= 8) {
       pipe_unit<1, D, true, CAP, SLOPES>(a, ring, slot_buf, gstep, cur, nxt);
     } else if constexpr (D == 128) {
       pipe_unit<2, D, true, CAP, SLOPES>(a, ring, slot_buf, gstep, cur, nxt);
@@ -947,6 +946,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     while (nxt.stage < 3) next_unit_step<SLOPES>(a, nxt);
     cur = nxt;
   }
+  if (a.n_tc_ctas > 0) rxk::griddep_wait();
 }
 
 bool make_maps(Maps4* m, const rx_pool_desc* pool, int BN) {
@@ -1017,22 +1017,47 @@ rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   if (!make_maps(&maps, pool, Lo::BS))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()));
-  extend_mod_kernel<D, CAP, SLOPES><<<grid, kExtendThreads, Lo::BYTES, s>>>(a, maps);
+  extend_mod_kernel<D, CAP, SLOPES><<<grid, kTileThreads, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 
 template <int D, bool CAP, bool SLOPES>
 rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
-  static std::atomic<bool> configured[kMaxDevices];
-  const rx_status cs =
-      ensure_smem(configured, decode_mod_kernel<D, CAP, SLOPES>, FusedMod<D>::SMEM);
-  if (cs != RX_OK) return cs;
-  Maps4 maps;
-  if (!make_maps(&maps, pool, Layout4<D>::BS))
-    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
-  decode_mod_kernel<D, CAP, SLOPES><<<ctas, kDecodeThreads, FusedMod<D>::SMEM, s>>>(a, maps);
-  return rx_internal::launch_status("rx_decode_attention_mod");
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.stream = s;
+  if (a.n_tc_ctas > 0) {
+    static std::atomic<bool> configured[kMaxDevices];
+    const rx_status cs = ensure_smem(configured, decode_mod_tile_kernel<D, CAP, SLOPES>,
+                                     Layout4<D>::BYTES);
+    if (cs != RX_OK) return cs;
+    Maps4 maps;
+    if (!make_maps(&maps, pool, Layout4<D>::BS))
+      return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+    decode_mod_tile_kernel<D, CAP, SLOPES>
+        <<<unsigned(a.n_tc_ctas), kTileThreads, Layout4<D>::BYTES, s>>>(a, maps);
+    const rx_status st = rx_internal::launch_status("rx_decode_attention_mod: tiles");
+    if (st != RX_OK) return st;
+  }
+  if (ctas > 0) {
+    constexpr int bytes = kPipeWarps * PipeCfg<D>::WARP_BYTES;
+    static_assert(bytes <= 227 * 1024 && PipeCfg<D>::WARP_BYTES % 16 == 0, "shared memory");
+    static std::atomic<bool> configured[kMaxDevices];
+    const rx_status cs =
+        ensure_smem(configured, decode_mod_stream_kernel<D, CAP, SLOPES>, bytes);
+    if (cs != RX_OK) return cs;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPipeWarps * 32);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.numAttrs = a.n_tc_ctas > 0 ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, decode_mod_stream_kernel<D, CAP, SLOPES>, a);
+    return rx_internal::launch_status("rx_decode_attention_mod: streams");
+  }
+  return RX_OK;
 }
 
 // By modification: none (masks), cap, slopes, both.
@@ -1169,18 +1194,11 @@ extern "C" rx_status rx_decode_attention_mod(
                mod ? *mod : none);
     const int64_t hkv = pool->num_kv_heads;
     const int64_t small_units = n_small * hkv, tc_ctas = info->n_work_tc * hkv;
-    // CTAs as in rx_decode_attention: the tiles, and CTAs for the warp-role units
-    // behind them when all fit in one wave, else some before them
+    // as many stream CTAs as SMs, or as units: with no more units than warps every
+    // unit has its own, on as many SMs as there are; more are taken from a counter
     const int64_t sms = rx_internal::sm_count();
-    const int64_t unit_ctas = (small_units + kPipeWarps - 1) / kPipeWarps;
-    int64_t warp_first = 0, ctas = tc_ctas;
-    if (tc_ctas + unit_ctas <= sms)
-      ctas = tc_ctas + unit_ctas;
-    else if (tc_ctas >= sms)
-      warp_first = std::min<int64_t>(unit_ctas, (sms + 3) / 4);
-    else
-      ctas = sms;
-    ctas += warp_first;
+    const int64_t ctas = std::min(small_units, sms);
+    const bool counted = small_units > sms * kPipeWarps || (tc_ctas > 0 && small_units > 0);
     a.work_small = d_plan + info->off_work;
     a.work = a.work_small + n_small * RX_WORK_WORDS;
     a.members = d_plan + info->off_members;
@@ -1188,11 +1206,12 @@ extern "C" rx_status rx_decode_attention_mod(
     a.ws_lse = ws_lse;
     a.n_small_units = int(small_units);
     a.n_tc_ctas = int(tc_ctas);
-    a.n_warp_first = int(warp_first);
-    a.unit_counter = counter;
     a.step = step;
-    if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
-      return rx_internal::launch_status("rx_decode_attention_mod: counter reset");
+    if (counted) {
+      a.unit_counter = counter;
+      if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
+        return rx_internal::launch_status("rx_decode_attention_mod: counter reset");
+    }
     st = pick(D, mod ? *mod : none, kDecode128, kDecode256, a, pool, unsigned(ctas), s);
     if (st != RX_OK) return st;
   }

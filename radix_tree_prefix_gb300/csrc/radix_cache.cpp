@@ -964,6 +964,8 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
     return members_k * G <= small_rows ? int64_t(1) : (members_k + warp_block - 1) / warp_block;
   };
   // chunk of the warp-role items: the longest that keeps enough units
+  const int64_t units_per_warp = window > 0 ? rx_internal::kWindowUnitsPerWarp
+                                            : rx_internal::kDecodeUnitsPerWarp;
   int64_t small_chunk = rx_internal::kDecodeSmallChunkMin;
   for (int64_t c = rx_internal::kDecodeSmallChunkMax; c > rx_internal::kDecodeSmallChunkMin;
        c /= 2) {
@@ -971,7 +973,7 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
     for (const Seg& s : segs)
       if (is_warp_seg(int64_t(s.members.size())))
         units += (s.ke - s.kb + c - 1) / c * warp_blocks(int64_t(s.members.size())) * num_kv_heads;
-    if (units >= int64_t(rx_internal::kDecodeWarpSlots) * rx_internal::kDecodeUnitsPerWarp) {
+    if (units >= int64_t(rx_internal::kDecodeWarpSlots) * units_per_warp) {
       small_chunk = c;
       break;
     }

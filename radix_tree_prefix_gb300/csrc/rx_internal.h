@@ -38,6 +38,10 @@ constexpr int kDecodeSmallChunkMin = 128;
 constexpr int kDecodeSmallChunkMax = 1024;
 constexpr int kDecodeWarpSlots = 152 * 6;
 constexpr int kDecodeUnitsPerWarp = 2;
+// A window makes contexts short and alike, so that two units a warp end as two
+// rounds and a rest (a chat step of 256 in a window of 1,024: chunks of 512 keys
+// 168 us, 256 154, 128 163).
+constexpr int kWindowUnitsPerWarp = 3;
 
 // Extend: query rows (query tokens x group heads) per CTA tile (the tcgen05
 // tile kernel owns 128 TMEM lanes = 128 rows).

@@ -841,22 +841,44 @@ def kv8_decode_attention(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, 
 
 
 # ---------------------------------- norm, rotation and modified scores
-def _cuda_args(what, dev, stream, *tensors):
-    """Checks the (name, tensor, dtype, elements) of a call: contiguous, of the
-    type, at least the elements, all on `dev` (a CUDA device index), which
-    must be the current device.  Returns the stream's handle."""
-    import torch
+class _Torch:
+    """What the calls below use of torch, looked up once: a small call's time on
+    the GPU is a few microseconds, and its arguments' checks take as long."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.bf16, self.f32 = torch.int32, torch.bfloat16, torch.float32
+        self.device = torch._C._cuda_getDevice
+        self.stream = torch._C._cuda_getCurrentRawStream
+
+
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _flat(what, name, t, dtype, n, dev):
+    """The pointer of a contiguous tensor of the type, with at least n elements,
+    on cuda:dev."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous {dtype} tensor of at least {n} "
+                         f"elements on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _current(what, tt, dev, stream):
+    """The handle of the call's stream; dev must be the current device."""
     if dev < 0:
         raise ValueError(f"{what}: the tensors are not on a GPU")
-    for name, t, dtype, n in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or \
-                not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be a contiguous {dtype} tensor of at least {n} "
-                             f"elements on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if torch.cuda.current_device() != dev:
+    if tt.device() != dev:
         raise ValueError(f"{what}: cuda:{dev} is not the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return tt.stream(dev)
     if stream.device_index != dev:
         raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     return stream.cuda_stream
@@ -887,48 +909,51 @@ def head_norm(q_weight, k_weight, eps, plus_one=False):
                  None if k_weight is None else k_weight.data_ptr(), float(eps),
                  1 if plus_one else 0)
     n.tensors = tuple(w for w in (q_weight, k_weight) if w is not None)
+    if len({(w.numel(), w.get_device()) for w in n.tensors}) > 1:
+        raise ValueError("head_norm: the weights have different sizes or lie on different devices")
+    n.dim = n.tensors[0].numel() if n.tensors else 0
+    n.device = n.tensors[0].get_device() if n.tensors else -1
     return n
 
 
-def _heads(what, name, t, T, d, dev):
+def _heads(what, name, t, T, H, d, dev, bf16):
     """Checks bf16 [T, H, d] with its heads side by side; (pointer, token
-    stride, H)."""
-    import torch
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or \
-            t.get_device() != dev or (t.numel() and (t.stride(2) != 1 or (
-                t.shape[1] > 1 and t.stride(1) != d))):
-        raise ValueError(f"{what}: {name} must be a bfloat16 tensor [{T}, H, {d}] on cuda:{dev} "
+    stride)."""
+    st = t.stride()
+    if t.dtype is not bf16 or t.shape != (T, H, d) or t.get_device() != dev or (
+            st[1:] != (d, 1) and t.numel() and (st[2] != 1 or (H > 1 and st[1] != d))):
+        raise ValueError(f"{what}: {name} must be a bfloat16 tensor [{T}, {H}, {d}] on cuda:{dev} "
                          f"whose heads lie side by side, got {t.dtype} {tuple(t.shape)} of strides "
-                         f"{t.stride()} on {t.device}")
-    # (one token's stride is free)
-    return t.data_ptr(), t.stride(0) if T > 1 else t.shape[1] * d, t.shape[1]
+                         f"{st} on {t.device}")
+    return t.data_ptr(), st[0] if T > 1 else H * d  # (a single token's stride is free)
 
 
 def _norm_args(what, norm, d, dev):
-    if norm is not None:
-        for w in norm.tensors:
-            if w.numel() != d or w.get_device() != dev:
-                raise ValueError(f"{what}: the norm's weights must have {d} elements on cuda:{dev}")
-    return None if norm is None else C.byref(norm)
+    if norm is None:
+        return None
+    if norm.tensors and (norm.dim != d or norm.device != dev):
+        raise ValueError(f"{what}: the norm's weights must have {d} elements on cuda:{dev}")
+    return C.byref(norm)
 
 
 def qk_rope(rope, d_positions, d_q, d_k, d_q_out, d_k_out, norm=None, stream=None):
     """rx_qk_rope: bf16 queries [T, Hq, d] and keys [T, Hkv, d] (views of one
     projection, if need be) normalised and rotated into the outputs, which may
     be the inputs."""
-    import torch
-    T, _, d = d_q.shape
-    dev = d_q.get_device()
-    s = _cuda_args("qk_rope", dev, stream, ("d_positions", d_positions, torch.int32, T))
-    q, qs, hq = _heads("qk_rope", "d_q", d_q, T, d, dev)
-    k, ks, hkv = _heads("qk_rope", "d_k", d_k, T, d, dev)
-    qo, qos, hqo = _heads("qk_rope", "d_q_out", d_q_out, T, d, dev)
-    ko, kos, hko = _heads("qk_rope", "d_k_out", d_k_out, T, d, dev)
-    if (hq, hkv) != (hqo, hko):
-        raise ValueError("qk_rope: the outputs have other head counts than the inputs")
-    _check(_lib.rx_qk_rope(None if rope is None else C.byref(rope),
-                           _norm_args("qk_rope", norm, d, dev), d, d_positions.data_ptr(), T, q,
-                           qs, hq, k, ks, hkv, qo, qos, ko, kos, s))
+    tt = _torch or _t()
+    T, hq, d = d_q.shape
+    hkv, dev, bf16 = d_k.shape[1], d_q.get_device(), tt.bf16
+    s = _current("qk_rope", tt, dev, stream)
+    pos = _flat("qk_rope", "d_positions", d_positions, tt.i32, T, dev)
+    q, qs = _heads("qk_rope", "d_q", d_q, T, hq, d, dev, bf16)
+    k, ks = _heads("qk_rope", "d_k", d_k, T, hkv, d, dev, bf16)
+    qo, qos = _heads("qk_rope", "d_q_out", d_q_out, T, hq, d, dev, bf16)
+    ko, kos = _heads("qk_rope", "d_k_out", d_k_out, T, hkv, d, dev, bf16)
+    st = _lib.rx_qk_rope(None if rope is None else C.byref(rope),
+                         _norm_args("qk_rope", norm, d, dev), d, pos, T, q, qs, hq, k, ks, hkv, qo,
+                         qos, ko, kos, s)
+    if st:
+        _check(st)
 
 
 def qkv_store(pool, layer, rope, d_positions, d_slots, d_q, d_k, d_v, d_q_out, norm=None,
@@ -936,24 +961,24 @@ def qkv_store(pool, layer, rope, d_positions, d_slots, d_q, d_k, d_v, d_q_out, n
     """rx_qkv_store: queries normalised and rotated into d_q_out, keys
     alike and values as they are into their slots of the pool.  d_q and
     d_q_out None: keys and values only."""
-    import torch
+    tt = _torch or _t()
     T, d, hkv = d_slots.numel(), pool.head_dim, pool.num_kv_heads
-    dev = d_k.get_device()
-    s = _cuda_args("qkv_store", dev, stream, ("d_positions", d_positions, torch.int32, T),
-                   ("d_slots", d_slots, torch.int32, T))
-    k, ks, hk = _heads("qkv_store", "d_k", d_k, T, d, dev)
-    v, vs, hv = _heads("qkv_store", "d_v", d_v, T, d, dev)
+    dev, bf16 = d_k.get_device(), tt.bf16
+    s = _current("qkv_store", tt, dev, stream)
+    pos = _flat("qkv_store", "d_positions", d_positions, tt.i32, T, dev)
+    slots = _flat("qkv_store", "d_slots", d_slots, tt.i32, T, dev)
+    k, ks = _heads("qkv_store", "d_k", d_k, T, hkv, d, dev, bf16)
+    v, vs = _heads("qkv_store", "d_v", d_v, T, hkv, d, dev, bf16)
     q, qs, hq, qo, qos = None, 0, 0, None, 0
     if d_q is not None:
-        q, qs, hq = _heads("qkv_store", "d_q", d_q, T, d, dev)
-        qo, qos, hqo = _heads("qkv_store", "d_q_out", d_q_out, T, d, dev)
-        if hqo != hq:
-            raise ValueError("qkv_store: d_q_out has another head count than d_q")
-    if hk != hkv or hv != hkv:
-        raise ValueError(f"qkv_store: the pool has {hkv} KV heads, d_k {hk} and d_v {hv}")
-    _check(_lib.rx_qkv_store(C.byref(pool), layer, None if rope is None else C.byref(rope),
-                             _norm_args("qkv_store", norm, d, dev), d_positions.data_ptr(),
-                             d_slots.data_ptr(), T, q, qs, hq, k, ks, v, vs, qo, qos, s))
+        hq = d_q.shape[1]
+        q, qs = _heads("qkv_store", "d_q", d_q, T, hq, d, dev, bf16)
+        qo, qos = _heads("qkv_store", "d_q_out", d_q_out, T, hq, d, dev, bf16)
+    st = _lib.rx_qkv_store(pool, layer, None if rope is None else C.byref(rope),
+                           _norm_args("qkv_store", norm, d, dev), pos, slots, T, q, qs, hq, k, ks,
+                           v, vs, qo, qos, s)
+    if st:
+        _check(st)
 
 
 class ScoreMod(rx_score_mod):
@@ -981,7 +1006,8 @@ def score_mod(softcap=0.0, window=0, slopes=None, key_begin=None, bidir_end=None
     return m
 
 
-def _mod_args(what, mod, dev, **need):
+def _mod_args(what, mod, dev, need):
+    """need: the elements that a call needs of each of the mod's tensors."""
     if mod is None:
         return None
     for field, t in mod.tensors.items():
@@ -996,43 +1022,46 @@ def extend_attention_mod(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len
                          d_tile_indptr, R, num_tiles, scale, mod, d_out, d_lse, stream=None):
     """rx_extend_attention_mod; d_out is bf16 or fp32.  A key_begin of the score
     mod has an entry for every token of d_q."""
-    import torch
-    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
-    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
+    tt = _torch or _t()
+    i32, bf16, what = tt.i32, tt.bf16, "extend_attention_mod"
+    narrow = d_out.dtype is bf16
     dev, n = d_q.get_device(), d_q.numel()
     nq = n // (hq * pool.head_dim)
-    s = _cuda_args("extend_attention_mod", dev, stream, ("d_q", d_q, bf16, 0),
-                   ("d_table", d_table, i32, 0), ("d_req_rows", d_req_rows, i32, R),
-                   ("d_prefix_len", d_prefix_len, i32, R),
-                   ("d_qo_indptr", d_qo_indptr, i32, R + 1),
-                   ("d_tile_indptr", d_tile_indptr, i32, R + 1),
-                   ("d_out", d_out, bf16 if ot else f32, n), ("d_lse", d_lse, f32, nq * hq))
-    m = _mod_args("extend_attention_mod", mod, dev, d_slopes=hq, d_key_begin=nq, d_bidir_end=R)
-    _check(_lib.rx_extend_attention_mod(
-        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
-        d_req_rows.data_ptr(), d_prefix_len.data_ptr(), d_qo_indptr.data_ptr(),
-        d_tile_indptr.data_ptr(), R, num_tiles, scale, m, d_out.data_ptr(), ot, d_lse.data_ptr(),
-        s))
+    s = _current(what, tt, dev, stream)
+    st = _lib.rx_extend_attention_mod(
+        pool, layer, _flat(what, "d_q", d_q, bf16, 0, dev), hq,
+        _flat(what, "d_table", d_table, i32, 0, dev), d_table.shape[1],
+        _flat(what, "d_req_rows", d_req_rows, i32, R, dev),
+        _flat(what, "d_prefix_len", d_prefix_len, i32, R, dev),
+        _flat(what, "d_qo_indptr", d_qo_indptr, i32, R + 1, dev),
+        _flat(what, "d_tile_indptr", d_tile_indptr, i32, R + 1, dev), R, num_tiles, scale,
+        _mod_args(what, mod, dev, {"d_slopes": hq, "d_key_begin": nq, "d_bidir_end": R}),
+        _flat(what, "d_out", d_out, bf16 if narrow else tt.f32, n, dev),
+        OUT_BF16 if narrow else OUT_F32, _flat(what, "d_lse", d_lse, tt.f32, nq * hq, dev), s)
+    if st:
+        _check(st)
 
 
 def decode_attention_mod(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, mod, d_out, d_lse,
                          d_workspace, step=0, stream=None):
     """rx_decode_attention_mod (drafts: B of them); d_out is bf16 or fp32."""
-    import torch
-    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
-    ot = OUT_BF16 if d_out.dtype is bf16 else OUT_F32
+    tt = _torch or _t()
+    i32, bf16, what = tt.i32, tt.bf16, "decode_attention_mod"
+    narrow = d_out.dtype is bf16
     dev, rows = d_q.get_device(), B * hq
-    s = _cuda_args("decode_attention_mod", dev, stream, ("d_q", d_q, bf16, rows * pool.head_dim),
-                   ("d_table", d_table, i32, 0), ("d_plan", d_plan, i32, info.plan_words),
-                   ("d_out", d_out, bf16 if ot else f32, rows * pool.head_dim),
-                   ("d_lse", d_lse, f32, rows),
-                   ("d_workspace", d_workspace, d_workspace.dtype, 0))
-    m = _mod_args("decode_attention_mod", mod, dev, d_slopes=hq, d_key_begin=B, d_ctx_len=B)
-    _check(_lib.rx_decode_attention_mod(
-        C.byref(pool), layer, d_q.data_ptr(), hq, d_table.data_ptr(), d_table.shape[1],
-        d_plan.data_ptr(), C.byref(info), B, step, scale, m, d_out.data_ptr(), ot,
-        d_lse.data_ptr(), d_workspace.data_ptr(),
-        d_workspace.numel() * d_workspace.element_size(), s))
+    n = rows * pool.head_dim
+    s = _current(what, tt, dev, stream)
+    st = _lib.rx_decode_attention_mod(
+        pool, layer, _flat(what, "d_q", d_q, bf16, n, dev), hq,
+        _flat(what, "d_table", d_table, i32, 0, dev), d_table.shape[1],
+        _flat(what, "d_plan", d_plan, i32, info.plan_words, dev), C.byref(info), B, step, scale,
+        _mod_args(what, mod, dev, {"d_slopes": hq, "d_key_begin": B, "d_ctx_len": B}),
+        _flat(what, "d_out", d_out, bf16 if narrow else tt.f32, n, dev),
+        OUT_BF16 if narrow else OUT_F32, _flat(what, "d_lse", d_lse, tt.f32, rows, dev),
+        _flat(what, "d_workspace", d_workspace, d_workspace.dtype, 0, dev),
+        d_workspace.numel() * d_workspace.element_size(), s)
+    if st:
+        _check(st)
 
 
 def decode_attention_static(pool, layer, d_q, hq, d_table, d_plan, info, B, scale, d_out, d_lse,
