@@ -37,26 +37,29 @@
 namespace {
 
 constexpr int kGroup = 16;  // keys of a small TMA box
-// Softmax warpgroups of a tile.
-constexpr int NW = 3, kTileThreads = 128 * (NW + 1);
 // A row's reference is raised when a score exceeds it by more than this (log2
 // units).  Raising stops the chain between the warpgroups until the product
 // before it has completed, so it is made rare; 2^32 times the weights' usual size
 // leaves fp32 (and bf16, of the same range) room for the sums of 2^60 keys.
 constexpr float kRaise = 32.f;
+constexpr int kPairWindow = 2048;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
 // 128: one of 64 keys reads Q's 16 columns from shared memory for half the
 // work); the softmax and O += P V go by tiles of BN = 64 keys, SUBS to a load.
 // Rings of NK and NV stages of K and V, NS of S (TMEM).
 constexpr int BN = 64;
-template <int D>
+// PAIR (head_dim 128): two CTAs an SM, each with half of its TMEM and shared memory
+// and 64 keys a load.
+template <int D, bool PAIR>
 struct Layout4 {
-  static constexpr int BS = D == 128 ? 128 : 64;
+  static constexpr int BS = D == 128 && !PAIR ? 128 : 64;
   static constexpr int SUBS = BS / BN;
   static constexpr int KV_BYTES = BS * D * 2;
-  static constexpr int NK = 3, NV = 2;
-  static constexpr int NS = D == 128 ? 3 : 4;
+  static constexpr int NW = PAIR ? 2 : 3;  // softmax warpgroups
+  static constexpr int THREADS = 128 * (NW + 1);
+  static constexpr int NK = PAIR ? 2 : 3, NV = 2;
+  static constexpr int NS = PAIR ? 2 : D == 128 ? 3 : 4;
   static constexpr int NB = NS * SUBS;  // tiles of P
   // Barriers of the reference's way from tile to tile: a warpgroup of three that
   // waits for tile g - 1 did tile g - 3 itself, so a ring of two is enough.
@@ -72,7 +75,7 @@ struct Layout4 {
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
-  static constexpr int TMEM_COLS = 512;
+  static constexpr int TMEM_COLS = PAIR ? 256 : 512;
   static_assert(O_COL + D <= TMEM_COLS, "TMEM budget");
   static_assert(BAR % 8 == 0 && DESC % 8 == 0, "alignment");
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -358,11 +361,11 @@ __device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int sp
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
-template <int D, bool DECODE, bool CAP, bool SLOPES>
+template <int D, bool PAIR, bool DECODE, bool CAP, bool SLOPES>
 __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
                                           int first, int step, int total) {
-  using Lo = Layout4<D>;
-  constexpr int NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
+  using Lo = Layout4<D, PAIR>;
+  constexpr int NW = Lo::NW, NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
   static_assert(NW <= 3, "reference barriers and sums");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
@@ -701,13 +704,13 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       tc::tc_fence_after();
       const int k0 = t.key_begin +
                      (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
-      const bool masked = k0 < lo_max || k0 + BN > lim_min;
       const bool behind = k0 + BN - 1 <= pos_min;
       // ---- first pass over the scores, 32 at a time: modified, back into TMEM, and
       // the row's maximum
       float mx = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
+        const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
         uint32_t sr[32];
         tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
         tc::tmem_ld_wait();
@@ -795,6 +798,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
+        const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
         uint32_t sr[32], pk[16];
         tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
         tc::tmem_ld_wait();
@@ -888,23 +892,23 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 
 // Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
 // attention_tc.cu.
-template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kTileThreads, 1)
+template <int D, bool PAIR, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  row_tiles<D, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), int(gridDim.x),
-                                   a.num_tiles * (a.hq / a.group));
+  row_tiles<D, PAIR, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), int(gridDim.x),
+                                         a.num_tiles * (a.hq / a.group));
 }
 
 // Decode: the plan's large items as tiles, a CTA each, and beside them the units
 // of its small ones on whatever SMs are free (two kernels: the softmax of the
 // tiles has three warpgroups, and a unit more registers than those leave).
 template <int D, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
     decode_mod_tile_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  row_tiles<D, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas, a.n_tc_ctas);
+  row_tiles<D, false, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas, a.n_tc_ctas);
 }
 
 // A warp a unit (an item and a KV head): unit blockIdx.x + gridDim.x * warp when
@@ -1006,19 +1010,31 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
   a->mul2 = make_float2(a->mul, a->mul);
 }
 
-template <int D, bool CAP, bool SLOPES>
-rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
-                            cudaStream_t s) {
-  using Lo = Layout4<D>;
+template <int D, bool PAIR, bool CAP, bool SLOPES>
+rx_status launch_extend(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
+  using Lo = Layout4<D, PAIR>;
   static std::atomic<bool> configured[kMaxDevices];
-  const rx_status cs = ensure_smem(configured, extend_mod_kernel<D, CAP, SLOPES>, Lo::BYTES);
+  const rx_status cs = ensure_smem(configured, extend_mod_kernel<D, PAIR, CAP, SLOPES>, Lo::BYTES);
   if (cs != RX_OK) return cs;
   Maps4 maps;
   if (!make_maps(&maps, pool, Lo::BS))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
-  const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()));
-  extend_mod_kernel<D, CAP, SLOPES><<<grid, kTileThreads, Lo::BYTES, s>>>(a, maps);
+  const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()) * (PAIR ? 2 : 1));
+  extend_mod_kernel<D, PAIR, CAP, SLOPES><<<grid, Lo::THREADS, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
+}
+
+template <int D, bool CAP, bool SLOPES>
+rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
+                            cudaStream_t s) {
+  // Row tiles of few keys, one after another in a CTA, are bound by the way from one
+  // to the next, which a second CTA on the SM fills (a prompt in a window of 1,024
+  // 179 us and 150, documents of 400 tokens 124 and 113); over long ranges, and under
+  // a cap, one CTA with deeper rings is faster (agent calls 380 and 399, 511 and 566).
+  if constexpr (D == 128 && !CAP)
+    if (a.key_begin || (a.window > 0 && a.window <= kPairWindow))
+      return launch_extend<D, true, CAP, SLOPES>(a, pool, ctas, s);
+  return launch_extend<D, false, CAP, SLOPES>(a, pool, ctas, s);
 }
 
 template <int D, bool CAP, bool SLOPES>
@@ -1033,13 +1049,13 @@ rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   if (a.n_tc_ctas > 0) {
     static std::atomic<bool> configured[kMaxDevices];
     const rx_status cs = ensure_smem(configured, decode_mod_tile_kernel<D, CAP, SLOPES>,
-                                     Layout4<D>::BYTES);
+                                     Layout4<D, false>::BYTES);
     if (cs != RX_OK) return cs;
     Maps4 maps;
-    if (!make_maps(&maps, pool, Layout4<D>::BS))
+    if (!make_maps(&maps, pool, Layout4<D, false>::BS))
       return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
     decode_mod_tile_kernel<D, CAP, SLOPES>
-        <<<unsigned(a.n_tc_ctas), kTileThreads, Layout4<D>::BYTES, s>>>(a, maps);
+        <<<unsigned(a.n_tc_ctas), Layout4<D, false>::THREADS, Layout4<D, false>::BYTES, s>>>(a, maps);
     const rx_status st = rx_internal::launch_status("rx_decode_attention_mod: tiles");
     if (st != RX_OK) return st;
   }
