@@ -888,7 +888,7 @@ rx_status rx_qkv_store(const rx_pool_desc* pool, int32_t layer,
  * j >= key_begin.  Each part is left out when its field is 0 or NULL.  A query
  * that sees no key gets zeros and lse = -inf. */
 typedef struct rx_score_mod {
-  float softcap;              /* > 0; 0: scores are not capped              */
+  float softcap;              /* 2^-40 to 2^40; 0: scores are not capped    */
   int32_t window;             /* keys back that a query sees, itself
                                  counted; 0: all                           */
   const float* d_slopes;      /* device fp32 [Hq]                          */
@@ -912,8 +912,8 @@ typedef struct rx_score_mod {
  * its rows sees; their V rows must be finite (a masked key weighs 0, and 0 times
  * an infinity would reach the tile's other queries), their K rows need not
  * be where they are masked.  d_ctx_len is not read.  Errors: RX_ERR_INVALID
- * as rx_extend_attention, for an unknown out_type, softcap < 0 or not finite,
- * window < 0, scale <= 0 or not finite. */
+ * as rx_extend_attention, for an unknown out_type, a softcap out of range,
+ * window < 0, a scale not in [2^-40, 2^40]. */
 rx_status rx_extend_attention_mod(
     const rx_pool_desc* pool, int32_t layer, const void* d_q,
     int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,

@@ -997,6 +997,7 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
         f = 0.f;
         if (i > 0) u = std::min(u, pow(7e-9 / fabs(double(kTanhNear[i])), 0.5 / i));
       }
+      if (fabs(c) > 1e37) u = -1.0;  // too large: no score is near
       a->cap_fold2[i] = make_float2(f, f);
     }
     a->cap_near = float(u / double(a->cap_in));
@@ -1116,11 +1117,15 @@ int32_t mod_error_flags(bool clear) {
 }  // namespace rx_internal
 
 // What both attention calls with modified scores check of them.
-static rx_status check_mod(const rx_score_mod* mod, int32_t out_type) {
+static rx_status check_mod(const rx_score_mod* mod, float scale, int32_t out_type) {
+  constexpr float kLeast = 9.094947e-13f, kMost = 1.0995116e12f;  // 2^-40, 2^40
+  if (!(scale >= kLeast && scale <= kMost))
+    return rx_internal::set_error(RX_ERR_INVALID, "attention: scale not within 2^-40 and 2^40");
   if (out_type != RX_OUT_F32 && out_type != RX_OUT_BF16)
     return rx_internal::set_error(RX_ERR_INVALID, "attention: unknown out_type");
-  if (mod && (!(mod->softcap >= 0.f) || !isfinite(mod->softcap)))
-    return rx_internal::set_error(RX_ERR_INVALID, "score mod: softcap < 0 or not finite");
+  if (mod && mod->softcap != 0.f && !(mod->softcap >= kLeast && mod->softcap <= kMost))
+    return rx_internal::set_error(RX_ERR_INVALID,
+                                  "score mod: softcap neither 0 nor within 2^-40 and 2^40");
   if (mod && mod->window < 0)
     return rx_internal::set_error(RX_ERR_INVALID, "score mod: window < 0");
   return RX_OK;
@@ -1133,7 +1138,7 @@ extern "C" rx_status rx_extend_attention_mod(
     int32_t R, int64_t num_tiles, float scale, const rx_score_mod* mod, void* d_out,
     int32_t out_type, float* d_lse, rx_stream_t stream) {
   rx_status st = rx_internal::check_pool(pool, layer);
-  if (st == RX_OK) st = check_mod(mod, out_type);
+  if (st == RX_OK) st = check_mod(mod, scale, out_type);
   if (st != RX_OK) return st;
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: Hq % Hkv != 0");
@@ -1143,8 +1148,6 @@ extern "C" rx_status rx_extend_attention_mod(
   if (!d_q || !d_req_to_token || !d_req_rows || !d_prefix_len || !d_qo_indptr ||
       !d_tile_indptr || !d_out || !d_lse || !aligned16(d_q) || !aligned16(d_out))
     return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: NULL or misaligned");
-  if (!(scale > 0.f) || !isfinite(scale))
-    return rx_internal::set_error(RX_ERR_INVALID, "rx_extend_attention_mod: scale must be above 0");
   const int D = pool->head_dim;
   const rx_score_mod none{};
   TcArgs a{};
@@ -1176,7 +1179,7 @@ extern "C" rx_status rx_decode_attention_mod(
     const rx_score_mod* mod, void* d_out, int32_t out_type, float* d_lse, void* d_workspace,
     size_t workspace_bytes, rx_stream_t stream) {
   rx_status st = rx_internal::check_pool(pool, layer);
-  if (st == RX_OK) st = check_mod(mod, out_type);
+  if (st == RX_OK) st = check_mod(mod, scale, out_type);
   if (st != RX_OK) return st;
   auto bad = [](const char* why) { return rx_internal::set_error(RX_ERR_INVALID, why); };
   if (!info || num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0 || B < 0 || step < 0)
@@ -1187,8 +1190,6 @@ extern "C" rx_status rx_decode_attention_mod(
   if (!d_q || !d_req_to_token || !d_plan || !d_out || !d_lse || !aligned16(d_q) ||
       !aligned16(d_out))
     return bad("rx_decode_attention_mod: NULL or misaligned");
-  if (!(scale > 0.f) || !isfinite(scale))
-    return bad("rx_decode_attention_mod: scale must be above 0");
   if (mod && (mod->window > 0 || mod->d_slopes) && !mod->d_ctx_len)
     return bad("rx_decode_attention_mod: a window or slopes need d_ctx_len");
   const int64_t n_small = info->n_work - info->n_work_tc;

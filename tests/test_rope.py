@@ -264,6 +264,30 @@ def test_qkv_store_equals_rotation_and_store(case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_store_with_queries_in_place(layout):
+    """Queries turned where they lie in the projection's rows, whose tokens are
+    no multiple of 32 bytes apart."""
+    import torch
+    T, hq, hkv, d = 50, 4, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    room = torch.randn((T, (hq + 2 * hkv) * d + 8), generator=g, device="cuda").to(torch.bfloat16)
+    x = room[:, 8:].unflatten(1, (hq + 2 * hkv, d))
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    before = room.clone()
+    pool = [torch.zeros((1, hkv, T + 1, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    want, tol = reference(_np(q), pos.cpu().numpy(), d, d, layout, {}, "", None, 0)
+    rx.qkv_store(rx.pool_desc(*pool), 0, rx.rope(d, layout=layout), pos, pos + 1, q, k, v, q)
+    assert rx.device_check() == 0
+    assert np.all(np.abs(_np(q) - want) <= tol)
+    rest = torch.ones_like(room, dtype=torch.bool)
+    rest[:, 8:8 + hq * d] = False
+    assert torch.equal(room[rest], before[rest])
+    assert torch.equal(pool[1][0, :, 1:].transpose(0, 1), v)
+
+
+@pytest.mark.gpu
 def test_norm_of_extreme_rows():
     """Rows of zeros (eps alone), of the smallest and of large magnitudes, and
     rows that are not finite, which stay within themselves."""

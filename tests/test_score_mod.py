@@ -53,6 +53,8 @@ def test_calls_refuse_before_any_cuda_call():
         for kw in (dict(layer=2), dict(layer=-1), dict(q=None), dict(q=X + 8), dict(hq=3),
                    dict(hq=0), dict(table=None), dict(out=None), dict(out=X + 8), dict(ot=2),
                    dict(ot=-1), dict(lse=None), dict(m=mod(softcap=-1.0)),
+                   dict(m=mod(softcap=2.0 ** -41)), dict(m=mod(softcap=2.0 ** 41)),
+                   dict(scale=2.0 ** -41), dict(scale=2.0 ** 41),
                    dict(m=mod(softcap=math.nan)), dict(m=mod(softcap=INF)),
                    dict(m=mod(window=-1)), dict(scale=0.0), dict(scale=-1.0),
                    dict(scale=math.nan), dict(scale=INF), dict(pool=rx.rx_pool_desc(X, X, 64, 2, 2, 96, 0))):
@@ -231,26 +233,33 @@ def _check(o, lse, want):
 
 
 class Extend:
-    """Requests of (prefix, suffix) tokens over shuffled runs of slots; every
-    pool row that no request's query sees holds NaN."""
+    """Requests of (prefix, suffix) tokens over shuffled runs of slots (pages:
+    each request's runs start at a multiple of `page` of its positions)."""
 
-    def __init__(self, reqs, hq, hkv, d, seed=0, mag=1.0, scale=None, runs=37, pad=3):
+    def __init__(self, reqs, hq, hkv, d, seed=0, mag=1.0, scale=None, runs=37, pad=3, page=0):
         import torch
         self.reqs, self.hq, self.hkv, self.d = reqs, hq, hkv, d
         self.scale = 1 / math.sqrt(d) if scale is None else scale
         rng = np.random.default_rng(seed)
         n = [p + s for p, s in reqs]
-        N = sum(n) + 8
+        if page:
+            room = [-(-x // page) * page for x in n]
+            N = sum(room) + 2 * page
+            pages = 1 + rng.permutation(sum(room) // page)
+            order = (pages[:, None] * page + np.arange(page)).reshape(-1)
+        else:
+            room = n
+            N = sum(n) + 8
+            cuts = np.arange(1, N - 7, runs)
+            order = np.concatenate([np.arange(c, min(c + runs, N - 7)) for c in
+                                    rng.permutation(cuts)])
         self.N = N
-        cuts = np.arange(1, N - 7, runs)
-        order = np.concatenate([np.arange(c, min(c + runs, N - 7)) for c in
-                                rng.permutation(cuts)])
         self.table = np.zeros((len(reqs) + 1, max(n) + 2), np.int32)
         self.rows = rng.permutation(len(reqs) + 1)[:len(reqs)].astype(np.int32)
         at = 0
         for r, x in enumerate(n):
             self.table[self.rows[r], :x] = order[at:at + x]
-            at += x
+            at += room[r]
         self.qo = np.concatenate([[0], np.cumsum([s for _, s in reqs])]).astype(np.int32)
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.k, self.v = _bf((2, hkv, N, d), g), _bf((2, hkv, N, d), g)
@@ -382,6 +391,22 @@ def test_extend_without_modification_is_extend_attention():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("page", [1, 8, 16, 32, 64, 128, 192])
+def test_extend_over_pages(d, page):
+    """Pages that groups and boxes of keys fall on, and that end inside them;
+    windows that begin inside a page."""
+    import torch
+    e = Extend([(70, 130), (0, 333), (1000, 1), (47, 17)], 8, 2, d, seed=page, page=page)
+    slopes = torch.exp2(-1.0 * torch.arange(1, 9, device="cuda"))
+    for mod in (dict(), dict(window=77), dict(softcap=20.0), dict(window=201, softcap=20.0,
+                                                                 slopes=slopes)):
+        out, lse = e.run(torch.bfloat16, **mod)
+        assert rx.device_check() == 0
+        e.check(out, lse, **mod)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_outputs_that_start_on_16_bytes(dtype):
     """Outputs and workspaces need 16-byte alignment, not more."""
@@ -419,7 +444,8 @@ def test_extend_reads_no_key_before_its_windows(d):
 @pytest.mark.gpu
 @pytest.mark.parametrize("mag,softcap,slope", [(1e-3, 1e-3, 0.0), (1e3, 30.0, 0.0),
                                                (1.0, 0.0, 1e4), (30.0, 1e5, -0.5),
-                                               (1e4, 0.0, 0.0)])
+                                               (1e4, 0.0, 0.0), (1.0, 2.0 ** 40, 0.0),
+                                               (1.0, 2.0 ** -40, 0.0), (10.0, 1e4, 0.1)])
 def test_extend_extreme_scores(mag, softcap, slope):
     import torch
     e = Extend([(50, 70), (0, 200)], 4, 2, 128, seed=4, mag=mag)
