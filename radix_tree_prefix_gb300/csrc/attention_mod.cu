@@ -449,8 +449,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     for (int k = 0, c = first; ok && c < total; ++k, c += step) {
       TileDesc t;
       if (!v) {
-        const int hkv = a.hq / a.group;
-        int bx = c / hkv, kvh = c - bx * hkv;
+        int bx = over_hkv<true>(a, c), kvh = c - bx * a.hkv;
         if (!DECODE && !a.heads_interleaved) {
           kvh = c / a.num_tiles;
           bx = c - kvh * a.num_tiles;
@@ -513,7 +512,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         if (r0 + lane < t.n_rows) {
           int64_t qi = 0, part = 0;
           int head = 0, lim = 0;
-          row_info<DECODE>(a, t, t.kvh, r0 + lane, qi, head, part, lim);
+          row_info<DECODE, true>(a, t, t.kvh, r0 + lane, qi, head, part, lim);
           src = a.q + (qi * a.hq + head) * D;
         }
 #pragma unroll 8
@@ -643,7 +642,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     if (valid) {
       int64_t qi = 0, part = 0;
       int head = 0;
-      row_info<DECODE>(a, t, t.kvh, row, qi, head, part, lim);
+      row_info<DECODE, true>(a, t, t.kvh, row, qi, head, part, lim);
       const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
       if (!DECODE) lim = max(lim, t.bidir);
       rm = row_mod(a, qi, head, pos);
@@ -897,7 +896,7 @@ __global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   row_tiles<D, PAIR, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), int(gridDim.x),
-                                         a.num_tiles * (a.hq / a.group));
+                                         a.num_tiles * a.hkv);
 }
 
 // Decode: the plan's large items as tiles, a CTA each, and beside them the units
@@ -933,7 +932,7 @@ __global__ void __launch_bounds__(kPipeWarps * 32, 1)
     cur.idx = int(blockIdx.x) + int(gridDim.x) * warp;
     cur.stage = 1;  // (it has its index)
   }
-  while (cur.stage < 3) next_unit_step<SLOPES>(a, cur);
+  while (cur.stage < 3) next_unit_step<SLOPES, true>(a, cur);
   while (cur.idx < a.n_small_units) {
     nxt.stage = 0;
     if (!a.unit_counter) {
@@ -947,7 +946,7 @@ __global__ void __launch_bounds__(kPipeWarps * 32, 1)
     } else if (lane == 0) {
       atomicOr(&g_tc_error, 1);  // the plan gives head_dim 256 no such item
     }
-    while (nxt.stage < 3) next_unit_step<SLOPES>(a, nxt);
+    while (nxt.stage < 3) next_unit_step<SLOPES, true>(a, nxt);
     cur = nxt;
   }
   if (a.n_tc_ctas > 0) rxk::griddep_wait();
@@ -978,6 +977,9 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
   a->row_stride = row_stride;
   a->hq = num_q_heads;
   a->group = num_q_heads / pool->num_kv_heads;
+  a->hkv = pool->num_kv_heads;
+  a->by_group = make_div(a->group);
+  a->by_hkv = make_div(a->hkv);
   a->scale_log2 = scale * kLog2e;
   a->tma_row_base = rows;
   a->tma_head_rows = pool->num_slots;

@@ -40,6 +40,25 @@ constexpr int kExtendInterleaveWaves = 8;
 constexpr int64_t kExtendInterleaveKvBytes = 32ll << 20;
 constexpr int BM = 128;
 
+// Division of 0 <= n < 2^31 by a constant d >= 1 of the launch: (n * mul) >> shift
+// with mul = ceil(2^shift / d) and shift = 31 + ceil(log2 d) is exact there (mul d
+// - 2^shift <= 2^(shift - 31)).  A division by a value the compiler does not know
+// is a chain of some thirty instructions, and a tile's description, its rows' offsets
+// and each unit's start hold several: with these 32 documents of 17..1010 tokens
+// took 108 us, with the operator 113; a 16k prompt with window 1024 217 and 222.
+struct Div {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return int((uint64_t(uint32_t(n)) * mul) >> shift);
+  }
+};
+inline Div make_div(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  const uint64_t two = 1ull << (31 + s);
+  return Div{uint32_t((two + uint64_t(d) - 1) / uint64_t(d)), uint32_t(31 + s)};
+}
+
 struct TcArgs {
   const bf16* q;
   const bf16* kpool;  // layer base, [Hkv][num_slots][D]
@@ -97,6 +116,8 @@ struct TcArgs {
   const int32_t* bidir_end;
   const int32_t* ctx_len;
   int out_bf16;
+  int hkv;
+  Div by_group, by_hkv;    // division by them
 };
 
 struct TileDesc {
@@ -110,6 +131,18 @@ struct TileDesc {
   int key_lo, bidir;
   int kvh;
 };
+
+// n / group, n / KV heads
+template <bool MOD>
+__device__ __forceinline__ int over_group(const TcArgs& a, int n) {
+  if constexpr (MOD) return a.by_group(n);
+  return n / a.group;
+}
+template <bool MOD>
+__device__ __forceinline__ int over_hkv(const TcArgs& a, int n) {
+  if constexpr (MOD) return a.by_hkv(n);
+  return n / (a.hq / a.group);
+}
 
 template <bool DECODE, bool MOD>
 __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
@@ -154,12 +187,12 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
     t.gr0 = (tile - a.tile_indptr[lo]) * BM;
     t.n_rows = min(BM, s_r * G - t.gr0);
     t.key_begin = 0;
-    t.key_end = t.prefix + (t.gr0 + t.n_rows - 1) / G + 1;
-    t.nomask_end = t.prefix + t.gr0 / G + 1;
+    t.key_end = t.prefix + over_group<MOD>(a, t.gr0 + t.n_rows - 1) + 1;
+    t.nomask_end = t.prefix + over_group<MOD>(a, t.gr0) + 1;
     t.member_off = t.part_base = 0;
     if constexpr (MOD) {
       // the keys that some row of the tile sees lie in [key_begin, key_end)
-      const int tok0 = t.gr0 / G, tok1 = (t.gr0 + t.n_rows - 1) / G;
+      const int tok0 = t.nomask_end - 1 - t.prefix, tok1 = t.key_end - 1 - t.prefix;
       t.bidir = a.bidir_end ? min(__ldg(a.bidir_end + lo), t.prefix + s_r) : 0;
       t.key_end = max(t.key_end, t.bidir);
       if (a.window > 0) t.key_begin = max(0, t.prefix + tok0 - a.window + 1);
@@ -179,19 +212,19 @@ __device__ __forceinline__ TileDesc describe(const TcArgs& a, int bx) {
 }
 
 // row i -> (query index, head, part index for decode, causal limit)
-template <bool DECODE>
+template <bool DECODE, bool MOD = false>
 __device__ __forceinline__ void row_info(const TcArgs& a, const TileDesc& t, int kvh, int i,
                                          int64_t& qi, int& head, int64_t& part, int& lim) {
   const int G = a.group;
   if constexpr (DECODE) {
-    const int unit = i / G;
+    const int unit = over_group<MOD>(a, i);
     qi = a.members[t.member_off + unit];
     head = kvh * G + (i - unit * G);
     part = int64_t(t.part_base) + unit;
     lim = t.key_end;
   } else {
     const int gr = t.gr0 + i;
-    const int tok = gr / G;
+    const int tok = over_group<MOD>(a, gr);
     qi = int64_t(t.q_base) + tok;
     head = kvh * G + (gr - tok * G);
     part = 0;
@@ -327,7 +360,7 @@ struct NextUnit {
   __device__ __forceinline__ int32_t word(int k) const { return __shfl_sync(0xffffffffu, wk, k); }
 };
 
-template <bool BACK = false>
+template <bool BACK = false, bool MOD = false>
 __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
   const int lane = threadIdx.x & 31;
   if (n.stage == 0) {
@@ -336,7 +369,7 @@ __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
     n.idx = __shfl_sync(0xffffffffu, n.idx, 0);
     n.wk = 0;
     if (n.idx < a.n_small_units && lane < RX_WORK_WORDS)
-      n.wk = __ldg(a.work_small + int64_t(n.idx / (a.hq / a.group)) * RX_WORK_WORDS + lane);
+      n.wk = __ldg(a.work_small + int64_t(over_hkv<MOD>(a, n.idx)) * RX_WORK_WORDS + lane);
   } else if (n.stage == 2) {
     const int32_t row = n.word(0), kb = n.word(1), kend = n.word(2), grow = n.word(7);
     if (n.idx < a.n_small_units) {
@@ -363,9 +396,9 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
   constexpr int NK = D / 16;  // k-steps of S^T, m-tiles of O^T
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int n_heads_kv = a.hq / a.group;
+  const int n_heads_kv = MOD ? a.hkv : a.hq / a.group;
   const int unit = cur.idx;
-  const int kvh = unit - (unit / n_heads_kv) * n_heads_kv;
+  const int kvh = unit - over_hkv<MOD>(a, unit) * n_heads_kv;
   const int G = a.group;
   const int32_t w_row = cur.word(0), w_kend = cur.word(2), w_grow = cur.word(7);
   const int32_t* trow = a.table + int64_t(w_row) * a.row_stride;
@@ -489,7 +522,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     const bool ok = r < n_rows;
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q);
     if (ok) {
-      const int u = r / G;
+      const int u = over_group<MOD>(a, r);
       const int64_t b = a.members[member_off + u];
       qrow = reinterpret_cast<const uint32_t*>(a.q + (b * a.hq + kvh * G + (r - u * G)) * D);
     }
@@ -509,7 +542,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * c + e;
         if (r < n_rows) {
-          const int u = r / G;
+          const int u = over_group<MOD>(a, r);
           const int64_t b = a.members[member_off + u];
           const int pos = a.ctx_len ? __ldg(a.ctx_len + b) + a.step - 1 : 0;
           rm[nt][e] = row_mod(a, b, kvh * G + (r - u * G), pos);
@@ -525,7 +558,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
 #pragma unroll 1
   for (int st = 0; st < n_steps; ++st) {
     // the next unit: index at step 0, work words at step 2, slots at step 4
-    if (st == 0 || st == 2 || st == 4) next_unit_step<SLOPES>(a, nxt);
+    if (st == 0 || st == 2 || st == 4) next_unit_step<SLOPES, MOD>(a, nxt);
     rxk::cp_async_wait<S - 2>();
     __syncwarp();
     const uint32_t stage = ring + ((gstep + uint32_t(st)) % S) * kStageBytes;
@@ -669,7 +702,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const int r = nt * 8 + 2 * c + e;
       if (r >= n_rows) continue;
-      const int uu = r / G;
+      const int uu = over_group<MOD>(a, r);
       const int head = kvh * G + (r - uu * G);
       const int64_t part = int64_t(part_base) + uu;
       float* dst = a.ws_o + (part * a.hq + head) * D;
