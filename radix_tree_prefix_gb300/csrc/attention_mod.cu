@@ -159,7 +159,8 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
       const int key = k0 + lane + 32 * i;
-      dst[i] = j < n_loads && key >= t.key_lo && key < t.key_end ? __ldg(t.trow + key) : -1;
+      dst[i] = j < n_loads && key >= t.key_lo && key < t.key_end ? __ldg(t.trow + key)
+                                                                 : kNoKey<true>;
     }
   };
 #pragma unroll
@@ -174,7 +175,7 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
       slot[i] = next[0][i];
 #pragma unroll
       for (int u = 0; u + 1 < AHEAD; ++u) next[u][i] = next[u + 1][i];
-      if (slot[i] >= a.num_slots || slot[i] < -1) {
+      if (slot[i] >= a.num_slots || (slot[i] < 0 && slot[i] != kNoKey<true>)) {
         atomicOr(&g_tc_error, 1);
         slot[i] = 0;
       }

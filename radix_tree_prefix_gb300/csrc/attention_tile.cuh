@@ -120,6 +120,11 @@ struct TcArgs {
   Div by_group, by_hkv;    // division by them
 };
 
+// A loader's mark, in a slot's place, for a key outside its range.  MOD: not -1, which
+// a table may hold by mistake and which is flagged as any slot outside the pool.
+template <bool MOD>
+constexpr int32_t kNoKey = MOD ? INT32_MIN : -1;
+
 struct TileDesc {
   const int32_t* trow;
   int key_begin, key_end, nomask_end, n_rows;
@@ -378,7 +383,7 @@ __device__ __forceinline__ void next_unit_step(const TcArgs& a, NextUnit& n) {
 #pragma unroll
       for (int i = 0; i < kSlotRegs; ++i) {
         const int at = lane + 32 * i;
-        n.s[i] = at < ke - kb ? __ldg(trow + (BACK ? ke - 1 - at : kb + at)) : -1;
+        n.s[i] = at < ke - kb ? __ldg(trow + (BACK ? ke - 1 - at : kb + at)) : kNoKey<MOD>;
       }
     }
   }
@@ -437,14 +442,14 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
   // [kb + 128 b, ..)) sits in half b % 2.  Block 0 comes prefetched with the
   // unit; block b + 1 is loaded into registers when block b is stored, and
   // stored when the first step of block b + 1 is issued, so no table read
-  // waits.  -1 past the key range; a slot outside the pool is flagged and
+  // waits.  kNoKey past the key range; a slot outside the pool is flagged and
   // read as slot 0.
   int32_t blk[kSlotRegs];
   auto store_block = [&](const int32_t (&r)[kSlotRegs], int half) {
 #pragma unroll
     for (int i = 0; i < kSlotRegs; ++i) {
       int32_t sl = r[i];
-      if (sl < -1 || sl >= a.num_slots) {
+      if ((sl < 0 && sl != kNoKey<MOD>) || sl >= a.num_slots) {
         atomicOr(&g_tc_error, 1);
         sl = 0;
       }
@@ -456,7 +461,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
 #pragma unroll
     for (int i = 0; i < kSlotRegs; ++i) {
       const int at = base + lane + 32 * i;
-      blk[i] = at < ke - kb ? __ldg(trow + (SLOPES ? ke - 1 - at : kb + at)) : -1;
+      blk[i] = at < ke - kb ? __ldg(trow + (SLOPES ? ke - 1 - at : kb + at)) : kNoKey<MOD>;
     }
   };
   if (n_steps > 0) {

@@ -939,12 +939,14 @@ def _norm_args(what, norm, d, dev):
 def qk_rope(rope, d_positions, d_q, d_k, d_q_out, d_k_out, norm=None, stream=None):
     """rx_qk_rope: bf16 queries [T, Hq, d] and keys [T, Hkv, d] (views of one
     projection, if need be) normalised and rotated into the outputs, which may
-    be the inputs."""
+    be the inputs.  rope None: not rotated, and d_positions may be None."""
     tt = _torch or _t()
     T, hq, d = d_q.shape
     hkv, dev, bf16 = d_k.shape[1], d_q.get_device(), tt.bf16
     s = _current("qk_rope", tt, dev, stream)
-    pos = _flat("qk_rope", "d_positions", d_positions, tt.i32, T, dev)
+    pos = None
+    if rope is not None or d_positions is not None:
+        pos = _flat("qk_rope", "d_positions", d_positions, tt.i32, T, dev)
     q, qs = _heads("qk_rope", "d_q", d_q, T, hq, d, dev, bf16)
     k, ks = _heads("qk_rope", "d_k", d_k, T, hkv, d, dev, bf16)
     qo, qos = _heads("qk_rope", "d_q_out", d_q_out, T, hq, d, dev, bf16)
@@ -960,12 +962,14 @@ def qkv_store(pool, layer, rope, d_positions, d_slots, d_q, d_k, d_v, d_q_out, n
               stream=None):
     """rx_qkv_store: queries normalised and rotated into d_q_out, keys
     alike and values as they are into their slots of the pool.  d_q and
-    d_q_out None: keys and values only."""
+    d_q_out None: keys and values only; rope None: as in qk_rope."""
     tt = _torch or _t()
     T, d, hkv = d_slots.numel(), pool.head_dim, pool.num_kv_heads
     dev, bf16 = d_k.get_device(), tt.bf16
     s = _current("qkv_store", tt, dev, stream)
-    pos = _flat("qkv_store", "d_positions", d_positions, tt.i32, T, dev)
+    pos = None
+    if rope is not None or d_positions is not None:
+        pos = _flat("qkv_store", "d_positions", d_positions, tt.i32, T, dev)
     slots = _flat("qkv_store", "d_slots", d_slots, tt.i32, T, dev)
     k, ks = _heads("qkv_store", "d_k", d_k, T, hkv, d, dev, bf16)
     v, vs = _heads("qkv_store", "d_v", d_v, T, hkv, d, dev, bf16)

@@ -376,3 +376,21 @@ def test_captured_and_on_another_stream():
     side.synchronize()
     assert torch.equal(out, other) and not torch.equal(out, want)
     assert rx.device_check() == 0
+
+
+@pytest.mark.gpu
+def test_norm_alone_needs_no_positions():
+    import torch
+    r = Rows(9, 4, 2, 128, True, seed=3)
+    norm = _norm("weight", r.w)
+    q, k = r.q.clone(), r.k.clone()
+    rx.qk_rope(None, None, r.q, r.k, q, k, norm)
+    for got, x, w in ((q, r.q, r.w[0]), (k, r.k, r.w[1])):
+        want, tol = reference(_np(x), None, 128, 0, "half", {}, "weight", _np(w), 1e-6)
+        assert (np.abs(_np(got) - want) <= tol).all()
+    pool = [torch.zeros((1, 2, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    slots = torch.arange(1, 10, dtype=torch.int32, device="cuda")
+    q2 = torch.empty_like(q)
+    rx.qkv_store(rx.pool_desc(*pool), 0, None, None, slots, r.q, r.k, r.v, q2, norm)
+    assert torch.equal(q2, q) and torch.equal(pool[0][0, :, 1:10], k.transpose(0, 1))
+    assert torch.equal(pool[1][0, :, 1:10], r.v.transpose(0, 1)) and rx.device_check() == 0

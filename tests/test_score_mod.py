@@ -678,3 +678,28 @@ def test_captured_streams_and_two_at_once():
     d2.check(*b, **kw)
     e.check(*f, **kw)
     assert rx.device_check() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("bad", [-1, -7, "num_slots", 2 ** 31 - 1])
+def test_slots_outside_the_pool_are_flagged_and_read_as_slot_0(d, bad):
+    """A table entry of -1 too, which is no mark for the end of a request."""
+    import torch
+    e = Extend([(70, 130), (0, 333)], 8, 2, d, seed=21)
+    c = Decode([40 + 3 * i for i in range(37)], 300, 8, 2, d, seed=1)
+    for x, rows in ((e, e.rows), (c, range(c.B))):
+        x.table = x.table.copy()
+        at = [(r, p) for r in rows for p in (0, 17, 39, 40)]
+        slots = {}
+        for slopes in (None, torch.full((8,), 0.01, device="cuda")):
+            for value in (0, x.k.shape[2] if bad == "num_slots" else bad):
+                for r, p in at:
+                    x.table[r, p] = value
+                got = x.run(softcap=30.0, slopes=slopes)
+                if value:
+                    with pytest.raises(rx.RxError, match="flags 2"):
+                        rx.device_check()
+                slots[value == 0] = got
+                assert rx.device_check() == 0
+            assert all(torch.equal(a, b) for a, b in zip(slots[True], slots[False]))
