@@ -9,39 +9,48 @@
 // One tile = 128 query rows that read one KV head over one key range, as in
 // attention_tc.cu (extend: suffix tokens x heads of a group; decode: members x
 // heads of a shared segment).  Modified scores cost the softmax warps several
-// times what the plain ones do (a cap alone some ten operations a score), and
-// two warpgroups that share a key tile wait for one another at its maximum. So
-// here the two warpgroups take whole key tiles in turn, thread = row:
-//   warps 0-7   warpgroup j % 2 takes key tile j: scores from TMEM, modified, masked,
-//               the row's maximum; then the row's reference m of tile j - 1
-//               comes from the other warpgroup through shared memory (barrier
-//               H), is raised if a score exceeds it by more than 2^32 (O is then
-//               rescaled in TMEM), and goes on to tile j + 1; only then the
-//               exponentials, P (bf16) into TMEM over S.  So one warpgroup's
-//               exponentials run beside the other's scores, and the chain between
-//               them is a compare and a barrier.  Each warpgroup keeps the row
-//               sums of its own tiles; they meet in the epilogue;
-//   warp 8      S_j = Q K_j^T into a ring of TMEM buffers; warp 11 O += P_j V_j;
-//   warps 9-10  K and V into shared memory: a tile of one run of slots is one TMA
-//               box per 64 columns, else every group of 16 keys that is a run
-//               (pages of 16 slots and more, aligned runs) one smaller box,
-//               and the groups left are gathered by 16-byte cp.async, whose
-//               completion is waited for only when the next tile's loads are out.
+// times what the plain ones do (a cap alone some seven operations a score), and two
+// warpgroups that share a key tile wait for one another at its maximum.  So here
+// three warpgroups (two with two CTAs an SM, PAIR) take whole key tiles in turn,
+// thread = row, and a CTA walks over row tiles:
+//   warps 0..    warpgroup j % NW takes key tile j (64 keys): scores from TMEM 32 at a
+//                time, modified, masked, and at once their weights 2^(s - m) (bf16)
+//                into TMEM over scores read already, under the reference m that the
+//                warpgroup used last.  At the tile's end the reference of tile j - 1
+//                comes from the warpgroup before through shared memory (barrier H):
+//                if m is another, this tile's weights are brought to it, or O (in
+//                TMEM) to m, whichever is smaller; then m goes on to tile j + 1.  Both
+//                are rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
+//                and a score may exceed it by 64, so that nothing but such a row ever
+//                stops for another tile.  Each warpgroup keeps the row sums of its own
+//                tiles; they meet in the row tile's end;
+//   then warp S  Q rows, and S_j = Q K_j^T into a ring of TMEM buffers;
+//   K, V         loaders, the K loader also finding row tiles and their key ranges for
+//                all the others.  Runs of 64 slots are one TMA box per 64 columns, runs
+//                of 16 (pages of 16 slots and more) smaller ones, and the groups left
+//                are gathered by 16-byte cp.async, whose completion is waited for only
+//                when the next tile's loads are out;
+//   PV           O += P_j V_j.
 // Rows of a tile see different keys: the key range is what some row sees, and
-// masks are applied only in key tiles that some row of the warp sees in part.
-// A masked score is -inf; a row that has seen no key yet has m = -inf and weighs
-// its masked keys 0, and one that never sees any gets o = 0, lse = -inf.
+// masks are applied only to keys that some row of the warp does not see.  A masked
+// score is -inf; a row that has seen no key yet has m = -inf and weighs its masked
+// keys 0, and one that never sees any gets o = 0, lse = -inf.
+//
+// What bounds it is the softmax warps' instructions, and fetching them: 64 rows' keys
+// take some 400 instructions a warp without a cap and 700 with one, at a little more
+// than half an issue slot a clock.  The loops are rolled, and the softmax role stands
+// first in the kernel (agent calls under a cap 458 us, behind the other roles 506).
 
 #include "attention_tile.cuh"
 
 namespace {
 
 constexpr int kGroup = 16;  // keys of a small TMA box
-// A row's reference is raised when a score exceeds it by more than this (log2
-// units).  Raising stops the chain between the warpgroups until the product
-// before it has completed, so it is made rare; 2^32 times the weights' usual size
-// leaves fp32 (and bf16, of the same range) room for the sums of 2^60 keys.
-constexpr float kRaise = 32.f;
+// A weight exceeds its reference by 2^kRaise at most.  fp32 (and bf16, of the same
+// range) then has room for sums of 2^20 keys with values up to 2^40, and a row whose
+// scores all lie 64 below a reference of 0 loses nothing of them (down to values of
+// 2^-60): what is raised or lowered are rows of extreme scores only.
+constexpr float kRaise = 64.f;
 constexpr int kPairWindow = 2048;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
@@ -58,7 +67,7 @@ struct Layout4 {
   static constexpr int KV_BYTES = BS * D * 2;
   static constexpr int NW = PAIR ? 2 : 3;  // softmax warpgroups
   static constexpr int THREADS = 128 * (NW + 1);
-  static constexpr int NK = PAIR ? 2 : 3, NV = 2;
+  static constexpr int NK = PAIR ? 2 : 3, NV = D == 128 && !PAIR ? 3 : 2;
   static constexpr int NS = PAIR ? 2 : D == 128 ? 3 : 4;
   static constexpr int NB = NS * SUBS;  // tiles of P
   // Barriers of the reference's way from tile to tile: a warpgroup of three that
@@ -87,7 +96,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 }
 
 struct Maps4 {
-  CUtensorMap k, v;      // boxes of a tile's keys x 64 columns
+  CUtensorMap k, v;      // boxes of 64 keys x 64 columns
   CUtensorMap k16, v16;  // boxes of 16 keys
 };
 
@@ -139,10 +148,12 @@ struct Ring {
 
 // One warp loads the K or V tiles of a row tile into its ring; barriers full
 // and empty of stage s at full0 + 8 s and empty0 + 8 s (empty: the products that
-// read the stage's last keys completed).  Returns false if a wait gave up.  One piece of code for both warps, its
-// loops rolled: with the roles' loops unrolled the kernel was 195 KB of code, and
-// its warps, each somewhere else in it, waited for instructions most of the
-// time.
+// read the stage's last keys completed).  Returns false if a wait gave up.  One piece
+// of code for both warps, its loops rolled (with the roles' loops unrolled the kernel
+// was 195 KB of code, and its warps, each somewhere else in it, waited for
+// instructions most of the time), and runs of slots found by two votes: a loader of
+// twice the instructions was what pages of 16 waited for (an agent's calls 519 us
+// without modification, now 422; on 64-key runs 339).
 template <int D, int BS, bool BACK>
 __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, int n_loads,
                                            const CUtensorMap* tm, const CUtensorMap* tm16,
@@ -150,18 +161,19 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
                                            uint32_t full0, uint32_t empty0, int stages,
                                            Ring& ring, volatile int* abort_flag) {
   constexpr int CPR = D / 8, CB = D / 64;
-  constexpr int SPL = BS / 32;   // slots per lane: keys lane + 32 i
-  constexpr int AHEAD = 3;       // tiles whose slots are on their way
+  constexpr int SPL = BS / 32;  // slots a lane: of keys SPL lane + i
+  constexpr int LPG = kGroup / SPL, LPW = 64 / SPL;  // lanes of a group, of 64 keys
+  constexpr uint32_t GROUPS = LPG == 4 ? 0x11111111u : 0x01010101u;  // their first lanes
+  constexpr uint32_t WIDES = LPW == 16 ? 0x00010001u : 1u;           // those of 64 keys
+  constexpr int AHEAD = 3;  // loads whose slots are on their way
   const int lane = threadIdx.x & 31;
   int32_t slot[SPL], next[AHEAD][SPL];
   auto load_slots = [&](int j, int32_t (&dst)[SPL]) {
-    const int k0 = t.key_begin + (BACK ? n_loads - 1 - j : j) * BS;
+    const int k0 = t.key_begin + (BACK ? n_loads - 1 - j : j) * BS + SPL * lane;
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-      const int key = k0 + lane + 32 * i;
-      dst[i] = j < n_loads && key >= t.key_lo && key < t.key_end ? __ldg(t.trow + key)
-                                                                 : kNoKey<true>;
-    }
+    for (int i = 0; i < SPL; ++i)
+      dst[i] = j < n_loads && k0 + i >= t.key_lo && k0 + i < t.key_end ? __ldg(t.trow + k0 + i)
+                                                                       : kNoKey<true>;
   };
 #pragma unroll
   for (int u = 0; u < AHEAD; ++u) load_slots(u, next[u]);
@@ -183,74 +195,71 @@ __device__ __forceinline__ bool load_tiles(const TcArgs& a, const TileDesc& t, i
     load_slots(j + AHEAD, next[AHEAD - 1]);
     const uint32_t full = full0 + 8u * uint32_t(ring.stage);
     const uint32_t dst = smem0 + uint32_t(ring.stage * BS * D * 2);
+    // Runs of slots, by the bits of their first lanes: of 64 keys (wide), and of 16 in
+    // the rest.  A lane's slots are a run, and go on in the next lane's.
+    bool run = true;
+#pragma unroll
+    for (int i = 1; i < SPL; ++i) run = run && slot[i] == slot[0] + i;
+    const uint32_t runs = __ballot_sync(0xffffffffu, run && slot[0] >= 0);
+    const uint32_t links = __ballot_sync(
+        0xffffffffu, __shfl_down_sync(0xffffffffu, slot[0], 1) == slot[0] + SPL);
+    uint32_t narrow = runs & (links | (GROUPS << (LPG - 1)));
+    narrow &= narrow >> 1;
+    narrow &= narrow >> 2;
+    if constexpr (LPG == 8) narrow &= narrow >> 4;
+    narrow &= GROUPS;
+    // (groups that are runs and linked to the next one)
+    uint32_t wide = narrow & ((links >> (LPG - 1)) | ((WIDES << (LPW - LPG))));
+    wide &= wide >> LPG;
+    wide &= wide >> (2 * LPG);
+    wide &= WIDES;
+    const uint32_t in_wide = wide * (GROUPS & (LPW == 16 ? 0xffffu : 0xffffffffu));
+    narrow &= ~in_wide;
+    uint32_t left = GROUPS & ~in_wide & ~narrow;
     if (ring.count >= stages &&
         !warp_wait(empty0 + 8u * uint32_t(ring.stage), ring.phase, abort_flag)) {
       ok = false;
       break;
     }
-    // which groups of 16 keys are runs of slots (bit g), and whether they all are one
-    const int32_t first = __shfl_sync(0xffffffffu, slot[0], 0);
-    bool one = first >= 0 && int64_t(first) + BS <= a.num_slots;
-    uint32_t runs = 0;
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-      one = one && slot[i] == first + lane + 32 * i;
-      const int32_t b = __shfl_sync(0xffffffffu, slot[i], lane & 16);
-      const uint32_t ok = __ballot_sync(
-          0xffffffffu, b >= 0 && int64_t(b) + kGroup <= a.num_slots && slot[i] == b + (lane & 15));
-      runs |= ((ok & 0xffffu) == 0xffffu ? 1u : 0u) << (2 * i) |
-              (ok >> 16 == 0xffffu ? 2u : 0u) << (2 * i);
+    if (lane == 0)
+      mbar_expect_tx(full, uint32_t(__popc(wide) * 64 + __popc(narrow) * kGroup) * (D * 2));
+    __syncwarp();
+    // a lane a box: columns 64 (lane % CB) of 64 keys, or of a group
+    const int n = lane / CB, col = lane % CB;
+    if (wide) {
+      const int32_t b = __shfl_sync(0xffffffffu, slot[0], (n * LPW) & 31);
+      if (n < BS / 64 && (wide >> (n * LPW) & 1u))
+        tc::tma_load_2d(dst + uint32_t((col * BS + n * 64) * 128), tm, col * 64, row0 + b, full);
     }
-    one = __all_sync(0xffffffffu, one);
-    bool gathered = false;
-    if (one) {
-      if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(BS * D * 2));
-      __syncwarp();
-      if (lane < CB)
-        tc::tma_load_2d(dst + uint32_t(lane * BS * 128), tm, lane * 64, row0 + first, full);
-    } else {
-      constexpr uint32_t ALL = (1u << (BS / kGroup)) - 1u;
-      gathered = runs != ALL;
-      if (lane == 0) mbar_expect_tx(full, uint32_t(__popc(runs) * kGroup * D * 2));
-      __syncwarp();
-      {
-        // a lane a box: columns 64 (lane % CB) of group lane / CB
-        const int g = lane / CB;
-        int32_t b = 0;
-#pragma unroll
-        for (int i = 0; i < SPL; ++i) {
-          const int32_t x = __shfl_sync(0xffffffffu, slot[i], 16 * (g & 1));
-          if (g >> 1 == i) b = x;
-        }
-        if (g < BS / kGroup && (runs >> g & 1u))
-          tc::tma_load_2d(dst + uint32_t((lane % CB) * BS * 128 + g * kGroup * 128), tm16,
-                          (lane % CB) * 64, row0 + b, full);
-      }
+    if (narrow) {
+      const int32_t b = __shfl_sync(0xffffffffu, slot[0], (n * LPG) & 31);
+      if (n < BS / kGroup && (narrow >> (n * LPG) & 1u))
+        tc::tma_load_2d(dst + uint32_t((col * BS + n * kGroup) * 128), tm16, col * 64, row0 + b,
+                        full);
+    }
+    const bool gathered = left != 0;
 #pragma unroll 1
-      for (uint32_t left = ALL & ~runs; left; left &= left - 1u) {
-        const int g = __ffs(left) - 1;
-        int32_t mine = slot[0];
+    for (; left; left &= left - 1u) {
+      const int first = __ffs(left) - 1;  // the group's first lane
+      // lanes 0-15 and 16-31 copy chunks (lane % 16) + 16 h of rows k and k + 8
 #pragma unroll
-        for (int i = 1; i < SPL; ++i) mine = (g >> 1) == i ? slot[i] : mine;
-        // lanes 0-15 and 16-31 copy chunks (lane % 16) + 16 h of rows 2k, 2k + 1
-#pragma unroll 4
-        for (int k = 0; k < 8; ++k) {
-          const int in = 2 * k + (lane >> 4);
-          const int32_t sl = __shfl_sync(0xffffffffu, mine, 16 * (g & 1) + in);
-          const bool ok = sl >= 0;
-          const bf16* src = src_base + int64_t(ok ? sl : 0) * D;
+      for (int k = 0; k < 8; ++k) {
+        const int32_t sl = __shfl_sync(0xffffffffu, slot[k % SPL],
+                                       first + k / SPL + (lane >> 4) * (LPG / 2));
+        const bool there = sl >= 0;
+        const bf16* src = src_base + int64_t(there ? sl : 0) * D;
+        const int row = first * SPL + k + (lane >> 4) * 8;
 #pragma unroll
-          for (int h = 0; h < CPR / 16; ++h) {
-            const int ch = (lane & 15) + 16 * h;
-            rxk::cp_async_16(sw128(dst, BS, g * kGroup + in, ch), src + ch * 8, ok);
-          }
+        for (int h = 0; h < CPR / 16; ++h) {
+          const int ch = (lane & 15) + 16 * h;
+          rxk::cp_async_16(sw128(dst, BS, row, ch), src + ch * 8, there);
         }
       }
-      if (gathered)
-        rxk::cp_async_commit();
-      else if (lane == 0)
-        tc::mbar_arrive(full);
     }
+    if (gathered)
+      rxk::cp_async_commit();
+    else if (lane == 0)
+      tc::mbar_arrive(full);
     // the gather of the tile before has had this tile's issue to land in
     if (pending) {
       if (gathered)
@@ -297,17 +306,19 @@ __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr
 #pragma unroll
     for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_fold2[d]);
 }
-// Raw scores capped in place, in log2 units.
-__device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near) {
+// Raw scores capped in place, in log2 units, less m.
+__device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near,
+                                           float m) {
   if (near) {
+    const float2 neg2 = make_float2(-m, -m);
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
       float2 p[8];
       cap_factors(a, sr, e, p);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float2 y = __fmul2_rn(make_float2(__uint_as_float(sr[e + 2 * k]),
-                                                __uint_as_float(sr[e + 2 * k + 1])), p[k]);
+        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2 * k]),
+                                                __uint_as_float(sr[e + 2 * k + 1])), p[k], neg2);
         sr[e + 2 * k] = __float_as_uint(y.x);
         sr[e + 2 * k + 1] = __float_as_uint(y.y);
       }
@@ -315,13 +326,13 @@ __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], 
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      sr[e] = __float_as_uint(a.cap_out * tanh_exp(__uint_as_float(sr[e]) * a.cap_in));
+      sr[e] = __float_as_uint(fmaf(a.cap_out, tanh_exp(__uint_as_float(sr[e]) * a.cap_in), -m));
   }
 }
-// sr * scale - slope |away + e|; behind: no key lies after the row's query, and the
-// bias is linear in the key.
+// sr * scale - slope |away + e| - m; behind: no key lies after the row's query, and
+// the bias is linear in the key.
 __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, float slope,
-                                           float away, bool behind) {
+                                           float away, bool behind, float m) {
   if (behind) {
     const float2 scale2 = make_float2(scale, scale);
     float2 in8[4];  // within a group of eight keys
@@ -330,7 +341,7 @@ __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, floa
       in8[u] = make_float2(slope * float(2 * u), slope * float(2 * u + 1));
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {
-      const float b = slope * (away + float(e));
+      const float b = fmaf(slope, away + float(e), -m);
       const float2 b2 = make_float2(b, b);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -344,15 +355,55 @@ __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, floa
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      sr[e] = __float_as_uint(
-          fmaf(-slope, fabsf(away + float(e)), __uint_as_float(sr[e]) * scale));
+      sr[e] = __float_as_uint(fmaf(-slope, fabsf(away + float(e)),
+                                   fmaf(__uint_as_float(sr[e]), scale, -m)));
   }
 }
-// -inf but in [from, from + span)
-__device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int span) {
+// sr * scale - m
+__device__ __forceinline__ void scale_scores(uint32_t (&sr)[32], float scale, float m) {
+  const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(-m, -m);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])),
+                                scale2, neg2);
+    sr[e] = __float_as_uint(x.x);
+    sr[e + 1] = __float_as_uint(x.y);
+  }
+}
+// -inf but for keys [from, to) of the 32, either of which may lie outside them.
+__device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int to) {
+  // (a shift by 32 gives 0)
+  const uint32_t seen = __funnelshift_lc(0u, ~0u, uint32_t(max(from, 0))) &
+                        ~__funnelshift_lc(0u, ~0u, uint32_t(max(to, 0)));
 #pragma unroll
   for (int e = 0; e < 32; ++e)
-    if (uint32_t(e - from) >= uint32_t(span)) sr[e] = 0xff800000u;
+    if (!(seen >> e & 1u)) sr[e] = 0xff800000u;
+}
+// 32 lanes x 16 columns of 32-bit values into registers.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// A tile's bf16 weights (32 columns of pairs) times f, a power of two: exact.
+__device__ __forceinline__ void scale_weights(uint32_t taddr, float f) {
+  tc::tmem_st_wait();  // the warp's own stores
+#pragma unroll 1
+  for (int c = 0; c < BN / 2; c += 16) {
+    uint32_t r[16];
+    tmem_ld16(taddr + uint32_t(c), r);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      r[e] = rxk::pack_bf16(__uint_as_float(r[e] << 16) * f,
+                            __uint_as_float(r[e] & 0xffff0000u) * f);
+    tmem_st16(taddr + uint32_t(c), r);
+  }
+  tc::tmem_st_wait();
 }
 
 // A CTA's row tiles first, first + step, .. below total, one after another: the
@@ -441,7 +492,262 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     return SLOPES || n_loads == 0 ? n_loads * SUBS : (t.key_end - t.key_begin + BN - 1) / BN;
   };
 
-  if (warp == SW + 1 || warp == SW + 2) {
+  if (warp < SW) {
+    // ------------------------------------------------------------ softmax
+    // (fences of the tcgen05 proxy are each lane's, before its warp arrives)
+    const int wg = warp >> 2;
+    const int i = (warp & 3) * 32 + lane;  // TMEM lane
+    const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
+    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);   // [2][BM]
+    float* sums = reinterpret_cast<float*>(gbase + Lo::SUM);  // [NW][BM]
+    int g0 = 0;    // the row tile's first tile among all of the CTA's
+    int used = 0;  // row tiles with keys before it
+#pragma unroll 1
+    for (int k = 0, c = first; c < total; ++k, c += step) {
+    TileDesc t;
+    if (!read_desc(k, t)) break;
+    const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
+    // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
+    // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
+    const bool m64 = t.n_rows <= 64;
+    const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
+    const bool valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
+    int64_t out_row = 0;  // of the outputs, or of the partial ones
+    int lim = t.key_end;
+    RowMod rm;
+    if (valid) {
+      int64_t qi = 0, part = 0;
+      int head = 0;
+      row_info<DECODE, true>(a, t, t.kvh, row, qi, head, part, lim);
+      const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
+      if (!DECODE) lim = max(lim, t.bidir);
+      rm = row_mod(a, qi, head, pos);
+      rm.lo = max(rm.lo, t.key_lo);
+      out_row = (DECODE ? part : qi) * a.hq + head;
+    } else {
+      // a lane without a row: nothing it holds is masked or counts
+      rm.lo = t.key_lo;
+      rm.pos = INT32_MAX;
+    }
+    const bool narrow = !DECODE && a.out_bf16;
+    if (n_loads == 0) {
+      // no row of the tile sees a key (decode: at this step of the plan)
+      if (valid && wg < 2) {
+        const int64_t at = out_row * D + wg * (D / 2);
+        uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
+                            : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
+        const int n = narrow ? D / 16 : D / 8;
+#pragma unroll 1
+        for (int u = 0; u < n; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = -INFINITY;
+      }
+      continue;
+    }
+    // what the rows of this warp have in common: keys [lo_max, lim_min) are seen
+    // by all of them, and keys up to pos_min lie behind all of them
+    const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
+    const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+    const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
+    float m_ref = valid ? -INFINITY : 0.f;  // reference of the row's weights, log2 units
+    float l = 0.f;            // sum of this warpgroup's weights under it
+    bool ok = true;
+    int j = (wg + NW - g0 % NW) % NW;
+    // tile j's buffer of P, and the phase of the buffer's barriers
+    int s = (g0 + j) % NB;
+    uint32_t phase = uint32_t((g0 + j) / NB) & 1u;
+#pragma unroll 1
+    for (; j < n_loads * SUBS; j += NW, s += NW) {
+      const int g = g0 + j;
+      if (s >= NB) {
+        s -= NB;
+        phase ^= 1u;
+      }
+      const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g & 1) + (warp & 3));
+      const uint32_t h_before = BAR_H + 8u * uint32_t(4 * ((g + 1) & 1) + (warp & 3));
+      const uint32_t h_parity = uint32_t((g - 1) >> 1) & 1u;
+      if (j >= n_tiles) {
+        // the half of the last load without keys; it takes its turn all the same, so
+        // that no barrier is arrived at before its last phase is done
+        if (!warp_wait(h_before, h_parity, abort_flag) ||
+            (g >= NB && !warp_wait(BAR_PF + 8u * uint32_t(s), phase ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        warp_arrive(h_bar);
+        warp_arrive(BAR_P + 8u * s);
+        continue;
+      }
+      if (!warp_wait(BAR_S + 8u * uint32_t(s / SUBS), phase, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const int k0 = t.key_begin +
+                     (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
+      const bool behind = k0 + BN - 1 <= pos_min;
+      const uint32_t p_col = tl + uint32_t(s * BN);
+      // ---- scores, 32 at a time: modified, and at once their weights under the
+      // reference this warpgroup used last (bf16 into TMEM over scores read already,
+      // their sum in fp32 before the rounding: lse is then good to fp32, and o to the
+      // roundings of its weights)
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        uint32_t sr[32], pk[16];
+        tc::tmem_ld32(p_col + uint32_t(c), sr);
+        tc::tmem_ld_wait();
+        if constexpr (CAP) {
+          float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
+                                         fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
+          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+          cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near),
+                     SLOPES ? 0.f : m_use);
+        }
+        if constexpr (SLOPES)
+          add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind,
+                     m_use);
+        else if constexpr (!CAP)
+          scale_scores(sr, a.scale_log2, m_use);
+        if (masked) mask_scores(sr, rm.lo - (k0 + c), lim - (k0 + c));
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
+                                         __uint_as_float(sr[e + 2 * u + 1])));
+        const float mx = valid ? fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) : 0.f;
+        const bool unset = m_ref == -INFINITY;
+        const bool grow = mx > (unset ? -INFINITY : kRaise);
+        if (__any_sync(0xffffffffu, grow)) {
+          // a row without a reference takes 0 if its scores are about that (tiles of other
+          // warpgroups that meet the row first then agree)
+          const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
+          if (grow) m_ref = m_use + by;
+          const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
+          l *= f;
+          if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
+          if (__any_sync(0xffffffffu, by != 0.f))
+            scale_scores(sr, 1.f, by);
+        }
+        float2 l4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
+                                       rxk::fast_exp2(__uint_as_float(sr[e + 1])));
+          l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
+          pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
+        }
+        tmem_st16(p_col + uint32_t(c / 2), pk);
+        const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+        l += lt.x + lt.y;
+      }
+      tc::tmem_st_wait();
+      // ---- the row's reference: that of tile g - 1 unless O has to be raised
+      if (j > 0) {
+        if (!warp_wait(h_before, h_parity, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const float m_prev = ref[((g - 1) & 1) * BM + i];
+        if (!__all_sync(0xffffffffu, m_prev == m_ref)) {
+          float down = 1.f;
+          const bool raise = m_prev != -INFINITY && m_ref > m_prev;
+          const float up = raise ? rxk::fast_exp2(m_prev - m_ref) : 1.f;
+          if (!raise && m_prev != -INFINITY) {
+            const float f = m_ref == -INFINITY ? 1.f : rxk::fast_exp2(m_ref - m_prev);
+            l *= f;
+            m_ref = m_prev;
+            down = f;
+          }
+          if (__any_sync(0xffffffffu, down != 1.f)) scale_weights(p_col, down);
+          if (__any_sync(0xffffffffu, raise)) {
+            // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
+            // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
+            // completed, and are done.)
+            if (!warp_wait(BAR_PF + 8u * uint32_t(s == 0 ? NB - 1 : s - 1),
+                           s == 0 ? phase ^ 1u : phase, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int oc = 0; oc < D; oc += 16) {
+              uint32_t r[16];
+              tmem_ld16(tl + uint32_t(Lo::O_COL + oc), r);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * up);
+              tmem_st16(tl + uint32_t(Lo::O_COL + oc), r);
+            }
+            tc::tmem_st_wait();
+          }
+        }
+      }
+      // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
+      ref[(g & 1) * BM + i] = m_ref;
+      warp_arrive(h_bar);
+      tc::tc_fence_before();
+      warp_arrive(BAR_P + 8u * s);
+    }
+    // Once the row tile's products are done, O stands under the last reference; the
+    // warpgroups bring their sums there and exchange them.
+    if (!ok || !warp_wait(BAR_FIN, uint32_t(used) & 1u, abort_flag)) break;
+    tc::tc_fence_after();
+    const float m_fin = ref[((g0 + n_tiles - 1) & 1) * BM + i];
+    sums[wg * BM + i] = m_ref == -INFINITY ? 0.f : l * rxk::fast_exp2(m_ref - m_fin);
+    warp_arrive(BAR_X);
+    if (!warp_wait(BAR_X, uint32_t(used) & 1u, abort_flag)) break;
+    g0 += n_loads * SUBS;
+    ++used;
+    if (wg < 2) {
+      float l_all = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) l_all += sums[w * BM + i];
+      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
+      // sector) a thread and store: the rows need no trip through shared memory.
+      constexpr int HC = D / 2;
+      const int64_t at = out_row * D + wg * HC;
+      const bool whole = (reinterpret_cast<uintptr_t>(DECODE ? a.ws_o : a.out) & 31) == 0;
+#pragma unroll 1
+      for (int oc = 0; oc < HC; oc += 16) {
+        uint32_t r[16];
+        tmem_ld16(tl + uint32_t(Lo::O_COL + wg * HC + oc), r);
+        tc::tmem_ld_wait();
+        if (oc + 16 >= HC) {  // the next row tile's products may overwrite O
+          tc::tc_fence_before();
+          warp_arrive(BAR_OE);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+        if (!valid) continue;
+        if (narrow) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[e] = rxk::pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          store_32(reinterpret_cast<bf16*>(a.out) + at + oc, h, whole);
+        } else {
+          float* dst = (DECODE ? a.ws_o : a.out) + at + oc;
+          store_32(dst, &r[0], whole);
+          store_32(dst + 8, &r[8], whole);
+        }
+      }
+      if (valid && wg == 0)
+        (DECODE ? a.ws_lse : a.lse)[out_row] =
+            l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_all);
+    }
+    }
+  } else if (warp == SW + 1 || warp == SW + 2) {
     // ------------------------------------------------------------- loaders
     const bool v = warp == SW + 2;
     Ring ring;
@@ -617,269 +923,6 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       tc::mbar_wait(BAR_END, 0, &drain_abort, kWaitLimit);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ softmax
-    // (fences of the tcgen05 proxy are each lane's, before its warp arrives)
-    const int wg = warp >> 2;
-    const int i = (warp & 3) * 32 + lane;  // TMEM lane
-    const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
-    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);   // [2][BM]
-    float* sums = reinterpret_cast<float*>(gbase + Lo::SUM);  // [NW][BM]
-    int g0 = 0;    // the row tile's first tile among all of the CTA's
-    int used = 0;  // row tiles with keys before it
-#pragma unroll 1
-    for (int k = 0, c = first; c < total; ++k, c += step) {
-    TileDesc t;
-    if (!read_desc(k, t)) break;
-    const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
-    // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
-    // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
-    const bool m64 = t.n_rows <= 64;
-    const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
-    const bool valid = (!m64 || (i & 16) == 0) && row < t.n_rows;
-    int64_t out_row = 0;  // of the outputs, or of the partial ones
-    int lim = t.key_end;
-    RowMod rm;
-    if (valid) {
-      int64_t qi = 0, part = 0;
-      int head = 0;
-      row_info<DECODE, true>(a, t, t.kvh, row, qi, head, part, lim);
-      const int pos = DECODE ? (a.ctx_len ? __ldg(a.ctx_len + qi) + a.step - 1 : 0) : lim - 1;
-      if (!DECODE) lim = max(lim, t.bidir);
-      rm = row_mod(a, qi, head, pos);
-      rm.lo = max(rm.lo, t.key_lo);
-      out_row = (DECODE ? part : qi) * a.hq + head;
-    } else {
-      // a lane without a row: nothing it holds is masked or counts
-      rm.lo = t.key_lo;
-      rm.pos = INT32_MAX;
-    }
-    const bool narrow = !DECODE && a.out_bf16;
-    if (n_loads == 0) {
-      // no row of the tile sees a key (decode: at this step of the plan)
-      if (valid && wg < 2) {
-        const int64_t at = out_row * D + wg * (D / 2);
-        uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
-                            : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
-        const int n = narrow ? D / 16 : D / 8;
-#pragma unroll 1
-        for (int u = 0; u < n; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (wg == 0) (DECODE ? a.ws_lse : a.lse)[out_row] = -INFINITY;
-      }
-      continue;
-    }
-    // what the rows of this warp have in common: keys [lo_max, lim_min) are seen
-    // by all of them, and keys up to pos_min lie behind all of them
-    const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
-    const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-    const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
-    float m_ref = -INFINITY;  // reference of the row's weights, log2 units
-    float l = 0.f;            // sum of this warpgroup's weights under it
-    bool ok = true;
-#pragma unroll 1
-    for (int j = (wg + NW - g0 % NW) % NW; j < n_loads * SUBS; j += NW) {
-      const int g = g0 + j;
-      const int s = g % NB;
-      const uint32_t h_bar = BAR_H + 8u * uint32_t(4 * (g % NH) + (warp & 3));
-      const uint32_t h_before = BAR_H + 8u * uint32_t(4 * ((g + NH - 1) % NH) + (warp & 3));
-      const uint32_t h_parity = uint32_t((g + NH - 1) / NH - 1) & 1u;
-      if (j >= n_tiles) {
-        // the half of the last load without keys; it takes its turn all the same, so
-        // that no barrier is arrived at before its last phase is done
-        if (!warp_wait(h_before, h_parity, abort_flag) ||
-            (g >= NB && !warp_wait(BAR_PF + 8u * uint32_t(s), uint32_t(g / NB - 1) & 1u,
-                                   abort_flag))) {
-          ok = false;
-          break;
-        }
-        warp_arrive(h_bar);
-        warp_arrive(BAR_P + 8u * s);
-        continue;
-      }
-      const int load = g / SUBS;
-      if (!warp_wait(BAR_S + 8u * uint32_t(load % NS), uint32_t(load / NS) & 1u, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc::tc_fence_after();
-      const int k0 = t.key_begin +
-                     (SLOPES ? (n_loads - 1 - j / SUBS) * BS + (j % SUBS) * BN : j * BN);
-      const bool behind = k0 + BN - 1 <= pos_min;
-      // ---- first pass over the scores, 32 at a time: modified, back into TMEM, and
-      // the row's maximum
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
-        uint32_t sr[32];
-        tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
-        tc::tmem_ld_wait();
-        if constexpr (CAP) {
-          float am[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
-                                         fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
-          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-          cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near));
-        }
-        if constexpr (SLOPES)
-          add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind);
-        if (masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
-        if constexpr (CAP || SLOPES) tc::tmem_st32(tl + uint32_t(s * BN + c), sr);
-        float mx4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
-                                         __uint_as_float(sr[e + 2 * u + 1])));
-        mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      }
-      if constexpr (CAP || SLOPES) tc::tmem_st_wait();
-      mx *= a.mul;
-      // ---- the row's reference: that of tile g - 1, raised if need be
-      if (!valid) mx = 0.f;
-      if (j == 0) {
-        m_ref = mx;
-      } else {
-        const int p = (g - 1) & 1;
-        if (!warp_wait(h_before, h_parity, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const float m_prev = ref[p * BM + i];
-        if (m_prev > m_ref) {
-          l *= rxk::fast_exp2(m_ref - m_prev);  // 0 from -inf
-          m_ref = m_prev;
-        }
-        const bool empty = m_ref == -INFINITY;  // no weight yet: O is 0
-        const bool grow = !empty && mx > m_ref + kRaise;
-        if (__any_sync(0xffffffffu, grow)) {
-          // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
-          // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
-          // completed, and are done.)
-          if (!warp_wait(BAR_PF + 8u * uint32_t((g - 1) % NB), uint32_t((g - 1) / NB) & 1u,
-                         abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const float alpha = grow ? rxk::fast_exp2(m_ref - mx) : 1.f;
-#pragma unroll 1
-          for (int oc = 0; oc < D; oc += 32) {
-            uint32_t r[32];
-            tc::tmem_ld32(tl + uint32_t(Lo::O_COL + oc), r);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tc::tmem_st32(tl + uint32_t(Lo::O_COL + oc), r);
-          }
-          tc::tmem_st_wait();
-          tc::tc_fence_before();
-          if (grow) {
-            l *= alpha;
-            m_ref = mx;
-          }
-        }
-        if (empty) m_ref = mx;
-      }
-      // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
-      ref[(g & 1) * BM + i] = m_ref;
-      warp_arrive(h_bar);
-      // ---- weights: bf16 into TMEM over S, their sum in fp32 before the rounding
-      // (lse is then good to fp32, and o to the roundings of its weights)
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      const float2 neg2 = make_float2(-m_use, -m_use);
-      float2 l4[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
-        uint32_t sr[32], pk[16];
-        tc::tmem_ld32(tl + uint32_t(s * BN + c), sr);
-        tc::tmem_ld_wait();
-        auto get2 = [&](int e) {
-          return make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-        };
-        auto put2 = [&](int e, float2 v) {
-          sr[e] = __float_as_uint(v.x);
-          sr[e + 1] = __float_as_uint(v.y);
-        };
-        // the exponents, in place
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) put2(e, __ffma2_rn(get2(e), a.mul2, neg2));
-        if (!CAP && !SLOPES && masked) mask_scores(sr, rm.lo - (k0 + c), max(0, lim - rm.lo));
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
-                                       rxk::fast_exp2(__uint_as_float(sr[e + 1])));
-          l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
-          pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
-        }
-        // (over scores read already)
-        tmem_st16(tl + uint32_t(s * BN + c / 2), pk);
-      }
-      const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
-      l += lt.x + lt.y;
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      warp_arrive(BAR_P + 8u * s);
-    }
-    // Once the row tile's products are done, O stands under the last reference; the
-    // warpgroups bring their sums there and exchange them.
-    if (!ok || !warp_wait(BAR_FIN, uint32_t(used) & 1u, abort_flag)) break;
-    tc::tc_fence_after();
-    const float m_fin = ref[((g0 + n_tiles - 1) & 1) * BM + i];
-    sums[wg * BM + i] = m_ref == -INFINITY ? 0.f : l * rxk::fast_exp2(m_ref - m_fin);
-    warp_arrive(BAR_X);
-    if (!warp_wait(BAR_X, uint32_t(used) & 1u, abort_flag)) break;
-    g0 += n_loads * SUBS;
-    ++used;
-    if (wg < 2) {
-      float l_all = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) l_all += sums[w * BM + i];
-      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-      // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
-      // sector) a thread and store: the rows need no trip through shared memory.
-      constexpr int HC = D / 2;
-      const int64_t at = out_row * D + wg * HC;
-      const bool whole = (reinterpret_cast<uintptr_t>(DECODE ? a.ws_o : a.out) & 31) == 0;
-#pragma unroll 1
-      for (int oc = 0; oc < HC; oc += 32) {
-        uint32_t r[32];
-        tc::tmem_ld32(tl + uint32_t(Lo::O_COL + wg * HC + oc), r);
-        tc::tmem_ld_wait();
-        if (oc + 32 >= HC) {  // the next row tile's products may overwrite O
-          tc::tc_fence_before();
-          warp_arrive(BAR_OE);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
-        if (!valid) continue;
-        if (narrow) {
-          uint32_t h[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            h[e] = rxk::pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          bf16* dst = reinterpret_cast<bf16*>(a.out) + at + oc;
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) store_32(dst + 2 * e, &h[e], whole);
-        } else {
-          float* dst = (DECODE ? a.ws_o : a.out) + at + oc;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) store_32(dst + e, &r[e], whole);
-        }
-      }
-      if (valid && wg == 0)
-        (DECODE ? a.ws_lse : a.lse)[out_row] =
-            l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_all);
-    }
-    }
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -908,7 +951,8 @@ __global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
     decode_mod_tile_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  row_tiles<D, false, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas, a.n_tc_ctas);
+  row_tiles<D, false, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas,
+                                         a.n_tc_ctas);
 }
 
 // A warp a unit (an item and a KV head): unit blockIdx.x + gridDim.x * warp when
@@ -953,9 +997,9 @@ __global__ void __launch_bounds__(kPipeWarps * 32, 1)
   if (a.n_tc_ctas > 0) rxk::griddep_wait();
 }
 
-bool make_maps(Maps4* m, const rx_pool_desc* pool, int BN) {
+bool make_maps(Maps4* m, const rx_pool_desc* pool) {
   const CUtensorMap *k, *v, *k16, *v16;
-  if (!pool_maps(pool, BN, &k, &v)) return false;
+  if (!pool_maps(pool, 64, &k, &v)) return false;
   m->k = *k;
   m->v = *v;
   if (!pool_maps(pool, kGroup, &k16, &v16)) return false;
@@ -1021,7 +1065,7 @@ rx_status launch_extend(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas
   const rx_status cs = ensure_smem(configured, extend_mod_kernel<D, PAIR, CAP, SLOPES>, Lo::BYTES);
   if (cs != RX_OK) return cs;
   Maps4 maps;
-  if (!make_maps(&maps, pool, Lo::BS))
+  if (!make_maps(&maps, pool))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()) * (PAIR ? 2 : 1));
   extend_mod_kernel<D, PAIR, CAP, SLOPES><<<grid, Lo::THREADS, Lo::BYTES, s>>>(a, maps);
@@ -1056,10 +1100,11 @@ rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
                                      Layout4<D, false>::BYTES);
     if (cs != RX_OK) return cs;
     Maps4 maps;
-    if (!make_maps(&maps, pool, Layout4<D, false>::BS))
+    if (!make_maps(&maps, pool))
       return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+    using Lo = Layout4<D, false>;
     decode_mod_tile_kernel<D, CAP, SLOPES>
-        <<<unsigned(a.n_tc_ctas), Layout4<D, false>::THREADS, Layout4<D, false>::BYTES, s>>>(a, maps);
+        <<<unsigned(a.n_tc_ctas), Lo::THREADS, Lo::BYTES, s>>>(a, maps);
     const rx_status st = rx_internal::launch_status("rx_decode_attention_mod: tiles");
     if (st != RX_OK) return st;
   }

@@ -703,3 +703,38 @@ def test_slots_outside_the_pool_are_flagged_and_read_as_slot_0(d, bad):
                 slots[value == 0] = got
                 assert rx.device_check() == 0
             assert all(torch.equal(a, b) for a, b in zip(slots[True], slots[False]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("shape", ["climb", "fall", "swing", "spikes", "low"])
+def test_scores_that_move_by_hundreds_from_tile_to_tile(d, shape):
+    """Every row's largest score so far is overtaken (or left far behind) again and
+    again, within tiles of 64 keys and from one to the next, in some rows only."""
+    import torch
+    e = Extend([(900, 70), (0, 400)], 8, 2, d, seed=31, mag=0.2)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    n = torch.arange(970, device="cuda").float()
+    amp = {"climb": n * 0.9 - 400, "fall": 400 - n * 0.9,
+           "swing": 300 * torch.sign(torch.sin(n * (math.pi / 64))),
+           "spikes": torch.where(n % 97 == 11, n * 0.5, torch.zeros_like(n)) - 90,
+           "low": -600 + torch.randn(970, generator=g, device="cuda")}[shape]
+    # one direction of unit length carries the amplitudes; half of the rows look along
+    # it, one in four the other way, the rest hardly at all
+    u = torch.zeros(d, device="cuda")
+    u[:16] = 0.25
+    look = torch.tensor([1.0, 1.0, -1.0, 0.01], device="cuda").repeat(e.q.shape[0], 2)
+    q = e.q.float()
+    q[..., :16] = look[..., None] * 0.25 / e.scale
+    e.q = q.to(torch.bfloat16)
+    for r, (p, s) in enumerate(e.reqs):
+        slot = e.up(e.table[e.rows[r], :p + s]).long()
+        k = e.k[:, :, slot].float() * 0.1
+        k[..., :16] = (u[:16] * amp[:p + s, None])
+        e.k[:, :, slot] = k.to(torch.bfloat16)
+    slopes = torch.full((8,), 0.03, device="cuda")
+    for mod in (dict(), dict(window=300), dict(slopes=slopes), dict(softcap=500.0),
+                dict(softcap=200.0, slopes=slopes)):
+        out, lse = e.run(**mod)
+        assert rx.device_check() == 0
+        e.check(out, lse, **mod)
