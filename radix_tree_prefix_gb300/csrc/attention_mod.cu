@@ -51,6 +51,7 @@ constexpr int kGroup = 16;  // keys of a small TMA box
 // scores all lie 64 below a reference of 0 loses nothing of them (down to values of
 // 2^-60): what is raised or lowered are rows of extreme scores only.
 constexpr float kRaise = 64.f;
+constexpr float kMostSum = 18446744073709551616.f;  // 2^kRaise
 constexpr int kPairWindow = 2048;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
@@ -80,7 +81,7 @@ struct Layout4 {
   static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
   static constexpr int DESC = SUM + 3 * BM * 4;   // the row tile in hand and the next
   static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
-  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 9;
+  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 10;
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
@@ -98,6 +99,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 struct Maps4 {
   CUtensorMap k, v;      // boxes of 64 keys x 64 columns
   CUtensorMap k16, v16;  // boxes of 16 keys
+  CUtensorMap q;         // boxes of 128 rows: the heads of a group of 128 / group tokens
 };
 
 // 32 bytes at a 16-byte boundary, in one store at a 32-byte one.
@@ -110,6 +112,15 @@ __device__ __forceinline__ void store_32(void* dst, const uint32_t* r, bool whol
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
   }
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 
 // One lane of the warp, known to the compiler as such.
@@ -306,6 +317,21 @@ __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr
 #pragma unroll
     for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_fold2[d]);
 }
+// 2^sr in bf16, and their sum before the rounding.
+__device__ __forceinline__ float weights_of(const uint32_t (&sr)[32], uint32_t (&pk)[16]) {
+  float2 l4[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
+                                 rxk::fast_exp2(__uint_as_float(sr[e + 1])));
+    l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
+    pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
+  }
+  const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+  return lt.x + lt.y;
+}
 // Raw scores capped in place, in log2 units, less m.
 __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], bool near,
                                            float m) {
@@ -419,6 +445,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   using Lo = Layout4<D, PAIR>;
   constexpr int NW = Lo::NW, NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
+  constexpr bool DIRECT = !CAP && D == 128 && (SLOPES || !PAIR);
   static_assert(NW <= 3, "reference barriers and sums");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
   const uint32_t base = rxk::smem_addr(gbase);
@@ -440,6 +467,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   const uint32_t BAR_DF = BAR_QE + 8u;    // descriptors of even and odd row tiles: written,
   const uint32_t BAR_DE = BAR_DF + 16u;   // read
   const uint32_t BAR_END = BAR_DE + 16u;  // every product issued is done
+  const uint32_t BAR_QF = BAR_END + 8u;   // a row tile's Q has landed, where a box brings it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lo::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
   TileDesc* descs = reinterpret_cast<TileDesc*>(gbase + Lo::DESC);
@@ -461,6 +489,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       tc::mbar_init(BAR_DE + 8u * b, SW + 3);
     }
     tc::mbar_init(BAR_END, 2);  // one commit per issuing thread
+    tc::mbar_init(BAR_QF, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -550,6 +579,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
     float m_ref = valid ? -INFINITY : 0.f;  // reference of the row's weights, log2 units
     float l = 0.f;            // sum of this warpgroup's weights under it
+    bool easy = false;  // every row has a reference
     bool ok = true;
     int j = (wg + NW - g0 % NW) % NW;
     // tile j's buffer of P, and the phase of the buffer's barriers
@@ -595,60 +625,75 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         const bool masked = k0 + c < lo_max || k0 + c + 32 > lim_min;
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         uint32_t sr[32], pk[16];
+        float sum = 0.f;
         tc::tmem_ld32(p_col + uint32_t(c), sr);
         tc::tmem_ld_wait();
-        if constexpr (CAP) {
-          float am[4] = {0.f, 0.f, 0.f, 0.f};
+        // DIRECT: where every key is seen and every row has its reference, weights at
+        // once.  One beyond the reference's reach shows in their sum; then the scores,
+        // still in TMEM, are taken again step by step.  (At head_dim 128 agent calls with
+        // slopes take 344 us so and 361 without, unmodified ones 330 and 338, a prompt with
+        // slopes in a window of 1,024 144 and 155.  Under a cap, whose range has to be
+        // looked at before, 472 and 459; at head_dim 256 slopes 564 and 557; two CTAs an
+        // SM without slopes, documents, 98.6 and 97.4.)
+        bool done = false;
+        if constexpr (DIRECT) {
+          if (easy && !masked && (!SLOPES || behind)) {
+            if constexpr (SLOPES)
+              add_slopes(sr, a.scale_log2, rm.slope, float(k0 + c - rm.pos), true, m_use);
+            else
+              scale_scores(sr, a.scale_log2, m_use);
+            sum = weights_of(sr, pk);
+            done = __all_sync(0xffffffffu, !valid || sum <= kMostSum);
+            if (!done) {
+              tc::tmem_ld32(p_col + uint32_t(c), sr);
+              tc::tmem_ld_wait();
+            }
+          }
+        }
+        if (!done) {
+          if constexpr (CAP) {
+            float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
+                                           fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
+            const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+            cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near),
+                       SLOPES ? 0.f : m_use);
+          }
+          if constexpr (SLOPES)
+            add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind,
+                       m_use);
+          else if constexpr (!CAP)
+            scale_scores(sr, a.scale_log2, m_use);
+          if (masked) mask_scores(sr, rm.lo - (k0 + c), lim - (k0 + c));
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
-                                         fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
-          const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-          cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near),
-                     SLOPES ? 0.f : m_use);
-        }
-        if constexpr (SLOPES)
-          add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind,
-                     m_use);
-        else if constexpr (!CAP)
-          scale_scores(sr, a.scale_log2, m_use);
-        if (masked) mask_scores(sr, rm.lo - (k0 + c), lim - (k0 + c));
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
-                                         __uint_as_float(sr[e + 2 * u + 1])));
-        const float mx = valid ? fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) : 0.f;
-        const bool unset = m_ref == -INFINITY;
-        const bool grow = mx > (unset ? -INFINITY : kRaise);
-        if (__any_sync(0xffffffffu, grow)) {
-          // a row without a reference takes 0 if its scores are about that (tiles of other
-          // warpgroups that meet the row first then agree)
-          const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
-          if (grow) m_ref = m_use + by;
-          const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
-          l *= f;
-          if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
-          if (__any_sync(0xffffffffu, by != 0.f))
-            scale_scores(sr, 1.f, by);
-        }
-        float2 l4[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 p = make_float2(rxk::fast_exp2(__uint_as_float(sr[e])),
-                                       rxk::fast_exp2(__uint_as_float(sr[e + 1])));
-          l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
-          pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
+              mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
+                                           __uint_as_float(sr[e + 2 * u + 1])));
+          const float mx = valid ? fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) : 0.f;
+          const bool unset = m_ref == -INFINITY;
+          const bool grow = mx > (unset ? -INFINITY : kRaise);
+          if (__any_sync(0xffffffffu, grow)) {
+            // a row without a reference takes 0 if its scores are about that (tiles of other
+            // warpgroups that meet the row first then agree)
+            const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
+            if (grow) m_ref = m_use + by;
+            const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
+            l *= f;
+            if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
+            if (__any_sync(0xffffffffu, by != 0.f)) scale_scores(sr, 1.f, by);
+          }
+          sum = weights_of(sr, pk);
+          if constexpr (DIRECT) easy = !__any_sync(0xffffffffu, m_ref == -INFINITY);
         }
         tmem_st16(p_col + uint32_t(c / 2), pk);
-        const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
-        l += lt.x + lt.y;
+        l += sum;
       }
       tc::tmem_st_wait();
       // ---- the row's reference: that of tile g - 1 unless O has to be raised
@@ -799,7 +844,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const uint32_t q_lo = ((sQ & 0x3FFFFu) >> 4) | (1u << 16);
     const uint32_t k_lo0 = (((base + Lo::K0) & 0x3FFFFu) >> 4) | (1u << 16);
     int sk = 0, sb = 0, count = 0, used = 0;  // used: row tiles with keys so far
-    uint32_t k_phase = 0, b_phase = 1;
+    uint32_t k_phase = 0, b_phase = 1, q_phase = 0;
     bool ok = true;
 #pragma unroll 1
     for (int k = 0, c = first; ok && c < total; ++k, c += step) {
@@ -807,33 +852,48 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       if (!read_desc(k, t)) break;
       const int n_loads = loads_of(t);
       if (n_loads == 0) continue;
-      // Q rows into shared memory once the last row tile's products have read
-      // theirs (zeros past the tile's rows): a lane finds four rows, and the warp
-      // copies whole rows, whose pieces lie together
+      // Q rows into shared memory once the last row tile's products have read theirs: a
+      // whole tile by a box per 64 columns, else gathered (zeros past the tile's rows; a
+      // lane finds four rows, and the warp copies whole rows, whose pieces lie together)
       if (used > 0 && !warp_wait(BAR_QE, uint32_t(used - 1) & 1u, abort_flag)) break;
       ++used;
-      constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows an instruction
+      if (!DECODE && a.q_boxes && t.n_rows == BM) {
+        if (lane == 0) tc::mbar_arrive_expect_tx(BAR_QF, uint32_t(BM * D * 2));
+        __syncwarp();
+        if (lane < D / 64)
+          tma_load_3d(sQ + uint32_t(lane * BM * 128), &maps.q, lane * 64, t.kvh * a.group,
+                      t.q_base + over_group<true>(a, t.gr0), BAR_QF);
+        if (!warp_wait(BAR_QF, q_phase, abort_flag)) {
+          // (it has landed before the CTA gives up its shared memory)
+          int drain_abort = 0;
+          tc::mbar_wait(BAR_QF, q_phase, &drain_abort, kWaitLimit);
+          break;
+        }
+        q_phase ^= 1u;
+      } else {
+        constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows an instruction
 #pragma unroll 1
-      for (int r0 = 0; r0 < BM; r0 += 32) {
-        const bf16* src = nullptr;
-        if (r0 + lane < t.n_rows) {
-          int64_t qi = 0, part = 0;
-          int head = 0, lim = 0;
-          row_info<DECODE, true>(a, t, t.kvh, r0 + lane, qi, head, part, lim);
-          src = a.q + (qi * a.hq + head) * D;
+        for (int r0 = 0; r0 < BM; r0 += 32) {
+          const bf16* src = nullptr;
+          if (r0 + lane < t.n_rows) {
+            int64_t qi = 0, part = 0;
+            int head = 0, lim = 0;
+            row_info<DECODE, true>(a, t, t.kvh, r0 + lane, qi, head, part, lim);
+            src = a.q + (qi * a.hq + head) * D;
+          }
+#pragma unroll
+          for (int r = 0; r < 32; r += RPI) {
+            const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(
+                0xffffffffu, reinterpret_cast<unsigned long long>(src), r + lane / CPR));
+            rxk::cp_async_16(sw128(sQ, BM, r0 + r + lane / CPR, lane % CPR),
+                             (from ? from : a.q) + lane % CPR * 8, from != nullptr);
+          }
         }
-#pragma unroll 8
-        for (int r = 0; r < 32; r += RPI) {
-          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(
-              0xffffffffu, reinterpret_cast<unsigned long long>(src), r + lane / CPR));
-          rxk::cp_async_16(sw128(sQ, BM, r0 + r + lane / CPR, lane % CPR),
-                           (from ? from : a.q) + lane % CPR * 8, from != nullptr);
-        }
+        rxk::cp_async_commit();
+        rxk::cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
       }
-      rxk::cp_async_commit();
-      rxk::cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
       if (elect_one()) {
         const uint32_t idesc = t.n_rows <= 64 ? tc::idesc_bf16(64, BS, 0)
                                               : tc::idesc_bf16(BM, BS, 0);
@@ -1008,6 +1068,21 @@ bool make_maps(Maps4* m, const rx_pool_desc* pool) {
   return true;
 }
 
+// Boxes over the queries: whole tiles only are read by them, whose tokens all exist, so
+// the map need not know how many there are.  Groups that do not divide a tile have none.
+bool make_q_map(CUtensorMap* m, const TcArgs& a, int D) {
+  if (BM % a.group != 0) return false;
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(a.hq), cuuint64_t(INT32_MAX)};
+  const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(a.hq) * D * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(a.group), cuuint32_t(BM / a.group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(a.q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* d_q,
                 int32_t num_q_heads, const int32_t* table, int64_t row_stride, float scale,
                 const rx_score_mod& m) {
@@ -1059,7 +1134,7 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
 }
 
 template <int D, bool PAIR, bool CAP, bool SLOPES>
-rx_status launch_extend(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
+rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
   using Lo = Layout4<D, PAIR>;
   static std::atomic<bool> configured[kMaxDevices];
   const rx_status cs = ensure_smem(configured, extend_mod_kernel<D, PAIR, CAP, SLOPES>, Lo::BYTES);
@@ -1067,6 +1142,7 @@ rx_status launch_extend(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas
   Maps4 maps;
   if (!make_maps(&maps, pool))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+  a.q_boxes = make_q_map(&maps.q, a, D);
   const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()) * (PAIR ? 2 : 1));
   extend_mod_kernel<D, PAIR, CAP, SLOPES><<<grid, Lo::THREADS, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");

@@ -116,6 +116,7 @@ struct TcArgs {
   const int32_t* bidir_end;
   const int32_t* ctx_len;
   int out_bf16;
+  int q_boxes;             // Q's whole row tiles are loaded by boxes
   int hkv;
   Div by_group, by_hkv;    // division by them
 };
