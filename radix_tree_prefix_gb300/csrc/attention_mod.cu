@@ -52,7 +52,7 @@ constexpr int kGroup = 16;  // keys of a small TMA box
 // 2^-60): what is raised or lowered are rows of extreme scores only.
 constexpr float kRaise = 64.f;
 constexpr float kMostSum = 18446744073709551616.f;  // 2^kRaise
-constexpr int kPairWindow = 2048;  // widest window for two CTAs an SM
+constexpr int kPairWindow = 1024;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
 // 128: one of 64 keys reads Q's 16 columns from shared memory for half the
@@ -511,9 +511,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   };
   // Loads of BS keys, and tiles of BN among them that hold keys.  With slopes the
   // loads go from the newest keys back: scores fall with distance, so a row's first
-  // maximum is about its last, where it would rise with almost every tile the
-  // other way round (an agent loop's calls under slopes of 2^(-8 h / 32): 639 us
-  // forwards, 418).
+  // reference is its last, where the other way round almost every tile would raise it
+  // (an agent loop's calls under slopes of 2^(-8 h / 32): 810 us forwards, 344).
   auto loads_of = [](const TileDesc& t) {
     return t.key_lo >= t.key_end ? 0 : (t.key_end - t.key_begin + BS - 1) / BS;
   };
@@ -1152,9 +1151,10 @@ template <int D, bool CAP, bool SLOPES>
 rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
   // Row tiles of few keys, one after another in a CTA, are bound by the way from one
-  // to the next, which a second CTA on the SM fills (a prompt in a window of 1,024
-  // 179 us and 150, documents of 400 tokens 124 and 113); over long ranges, and under
-  // a cap, one CTA with deeper rings is faster (agent calls 380 and 399, 511 and 566).
+  // to the next, which a second CTA on the SM fills (agent calls in a window of 128
+  // 75 us and 56, of 512 108 and 101, documents of 400 tokens 100 and 97); over longer
+  // ranges one CTA with deeper rings is faster (a window of 2,048 251 and 275, of 3,000
+  // 324 and 383), and under a cap always (a prompt in a window of 1,024 196 and 205).
   if constexpr (D == 128 && !CAP)
     if (a.key_begin || (a.window > 0 && a.window <= kPairWindow))
       return launch_extend<D, true, CAP, SLOPES>(a, pool, ctas, s);
