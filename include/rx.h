@@ -910,8 +910,9 @@ typedef struct rx_score_mod {
  * weights are rounded to bf16 for the product with V.  A tile of 128 query
  * rows (rx_extend_plan) reads the keys from the first to the last that one of
  * its rows sees; their V rows must be finite (a masked key weighs 0, and 0 times
- * an infinity would reach the tile's other queries), their K rows need not
- * be where they are masked.  d_ctx_len is not read.  Errors: RX_ERR_INVALID
+ * an infinity would reach the tile's other queries) and at most 2^40 in magnitude
+ * (a weight stands under a reference that it may exceed by 2^64), their K rows need
+ * not be finite where they are masked.  d_ctx_len is not read.  Errors: RX_ERR_INVALID
  * as rx_extend_attention, for an unknown out_type, a softcap out of range,
  * window < 0, a scale not in [2^-40, 2^40]. */
 rx_status rx_extend_attention_mod(
@@ -944,7 +945,7 @@ rx_status rx_plan_decode_window(const rx_cache* cache, int32_t B,
  * several (else 0); its tokens must be stored first.  d_key_begin is [B];
  * d_bidir_end is not read (every key of a context lies before its query).
  * d_ctx_len is needed with a window or slopes.  The V rows of the plan's keys
- * must be finite.  Numerics as rx_extend_attention_mod.  Errors:
+ * must be finite and at most 2^40.  Numerics as rx_extend_attention_mod.  Errors:
  * RX_ERR_INVALID as rx_decode_attention and rx_extend_attention_mod, for
  * step < 0 and a missing d_ctx_len. */
 rx_status rx_decode_attention_mod(
@@ -1098,7 +1099,8 @@ rx_status rx_host_free(void* p);
 
 /* Synchronise the current device and read the kernels' error words (then
  * clear them).  *out_flags (may be NULL): bit 0 = rx_kv_store, rx_qkv_store,
- * rx_kv8_store or rx_kv8_load met a slot outside [1, num_slots) and skipped it; bit 1 = an attention kernel
+ * rx_kv8_store or rx_kv8_load met a slot outside [1, num_slots) and skipped it;
+ * bit 1 = an attention kernel
  * read a slot outside [0, num_slots) from req_to_token and used slot 0
  * instead; bit 2 = a tensor-core kernel gave up a barrier wait after its
  * time limit (about 2 s) and returned without results (every output of

@@ -576,7 +576,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
     const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
-    float m_ref = valid ? -INFINITY : 0.f;  // reference of the row's weights, log2 units
+    // reference of the row's weights, log2 units
+    float m_ref = valid ? (CAP && !SLOPES ? a.cap_ref : -INFINITY) : 0.f;
+    // no score can leave its reach, and the tiles need not agree on it
+    const bool bounded = CAP && !SLOPES && a.cap_ref > -INFINITY;
     float l = 0.f;            // sum of this warpgroup's weights under it
     bool easy = false;  // every row has a reference
     bool ok = true;
@@ -597,12 +600,12 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       if (j >= n_tiles) {
         // the half of the last load without keys; it takes its turn all the same, so
         // that no barrier is arrived at before its last phase is done
-        if (!warp_wait(h_before, h_parity, abort_flag) ||
+        if ((!bounded && !warp_wait(h_before, h_parity, abort_flag)) ||
             (g >= NB && !warp_wait(BAR_PF + 8u * uint32_t(s), phase ^ 1u, abort_flag))) {
           ok = false;
           break;
         }
-        warp_arrive(h_bar);
+        if (!bounded) warp_arrive(h_bar);
         warp_arrive(BAR_P + 8u * s);
         continue;
       }
@@ -668,25 +671,27 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           else if constexpr (!CAP)
             scale_scores(sr, a.scale_log2, m_use);
           if (masked) mask_scores(sr, rm.lo - (k0 + c), lim - (k0 + c));
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (!bounded) {
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
+            for (int e = 0; e < 32; e += 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
-                                           __uint_as_float(sr[e + 2 * u + 1])));
-          const float mx = valid ? fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) : 0.f;
-          const bool unset = m_ref == -INFINITY;
-          const bool grow = mx > (unset ? -INFINITY : kRaise);
-          if (__any_sync(0xffffffffu, grow)) {
-            // a row without a reference takes 0 if its scores are about that (tiles of other
-            // warpgroups that meet the row first then agree)
-            const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
-            if (grow) m_ref = m_use + by;
-            const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
-            l *= f;
-            if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
-            if (__any_sync(0xffffffffu, by != 0.f)) scale_scores(sr, 1.f, by);
+              for (int u = 0; u < 4; ++u)
+                mx4[u] = fmaxf(mx4[u], fmaxf(__uint_as_float(sr[e + 2 * u]),
+                                             __uint_as_float(sr[e + 2 * u + 1])));
+            const float mx = valid ? fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) : 0.f;
+            const bool unset = m_ref == -INFINITY;
+            const bool grow = mx > (unset ? -INFINITY : kRaise);
+            if (__any_sync(0xffffffffu, grow)) {
+              // a row without a reference takes 0 if its scores are about that (tiles of other
+              // warpgroups that meet the row first then agree)
+              const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
+              if (grow) m_ref = m_use + by;
+              const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
+              l *= f;
+              if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
+              if (__any_sync(0xffffffffu, by != 0.f)) scale_scores(sr, 1.f, by);
+            }
           }
           sum = weights_of(sr, pk);
           if constexpr (DIRECT) easy = !__any_sync(0xffffffffu, m_ref == -INFINITY);
@@ -696,7 +701,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       }
       tc::tmem_st_wait();
       // ---- the row's reference: that of tile g - 1 unless O has to be raised
-      if (j > 0) {
+      if (j > 0 && !bounded) {
         if (!warp_wait(h_before, h_parity, abort_flag)) {
           ok = false;
           break;
@@ -737,8 +742,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
       }
       // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
-      ref[(g & 1) * BM + i] = m_ref;
-      warp_arrive(h_bar);
+      if (!bounded) {
+        ref[(g & 1) * BM + i] = m_ref;
+        warp_arrive(h_bar);
+      }
       tc::tc_fence_before();
       warp_arrive(BAR_P + 8u * s);
     }
@@ -746,7 +753,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     // warpgroups bring their sums there and exchange them.
     if (!ok || !warp_wait(BAR_FIN, uint32_t(used) & 1u, abort_flag)) break;
     tc::tc_fence_after();
-    const float m_fin = ref[((g0 + n_tiles - 1) & 1) * BM + i];
+    const float m_fin = bounded ? m_ref : ref[((g0 + n_tiles - 1) & 1) * BM + i];
     sums[wg * BM + i] = m_ref == -INFINITY ? 0.f : l * rxk::fast_exp2(m_ref - m_fin);
     warp_arrive(BAR_X);
     if (!warp_wait(BAR_X, uint32_t(used) & 1u, abort_flag)) break;
@@ -1122,6 +1129,9 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
       a->cap_fold2[i] = make_float2(f, f);
     }
     a->cap_near = float(u / double(a->cap_in));
+    // Capped scores lie within +-cap_out: where their weights under one reference stay
+    // within 2^-88 and 2^kRaise, that is every row's, and no maximum is taken.
+    a->cap_ref = a->cap_out <= 76.f ? fmaxf(0.f, ceilf(a->cap_out) - kRaise) : -INFINITY;
   }
   a->window = m.window;
   a->slopes = m.d_slopes;

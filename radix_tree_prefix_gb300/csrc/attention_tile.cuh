@@ -110,6 +110,7 @@ struct TcArgs {
   float2 cap_fold2[5];     // of kTanhNear with cap_in and cap_out in it, twice: a raw
   float cap_near;          // score of at most this magnitude times a polynomial in its
                            // square
+  float cap_ref;           // the reference of every row's weights, or -inf: none fits
   int window;              // 0: none
   const float* slopes;
   const int32_t* key_begin;

@@ -13,7 +13,7 @@
 // position (the fraction's own error is 2^-52 of f_i: 2^-23 of a turn at
 // position 2^31).  Only the turn's fraction goes to fp32, and its sine and
 // cosine are taken within half a turn, where the special-function unit is
-// good to 2^-20.5, far below a bf16 rounding (2^-9).  No table of angles is
+// good to 2^-20.5, far below a bf16 rounding (2^-8).  No table of angles is
 // read and no position is too far.
 //
 // Bound by HBM: every row is read once and written once.  A thread holds the
@@ -42,7 +42,6 @@
 static __device__ int32_t g_rope_error;
 
 namespace {
-
 
 struct RopeArgs {
   rx_rope rope;
