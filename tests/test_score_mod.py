@@ -738,3 +738,25 @@ def test_scores_that_move_by_hundreds_from_tile_to_tile(d, shape):
         out, lse = e.run(**mod)
         assert rx.device_check() == 0
         e.check(out, lse, **mod)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softcap", [1.0, 44.0, 52.6, 52.8, 90.0])
+@pytest.mark.parametrize("d", [128, 256])
+def test_caps_that_scores_reach(d, softcap):
+    """Scores at both ends of the cap, in extend and in decode's tiles and streams, at caps
+    around 76 ln 2, up to which every row's weights stand under one reference."""
+    import torch
+    e = Extend([(300, 70), (0, 200)], 8, 2, d, seed=5, mag=2.0 * softcap)
+    for sign in (1, -1):
+        # (the first request's rows see nothing but one end)
+        e.k[:, :, :, 0] = sign * e.k[:, :, :, 0].abs().clamp(min=0.5)
+        e.q[:70, :, 0] = 8 * softcap
+        for kw in (dict(softcap=softcap), dict(softcap=softcap, window=90)):
+            out, lse = e.run(**kw)
+            assert rx.device_check() == 0
+            e.check(out, lse, **kw)
+    c = Decode([40 + 3 * i for i in range(37)], 700, 8, 2, d, seed=1, mag=2.0 * softcap)
+    out, lse = c.run(softcap=softcap)
+    assert rx.device_check() == 0
+    c.check(out, lse, softcap=softcap)
