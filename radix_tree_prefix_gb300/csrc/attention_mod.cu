@@ -22,7 +22,8 @@
 //                TMEM) to m, whichever is smaller; then m goes on to tile j + 1.  Both
 //                are rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
 //                and a score may exceed it by 64, so that nothing but such a row ever
-//                stops for another tile.  Each warpgroup keeps the row sums of its own
+//                stops for another tile.  (Under a cap of at most 52 m is one number, and
+//                nothing is handed on.)  Each warpgroup keeps the row sums of its own
 //                tiles; they meet in the row tile's end;
 //   then warp S  Q rows, and S_j = Q K_j^T into a ring of TMEM buffers;
 //   K, V         loaders, the K loader also finding row tiles and their key ranges for
@@ -36,10 +37,15 @@
 // score is -inf; a row that has seen no key yet has m = -inf and weighs its masked
 // keys 0, and one that never sees any gets o = 0, lse = -inf.
 //
-// What bounds it is the softmax warps' instructions, and fetching them: 64 rows' keys
-// take some 400 instructions a warp without a cap and 700 with one, at a little more
-// than half an issue slot a clock.  The loops are rolled, and the softmax role stands
-// first in the kernel (agent calls under a cap 458 us, behind the other roles 506).
+// What bounds it is the softmax warps' instructions, and fetching them: a tile takes
+// some 400 of a warp without a cap and 600 with one, at a little more than half an
+// issue slot a clock.  The loops are rolled, and the softmax role stands first in the
+// kernel (behind the other roles agent calls under a cap took 506 us, so 458).  At
+// head_dim 256 it is shared memory's bandwidth and V's ring of two tiles.  One GB300,
+// 40 calls of 200 queries over 3,000 common keys, 32 / 8 heads of 128: 330 us without
+// modification (1,240 TFLOP/s), 344 with slopes, 434 under a cap; 64 chat turns of 200
+// queries over 2,000 to 3,800 keys, 16 / 4 heads of 256, pages of 16, slopes: 556 us
+// (1,100 TFLOP/s).
 
 #include "attention_tile.cuh"
 
