@@ -18,9 +18,9 @@
 //                into TMEM over scores read already, under the reference m that the
 //                warpgroup used last.  At the tile's end the reference of tile j - 1
 //                comes from the warpgroup before through shared memory (barrier H):
-//                if m is another, this tile's weights are brought to it, or O (in
-//                TMEM) to m, whichever is smaller; then m goes on to tile j + 1.  Both
-//                are rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
+//                if it is larger, this tile's weights are brought down to it, if it
+//                is smaller, O (in TMEM) to m, and m goes on to tile j + 1.  Both are
+//                rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
 //                and a score may exceed it by 64, so that nothing but such a row ever
 //                stops for another tile.  (Under a cap of at most 52 m is one number, and
 //                nothing is handed on.)  Each warpgroup keeps the row sums of its own

@@ -324,6 +324,33 @@ __device__ __forceinline__ float capped(const TcArgs& a, float s) {
   return u * p;
 }
 
+// capped of a lane's scores, all of a warp's the same way: branches for each one would
+// put their chains one behind the other.
+__device__ __forceinline__ void cap_all(const TcArgs& a, float (&x)[2][4]) {
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i >> 2][i & 3]));
+  if (__all_sync(0xffffffffu, most * a.cap_in <= 1.f)) {
+    float u[8], v[8], p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = x[i >> 2][i & 3] * a.cap_in;
+      v[i] = u[i] * u[i];
+      p[i] = a.cap_poly[kTanhTerms - 1];
+    }
+#pragma unroll
+    for (int d = kTanhTerms - 2; d >= 0; --d)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = fmaf(p[i], v[i], a.cap_poly[d]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = u[i] * p[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i >> 2][i & 3] = a.cap_out * tanh_exp(x[i >> 2][i & 3] * a.cap_in);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Warp role of the fused decode kernel: work items of <= 16 query rows at
 // head_dim 128, <= 8 at 256 (a request's private tail, or a shared segment
@@ -562,6 +589,119 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
   const uint32_t v_lane =
       uint32_t((16 + (lane & 7) + (lane >> 4) * 8) * kRowPitch + ((lane >> 3) & 1) * 16);
 
+  // Two steps at a time where the ring has the stages and rows the registers: a step's
+  // products, modification and exponentials are chains of some 1,200 cycles that hardly
+  // fill a warp's issue slots, two together take little more than one.
+  constexpr bool TWO = MOD && NR == 1 && S >= 4;
+  if constexpr (TWO) {
+#pragma unroll 1
+    for (int st = 0; st < n_steps; st += 2) {
+      if (st <= 4) next_unit_step<SLOPES, MOD>(a, nxt);
+      // (its stage was read in the last round)
+      if (st + S - 1 < n_steps) issue(st + S - 1);
+      rxk::cp_async_commit();
+      rxk::cp_async_wait<S - 2>();
+      __syncwarp();
+      const bool two = st + 1 < n_steps;
+      uint32_t stage[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        stage[u] = ring + ((gstep + uint32_t(st + u)) % S) * kStageBytes;
+      float sacc[2][4], sodd[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sacc[u][e] = sodd[u][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a0, a1, a2, a3;
+          rxk::ldsm_x4(stage[u] + k_lane + uint32_t(kk * 32), a0, a1, a2, a3);
+          rxk::mma_bf16((kk & 1) ? sodd[u] : sacc[u], a0, a1, a2, a3, qb[0][kk][0], qb[0][kk][1]);
+        }
+      float x[2][4];
+      bool grow = false;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // (what an absent step's stage holds decides nothing)
+          x[u][e] = u == 0 || two ? sacc[u][e] + sodd[u][e] : 0.f;
+      if constexpr (CAP)
+        cap_all(a, x);
+      else
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] *= a.scale_log2;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int key0 = SLOPES ? ke - 1 - ((st + u) * 16 + g) : kb + (st + u) * 16 + g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = SLOPES ? key0 - 8 * (e >> 1) : key0 + 8 * (e >> 1);
+          const RowMod& r = rm[0][e & 1];
+          float y = x[u][e];
+          if constexpr (SLOPES) y = fmaf(-r.slope, fabsf(float(key - r.pos)), y);
+          x[u][e] = key >= max(kb, r.lo) && key < ke ? y : -INFINITY;
+          grow |= x[u][e] > m_ref[0][e & 1] + kRescaleThreshold;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          if (mx > m_ref[0][e]) {
+            const float alpha = rxk::fast_exp2(m_ref[0][e] - mx);  // 0 from -inf
+            m_ref[0][e] = mx;
+            l_run[0][e] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < NK; ++mt) {
+              o[0][mt][e] *= alpha;
+              o[0][mt][2 + e] *= alpha;
+            }
+          }
+        }
+      }
+      uint32_t pb[2][2];
+      const int src1 = 8 * c + (g >> 1), src2 = src1 + 4;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t pk[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m_use = m_ref[0][e] == -INFINITY ? 0.f : m_ref[0][e];
+          const float p0 = rxk::fast_exp2(x[u][e] - m_use);
+          const float p1 = rxk::fast_exp2(x[u][2 + e] - m_use);
+          pk[e] = rxk::pack_bf16(p0, p1);
+          l_run[0][e] += p0 + p1;
+        }
+        const uint32_t v0 = __shfl_sync(0xffffffffu, pk[0], src1);
+        const uint32_t v1 = __shfl_sync(0xffffffffu, pk[1], src1);
+        const uint32_t w0 = __shfl_sync(0xffffffffu, pk[0], src2);
+        const uint32_t w1 = __shfl_sync(0xffffffffu, pk[1], src2);
+        const uint32_t s1 = (g & 1) ? v1 : v0, s2 = (g & 1) ? w1 : w0;
+        pb[u][0] = __byte_perm(s1, s2, 0x5410);
+        pb[u][1] = __byte_perm(s1, s2, 0x7632);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u == 1 && !two) break;  // (nothing was loaded there)
+#pragma unroll
+        for (int mt = 0; mt < NK; ++mt) {
+          uint32_t a0, a1, a2, a3;
+          rxk::ldsm_x4_t(stage[u] + v_lane + uint32_t(mt * 32), a0, a1, a2, a3);
+          rxk::mma_bf16(o[0][mt], a0, a1, a2, a3, pb[u][0], pb[u][1]);
+        }
+      }
+      __syncwarp();  // every lane is done with these stages before they are refilled
+      if (st + S < n_steps) issue(st + S);
+      rxk::cp_async_commit();
+    }
+  } else {
 #pragma unroll 1
   for (int st = 0; st < n_steps; ++st) {
     // the next unit: index at step 0, work words at step 2, slots at step 4
@@ -693,6 +833,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     __syncwarp();  // every lane is done with this stage before it is refilled
     if (st + S - 1 < n_steps) issue(st + S - 1);
     rxk::cp_async_commit();
+  }
   }
   rxk::cp_async_wait<0>();
   __syncwarp();
