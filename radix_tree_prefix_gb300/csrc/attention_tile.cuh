@@ -313,27 +313,17 @@ constexpr float kTanhNear[kTanhNearTerms] = {0.99999994f, -0.3333231f, 0.1331017
 __device__ __forceinline__ float tanh_exp(float u) {
   return fmaf(-2.f, __fdividef(1.f, 1.f + rxk::fast_exp2(u * (2.f * kLog2e))), 1.f);
 }
-// softcap * tanh(scale * s / softcap) * log2(e)
-__device__ __forceinline__ float capped(const TcArgs& a, float s) {
-  const float u = s * a.cap_in;
-  if (fabsf(u) > 1.f) return a.cap_out * tanh_exp(u);
-  const float v = u * u;
-  float p = a.cap_poly[kTanhTerms - 1];
-#pragma unroll
-  for (int i = kTanhTerms - 2; i >= 0; --i) p = fmaf(p, v, a.cap_poly[i]);
-  return u * p;
-}
-
-// capped of a lane's scores, all of a warp's the same way: branches for each one would
-// put their chains one behind the other.
-__device__ __forceinline__ void cap_all(const TcArgs& a, float (&x)[2][4]) {
+// softcap * tanh(scale * s / softcap) * log2(e) of a lane's scores, all of a warp's the
+// same way: branches for each one would put their chains one behind the other.
+template <int N>
+__device__ __forceinline__ void cap_all(const TcArgs& a, float (&x)[N][4]) {
   float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i >> 2][i & 3]));
+  for (int i = 0; i < 4 * N; ++i) most = fmaxf(most, fabsf(x[i >> 2][i & 3]));
   if (__all_sync(0xffffffffu, most * a.cap_in <= 1.f)) {
-    float u[8], v[8], p[8];
+    float u[4 * N], v[4 * N], p[4 * N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4 * N; ++i) {
       u[i] = x[i >> 2][i & 3] * a.cap_in;
       v[i] = u[i] * u[i];
       p[i] = a.cap_poly[kTanhTerms - 1];
@@ -341,12 +331,12 @@ __device__ __forceinline__ void cap_all(const TcArgs& a, float (&x)[2][4]) {
 #pragma unroll
     for (int d = kTanhTerms - 2; d >= 0; --d)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = fmaf(p[i], v[i], a.cap_poly[d]);
+      for (int i = 0; i < 4 * N; ++i) p[i] = fmaf(p[i], v[i], a.cap_poly[d]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = u[i] * p[i];
+    for (int i = 0; i < 4 * N; ++i) x[i >> 2][i & 3] = u[i] * p[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4 * N; ++i)
       x[i >> 2][i & 3] = a.cap_out * tanh_exp(x[i >> 2][i & 3] * a.cap_in);
   }
 }
@@ -737,6 +727,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
     const bool in0 = SLOPES ? key0 >= kb : key0 < ke, in1 = SLOPES ? key0 - 8 >= kb : key0 + 8 < ke;
     float x[NR][4];
     bool grow = false;
+    if constexpr (CAP) cap_all(a, sacc);
 #pragma unroll
     for (int nt = 0; nt < NR; ++nt) {
       if constexpr (MOD) {
@@ -744,7 +735,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
         for (int e = 0; e < 4; ++e) {
           const int key = SLOPES ? key0 - 8 * (e >> 1) : key0 + 8 * (e >> 1);
           const RowMod& r = rm[nt][e & 1];
-          float y = CAP ? capped(a, sacc[nt][e]) : sacc[nt][e] * a.scale_log2;
+          float y = CAP ? sacc[nt][e] : sacc[nt][e] * a.scale_log2;
           if constexpr (SLOPES) y = fmaf(-r.slope, fabsf(float(key - r.pos)), y);
           x[nt][e] = (e >> 1 ? in1 : in0) && key >= r.lo ? y : -INFINITY;
         }
