@@ -42,10 +42,10 @@
 // issue slot a clock.  The loops are rolled, and the softmax role stands first in the
 // kernel (behind the other roles agent calls under a cap took 506 us, so 458).  At
 // head_dim 256 it is shared memory's bandwidth and V's ring of two tiles.  One GB300,
-// 40 calls of 200 queries over 3,000 common keys, 32 / 8 heads of 128: 330 us without
-// modification (1,240 TFLOP/s), 344 with slopes, 434 under a cap; 64 chat turns of 200
-// queries over 2,000 to 3,800 keys, 16 / 4 heads of 256, pages of 16, slopes: 556 us
-// (1,100 TFLOP/s).
+// 40 calls of 200 queries over 3,000 common keys, 32 / 8 heads of 128: 324 us without
+// modification (1,260 TFLOP/s), 339 with slopes, 425 under a cap; 64 chat turns of 200
+// queries over 2,000 to 3,800 keys, 16 / 4 heads of 256, pages of 16, slopes: 550 us
+// (1,115 TFLOP/s).
 
 #include "attention_tile.cuh"
 
@@ -85,9 +85,10 @@ struct Layout4 {
   static constexpr int V0 = K0 + NK * KV_BYTES;
   static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
   static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
-  static constexpr int DESC = SUM + 3 * BM * 4;   // the row tile in hand and the next
+  static constexpr int NEXT = SUM + 3 * BM * 4;   // answer to a request for another row tile
+  static constexpr int DESC = NEXT + 16;          // the row tile in hand and the next
   static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
-  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 10;
+  static constexpr int NBAR = 2 * NK + 2 * NV + NS + 2 * NB + 4 * NH + 11;
   static constexpr int MISC = BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int O_COL = NB * BN;
@@ -127,6 +128,28 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+// Asks for a CTA of the grid that has not started, to be run by this one in its place
+// (16 bytes of answer at dst, 16-byte aligned); not to be asked again after a refusal.
+__device__ __forceinline__ void ask_next(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];\n" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// Its index, -1: none is left.
+__device__ __forceinline__ int next_tile(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}\n"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
 }
 
 // One lane of the warp, known to the compiler as such.
@@ -438,16 +461,19 @@ __device__ __forceinline__ void scale_weights(uint32_t taddr, float f) {
   tc::tmem_st_wait();
 }
 
-// A CTA's row tiles first, first + step, .. below total, one after another: the
-// loaders and the issuing warps run ahead into the next row tile while the softmax
-// warps finish one and write it.  (One CTA a row tile left its SM idle for some 9
-// us of start and end: a prompt of 8,191 in a window of 1,024 took 253 us.)
+// A CTA's row tiles one after another: `first`, and (extend) whatever CTAs of the grid
+// have not started when its K loader asks for another, so that tiles of different
+// lengths spread over the SMs without a counter (dealt out in turn, agent calls under a
+// cap took 434 us, so 425, a prompt of 8,191 395 and 375, documents 97 and 95; row tiles
+// of four key tiles, a window of 200, 60 and 64).  The loaders and the issuing warps run
+// ahead into the next row tile while the softmax warps finish one and write it.  (One CTA
+// a row tile left its SM idle for some 9 us of start and end.)
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
 template <int D, bool PAIR, bool DECODE, bool CAP, bool SLOPES>
 __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
-                                          int first, int step, int total) {
+                                          int first) {
   using Lo = Layout4<D, PAIR>;
   constexpr int NW = Lo::NW, NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
@@ -474,6 +500,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   const uint32_t BAR_DE = BAR_DF + 16u;   // read
   const uint32_t BAR_END = BAR_DE + 16u;  // every product issued is done
   const uint32_t BAR_QF = BAR_END + 8u;   // a row tile's Q has landed, where a box brings it
+  const uint32_t BAR_NEXT = BAR_QF + 8u;  // the answer to a request for another row tile has
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Lo::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + Lo::MISC + 4);
   TileDesc* descs = reinterpret_cast<TileDesc*>(gbase + Lo::DESC);
@@ -496,6 +523,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     }
     tc::mbar_init(BAR_END, 2);  // one commit per issuing thread
     tc::mbar_init(BAR_QF, 1);
+    tc::mbar_init(BAR_NEXT, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -537,9 +565,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     int g0 = 0;    // the row tile's first tile among all of the CTA's
     int used = 0;  // row tiles with keys before it
 #pragma unroll 1
-    for (int k = 0, c = first; c < total; ++k, c += step) {
+    for (int k = 0;; ++k) {
     TileDesc t;
-    if (!read_desc(k, t)) break;
+    if (!read_desc(k, t) || t.kvh < 0) break;
     const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
     // the tile row in lane i: row i, or with M = 64 products (at most 64 rows) row
     // 16 (i / 32) + i % 16 in the first 16 lanes of each quadrant
@@ -808,31 +836,55 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     // ------------------------------------------------------------- loaders
     const bool v = warp == SW + 2;
     Ring ring;
-    bool ok = true;
+    int c = first;  // -1: no row tile is left
 #pragma unroll 1
-    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+    for (int k = 0;; ++k) {
       TileDesc t;
       if (!v) {
-        int bx = over_hkv<true>(a, c), kvh = c - bx * a.hkv;
-        if (!DECODE && !a.heads_interleaved) {
-          kvh = c / a.num_tiles;
-          bx = c - kvh * a.num_tiles;
+        if (c >= 0) {
+          int bx = over_hkv<true>(a, c), kvh = c - bx * a.hkv;
+          if (!DECODE && !a.heads_interleaved) {
+            kvh = c / a.num_tiles;
+            bx = c - kvh * a.num_tiles;
+          }
+          t = describe<DECODE, true>(a, bx);
+          t.kvh = kvh;
+        } else {
+          t.kvh = -1;
         }
-        t = describe<DECODE, true>(a, bx);
-        t.kvh = kvh;
         if (k >= 2 && !warp_wait(BAR_DE + 8u * uint32_t(k & 1), uint32_t((k >> 1) - 1) & 1u,
                                  abort_flag))
           break;
         if (lane == 0) descs[k & 1] = t;
         warp_arrive(BAR_DF + 8u * uint32_t(k & 1));
-      } else if (!read_desc(k, t)) {
+        if (c < 0) break;
+        if (!DECODE && lane == 0) {
+          tc::mbar_arrive_expect_tx(BAR_NEXT, 16);
+          ask_next(base + Lo::NEXT, BAR_NEXT);
+        }
+      } else if (!read_desc(k, t) || t.kvh < 0) {
         break;
       }
-      ok = load_tiles<D, BS, SLOPES>(
+      const bool ok = load_tiles<D, BS, SLOPES>(
           a, t, loads_of(t), v ? &maps.v : &maps.k, v ? &maps.v16 : &maps.k16,
           (v ? a.vpool : a.kpool) + int64_t(t.kvh) * a.head_stride,
           int(a.tma_row_base + int64_t(t.kvh) * a.tma_head_rows), base + (v ? Lo::V0 : Lo::K0),
           v ? VF : KF, v ? VE : KE, v ? NV : NK, ring, abort_flag);
+      if (!v) {
+        c = -1;
+        if constexpr (!DECODE) {
+          // (waited for after a failure too: it is written into shared memory)
+          int drain_abort = 0;
+          if (!tc::mbar_wait(BAR_NEXT, uint32_t(k) & 1u, &drain_abort, kWaitLimit)) {
+            *abort_flag = 1;
+            break;
+          }
+          c = next_tile(base + Lo::NEXT);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
     }
     // Before the CTA gives up its shared memory the last load of every stage has
     // landed: at once on the normal path; after a wait of another warp gave up, one
@@ -859,9 +911,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     uint32_t k_phase = 0, b_phase = 1, q_phase = 0;
     bool ok = true;
 #pragma unroll 1
-    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+    for (int k = 0; ok; ++k) {
       TileDesc t;
-      if (!read_desc(k, t)) break;
+      if (!read_desc(k, t) || t.kvh < 0) break;
       const int n_loads = loads_of(t);
       if (n_loads == 0) continue;
       // Q rows into shared memory once the last row tile's products have read theirs: a
@@ -952,9 +1004,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     uint32_t v_phase = 0, p_phase = 0;
     bool ok = true;
 #pragma unroll 1
-    for (int k = 0, c = first; ok && c < total; ++k, c += step) {
+    for (int k = 0; ok; ++k) {
       TileDesc t;
-      if (!read_desc(k, t)) break;
+      if (!read_desc(k, t) || t.kvh < 0) break;
       const int n_loads = loads_of(t), n_tiles = tiles_of(t, n_loads);
       if (n_loads == 0) continue;
       if (elect_one()) {
@@ -1005,14 +1057,13 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   }
 }
 
-// Extend: row tiles dealt out to a CTA an SM, the heaviest first; heads as in
-// attention_tc.cu.
+// Extend: a CTA a row tile in the grid, the heaviest first, of which one an SM (PAIR:
+// two) runs and takes the others over; heads as in attention_tc.cu.
 template <int D, bool PAIR, bool CAP, bool SLOPES>
 __global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  row_tiles<D, PAIR, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), int(gridDim.x),
-                                         a.num_tiles * a.hkv);
+  row_tiles<D, PAIR, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x));
 }
 
 // Decode: the plan's large items as tiles, a CTA each, and beside them the units
@@ -1023,8 +1074,7 @@ __global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
     decode_mod_tile_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   rxk::griddep_launch_dependents();
-  row_tiles<D, false, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x), a.n_tc_ctas,
-                                         a.n_tc_ctas);
+  row_tiles<D, false, true, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x));
 }
 
 // A warp a unit (an item and a KV head): unit blockIdx.x + gridDim.x * warp when
@@ -1158,8 +1208,7 @@ rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, unsigned ctas, cudaS
   if (!make_maps(&maps, pool))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   a.q_boxes = make_q_map(&maps.q, a, D);
-  const unsigned grid = std::min(ctas, unsigned(rx_internal::sm_count()) * (PAIR ? 2 : 1));
-  extend_mod_kernel<D, PAIR, CAP, SLOPES><<<grid, Lo::THREADS, Lo::BYTES, s>>>(a, maps);
+  extend_mod_kernel<D, PAIR, CAP, SLOPES><<<ctas, Lo::THREADS, Lo::BYTES, s>>>(a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 
