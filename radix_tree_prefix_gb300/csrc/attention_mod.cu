@@ -23,7 +23,8 @@
 //                rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
 //                and a score may exceed it by 64, so that nothing but such a row ever
 //                stops for another tile.  (Under a cap of at most 52 m is one number, and
-//                nothing is handed on.)  Each warpgroup keeps the row sums of its own
+//                nothing is handed on, unless a row sees 64 keys or fewer: such a row's m
+//                is its first maximum.)  Each warpgroup keeps the row sums of its own
 //                tiles; they meet in the row tile's end;
 //   then warp S  Q rows, and S_j = Q K_j^T into a ring of TMEM buffers;
 //   K, V         loaders, the K loader also finding row tiles and their key ranges for
@@ -610,10 +611,16 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
     const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
+    // A row of few keys takes its first maximum for a reference: the rounding of a weight
+    // that is nearly all of the row's sum would be the output's (a single key's weight is
+    // then 1).  In longer rows the roundings of weights differ.
+    const bool few = valid && lim - rm.lo <= BN;
+    // No score can leave the reach of one reference, and the tiles need not agree on it.
+    // (The same for the warps of a quadrant in every warpgroup.)
+    const bool bounded =
+        CAP && !SLOPES && a.cap_ref > -INFINITY && !__any_sync(0xffffffffu, few);
     // reference of the row's weights, log2 units
-    float m_ref = valid ? (CAP && !SLOPES ? a.cap_ref : -INFINITY) : 0.f;
-    // no score can leave its reach, and the tiles need not agree on it
-    const bool bounded = CAP && !SLOPES && a.cap_ref > -INFINITY;
+    float m_ref = !valid ? 0.f : bounded ? a.cap_ref : -INFINITY;
     float l = 0.f;            // sum of this warpgroup's weights under it
     bool easy = false;  // every row has a reference
     bool ok = true;
@@ -639,7 +646,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           ok = false;
           break;
         }
-        if (!bounded) warp_arrive(h_bar);
+        warp_arrive(h_bar);
         warp_arrive(BAR_P + 8u * s);
         continue;
       }
@@ -719,7 +726,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
             if (__any_sync(0xffffffffu, grow)) {
               // a row without a reference takes 0 if its scores are about that (tiles of other
               // warpgroups that meet the row first then agree)
-              const float by = grow && !(unset && fabsf(mx) <= kRaise) ? rintf(mx) : 0.f;
+              float by = 0.f;
+              if (grow && !(unset && !few && fabsf(mx) <= kRaise)) by = unset && few ? mx : rintf(mx);
               if (grow) m_ref = m_use + by;
               const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
               l *= f;
@@ -776,10 +784,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
       }
       // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
-      if (!bounded) {
-        ref[(g & 1) * BM + i] = m_ref;
-        warp_arrive(h_bar);
-      }
+      if (!bounded) ref[(g & 1) * BM + i] = m_ref;
+      warp_arrive(h_bar);  // (always, so that its phases are counted alike)
       tc::tc_fence_before();
       warp_arrive(BAR_P + 8u * s);
     }

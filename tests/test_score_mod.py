@@ -760,3 +760,28 @@ def test_caps_that_scores_reach(d, softcap):
     out, lse = c.run(softcap=softcap)
     assert rx.device_check() == 0
     c.check(out, lse, softcap=softcap)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("kind", ["none", "cap", "high_cap", "slopes"])
+def test_a_row_of_one_key_is_its_value(d, kind):
+    """Windows of one key, documents of one token, and a prompt's first token: the weight
+    is 1 and rounds to nothing, whatever the score."""
+    import torch
+    e = Extend([(300, 70), (0, 200), (64, 130)], 8, 2, d, seed=6, mag=3.0)
+    kw = {"none": dict(), "cap": dict(softcap=30.0), "high_cap": dict(softcap=60.0),
+          "slopes": dict(slopes=torch.full((8,), 0.3, device="cuda"))}[kind]
+    value = torch.cat([e.v[1][:, e.up(e.table[e.rows[r], p:p + s]).long()]
+                       for r, (p, s) in enumerate(e.reqs)], 1).repeat_interleave(4, 0)
+    value = value.transpose(0, 1).float()
+    alone = [np.arange(p, p + s) // 3 * 3 for p, s in e.reqs]  # every third token
+    for mod in (dict(window=1), dict(key_begin=alone)):
+        out, _ = e.run(**mod, **kw)
+        assert rx.device_check() == 0
+        rows = torch.ones(e.total, dtype=torch.bool, device="cuda") if "window" in mod else \
+            torch.from_numpy(np.concatenate([np.arange(p, p + s) % 3 == 0
+                                             for p, s in e.reqs])).cuda()
+        assert torch.equal(out[:e.total][rows], value[rows])
+    out, _ = e.run(**kw)
+    assert torch.equal(out[70], value[70])
