@@ -462,6 +462,127 @@ __device__ __forceinline__ void scale_weights(uint32_t taddr, float f) {
   tc::tmem_st_wait();
 }
 
+// SPLIT: the CTAs of a cluster share one row tile's keys.
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_size() {
+  int n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;\n" ::: "memory");
+}
+// The address of what lies at a shared-memory address of this CTA in CTA `rank`.
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, int rank) {
+  uint32_t x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(x) : "r"(addr), "r"(rank));
+  return x;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+
+// The keys of this CTA's share, and in t.member_off how many CTAs have one: shares of
+// kLeastShare keys and more, in whole loads.
+constexpr int kLeastShare = 512;
+__device__ __forceinline__ void cut_keys(TileDesc& t) {
+  const int n = cluster_size(), rank = cluster_rank();
+  const int keys = max(0, t.key_end - t.key_begin);
+  const int share = max(kLeastShare, ((keys + n - 1) / n + 127) & ~127);
+  t.member_off = (keys + share - 1) / share;
+  const int begin = t.key_begin + rank * share;
+  t.key_end = min(t.key_end, begin + share);
+  t.key_lo = max(t.key_lo, begin);
+  t.key_begin = begin;
+}
+
+// The end of a row tile whose keys were shared: every CTA's O, under its rows' references
+// m (ref[i]) and sums l (ref[BM + i]), is brought to the common reference and sum and put
+// into shared memory, and CTA r adds up and writes the r-th part of the rows.  All
+// threads; nothing of the roles is under way.
+template <int D>
+__device__ __forceinline__ void join_rows(const TcArgs& a, const TileDesc& t, uint8_t* gbase,
+                                          const float* ref, uint32_t o_tmem, int threads,
+                                          bool mine) {
+  if (t.member_off <= 1) return;  // (the same in the whole cluster)
+  constexpr int PITCH = D + 4;    // floats a row
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = cluster_size(), rank = cluster_rank(), part = BM / n;
+  const uint32_t stage = rxk::smem_addr(gbase), refs = rxk::smem_addr(ref);
+  const bool m64 = t.n_rows <= 64;
+  auto row_of = [&](int i, int64_t& out_row) {
+    const int row = m64 ? (((i >> 5) << 4) | (i & 15)) : i;
+    if ((m64 && (i & 16)) || row >= t.n_rows) return false;
+    int64_t qi = 0, p = 0;
+    int head = 0, lim = 0;
+    row_info<false, true>(a, t, t.kvh, row, qi, head, p, lim);
+    out_row = qi * a.hq + head;
+    return true;
+  };
+  cluster_barrier();
+  if (warp < 8) {
+    const int i = (warp & 3) * 32 + lane, half = warp >> 2;
+    float m = -INFINITY, l = 0.f;
+    for (int r = 0; r < n; ++r) m = fmaxf(m, ld_cluster(of_rank(refs + 4u * i, r)));
+    for (int r = 0; r < n; ++r) {
+      const float mr = ld_cluster(of_rank(refs + 4u * i, r));
+      const float lr = ld_cluster(of_rank(refs + 4u * (BM + i), r));
+      if (mr > -INFINITY) l = fmaf(lr, rxk::fast_exp2(mr - m), l);
+    }
+    const float f = l == 0.f || ref[i] == -INFINITY ? 0.f : rxk::fast_exp2(ref[i] - m) / l;
+    const uint32_t tl = o_tmem + (uint32_t((warp & 3) * 32) << 16);
+#pragma unroll 1
+    for (int oc = half * (D / 2); oc < (half + 1) * (D / 2); oc += 16) {
+      uint32_t x[16];
+      if (mine) {
+        tmem_ld16(tl + uint32_t(oc), x);
+        tc::tmem_ld_wait();
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x[e] = mine && !(f == 0.f) ? __float_as_uint(__uint_as_float(x[e]) * f) : 0u;
+      uint4* dst = reinterpret_cast<uint4*>(gbase + (i * PITCH + oc) * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    }
+    int64_t out_row = 0;
+    if (half == 0 && i / part == rank && row_of(i, out_row))
+      a.lse[out_row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  }
+  cluster_barrier();
+  for (int k = tid; k < part * (D / 4); k += threads) {
+    const int i = rank * part + k / (D / 4), c = k % (D / 4) * 4;
+    int64_t out_row = 0;
+    if (!row_of(i, out_row)) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < n; ++r) {
+      const float4 y = ld_cluster4(of_rank(stage + uint32_t((i * PITCH + c) * 4), r));
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + out_row * D + c) =
+          make_uint2(rxk::pack_bf16(x.x, x.y), rxk::pack_bf16(x.z, x.w));
+    else
+      *reinterpret_cast<float4*>(a.out + out_row * D + c) = x;
+  }
+  cluster_barrier();  // (no CTA leaves while its rows are read)
+}
+
 // A CTA's row tiles one after another: `first`, and (extend) whatever CTAs of the grid
 // have not started when its K loader asks for another, so that tiles of different
 // lengths spread over the SMs without a counter (dealt out in turn, agent calls under a
@@ -472,7 +593,7 @@ __device__ __forceinline__ void scale_weights(uint32_t taddr, float f) {
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
-template <int D, bool PAIR, bool DECODE, bool CAP, bool SLOPES>
+template <int D, bool PAIR, bool DECODE, bool CAP, bool SLOPES, bool SPLIT = false>
 __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
                                           int first) {
   using Lo = Layout4<D, PAIR>;
@@ -595,7 +716,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const bool narrow = !DECODE && a.out_bf16;
     if (n_loads == 0) {
       // no row of the tile sees a key (decode: at this step of the plan)
-      if (valid && wg < 2) {
+      if (SPLIT && t.member_off > 1) {
+        if (wg == 0) ref[i] = -INFINITY, ref[BM + i] = 0.f;
+      } else if (valid && wg < 2 && (!SPLIT || cluster_rank() == 0)) {
         const int64_t at = out_row * D + wg * (D / 2);
         uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
                             : reinterpret_cast<uint4*>((DECODE ? a.ws_o : a.out) + at);
@@ -727,7 +850,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
               // a row without a reference takes 0 if its scores are about that (tiles of other
               // warpgroups that meet the row first then agree)
               float by = 0.f;
-              if (grow && !(unset && !few && fabsf(mx) <= kRaise)) by = unset && few ? mx : rintf(mx);
+              if (grow && !(unset && !few && fabsf(mx) <= kRaise))
+                by = unset && few ? mx : rintf(mx);
               if (grow) m_ref = m_use + by;
               const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
               l *= f;
@@ -803,6 +927,12 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
       float l_all = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) l_all += sums[w * BM + i];
+      if constexpr (SPLIT) {
+        if (t.member_off > 1) {  // (read by all of the cluster once every role has ended)
+          if (wg == 0) ref[i] = m_fin, ref[BM + i] = l_all;
+          continue;
+        }
+      }
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
       // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
       // sector) a thread and store: the rows need no trip through shared memory.
@@ -855,6 +985,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           }
           t = describe<DECODE, true>(a, bx);
           t.kvh = kvh;
+          if constexpr (SPLIT) cut_keys(t);
         } else {
           t.kvh = -1;
         }
@@ -864,7 +995,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         if (lane == 0) descs[k & 1] = t;
         warp_arrive(BAR_DF + 8u * uint32_t(k & 1));
         if (c < 0) break;
-        if (!DECODE && lane == 0) {
+        if (!DECODE && !SPLIT && lane == 0) {
           tc::mbar_arrive_expect_tx(BAR_NEXT, 16);
           ask_next(base + Lo::NEXT, BAR_NEXT);
         }
@@ -878,7 +1009,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           v ? VF : KF, v ? VE : KE, v ? NV : NK, ring, abort_flag);
       if (!v) {
         c = -1;
-        if constexpr (!DECODE) {
+        if constexpr (!DECODE && !SPLIT) {
           // (waited for after a failure too: it is written into shared memory)
           int drain_abort = 0;
           if (!tc::mbar_wait(BAR_NEXT, uint32_t(k) & 1u, &drain_abort, kWaitLimit)) {
@@ -1057,6 +1188,13 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) atomicOr(&g_tc_error, 2);
+  if constexpr (SPLIT) {
+    tc::tc_fence_after();
+    join_rows<D>(a, descs[0], gbase, reinterpret_cast<float*>(gbase + Lo::REF),
+                 tmem + uint32_t(Lo::O_COL), Lo::THREADS, loads_of(descs[0]) > 0);
+    tc::tc_fence_before();
+    __syncthreads();
+  }
   if (warp == SW) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, Lo::TMEM_COLS);
@@ -1070,6 +1208,15 @@ __global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   row_tiles<D, PAIR, false, CAP, SLOPES>(a, maps, smem_raw, int(blockIdx.x));
+}
+
+// The same for calls of few row tiles over long contexts: a cluster a row tile.
+template <int D, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
+    extend_mod_split_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  row_tiles<D, false, false, CAP, SLOPES, true>(a, maps, smem_raw,
+                                                int(blockIdx.x) / cluster_size());
 }
 
 // Decode: the plan's large items as tiles, a CTA each, and beside them the units
@@ -1218,9 +1365,49 @@ rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, unsigned ctas, cudaS
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 
+// CTAs a row tile: as many as have an SM each and kLeastShare keys of the longest context
+// that the table holds (or the window lets see), 8 at most.  (8 tokens over 30,000 keys 48
+// us and with one CTA 249, two requests of 20 to 40 over 4,000 at head_dim 256 27 and 63,
+// 30 over 600, which one CTA has, 15 and 16.  Shares of 256 keys 23 us for the second, 17
+// for the third.)
+int split_of(const TcArgs& a, unsigned ctas) {
+  const int64_t keys = a.window > 0 ? std::min<int64_t>(a.row_stride, a.window) : a.row_stride;
+  int n = 8;
+  while (n > 1 && (int64_t(ctas) * n > rx_internal::sm_count() || keys < kLeastShare * n)) n /= 2;
+  return n;
+}
+
+template <int D, bool CAP, bool SLOPES>
+rx_status launch_extend_split(TcArgs a, const rx_pool_desc* pool, unsigned ctas, int n,
+                              cudaStream_t s) {
+  using Lo = Layout4<D, false>;
+  static std::atomic<bool> configured[kMaxDevices];
+  const rx_status cs = ensure_smem(configured, extend_mod_split_kernel<D, CAP, SLOPES>, Lo::BYTES);
+  if (cs != RX_OK) return cs;
+  Maps4 maps;
+  if (!make_maps(&maps, pool))
+    return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
+  a.q_boxes = make_q_map(&maps.q, a, D);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(n);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(ctas * unsigned(n));
+  cfg.blockDim = dim3(Lo::THREADS);
+  cfg.dynamicSmemBytes = Lo::BYTES;
+  cfg.stream = s;
+  cudaLaunchKernelEx(&cfg, extend_mod_split_kernel<D, CAP, SLOPES>, a, maps);
+  return rx_internal::launch_status("rx_extend_attention_mod: split");
+}
+
 template <int D, bool CAP, bool SLOPES>
 rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
+  const int n = split_of(a, ctas);
+  if (n > 1) return launch_extend_split<D, CAP, SLOPES>(a, pool, ctas, n, s);
   // Row tiles of few keys, one after another in a CTA, are bound by the way from one
   // to the next, which a second CTA on the SM fills (agent calls in a window of 128
   // 75 us and 56, of 512 108 and 101, documents of 400 tokens 100 and 97); over longer

@@ -785,3 +785,33 @@ def test_a_row_of_one_key_is_its_value(d, kind):
         assert torch.equal(out[:e.total][rows], value[rows])
     out, _ = e.run(**kw)
     assert torch.equal(out[70], value[70])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("kind", ["none", "cap", "high_cap", "slopes", "window", "docs", "both_ways",
+                                  "empty", "all"])
+def test_few_row_tiles_over_long_contexts(d, kind):
+    """Calls whose row tiles share their keys among CTAs: contexts of shares of 512 keys and
+    of less than one, rows that see keys of one share only, or none."""
+    import torch
+    reqs = [(9000, 5), (4000, 40), (30, 3), (0, 1), (1500, 33)]
+    e = Extend(reqs, 8, 2, d, seed=len(kind), mag=2.0)
+    rng = np.random.default_rng(3)
+    kw = {"none": dict(), "cap": dict(softcap=20.0), "high_cap": dict(softcap=60.0),
+          "slopes": dict(slopes=torch.exp2(-1.0 * torch.arange(1, 9, device="cuda"))),
+          "window": dict(window=3001), "docs": dict(), "both_ways": dict(bidir=[9003, 10, 33, 0, 9]),
+          "empty": dict(), "all": dict(softcap=30.0, window=2500)}[kind]
+    if kind in ("docs", "all"):
+        kw["key_begin"] = [_docs(rng, p + s, 700)[p:] for p, s in reqs]
+    if kind == "empty":
+        kw["key_begin"] = [np.where(np.arange(s) % 2, p + s + 5, p // 2) for p, s in reqs]
+    if kind == "all":
+        kw["slopes"] = torch.full((8,), 0.01, device="cuda")
+        kw["bidir"] = [100, 4040, 5, 1, 1533]
+    for dt in (torch.float32, torch.bfloat16):
+        out, lse = e.run(dt, **kw)
+        assert rx.device_check() == 0
+        e.check(out, lse, **kw)
+        again, _ = e.run(dt, **kw)
+        assert torch.equal(out, again)
