@@ -426,6 +426,16 @@ __device__ __forceinline__ void scale_scores(uint32_t (&sr)[32], float scale, fl
     sr[e + 1] = __float_as_uint(x.y);
   }
 }
+// A row's sums of the warpgroups (one a row, of BM) added up in the order of the row
+// tile's own key tiles: warpgroup `first` has its first one, which depends on the row tiles
+// that the CTA came to take over.  (Added up by warpgroup, a call's last bits changed from
+// one run to the next.)
+template <int NW>
+__device__ __forceinline__ float add_sums(const float* x, int first) {
+  const float a = x[first * BM], b = x[(first + 1 == NW ? 0 : first + 1) * BM];
+  if (NW == 2) return a + b;
+  return a + b + x[(first == 0 ? NW - 1 : first - 1) * BM];
+}
 // -inf but for keys [from, to) of the 32, either of which may lie outside them.
 __device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int to) {
   // (a shift by 32 gives 0)
@@ -747,7 +757,8 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     float l = 0.f;            // sum of this warpgroup's weights under it
     bool easy = false;  // every row has a reference
     bool ok = true;
-    int j = (wg + NW - g0 % NW) % NW;
+    const int first_wg = g0 % NW;  // the warpgroup of tile 0
+    int j = (wg + NW - first_wg) % NW;
     // tile j's buffer of P, and the phase of the buffer's barriers
     int s = (g0 + j) % NB;
     uint32_t phase = uint32_t((g0 + j) / NB) & 1u;
@@ -924,9 +935,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     g0 += n_loads * SUBS;
     ++used;
     if (wg < 2) {
-      float l_all = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) l_all += sums[w * BM + i];
+      const float l_all = add_sums<NW>(sums + i, first_wg);
       if constexpr (SPLIT) {
         if (t.member_off > 1) {  // (read by all of the cluster once every role has ended)
           if (wg == 0) ref[i] = m_fin, ref[BM + i] = l_all;
