@@ -455,7 +455,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// A tile's bf16 weights (32 columns of pairs) times f, a power of two: exact.
+// A tile's bf16 weights (32 columns of pairs) times f, a power of two or 0: exact.
 __device__ __forceinline__ void scale_weights(uint32_t taddr, float f) {
   tc::tmem_st_wait();  // the warp's own stores
 #pragma unroll 1
@@ -885,17 +885,19 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
         }
         const float m_prev = ref[((g - 1) & 1) * BM + i];
         if (!__all_sync(0xffffffffu, m_prev == m_ref)) {
-          float down = 1.f;
-          const bool raise = m_prev != -INFINITY && m_ref > m_prev;
-          const float up = raise ? rxk::fast_exp2(m_prev - m_ref) : 1.f;
-          if (!raise && m_prev != -INFINITY) {
-            const float f = m_ref == -INFINITY ? 1.f : rxk::fast_exp2(m_ref - m_prev);
-            l *= f;
-            m_ref = m_prev;
-            down = f;
+          float down = 1.f, up = 1.f;  // what the tile's weights and O are multiplied by
+          if (m_prev != -INFINITY) {
+            float m = fmaxf(m_prev, m_ref);
+            // (few keys: weights go down by a power of two, beyond which O does)
+            if (few && m_ref > -INFINITY && m_ref < m_prev)
+              m = fmaxf(m_prev, m_ref + ceilf(m_prev - m_ref));
+            if (m_ref > -INFINITY) down = rxk::fast_exp2(m_ref - m);
+            up = rxk::fast_exp2(m_prev - m);
+            l *= down;
+            m_ref = m;
           }
           if (__any_sync(0xffffffffu, down != 1.f)) scale_weights(p_col, down);
-          if (__any_sync(0xffffffffu, raise)) {
+          if (__any_sync(0xffffffffu, up != 1.f)) {
             // O is rescaled once PV of tile g - 1 has written it.  (Its barrier cannot be
             // a phase behind: that tile's scores were issued after PV of tile g - 1 - NB
             // completed, and are done.)
