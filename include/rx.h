@@ -907,7 +907,12 @@ typedef struct rx_score_mod {
 
 /* rx_extend_attention with modified scores (mod NULL: none), into fp32 or
  * bf16 (out_type).  Scores, statistics and sums are held in fp32; softmax
- * weights are rounded to bf16 for the product with V.  A tile of 128 query
+ * weights are rounded to bf16 for the product with V, and the output divided by a
+ * sum in which the heaviest ones count as they were rounded, so that a row whose one
+ * key outweighs the rest does not bear its weight's rounding (rows of 16 keys and
+ * fewer: by the sum before the rounding, within 2^-8 of sum p_j |v_j|).  lse is
+ * that of the weights before their rounding.  The same call gives the same bits
+ * every time.  A tile of 128 query
  * rows (rx_extend_plan) reads the keys from the first to the last that one of
  * its rows sees; their V rows must be finite (a masked key weighs 0, and 0 times
  * an infinity would reach the tile's other queries) and at most 2^40 in magnitude

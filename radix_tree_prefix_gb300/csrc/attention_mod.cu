@@ -23,7 +23,7 @@
 //                rare: m is an integer, 0 unless a row's scores lie beyond 2^+-64,
 //                and a score may exceed it by 64, so that nothing but such a row ever
 //                stops for another tile.  (Under a cap of at most 52 m is one number, and
-//                nothing is handed on, unless a row sees 64 keys or fewer: such a row's m
+//                nothing is handed on, unless a row sees 16 keys or fewer: such a row's m
 //                is its first maximum.)  Each warpgroup keeps the row sums of its own
 //                tiles; they meet in the row tile's end;
 //   then warp S  Q rows, and S_j = Q K_j^T into a ring of TMEM buffers;
@@ -59,6 +59,8 @@ constexpr int kGroup = 16;  // keys of a small TMA box
 // 2^-60): what is raised or lowered are rows of extreme scores only.
 constexpr float kRaise = 64.f;
 constexpr float kMostSum = 18446744073709551616.f;  // 2^kRaise
+constexpr int kFew = 16;  // keys of a row that takes a score of its own for a reference
+constexpr float kOffUnit = 8388608.f;  // 2^23: of what a weight's rounding adds to its sum
 constexpr int kPairWindow = 1024;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
@@ -84,8 +86,10 @@ struct Layout4 {
   static constexpr int Q = 0;
   static constexpr int K0 = BM * D * 2;
   static constexpr int V0 = K0 + NK * KV_BYTES;
-  static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references, of even and odd tiles
-  static constexpr int SUM = REF + 2 * BM * 4;    // rows' sums, by warpgroup
+  static constexpr int REF = V0 + NV * KV_BYTES;  // rows' references
+  static constexpr int MORE = REF + BM * 4;       // what their sums have more than for lse
+  static constexpr int SUM = MORE + BM * 4;       // rows' sums, by the warpgroups' first tiles
+  static constexpr int JOIN = V0;  // SPLIT, at the end: rows' references and both their sums
   static constexpr int NEXT = SUM + 3 * BM * 4;   // answer to a request for another row tile
   static constexpr int DESC = NEXT + 16;          // the row tile in hand and the next
   static constexpr int BAR = DESC + 2 * int(sizeof(TileDesc));
@@ -97,6 +101,7 @@ struct Layout4 {
   static_assert(O_COL + D <= TMEM_COLS, "TMEM budget");
   static_assert(BAR % 8 == 0 && DESC % 8 == 0, "alignment");
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(PAIR || BM * (D + 4) * 4 <= JOIN, "the joined rows' room (join_rows)");
 };
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
@@ -347,8 +352,14 @@ __device__ __forceinline__ void cap_factors(const TcArgs& a, const uint32_t (&sr
 #pragma unroll
     for (int k = 0; k < 8; ++k) p[k] = __ffma2_rn(p[k], v[k], a.cap_fold2[d]);
 }
-// 2^sr in bf16, and their sum before the rounding.
-__device__ __forceinline__ float weights_of(const uint32_t (&sr)[32], uint32_t (&pk)[16]) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^sr in bf16, and their sum before the rounding; the largest of them and of top into top.
+__device__ __forceinline__ float weights_of(const uint32_t (&sr)[32], uint32_t (&pk)[16],
+                                            float& top) {
   float2 l4[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) l4[u] = make_float2(0.f, 0.f);
@@ -358,6 +369,7 @@ __device__ __forceinline__ float weights_of(const uint32_t (&sr)[32], uint32_t (
                                  rxk::fast_exp2(__uint_as_float(sr[e + 1])));
     l4[(e >> 1) & 3] = __fadd2_rn(l4[(e >> 1) & 3], p);
     pk[e >> 1] = rxk::pack_bf16(p.x, p.y);
+    top = max3(top, p.x, p.y);
   }
   const float2 lt = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
   return lt.x + lt.y;
@@ -425,16 +437,6 @@ __device__ __forceinline__ void scale_scores(uint32_t (&sr)[32], float scale, fl
     sr[e] = __float_as_uint(x.x);
     sr[e + 1] = __float_as_uint(x.y);
   }
-}
-// A row's sums of the warpgroups (one a row, of BM) added up in the order of the row
-// tile's own key tiles: warpgroup `first` has its first one, which depends on the row tiles
-// that the CTA came to take over.  (Added up by warpgroup, a call's last bits changed from
-// one run to the next.)
-template <int NW>
-__device__ __forceinline__ float add_sums(const float* x, int first) {
-  const float a = x[first * BM], b = x[(first + 1 == NW ? 0 : first + 1) * BM];
-  if (NW == 2) return a + b;
-  return a + b + x[(first == 0 ? NW - 1 : first - 1) * BM];
 }
 // -inf but for keys [from, to) of the 32, either of which may lie outside them.
 __device__ __forceinline__ void mask_scores(uint32_t (&sr)[32], int from, int to) {
@@ -521,7 +523,8 @@ __device__ __forceinline__ void cut_keys(TileDesc& t) {
 }
 
 // The end of a row tile whose keys were shared: every CTA's O, under its rows' references
-// m (ref[i]) and sums l (ref[BM + i]), is brought to the common reference and sum and put
+// m (ref[i]) and sums (ref[BM + i] what O is divided by, ref[2 BM + i] of the weights before
+// their rounding), is brought to the common reference and sum and put
 // into shared memory, and CTA r adds up and writes the r-th part of the rows.  All
 // threads; nothing of the roles is under way.
 template <int D>
@@ -546,14 +549,16 @@ __device__ __forceinline__ void join_rows(const TcArgs& a, const TileDesc& t, ui
   cluster_barrier();
   if (warp < 8) {
     const int i = (warp & 3) * 32 + lane, half = warp >> 2;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, lo = 0.f;
     for (int r = 0; r < n; ++r) m = fmaxf(m, ld_cluster(of_rank(refs + 4u * i, r)));
     for (int r = 0; r < n; ++r) {
       const float mr = ld_cluster(of_rank(refs + 4u * i, r));
-      const float lr = ld_cluster(of_rank(refs + 4u * (BM + i), r));
-      if (mr > -INFINITY) l = fmaf(lr, rxk::fast_exp2(mr - m), l);
+      if (!(mr > -INFINITY)) continue;
+      const float to = rxk::fast_exp2(mr - m);
+      lo = fmaf(ld_cluster(of_rank(refs + 4u * (BM + i), r)), to, lo);
+      l = fmaf(ld_cluster(of_rank(refs + 4u * (2 * BM + i), r)), to, l);
     }
-    const float f = l == 0.f || ref[i] == -INFINITY ? 0.f : rxk::fast_exp2(ref[i] - m) / l;
+    const float f = lo == 0.f || ref[i] == -INFINITY ? 0.f : rxk::fast_exp2(ref[i] - m) / lo;
     const uint32_t tl = o_tmem + (uint32_t((warp & 3) * 32) << 16);
 #pragma unroll 1
     for (int oc = half * (D / 2); oc < (half + 1) * (D / 2); oc += 16) {
@@ -692,8 +697,10 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const int wg = warp >> 2;
     const int i = (warp & 3) * 32 + lane;  // TMEM lane
     const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
-    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);   // [2][BM]
+    float* ref = reinterpret_cast<float*>(gbase + Lo::REF);   // [BM]
+    int16_t* more = reinterpret_cast<int16_t*>(gbase + Lo::MORE);  // [BM][2]
     float* sums = reinterpret_cast<float*>(gbase + Lo::SUM);  // [NW][BM]
+    float* join = reinterpret_cast<float*>(gbase + Lo::JOIN);  // [3][BM]
     int g0 = 0;    // the row tile's first tile among all of the CTA's
     int used = 0;  // row tiles with keys before it
 #pragma unroll 1
@@ -727,7 +734,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     if (n_loads == 0) {
       // no row of the tile sees a key (decode: at this step of the plan)
       if (SPLIT && t.member_off > 1) {
-        if (wg == 0) ref[i] = -INFINITY, ref[BM + i] = 0.f;
+        if (wg == 0) join[i] = -INFINITY, join[BM + i] = join[2 * BM + i] = 0.f;
       } else if (valid && wg < 2 && (!SPLIT || cluster_rank() == 0)) {
         const int64_t at = out_row * D + wg * (D / 2);
         uint4* dst = narrow ? reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + at)
@@ -744,21 +751,29 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     const int lo_max = __reduce_max_sync(0xffffffffu, rm.lo);
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
     const int pos_min = __reduce_min_sync(0xffffffffu, rm.pos);
-    // A row of few keys takes its first maximum for a reference: the rounding of a weight
-    // that is nearly all of the row's sum would be the output's (a single key's weight is
-    // then 1).  In longer rows the roundings of weights differ.
-    const bool few = valid && lim - rm.lo <= BN;
+    // The product with V takes rounded weights, and the rounding of one that is nearly all
+    // of its row's sum must not be the output's.  O is therefore divided by a sum in which the
+    // heaviest weight of each warpgroup counts as it was rounded (top): that weight's rounding
+    // then cancels as it would if all of them did (its share of the rest's is small: with a
+    // heaviest weight of 0.05 to 0.4 of the sum the outputs' errors are the same within 2 %),
+    // for an instruction in place of three a pair of weights.  (Agent calls under a cap 433 us
+    // without it and 442; a sum of all rounded weights takes 33 us more than none, as products
+    // of mma.sync with ones 97.)  A row of few keys, where such a sum could double the error of the light
+    // ones, takes the first maximum it meets for a reference instead, so that a single key's
+    // weight is 1 and its value comes out as it is.  All other references are integers, and
+    // what brings weights from one to another a power of two.
+    const bool few = valid && lim - rm.lo <= kFew;
     // No score can leave the reach of one reference, and the tiles need not agree on it.
     // (The same for the warps of a quadrant in every warpgroup.)
     const bool bounded =
         CAP && !SLOPES && a.cap_ref > -INFINITY && !__any_sync(0xffffffffu, few);
     // reference of the row's weights, log2 units
     float m_ref = !valid ? 0.f : bounded ? a.cap_ref : -INFINITY;
-    float l = 0.f;            // sum of this warpgroup's weights under it
+    float l = 0.f;            // sum of this warpgroup's weights under it, before their
+    float top = 0.f;          // rounding, and the largest of them
     bool easy = false;  // every row has a reference
     bool ok = true;
-    const int first_wg = g0 % NW;  // the warpgroup of tile 0
-    int j = (wg + NW - first_wg) % NW;
+    int j = (wg + NW - g0 % NW) % NW;
     // tile j's buffer of P, and the phase of the buffer's barriers
     int s = (g0 + j) % NB;
     uint32_t phase = uint32_t((g0 + j) / NB) & 1u;
@@ -819,9 +834,12 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
               add_slopes(sr, a.scale_log2, rm.slope, float(k0 + c - rm.pos), true, m_use);
             else
               scale_scores(sr, a.scale_log2, m_use);
-            sum = weights_of(sr, pk);
+            float t = top;
+            sum = weights_of(sr, pk, t);
             done = __all_sync(0xffffffffu, !valid || sum <= kMostSum);
-            if (!done) {
+            if (done) {
+              top = t;
+            } else {
               tc::tmem_ld32(p_col + uint32_t(c), sr);
               tc::tmem_ld_wait();
             }
@@ -866,11 +884,12 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
               if (grow) m_ref = m_use + by;
               const float f = unset ? 1.f : rxk::fast_exp2(-by);  // (unset: no weights yet)
               l *= f;
+              top *= f;
               if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) scale_weights(p_col, f);
               if (__any_sync(0xffffffffu, by != 0.f)) scale_scores(sr, 1.f, by);
             }
           }
-          sum = weights_of(sr, pk);
+          sum = weights_of(sr, pk, top);
           if constexpr (DIRECT) easy = !__any_sync(0xffffffffu, m_ref == -INFINITY);
         }
         tmem_st16(p_col + uint32_t(c / 2), pk);
@@ -883,7 +902,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           ok = false;
           break;
         }
-        const float m_prev = ref[((g - 1) & 1) * BM + i];
+        const float m_prev = ref[i];
         if (!__all_sync(0xffffffffu, m_prev == m_ref)) {
           float down = 1.f, up = 1.f;  // what the tile's weights and O are multiplied by
           if (m_prev != -INFINITY) {
@@ -894,6 +913,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
             if (m_ref > -INFINITY) down = rxk::fast_exp2(m_ref - m);
             up = rxk::fast_exp2(m_prev - m);
             l *= down;
+            top *= down;
             m_ref = m;
           }
           if (__any_sync(0xffffffffu, down != 1.f)) scale_weights(p_col, down);
@@ -920,40 +940,56 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           }
         }
       }
-      // (the slot's reader of tile j - 2 passed its own barrier before this tile's)
-      if (!bounded) ref[(g & 1) * BM + i] = m_ref;
+      // (its reader, this thread of the next tile's warpgroup, waits for barrier H)
+      if (!bounded) ref[i] = m_ref;
       warp_arrive(h_bar);  // (always, so that its phases are counted alike)
       tc::tc_fence_before();
       warp_arrive(BAR_P + 8u * s);
     }
     // Once the row tile's products are done, O stands under the last reference; the
-    // warpgroups bring their sums there and exchange them.
+    // warpgroups bring there and exchange their sums as O is divided by them, and what these
+    // have more than for lse (16 bits, in 2^-23 of a sum: there is no room for second sums).
+    // From here on a warpgroup is known by its first tile: summed by warpgroup, a call's last
+    // bits would hang on which row tiles the CTA came to take over.
     if (!ok || !warp_wait(BAR_FIN, uint32_t(used) & 1u, abort_flag)) break;
     tc::tc_fence_after();
-    const float m_fin = bounded ? m_ref : ref[((g0 + n_tiles - 1) & 1) * BM + i];
-    sums[wg * BM + i] = m_ref == -INFINITY ? 0.f : l * rxk::fast_exp2(m_ref - m_fin);
+    const float m_fin = bounded ? m_ref : ref[i];
+    const int first = (wg + NW - g0 % NW) % NW;
+    const float wide = few ? 0.f : __uint_as_float(rxk::pack_bf16(0.f, top)) - top;
+    const int off = min(max(__float2int_rn(__fdividef(wide * kOffUnit, l)), -32768), 32767);
+    if (first > 0) more[2 * i + first - 1] = int16_t(off);
+    sums[first * BM + i] =
+        m_ref == -INFINITY ? 0.f : (l + wide) * rxk::fast_exp2(m_ref - m_fin);
     warp_arrive(BAR_X);
     if (!warp_wait(BAR_X, uint32_t(used) & 1u, abort_flag)) break;
     g0 += n_loads * SUBS;
     ++used;
-    if (wg < 2) {
-      const float l_all = add_sums<NW>(sums + i, first_wg);
+    if (first < 2) {
+      float l_all = 0.f, l_more = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float x = sums[w * BM + i];
+        l_all += x;
+        if (first == 0)
+          l_more = fmaf(x, float(w == 0 ? off : int(more[2 * i + w - 1])), l_more);
+      }
+      const float l_lse = fmaf(l_more, -1.f / kOffUnit, l_all);
       if constexpr (SPLIT) {
         if (t.member_off > 1) {  // (read by all of the cluster once every role has ended)
-          if (wg == 0) ref[i] = m_fin, ref[BM + i] = l_all;
+          if (first == 0) join[i] = m_fin, join[BM + i] = l_all, join[2 * BM + i] = l_lse;
           continue;
         }
       }
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-      // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of its rows, 32 bytes (a
+      // Warpgroup w < 2 writes columns [w D/2, (w+1) D/2) of the rows, 32 bytes (a
       // sector) a thread and store: the rows need no trip through shared memory.
       constexpr int HC = D / 2;
-      const int64_t at = out_row * D + wg * HC;
+      const int64_t at = out_row * D + first * HC;
       const bool whole = (reinterpret_cast<uintptr_t>(DECODE ? a.ws_o : a.out) & 31) == 0;
 #pragma unroll 1
       for (int oc = 0; oc < HC; oc += 16) {
         uint32_t r[16];
-        tmem_ld16(tl + uint32_t(Lo::O_COL + wg * HC + oc), r);
+        tmem_ld16(tl + uint32_t(Lo::O_COL + first * HC + oc), r);
         tc::tmem_ld_wait();
         if (oc + 16 >= HC) {  // the next row tile's products may overwrite O
           tc::tc_fence_before();
@@ -974,9 +1010,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           store_32(dst + 8, &r[8], whole);
         }
       }
-      if (valid && wg == 0)
+      if (valid && first == 0)
         (DECODE ? a.ws_lse : a.lse)[out_row] =
-            l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_all);
+            l_all == 0.f ? -INFINITY : m_fin * kLn2 + logf(l_lse);
     }
     }
   } else if (warp == SW + 1 || warp == SW + 2) {
@@ -1201,7 +1237,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
   if (tid == 0 && *abort_flag) atomicOr(&g_tc_error, 2);
   if constexpr (SPLIT) {
     tc::tc_fence_after();
-    join_rows<D>(a, descs[0], gbase, reinterpret_cast<float*>(gbase + Lo::REF),
+    join_rows<D>(a, descs[0], gbase, reinterpret_cast<float*>(gbase + Lo::JOIN),
                  tmem + uint32_t(Lo::O_COL), Lo::THREADS, loads_of(descs[0]) > 0);
     tc::tc_fence_before();
     __syncthreads();

@@ -524,11 +524,14 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
   for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
     for (int mt = 0; mt < NK; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
-  float m_ref[NR][2], l_run[NR][2];
+  // (MOD: l_run is the sum of the weights before their rounding, for lse, and l_bf the sum
+  // of those that the product with V takes, for o: the rounding of a weight that is nearly
+  // all of a row's then cancels)
+  float m_ref[NR][2], l_run[NR][2], l_bf[NR][2];
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
     m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
-    l_run[nt][0] = l_run[nt][1] = 0.f;
+    l_run[nt][0] = l_run[nt][1] = l_bf[nt][0] = l_bf[nt][1] = 0.f;
   }
 
 #pragma unroll 1
@@ -648,6 +651,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
             const float alpha = rxk::fast_exp2(m_ref[0][e] - mx);  // 0 from -inf
             m_ref[0][e] = mx;
             l_run[0][e] *= alpha;
+            l_bf[0][e] *= alpha;
 #pragma unroll
             for (int mt = 0; mt < NK; ++mt) {
               o[0][mt][e] *= alpha;
@@ -668,6 +672,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
           const float p1 = rxk::fast_exp2(x[u][2 + e] - m_use);
           pk[e] = rxk::pack_bf16(p0, p1);
           l_run[0][e] += p0 + p1;
+          l_bf[0][e] += __uint_as_float(pk[e] << 16) + __uint_as_float(pk[e] & 0xffff0000u);
         }
         const uint32_t v0 = __shfl_sync(0xffffffffu, pk[0], src1);
         const uint32_t v1 = __shfl_sync(0xffffffffu, pk[1], src1);
@@ -770,6 +775,7 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
             const float alpha = rxk::fast_exp2(m_ref[nt][e] - mx[nt][e]);  // 0 from -inf
             m_ref[nt][e] = mx[nt][e];
             l_run[nt][e] *= alpha;
+            if constexpr (MOD) l_bf[nt][e] *= alpha;
 #pragma unroll
             for (int mt = 0; mt < NK; ++mt) {
               o[nt][mt][e] *= alpha;
@@ -789,6 +795,8 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
           const float p1 = rxk::fast_exp2(x[nt][2 + e] - m_use);
           pk[nt][e] = rxk::pack_bf16(p0, p1);
           l_run[nt][e] += p0 + p1;
+          l_bf[nt][e] +=
+              __uint_as_float(pk[nt][e] << 16) + __uint_as_float(pk[nt][e] & 0xffff0000u);
           continue;
         }
         uint32_t h;
@@ -839,13 +847,20 @@ __device__ __forceinline__ void pipe_unit(const TcArgs& a, uint32_t ring, int32_
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
+      float lo = l;  // what o is divided by
+      if constexpr (MOD) {
+        lo = l_bf[nt][e];
+        lo += __shfl_xor_sync(0xffffffffu, lo, 4);
+        lo += __shfl_xor_sync(0xffffffffu, lo, 8);
+        lo += __shfl_xor_sync(0xffffffffu, lo, 16);
+      }
       const int r = nt * 8 + 2 * c + e;
       if (r >= n_rows) continue;
       const int uu = over_group<MOD>(a, r);
       const int head = kvh * G + (r - uu * G);
       const int64_t part = int64_t(part_base) + uu;
       float* dst = a.ws_o + (part * a.hq + head) * D;
-      const float inv = l > 0.f ? 1.f / l : 0.f;  // an empty chunk: zero partial, lse -inf
+      const float inv = lo > 0.f ? 1.f / lo : 0.f;  // an empty chunk: zero partial, lse -inf
 #pragma unroll
       for (int mt = 0; mt < NK; ++mt) {
         dst[16 * mt + g] = o[nt][mt][e] * inv;
