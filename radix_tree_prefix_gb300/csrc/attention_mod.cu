@@ -1384,7 +1384,8 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
       if (fabs(c) > 1e37) u = -1.0;  // too large: no score is near
       a->cap_fold2[i] = make_float2(f, f);
     }
-    a->cap_near = float(u / double(a->cap_in));
+    // (no further than a raw score's square is in fp32)
+    a->cap_near = float(std::min(u / double(a->cap_in), 1e19));
     // Capped scores lie within +-cap_out: where their weights under one reference stay
     // within 2^-88 and 2^kRaise, that is every row's, and no maximum is taken.
     a->cap_ref = a->cap_out <= 76.f ? fmaxf(0.f, ceilf(a->cap_out) - kRaise) : -INFINITY;
