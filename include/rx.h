@@ -886,7 +886,8 @@ rx_status rx_qkv_store(const rx_pool_desc* pool, int32_t layer,
  *   s = softcap * tanh(scale * q.k / softcap) - slope_h * |i - j|
  * and sees it if  (j <= i or j < bidir_end)  and  i - j < window  and
  * j >= key_begin.  Each part is left out when its field is 0 or NULL.  A query
- * that sees no key gets zeros and lse = -inf. */
+ * that sees no key gets zeros and lse = -inf.  A capped score is off by at most
+ * 2^-20 of itself, or 2^-15 under a softcap of at most 88. */
 typedef struct rx_score_mod {
   float softcap;              /* 2^-40 to 2^40; 0: scores are not capped    */
   int32_t window;             /* keys back that a query sees, itself

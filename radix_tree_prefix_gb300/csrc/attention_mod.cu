@@ -61,6 +61,9 @@ constexpr float kRaise = 64.f;
 constexpr float kMostSum = 18446744073709551616.f;  // 2^kRaise
 constexpr int kFew = 16;  // keys of a row that takes a score of its own for a reference
 constexpr float kOffUnit = 8388608.f;  // 2^23: of what a weight's rounding adds to its sum
+// Kernels by what caps their scores: nothing, a cap of at most kLowCap, a higher one.
+constexpr int kNoCap = 0, kCap = 1, kHighCap = 2;
+constexpr float kLowCap = 128.f;  // in log2 units
 constexpr int kPairWindow = 1024;  // widest window for two CTAs an SM
 
 // Keys are loaded, and S computed, BS at a time (the wider product at head_dim
@@ -397,6 +400,26 @@ __device__ __forceinline__ void cap_scores(const TcArgs& a, uint32_t (&sr)[32], 
       sr[e] = __float_as_uint(fmaf(a.cap_out, tanh_exp(__uint_as_float(sr[e]) * a.cap_in), -m));
   }
 }
+// The same score by score: the exponential's error is one of the cap, which the scores of
+// other rows and keys must not bear that are far below it.  (Under caps of at most 88 it is
+// below 2^-15, nothing beside a weight's rounding, and scores go the one way or the other
+// together: a prompt in a window under a cap of 30, whose scores come near it, takes 184 us
+// so and 230 score by score.  Kernels of their own, because as a third way in the loop,
+// inline or not, it cost calls that never take it 3 %.)
+__device__ __forceinline__ void cap_each(const TcArgs& a, uint32_t (&sr)[32], float m) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 16) {
+    float2 p[8];
+    cap_factors(a, sr, e, p);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = __uint_as_float(sr[e + k]);
+      const float far = a.cap_out * tanh_exp(x * a.cap_in);
+      const float near = x * (k & 1 ? p[k >> 1].y : p[k >> 1].x);
+      sr[e + k] = __float_as_uint((fabsf(x) <= a.cap_near ? near : far) - m);
+    }
+  }
+}
 // sr * scale - slope |away + e| - m; behind: no key lies after the row's query, and
 // the bias is linear in the key.
 __device__ __forceinline__ void add_slopes(uint32_t (&sr)[32], float scale, float slope,
@@ -608,13 +631,13 @@ __device__ __forceinline__ void join_rows(const TcArgs& a, const TileDesc& t, ui
 // CAP, SLOPES: what modifies the scores (with neither, masks alone).  Each is a
 // kernel of its own: jumps over the code of what a call does not use cost its
 // warps more in instruction fetches than the work.
-template <int D, bool PAIR, bool DECODE, bool CAP, bool SLOPES, bool SPLIT = false>
+template <int D, bool PAIR, bool DECODE, int CAP, bool SLOPES, bool SPLIT = false>
 __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, uint8_t* gbase,
                                           int first) {
   using Lo = Layout4<D, PAIR>;
   constexpr int NW = Lo::NW, NK = Lo::NK, NV = Lo::NV, NS = Lo::NS, NB = Lo::NB, BS = Lo::BS;
   constexpr int SUBS = Lo::SUBS, NH = Lo::NH;
-  constexpr bool DIRECT = !CAP && D == 128 && (SLOPES || !PAIR);
+  constexpr bool DIRECT = CAP == kNoCap && D == 128 && (SLOPES || !PAIR);
   static_assert(NW <= 3, "reference barriers and sums");
   constexpr int SW = 4 * NW;  // softmax warps; behind them S, K, V and PV
   const uint32_t base = rxk::smem_addr(gbase);
@@ -766,7 +789,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
     // No score can leave the reach of one reference, and the tiles need not agree on it.
     // (The same for the warps of a quadrant in every warpgroup.)
     const bool bounded =
-        CAP && !SLOPES && a.cap_ref > -INFINITY && !__any_sync(0xffffffffu, few);
+        CAP == kCap && !SLOPES && a.cap_ref > -INFINITY && !__any_sync(0xffffffffu, few);
     // reference of the row's weights, log2 units
     float m_ref = !valid ? 0.f : bounded ? a.cap_ref : -INFINITY;
     float l = 0.f;            // sum of this warpgroup's weights under it, before their
@@ -846,7 +869,9 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           }
         }
         if (!done) {
-          if constexpr (CAP) {
+          if constexpr (CAP == kHighCap) {
+            cap_each(a, sr, SLOPES ? 0.f : m_use);
+          } else if constexpr (CAP) {
             float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
@@ -861,7 +886,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           if constexpr (SLOPES)
             add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind,
                        m_use);
-          else if constexpr (!CAP)
+          else if constexpr (CAP == kNoCap)
             scale_scores(sr, a.scale_log2, m_use);
           if (masked) mask_scores(sr, rm.lo - (k0 + c), lim - (k0 + c));
           if (!bounded) {
@@ -1250,7 +1275,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
 
 // Extend: a CTA a row tile in the grid, the heaviest first, of which one an SM (PAIR:
 // two) runs and takes the others over; heads as in attention_tc.cu.
-template <int D, bool PAIR, bool CAP, bool SLOPES>
+template <int D, bool PAIR, int CAP, bool SLOPES>
 __global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
     extend_mod_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1258,7 +1283,7 @@ __global__ void __launch_bounds__(Layout4<D, PAIR>::THREADS, PAIR ? 2 : 1)
 }
 
 // The same for calls of few row tiles over long contexts: a cluster a row tile.
-template <int D, bool CAP, bool SLOPES>
+template <int D, int CAP, bool SLOPES>
 __global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
     extend_mod_split_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1269,7 +1294,7 @@ __global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
 // Decode: the plan's large items as tiles, a CTA each, and beside them the units
 // of its small ones on whatever SMs are free (two kernels: the softmax of the
 // tiles has three warpgroups, and a unit more registers than those leave).
-template <int D, bool CAP, bool SLOPES>
+template <int D, int CAP, bool SLOPES>
 __global__ void __launch_bounds__(Layout4<D, false>::THREADS, 1)
     decode_mod_tile_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Maps4 maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1399,7 +1424,7 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
   a->mul2 = make_float2(a->mul, a->mul);
 }
 
-template <int D, bool PAIR, bool CAP, bool SLOPES>
+template <int D, bool PAIR, int CAP, bool SLOPES>
 rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
   using Lo = Layout4<D, PAIR>;
   static std::atomic<bool> configured[kMaxDevices];
@@ -1425,7 +1450,7 @@ int split_of(const TcArgs& a, unsigned ctas) {
   return n;
 }
 
-template <int D, bool CAP, bool SLOPES>
+template <int D, int CAP, bool SLOPES>
 rx_status launch_extend_split(TcArgs a, const rx_pool_desc* pool, unsigned ctas, int n,
                               cudaStream_t s) {
   using Lo = Layout4<D, false>;
@@ -1451,7 +1476,7 @@ rx_status launch_extend_split(TcArgs a, const rx_pool_desc* pool, unsigned ctas,
   return rx_internal::launch_status("rx_extend_attention_mod: split");
 }
 
-template <int D, bool CAP, bool SLOPES>
+template <int D, int CAP, bool SLOPES>
 rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
   const int n = split_of(a, ctas);
@@ -1461,13 +1486,13 @@ rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
   // 75 us and 56, of 512 108 and 101, documents of 400 tokens 100 and 97); over longer
   // ranges one CTA with deeper rings is faster (a window of 2,048 251 and 275, of 3,000
   // 324 and 383), and under a cap always (a prompt in a window of 1,024 196 and 205).
-  if constexpr (D == 128 && !CAP)
+  if constexpr (D == 128 && CAP == kNoCap)
     if (a.key_begin || (a.window > 0 && a.window <= kPairWindow))
       return launch_extend<D, true, CAP, SLOPES>(a, pool, ctas, s);
   return launch_extend<D, false, CAP, SLOPES>(a, pool, ctas, s);
 }
 
-template <int D, bool CAP, bool SLOPES>
+template <int D, int CAP, bool SLOPES>
 rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
@@ -1495,36 +1520,35 @@ rx_status launch_decode_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned 
     static_assert(bytes <= 227 * 1024 && PipeCfg<D>::WARP_BYTES % 16 == 0, "shared memory");
     static std::atomic<bool> configured[kMaxDevices];
     const rx_status cs =
-        ensure_smem(configured, decode_mod_stream_kernel<D, CAP, SLOPES>, bytes);
+        ensure_smem(configured, decode_mod_stream_kernel<D, CAP != kNoCap, SLOPES>, bytes);
     if (cs != RX_OK) return cs;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kPipeWarps * 32);
     cfg.dynamicSmemBytes = bytes;
     cfg.numAttrs = a.n_tc_ctas > 0 ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, decode_mod_stream_kernel<D, CAP, SLOPES>, a);
+    cudaLaunchKernelEx(&cfg, decode_mod_stream_kernel<D, CAP != kNoCap, SLOPES>, a);
     return rx_internal::launch_status("rx_decode_attention_mod: streams");
   }
   return RX_OK;
 }
 
-// By modification: none (masks), cap, slopes, both.
+// By modification: none (masks), slopes; a cap, and slopes; a high cap, and slopes.
 using Launch = rx_status (*)(const TcArgs&, const rx_pool_desc*, unsigned, cudaStream_t);
-constexpr Launch kExtend128[4] = {
-    launch_extend_mod<128, false, false>, launch_extend_mod<128, true, false>,
-    launch_extend_mod<128, false, true>, launch_extend_mod<128, true, true>};
-constexpr Launch kExtend256[4] = {
-    launch_extend_mod<256, false, false>, launch_extend_mod<256, true, false>,
-    launch_extend_mod<256, false, true>, launch_extend_mod<256, true, true>};
-constexpr Launch kDecode128[4] = {
-    launch_decode_mod<128, false, false>, launch_decode_mod<128, true, false>,
-    launch_decode_mod<128, false, true>, launch_decode_mod<128, true, true>};
-constexpr Launch kDecode256[4] = {
-    launch_decode_mod<256, false, false>, launch_decode_mod<256, true, false>,
-    launch_decode_mod<256, false, true>, launch_decode_mod<256, true, true>};
+template <int D>
+constexpr Launch kExtend[6] = {
+    launch_extend_mod<D, kNoCap, false>,   launch_extend_mod<D, kNoCap, true>,
+    launch_extend_mod<D, kCap, false>,     launch_extend_mod<D, kCap, true>,
+    launch_extend_mod<D, kHighCap, false>, launch_extend_mod<D, kHighCap, true>};
+template <int D>
+constexpr Launch kDecode[6] = {
+    launch_decode_mod<D, kNoCap, false>,   launch_decode_mod<D, kNoCap, true>,
+    launch_decode_mod<D, kCap, false>,     launch_decode_mod<D, kCap, true>,
+    launch_decode_mod<D, kHighCap, false>, launch_decode_mod<D, kHighCap, true>};
 
-rx_status pick(int D, const rx_score_mod& m, const Launch (&f128)[4], const Launch (&f256)[4],
+rx_status pick(int D, const rx_score_mod& m, const Launch (&f128)[6], const Launch (&f256)[6],
                const TcArgs& a, const rx_pool_desc* pool, unsigned ctas, cudaStream_t s) {
-  const int which = (m.softcap > 0.f ? 1 : 0) | (m.d_slopes ? 2 : 0);
+  const int cap = !(m.softcap > 0.f) ? kNoCap : a.cap_out <= kLowCap ? kCap : kHighCap;
+  const int which = 2 * cap + (m.d_slopes ? 1 : 0);
   return (D == 128 ? f128[which] : f256[which])(a, pool, ctas, s);
 }
 
@@ -1599,7 +1623,7 @@ extern "C" rx_status rx_extend_attention_mod(
   a.lse = d_lse;
   a.out_bf16 = out_type == RX_OUT_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return pick(D, mod ? *mod : none, kExtend128, kExtend256, a, pool, unsigned(ctas), s);
+  return pick(D, mod ? *mod : none, kExtend<128>, kExtend<256>, a, pool, unsigned(ctas), s);
 }
 
 extern "C" rx_status rx_decode_attention_mod(
@@ -1659,7 +1683,7 @@ extern "C" rx_status rx_decode_attention_mod(
       if (cudaMemsetAsync(counter, 0, sizeof(int32_t), s) != cudaSuccess)
         return rx_internal::launch_status("rx_decode_attention_mod: counter reset");
     }
-    st = pick(D, mod ? *mod : none, kDecode128, kDecode256, a, pool, unsigned(ctas), s);
+    st = pick(D, mod ? *mod : none, kDecode<128>, kDecode<256>, a, pool, unsigned(ctas), s);
     if (st != RX_OK) return st;
   }
   return rx_internal::merge_parts(D, d_plan + info->off_req_part_indptr,

@@ -309,35 +309,35 @@ constexpr float kTanh[kTanhTerms] = {0.99999994f, -0.3333284f,   0.13325204f,  -
 constexpr int kTanhNearTerms = 5;
 constexpr float kTanhNear[kTanhNearTerms] = {0.99999994f, -0.3333231f, 0.13310173f, -0.05210148f,
                                              0.015475428f};
-// tanh(u) = 1 - 2 / (1 + e^2u), off by some 2^-22 at most
+// tanh(u) = 1 - 2 / (1 + e^2u), off by some 2^-22 at most: for |u| above 0.6, where that is
+// less than 2^-20 of it
 __device__ __forceinline__ float tanh_exp(float u) {
   return fmaf(-2.f, __fdividef(1.f, 1.f + rxk::fast_exp2(u * (2.f * kLog2e))), 1.f);
 }
-// softcap * tanh(scale * s / softcap) * log2(e) of a lane's scores, all of a warp's the
-// same way: branches for each one would put their chains one behind the other.
+// softcap * tanh(scale * s / softcap) * log2(e) of a lane's scores: all by the polynomial
+// first (branches for each one would put their chains one behind the other), and where some
+// score of the warp lies beyond its range, those that do by the exponential.
 template <int N>
 __device__ __forceinline__ void cap_all(const TcArgs& a, float (&x)[N][4]) {
+  float u[4 * N], v[4 * N], p[4 * N];
   float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4 * N; ++i) most = fmaxf(most, fabsf(x[i >> 2][i & 3]));
-  if (__all_sync(0xffffffffu, most * a.cap_in <= 1.f)) {
-    float u[4 * N], v[4 * N], p[4 * N];
+  for (int i = 0; i < 4 * N; ++i) {
+    u[i] = x[i >> 2][i & 3] * a.cap_in;
+    most = fmaxf(most, fabsf(u[i]));
+    v[i] = u[i] * u[i];
+    p[i] = a.cap_poly[kTanhTerms - 1];
+  }
 #pragma unroll
-    for (int i = 0; i < 4 * N; ++i) {
-      u[i] = x[i >> 2][i & 3] * a.cap_in;
-      v[i] = u[i] * u[i];
-      p[i] = a.cap_poly[kTanhTerms - 1];
-    }
+  for (int d = kTanhTerms - 2; d >= 0; --d)
 #pragma unroll
-    for (int d = kTanhTerms - 2; d >= 0; --d)
+    for (int i = 0; i < 4 * N; ++i) p[i] = fmaf(p[i], v[i], a.cap_poly[d]);
 #pragma unroll
-      for (int i = 0; i < 4 * N; ++i) p[i] = fmaf(p[i], v[i], a.cap_poly[d]);
-#pragma unroll
-    for (int i = 0; i < 4 * N; ++i) x[i >> 2][i & 3] = u[i] * p[i];
-  } else {
+  for (int i = 0; i < 4 * N; ++i) x[i >> 2][i & 3] = u[i] * p[i];
+  if (!__all_sync(0xffffffffu, most <= 1.f)) {
 #pragma unroll
     for (int i = 0; i < 4 * N; ++i)
-      x[i >> 2][i & 3] = a.cap_out * tanh_exp(x[i >> 2][i & 3] * a.cap_in);
+      if (!(fabsf(u[i]) <= 1.f)) x[i >> 2][i & 3] = a.cap_out * tanh_exp(u[i]);
   }
 }
 
