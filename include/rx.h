@@ -835,6 +835,7 @@ typedef struct rx_rope {
 rx_status rx_rope_init(const rx_rope_config* cfg, rx_rope* out);
 
 /* RMS norm of each head's row: x / sqrt(mean(x^2) + eps) * w, or times 1 + w.
+ * The squares are summed in fp32: elements are at most 2^59 in magnitude.
  * Weights: device bf16 [head_dim], 16-byte aligned; a NULL weight leaves
  * queries or keys as they are. */
 typedef struct rx_head_norm {
@@ -845,7 +846,8 @@ typedef struct rx_head_norm {
 } rx_head_norm;
 
 /* Queries and keys of T tokens normalised (norm; NULL: not) and rotated to
- * their positions (rope; NULL: not), in fp32, rounded once to bf16.
+ * their positions (rope; NULL: not), in fp32, rounded once to bf16.  Elements that
+ * neither touches keep their bits.
  * d_positions: device int32 [T], of any value (not read without a rotation).
  * d_q: device bf16, token t's heads at d_q + t * q_stride elements,
  * [num_q_heads][head_dim] side by side; d_k alike.  Strides are in elements,

@@ -5,8 +5,8 @@
 //   y = x / sqrt(mean(x^2) + eps) * w        (the norm, if any; w or 1 + w)
 //   (a, b) -> m (a cos t - b sin t, a sin t + b cos t),  t = position * f_i
 // for the pairs (a, b) = (y_i, y_{i + rot/2}) or (y_2i, y_2i+1) of the first
-// rot elements; the rest of the row stays.  Everything is held in fp32 and
-// rounded once, to bf16.
+// rot elements; the rest of the row stays, to the bit where nothing is normalised.
+// Everything else is held in fp32 and rounded once, to bf16.
 //
 // Angles: f_i is held as a 64-bit fraction of a turn, so position * f_i
 // modulo one turn is one 64-bit integer product that is exact for every
@@ -21,9 +21,10 @@
 // D/16 threads hold a head and a pair's two elements meet in one thread
 // without a shuffle; a warp takes 32/(D/16) heads at a time, computes its
 // eight sines and cosines a lane once, and walks its token's heads with them.
-// Measured: 32,767 tokens of 40 heads of 128 in 104 us (6.46 TB/s, 95% of a
-// copy's rate), the append of 51,200 tokens of 24 heads of 256 in 219 us (5.75
-// TB/s, 85%; its writes go to nine places), one token 3 us.
+// Measured: 32,767 tokens of 40 heads of 128 in 109 us (6.16 TB/s, 91% of a
+// copy's rate; 2 us less where the rest of a row was turned by an angle of 0), the
+// append of 51,200 tokens of 24 heads of 256 in 224 us (5.6 TB/s, 83%; its writes go
+// to nine places), one token 3 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -120,8 +121,29 @@ __device__ __forceinline__ void turn_share(uint4& ua, uint4& ub, bool sums, bool
   ub = pack8(b);
 }
 
-// The sines and cosines of the eight pairs of share c at a position; pairs behind
-// the rotated part stay.
+// The first n pairs of a share from the turned pieces, the others as they were (a product
+// with a sine of 0 takes an infinity from one element into the next, and loses a zero's sign
+// and a NaN's bits).  Of shares whose pairs do not all turn or all stay.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void keep_rest(uint4& ta, uint4& tb, const uint4& a, const uint4& b,
+                                          int n) {
+  if constexpr (INTERLEAVED) {  // a pair is a word
+    ta = make_uint4(n > 0 ? ta.x : a.x, n > 1 ? ta.y : a.y, n > 2 ? ta.z : a.z,
+                    n > 3 ? ta.w : a.w);
+    tb = make_uint4(n > 4 ? tb.x : b.x, n > 5 ? tb.y : b.y, n > 6 ? tb.z : b.z,
+                    n > 7 ? tb.w : b.w);
+  } else {
+    auto first = [&](uint32_t t, uint32_t old, int i) {  // elements i and i + 1
+      return n > i + 1 ? t : n > i ? __byte_perm(t, old, 0x7610) : old;
+    };
+    ta = make_uint4(first(ta.x, a.x, 0), first(ta.y, a.y, 2), first(ta.z, a.z, 4),
+                    first(ta.w, a.w, 6));
+    tb = make_uint4(first(tb.x, b.x, 0), first(tb.y, b.y, 2), first(tb.z, b.z, 4),
+                    first(tb.w, b.w, 6));
+  }
+}
+
+// The sines and cosines of the eight pairs of share c at a position.
 __device__ __forceinline__ void angles(const rx_rope& r, int c, int32_t pos, float (&cs)[8],
                                        float (&sn)[8]) {
 #pragma unroll
@@ -176,7 +198,7 @@ struct Head {
 // (a chat turn's append 219 us; three steps ahead with 80 registers 252, and a ring
 // of shared memory under warps that walk over tokens 287).
 constexpr int kWarps = 2;  // per CTA
-template <int D, bool INTERLEAVED, bool STORE>
+template <int D, bool INTERLEAVED, bool STORE, bool PART>
 __global__ void __launch_bounds__(kWarps * 32, 16)
     rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int TPH = D / 16;  // threads a head
@@ -226,6 +248,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16)
   if (h < heads) load(Head<D, STORE>(a, h).from(rows), nx, ny);
   float cs[8], sn[8];
   angles(a.rope, c, a.pos ? __ldg(a.pos + t) : 0, cs, sn);
+  const int n = a.rope.rot_dim / 2 - 8 * c;  // pairs of the share that turn (or all, or none)
+  const bool turns = n > 0;
 #pragma unroll 1
   for (int h0 = part * HPW; h0 < heads; h0 += step, h += step) {
     uint4 x = nx, y = ny;
@@ -241,7 +265,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16)
       }
       uint4 rx = x, ry = y;
       turn_share<D, INTERLEAVED>(rx, ry, norm_q || norm_k, norm, w, a.eps, a.offset, cs, sn);
-      if (!is_v) {
+      if (PART && !norm) keep_rest<INTERLEAVED>(rx, ry, x, y, n);
+      if (norm || (turns && !is_v)) {  // (else the share's bits stay as they are)
         x = rx;
         y = ry;
       }
@@ -318,6 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (norm) load(is_q ? a.q_weight : a.k_weight, w[0], w[1]);
     uint4 rx = x, ry = y;
     turn_share<D, false>(rx, ry, norm_q || norm_k, norm, w, a.eps, a.offset, cs, sn);
+    if (!norm) keep_rest<false>(rx, ry, x, y, rot / 2 - 8 * c);
     if (!is_v) {
       x = rx;
       y = ry;
@@ -341,12 +367,13 @@ void launch(const RopeArgs& a, cudaStream_t s) {
   const int64_t all = (a.T * a.split + kWarps - 1) / kWarps;
   const dim3 block{kWarps * 32};
   const dim3 grid{unsigned(all)};
-  if (a.rope.layout == RX_ROPE_HALF && a.rope.rot_dim % 16 != 0)
-    rope_odd_kernel<D, STORE><<<grid, block, 0, s>>>(a);
-  else if (a.rope.layout == RX_ROPE_INTERLEAVED)
-    rope_kernel<D, true, STORE><<<grid, block, 0, s>>>(a);
+  const bool half = a.rope.layout == RX_ROPE_HALF;
+  if (a.rope.rot_dim % 16 != 0)  // a share has pairs of both kinds
+    half ? rope_odd_kernel<D, STORE><<<grid, block, 0, s>>>(a)
+         : rope_kernel<D, true, STORE, true><<<grid, block, 0, s>>>(a);
   else
-    rope_kernel<D, false, STORE><<<grid, block, 0, s>>>(a);
+    half ? rope_kernel<D, false, STORE, false><<<grid, block, 0, s>>>(a)
+         : rope_kernel<D, true, STORE, false><<<grid, block, 0, s>>>(a);
 }
 
 // What both calls check and fill in: the rotation, the norm and the inputs.
