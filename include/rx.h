@@ -470,6 +470,8 @@ typedef struct rx_decode_plan_info {
                              newest token lies in a private tail run by the
                              warp role (group <= 16), so
                              rx_decode_steps stores it inside that kernel */
+  int64_t window;         /* rx_plan_decode_window's: no key behind it is in the
+                             plan, and calls that need one refuse it; 0: none */
 } rx_decode_plan_info;
 
 /* Plan one decode step for a batch of B requests.  prompt_node[b] is the
@@ -935,8 +937,9 @@ rx_status rx_extend_attention_mod(
  * step's window of any request reaches are left out of the plan, and a
  * request whose window ends before a shared segment is not among the
  * segment's members.  distinct_kv_tokens counts the keys that step 0 reads.
- * Such a plan serves rx_decode_attention_mod with this window or a
- * smaller one only.  Errors: as rx_plan_decode_steps, and window < 0. */
+ * Such a plan (its info says the window) serves rx_decode_attention_mod with
+ * this window or a smaller one only; any other call refuses it.  Errors: as
+ * rx_plan_decode_steps, and window < 0. */
 rx_status rx_plan_decode_window(const rx_cache* cache, int32_t B,
                                 int32_t n_steps, int32_t window,
                                 const rx_node* prompt_node,
@@ -955,7 +958,7 @@ rx_status rx_plan_decode_window(const rx_cache* cache, int32_t B,
  * d_ctx_len is needed with a window or slopes.  The V rows of the plan's keys
  * must be finite and at most 2^40.  Numerics as rx_extend_attention_mod.  Errors:
  * RX_ERR_INVALID as rx_decode_attention and rx_extend_attention_mod, for
- * step < 0 and a missing d_ctx_len. */
+ * step < 0, a missing d_ctx_len, and a plan of a smaller window than mod's. */
 rx_status rx_decode_attention_mod(
     const rx_pool_desc* pool, int32_t layer, const void* d_q,
     int32_t num_q_heads, const int32_t* d_req_to_token, int64_t row_stride,

@@ -184,6 +184,8 @@ rx_status decode_attention_impl(const rx_pool_desc* pool, int32_t layer, const v
   if (!d_q || !d_req_to_token || !d_plan || !d_out || !d_lse || !aligned16(d_q) ||
       !aligned16(d_out) || info->n_work > INT32_MAX)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_decode_attention: NULL or misaligned");
+  if (info->window > 0)
+    return rx_internal::set_error(RX_ERR_INVALID, rx_internal::kWindowPlan);
   const int D = pool->head_dim;
   const int32_t* work = d_plan + info->off_work;
   const int32_t* members = d_plan + info->off_members;
@@ -271,6 +273,9 @@ extern "C" rx_status rx_decode_steps(const rx_pool_desc* pool, int32_t layer, in
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_decode_steps: Hq % Hkv != 0");
   const int G = num_q_heads / pool->num_kv_heads;
+  for (int32_t i = 0; i < n_steps; ++i)  // before anything is launched
+    if (B > 0 && steps[i].info && steps[i].info->window > 0)
+      return rx_internal::set_error(RX_ERR_INVALID, rx_internal::kWindowPlan);
   // A run of steps of one plan whose new tokens all lie in private tails (another
   // plan's shared segments may hold what the steps before stored): every step has
   // its own work counter (zeroed here at once, after the largest step's
@@ -350,6 +355,7 @@ extern "C" rx_status rx_decode_attention_static(const rx_pool_desc* pool, int32_
                                                 float scale, float* d_out, float* d_lse,
                                                 rx_stream_t stream) {
   if (!info) return rx_internal::set_error(RX_ERR_INVALID, "rx_decode_attention_static: no plan info");
+  if (info->window > 0) return rx_internal::set_error(RX_ERR_INVALID, rx_internal::kWindowPlan);
   if (info->workspace_bytes > int64_t(RX_DECODE_STATIC_SCRATCH_BYTES)) {
     static thread_local char buf[256];
     snprintf(buf, sizeof(buf),

@@ -1646,6 +1646,8 @@ extern "C" rx_status rx_decode_attention_mod(
     return bad("rx_decode_attention_mod: NULL or misaligned");
   if (mod && (mod->window > 0 || mod->d_slopes) && !mod->d_ctx_len)
     return bad("rx_decode_attention_mod: a window or slopes need d_ctx_len");
+  if (info->window > 0 && (!mod || mod->window == 0 || mod->window > info->window))
+    return bad("rx_decode_attention_mod: the plan was made for a smaller window");
   const int64_t n_small = info->n_work - info->n_work_tc;
   if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
       info->n_work > INT32_MAX / pool->num_kv_heads)

@@ -983,6 +983,8 @@ rx_status decode8(
   if (info->n_work < 0 || n_small < 0 || info->n_work_tc < 0 || info->n_parts < 0 ||
       info->n_work > INT32_MAX / hkv)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_attention: bad plan info");
+  if (info->window > 0)
+    return rx_internal::set_error(RX_ERR_INVALID, rx_internal::kWindowPlan);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // the workspace layout of rx_plan_decode: partial rows, their lse, a counter
   const int64_t o_bytes = (info->n_parts * num_q_heads * int64_t(D) * 4 + 255) / 256 * 256;
@@ -1143,6 +1145,9 @@ extern "C" rx_status rx_kv8_decode_steps(const rx_kv8_pool_desc* pool, int32_t l
   if (r != RX_OK) return r;
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0)
     return rx_internal::set_error(RX_ERR_INVALID, "rx_kv8_decode_steps: Hq % Hkv != 0");
+  for (int32_t i = 0; i < n_steps; ++i)  // before anything is launched
+    if (B > 0 && steps[i].info && steps[i].info->window > 0)
+      return rx_internal::set_error(RX_ERR_INVALID, rx_internal::kWindowPlan);
   // Every step has its own unit counter, reset together behind the largest
   // step's partials if the workspace has room, and the launches of steps that
   // follow on under one plan are chained: the store is launched while the merge

@@ -1066,6 +1066,7 @@ static rx_status plan_decode_impl(const rx_cache* c, int32_t B, int32_t n_steps,
                           std::max<int64_t>(256, (4 * int64_t(n_steps) + 255) / 256 * 256);
   info->distinct_kv_tokens = distinct;
   info->tails_private = tails_private ? 1 : 0;
+  info->window = window;
   if (!plan || plan_cap < info->plan_words)
     return fail(RX_ERR_INVALID, "rx_plan_decode: plan needs %lld words, capacity %lld",
                 (long long)info->plan_words, (long long)plan_cap);

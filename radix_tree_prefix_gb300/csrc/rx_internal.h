@@ -60,6 +60,9 @@ rx_status launch_status(const char* what);
 int sm_count();
 // The driver's cuTensorMapEncodeTiled, NULL if it cannot be found.
 void* tensor_map_encoder();
+// What calls without a window answer to a plan that has one.
+constexpr const char* kWindowPlan =
+    "decode: the plan leaves out the keys behind a window (rx_plan_decode_window)";
 // Error words of the kernels of each file: bit 0 = slot out of range.
 int32_t kv_store_error_flags(bool clear);
 int32_t tc_error_flags(bool clear);
