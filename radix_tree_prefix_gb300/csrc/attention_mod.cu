@@ -1438,39 +1438,73 @@ rx_status launch_extend(TcArgs a, const rx_pool_desc* pool, unsigned ctas, cudaS
   return rx_internal::launch_status("rx_extend_attention_mod");
 }
 
-// CTAs a row tile: as many as have an SM each and kLeastShare keys of the longest context
-// that the table holds (or the window lets see), 8 at most.  (8 tokens over 30,000 keys 48
-// us and with one CTA 249, two requests of 20 to 40 over 4,000 at head_dim 256 27 and 63,
-// 30 over 600, which one CTA has, 15 and 16.  Shares of 256 keys 23 us for the second, 17
-// for the third.)
-int split_of(const TcArgs& a, unsigned ctas) {
+void split_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas, int n,
+                  int threads, int bytes) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = unsigned(n);
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+  cfg->gridDim = dim3(ctas * unsigned(n));
+  cfg->blockDim = dim3(unsigned(threads));
+  cfg->dynamicSmemBytes = size_t(bytes);
+}
+
+// CTAs a row tile, 8 at most: as many as have kLeastShare keys each of the longest context
+// that the table holds (or the window lets see), and whose clusters all run at once.  (A
+// cluster's CTAs, an SM each, lie in one GPC, whose SMs are no multiple of 8, and clusters in
+// more than one wave lose to smaller ones: 16 row tiles of 8,000 keys at head_dim 128 take
+// 48 us as clusters of 8 and 36 of 4, 38 row tiles 69 of 4 and 64 of 2.)  8 tokens over
+// 30,000 keys 48 us and with one CTA 249, two requests of 20 to 40 over 4,000 at head_dim 256
+// 27 and 63, 30 over 600, which one CTA has, 15 and 16.  Shares of 256 keys 23 us for the
+// second, 17 for the third.
+template <int D, int CAP, bool SLOPES>
+rx_status split_of(const TcArgs& a, unsigned ctas, int* split) {
+  using Lo = Layout4<D, false>;
+  constexpr auto* kernel = extend_mod_split_kernel<D, CAP, SLOPES>;
+  static std::atomic<bool> configured[kMaxDevices];
+  static std::atomic<int> fit[kMaxDevices][4];  // clusters of 2^lg CTAs at once, + 1
   const int64_t keys = a.window > 0 ? std::min<int64_t>(a.row_stride, a.window) : a.row_stride;
-  int n = 8;
-  while (n > 1 && (int64_t(ctas) * n > rx_internal::sm_count() || keys < kLeastShare * n)) n /= 2;
-  return n;
+  *split = 1;
+  if (int64_t(ctas) * 2 > rx_internal::sm_count() || keys < kLeastShare * 2) return RX_OK;
+  const rx_status st = ensure_smem(configured, kernel, Lo::BYTES);
+  if (st != RX_OK) return st;
+  int dev = -1;
+  cudaGetDevice(&dev);
+  for (int lg = 3; lg >= 1; --lg) {
+    if (keys < kLeastShare << lg) continue;
+    int n = fit[dev][lg].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute attr[1];
+      split_config(&cfg, attr, 1, 1 << lg, Lo::THREADS, Lo::BYTES);
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // no cluster of this size
+        c = 0;
+      }
+      n = c + 1;
+      fit[dev][lg].store(n, std::memory_order_relaxed);
+    }
+    if (ctas <= unsigned(n - 1)) {
+      *split = 1 << lg;
+      break;
+    }
+  }
+  return RX_OK;
 }
 
 template <int D, int CAP, bool SLOPES>
 rx_status launch_extend_split(TcArgs a, const rx_pool_desc* pool, unsigned ctas, int n,
                               cudaStream_t s) {
   using Lo = Layout4<D, false>;
-  static std::atomic<bool> configured[kMaxDevices];
-  const rx_status cs = ensure_smem(configured, extend_mod_split_kernel<D, CAP, SLOPES>, Lo::BYTES);
-  if (cs != RX_OK) return cs;
   Maps4 maps;
   if (!make_maps(&maps, pool))
     return rx_internal::set_error(RX_ERR_CUDA, "could not encode the pool's TMA tensor maps");
   a.q_boxes = make_q_map(&maps.q, a, D);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(n);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(ctas * unsigned(n));
-  cfg.blockDim = dim3(Lo::THREADS);
-  cfg.dynamicSmemBytes = Lo::BYTES;
+  split_config(&cfg, attr, ctas, n, Lo::THREADS, Lo::BYTES);
   cfg.stream = s;
   cudaLaunchKernelEx(&cfg, extend_mod_split_kernel<D, CAP, SLOPES>, a, maps);
   return rx_internal::launch_status("rx_extend_attention_mod: split");
@@ -1479,7 +1513,9 @@ rx_status launch_extend_split(TcArgs a, const rx_pool_desc* pool, unsigned ctas,
 template <int D, int CAP, bool SLOPES>
 rx_status launch_extend_mod(const TcArgs& a, const rx_pool_desc* pool, unsigned ctas,
                             cudaStream_t s) {
-  const int n = split_of(a, ctas);
+  int n = 1;
+  const rx_status st = split_of<D, CAP, SLOPES>(a, ctas, &n);
+  if (st != RX_OK) return st;
   if (n > 1) return launch_extend_split<D, CAP, SLOPES>(a, pool, ctas, n, s);
   // Row tiles of few keys, one after another in a CTA, are bound by the way from one
   // to the next, which a second CTA on the SM fills (agent calls in a window of 128
