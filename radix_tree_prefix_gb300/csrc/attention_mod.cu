@@ -869,9 +869,7 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
           }
         }
         if (!done) {
-          if constexpr (CAP == kHighCap) {
-            cap_each(a, sr, SLOPES ? 0.f : m_use);
-          } else if constexpr (CAP) {
+          if constexpr (CAP != kNoCap) {
             float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
@@ -880,8 +878,11 @@ __device__ __forceinline__ void row_tiles(const TcArgs& a, const Maps4& maps, ui
                 am[u] = fmaxf(am[u], fmaxf(fabsf(__uint_as_float(sr[e + 2 * u])),
                                            fabsf(__uint_as_float(sr[e + 2 * u + 1]))));
             const float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-            cap_scores(a, sr, __all_sync(0xffffffffu, !valid || most <= a.cap_near),
-                       SLOPES ? 0.f : m_use);
+            const bool near = __all_sync(0xffffffffu, !valid || most <= a.cap_near);
+            if (CAP == kHighCap && !near)
+              cap_each(a, sr, SLOPES ? 0.f : m_use);
+            else
+              cap_scores(a, sr, CAP == kHighCap || near, SLOPES ? 0.f : m_use);
           }
           if constexpr (SLOPES)
             add_slopes(sr, CAP ? 1.f : a.scale_log2, rm.slope, float(k0 + c - rm.pos), behind,
@@ -1420,8 +1421,6 @@ void set_common(TcArgs* a, const rx_pool_desc* pool, int32_t layer, const void* 
   a->key_begin = m.d_key_begin;
   a->bidir_end = m.d_bidir_end;
   a->ctx_len = m.d_ctx_len;
-  a->mul = a->cap_in != 0.f || m.d_slopes ? 1.f : a->scale_log2;
-  a->mul2 = make_float2(a->mul, a->mul);
 }
 
 template <int D, bool PAIR, int CAP, bool SLOPES>

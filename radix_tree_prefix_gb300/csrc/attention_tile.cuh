@@ -44,8 +44,9 @@ constexpr int BM = 128;
 // with mul = ceil(2^shift / d) and shift = 31 + ceil(log2 d) is exact there (mul d
 // - 2^shift <= 2^(shift - 31)).  A division by a value the compiler does not know
 // is a chain of some thirty instructions, and a tile's description, its rows' offsets
-// and each unit's start hold several: with these 32 documents of 17..1010 tokens
-// took 108 us, with the operator 113; a 16k prompt with window 1024 217 and 222.
+// and each unit's start hold several: when the tile took 217 us for a prompt of
+// 8,191 tokens in a window of 1,024 and 108 for 5 prompts of 1,500 to 2,500 tokens in
+// documents of 400, the operator made them 222 and 113.
 struct Div {
   uint32_t mul, shift;
   __device__ __forceinline__ int operator()(int n) const {
@@ -104,9 +105,6 @@ struct TcArgs {
   float cap_in;            // scale / softcap, 0: no cap
   float cap_out;           // softcap * log2(e)
   float cap_poly[7];       // of tanh (kTanh), times cap_out
-  float mul;               // what a modified score is still to be multiplied by: 1, or
-                           // scale_log2 when nothing but masks modifies it
-  float2 mul2;             // twice, for two scores at a time
   float2 cap_fold2[5];     // of kTanhNear with cap_in and cap_out in it, twice: a raw
   float cap_near;          // score of at most this magnitude times a polynomial in its
                            // square
