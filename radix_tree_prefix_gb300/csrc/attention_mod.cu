@@ -43,10 +43,10 @@
 // issue slot a clock.  The loops are rolled, and the softmax role stands first in the
 // kernel (behind the other roles agent calls under a cap took 506 us, so 458).  At
 // head_dim 256 it is shared memory's bandwidth and V's ring of two tiles.  One GB300,
-// 40 calls of 200 queries over 3,000 common keys, 32 / 8 heads of 128: 324 us without
-// modification (1,260 TFLOP/s), 339 with slopes, 425 under a cap; 64 chat turns of 200
-// queries over 2,000 to 3,800 keys, 16 / 4 heads of 256, pages of 16, slopes: 550 us
-// (1,115 TFLOP/s).
+// 40 calls of 200 queries over 3,000 common keys, 32 / 8 heads of 128: 329 us without
+// modification (1,245 TFLOP/s), 343 with slopes, 436 under a cap; 64 chat turns of 200
+// queries over 2,000 to 3,800 keys, 16 / 4 heads of 256, pages of 16, slopes: 566 us
+// (1,083 TFLOP/s).
 
 #include "attention_tile.cuh"
 
