@@ -1031,8 +1031,8 @@ def extend_attention_mod(pool, layer, d_q, hq, d_table, d_req_rows, d_prefix_len
     i32, bf16, what = tt.i32, tt.bf16, "extend_attention_mod"
     narrow = d_out.dtype is bf16
     dev, n = d_q.get_device(), d_q.numel()
-    nq = n // (hq * pool.head_dim)
     s = _current(what, tt, dev, stream)
+    nq = n // (hq * pool.head_dim) if hq > 0 else 0  # (the call refuses it)
     st = _lib.rx_extend_attention_mod(
         pool, layer, _flat(what, "d_q", d_q, bf16, 0, dev), hq,
         _flat(what, "d_table", d_table, i32, 0, dev), d_table.shape[1],
