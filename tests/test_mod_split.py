@@ -81,3 +81,24 @@ def test_as_many_row_tiles_as_clusters_may_have(d, tiles):
     out, lse = e.run(softcap=30.0)
     assert rx.device_check() == 0
     e.check(out, lse, softcap=30.0)
+
+
+@pytest.mark.gpu
+def test_a_first_call_may_be_captured():
+    """What a cluster's size is asked of the device, also while a stream is captured (no other
+    test shares keys under a high cap with slopes)."""
+    import torch
+    e = Extend([(4500, 5)], 8, 2, 256, seed=3)
+    e.run()
+    slopes = torch.full((8,), 0.01, device="cuda")
+    a = list(e.args)
+    a[12] = rx.score_mod(softcap=150.0, slopes=slopes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rx.extend_attention_mod(*a)
+    for t in a[13:15]:
+        t.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert rx.device_check() == 0
+    e.check(*a[13:15], softcap=150.0, slopes=slopes)
